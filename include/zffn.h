@@ -327,6 +327,141 @@ zffn_status zffn_moe_swiglu_q4k_residual(const void *x, const int32_t *expert_id
                                          const void *Wu, const void *Wd, float *y, int T, int H,
                                          int I, int E, int top_k, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * Layers held in 8-bit floating point.  Weights and activations are e4m3 bytes
+ * (1 sign, 4 exponent, 3 mantissa bits; largest value 448; 0x7F and 0xFF are
+ * NaN) with one fp32 scale for each block of 128: a matrix [N][K] of weights
+ * carries scales [ceil(N/128)][ceil(K/128)], a matrix [M][K] of activations
+ * carries [M][ceil(K/128)].  A value is its byte's value times its block's
+ * scale; the last block of either axis may be cut.  The source pages have no
+ * counterpart of these entry points: they are the same routed and dense blocks
+ * for weights in this format, and the parts of such a layer on their own.
+ * ------------------------------------------------------------------------- */
+typedef enum { ZFFN_DT_F32 = 0, ZFFN_DT_BF16 = 1 } zffn_dtype;
+
+/* Quantise x to e4m3 with a power-of-two scale for each block:
+ *     s = the least 2^p (p >= -126) with |x| <= 448 s over the block's finite
+ *         values, 1 for a block of zeros;   q = e4m3(x / s)
+ * The division is exact, so q is rounded once (to nearest, ties to even);
+ * infinities become +-448, NaN stays NaN, and neither changes its block's scale.
+ *   x: dtype (zffn_dtype) [rows][cols].   q: output, bytes [rows][cols].
+ *   block_rows: 1 (activations: 1 x 128 blocks) or 128 (weights: 128 x 128).
+ *   scale: output, fp32 [ceil(rows / block_rows)][ceil(cols / 128)].
+ * Any rows, cols >= 1 (rows <= 2^31 - 1, cols <= 2^20); x aligned to its
+ * element, scale to 4 bytes (16-byte aligned x and rows are read faster).
+ * Errors: INVALID_ARG, CUDA. */
+zffn_status zffn_fp8_quantize(int dtype, const void *x, void *q, float *scale, int64_t rows,
+                              int64_t cols, int block_rows, void *stream);
+
+/* out[r][c] = value of byte q[r][c] times its block's scale, fp32 (one rounding;
+ * exact for power-of-two scales).  Arguments as for zffn_fp8_quantize. */
+zffn_status zffn_fp8_dequant(const void *q, const float *scale, float *out, int64_t rows,
+                             int64_t cols, int block_rows, void *stream);
+
+/* Product of block-scaled matrices, dense or grouped by expert:
+ *     y[m][n] = sum_b a_scale[m][b] w_scale[n / 128][b] sum_{k in block b} a[m][k] w[n][k]
+ * Each block's sum and the sum over blocks are fp32; y is rounded once.
+ *   a: e4m3 [M][K], a_scale fp32 [M][ceil(K/128)].
+ *   offsets: NULL (dense, E = 1), or int32 [E + 1] (device, ascending, as
+ *     zffn_moe_sort writes it): rows offsets[e] .. offsets[e+1] - 1 of a are
+ *     multiplied with expert e's weights; rows of y outside every expert are
+ *     set to 0.
+ *   w: e4m3 [E][N][K], w_scale fp32 [E][ceil(N/128)][ceil(K/128)].
+ *   y: y_dtype (zffn_dtype) [M][N], overwritten.
+ * Requirements: 1 <= M <= 2^24, 1 <= N <= 2^20, 16 <= K <= 65536, K % 16 == 0,
+ * 1 <= E <= 4096, E * N < 2^31; a and w 16-byte aligned, scales and offsets
+ * 4-byte, y to its element (a 16-byte aligned y with N % 8 == 0 is written
+ * faster).  No workspace.  The gradient by a is the same product on transposed
+ * weights: bytes [K][N] and scales [ceil(K/128)][ceil(N/128)].
+ * Errors: INVALID_ARG, CUDA. */
+zffn_status zffn_fp8_matmul(const void *a, const float *a_scale, const void *w,
+                            const float *w_scale, const int32_t *offsets, int y_dtype, void *y,
+                            int M, int N, int K, int E, void *stream);
+
+/* The SwiGLU block on block-scaled weights, dense or grouped by expert:
+ *     h = quantise(silu(a . Wg^T) (*) (a . Wu^T))      (1 x 128 blocks, as above)
+ *     y = h . Wd^T
+ * with the products of zffn_fp8_matmul; SwiGLU and the quantisation are applied
+ * in fp32 before h is stored.
+ *   a: e4m3 [P][H] with a_scale [P][ceil(H/128)]; offsets as for zffn_fp8_matmul
+ *   (NULL: dense, E = 1).
+ *   Wg, Wu: e4m3 [E][I][H], sg, su fp32 [E][ceil(I/128)][ceil(H/128)].
+ *   Wd: e4m3 [E][H][I], sd fp32 [E][ceil(H/128)][ceil(I/128)].
+ *   y: y_dtype [P][H], overwritten; rows outside every expert are set to 0.
+ * Requirements: 1 <= P <= 2^24, H and I multiples of 16 in [16, 65536], E as
+ * above, alignments as above.  Uses library workspace for h (zffn_reserve with
+ * T * top_k >= P covers it).  Errors: INVALID_ARG, CUDA, NO_WORKSPACE. */
+zffn_status zffn_fp8_experts(const void *a, const float *a_scale, const int32_t *offsets,
+                             const void *Wg, const float *sg, const void *Wu, const float *su,
+                             const void *Wd, const float *sd, int y_dtype, void *y, int P, int H,
+                             int I, int E, void *stream);
+
+/* Sort of the (token, slot) pairs by expert, stable: pairs of one expert keep
+ * their order.  Pair f = t * top_k + j has key expert_ids[t][j]; a pair whose id
+ * is outside [0, E) belongs to no expert.
+ *   row_slot: output, int32 [T * top_k]: the pair of each sorted row, -1 for the
+ *     rows from offsets[E] on.
+ *   slot_row: output, int32 [T][top_k]: the sorted row of each pair, or -1.
+ *   offsets: output, int32 [E + 1]: expert e's rows are offsets[e] ..
+ *     offsets[e + 1] - 1.
+ * Requirements: T >= 1, 1 <= E <= 4096, 1 <= top_k <= 64, T * top_k <= 2^24,
+ * 4-byte aligned pointers.  No workspace.  Errors: INVALID_ARG, CUDA. */
+zffn_status zffn_moe_sort(const int32_t *expert_ids, int32_t *row_slot, int32_t *slot_row,
+                          int32_t *offsets, int T, int E, int top_k, void *stream);
+
+/* Tokens to sorted rows: xs[slot_row[t][j]] = x[t] for every pair with a row;
+ * rows with row_slot -1 are set to zero bytes.
+ *   x: [T] rows of row_bytes bytes of any type.  xs: output, [T * top_k] rows.
+ *   scale, xs_scale: NULL, or a second array moved the same way (the scales of
+ *     8-bit rows): fp32 [T][scale_cols] -> [T * top_k][scale_cols].
+ * Requirements as zffn_moe_sort; 1 <= row_bytes <= 2^20, 0 <= scale_cols <= 2^16;
+ * scale and xs_scale both NULL exactly when scale_cols is 0.  Copies are as
+ * wide as row_bytes and the pointers' alignment allow (16 bytes at best).
+ * Errors: INVALID_ARG, CUDA. */
+zffn_status zffn_moe_dispatch(const void *x, int64_t row_bytes, const float *scale,
+                              int64_t scale_cols, const int32_t *row_slot,
+                              const int32_t *slot_row, void *xs, float *xs_scale, int T, int top_k,
+                              void *stream);
+
+/* Sorted rows back to tokens: y[t] (+)= sum_j weights[t][j] rows[slot_row[t][j]],
+ * over the pairs with a row, j ascending, in fp32 (the same result every time).
+ *   rows: dtype [T * top_k][H].  weights: fp32 [T][top_k], or NULL for ones (which
+ *     makes this the gradient of zffn_moe_dispatch).  y: fp32 [T][H].
+ *   accumulate: 0 overwrites y, non-zero adds to it.
+ * Requirements as zffn_moe_sort; 1 <= H <= 65536; rows aligned to its element,
+ * the others to 4 bytes.  Errors: INVALID_ARG, CUDA. */
+zffn_status zffn_moe_combine(int dtype, const void *rows, const int32_t *slot_row,
+                             const float *weights, float *y, int T, int H, int top_k,
+                             int accumulate, void *stream);
+
+/* Gradients of zffn_moe_combine by its rows and its weights:
+ *     drows[r] = weights[t][j] dy[t]  for the pair (t, j) of row r (0 if none),
+ *     dweights[t][j] = sum_c dy[t][c] rows[slot_row[t][j]][c]  (0 without a row),
+ * the sums in fp32 in a fixed order.
+ *   dy: fp32 [T][H].  rows, drows: dtype [T * top_k][H].  weights, dweights: fp32
+ *   [T][top_k].  drows or dweights may be NULL (not wanted), not both; rows may
+ *   be NULL when dweights is, and weights when drows is.
+ * Requirements as zffn_moe_combine.  Errors: INVALID_ARG, CUDA. */
+zffn_status zffn_moe_combine_grad(int dtype, const float *dy, const void *rows,
+                                  const int32_t *row_slot, const int32_t *slot_row,
+                                  const float *weights, void *drows, float *dweights, int T, int H,
+                                  int top_k, void *stream);
+
+/* The routed block on block-scaled weights, from bf16 tokens to fp32 tokens:
+ *     y[t] (+)= sum_j expert_weights[t][j] FFN_{expert_ids[t][j]}(quantise(x[t]))
+ * composed of the entry points above (quantise, sort, dispatch, experts with
+ * bf16 rows, combine) in stream order, with their results in library
+ * workspace (see zffn_reserve).
+ *   x: bf16 [T][H]; expert_ids, expert_weights as for zffn_moe_swiglu_q4k (e.g.
+ *   from zffn_moe_router_topk); weights and scales as for zffn_fp8_experts.
+ *   y: fp32 [T][H].
+ * Errors: INVALID_ARG, CUDA, NO_WORKSPACE. */
+zffn_status zffn_moe_swiglu_fp8(const void *x, const int32_t *expert_ids,
+                                const float *expert_weights, const void *Wg, const float *sg,
+                                const void *Wu, const float *su, const void *Wd, const float *sd,
+                                float *y, int T, int H, int I, int E, int top_k, int accumulate,
+                                void *stream);
+
 /* Single-token dense block (T = 1) that allocates no device memory.  The
  * source pages have no counterpart of this entry point.  It is for callers
  * that cannot let the library call cudaMalloc/cudaFree during a call -- for

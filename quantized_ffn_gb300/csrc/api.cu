@@ -108,12 +108,14 @@ zffn_status ensure_workspace(size_t bytes, Workspace **out) {
 
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-// A failed host-side check: record why (zffn_last_error) and return INVALID_ARG.
+}  // namespace
+
 zffn_status invalid(const char *why) {
     t_last_error = why;
     return ZFFN_ERR_INVALID_ARG;
 }
 
+namespace {
 zffn_status check_shape(int T, int H, int I) {
     if (T < 1) return invalid("T must be at least 1");
     if (H < 256 || H > 16384 || H % 256 != 0)
@@ -122,6 +124,8 @@ zffn_status check_shape(int T, int H, int I) {
     return ZFFN_OK;
 }
 
+}  // namespace
+
 zffn_status to_status(cudaError_t e) {
     if (e == cudaSuccess) return ZFFN_OK;
     t_last_error = cudaGetErrorString(e);
@@ -129,7 +133,12 @@ zffn_status to_status(cudaError_t e) {
     return ZFFN_ERR_CUDA;
 }
 
-}  // namespace
+zffn_status workspace_at_least(size_t bytes, uint8_t **base) {
+    Workspace *w = nullptr;
+    const zffn_status st = ensure_workspace(bytes, &w);
+    if (st == ZFFN_OK) *base = static_cast<uint8_t *>(w->ptr);
+    return st;
+}
 
 void set_last_error(const char *what) { t_last_error = what; }
 
@@ -644,8 +653,9 @@ zffn_status zffn_reserve(int T_max, int H_max, int I_max, int E_max, int top_k_m
         return invalid("every size must be at least 1");
     if (device_info().device < 0) return ZFFN_ERR_CUDA;
     const Layout L = layout_for(T_max, H_max, I_max, E_max, top_k_max);
+    const size_t f8 = fp8_workspace_bytes(T_max, H_max, I_max, E_max, top_k_max);
     Workspace *w = nullptr;
-    return ensure_workspace(L.total, &w);
+    return ensure_workspace(f8 > L.total ? f8 : L.total, &w);
 }
 
 int zffn_single_token_launches(int H, int I, int E, int top_k) {

@@ -1,0 +1,422 @@
+// moe_sort.cu -- (token, slot) pairs sorted by expert, tokens' rows to their
+// sorted places and the weighted sum back, and the gradients of both.
+#include "moe_sort.h"
+
+#include "zffn_internal.cuh"
+
+namespace zffn {
+
+namespace {
+
+// ---------------------------------------------------------------------------
+// Sort: a stable counting sort.  Every warp owns a contiguous run of pairs and
+// a histogram over experts of its own; a pair's row is
+//   rows of lower experts + this expert's pairs of lower warps + those before it
+//   in its own warp's run,
+// so no atomics decide an order and the result is the same every time.  One
+// launch: a cluster of CTAs shares the warps' totals through distributed
+// shared memory.  Latency bound (16 bytes a pair move).
+// ---------------------------------------------------------------------------
+constexpr int kSortMaxWarps = 32;
+constexpr int kSortCluster = 8;
+
+__device__ __forceinline__ int ld_cluster_s32(uint32_t addr) {
+    int v;
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+// Shared memory: hist [warps][E], total [E] (this CTA's pairs of each expert),
+// base [E], 33 words of scan scratch.
+template <int CS>
+__global__ void __launch_bounds__(kSortMaxWarps * 32)
+    moe_sort_kernel(const int32_t *__restrict__ ids, int32_t *__restrict__ row_slot, int32_t *__restrict__ slot_row,
+                    int32_t *__restrict__ offsets, int P, int E) {
+    extern __shared__ int sm[];
+    const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int *hist = sm, *total = sm + warps * E, *base = total + E, *scratch = base + E;
+    const int rank = CS > 1 ? (int)cluster_ctarank() : 0;
+    for (int i = threadIdx.x; i < warps * E; i += blockDim.x) hist[i] = 0;
+    __syncthreads();
+    // this warp's run of pairs, a multiple of 32 long
+    const int64_t all = (int64_t)CS * warps;
+    const int64_t run = ((P + all - 1) / all + 31) / 32 * 32;
+    const int64_t lo = ((int64_t)rank * warps + warp) * run;
+    const int64_t hi = lo + run < P ? lo + run : P;
+    int *mine = hist + warp * E;
+    for (int64_t i = lo; i < hi; i += 32) {
+        int e = i + lane < hi ? __ldg(ids + i + lane) : -1;
+        if (e < 0 || e >= E) e = -1;
+        const unsigned same = __match_any_sync(0xffffffffu, e);
+        if (e >= 0 && lane == __ffs(same) - 1) mine[e] += __popc(same);
+        __syncwarp();
+    }
+    __syncthreads();
+    // each expert: exclusive sums over this CTA's warps, and the CTA's total
+    for (int e = threadIdx.x; e < E; e += blockDim.x) {
+        int n = 0;
+        for (int w = 0; w < warps; ++w) {
+            const int c = hist[w * E + e];
+            hist[w * E + e] = n;
+            n += c;
+        }
+        total[e] = n;
+    }
+    if (CS > 1) cluster_sync_all();
+    else __syncthreads();
+    // over the cluster: the expert's pairs in all CTAs (base, scanned below) and
+    // in the CTAs before this one (kept in total)
+    const uint32_t t_addr = smem_u32(total);
+    for (int e = threadIdx.x; e < E; e += blockDim.x) {
+        int n = 0, before = 0;
+        if (CS > 1) {
+#pragma unroll
+            for (int r = 0; r < CS; ++r) {
+                const int c = ld_cluster_s32(mapa_shared(t_addr + 4 * e, r));
+                if (r < rank) before += c;
+                n += c;
+            }
+        } else {
+            n = total[e];
+        }
+        base[e] = n;
+        // (the other CTAs still read total: what comes before is put into hist)
+        for (int w = 0; CS > 1 && w < warps; ++w) hist[w * E + e] += before;
+    }
+    __syncthreads();
+    // exclusive scan of base over the experts: contiguous shares, warp scans
+    const int per = (E + blockDim.x - 1) / blockDim.x;
+    const int e0 = threadIdx.x * per, e1 = min(E, e0 + per);
+    int sum = 0;
+    for (int e = e0; e < e1; ++e) sum += base[e];
+    int inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += t;
+    }
+    if (lane == 31) scratch[warp] = inc;
+    __syncthreads();
+    if (warp == 0) {
+        const int wt = lane < warps ? scratch[lane] : 0;
+        int winc = wt;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int t = __shfl_up_sync(0xffffffffu, winc, o);
+            if (lane >= o) winc += t;
+        }
+        scratch[lane] = winc - wt;
+        if (lane == 31) scratch[32] = winc;
+    }
+    __syncthreads();
+    int at = scratch[warp] + inc - sum;
+    for (int e = e0; e < e1; ++e) {
+        const int c = base[e];
+        base[e] = at;
+        if (rank == 0) offsets[e] = at;
+        at += c;
+    }
+    const int used = scratch[32];
+    if (rank == 0 && threadIdx.x == 0) offsets[E] = used;
+    __syncthreads();
+    for (int64_t i = lo; i < hi; i += 32) {
+        const bool in = i + lane < hi;
+        int e = in ? __ldg(ids + i + lane) : -1;
+        if (e < 0 || e >= E) e = -1;
+        const unsigned same = __match_any_sync(0xffffffffu, e);
+        int row = -1;
+        if (e >= 0) row = base[e] + mine[e] + __popc(same & ((1u << lane) - 1));
+        __syncwarp();
+        if (e >= 0 && lane == __ffs(same) - 1) mine[e] += __popc(same);
+        __syncwarp();
+        if (in) slot_row[i + lane] = row;
+        if (row >= 0) row_slot[row] = (int)(i + lane);
+        // a row from `used` on is nobody's: its own index is as good a place as any
+        if (in && i + lane >= used) row_slot[i + lane] = -1;
+    }
+    if (CS > 1) cluster_sync_all();   // no CTA leaves while another reads its totals
+}
+
+// ---------------------------------------------------------------------------
+// Rows to their sorted places.  One thread block per token: its row is read
+// once and written to each of its places.  Bound by HBM writes.
+// ---------------------------------------------------------------------------
+constexpr int kRowThreads = 128;
+
+template <typename V>
+__device__ __forceinline__ void copy_row(const V *__restrict__ src, V *__restrict__ dst, int64_t n, int64_t P,
+                                         const int32_t *rows, const int32_t *row_slot, int64_t t, int k) {
+    for (int64_t c = threadIdx.x; c < n; c += blockDim.x) {
+        const V v = __ldg(src + t * n + c);
+        for (int j = 0; j < k; ++j) {
+            const int64_t r = rows[j];
+            if (r >= 0 && r < P) dst[r * n + c] = v;
+        }
+    }
+    // rows of no pair: block t looks after rows t k .. t k + k - 1
+    for (int j = 0; j < k; ++j) {
+        const int64_t r = t * k + j;
+        if (row_slot[r] >= 0) continue;
+        for (int64_t c = threadIdx.x; c < n; c += blockDim.x) dst[r * n + c] = V{};
+    }
+}
+
+template <typename V>
+__global__ void __launch_bounds__(kRowThreads)
+    moe_dispatch_kernel(const V *__restrict__ x, int64_t n, const uint32_t *__restrict__ scale, int64_t ns,
+                        const int32_t *__restrict__ row_slot, const int32_t *__restrict__ slot_row, V *__restrict__ xs,
+                        uint32_t *__restrict__ xs_scale, int T, int k) {
+    __shared__ int32_t rows[64];
+    const int64_t t = blockIdx.x, P = (int64_t)T * k;
+    if ((int)threadIdx.x < k) rows[threadIdx.x] = slot_row[t * k + threadIdx.x];
+    __syncthreads();
+    copy_row(x, xs, n, P, rows, row_slot, t, k);
+    if (ns) copy_row(scale, xs_scale, ns, P, rows, row_slot, t, k);
+}
+
+// ---------------------------------------------------------------------------
+// Vectors of the row type: VEC elements as fp32.
+// ---------------------------------------------------------------------------
+template <int VEC> struct Vec { float v[VEC]; };
+
+template <int VEC> __device__ __forceinline__ Vec<VEC> load_vec(const float *p) {
+    Vec<VEC> r;
+    if (VEC == 8) {
+#pragma unroll
+        for (int i = 0; i < VEC / 4; ++i) {
+            const float4 f = __ldg(reinterpret_cast<const float4 *>(p) + i);
+            r.v[4 * i] = f.x; r.v[4 * i + 1] = f.y; r.v[4 * i + 2] = f.z; r.v[4 * i + 3] = f.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) r.v[i] = __ldg(p + i);
+    }
+    return r;
+}
+template <int VEC> __device__ __forceinline__ Vec<VEC> load_vec(const __nv_bfloat16 *p) {
+    Vec<VEC> r;
+    if (VEC == 8) {
+        const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p));
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < VEC / 2; ++i) {
+            r.v[2 * i] = __uint_as_float(w[i] << 16);
+            r.v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) r.v[i] = __bfloat162float(p[i]);
+    }
+    return r;
+}
+template <int VEC> __device__ __forceinline__ void store_vec(float *p, const Vec<VEC> &r) {
+    if (VEC == 8) {
+#pragma unroll
+        for (int i = 0; i < VEC / 4; ++i)
+            reinterpret_cast<float4 *>(p)[i] = make_float4(r.v[4 * i], r.v[4 * i + 1], r.v[4 * i + 2], r.v[4 * i + 3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) p[i] = r.v[i];
+    }
+}
+// (one rounding to bf16, to nearest even)
+template <int VEC> __device__ __forceinline__ void store_vec(__nv_bfloat16 *p, const Vec<VEC> &r) {
+    if (VEC == 8) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < VEC / 2; ++i) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(r.v[2 * i], r.v[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t *>(&b);
+        }
+        *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) p[i] = __float2bfloat16_rn(r.v[i]);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Sorted rows back to tokens: one thread block per token, fp32 sums over its
+// slots in order.  Bound by HBM reads.
+// ---------------------------------------------------------------------------
+template <typename T, int VEC>
+__global__ void __launch_bounds__(kRowThreads)
+    moe_combine_kernel(const T *__restrict__ rows, const int32_t *__restrict__ slot_row, const float *__restrict__ weights,
+                       float *__restrict__ y, int Tn, int H, int k, bool accumulate) {
+    __shared__ int32_t row[64];
+    __shared__ float wt[64];
+    const int64_t t = blockIdx.x, P = (int64_t)Tn * k;
+    if ((int)threadIdx.x < k) {
+        const int r = slot_row[t * k + threadIdx.x];
+        row[threadIdx.x] = r < P ? r : -1;
+        wt[threadIdx.x] = weights ? weights[t * k + threadIdx.x] : 1.0f;
+    }
+    __syncthreads();
+    for (int c = threadIdx.x * VEC; c < H; c += kRowThreads * VEC) {
+        Vec<VEC> acc;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) acc.v[i] = 0.0f;
+        float *py = y + t * H + c;
+        if (accumulate) {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) acc.v[i] = py[i];
+        }
+#pragma unroll 8
+        for (int j = 0; j < k; ++j) {
+            const int r = row[j];
+            if (r < 0) continue;
+            const Vec<VEC> v = load_vec<VEC>(rows + (int64_t)r * H + c);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) acc.v[i] = fmaf(wt[j], v.v[i], acc.v[i]);
+        }
+        store_vec<VEC>(py, acc);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Gradients of the combine: a warp per (token, slot); the token's dy row is
+// shared by the block's warps through L1.  Bound by HBM.
+// ---------------------------------------------------------------------------
+constexpr int kGradWarps = 8;
+
+template <typename T, int VEC>
+__global__ void __launch_bounds__(kGradWarps * 32)
+    moe_combine_grad_kernel(const float *__restrict__ dy, const T *__restrict__ rows, const int32_t *__restrict__ row_slot,
+                            const int32_t *__restrict__ slot_row, const float *__restrict__ weights,
+                            T *__restrict__ drows, float *__restrict__ dweights, int Tn, int H, int k) {
+    const int64_t t = blockIdx.x, P = (int64_t)Tn * k;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const float *d = dy + t * H;
+    for (int j = warp; j < k; j += kGradWarps) {
+        const int64_t f = t * k + j;
+        const int64_t r = slot_row[f];
+        if (r >= 0 && r < P) {
+            const float w = drows ? weights[f] : 0.0f;
+            float dot = 0.0f;
+#pragma unroll 4
+            for (int c = lane * VEC; c < H; c += 32 * VEC) {
+                const Vec<VEC> g = load_vec<VEC>(d + c);
+                if (dweights) {
+                    const Vec<VEC> v = load_vec<VEC>(rows + r * H + c);
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) dot = fmaf(g.v[i], v.v[i], dot);
+                }
+                if (drows) {
+                    Vec<VEC> o;
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) o.v[i] = w * g.v[i];
+                    store_vec<VEC>(drows + r * H + c, o);
+                }
+            }
+            if (dweights) {
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+                if (lane == 0) dweights[f] = dot;
+            }
+        } else if (dweights && lane == 0) {
+            dweights[f] = 0.0f;
+        }
+        // row f itself, where no pair has it
+        if (drows && row_slot[f] < 0) {
+            Vec<VEC> o;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) o.v[i] = 0.0f;
+            for (int c = lane * VEC; c < H; c += 32 * VEC) store_vec<VEC>(drows + f * H + c, o);
+        }
+    }
+}
+
+inline uintptr_t bits(const void *p) { return reinterpret_cast<uintptr_t>(p); }
+
+template <typename V>
+cudaError_t dispatch_as(const void *x, int64_t row_bytes, const void *scale, int64_t scale_bytes,
+                        const int32_t *row_slot, const int32_t *slot_row, void *xs, void *xs_scale, int T, int k,
+                        cudaStream_t s) {
+    moe_dispatch_kernel<V><<<T, kRowThreads, 0, s>>>(
+        static_cast<const V *>(x), row_bytes / (int64_t)sizeof(V), static_cast<const uint32_t *>(scale), scale_bytes / 4,
+        row_slot, slot_row, static_cast<V *>(xs), static_cast<uint32_t *>(xs_scale), T, k);
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t combine_as(const T *rows, const int32_t *slot_row, const float *weights, float *y, int Tn, int H, int k,
+                       bool accumulate, cudaStream_t s) {
+    if (((bits(rows) | bits(y)) & 15) == 0 && H % 8 == 0)
+        moe_combine_kernel<T, 8><<<Tn, kRowThreads, 0, s>>>(rows, slot_row, weights, y, Tn, H, k, accumulate);
+    else
+        moe_combine_kernel<T, 1><<<Tn, kRowThreads, 0, s>>>(rows, slot_row, weights, y, Tn, H, k, accumulate);
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t grad_as(const float *dy, const T *rows, const int32_t *row_slot, const int32_t *slot_row,
+                    const float *weights, T *drows, float *dweights, int Tn, int H, int k, cudaStream_t s) {
+    if (((bits(dy) | bits(rows) | bits(drows)) & 15) == 0 && H % 8 == 0)
+        moe_combine_grad_kernel<T, 8><<<Tn, kGradWarps * 32, 0, s>>>(dy, rows, row_slot, slot_row, weights, drows, dweights, Tn, H, k);
+    else
+        moe_combine_grad_kernel<T, 1><<<Tn, kGradWarps * 32, 0, s>>>(dy, rows, row_slot, slot_row, weights, drows, dweights, Tn, H, k);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_moe_sort(const int32_t *ids, int32_t *row_slot, int32_t *slot_row, int32_t *offsets,
+                            int T, int E, int k, cudaStream_t s) {
+    const int64_t P = (int64_t)T * k;
+    // as many warps as their histograms fit into 160 KB (E = 4096: 8), and no
+    // more than the pairs fill
+    int warps = (160 * 1024) / (4 * E);
+    if (warps > kSortMaxWarps) warps = kSortMaxWarps;
+    const bool one = P <= 32 * kSortMaxWarps;
+    if (one && warps > (P + 31) / 32) warps = (int)((P + 31) / 32);
+    const int smem = 4 * ((warps + 2) * E + 33);
+    const void *fn = one ? (const void *)moe_sort_kernel<1> : (const void *)moe_sort_kernel<kSortCluster>;
+    const cudaError_t e = ensure_dynamic_smem(fn, (size_t)smem);
+    if (e != cudaSuccess) return e;
+    if (one) {
+        moe_sort_kernel<1><<<1, warps * 32, smem, s>>>(ids, row_slot, slot_row, offsets, (int)P, E);
+        return cudaGetLastError();
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kSortCluster);
+    cfg.blockDim = dim3(warps * 32);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kSortCluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, moe_sort_kernel<kSortCluster>, ids, row_slot, slot_row, offsets, (int)P, E);
+}
+
+cudaError_t launch_moe_dispatch(const void *x, int64_t row_bytes, const void *scale, int64_t scale_bytes,
+                                const int32_t *row_slot, const int32_t *slot_row, void *xs, void *xs_scale,
+                                int T, int k, cudaStream_t s) {
+    const uintptr_t a = bits(x) | bits(xs) | (uintptr_t)row_bytes;   // the widest copy that every row allows
+    if ((a & 15) == 0) return dispatch_as<uint4>(x, row_bytes, scale, scale_bytes, row_slot, slot_row, xs, xs_scale, T, k, s);
+    if ((a & 3) == 0) return dispatch_as<uint32_t>(x, row_bytes, scale, scale_bytes, row_slot, slot_row, xs, xs_scale, T, k, s);
+    if ((a & 1) == 0) return dispatch_as<uint16_t>(x, row_bytes, scale, scale_bytes, row_slot, slot_row, xs, xs_scale, T, k, s);
+    return dispatch_as<uint8_t>(x, row_bytes, scale, scale_bytes, row_slot, slot_row, xs, xs_scale, T, k, s);
+}
+
+cudaError_t launch_moe_combine(int dtype, const void *rows, const int32_t *slot_row, const float *weights,
+                               float *y, int T, int H, int k, bool accumulate, cudaStream_t s) {
+    if (dtype == ZFFN_DT_F32)
+        return combine_as(static_cast<const float *>(rows), slot_row, weights, y, T, H, k, accumulate, s);
+    return combine_as(static_cast<const __nv_bfloat16 *>(rows), slot_row, weights, y, T, H, k, accumulate, s);
+}
+
+cudaError_t launch_moe_combine_grad(int dtype, const float *dy, const void *rows, const int32_t *row_slot,
+                                    const int32_t *slot_row, const float *weights, void *drows,
+                                    float *dweights, int T, int H, int k, cudaStream_t s) {
+    if (dtype == ZFFN_DT_F32)
+        return grad_as(dy, static_cast<const float *>(rows), row_slot, slot_row, weights, static_cast<float *>(drows),
+                       dweights, T, H, k, s);
+    return grad_as(dy, static_cast<const __nv_bfloat16 *>(rows), row_slot, slot_row, weights,
+                   static_cast<__nv_bfloat16 *>(drows), dweights, T, H, k, s);
+}
+
+}  // namespace zffn

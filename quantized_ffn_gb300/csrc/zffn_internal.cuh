@@ -467,6 +467,15 @@ struct DeviceInfo {
 };
 const DeviceInfo &device_info();   // current device (cached per device)
 void set_last_error(const char *what);   // text returned by zffn_last_error()
+// A failed host-side check: record why (zffn_last_error) and return INVALID_ARG.
+zffn_status invalid(const char *why);
+// A CUDA status as the library's; an error is recorded for zffn_last_error.
+zffn_status to_status(cudaError_t e);
+// The current device's workspace, grown to at least `bytes`.  Its first 256 bytes
+// belong to the one-launch routed path (a count that outlives a call).
+zffn_status workspace_at_least(size_t bytes, uint8_t **base);
+// Workspace of the block-scaled 8-bit entry points for calls up to these sizes.
+size_t fp8_workspace_bytes(int T, int H, int I, int E, int k);
 // Raise `fn`'s dynamic shared-memory limit on the current device to at least
 // `bytes` (never lowers it).  Thread-safe: one lock covers the check, the
 // attribute call and the per-device record of the largest request so far.

@@ -10,7 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -63,6 +63,15 @@ def load() -> ctypes.CDLL:
                 "zffn_moe_swiglu_q4k_wd": ([P, P, P, P, P, P, I32, P, I32, I32, I32, I32, I32, P], I32),
                 "zffn_moe_swiglu_q4k_scaled": ([P, P, P, P, P, P, P, I32, P, I32, I32, I32, I32, I32, I32, P],
                                                I32),
+                "zffn_fp8_quantize": ([I32, P, P, P, I64, I64, I32, P], I32),
+                "zffn_fp8_dequant": ([P, P, P, I64, I64, I32, P], I32),
+                "zffn_fp8_matmul": ([P, P, P, P, P, I32, P, I32, I32, I32, I32, P], I32),
+                "zffn_fp8_experts": ([P, P, P, P, P, P, P, P, P, I32, P, I32, I32, I32, I32, P], I32),
+                "zffn_moe_sort": ([P, P, P, P, I32, I32, I32, P], I32),
+                "zffn_moe_dispatch": ([P, I64, P, I64, P, P, P, P, I32, I32, P], I32),
+                "zffn_moe_combine": ([I32, P, P, P, P, I32, I32, I32, I32, P], I32),
+                "zffn_moe_combine_grad": ([I32, P, P, P, P, P, P, P, I32, I32, I32, P], I32),
+                "zffn_moe_swiglu_fp8": ([P, P, P, P, P, P, P, P, P, P, I32, I32, I32, I32, I32, I32, P], I32),
                 "zffn_rmsnorm_bf16": ([P, P, ctypes.c_float, P, I32, I32, P], I32),
                 "zffn_swiglu_q4k_prenorm_residual": ([P, P, ctypes.c_float, P, P, P, I32, I32, I32, P],
                                                      I32),
@@ -289,6 +298,227 @@ def moe_router_topk(logits: torch.Tensor, top_k: int, expert_ids: Optional[torch
         _cuda(expert_weights, "expert_weights", torch.float32), T, E, top_k, _stream(stream)),
         "zffn_moe_router_topk")
     return expert_ids, expert_weights
+
+
+# ---- layers in 8-bit floating point ---------------------------------------------------------
+# e4m3 values are torch.float8_e4m3fn tensors (torch.uint8 tensors of the same bytes are taken
+# too) with one fp32 scale for each block of 128 (include/zffn.h).
+
+DT_F32, DT_BF16 = 0, 1
+_DTYPES = {torch.float32: DT_F32, torch.bfloat16: DT_BF16}
+
+
+def _dtype(t: torch.Tensor, name: str) -> int:
+    d = _DTYPES.get(t.dtype)
+    if d is None:
+        raise ValueError(f"{name} must be torch.float32 or torch.bfloat16, got {t.dtype}")
+    return d
+
+
+def _f8(t: torch.Tensor, name: str):
+    return _cuda(t, name, torch.uint8 if t.dtype == torch.uint8 else torch.float8_e4m3fn)
+
+
+def _shaped(t: torch.Tensor, name: str, dtype, shape):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    return _cuda(t, name, dtype)
+
+
+def _blocks(n: int) -> int:
+    return -(-n // 128)
+
+
+def fp8_quantize(x: torch.Tensor, block_rows: int = 1, q: Optional[torch.Tensor] = None,
+                 scale: Optional[torch.Tensor] = None, stream=None):
+    """(q float8_e4m3fn [R, C], scale fp32 [ceil(R / block_rows), ceil(C / 128)]) of x (bf16 or
+    fp32 [R, C]): power-of-two scales for blocks of block_rows (1 or 128) x 128."""
+    R, C = x.shape
+    if q is None:
+        q = torch.empty((R, C), dtype=torch.float8_e4m3fn, device=x.device)
+    if block_rows not in (1, 128):
+        raise ValueError("block_rows must be 1 or 128")
+    shape = (-(-R // block_rows), _blocks(C))
+    if scale is None:
+        scale = torch.empty(shape, dtype=torch.float32, device=x.device)
+    if q.shape != x.shape:
+        raise ValueError(f"q must have shape {tuple(x.shape)}, got {tuple(q.shape)}")
+    _check(load().zffn_fp8_quantize(_dtype(x, "x"), _cuda(x, "x"), _f8(q, "q"),
+                                    _shaped(scale, "scale", torch.float32, shape), R, C, block_rows,
+                                    _stream(stream)), "zffn_fp8_quantize")
+    return q, scale
+
+
+def fp8_dequant(q: torch.Tensor, scale: torch.Tensor, block_rows: int = 1,
+                out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """fp32 [R, C]: each e4m3 value times its block's scale."""
+    R, C = q.shape
+    if block_rows not in (1, 128):
+        raise ValueError("block_rows must be 1 or 128")
+    if out is None:
+        out = torch.empty((R, C), dtype=torch.float32, device=q.device)
+    _check(load().zffn_fp8_dequant(
+        _f8(q, "q"), _shaped(scale, "scale", torch.float32, (-(-R // block_rows), _blocks(C))),
+        _shaped(out, "out", torch.float32, (R, C)), R, C, block_rows, _stream(stream)), "zffn_fp8_dequant")
+    return out
+
+
+def _offsets(offsets: Optional[torch.Tensor], E: int):
+    return None if offsets is None else _shaped(offsets, "offsets", torch.int32, (E + 1,))
+
+
+def fp8_matmul(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
+               offsets: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+               dtype=torch.float32, stream=None) -> torch.Tensor:
+    """y[M, N] = (a * a_scale) (w * w_scale)^T of e4m3 matrices with scales for blocks of 128:
+    a [M, K] (scales [M, K/128]), w [N, K] (scales [N/128, K/128]).  With offsets (int32 [E + 1],
+    MoePlan.offsets) w is [E, N, K] and rows offsets[e]:offsets[e + 1] take expert e; rows of no
+    expert become 0.  y: given (fp32 or bf16), or made with `dtype`."""
+    M, K = a.shape
+    E = 1 if offsets is None else w.shape[0]
+    N = w.shape[-2]
+    lead = () if offsets is None else (E,)
+    if y is None:
+        y = torch.empty((M, N), dtype=dtype, device=a.device)
+    if tuple(w.shape) != (*lead, N, K):
+        raise ValueError(f"w must have shape {(*lead, 'N', K)}, got {tuple(w.shape)}")
+    _check(load().zffn_fp8_matmul(
+        _f8(a, "a"), _shaped(a_scale, "a_scale", torch.float32, (M, _blocks(K))), _f8(w, "w"),
+        _shaped(w_scale, "w_scale", torch.float32, (*lead, _blocks(N), _blocks(K))), _offsets(offsets, E),
+        _dtype(y, "y"), _shaped(y, "y", y.dtype, (M, N)), M, N, K, E, _stream(stream)), "zffn_fp8_matmul")
+    return y
+
+
+def fp8_experts(a: torch.Tensor, a_scale: torch.Tensor, Wg: torch.Tensor, sg: torch.Tensor, Wu: torch.Tensor,
+                su: torch.Tensor, Wd: torch.Tensor, sd: torch.Tensor, offsets: Optional[torch.Tensor] = None,
+                y: Optional[torch.Tensor] = None, dtype=torch.bfloat16, stream=None) -> torch.Tensor:
+    """y[P, H] = quantise(silu(a Wg^T) * (a Wu^T)) Wd^T on e4m3 weights Wg, Wu [I, H], Wd [H, I]
+    with scales for blocks of 128; with offsets the weights are stacked [E, ...] and the rows of
+    each expert take its own (rows of no expert become 0)."""
+    P, H = a.shape
+    E = 1 if offsets is None else Wg.shape[0]
+    I = Wg.shape[-2]
+    lead = () if offsets is None else (E,)
+    if y is None:
+        y = torch.empty((P, H), dtype=dtype, device=a.device)
+    for t, name, shape in ((Wg, "Wg", (I, H)), (Wu, "Wu", (I, H)), (Wd, "Wd", (H, I))):
+        if tuple(t.shape) != (*lead, *shape):
+            raise ValueError(f"{name} must have shape {(*lead, *shape)}, got {tuple(t.shape)}")
+    f32, bi, bh = torch.float32, _blocks(I), _blocks(H)
+    _check(load().zffn_fp8_experts(
+        _f8(a, "a"), _shaped(a_scale, "a_scale", f32, (P, bh)), _offsets(offsets, E), _f8(Wg, "Wg"),
+        _shaped(sg, "sg", f32, (*lead, bi, bh)), _f8(Wu, "Wu"), _shaped(su, "su", f32, (*lead, bi, bh)),
+        _f8(Wd, "Wd"), _shaped(sd, "sd", f32, (*lead, bh, bi)), _dtype(y, "y"), _shaped(y, "y", y.dtype, (P, H)),
+        P, H, I, E, _stream(stream)), "zffn_fp8_experts")
+    return y
+
+
+class MoePlan(NamedTuple):
+    """(token, slot) pairs sorted by expert: row_slot int32 [T * top_k] (the pair t * top_k + j of
+    each row, -1 past the last expert), slot_row int32 [T, top_k] (the row of each pair, or -1),
+    offsets int32 [E + 1] (expert e's rows are offsets[e]:offsets[e + 1])."""
+    row_slot: torch.Tensor
+    slot_row: torch.Tensor
+    offsets: torch.Tensor
+
+
+def moe_sort(expert_ids: torch.Tensor, E: int, plan: Optional[MoePlan] = None, stream=None) -> MoePlan:
+    """The stable sort of expert_ids (int32 [T, top_k], e.g. from moe_router_topk) by expert; ids
+    outside [0, E) get no row."""
+    T, k = expert_ids.shape
+    if plan is None:
+        dev = expert_ids.device
+        plan = MoePlan(torch.empty((T * k,), dtype=torch.int32, device=dev),
+                       torch.empty((T, k), dtype=torch.int32, device=dev),
+                       torch.empty((E + 1,), dtype=torch.int32, device=dev))
+    _check(load().zffn_moe_sort(
+        _cuda(expert_ids, "expert_ids", torch.int32), _shaped(plan.row_slot, "row_slot", torch.int32, (T * k,)),
+        _shaped(plan.slot_row, "slot_row", torch.int32, (T, k)),
+        _shaped(plan.offsets, "offsets", torch.int32, (E + 1,)), T, E, k, _stream(stream)), "zffn_moe_sort")
+    return plan
+
+
+def moe_dispatch(x: torch.Tensor, plan: MoePlan, scale: Optional[torch.Tensor] = None,
+                 out: Optional[torch.Tensor] = None, scale_out: Optional[torch.Tensor] = None, stream=None):
+    """xs[T * top_k, H]: every token's row of x (any type) at its sorted places, 0 in rows of no
+    pair.  With scale (fp32 [T, C], the scales of 8-bit rows) returns (xs, scales moved alike)."""
+    T, H = x.shape
+    k = plan.slot_row.shape[1]
+    P = T * k
+    if out is None:
+        out = torch.empty((P, H), dtype=x.dtype, device=x.device)
+    C = 0
+    if scale is not None:
+        C = scale.shape[1]
+        if scale_out is None:
+            scale_out = torch.empty((P, C), dtype=torch.float32, device=x.device)
+    _check(load().zffn_moe_dispatch(
+        _cuda(x, "x"), H * x.element_size(), None if scale is None else _shaped(scale, "scale", torch.float32, (T, C)),
+        C, _shaped(plan.row_slot, "row_slot", torch.int32, (P,)), _shaped(plan.slot_row, "slot_row", torch.int32, (T, k)),
+        _shaped(out, "out", x.dtype, (P, H)),
+        None if scale is None else _shaped(scale_out, "scale_out", torch.float32, (P, C)), T, k,
+        _stream(stream)), "zffn_moe_dispatch")
+    return out if scale is None else (out, scale_out)
+
+
+def moe_combine(rows: torch.Tensor, plan: MoePlan, weights: Optional[torch.Tensor] = None,
+                y: Optional[torch.Tensor] = None, accumulate: bool = False, stream=None) -> torch.Tensor:
+    """y[T, H] fp32 (+)= sum_j weights[t, j] rows[row of (t, j)] (rows bf16 or fp32 [T * top_k, H];
+    weights fp32 [T, top_k], or None for ones: the gradient of moe_dispatch)."""
+    T, k = plan.slot_row.shape
+    H = rows.shape[1]
+    if y is None:
+        if accumulate:
+            raise ValueError("accumulate=True needs y")
+        y = torch.empty((T, H), dtype=torch.float32, device=rows.device)
+    _check(load().zffn_moe_combine(
+        _dtype(rows, "rows"), _shaped(rows, "rows", rows.dtype, (T * k, H)),
+        _cuda(plan.slot_row, "slot_row", torch.int32),
+        None if weights is None else _shaped(weights, "weights", torch.float32, (T, k)),
+        _shaped(y, "y", torch.float32, (T, H)), T, H, k, int(bool(accumulate)), _stream(stream)), "zffn_moe_combine")
+    return y
+
+
+def moe_combine_grad(dy: torch.Tensor, rows: torch.Tensor, plan: MoePlan, weights: torch.Tensor,
+                     drows: Optional[torch.Tensor] = None, dweights: Optional[torch.Tensor] = None, stream=None):
+    """(drows [T * top_k, H] of rows' type, dweights fp32 [T, top_k]): the gradients of
+    moe_combine(rows, plan, weights) for dy fp32 [T, H]; drows is 0 in rows of no pair."""
+    T, k = plan.slot_row.shape
+    H = rows.shape[1]
+    if drows is None:
+        drows = torch.empty_like(rows)
+    if dweights is None:
+        dweights = torch.empty((T, k), dtype=torch.float32, device=rows.device)
+    _check(load().zffn_moe_combine_grad(
+        _dtype(rows, "rows"), _shaped(dy, "dy", torch.float32, (T, H)), _shaped(rows, "rows", rows.dtype, (T * k, H)),
+        _shaped(plan.row_slot, "row_slot", torch.int32, (T * k,)), _cuda(plan.slot_row, "slot_row", torch.int32),
+        _shaped(weights, "weights", torch.float32, (T, k)), _shaped(drows, "drows", rows.dtype, (T * k, H)),
+        _shaped(dweights, "dweights", torch.float32, (T, k)), T, H, k, _stream(stream)), "zffn_moe_combine_grad")
+    return drows, dweights
+
+
+def moe_swiglu_fp8(x: torch.Tensor, expert_ids: torch.Tensor, expert_weights: torch.Tensor, Wg: torch.Tensor,
+                   sg: torch.Tensor, Wu: torch.Tensor, su: torch.Tensor, Wd: torch.Tensor, sd: torch.Tensor,
+                   y: Optional[torch.Tensor] = None, accumulate: bool = False, stream=None) -> torch.Tensor:
+    """Routed experts on e4m3 weights: y[T, H] fp32 (+)= sum_j w[t, j] FFN_{ids[t, j]}(quantise(x[t])),
+    x bf16 [T, H], weights stacked [E, ...] as for fp8_experts."""
+    T, H = x.shape
+    E, I, _ = Wg.shape
+    k = expert_ids.shape[1]
+    if y is None:
+        if accumulate:
+            raise ValueError("accumulate=True needs y")
+        y = torch.empty((T, H), dtype=torch.float32, device=x.device)
+    for t, name, shape in ((Wg, "Wg", (E, I, H)), (Wu, "Wu", (E, I, H)), (Wd, "Wd", (E, H, I))):
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    f32, bi, bh = torch.float32, _blocks(I), _blocks(H)
+    _check(load().zffn_moe_swiglu_fp8(
+        _cuda(x, "x", torch.bfloat16), _shaped(expert_ids, "expert_ids", torch.int32, (T, k)),
+        _shaped(expert_weights, "expert_weights", f32, (T, k)), _f8(Wg, "Wg"), _shaped(sg, "sg", f32, (E, bi, bh)),
+        _f8(Wu, "Wu"), _shaped(su, "su", f32, (E, bi, bh)), _f8(Wd, "Wd"), _shaped(sd, "sd", f32, (E, bh, bi)),
+        _shaped(y, "y", f32, (T, H)), T, H, I, E, k, int(bool(accumulate)), _stream(stream)), "zffn_moe_swiglu_fp8")
+    return y
 
 
 def _host(t: torch.Tensor, name: str, dtype, shape):
