@@ -1,91 +1,472 @@
-// fp8_matmul.cu -- products of block-scaled e4m3 matrices, dense or grouped by
-// expert, plain or with SwiGLU and quantisation of the result.
-//
-// One warp per output block of 1 row x 128 columns; every lane sums four
-// columns over K on the CUDA cores.  The simplest form that covers every size.
+// fp8_matmul.cu -- products of block-scaled e4m3 matrices on the 5th-generation
+// tensor cores, dense or grouped by expert, plain or with SwiGLU and
+// quantisation of the result:
+//     y[m][n] = sum_b sa[m][b] sw[n/128][b] sum_{k in block b} a[m][k] w[n][k]
+// The scales are any fp32 values, so a block's product (K = 128, four MMAs of
+// K = 32) is one accumulation in tensor memory, and the sum over blocks is kept
+// in registers: acc += d * (sa * sw), one fp32 multiply-add per value and block
+// (the scales' product is rounded once before).
+#include <cudaTypedefs.h>
+
 #include "fp8.h"
 #include "zffn_internal.cuh"
 
 namespace zffn {
+namespace f8 {
 
-namespace {
+// ---- pieces -----------------------------------------------------------------
 
-__device__ __forceinline__ void f8x4_to_f32(uint32_t v, float (&f)[4]) {
-    uint32_t a, b;
-    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
-        : "=r"(a), "=r"(b)
-        : "r"(v));
-    f[0] = half_bits_to_float(a); f[1] = half_bits_to_float(a >> 16);
-    f[2] = half_bits_to_float(b); f[3] = half_bits_to_float(b >> 16);
+// D[tmem] (+)= A[smem desc] * B[smem desc]^T, e4m3 inputs, fp32 accumulate.
+__device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
 }
+// Instruction descriptor: A = B = e4m3 (format code 0), D = fp32, both K-major.
+__host__ __device__ constexpr uint32_t idesc_f8_f32(int M, int N) {
+    return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ void named_barrier(int id, int threads) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ float swiglu(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
 
-// sum over K of row m of a and row n of expert e's w, with both scales
-__device__ float dot_row(const uint8_t *a, const float *as, const uint8_t *w, const float *ws, int K) {
-    float acc = 0.0f;
-    for (int b = 0; b * kF8Block < K; ++b) {
-        const int k1 = min(K, (b + 1) * kF8Block);
-        float s = 0.0f;
-        for (int k = b * kF8Block; k < k1; k += 4) {
-            float x[4], y[4];
-            f8x4_to_f32(*reinterpret_cast<const uint32_t *>(a + k), x);
-            f8x4_to_f32(*reinterpret_cast<const uint32_t *>(w + k), y);
+// A tile of rows of one expert (e == E: rows that belong to no expert).
+struct RowTile {
+    int e, row0, rows;
+};
+// Row tile t of a call: every expert's rows in tiles of at most `tr`, experts in
+// order, then the rows past the last expert.  Called by one full warp; false
+// past the last tile.  offsets are kept within [0, M] whatever they hold.
+__device__ __forceinline__ bool row_tile(const int32_t *offsets, int E, int M, int tr, int t, RowTile &out) {
+    const int lane = threadIdx.x & 31;
+    if (!offsets) {
+        out = {0, t * tr, min(tr, M - t * tr)};
+        return out.rows > 0;
+    }
+    const int per = (E + 32) / 32, g0 = min(lane * per, E + 1), g1 = min(g0 + per, E + 1);
+    auto lo = [&](int g) { return min(max(__ldg(offsets + g), 0), M); };
+    auto hi = [&](int g) { return g < E ? min(max(__ldg(offsets + g + 1), 0), M) : M; };
+    int n = 0;
+    for (int g = g0; g < g1; ++g) n += (max(hi(g) - lo(g), 0) + tr - 1) / tr;
+    int inc = n;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s = fmaf(x[i], y[i], s);
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += v;
+    }
+    int left = t - (inc - n);
+    const bool mine = left >= 0 && left < n;
+    if (mine) {
+        for (int g = g0; g < g1; ++g) {
+            const int r = max(hi(g) - lo(g), 0), c = (r + tr - 1) / tr;
+            if (left < c) {
+                out = {g, lo(g) + left * tr, min(tr, r - left * tr)};
+                break;
+            }
+            left -= c;
         }
-        acc = fmaf(s, as[b] * ws[b], acc);
     }
-    return acc;
+    const unsigned who = __ballot_sync(0xffffffffu, mine);
+    if (!who) return false;
+    const int src = __ffs(who) - 1;
+    out.e = __shfl_sync(0xffffffffu, out.e, src);
+    out.row0 = __shfl_sync(0xffffffffu, out.row0, src);
+    out.rows = __shfl_sync(0xffffffffu, out.rows, src);
+    return true;
 }
 
-__global__ void __launch_bounds__(128) fp8_matmul_kernel(Fp8Args p) {
-    const int nb = (int)f8_blocks(p.N), kb = (int)f8_blocks(p.K), lane = threadIdx.x & 31;
-    const int64_t unit = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-    const int64_t m = unit / nb;
-    const int b = (int)(unit - m * nb);
-    if (m >= p.M) return;
-    int e = 0;
-    if (p.offsets) {
-        while (e < p.E && !(m >= p.offsets[e] && m < p.offsets[e + 1])) ++e;
+struct Params {
+    const float *sa, *sw0, *sw1;
+    const int32_t *offsets;
+    void *y;
+    float *y_scale;
+    int *err;
+    int M, N, K, E;
+    int row_tiles;      // bound of the number of row tiles
+    int y_bf16;         // plain: y is bf16 (else fp32)
+    int vec;            // y's rows take 4-element stores
+};
+struct Maps {
+    CUtensorMap a, w0, w1;
+};
+
+// ---------------------------------------------------------------------------
+// Few rows an expert: the weights on the MMA's M side.  A block takes 128 rows
+// of W (GU: 128 gate and 128 up rows) times TN rows of a; a cluster of
+// blocks splits K and joins through distributed shared memory in rank order, so
+// that the result is the same every time.  Bound by HBM: every weight byte is
+// read once, by TMA, into a ring.
+//
+// Roles: warps 0 .. 4 NW - 1 take a block's product out of tensor memory, scale
+// and sum it in registers, and write the result; then one warp loads by TMA and
+// one issues the MMAs.
+// ---------------------------------------------------------------------------
+template <int TN_, bool GU_>
+struct SmallCfg {
+    static constexpr int TN = TN_;
+    static constexpr bool GU = GU_;
+    static constexpr int NW = GU ? 2 : 1;                    // weight tiles
+    static constexpr int W_BYTES = 128 * 128;
+    static constexpr int STAGE = NW * W_BYTES + TN * 128;
+    // TN = 64 holds 64 sums a thread: one block an SM with a deep ring, else two
+    static constexpr int BLOCKS = TN == 64 ? 1 : 2;
+    static constexpr int RING = BLOCKS == 2 ? 110 * 1024 : 205 * 1024;
+    static constexpr int NS = RING / STAGE;
+    static constexpr int NB = TN == 16 ? 4 : 2;              // accumulators in tensor memory
+    static constexpr int TMEM_COLS = NB * NW * TN;           // 64 .. 256, a power of two
+    static constexpr int SEG = 4;                            // K blocks of scales kept at a time
+    static constexpr int TAB = NW * SEG * TN;                // floats of one segment's scales
+    static constexpr int EPI = 4 * NW;                       // warps that sum
+    static constexpr int THREADS = (EPI + 2) * 32;
+    static constexpr int OFF_TAB = NS * STAGE;
+    static constexpr int OFF_BAR = OFF_TAB + 2 * TAB * 4;
+    static constexpr int SMEM = OFF_BAR + (2 * NS + 2 * NB + 1) * 8 + 32 + 1024;
+    static_assert(NW * TN * 128 * 4 <= NS * STAGE, "the partial sums reuse the ring");
+};
+
+template <class C>
+__global__ void __launch_bounds__(C::THREADS, C::BLOCKS) small_kernel(const __grid_constant__ Maps maps, const Params p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    float *tab = reinterpret_cast<float *>(smem + C::OFF_TAB);
+    uint64_t *s_full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
+    uint64_t *s_empty = s_full + C::NS, *t_full = s_empty + C::NS, *t_empty = t_full + C::NB, *done = t_empty + C::NB;
+    int *info = reinterpret_cast<int *>(done + 1);           // abort, TMEM base, row tile (3), found
+    volatile int *abort_flag = info;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint32_t split, rank;
+    asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(split));
+    rank = cluster_ctarank();
+    const int tile = blockIdx.x / split;
+    const int nt = tile / p.row_tiles;                        // row tiles of one expert follow each other,
+                                                              // so that its weights are found in L2
+    if (warp == 0) {
+        RowTile rt{0, 0, 0};
+        const bool found = row_tile(p.offsets, p.E, p.M, C::TN, tile - nt * p.row_tiles, rt);
+        if (lane == 0) {
+            info[0] = 0;
+            info[2] = rt.e;
+            info[3] = rt.row0;
+            info[4] = rt.rows;
+            info[5] = found;
+        }
+    } else if (warp == 1 && lane == 0) {
+        for (int i = 0; i < C::NS; ++i) { mbar_init(&s_full[i], 1); mbar_init(&s_empty[i], 1); }
+        for (int i = 0; i < C::NB; ++i) { mbar_init(&t_full[i], 1); mbar_init(&t_empty[i], C::EPI); }
+        mbar_init(done, 1);
+        fence_mbarrier_init();
     }
-    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int i = 0; i < 4 && e < p.E; ++i) {
-        const int n = b * kF8Block + lane * 4 + i;
-        if (n >= p.N) continue;
-        const int64_t row = (int64_t)e * p.N + n, srow = ((int64_t)e * nb + b) * kb;
-        v[i] = dot_row(p.a + m * p.K, p.a_scale + m * kb, p.w + row * p.K, p.w_scale + srow, p.K);
-        if (p.w1) {
-            const float u = dot_row(p.a + m * p.K, p.a_scale + m * kb, p.w1 + row * p.K, p.w1_scale + srow, p.K);
-            v[i] = __fdividef(v[i], 1.0f + __expf(-v[i])) * u;
+    __syncthreads();
+    const int e = info[2], row0 = info[3], rows = info[4], n0 = nt * 128;
+    if (!info[5]) return;
+    if (e >= p.E) {
+        // rows of no expert: zeros (no product reads their h)
+        if (!C::GU)
+            for (int j = rank; j < rows; j += split)
+                for (int n = n0 + threadIdx.x; n < min(n0 + 128, p.N); n += C::THREADS) {
+                    const int64_t at = (int64_t)(row0 + j) * p.N + n;
+                    if (p.y_bf16) static_cast<__nv_bfloat16 *>(p.y)[at] = __float2bfloat16_rn(0.0f);
+                    else static_cast<float *>(p.y)[at] = 0.0f;
+                }
+        return;
+    }
+    if (warp == C::EPI + 1) {
+        tmem_alloc(reinterpret_cast<uint32_t *>(info + 1), C::TMEM_COLS);
+        tmem_relinquish();
+        tc_fence_before();
+    }
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(info + 1);
+    const int KB = (p.K + kF8Block - 1) / kF8Block;
+    const int kb0 = (int)((int64_t)KB * rank / split), nkb = (int)((int64_t)KB * (rank + 1) / split) - kb0;
+    float acc[C::TN];
+#pragma unroll
+    for (int j = 0; j < C::TN; ++j) acc[j] = 0.0f;
+
+    if (warp == C::EPI) {
+        // ---- TMA producer
+        if (lane == 0) {
+            int i = 0;
+            for (; i < nkb; ++i) {
+                const int s = i % C::NS;
+                if (i >= C::NS && !mbar_wait(&s_empty[s], ((i / C::NS) & 1) ^ 1, abort_flag, p.err)) break;
+                uint8_t *st = smem + s * C::STAGE;
+                mbar_arrive_expect_tx(&s_full[s], C::STAGE);
+                const int kc = (kb0 + i) * kF8Block;
+                tma_load_2d(st, &maps.w0, &s_full[s], kc, e * p.N + n0);
+                if (C::GU) tma_load_2d(st + C::W_BYTES, &maps.w1, &s_full[s], kc, e * p.N + n0);
+                tma_load_2d(st + C::NW * C::W_BYTES, &maps.a, &s_full[s], kc, row0);
+            }
+            if (*abort_flag)   // wait for the copies in flight before the block leaves
+                for (int j = i > C::NS ? i - C::NS : 0; j < i; ++j)
+                    mbar_wait(&s_full[j % C::NS], (j / C::NS) & 1, nullptr, p.err);
+        }
+        __syncwarp();
+    } else if (warp == C::EPI + 1) {
+        // ---- MMA issuer
+        constexpr uint32_t idesc = idesc_f8_f32(128, C::TN);
+        if (lane == 0) {
+            for (int i = 0; i < nkb; ++i) {
+                const int s = i % C::NS, b = i % C::NB;
+                if (!mbar_wait(&s_full[s], (i / C::NS) & 1, abort_flag, p.err)) break;
+                if (i >= C::NB && !mbar_wait(&t_empty[b], ((i / C::NB) & 1) ^ 1, abort_flag, p.err)) break;
+                tc_fence_after();
+                const uint32_t st = smem_u32(smem + s * C::STAGE);
+                const uint64_t bd = smem_desc_k_sw128(st + C::NW * C::W_BYTES);
+#pragma unroll
+                for (int w = 0; w < C::NW; ++w) {
+                    const uint64_t ad = smem_desc_k_sw128(st + w * C::W_BYTES);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)   // 32 bytes of K a step
+                        tc_mma_f8(tmem + (b * C::NW + w) * C::TN, ad + 2 * k, bd + 2 * k, idesc, k != 0);
+                }
+                tc_commit(&s_empty[s]);
+                tc_commit(&t_full[b]);
+            }
+            tc_commit(done);
+            mbar_wait(done, 0, nullptr, p.err);
+        }
+        __syncwarp();
+    } else {
+        // ---- scale and sum: thread = one row of W
+        const int w = warp >> 2, q = warp & 3, tid = threadIdx.x & 127;
+        const int nb = (p.N + kF8Block - 1) / kF8Block;
+        const float *sw = (w ? p.sw1 : p.sw0) + ((int64_t)e * nb + nt) * KB;
+        const uint32_t taddr = tmem + w * C::TN + ((uint32_t)(q * 32) << 16);
+        constexpr int PER = (C::SEG * C::TN + 127) / 128;
+        float next[PER];
+        // the scales' products of segment g: [K block][row of a]
+        auto fetch = [&](int g) {
+#pragma unroll
+            for (int r = 0; r < PER; ++r) {
+                const int v = r * 128 + tid, j = v / C::SEG, i = g * C::SEG + v % C::SEG;
+                next[r] = v < C::SEG * C::TN && j < rows && i < nkb
+                              ? __ldg(p.sa + (int64_t)(row0 + j) * KB + kb0 + i) * __ldg(sw + kb0 + i)
+                              : 0.0f;
+            }
+        };
+        fetch(0);
+        for (int i = 0; i < nkb; ++i) {
+            const int g = i / C::SEG, b = i % C::NB;
+            float *seg = tab + (g & 1) * C::TAB + w * C::SEG * C::TN;
+            if (i % C::SEG == 0) {
+                // (this half of the table was last read two segments ago, before
+                // the barrier of the one between)
+#pragma unroll
+                for (int r = 0; r < PER; ++r) {
+                    const int v = r * 128 + tid;
+                    if (v < C::SEG * C::TN) seg[(v % C::SEG) * C::TN + v / C::SEG] = next[r];
+                }
+                named_barrier(1 + w, 128);
+                fetch(g + 1);
+            }
+            // (a thread that gives up still meets the others at the barriers)
+            mbar_wait(&t_full[b], (i / C::NB) & 1, abort_flag, p.err);
+            tc_fence_after();
+            const float4 *s4 = reinterpret_cast<const float4 *>(seg + (i % C::SEG) * C::TN);
+            const uint32_t from = taddr + b * C::NW * C::TN;
+            constexpr int STEP = C::TN >= 32 ? 32 : 16;
+#pragma unroll
+            for (int c = 0; c < C::TN; c += STEP) {
+                uint32_t d[STEP];
+                if constexpr (STEP == 32) tmem_ld_32x32b_x32(from + c, d);
+                else tmem_ld_32x32b_x16(from + c, d);
+                tmem_ld_wait(d);
+                if (c + STEP == C::TN) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&t_empty[b]);
+                }
+#pragma unroll
+                for (int j = 0; j < STEP; j += 4) {
+                    const float4 s = s4[(c + j) / 4];
+                    acc[c + j] = fmaf(__uint_as_float(d[j]), s.x, acc[c + j]);
+                    acc[c + j + 1] = fmaf(__uint_as_float(d[j + 1]), s.y, acc[c + j + 1]);
+                    acc[c + j + 2] = fmaf(__uint_as_float(d[j + 2]), s.z, acc[c + j + 2]);
+                    acc[c + j + 3] = fmaf(__uint_as_float(d[j + 3]), s.w, acc[c + j + 3]);
+                }
+            }
         }
     }
-    int sp = 0;
-    if (p.w1) {
-        float top = 0.0f;
+    // every product has been taken out of tensor memory, so every copy into the
+    // ring has been read: it now holds the partial sums, [weight tile][row][128]
+    __syncthreads();
+    float *part = reinterpret_cast<float *>(smem);
+    if (warp < C::EPI) {
+        float *mine = part + (warp >> 2) * C::TN * 128 + (threadIdx.x & 127);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) top = fmaxf(top, finite_abs(v[i]));
+        for (int j = 0; j < C::TN; ++j) mine[j * 128] = acc[j];
+    }
+    if (warp == C::EPI + 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, C::TMEM_COLS);
+    }
+    if (split > 1) cluster_sync_all();
+    else __syncthreads();
+    if (warp < C::EPI) {
+        // a warp per row, 4 columns a lane: the ranks' sums in rank order
+        const uint32_t base = smem_u32(part);
+        const int n = n0 + lane * 4;
+        for (int j = rank + split * warp; j < rows; j += split * C::EPI) {
+            float v[C::NW][4];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        sp = f8_scale_exp(top);
-        if (lane == 0) p.y_scale[m * nb + b] = pow2f(sp);
+            for (int w = 0; w < C::NW; ++w) {
+                const uint32_t at = base + ((w * C::TN + j) * 128 + lane * 4) * 4;
+                float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                for (uint32_t r = 0; r < split; ++r) {
+                    const float4 f = ld_cluster_f4(mapa_shared(at, r));
+                    s.x += f.x; s.y += f.y; s.z += f.z; s.w += f.w;
+                }
+                v[w][0] = s.x; v[w][1] = s.y; v[w][2] = s.z; v[w][3] = s.w;
+            }
+            const int64_t row = row0 + j;
+            if constexpr (C::GU) {
+                float h[4], top = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    h[i] = n < p.N ? swiglu(v[0][i], v[1][i]) : 0.0f;   // (N is a multiple of 16)
+                    top = fmaxf(top, finite_abs(h[i]));
+                }
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                const int sp = f8_scale_exp(top);
+                const float inv = pow2f(-sp);
+                if (n < p.N)
+                    *reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(p.y) + row * p.N + n) =
+                        f8x4_satfinite(h[0] * inv, h[1] * inv, h[2] * inv, h[3] * inv);
+                if (lane == 0) p.y_scale[row * ((p.N + kF8Block - 1) / kF8Block) + nt] = pow2f(sp);
+            } else if (p.vec && n + 3 < p.N) {
+                if (p.y_bf16) {
+                    const __nv_bfloat162 lo = __floats2bfloat162_rn(v[0][0], v[0][1]), hi = __floats2bfloat162_rn(v[0][2], v[0][3]);
+                    *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.y) + row * p.N + n) =
+                        make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+                } else {
+                    *reinterpret_cast<float4 *>(static_cast<float *>(p.y) + row * p.N + n) =
+                        make_float4(v[0][0], v[0][1], v[0][2], v[0][3]);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (n + i < p.N) {
+                        if (p.y_bf16) static_cast<__nv_bfloat16 *>(p.y)[row * p.N + n + i] = __float2bfloat16_rn(v[0][i]);
+                        else static_cast<float *>(p.y)[row * p.N + n + i] = v[0][i];
+                    }
+            }
+        }
     }
-    for (int i = 0; i < 4; ++i) {
-        const int n = b * kF8Block + lane * 4 + i;
-        if (n >= p.N) continue;
-        const int64_t at = m * p.N + n;
-        if (p.w1) static_cast<uint8_t *>(p.y)[at] = (uint8_t)f8x2_satfinite(v[i] * pow2f(-sp), 0.0f);
-        else if (p.y_dtype == ZFFN_DT_F32) static_cast<float *>(p.y)[at] = v[i];
-        else static_cast<__nv_bfloat16 *>(p.y)[at] = __float2bfloat16_rn(v[i]);
-    }
+    if (split > 1) cluster_sync_all();   // no block leaves while another reads its sums
 }
 
-}  // namespace
+// ---- host -------------------------------------------------------------------
+
+static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void *ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            ptr = nullptr;
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+    }();
+    return fn;
+}
+
+// Byte matrix [rows][K] in boxes of 128 columns, 128-byte swizzle, zeros past the edges.
+static bool encode(CUtensorMap *m, const void *base, int64_t rows, int K, int box_rows) {
+    const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)K};
+    const cuuint32_t box[2] = {128, (cuuint32_t)box_rows};
+    const cuuint32_t estr[2] = {1, 1};
+    return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, estr,
+                       CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+static Params params(const Fp8Args &a) {
+    Params p{};
+    p.sa = a.a_scale;
+    p.sw0 = a.w_scale;
+    p.sw1 = a.w1_scale;
+    p.offsets = a.offsets;
+    p.y = a.y;
+    p.y_scale = a.y_scale;
+    p.err = a.err;
+    p.M = a.M; p.N = a.N; p.K = a.K; p.E = a.E;
+    p.y_bf16 = a.y_dtype == ZFFN_DT_BF16;
+    p.vec = a.N % 4 == 0 && (reinterpret_cast<uintptr_t>(a.y) & (p.y_bf16 ? 7 : 15)) == 0;
+    return p;
+}
+
+// Row tiles of at most tr rows, at most: every expert may have one cut tile, and
+// so may the rows of no expert.
+static int64_t row_tiles_bound(const Fp8Args &a, int tr) {
+    if (!a.offsets) return ((int64_t)a.M + tr - 1) / tr;
+    return a.M / tr + (a.E + 1 < a.M ? a.E + 1 : a.M);
+}
+
+template <class C>
+static cudaError_t launch_small(const Fp8Args &a, cudaStream_t s) {
+    const DeviceInfo &di = device_info();
+    Maps maps;
+    if (!encode(&maps.a, a.a, a.M, a.K, C::TN) || !encode(&maps.w0, a.w, (int64_t)a.E * a.N, a.K, 128) ||
+        !encode(&maps.w1, C::GU ? a.w1 : a.w, (int64_t)a.E * a.N, a.K, 128))
+        return cudaErrorInvalidValue;
+    Params p = params(a);
+    const int64_t rt = row_tiles_bound(a, C::TN), tiles = rt * f8_blocks(a.N);
+    const int KB = (int)f8_blocks(a.K);
+    // split K so that the blocks fill the SMs, two K blocks each at least
+    int64_t split = (int64_t)di.num_sms * C::BLOCKS / tiles;
+    split = split > 8 ? 8 : split;
+    split = split > KB / 2 ? KB / 2 : split;
+    split = split < 1 ? 1 : split;
+    if (rt > 0x7fffffff || tiles * split > 0x7fffffff) return cudaErrorInvalidValue;
+    p.row_tiles = (int)rt;
+    const cudaError_t e = ensure_dynamic_smem((const void *)small_kernel<C>, C::SMEM);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(tiles * split));
+    cfg.blockDim = dim3(C::THREADS);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)split;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, small_kernel<C>, maps, p);
+}
+
+template <bool GU>
+static cudaError_t launch(const Fp8Args &a, cudaStream_t s) {
+    // rows a tile: the least of 16, 32, 64 that takes an expert's rows (with some
+    // spread over their mean) at once, so that its weights are read once
+    const int64_t mean = a.offsets ? ((int64_t)a.M * 3 / 2 + a.E - 1) / a.E : a.M;
+    if (mean <= 16) return launch_small<SmallCfg<16, GU>>(a, s);
+    if (mean <= 32) return launch_small<SmallCfg<32, GU>>(a, s);
+    return launch_small<SmallCfg<64, GU>>(a, s);
+}
+
+}  // namespace f8
 
 cudaError_t launch_fp8_matmul(const Fp8Args &a, cudaStream_t s) {
-    const int64_t units = (int64_t)a.M * f8_blocks(a.N), grid = (units + 3) / 4;
-    if (grid > 0x7fffffff) return cudaErrorInvalidValue;
-    fp8_matmul_kernel<<<(unsigned)grid, 128, 0, s>>>(a);
-    return cudaGetLastError();
+    if (!f8::encode_fn()) return cudaErrorNotSupported;
+    return a.w1 ? f8::launch<true>(a, s) : f8::launch<false>(a, s);
 }
 
 }  // namespace zffn
