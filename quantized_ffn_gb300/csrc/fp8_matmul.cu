@@ -26,6 +26,16 @@ __device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t a_desc, uint
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
+// The same over a CTA pair: D in both CTAs' tensor memory, A from both, B split between them.
+__device__ __forceinline__ void tc_mma_f8_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                               uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
 // Instruction descriptor: A = B = e4m3 (format code 0), D = fp32, both K-major.
 __host__ __device__ constexpr uint32_t idesc_f8_f32(int M, int N) {
     return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
@@ -97,7 +107,7 @@ struct Params {
     int M, N, K, E;
     int row_tiles;      // bound of the number of row tiles
     int y_bf16;         // plain: y is bf16 (else fp32)
-    int vec;            // y's rows take 4-element stores
+    int vec;            // y's rows take vector stores (small: 4 elements, large: 16 bytes)
 };
 struct Maps {
     CUtensorMap a, w0, w1;
@@ -371,6 +381,348 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) small_kernel(const __gr
     if (split > 1) cluster_sync_all();   // no block leaves while another reads its sums
 }
 
+// ---------------------------------------------------------------------------
+// Many rows: a on the MMA's M side, 128 rows a CTA (a CTA pair: 256, the W rows
+// split between the two, which halves W's way through L2) times 256 rows of W
+// (GU: 128 gate and 128 up rows, by 32 in turn, so that a thread holds a gate
+// value and its up value).  In this orientation a thread's sums belong to one
+// row of a and one block of W's rows, so its scale of a K block is one number.
+// Persistent: every cluster takes tiles in turn; two accumulators in tensor
+// memory let the MMAs of the next block (and of the next tile) run while one is
+// taken out.
+//
+// Roles: warps 0 .. 15 scale and sum (group w = warp / 4 takes columns 64 w ..
+// 64 w + 63, 64 sums a thread), warp 16 loads by TMA, warp 17 issues the MMAs.
+// ---------------------------------------------------------------------------
+template <bool PAIR_, bool GU_>
+struct LargeCfg {
+    static constexpr bool PAIR = PAIR_, GU = GU_;
+    static constexpr int CTAS = PAIR ? 2 : 1;
+    static constexpr int TM = 128 * CTAS;                    // rows of a
+    static constexpr int TNW = GU ? 128 : 256;               // rows of W (of each, GU)
+    static constexpr int W_ROWS = 256 / CTAS;                // W rows that a CTA holds
+    static constexpr int W_BOX = GU ? 32 : 128;
+    static constexpr int A_BYTES = 128 * 128;
+    static constexpr int STAGE = A_BYTES + W_ROWS * 128;
+    static constexpr int NS = PAIR ? 6 : 4;
+    static constexpr int NB = 2;
+    static constexpr int EPI = 16;
+    static constexpr int THREADS = (EPI + 2) * 32;
+    static constexpr int GROUP = 8;                          // dense: row tiles that share a W tile in turn
+    static constexpr int OFF_TOP = NS * STAGE;               // GU: largest h of (tile parity, group, row)
+    static constexpr int OFF_BAR = OFF_TOP + (GU ? 2 * 4 * 128 * 4 : 0);
+    static constexpr int OFF_CUM = OFF_BAR + (2 * NS + 2 * NB + 1) * 8 + 24;
+    static constexpr int SMEM = OFF_CUM + 1024;              // + the row tiles before each group of rows
+};
+
+// Tile i of a cluster's walk: the group of rows, its rows, the W tile.
+template <class C>
+struct Walk {
+    int e, row0, rows, nt;   // rows: of the tile, <= C::TM
+    int64_t t;
+    int g;                   // grouped: the expert of the tile before
+
+    __device__ __forceinline__ void start(int cluster) { t = cluster; g = 0; }
+    // false past the last tile.  One full warp.  cum[g]: row tiles before group g.
+    __device__ __forceinline__ bool get(const Params &p, const int *cum, int n_tiles) {
+        if (!p.offsets) {
+            const int rt_all = p.row_tiles;
+            if (t >= (int64_t)rt_all * n_tiles) return false;
+            const int band = (int)(t / ((int64_t)C::GROUP * n_tiles)), first = band * C::GROUP;
+            const int in = (int)(t - (int64_t)first * n_tiles), wide = min(C::GROUP, rt_all - first);
+            nt = in / wide;
+            e = 0;
+            row0 = (first + in - nt * wide) * C::TM;
+            rows = min(C::TM, p.M - row0);
+            return true;
+        }
+        const int groups = p.E + 1;
+        if (t >= (int64_t)cum[groups] * n_tiles) return false;
+        const int rt = (int)(t / n_tiles), lane = threadIdx.x & 31;
+        nt = (int)(t - (int64_t)rt * n_tiles);
+        for (;; g += 32) {   // the group whose tiles hold rt: ascending from the last one
+            const unsigned past = __ballot_sync(0xffffffffu, cum[min(g + lane + 1, groups)] > rt);
+            if (past) {
+                g += __ffs(past) - 1;
+                break;
+            }
+        }
+        e = g;
+        const int lo = min(max(__ldg(p.offsets + g), 0), p.M);
+        const int hi = g < p.E ? min(max(__ldg(p.offsets + g + 1), 0), p.M) : p.M;
+        const int done = (rt - cum[g]) * C::TM;
+        row0 = lo + done;
+        rows = min(C::TM, hi - row0);
+        return true;
+    }
+};
+
+template <class C>
+__global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_constant__ Maps maps, const Params p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    float *tops = reinterpret_cast<float *>(smem + C::OFF_TOP);
+    uint64_t *s_full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
+    uint64_t *s_empty = s_full + C::NS, *t_full = s_empty + C::NS, *t_empty = t_full + C::NB, *done = t_empty + C::NB;
+    int *info = reinterpret_cast<int *>(done + 1);           // abort, TMEM base
+    int *cum = reinterpret_cast<int *>(smem + C::OFF_CUM);
+    volatile int *abort_flag = info;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = C::PAIR ? (int)cluster_ctarank() : 0;
+    const int KB = (p.K + kF8Block - 1) / kF8Block;
+    const int n_tiles = (p.N + C::TNW - 1) / C::TNW;
+
+    if (warp == C::EPI && lane == 0) {
+        info[0] = 0;
+        for (int i = 0; i < C::NS; ++i) { mbar_init(&s_full[i], 1); mbar_init(&s_empty[i], 1); }
+        for (int i = 0; i < C::NB; ++i) { mbar_init(&t_full[i], 1); mbar_init(&t_empty[i], C::EPI * C::CTAS); }
+        mbar_init(done, 1);
+        fence_mbarrier_init();
+        prefetch_tensormap(&maps.a);
+        prefetch_tensormap(&maps.w0);
+        if (C::GU) prefetch_tensormap(&maps.w1);
+    }
+    if (warp == C::EPI + 1) {
+        uint32_t *dst = reinterpret_cast<uint32_t *>(info + 1);
+        if constexpr (C::PAIR) { tmem_alloc_pair(dst, 512); tmem_relinquish_pair(); }
+        else { tmem_alloc(dst, 512); tmem_relinquish(); }
+        tc_fence_before();
+    }
+    if (p.offsets) {
+        // row tiles of each group (the experts, then the rows of none: h needs no
+        // zeros there), then their exclusive sums
+        for (int g = threadIdx.x; g <= p.E; g += C::THREADS) {
+            const int lo = min(max(__ldg(p.offsets + g), 0), p.M);
+            const int hi = g < p.E ? min(max(__ldg(p.offsets + g + 1), 0), p.M) : (C::GU ? lo : p.M);
+            cum[g] = (max(hi - lo, 0) + C::TM - 1) / C::TM;
+        }
+        __syncthreads();
+        if (warp == 0) {
+            const int per = (p.E + 32) / 32, g0 = min(lane * per, p.E + 1), g1 = min(g0 + per, p.E + 1);
+            int n = 0;
+            for (int g = g0; g < g1; ++g) n += cum[g];
+            int inc = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += v;
+            }
+            int at = inc - n;
+            for (int g = g0; g < g1; ++g) {
+                const int c = cum[g];
+                cum[g] = at;
+                at += c;
+            }
+            if (lane == 31) cum[p.E + 1] = inc;
+        }
+    }
+    __syncthreads();
+    if (C::PAIR) cluster_sync_all();   // the peer's barriers are set up
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(info + 1);
+    const int clusters = gridDim.x / C::CTAS;
+    Walk<C> wk;
+    wk.start(blockIdx.x / C::CTAS);
+
+    if (warp == C::EPI) {
+        // ---- TMA producer: this CTA's rows of a and share of W's rows
+        const uint32_t full0 = C::PAIR ? mapa_shared(smem_u32(s_full), 0) : 0;
+        uint32_t it = 0;
+        bool ok = true;
+        for (; ok && wk.get(p, cum, n_tiles); wk.t += clusters) {
+            for (int i = 0; i < KB && lane == 0 && wk.e < p.E; ++i, ++it) {
+                const uint32_t s = it % C::NS;
+                if (it >= C::NS && !mbar_wait(&s_empty[s], ((it / C::NS) & 1) ^ 1, abort_flag, p.err)) { ok = false; break; }
+                uint8_t *st = smem + s * C::STAGE;
+                if (rank == 0) mbar_arrive_expect_tx(&s_full[s], C::STAGE * C::CTAS);
+                auto load = [&](uint8_t *dst, const CUtensorMap *m, int c1) {
+                    if constexpr (C::PAIR) tma_load_2d_pair(dst, m, full0 + s * 8, i * kF8Block, c1);
+                    else tma_load_2d(dst, m, &s_full[s], i * kF8Block, c1);
+                };
+                load(st, &maps.a, wk.row0 + 128 * rank);
+                const int w_row = wk.e * p.N + wk.nt * C::TNW;
+#pragma unroll
+                for (int b = 0; b < C::W_ROWS / C::W_BOX; ++b) {
+                    uint8_t *dst = st + C::A_BYTES + b * C::W_BOX * 128;
+                    const int at = rank * (C::W_ROWS / C::W_BOX) + b;   // box of the whole W tile
+                    if constexpr (C::GU) load(dst, at & 1 ? &maps.w1 : &maps.w0, w_row + (at >> 1) * 32);
+                    else load(dst, &maps.w0, w_row + at * C::W_BOX);
+                }
+            }
+            ok = __shfl_sync(0xffffffffu, ok && !*abort_flag, 0);
+        }
+        // (a launch that gave up: wait for the copies in flight before leaving)
+        if (lane == 0 && *abort_flag && rank == 0)
+            for (uint32_t j = it > C::NS ? it - C::NS : 0; j < it; ++j)
+                mbar_wait(&s_full[j % C::NS], (j / C::NS) & 1, nullptr, p.err);
+        __syncwarp();
+    } else if (warp == C::EPI + 1) {
+        // ---- MMA issuer (of a pair: its first CTA)
+        constexpr uint32_t idesc = idesc_f8_f32(C::TM, 256);
+        if (rank == 0) {
+            uint32_t it = 0;
+            bool ok = true;
+            for (; ok && wk.get(p, cum, n_tiles); wk.t += clusters) {
+                for (int i = 0; i < KB && lane == 0 && wk.e < p.E; ++i, ++it) {
+                    const uint32_t s = it % C::NS, b = it % C::NB;
+                    if (it >= C::NB && !mbar_wait(&t_empty[b], ((it / C::NB) & 1) ^ 1, abort_flag, p.err)) { ok = false; break; }
+                    if (!mbar_wait(&s_full[s], (it / C::NS) & 1, abort_flag, p.err)) { ok = false; break; }
+                    tc_fence_after();
+                    const uint32_t st = smem_u32(smem + s * C::STAGE);
+                    const uint64_t ad = smem_desc_k_sw128(st), bd = smem_desc_k_sw128(st + C::A_BYTES);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {   // 32 bytes of K a step
+                        if constexpr (C::PAIR) tc_mma_f8_pair(tmem + b * 256, ad + 2 * k, bd + 2 * k, idesc, k != 0);
+                        else tc_mma_f8(tmem + b * 256, ad + 2 * k, bd + 2 * k, idesc, k != 0);
+                    }
+                    if constexpr (C::PAIR) { tc_commit_pair(&s_empty[s]); tc_commit_pair(&t_full[b]); }
+                    else { tc_commit(&s_empty[s]); tc_commit(&t_full[b]); }
+                }
+                ok = __shfl_sync(0xffffffffu, ok && !*abort_flag, 0);
+            }
+            if (lane == 0) {
+                if constexpr (C::PAIR) tc_commit_pair(done);
+                else tc_commit(done);
+            }
+        }
+        // (both CTAs of a pair: no commit's arrival is left on its way)
+        if (lane == 0) mbar_wait(done, 0, nullptr, p.err);
+        __syncwarp();
+    } else {
+        // ---- scale and sum: thread = one row of a, 64 columns
+        const int w = warp >> 2, q = warp & 3, lrow = q * 32 + lane;
+        const int nb = (p.N + kF8Block - 1) / kF8Block;
+        const uint32_t taddr = tmem + w * 64 + ((uint32_t)(q * 32) << 16);
+        const uint32_t empty0 = C::PAIR ? mapa_shared(smem_u32(t_empty), 0) : 0;
+        uint32_t it = 0;
+        int parity = 0;
+        for (; wk.get(p, cum, n_tiles); wk.t += clusters) {
+            const int mine = wk.rows - 128 * rank;           // rows of this CTA (may be none)
+            const int64_t row = wk.row0 + min(128 * rank + lrow, wk.rows - 1);
+            float acc[64];
+#pragma unroll
+            for (int j = 0; j < 64; ++j) acc[j] = 0.0f;
+            if (wk.e < p.E) {
+                const int b0 = C::GU ? wk.nt : min(wk.nt * 2 + (w >> 1), nb - 1);
+                const float *pa = p.sa + row * KB;
+                const float *p0 = p.sw0 + ((int64_t)wk.e * nb + b0) * KB, *p1 = C::GU ? p.sw1 + ((int64_t)wk.e * nb + b0) * KB : p0;
+                // scales two K blocks ahead
+                float fa[2], f0[2], f1[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int i = min(k, KB - 1);
+                    fa[k] = __ldg(pa + i);
+                    f0[k] = __ldg(p0 + i);
+                    f1[k] = C::GU ? __ldg(p1 + i) : 0.0f;
+                }
+                for (int i = 0; i < KB; ++i, ++it) {
+                    const uint32_t b = it % C::NB;
+                    const float s0 = fa[0] * f0[0], s1 = C::GU ? fa[0] * f1[0] : s0;
+                    fa[0] = fa[1]; f0[0] = f0[1]; f1[0] = f1[1];
+                    const int nx = min(i + 2, KB - 1);
+                    fa[1] = __ldg(pa + nx);
+                    f0[1] = __ldg(p0 + nx);
+                    if (C::GU) f1[1] = __ldg(p1 + nx);
+                    mbar_wait(&t_full[b], (it / C::NB) & 1, abort_flag, p.err);
+                    __syncwarp();
+                    tc_fence_after();
+#pragma unroll
+                    for (int c = 0; c < 64; c += 16) {
+                        uint32_t d[16];
+                        tmem_ld_32x32b_x16(taddr + b * 256 + c, d);
+                        tmem_ld_wait(d);
+                        if (c == 48) {
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) {
+                                if constexpr (C::PAIR) mbar_arrive_cluster(empty0 + b * 8);
+                                else mbar_arrive(&t_empty[b]);
+                            }
+                        }
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) acc[c + j] = fmaf(__uint_as_float(d[j]), c < 32 ? s0 : s1, acc[c + j]);
+                    }
+                }
+            }
+            const bool live = lrow < mine;
+            if constexpr (C::GU) {
+                // h of features 32 w .. 32 w + 31 of the tile; the block's largest
+                // over the four groups through shared memory
+                const int n = wk.nt * 128 + w * 32;
+                float top = 0.0f;
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    acc[j] = n + j < p.N ? swiglu(acc[j], acc[32 + j]) : 0.0f;
+                    top = fmaxf(top, finite_abs(acc[j]));
+                }
+                float *t4 = tops + parity * 4 * 128 + lrow;
+                t4[w * 128] = top;
+                named_barrier(1, C::EPI * 32);
+                top = fmaxf(fmaxf(t4[0], t4[128]), fmaxf(t4[256], t4[384]));
+                parity ^= 1;
+                if (live) {
+                    const int sp = f8_scale_exp(top);
+                    const float inv = pow2f(-sp);
+                    uint8_t *h = static_cast<uint8_t *>(p.y) + row * p.N + n;
+#pragma unroll
+                    for (int j = 0; j < 32; j += 16)   // (N is a multiple of 16, h 16-byte aligned)
+                        if (n + j < p.N) {
+                            uint32_t v[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                v[k] = f8x4_satfinite(acc[j + 4 * k] * inv, acc[j + 4 * k + 1] * inv, acc[j + 4 * k + 2] * inv,
+                                                      acc[j + 4 * k + 3] * inv);
+                            *reinterpret_cast<uint4 *>(h + j) = make_uint4(v[0], v[1], v[2], v[3]);
+                        }
+                    if (w == 0) p.y_scale[row * nb + wk.nt] = pow2f(sp);
+                }
+            } else if (live) {
+                const int n = wk.nt * 256 + w * 64;
+                if (p.y_bf16) {
+                    __nv_bfloat16 *y = static_cast<__nv_bfloat16 *>(p.y) + row * p.N + n;
+#pragma unroll
+                    for (int j = 0; j < 64; j += 8) {
+                        if (p.vec && n + j + 7 < p.N) {
+                            uint32_t v[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const __nv_bfloat162 two = __floats2bfloat162_rn(acc[j + 2 * k], acc[j + 2 * k + 1]);
+                                v[k] = *reinterpret_cast<const uint32_t *>(&two);
+                            }
+                            *reinterpret_cast<uint4 *>(y + j) = make_uint4(v[0], v[1], v[2], v[3]);
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                if (n + j + k < p.N) y[j + k] = __float2bfloat16_rn(acc[j + k]);
+                        }
+                    }
+                } else {
+                    float *y = static_cast<float *>(p.y) + row * p.N + n;
+#pragma unroll
+                    for (int j = 0; j < 64; j += 4) {
+                        if (p.vec && n + j + 3 < p.N) *reinterpret_cast<float4 *>(y + j) = make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
+                        else {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                if (n + j + k < p.N) y[j + k] = acc[j + k];
+                        }
+                    }
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    // (of a pair: no CTA leaves while the other's MMAs may read its shared memory
+    // or it may still arrive on the other's barriers)
+    if (C::PAIR) cluster_sync_all();
+    if (warp == C::EPI + 1) {
+        tc_fence_after();
+        if constexpr (C::PAIR) tmem_dealloc_pair(tmem, 512);
+        else tmem_dealloc(tmem, 512);
+    }
+}
+
 // ---- host -------------------------------------------------------------------
 
 static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
@@ -407,7 +759,6 @@ static Params params(const Fp8Args &a) {
     p.err = a.err;
     p.M = a.M; p.N = a.N; p.K = a.K; p.E = a.E;
     p.y_bf16 = a.y_dtype == ZFFN_DT_BF16;
-    p.vec = a.N % 4 == 0 && (reinterpret_cast<uintptr_t>(a.y) & (p.y_bf16 ? 7 : 15)) == 0;
     return p;
 }
 
@@ -435,6 +786,7 @@ static cudaError_t launch_small(const Fp8Args &a, cudaStream_t s) {
     split = split < 1 ? 1 : split;
     if (rt > 0x7fffffff || tiles * split > 0x7fffffff) return cudaErrorInvalidValue;
     p.row_tiles = (int)rt;
+    p.vec = a.N % 4 == 0 && (reinterpret_cast<uintptr_t>(a.y) & (p.y_bf16 ? 7 : 15)) == 0;
     const cudaError_t e = ensure_dynamic_smem((const void *)small_kernel<C>, C::SMEM);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -452,11 +804,50 @@ static cudaError_t launch_small(const Fp8Args &a, cudaStream_t s) {
     return cudaLaunchKernelEx(&cfg, small_kernel<C>, maps, p);
 }
 
+template <class C>
+static cudaError_t launch_large(const Fp8Args &a, cudaStream_t s) {
+    const DeviceInfo &di = device_info();
+    Maps maps;
+    if (!encode(&maps.a, a.a, a.M, a.K, 128) || !encode(&maps.w0, a.w, (int64_t)a.E * a.N, a.K, C::W_BOX) ||
+        !encode(&maps.w1, C::GU ? a.w1 : a.w, (int64_t)a.E * a.N, a.K, C::W_BOX))
+        return cudaErrorInvalidValue;
+    Params p = params(a);
+    const int64_t rt = row_tiles_bound(a, C::TM), tiles = rt * ((a.N + C::TNW - 1) / C::TNW);
+    if (rt > 0x7fffffff) return cudaErrorInvalidValue;
+    p.row_tiles = (int)rt;
+    p.vec = a.N % (p.y_bf16 ? 8 : 4) == 0 && (reinterpret_cast<uintptr_t>(a.y) & 15) == 0;
+    int64_t clusters = di.num_sms / C::CTAS;
+    if (tiles < clusters) clusters = tiles;
+    const size_t smem = C::SMEM + (a.offsets ? ((size_t)a.E + 2) * 4 : 0);
+    const cudaError_t e = ensure_dynamic_smem((const void *)large_kernel<C>, smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(clusters * C::CTAS));
+    cfg.blockDim = dim3(C::THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = C::CTAS;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, large_kernel<C>, maps, p);
+}
+
 template <bool GU>
 static cudaError_t launch(const Fp8Args &a, cudaStream_t s) {
     // rows a tile: the least of 16, 32, 64 that takes an expert's rows (with some
     // spread over their mean) at once, so that its weights are read once
     const int64_t mean = a.offsets ? ((int64_t)a.M * 3 / 2 + a.E - 1) / a.E : a.M;
+    // many rows: the large tiles, where they fill the SMs at least twice over (a
+    // dense call with fewer splits K instead)
+    const int64_t per = (a.N + LargeCfg<false, GU>::TNW - 1) / LargeCfg<false, GU>::TNW;
+    if (a.offsets ? a.M / a.E > 64 : a.M > 64 && (a.M + 127) / 128 * per >= 76) {
+        if (!a.offsets && a.M >= 256) return launch_large<LargeCfg<true, GU>>(a, s);
+        return launch_large<LargeCfg<false, GU>>(a, s);
+    }
     if (mean <= 16) return launch_small<SmallCfg<16, GU>>(a, s);
     if (mean <= 32) return launch_small<SmallCfg<32, GU>>(a, s);
     return launch_small<SmallCfg<64, GU>>(a, s);

@@ -110,7 +110,8 @@ def product_inputs(rng, M, N, K, E=0):
 
 SHAPES = [(1, 1, 16), (1, 128, 128), (1, 2057, 1040), (2, 130, 144), (7, 64, 16), (16, 129, 4096), (17, 256, 400),
           (33, 300, 1040), (64, 1000, 512), (65, 384, 272), (100, 129, 2064), (128, 256, 256), (129, 257, 272),
-          (200, 512, 1024), (256, 1024, 384), (300, 2049, 528), (513, 768, 1152)]
+          (200, 512, 1024), (256, 1024, 384), (300, 2049, 528), (513, 768, 1152), (130, 10001, 272), (255, 9728, 144),
+          (256, 9999, 400), (700, 4096, 272), (1030, 2568, 1040), (2500, 1032, 16)]
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
@@ -307,6 +308,24 @@ def test_experts(P, H, I, E, kind, dtype):
         d = zffn.fp8_experts(f8(a), f32(sa), f8(wg[0]), f32(sg[0]), f8(wu[0]), f32(su[0]), f8(wd[0]), f32(sd[0]), dtype=dtype)
         assert torch.equal(d, y)
     assert zffn.get_device_error() == zffn.OK
+
+
+@pytest.mark.parametrize("P,H,I,kind", [(700, 256, 9808, "random"), (200, 272, 9744, "unused")])
+def test_experts_of_large_tiles(P, H, I, kind):
+    # wide enough that the dense gate/up product fills the SMs with large tiles, its down product not;
+    # one expert's grouped form may take other tiles, so each is held to the bound
+    rng = np.random.default_rng(P + H + I)
+    t = expert_inputs(rng, P, H, I, 1)
+    cut = split_rows(rng, P, 1, kind)
+    a, sa, wg, sg, wu, su, wd, sd = t
+    for offsets in (dev(cut), None):
+        if offsets is None:
+            y = zffn.fp8_experts(f8(a), f32(sa), f8(wg[0]), f32(sg[0]), f8(wu[0]), f32(su[0]), f8(wd[0]), f32(sd[0]), dtype=torch.float32)
+            want, tol = experts_ref(*t, np.array([0, P]))
+        else:
+            y = zffn.fp8_experts(f8(a), f32(sa), f8(wg), f32(sg), f8(wu), f32(su), f8(wd), f32(sd), offsets=offsets, dtype=torch.float32)
+            want, tol = experts_ref(*t, cut)
+        assert np.all(np.abs(y.double().cpu().numpy() - want) <= tol + 1e-37)
 
 
 def test_routed_layer_end_to_end():
