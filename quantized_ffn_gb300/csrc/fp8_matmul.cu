@@ -51,6 +51,15 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
 __device__ __forceinline__ void named_barrier(int id, int threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
+// acc += d * s on a pair of fp32 values (one instruction, each half rounded once).
+__device__ __forceinline__ void fma2(float2 &acc, uint32_t d0, uint32_t d1, float s) {
+    asm("{\n\t.reg .b64 a, d, f;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 d, {%2, %3};\n\tmov.b64 f, {%4, %4};\n\t"
+        "fma.rn.f32x2 a, d, f, a;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "+f"(acc.x), "+f"(acc.y)
+        : "r"(d0), "r"(d1), "f"(s));
+}
+template <int R> __device__ __forceinline__ void reg_alloc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
+template <int R> __device__ __forceinline__ void reg_dealloc() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
 __device__ __forceinline__ float swiglu(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
 
 // A tile of rows of one expert (e == E: rows that belong to no expert).
@@ -384,15 +393,15 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) small_kernel(const __gr
 // ---------------------------------------------------------------------------
 // Many rows: a on the MMA's M side, 128 rows a CTA (a CTA pair: 256, the W rows
 // split between the two, which halves W's way through L2) times 256 rows of W
-// (GU: 128 gate and 128 up rows, by 32 in turn, so that a thread holds a gate
+// (GU: 128 gate and 128 up rows, by 64 in turn, so that a thread holds a gate
 // value and its up value).  In this orientation a thread's sums belong to one
 // row of a and one block of W's rows, so its scale of a K block is one number.
 // Persistent: every cluster takes tiles in turn; two accumulators in tensor
 // memory let the MMAs of the next block (and of the next tile) run while one is
 // taken out.
 //
-// Roles: warps 0 .. 15 scale and sum (group w = warp / 4 takes columns 64 w ..
-// 64 w + 63, 64 sums a thread), warp 16 loads by TMA, warp 17 issues the MMAs.
+// Roles: warps 0 .. 7 scale and sum (group w = warp / 4 takes columns 128 w ..
+// 128 w + 127, 128 sums a thread), warp 8 loads by TMA, warp 9 issues the MMAs.
 // ---------------------------------------------------------------------------
 template <bool PAIR_, bool GU_>
 struct LargeCfg {
@@ -401,16 +410,19 @@ struct LargeCfg {
     static constexpr int TM = 128 * CTAS;                    // rows of a
     static constexpr int TNW = GU ? 128 : 256;               // rows of W (of each, GU)
     static constexpr int W_ROWS = 256 / CTAS;                // W rows that a CTA holds
-    static constexpr int W_BOX = GU ? 32 : 128;
+    static constexpr int W_BOX = GU ? 64 : 128;
     static constexpr int A_BYTES = 128 * 128;
     static constexpr int STAGE = A_BYTES + W_ROWS * 128;
     static constexpr int NS = PAIR ? 6 : 4;
     static constexpr int NB = 2;
-    static constexpr int EPI = 16;
-    static constexpr int THREADS = (EPI + 2) * 32;
+    static constexpr int EPI = 8;
+    static constexpr int THREADS = 384;                      // three warpgroups
+    // registers a thread: 168 at launch (what 384 threads can have), then shifted
+    // to the two summing warpgroups: 256 * 224 + 128 * 56 = 384 * 168
+    static constexpr int REGS = 168, REGS_SUM = 224, REGS_REST = 56;
     static constexpr int GROUP = 8;                          // dense: row tiles that share a W tile in turn
     static constexpr int OFF_TOP = NS * STAGE;               // GU: largest h of (tile parity, group, row)
-    static constexpr int OFF_BAR = OFF_TOP + (GU ? 2 * 4 * 128 * 4 : 0);
+    static constexpr int OFF_BAR = OFF_TOP + (GU ? 2 * 2 * 128 * 4 : 0);
     static constexpr int OFF_CUM = OFF_BAR + (2 * NS + 2 * NB + 1) * 8 + 24;
     static constexpr int SMEM = OFF_CUM + 1024;              // + the row tiles before each group of rows
 };
@@ -523,6 +535,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
     const int clusters = gridDim.x / C::CTAS;
     Walk<C> wk;
     wk.start(blockIdx.x / C::CTAS);
+    if (warp >= C::EPI) reg_dealloc<C::REGS_REST>();
 
     if (warp == C::EPI) {
         // ---- TMA producer: this CTA's rows of a and share of W's rows
@@ -545,7 +558,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
                 for (int b = 0; b < C::W_ROWS / C::W_BOX; ++b) {
                     uint8_t *dst = st + C::A_BYTES + b * C::W_BOX * 128;
                     const int at = rank * (C::W_ROWS / C::W_BOX) + b;   // box of the whole W tile
-                    if constexpr (C::GU) load(dst, at & 1 ? &maps.w1 : &maps.w0, w_row + (at >> 1) * 32);
+                    if constexpr (C::GU) load(dst, at & 1 ? &maps.w1 : &maps.w0, w_row + (at >> 1) * 64);
                     else load(dst, &maps.w0, w_row + at * C::W_BOX);
                 }
             }
@@ -588,22 +601,23 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
         // (both CTAs of a pair: no commit's arrival is left on its way)
         if (lane == 0) mbar_wait(done, 0, nullptr, p.err);
         __syncwarp();
-    } else {
-        // ---- scale and sum: thread = one row of a, 64 columns
+    } else if (warp < C::EPI) {
+        // ---- scale and sum: thread = one row of a, 128 columns
+        reg_alloc<C::REGS_SUM>();
         const int w = warp >> 2, q = warp & 3, lrow = q * 32 + lane;
         const int nb = (p.N + kF8Block - 1) / kF8Block;
-        const uint32_t taddr = tmem + w * 64 + ((uint32_t)(q * 32) << 16);
+        const uint32_t taddr = tmem + w * 128 + ((uint32_t)(q * 32) << 16);
         const uint32_t empty0 = C::PAIR ? mapa_shared(smem_u32(t_empty), 0) : 0;
         uint32_t it = 0;
         int parity = 0;
         for (; wk.get(p, cum, n_tiles); wk.t += clusters) {
             const int mine = wk.rows - 128 * rank;           // rows of this CTA (may be none)
             const int64_t row = wk.row0 + min(128 * rank + lrow, wk.rows - 1);
-            float acc[64];
+            float2 acc[64];
 #pragma unroll
-            for (int j = 0; j < 64; ++j) acc[j] = 0.0f;
+            for (int j = 0; j < 64; ++j) acc[j] = make_float2(0.0f, 0.0f);
             if (wk.e < p.E) {
-                const int b0 = C::GU ? wk.nt : min(wk.nt * 2 + (w >> 1), nb - 1);
+                const int b0 = C::GU ? wk.nt : min(wk.nt * 2 + w, nb - 1);
                 const float *pa = p.sa + row * KB;
                 const float *p0 = p.sw0 + ((int64_t)wk.e * nb + b0) * KB, *p1 = C::GU ? p.sw1 + ((int64_t)wk.e * nb + b0) * KB : p0;
                 // scales two K blocks ahead
@@ -616,7 +630,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
                     f1[k] = C::GU ? __ldg(p1 + i) : 0.0f;
                 }
                 for (int i = 0; i < KB; ++i, ++it) {
-                    const uint32_t b = it % C::NB;
+                    const uint32_t b = it % C::NB, from = taddr + b * 256;
                     const float s0 = fa[0] * f0[0], s1 = C::GU ? fa[0] * f1[0] : s0;
                     fa[0] = fa[1]; f0[0] = f0[1]; f1[0] = f1[1];
                     const int nx = min(i + 2, KB - 1);
@@ -626,12 +640,15 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
                     mbar_wait(&t_full[b], (it / C::NB) & 1, abort_flag, p.err);
                     __syncwarp();
                     tc_fence_after();
+                    // the next 32 columns are on their way while the last are summed
+                    uint32_t d[2][32];
+                    tmem_ld_32x32b_x32(from, d[0]);
 #pragma unroll
-                    for (int c = 0; c < 64; c += 16) {
-                        uint32_t d[16];
-                        tmem_ld_32x32b_x16(taddr + b * 256 + c, d);
-                        tmem_ld_wait(d);
-                        if (c == 48) {
+                    for (int c = 0; c < 4; ++c) {
+                        tmem_ld_wait(d[c & 1]);
+                        if (c < 3) {
+                            tmem_ld_32x32b_x32(from + 32 * (c + 1), d[(c + 1) & 1]);
+                        } else {
                             tc_fence_before();
                             __syncwarp();
                             if (lane == 0) {
@@ -640,71 +657,77 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
                             }
                         }
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) acc[c + j] = fmaf(__uint_as_float(d[j]), c < 32 ? s0 : s1, acc[c + j]);
+                        for (int j = 0; j < 16; ++j) fma2(acc[c * 16 + j], d[c & 1][2 * j], d[c & 1][2 * j + 1], c < 2 ? s0 : s1);
                     }
                 }
             }
             const bool live = lrow < mine;
             if constexpr (C::GU) {
-                // h of features 32 w .. 32 w + 31 of the tile; the block's largest
-                // over the four groups through shared memory
-                const int n = wk.nt * 128 + w * 32;
+                // h of features 64 w .. 64 w + 63 of the tile; the block's largest
+                // over the two groups through shared memory
+                const int n = wk.nt * 128 + w * 64;
                 float top = 0.0f;
 #pragma unroll
                 for (int j = 0; j < 32; ++j) {
-                    acc[j] = n + j < p.N ? swiglu(acc[j], acc[32 + j]) : 0.0f;
-                    top = fmaxf(top, finite_abs(acc[j]));
+                    acc[j].x = n + 2 * j < p.N ? swiglu(acc[j].x, acc[32 + j].x) : 0.0f;
+                    acc[j].y = n + 2 * j < p.N ? swiglu(acc[j].y, acc[32 + j].y) : 0.0f;
+                    top = fmaxf(top, fmaxf(finite_abs(acc[j].x), finite_abs(acc[j].y)));
                 }
-                float *t4 = tops + parity * 4 * 128 + lrow;
-                t4[w * 128] = top;
+                float *t2 = tops + parity * 2 * 128 + lrow;
+                t2[w * 128] = top;
                 named_barrier(1, C::EPI * 32);
-                top = fmaxf(fmaxf(t4[0], t4[128]), fmaxf(t4[256], t4[384]));
+                top = fmaxf(t2[0], t2[128]);
                 parity ^= 1;
                 if (live) {
                     const int sp = f8_scale_exp(top);
                     const float inv = pow2f(-sp);
                     uint8_t *h = static_cast<uint8_t *>(p.y) + row * p.N + n;
 #pragma unroll
-                    for (int j = 0; j < 32; j += 16)   // (N is a multiple of 16, h 16-byte aligned)
-                        if (n + j < p.N) {
+                    for (int j = 0; j < 32; j += 8)   // (N is a multiple of 16, h 16-byte aligned)
+                        if (n + 2 * j < p.N) {
                             uint32_t v[4];
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
-                                v[k] = f8x4_satfinite(acc[j + 4 * k] * inv, acc[j + 4 * k + 1] * inv, acc[j + 4 * k + 2] * inv,
-                                                      acc[j + 4 * k + 3] * inv);
-                            *reinterpret_cast<uint4 *>(h + j) = make_uint4(v[0], v[1], v[2], v[3]);
+                                v[k] = f8x4_satfinite(acc[j + 2 * k].x * inv, acc[j + 2 * k].y * inv, acc[j + 2 * k + 1].x * inv,
+                                                      acc[j + 2 * k + 1].y * inv);
+                            *reinterpret_cast<uint4 *>(h + 2 * j) = make_uint4(v[0], v[1], v[2], v[3]);
                         }
                     if (w == 0) p.y_scale[row * nb + wk.nt] = pow2f(sp);
                 }
             } else if (live) {
-                const int n = wk.nt * 256 + w * 64;
+                const int n = wk.nt * 256 + w * 128;
                 if (p.y_bf16) {
                     __nv_bfloat16 *y = static_cast<__nv_bfloat16 *>(p.y) + row * p.N + n;
 #pragma unroll
-                    for (int j = 0; j < 64; j += 8) {
-                        if (p.vec && n + j + 7 < p.N) {
+                    for (int j = 0; j < 64; j += 4) {
+                        if (p.vec && n + 2 * j + 7 < p.N) {
                             uint32_t v[4];
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
-                                const __nv_bfloat162 two = __floats2bfloat162_rn(acc[j + 2 * k], acc[j + 2 * k + 1]);
+                                const __nv_bfloat162 two = __floats2bfloat162_rn(acc[j + k].x, acc[j + k].y);
                                 v[k] = *reinterpret_cast<const uint32_t *>(&two);
                             }
-                            *reinterpret_cast<uint4 *>(y + j) = make_uint4(v[0], v[1], v[2], v[3]);
+                            *reinterpret_cast<uint4 *>(y + 2 * j) = make_uint4(v[0], v[1], v[2], v[3]);
                         } else {
 #pragma unroll
-                            for (int k = 0; k < 8; ++k)
-                                if (n + j + k < p.N) y[j + k] = __float2bfloat16_rn(acc[j + k]);
+                            for (int k = 0; k < 4; ++k) {
+                                if (n + 2 * (j + k) < p.N) y[2 * (j + k)] = __float2bfloat16_rn(acc[j + k].x);
+                                if (n + 2 * (j + k) + 1 < p.N) y[2 * (j + k) + 1] = __float2bfloat16_rn(acc[j + k].y);
+                            }
                         }
                     }
                 } else {
                     float *y = static_cast<float *>(p.y) + row * p.N + n;
 #pragma unroll
-                    for (int j = 0; j < 64; j += 4) {
-                        if (p.vec && n + j + 3 < p.N) *reinterpret_cast<float4 *>(y + j) = make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
+                    for (int j = 0; j < 64; j += 2) {
+                        if (p.vec && n + 2 * j + 3 < p.N)
+                            *reinterpret_cast<float4 *>(y + 2 * j) = make_float4(acc[j].x, acc[j].y, acc[j + 1].x, acc[j + 1].y);
                         else {
 #pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                if (n + j + k < p.N) y[j + k] = acc[j + k];
+                            for (int k = 0; k < 2; ++k) {
+                                if (n + 2 * (j + k) < p.N) y[2 * (j + k)] = acc[j + k].x;
+                                if (n + 2 * (j + k) + 1 < p.N) y[2 * (j + k) + 1] = acc[j + k].y;
+                            }
                         }
                     }
                 }
@@ -819,6 +842,12 @@ static cudaError_t launch_large(const Fp8Args &a, cudaStream_t s) {
     int64_t clusters = di.num_sms / C::CTAS;
     if (tiles < clusters) clusters = tiles;
     const size_t smem = C::SMEM + (a.offsets ? ((size_t)a.E + 2) * 4 : 0);
+    // the registers' shift adds up only for the count that the kernel is launched with
+    static const int regs = [] {
+        cudaFuncAttributes f{};
+        return cudaFuncGetAttributes(&f, large_kernel<C>) == cudaSuccess ? f.numRegs : 0;
+    }();
+    if (regs != C::REGS) return cudaErrorInvalidConfiguration;
     const cudaError_t e = ensure_dynamic_smem((const void *)large_kernel<C>, smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
