@@ -410,7 +410,7 @@ struct LargeCfg {
     static constexpr int TM = 128 * CTAS;                    // rows of a
     static constexpr int TNW = GU ? 128 : 256;               // rows of W (of each, GU)
     static constexpr int W_ROWS = 256 / CTAS;                // W rows that a CTA holds
-    static constexpr int W_BOX = GU ? 64 : 128;
+    static constexpr int W_BOX = 64;
     static constexpr int A_BYTES = 128 * 128;
     static constexpr int STAGE = A_BYTES + W_ROWS * 128;
     static constexpr int NS = PAIR ? 6 : 4;
@@ -421,7 +421,8 @@ struct LargeCfg {
     // to the two summing warpgroups: 256 * 224 + 128 * 56 = 384 * 168
     static constexpr int REGS = 168, REGS_SUM = 224, REGS_REST = 56;
     static constexpr int GROUP = 8;                          // dense: row tiles that share a W tile in turn
-    static constexpr int OFF_TOP = NS * STAGE;               // GU: largest h of (tile parity, group, row)
+    static constexpr int OFF_OUT = NS * STAGE;               // 2 KB a summing warp: 32 rows x 64 bytes of the result
+    static constexpr int OFF_TOP = OFF_OUT + EPI * 2048;     // GU: largest h of (tile parity, group, row)
     static constexpr int OFF_BAR = OFF_TOP + (GU ? 2 * 2 * 128 * 4 : 0);
     static constexpr int OFF_CUM = OFF_BAR + (2 * NS + 2 * NB + 1) * 8 + 24;
     static constexpr int SMEM = OFF_CUM + 1024;              // + the row tiles before each group of rows
@@ -559,7 +560,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
                     uint8_t *dst = st + C::A_BYTES + b * C::W_BOX * 128;
                     const int at = rank * (C::W_ROWS / C::W_BOX) + b;   // box of the whole W tile
                     if constexpr (C::GU) load(dst, at & 1 ? &maps.w1 : &maps.w0, w_row + (at >> 1) * 64);
-                    else load(dst, &maps.w0, w_row + at * C::W_BOX);
+                    else load(dst, &maps.w0, w_row + at * 64);
                 }
             }
             ok = __shfl_sync(0xffffffffu, ok && !*abort_flag, 0);
@@ -578,8 +579,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
             for (; ok && wk.get(p, cum, n_tiles); wk.t += clusters) {
                 for (int i = 0; i < KB && lane == 0 && wk.e < p.E; ++i, ++it) {
                     const uint32_t s = it % C::NS, b = it % C::NB;
-                    if (it >= C::NB && !mbar_wait(&t_empty[b], ((it / C::NB) & 1) ^ 1, abort_flag, p.err)) { ok = false; break; }
                     if (!mbar_wait(&s_full[s], (it / C::NS) & 1, abort_flag, p.err)) { ok = false; break; }
+                    if (it >= C::NB && !mbar_wait(&t_empty[b], ((it / C::NB) & 1) ^ 1, abort_flag, p.err)) { ok = false; break; }
                     tc_fence_after();
                     const uint32_t st = smem_u32(smem + s * C::STAGE);
                     const uint64_t ad = smem_desc_k_sw128(st), bd = smem_desc_k_sw128(st + C::A_BYTES);
@@ -588,8 +589,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
                         if constexpr (C::PAIR) tc_mma_f8_pair(tmem + b * 256, ad + 2 * k, bd + 2 * k, idesc, k != 0);
                         else tc_mma_f8(tmem + b * 256, ad + 2 * k, bd + 2 * k, idesc, k != 0);
                     }
-                    if constexpr (C::PAIR) { tc_commit_pair(&s_empty[s]); tc_commit_pair(&t_full[b]); }
-                    else { tc_commit(&s_empty[s]); tc_commit(&t_full[b]); }
+                    if constexpr (C::PAIR) { tc_commit_pair(&t_full[b]); tc_commit_pair(&s_empty[s]); }
+                    else { tc_commit(&t_full[b]); tc_commit(&s_empty[s]); }
                 }
                 ok = __shfl_sync(0xffffffffu, ok && !*abort_flag, 0);
             }
@@ -608,64 +609,104 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
         const int nb = (p.N + kF8Block - 1) / kF8Block;
         const uint32_t taddr = tmem + w * 128 + ((uint32_t)(q * 32) << 16);
         const uint32_t empty0 = C::PAIR ? mapa_shared(smem_u32(t_empty), 0) : 0;
+        uint8_t *out = smem + C::OFF_OUT + warp * 2048;
         uint32_t it = 0;
         int parity = 0;
-        for (; wk.get(p, cum, n_tiles); wk.t += clusters) {
-            const int mine = wk.rows - 128 * rank;           // rows of this CTA (may be none)
-            const int64_t row = wk.row0 + min(128 * rank + lrow, wk.rows - 1);
+        // scales two K blocks ahead; those of the next tile are asked for before
+        // this one is stored
+        const float *pa = nullptr, *p0 = nullptr, *p1 = nullptr;
+        float fa[2], f0[2], f1[2];
+        auto prime = [&] {
+            if (wk.e >= p.E) return;
+            const int b0 = C::GU ? wk.nt : min(wk.nt * 2 + w, nb - 1);
+            pa = p.sa + (int64_t)(wk.row0 + min(128 * rank + lrow, wk.rows - 1)) * KB;
+            p0 = p.sw0 + ((int64_t)wk.e * nb + b0) * KB;
+            p1 = C::GU ? p.sw1 + ((int64_t)wk.e * nb + b0) * KB : p0;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int i = min(k, KB - 1);
+                fa[k] = __ldg(pa + i);
+                f0[k] = __ldg(p0 + i);
+                f1[k] = C::GU ? __ldg(p1 + i) : 0.0f;
+            }
+        };
+        bool have = wk.get(p, cum, n_tiles);
+        if (have) prime();
+        while (have) {
             float2 acc[64];
 #pragma unroll
             for (int j = 0; j < 64; ++j) acc[j] = make_float2(0.0f, 0.0f);
-            if (wk.e < p.E) {
-                const int b0 = C::GU ? wk.nt : min(wk.nt * 2 + w, nb - 1);
-                const float *pa = p.sa + row * KB;
-                const float *p0 = p.sw0 + ((int64_t)wk.e * nb + b0) * KB, *p1 = C::GU ? p.sw1 + ((int64_t)wk.e * nb + b0) * KB : p0;
-                // scales two K blocks ahead
-                float fa[2], f0[2], f1[2];
+            for (int i = 0; i < KB && wk.e < p.E; ++i, ++it) {
+                const uint32_t b = it % C::NB, from = taddr + b * 256;
+                const float s0 = fa[0] * f0[0], s1 = C::GU ? fa[0] * f1[0] : s0;
+                fa[0] = fa[1]; f0[0] = f0[1]; f1[0] = f1[1];
+                const int nx = min(i + 2, KB - 1);
+                fa[1] = __ldg(pa + nx);
+                f0[1] = __ldg(p0 + nx);
+                if (C::GU) f1[1] = __ldg(p1 + nx);
+                mbar_wait(&t_full[b], (it / C::NB) & 1, abort_flag, p.err);
+                __syncwarp();
+                tc_fence_after();
+                // the next 32 columns are on their way while the last are summed
+                uint32_t d[2][32];
+                tmem_ld_32x32b_x32(from, d[0]);
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const int i = min(k, KB - 1);
-                    fa[k] = __ldg(pa + i);
-                    f0[k] = __ldg(p0 + i);
-                    f1[k] = C::GU ? __ldg(p1 + i) : 0.0f;
-                }
-                for (int i = 0; i < KB; ++i, ++it) {
-                    const uint32_t b = it % C::NB, from = taddr + b * 256;
-                    const float s0 = fa[0] * f0[0], s1 = C::GU ? fa[0] * f1[0] : s0;
-                    fa[0] = fa[1]; f0[0] = f0[1]; f1[0] = f1[1];
-                    const int nx = min(i + 2, KB - 1);
-                    fa[1] = __ldg(pa + nx);
-                    f0[1] = __ldg(p0 + nx);
-                    if (C::GU) f1[1] = __ldg(p1 + nx);
-                    mbar_wait(&t_full[b], (it / C::NB) & 1, abort_flag, p.err);
-                    __syncwarp();
-                    tc_fence_after();
-                    // the next 32 columns are on their way while the last are summed
-                    uint32_t d[2][32];
-                    tmem_ld_32x32b_x32(from, d[0]);
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        tmem_ld_wait(d[c & 1]);
-                        if (c < 3) {
-                            tmem_ld_32x32b_x32(from + 32 * (c + 1), d[(c + 1) & 1]);
-                        } else {
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) {
-                                if constexpr (C::PAIR) mbar_arrive_cluster(empty0 + b * 8);
-                                else mbar_arrive(&t_empty[b]);
-                            }
+                for (int c = 0; c < 4; ++c) {
+                    tmem_ld_wait(d[c & 1]);
+                    if (c < 3) {
+                        tmem_ld_32x32b_x32(from + 32 * (c + 1), d[(c + 1) & 1]);
+                    } else {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) {
+                            if constexpr (C::PAIR) mbar_arrive_cluster(empty0 + b * 8);
+                            else mbar_arrive(&t_empty[b]);
                         }
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) fma2(acc[c * 16 + j], d[c & 1][2 * j], d[c & 1][2 * j + 1], c < 2 ? s0 : s1);
                     }
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) fma2(acc[c * 16 + j], d[c & 1][2 * j], d[c & 1][2 * j + 1], c < 2 ? s0 : s1);
                 }
             }
-            const bool live = lrow < mine;
+            const int wrow = 128 * rank + q * 32;            // this warp's first row of the tile
+            const int left = wk.rows - wrow;                 // and how many are the tile's
+            const int64_t row = wk.row0 + wrow;
+            const int nt = wk.nt;
+            wk.t += clusters;
+            have = wk.get(p, cum, n_tiles);
+            if (have) prime();
+            // 64 bytes of every row of the warp, by 16 per thread, through shared
+            // memory: a row's bytes are then written by neighbouring lanes (each lane
+            // storing its own row would touch 32 lines an instruction: 3.4 us a tile
+            // of 256 columns in bf16)
+            auto store = [&](uint8_t *dst, int64_t pitch, int bytes, int elem, bool vec, const uint4 (&v)[4]) {
+                __syncwarp();
+#pragma unroll
+                for (int c = 0; c < 4; ++c) *reinterpret_cast<uint4 *>(out + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) = v[c];
+                __syncwarp();
+                if (vec) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = i * 8 + (lane >> 2), c = lane & 3;
+                        if (r < left && c * 16 < bytes)
+                            *reinterpret_cast<uint4 *>(dst + r * pitch + c * 16) =
+                                *reinterpret_cast<const uint4 *>(out + r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+                    }
+                } else {
+                    // rows of any alignment: element by element
+                    const int at = lane * elem & 63;
+                    for (int r = lane * elem >> 6; r < left && r < 32; r += elem >> 1) {
+                        const uint8_t *from = out + r * 64 + (((at >> 4) ^ ((r >> 1) & 3)) << 4) + (at & 15);
+                        if (at < bytes) {
+                            if (elem == 2) *reinterpret_cast<uint16_t *>(dst + r * pitch + at) = *reinterpret_cast<const uint16_t *>(from);
+                            else *reinterpret_cast<uint32_t *>(dst + r * pitch + at) = *reinterpret_cast<const uint32_t *>(from);
+                        }
+                    }
+                }
+            };
             if constexpr (C::GU) {
                 // h of features 64 w .. 64 w + 63 of the tile; the block's largest
                 // over the two groups through shared memory
-                const int n = wk.nt * 128 + w * 64;
+                const int n = nt * 128 + w * 64;
                 float top = 0.0f;
 #pragma unroll
                 for (int j = 0; j < 32; ++j) {
@@ -678,57 +719,53 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
                 named_barrier(1, C::EPI * 32);
                 top = fmaxf(t2[0], t2[128]);
                 parity ^= 1;
-                if (live) {
-                    const int sp = f8_scale_exp(top);
-                    const float inv = pow2f(-sp);
-                    uint8_t *h = static_cast<uint8_t *>(p.y) + row * p.N + n;
+                const int sp = f8_scale_exp(top);
+                const float inv = pow2f(-sp);
+                uint4 v[4];
 #pragma unroll
-                    for (int j = 0; j < 32; j += 8)   // (N is a multiple of 16, h 16-byte aligned)
-                        if (n + 2 * j < p.N) {
-                            uint32_t v[4];
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t u[4];
 #pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                v[k] = f8x4_satfinite(acc[j + 2 * k].x * inv, acc[j + 2 * k].y * inv, acc[j + 2 * k + 1].x * inv,
-                                                      acc[j + 2 * k + 1].y * inv);
-                            *reinterpret_cast<uint4 *>(h + 2 * j) = make_uint4(v[0], v[1], v[2], v[3]);
-                        }
-                    if (w == 0) p.y_scale[row * nb + wk.nt] = pow2f(sp);
+                    for (int k = 0; k < 4; ++k) {
+                        const float2 lo = acc[c * 8 + 2 * k], hi = acc[c * 8 + 2 * k + 1];
+                        u[k] = f8x4_satfinite(lo.x * inv, lo.y * inv, hi.x * inv, hi.y * inv);
+                    }
+                    v[c] = make_uint4(u[0], u[1], u[2], u[3]);
                 }
-            } else if (live) {
-                const int n = wk.nt * 256 + w * 128;
+                // (N is a multiple of 16 and h 16-byte aligned)
+                store(static_cast<uint8_t *>(p.y) + row * p.N + n, p.N, p.N - n, 1, true, v);
+                if (w == 0 && lane < left) p.y_scale[(row + lane) * nb + nt] = pow2f(sp);
+            } else {
+                const int n = nt * 256 + w * 128;
                 if (p.y_bf16) {
-                    __nv_bfloat16 *y = static_cast<__nv_bfloat16 *>(p.y) + row * p.N + n;
+                    uint8_t *dst = static_cast<uint8_t *>(p.y) + (row * p.N + n) * 2;
 #pragma unroll
-                    for (int j = 0; j < 64; j += 4) {
-                        if (p.vec && n + 2 * j + 7 < p.N) {
-                            uint32_t v[4];
+                    for (int c = 0; c < 4; ++c) {            // 32 columns
+                        uint4 v[4];
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const __nv_bfloat162 two = __floats2bfloat162_rn(acc[j + k].x, acc[j + k].y);
-                                v[k] = *reinterpret_cast<const uint32_t *>(&two);
-                            }
-                            *reinterpret_cast<uint4 *>(y + 2 * j) = make_uint4(v[0], v[1], v[2], v[3]);
-                        } else {
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t u[4];
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
-                                if (n + 2 * (j + k) < p.N) y[2 * (j + k)] = __float2bfloat16_rn(acc[j + k].x);
-                                if (n + 2 * (j + k) + 1 < p.N) y[2 * (j + k) + 1] = __float2bfloat16_rn(acc[j + k].y);
+                                const float2 f = acc[c * 16 + i * 4 + k];
+                                const __nv_bfloat162 two = __floats2bfloat162_rn(f.x, f.y);
+                                u[k] = *reinterpret_cast<const uint32_t *>(&two);
                             }
+                            v[i] = make_uint4(u[0], u[1], u[2], u[3]);
                         }
+                        store(dst + c * 64, (int64_t)p.N * 2, (p.N - n) * 2 - c * 64, 2, p.vec, v);
                     }
                 } else {
-                    float *y = static_cast<float *>(p.y) + row * p.N + n;
+                    uint8_t *dst = static_cast<uint8_t *>(p.y) + (row * p.N + n) * 4;
 #pragma unroll
-                    for (int j = 0; j < 64; j += 2) {
-                        if (p.vec && n + 2 * j + 3 < p.N)
-                            *reinterpret_cast<float4 *>(y + 2 * j) = make_float4(acc[j].x, acc[j].y, acc[j + 1].x, acc[j + 1].y);
-                        else {
+                    for (int c = 0; c < 8; ++c) {            // 16 columns
+                        uint4 v[4];
 #pragma unroll
-                            for (int k = 0; k < 2; ++k) {
-                                if (n + 2 * (j + k) < p.N) y[2 * (j + k)] = acc[j + k].x;
-                                if (n + 2 * (j + k) + 1 < p.N) y[2 * (j + k) + 1] = acc[j + k].y;
-                            }
+                        for (int i = 0; i < 4; ++i) {
+                            const float2 lo = acc[c * 8 + i * 2], hi = acc[c * 8 + i * 2 + 1];
+                            v[i] = make_uint4(__float_as_uint(lo.x), __float_as_uint(lo.y), __float_as_uint(hi.x), __float_as_uint(hi.y));
                         }
+                        store(dst + c * 64, (int64_t)p.N * 4, (p.N - n) * 4 - c * 64, 4, p.vec, v);
                     }
                 }
             }
@@ -873,7 +910,8 @@ static cudaError_t launch(const Fp8Args &a, cudaStream_t s) {
     // many rows: the large tiles, where they fill the SMs at least twice over (a
     // dense call with fewer splits K instead)
     const int64_t per = (a.N + LargeCfg<false, GU>::TNW - 1) / LargeCfg<false, GU>::TNW;
-    if (a.offsets ? a.M / a.E > 64 : a.M > 64 && (a.M + 127) / 128 * per >= 76) {
+    const bool fits = LargeCfg<false, GU>::SMEM + (a.E + 2) * 4 <= device_info().max_smem_optin;   // (E <= 4046)
+    if (a.offsets ? fits && a.M / a.E > 64 : a.M > 64 && (a.M + 127) / 128 * per >= 76) {
         if (!a.offsets && a.M >= 256) return launch_large<LargeCfg<true, GU>>(a, s);
         return launch_large<LargeCfg<false, GU>>(a, s);
     }
