@@ -115,6 +115,7 @@ struct Params {
     int *err;
     int M, N, K, E;
     int row_tiles;      // bound of the number of row tiles
+    int n_tiles;        // large: tiles of W's rows
     int y_bf16;         // plain: y is bf16 (else fp32)
     int vec;            // y's rows take vector stores (small: 4 elements, large: 16 bytes)
 };
@@ -401,7 +402,8 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) small_kernel(const __gr
 // taken out.
 //
 // Roles: warps 0 .. 7 scale and sum (group w = warp / 4 takes columns 128 w ..
-// 128 w + 127, 128 sums a thread), warp 8 loads by TMA, warp 9 issues the MMAs.
+// 128 w + 127, 128 sums a thread), warp 8 loads by TMA, warp 9 issues the MMAs,
+// warp 10 brings the scales to shared memory.
 // ---------------------------------------------------------------------------
 template <bool PAIR_, bool GU_>
 struct LargeCfg {
@@ -410,7 +412,7 @@ struct LargeCfg {
     static constexpr int TM = 128 * CTAS;                    // rows of a
     static constexpr int TNW = GU ? 128 : 256;               // rows of W (of each, GU)
     static constexpr int W_ROWS = 256 / CTAS;                // W rows that a CTA holds
-    static constexpr int W_BOX = 64;
+    static constexpr int W_BOX = GU ? 64 : 128;
     static constexpr int A_BYTES = 128 * 128;
     static constexpr int STAGE = A_BYTES + W_ROWS * 128;
     static constexpr int NS = PAIR ? 6 : 4;
@@ -418,13 +420,17 @@ struct LargeCfg {
     static constexpr int EPI = 8;
     static constexpr int THREADS = 384;                      // three warpgroups
     // registers a thread: 168 at launch (what 384 threads can have), then shifted
-    // to the two summing warpgroups: 256 * 224 + 128 * 56 = 384 * 168
-    static constexpr int REGS = 168, REGS_SUM = 224, REGS_REST = 56;
+    // to the two summing warpgroups: 256 * 208 + 128 * 88 = 384 * 168
+    static constexpr int REGS = 168, REGS_SUM = 208, REGS_REST = 88;
     static constexpr int GROUP = 8;                          // dense: row tiles that share a W tile in turn
+    // scales: slots of SEG K blocks, [K block][128 rows of a, then 2 of W's blocks]
+    static constexpr int SEG = 4, SLOTS = 4, SROW = 136;
+    static constexpr int SLOT = SEG * SROW;                  // floats (a pitch of 136 spreads the K blocks over the banks)
     static constexpr int OFF_OUT = NS * STAGE;               // 2 KB a summing warp: 32 rows x 64 bytes of the result
     static constexpr int OFF_TOP = OFF_OUT + EPI * 2048;     // GU: largest h of (tile parity, group, row)
-    static constexpr int OFF_BAR = OFF_TOP + (GU ? 2 * 2 * 128 * 4 : 0);
-    static constexpr int OFF_CUM = OFF_BAR + (2 * NS + 2 * NB + 1) * 8 + 24;
+    static constexpr int OFF_SC = OFF_TOP + (GU ? 2 * 2 * 128 * 4 : 0);
+    static constexpr int OFF_BAR = OFF_SC + SLOTS * SLOT * 4;
+    static constexpr int OFF_CUM = OFF_BAR + (2 * NS + 2 * NB + 2 * SLOTS + 1) * 8 + 24;
     static constexpr int SMEM = OFF_CUM + 1024;              // + the row tiles before each group of rows
 };
 
@@ -432,38 +438,36 @@ struct LargeCfg {
 template <class C>
 struct Walk {
     int e, row0, rows, nt;   // rows: of the tile, <= C::TM
-    int64_t t;
-    int g;                   // grouped: the expert of the tile before
+    int t;
 
-    __device__ __forceinline__ void start(int cluster) { t = cluster; g = 0; }
+    __device__ __forceinline__ void start(int cluster) { t = cluster; e = 0; }
     // false past the last tile.  One full warp.  cum[g]: row tiles before group g.
-    __device__ __forceinline__ bool get(const Params &p, const int *cum, int n_tiles) {
+    __device__ __forceinline__ bool get(const Params &p, const int *cum) {
+        const int n_tiles = p.n_tiles;
         if (!p.offsets) {
             const int rt_all = p.row_tiles;
-            if (t >= (int64_t)rt_all * n_tiles) return false;
-            const int band = (int)(t / ((int64_t)C::GROUP * n_tiles)), first = band * C::GROUP;
-            const int in = (int)(t - (int64_t)first * n_tiles), wide = min(C::GROUP, rt_all - first);
+            if (t >= rt_all * n_tiles) return false;
+            const int first = t / (C::GROUP * n_tiles) * C::GROUP;
+            const int in = t - first * n_tiles, wide = min(C::GROUP, rt_all - first);
             nt = in / wide;
-            e = 0;
             row0 = (first + in - nt * wide) * C::TM;
             rows = min(C::TM, p.M - row0);
             return true;
         }
         const int groups = p.E + 1;
-        if (t >= (int64_t)cum[groups] * n_tiles) return false;
-        const int rt = (int)(t / n_tiles), lane = threadIdx.x & 31;
-        nt = (int)(t - (int64_t)rt * n_tiles);
-        for (;; g += 32) {   // the group whose tiles hold rt: ascending from the last one
-            const unsigned past = __ballot_sync(0xffffffffu, cum[min(g + lane + 1, groups)] > rt);
+        if (t >= cum[groups] * n_tiles) return false;
+        const int rt = t / n_tiles, lane = threadIdx.x & 31;
+        nt = t - rt * n_tiles;
+        for (;; e += 32) {   // the group whose tiles hold rt: ascending from the last one
+            const unsigned past = __ballot_sync(0xffffffffu, cum[min(e + lane + 1, groups)] > rt);
             if (past) {
-                g += __ffs(past) - 1;
+                e += __ffs(past) - 1;
                 break;
             }
         }
-        e = g;
-        const int lo = min(max(__ldg(p.offsets + g), 0), p.M);
-        const int hi = g < p.E ? min(max(__ldg(p.offsets + g + 1), 0), p.M) : p.M;
-        const int done = (rt - cum[g]) * C::TM;
+        const int lo = min(max(__ldg(p.offsets + e), 0), p.M);
+        const int hi = e < p.E ? min(max(__ldg(p.offsets + e + 1), 0), p.M) : p.M;
+        const int done = (rt - cum[e]) * C::TM;
         row0 = lo + done;
         rows = min(C::TM, hi - row0);
         return true;
@@ -476,19 +480,21 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     float *tops = reinterpret_cast<float *>(smem + C::OFF_TOP);
     uint64_t *s_full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
-    uint64_t *s_empty = s_full + C::NS, *t_full = s_empty + C::NS, *t_empty = t_full + C::NB, *done = t_empty + C::NB;
+    uint64_t *s_empty = s_full + C::NS, *t_full = s_empty + C::NS, *t_empty = t_full + C::NB;
+    uint64_t *c_full = t_empty + C::NB, *c_empty = c_full + C::SLOTS, *done = c_empty + C::SLOTS;
     int *info = reinterpret_cast<int *>(done + 1);           // abort, TMEM base
+    float *scales = reinterpret_cast<float *>(smem + C::OFF_SC);
     int *cum = reinterpret_cast<int *>(smem + C::OFF_CUM);
     volatile int *abort_flag = info;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = C::PAIR ? (int)cluster_ctarank() : 0;
     const int KB = (p.K + kF8Block - 1) / kF8Block;
-    const int n_tiles = (p.N + C::TNW - 1) / C::TNW;
 
     if (warp == C::EPI && lane == 0) {
         info[0] = 0;
         for (int i = 0; i < C::NS; ++i) { mbar_init(&s_full[i], 1); mbar_init(&s_empty[i], 1); }
         for (int i = 0; i < C::NB; ++i) { mbar_init(&t_full[i], 1); mbar_init(&t_empty[i], C::EPI * C::CTAS); }
+        for (int i = 0; i < C::SLOTS; ++i) { mbar_init(&c_full[i], 1); mbar_init(&c_empty[i], C::EPI); }
         mbar_init(done, 1);
         fence_mbarrier_init();
         prefetch_tensormap(&maps.a);
@@ -533,7 +539,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
     if (C::PAIR) cluster_sync_all();   // the peer's barriers are set up
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(info + 1);
-    const int clusters = gridDim.x / C::CTAS;
     Walk<C> wk;
     wk.start(blockIdx.x / C::CTAS);
     if (warp >= C::EPI) reg_dealloc<C::REGS_REST>();
@@ -543,7 +548,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
         const uint32_t full0 = C::PAIR ? mapa_shared(smem_u32(s_full), 0) : 0;
         uint32_t it = 0;
         bool ok = true;
-        for (; ok && wk.get(p, cum, n_tiles); wk.t += clusters) {
+        for (; ok && wk.get(p, cum); wk.t += gridDim.x / C::CTAS) {
             for (int i = 0; i < KB && lane == 0 && wk.e < p.E; ++i, ++it) {
                 const uint32_t s = it % C::NS;
                 if (it >= C::NS && !mbar_wait(&s_empty[s], ((it / C::NS) & 1) ^ 1, abort_flag, p.err)) { ok = false; break; }
@@ -559,8 +564,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
                 for (int b = 0; b < C::W_ROWS / C::W_BOX; ++b) {
                     uint8_t *dst = st + C::A_BYTES + b * C::W_BOX * 128;
                     const int at = rank * (C::W_ROWS / C::W_BOX) + b;   // box of the whole W tile
-                    if constexpr (C::GU) load(dst, at & 1 ? &maps.w1 : &maps.w0, w_row + (at >> 1) * 64);
-                    else load(dst, &maps.w0, w_row + at * 64);
+                    if constexpr (C::GU) load(dst, at & 1 ? &maps.w1 : &maps.w0, w_row + (at >> 1) * C::W_BOX);
+                    else load(dst, &maps.w0, w_row + at * C::W_BOX);
                 }
             }
             ok = __shfl_sync(0xffffffffu, ok && !*abort_flag, 0);
@@ -576,7 +581,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
         if (rank == 0) {
             uint32_t it = 0;
             bool ok = true;
-            for (; ok && wk.get(p, cum, n_tiles); wk.t += clusters) {
+            for (; ok && wk.get(p, cum); wk.t += gridDim.x / C::CTAS) {
                 for (int i = 0; i < KB && lane == 0 && wk.e < p.E; ++i, ++it) {
                     const uint32_t s = it % C::NS, b = it % C::NB;
                     if (!mbar_wait(&s_full[s], (it / C::NS) & 1, abort_flag, p.err)) { ok = false; break; }
@@ -602,6 +607,40 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
         // (both CTAs of a pair: no commit's arrival is left on its way)
         if (lane == 0) mbar_wait(done, 0, nullptr, p.err);
         __syncwarp();
+    } else if (warp == C::EPI + 2) {
+        // ---- scales: this CTA's rows of a, and the tile's blocks of W (plain: two
+        // blocks of rows; GU: gate and up), SEG K blocks at a time
+        const int nb = (p.N + kF8Block - 1) / kF8Block;
+        uint32_t ck = 0;
+        bool ok = true;
+        for (; ok && wk.get(p, cum); wk.t += gridDim.x / C::CTAS) {
+            const int b0 = C::GU ? wk.nt : wk.nt * 2, b1 = C::GU ? b0 : min(b0 + 1, nb - 1);
+            for (int i = 0; i < KB && wk.e < p.E; i += C::SEG, ++ck) {
+                const uint32_t c = ck % C::SLOTS;
+                ok = ck < C::SLOTS || mbar_wait(&c_empty[c], ((ck / C::SLOTS) & 1) ^ 1, abort_flag, p.err);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                float *dst = scales + c * C::SLOT;
+                const int kb = min(i + (lane & 3), KB - 1);
+                const float *pa = p.sa + (int64_t)wk.row0 * KB + kb;
+                float f[4];
+#pragma unroll
+                for (int r0 = 0; r0 < 128; r0 += 32) {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        f[r] = __ldg(pa + (int64_t)min(128 * rank + r0 + r * 8 + (lane >> 2), wk.rows - 1) * KB);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) dst[(lane & 3) * C::SROW + r0 + r * 8 + (lane >> 2)] = f[r];
+                }
+                if (lane < 8) {
+                    const float *pw = C::GU && (lane >> 2) ? p.sw1 : p.sw0;
+                    dst[(lane & 3) * C::SROW + 128 + (lane >> 2)] =
+                        __ldg(pw + ((int64_t)wk.e * nb + ((lane >> 2) ? b1 : b0)) * KB + kb);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&c_full[c]);
+            }
+        }
     } else if (warp < C::EPI) {
         // ---- scale and sum: thread = one row of a, 128 columns
         reg_alloc<C::REGS_SUM>();
@@ -610,51 +649,32 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
         const uint32_t taddr = tmem + w * 128 + ((uint32_t)(q * 32) << 16);
         const uint32_t empty0 = C::PAIR ? mapa_shared(smem_u32(t_empty), 0) : 0;
         uint8_t *out = smem + C::OFF_OUT + warp * 2048;
-        uint32_t it = 0;
+        uint32_t it = 0, ck = 0;
         int parity = 0;
-        // scales two K blocks ahead; those of the next tile are asked for before
-        // this one is stored
-        const float *pa = nullptr, *p0 = nullptr, *p1 = nullptr;
-        float fa[2], f0[2], f1[2];
-        auto prime = [&] {
-            if (wk.e >= p.E) return;
-            const int b0 = C::GU ? wk.nt : min(wk.nt * 2 + w, nb - 1);
-            pa = p.sa + (int64_t)(wk.row0 + min(128 * rank + lrow, wk.rows - 1)) * KB;
-            p0 = p.sw0 + ((int64_t)wk.e * nb + b0) * KB;
-            p1 = C::GU ? p.sw1 + ((int64_t)wk.e * nb + b0) * KB : p0;
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int i = min(k, KB - 1);
-                fa[k] = __ldg(pa + i);
-                f0[k] = __ldg(p0 + i);
-                f1[k] = C::GU ? __ldg(p1 + i) : 0.0f;
-            }
-        };
-        bool have = wk.get(p, cum, n_tiles);
-        if (have) prime();
-        while (have) {
+        for (; wk.get(p, cum); wk.t += gridDim.x / C::CTAS) {
             float2 acc[64];
 #pragma unroll
             for (int j = 0; j < 64; ++j) acc[j] = make_float2(0.0f, 0.0f);
             for (int i = 0; i < KB && wk.e < p.E; ++i, ++it) {
-                const uint32_t b = it % C::NB, from = taddr + b * 256;
-                const float s0 = fa[0] * f0[0], s1 = C::GU ? fa[0] * f1[0] : s0;
-                fa[0] = fa[1]; f0[0] = f0[1]; f1[0] = f1[1];
-                const int nx = min(i + 2, KB - 1);
-                fa[1] = __ldg(pa + nx);
-                f0[1] = __ldg(p0 + nx);
-                if (C::GU) f1[1] = __ldg(p1 + nx);
+                const uint32_t b = it % C::NB, c4 = ck % C::SLOTS;
+                if (i % C::SEG == 0) mbar_wait(&c_full[c4], (ck / C::SLOTS) & 1, abort_flag, p.err);
+                const float *sc = scales + c4 * C::SLOT + (i % C::SEG) * C::SROW;
+                const float sa = sc[lrow], s0 = sa * sc[128 + (C::GU ? 0 : w)], s1 = C::GU ? sa * sc[129] : s0;
                 mbar_wait(&t_full[b], (it / C::NB) & 1, abort_flag, p.err);
                 __syncwarp();
+                if (i % C::SEG == C::SEG - 1 || i == KB - 1) {
+                    if (lane == 0) mbar_arrive(&c_empty[c4]);
+                    ++ck;
+                }
                 tc_fence_after();
                 // the next 32 columns are on their way while the last are summed
                 uint32_t d[2][32];
-                tmem_ld_32x32b_x32(from, d[0]);
+                tmem_ld_32x32b_x32(taddr + b * 256, d[0]);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     tmem_ld_wait(d[c & 1]);
                     if (c < 3) {
-                        tmem_ld_32x32b_x32(from + 32 * (c + 1), d[(c + 1) & 1]);
+                        tmem_ld_32x32b_x32(taddr + b * 256 + 32 * (c + 1), d[(c + 1) & 1]);
                     } else {
                         tc_fence_before();
                         __syncwarp();
@@ -671,9 +691,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
             const int left = wk.rows - wrow;                 // and how many are the tile's
             const int64_t row = wk.row0 + wrow;
             const int nt = wk.nt;
-            wk.t += clusters;
-            have = wk.get(p, cum, n_tiles);
-            if (have) prime();
             // 64 bytes of every row of the warp, by 16 per thread, through shared
             // memory: a row's bytes are then written by neighbouring lanes (each lane
             // storing its own row would touch 32 lines an instruction: 3.4 us a tile
@@ -873,8 +890,9 @@ static cudaError_t launch_large(const Fp8Args &a, cudaStream_t s) {
         return cudaErrorInvalidValue;
     Params p = params(a);
     const int64_t rt = row_tiles_bound(a, C::TM), tiles = rt * ((a.N + C::TNW - 1) / C::TNW);
-    if (rt > 0x7fffffff) return cudaErrorInvalidValue;
+    if (tiles + di.num_sms > 0x7fffffff) return cudaErrorInvalidValue;
     p.row_tiles = (int)rt;
+    p.n_tiles = (a.N + C::TNW - 1) / C::TNW;
     p.vec = a.N % (p.y_bf16 ? 8 : 4) == 0 && (reinterpret_cast<uintptr_t>(a.y) & 15) == 0;
     int64_t clusters = di.num_sms / C::CTAS;
     if (tiles < clusters) clusters = tiles;
