@@ -60,6 +60,28 @@ __device__ __forceinline__ void fma2(float2 &acc, uint32_t d0, uint32_t d1, floa
 }
 template <int R> __device__ __forceinline__ void reg_alloc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
 template <int R> __device__ __forceinline__ void reg_dealloc() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
+// mbar_wait of the large tiles' roles: the barrier is asked without suspending the
+// thread (a suspended thread is woken hundreds of clocks late, once for every
+// K block on the way from the tensor cores to the sums and back), and the bound
+// is a count of tries: the roles have no registers to spare for the clock.
+__device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, volatile int *abort, int *err) {
+    for (int n = 0;; ++n) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity)
+            : "memory");
+        if (ok) return true;
+        if (n > (1 << 26) || ((n & 1023) == 1023 && *abort)) {
+            record_error(err, ZFFN_ERR_TIMEOUT);
+            *abort = 1;
+            return false;
+        }
+    }
+}
 __device__ __forceinline__ float swiglu(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
 
 // A tile of rows of one expert (e == E: rows that belong to no expert).
@@ -551,7 +573,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
         for (; ok && wk.get(p, cum); wk.t += gridDim.x / C::CTAS) {
             for (int i = 0; i < KB && lane == 0 && wk.e < p.E; ++i, ++it) {
                 const uint32_t s = it % C::NS;
-                if (it >= C::NS && !mbar_wait(&s_empty[s], ((it / C::NS) & 1) ^ 1, abort_flag, p.err)) { ok = false; break; }
+                if (it >= C::NS && !bar_wait(&s_empty[s], ((it / C::NS) & 1) ^ 1, abort_flag, p.err)) { ok = false; break; }
                 uint8_t *st = smem + s * C::STAGE;
                 if (rank == 0) mbar_arrive_expect_tx(&s_full[s], C::STAGE * C::CTAS);
                 auto load = [&](uint8_t *dst, const CUtensorMap *m, int c1) {
@@ -581,28 +603,36 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
         if (rank == 0) {
             uint32_t it = 0;
             bool ok = true;
+            // (the whole warp walks and waits, one elected lane issues: in code that
+            // only one thread runs, every MMA cost 115 clocks to issue)
             for (; ok && wk.get(p, cum); wk.t += gridDim.x / C::CTAS) {
-                for (int i = 0; i < KB && lane == 0 && wk.e < p.E; ++i, ++it) {
+                for (int i = 0; i < KB && wk.e < p.E; ++i, ++it) {
                     const uint32_t s = it % C::NS, b = it % C::NB;
-                    if (!mbar_wait(&s_full[s], (it / C::NS) & 1, abort_flag, p.err)) { ok = false; break; }
-                    if (it >= C::NB && !mbar_wait(&t_empty[b], ((it / C::NB) & 1) ^ 1, abort_flag, p.err)) { ok = false; break; }
+                    ok = bar_wait(&s_full[s], (it / C::NS) & 1, abort_flag, p.err) &&
+                         (it < C::NB || bar_wait(&t_empty[b], ((it / C::NB) & 1) ^ 1, abort_flag, p.err));
+                    if (!__all_sync(0xffffffffu, ok)) break;
                     tc_fence_after();
-                    const uint32_t st = smem_u32(smem + s * C::STAGE);
+                    const uint32_t st = smem_u32(smem) + s * C::STAGE;
                     const uint64_t ad = smem_desc_k_sw128(st), bd = smem_desc_k_sw128(st + C::A_BYTES);
+                    const uint32_t dst = tmem + b * 256;
+                    if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {   // 32 bytes of K a step
-                        if constexpr (C::PAIR) tc_mma_f8_pair(tmem + b * 256, ad + 2 * k, bd + 2 * k, idesc, k != 0);
-                        else tc_mma_f8(tmem + b * 256, ad + 2 * k, bd + 2 * k, idesc, k != 0);
+                        for (int k = 0; k < 4; ++k) {   // 32 bytes of K a step
+                            if constexpr (C::PAIR) tc_mma_f8_pair(dst, ad + 2 * k, bd + 2 * k, idesc, k != 0);
+                            else tc_mma_f8(dst, ad + 2 * k, bd + 2 * k, idesc, k != 0);
+                        }
+                        if constexpr (C::PAIR) { tc_commit_pair(&t_full[b]); tc_commit_pair(&s_empty[s]); }
+                        else { tc_commit(&t_full[b]); tc_commit(&s_empty[s]); }
                     }
-                    if constexpr (C::PAIR) { tc_commit_pair(&t_full[b]); tc_commit_pair(&s_empty[s]); }
-                    else { tc_commit(&t_full[b]); tc_commit(&s_empty[s]); }
+                    __syncwarp();
                 }
-                ok = __shfl_sync(0xffffffffu, ok && !*abort_flag, 0);
+                ok = __all_sync(0xffffffffu, ok && !*abort_flag);
             }
-            if (lane == 0) {
+            if (elect_one()) {
                 if constexpr (C::PAIR) tc_commit_pair(done);
                 else tc_commit(done);
             }
+            __syncwarp();
         }
         // (both CTAs of a pair: no commit's arrival is left on its way)
         if (lane == 0) mbar_wait(done, 0, nullptr, p.err);
@@ -617,7 +647,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
             const int b0 = C::GU ? wk.nt : wk.nt * 2, b1 = C::GU ? b0 : min(b0 + 1, nb - 1);
             for (int i = 0; i < KB && wk.e < p.E; i += C::SEG, ++ck) {
                 const uint32_t c = ck % C::SLOTS;
-                ok = ck < C::SLOTS || mbar_wait(&c_empty[c], ((ck / C::SLOTS) & 1) ^ 1, abort_flag, p.err);
+                ok = ck < C::SLOTS || bar_wait(&c_empty[c], ((ck / C::SLOTS) & 1) ^ 1, abort_flag, p.err);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 float *dst = scales + c * C::SLOT;
@@ -657,10 +687,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
             for (int j = 0; j < 64; ++j) acc[j] = make_float2(0.0f, 0.0f);
             for (int i = 0; i < KB && wk.e < p.E; ++i, ++it) {
                 const uint32_t b = it % C::NB, c4 = ck % C::SLOTS;
-                if (i % C::SEG == 0) mbar_wait(&c_full[c4], (ck / C::SLOTS) & 1, abort_flag, p.err);
+                if (i % C::SEG == 0) bar_wait(&c_full[c4], (ck / C::SLOTS) & 1, abort_flag, p.err);
                 const float *sc = scales + c4 * C::SLOT + (i % C::SEG) * C::SROW;
                 const float sa = sc[lrow], s0 = sa * sc[128 + (C::GU ? 0 : w)], s1 = C::GU ? sa * sc[129] : s0;
-                mbar_wait(&t_full[b], (it / C::NB) & 1, abort_flag, p.err);
+                bar_wait(&t_full[b], (it / C::NB) & 1, abort_flag, p.err);
                 __syncwarp();
                 if (i % C::SEG == C::SEG - 1 || i == KB - 1) {
                     if (lane == 0) mbar_arrive(&c_empty[c4]);
