@@ -425,7 +425,7 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) small_kernel(const __gr
 //
 // Roles: warps 0 .. 7 scale and sum (group w = warp / 4 takes columns 128 w ..
 // 128 w + 127, 128 sums a thread), warp 8 loads by TMA, warp 9 issues the MMAs,
-// warp 10 brings the scales to shared memory.
+// warps 10 and 11 bring the scales to shared memory.
 // ---------------------------------------------------------------------------
 template <bool PAIR_, bool GU_>
 struct LargeCfg {
@@ -442,8 +442,8 @@ struct LargeCfg {
     static constexpr int EPI = 8;
     static constexpr int THREADS = 384;                      // three warpgroups
     // registers a thread: 168 at launch (what 384 threads can have), then shifted
-    // to the two summing warpgroups: 256 * 208 + 128 * 88 = 384 * 168
-    static constexpr int REGS = 168, REGS_SUM = 208, REGS_REST = 88;
+    // to the two summing warpgroups: 256 * 224 + 128 * 56 = 384 * 168
+    static constexpr int REGS = 168, REGS_SUM = 224, REGS_REST = 56;
     static constexpr int GROUP = 8;                          // dense: row tiles that share a W tile in turn
     // scales: slots of SEG K blocks, [K block][128 rows of a, then 2 of W's blocks]
     static constexpr int SEG = 4, SLOTS = 4, SROW = 136;
@@ -516,7 +516,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
         info[0] = 0;
         for (int i = 0; i < C::NS; ++i) { mbar_init(&s_full[i], 1); mbar_init(&s_empty[i], 1); }
         for (int i = 0; i < C::NB; ++i) { mbar_init(&t_full[i], 1); mbar_init(&t_empty[i], C::EPI * C::CTAS); }
-        for (int i = 0; i < C::SLOTS; ++i) { mbar_init(&c_full[i], 1); mbar_init(&c_empty[i], C::EPI); }
+        for (int i = 0; i < C::SLOTS; ++i) { mbar_init(&c_full[i], 2); mbar_init(&c_empty[i], C::EPI); }
         mbar_init(done, 1);
         fence_mbarrier_init();
         prefetch_tensormap(&maps.a);
@@ -637,9 +637,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
         // (both CTAs of a pair: no commit's arrival is left on its way)
         if (lane == 0) mbar_wait(done, 0, nullptr, p.err);
         __syncwarp();
-    } else if (warp == C::EPI + 2) {
+    } else if (warp >= C::EPI + 2) {
         // ---- scales: this CTA's rows of a, and the tile's blocks of W (plain: two
-        // blocks of rows; GU: gate and up), SEG K blocks at a time
+        // blocks of rows; GU: gate and up), SEG K blocks at a time, 64 rows a warp
+        const int half = (warp - C::EPI - 2) * 64;
         const int nb = (p.N + kF8Block - 1) / kF8Block;
         uint32_t ck = 0;
         bool ok = true;
@@ -653,20 +654,17 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
                 float *dst = scales + c * C::SLOT;
                 const int kb = min(i + (lane & 3), KB - 1);
                 const float *pa = p.sa + (int64_t)wk.row0 * KB + kb;
-                float f[4];
+                float f[8];
 #pragma unroll
-                for (int r0 = 0; r0 < 128; r0 += 32) {
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        f[r] = __ldg(pa + (int64_t)min(128 * rank + r0 + r * 8 + (lane >> 2), wk.rows - 1) * KB);
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) dst[(lane & 3) * C::SROW + r0 + r * 8 + (lane >> 2)] = f[r];
-                }
-                if (lane < 8) {
+                for (int r = 0; r < 8; ++r)
+                    f[r] = __ldg(pa + (int64_t)min(128 * rank + half + r * 8 + (lane >> 2), wk.rows - 1) * KB);
+                if (half == 0 && lane < 8) {
                     const float *pw = C::GU && (lane >> 2) ? p.sw1 : p.sw0;
                     dst[(lane & 3) * C::SROW + 128 + (lane >> 2)] =
                         __ldg(pw + ((int64_t)wk.e * nb + ((lane >> 2) ? b1 : b0)) * KB + kb);
                 }
+#pragma unroll
+                for (int r = 0; r < 8; ++r) dst[(lane & 3) * C::SROW + half + r * 8 + (lane >> 2)] = f[r];
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&c_full[c]);
             }
@@ -685,38 +683,45 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
             float2 acc[64];
 #pragma unroll
             for (int j = 0; j < 64; ++j) acc[j] = make_float2(0.0f, 0.0f);
+            // The last 32 columns of a K block are summed while the first of the next
+            // are on their way (d[1] and their scale go from one turn to the next).
+            uint32_t d[2][32];
+            float last = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) d[1][j] = 0;
             for (int i = 0; i < KB && wk.e < p.E; ++i, ++it) {
-                const uint32_t b = it % C::NB, c4 = ck % C::SLOTS;
+                const uint32_t b = it % C::NB, c4 = ck % C::SLOTS, from = taddr + b * 256;
                 if (i % C::SEG == 0) bar_wait(&c_full[c4], (ck / C::SLOTS) & 1, abort_flag, p.err);
                 const float *sc = scales + c4 * C::SLOT + (i % C::SEG) * C::SROW;
                 const float sa = sc[lrow], s0 = sa * sc[128 + (C::GU ? 0 : w)], s1 = C::GU ? sa * sc[129] : s0;
                 bar_wait(&t_full[b], (it / C::NB) & 1, abort_flag, p.err);
                 __syncwarp();
+                tc_fence_after();
+                tmem_ld_32x32b_x32(from, d[0]);
                 if (i % C::SEG == C::SEG - 1 || i == KB - 1) {
                     if (lane == 0) mbar_arrive(&c_empty[c4]);
                     ++ck;
                 }
-                tc_fence_after();
-                // the next 32 columns are on their way while the last are summed
-                uint32_t d[2][32];
-                tmem_ld_32x32b_x32(taddr + b * 256, d[0]);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
+                for (int j = 0; j < 16; ++j) fma2(acc[48 + j], d[1][2 * j], d[1][2 * j + 1], last);
+#pragma unroll
+                for (int c = 0; c < 3; ++c) {
                     tmem_ld_wait(d[c & 1]);
-                    if (c < 3) {
-                        tmem_ld_32x32b_x32(taddr + b * 256 + 32 * (c + 1), d[(c + 1) & 1]);
-                    } else {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) {
-                            if constexpr (C::PAIR) mbar_arrive_cluster(empty0 + b * 8);
-                            else mbar_arrive(&t_empty[b]);
-                        }
-                    }
+                    tmem_ld_32x32b_x32(from + 32 * (c + 1), d[(c + 1) & 1]);
 #pragma unroll
                     for (int j = 0; j < 16; ++j) fma2(acc[c * 16 + j], d[c & 1][2 * j], d[c & 1][2 * j + 1], c < 2 ? s0 : s1);
                 }
+                last = s1;
+                tmem_ld_wait(d[1]);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if constexpr (C::PAIR) mbar_arrive_cluster(empty0 + b * 8);
+                    else mbar_arrive(&t_empty[b]);
+                }
             }
+#pragma unroll
+            for (int j = 0; j < 16; ++j) fma2(acc[48 + j], d[1][2 * j], d[1][2 * j + 1], last);
             const int wrow = 128 * rank + q * 32;            // this warp's first row of the tile
             const int left = wk.rows - wrow;                 // and how many are the tile's
             const int64_t row = wk.row0 + wrow;
