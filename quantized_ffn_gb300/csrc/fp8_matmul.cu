@@ -48,6 +48,13 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
                  : "memory");
     return v;
 }
+// 2-D TMA tile store shared -> global, tracked by the issuing thread's bulk-async group.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, uint32_t smem_src, int c0, int c1) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(smem_src), "r"(c0), "r"(c1)
+                 : "memory");
+}
 __device__ __forceinline__ void named_barrier(int id, int threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
@@ -142,7 +149,7 @@ struct Params {
     int vec;            // y's rows take vector stores (small: 4 elements, large: 16 bytes)
 };
 struct Maps {
-    CUtensorMap a, w0, w1;
+    CUtensorMap a, w0, w1, y;   // y: the large tiles' stores
 };
 
 // ---------------------------------------------------------------------------
@@ -437,7 +444,7 @@ struct LargeCfg {
     static constexpr int W_BOX = GU ? 64 : 128;
     static constexpr int A_BYTES = 128 * 128;
     static constexpr int STAGE = A_BYTES + W_ROWS * 128;
-    static constexpr int NS = PAIR ? 6 : 4;
+    static constexpr int NS = PAIR ? 4 : 3;
     static constexpr int NB = 2;
     static constexpr int EPI = 8;
     static constexpr int THREADS = 384;                      // three warpgroups
@@ -448,12 +455,16 @@ struct LargeCfg {
     // scales: slots of SEG K blocks, [K block][128 rows of a, then 2 of W's blocks]
     static constexpr int SEG = 4, SLOTS = 4, SROW = 136;
     static constexpr int SLOT = SEG * SROW;                  // floats (a pitch of 136 spreads the K blocks over the banks)
-    static constexpr int OFF_OUT = NS * STAGE;               // 2 KB a summing warp: 32 rows x 64 bytes of the result
-    static constexpr int OFF_TOP = OFF_OUT + EPI * 2048;     // GU: largest h of (tile parity, group, row)
+    // a summing warp's 32 rows on their way out: boxes of 128 bytes a row (GU: one of
+    // 64), swizzled as the store's tensor map has it
+    static constexpr int OUT_BOX = GU ? 64 : 128;
+    static constexpr int OUT_BYTES = GU ? 2048 : 8192;
+    static constexpr int OFF_OUT = NS * STAGE;
+    static constexpr int OFF_TOP = OFF_OUT + EPI * OUT_BYTES;     // GU: largest h of (tile parity, group, row)
     static constexpr int OFF_SC = OFF_TOP + (GU ? 2 * 2 * 128 * 4 : 0);
     static constexpr int OFF_BAR = OFF_SC + SLOTS * SLOT * 4;
-    static constexpr int OFF_CUM = OFF_BAR + (2 * NS + 2 * NB + 2 * SLOTS + 1) * 8 + 24;
-    static constexpr int SMEM = OFF_CUM + 1024;              // + the row tiles before each group of rows
+    static constexpr int OFF_CUM = OFF_BAR + (2 * NS + 2 * NB + 2 * SLOTS + 1) * 8 + 24;   // (a multiple of 8)
+    static constexpr int SMEM = OFF_CUM + 1024;              // + {row tiles before, first row} of each group of rows
 };
 
 // Tile i of a cluster's walk: the group of rows, its rows, the W tile.
@@ -463,8 +474,9 @@ struct Walk {
     int t;
 
     __device__ __forceinline__ void start(int cluster) { t = cluster; e = 0; }
-    // false past the last tile.  One full warp.  cum[g]: row tiles before group g.
-    __device__ __forceinline__ bool get(const Params &p, const int *cum) {
+    // false past the last tile.  One full warp.  cum[g]: row tiles before group
+    // g and its first row; one entry past the last.
+    __device__ __forceinline__ bool get(const Params &p, const int2 *cum) {
         const int n_tiles = p.n_tiles;
         if (!p.offsets) {
             const int rt_all = p.row_tiles;
@@ -477,21 +489,19 @@ struct Walk {
             return true;
         }
         const int groups = p.E + 1;
-        if (t >= cum[groups] * n_tiles) return false;
+        if (t >= cum[groups].x * n_tiles) return false;
         const int rt = t / n_tiles, lane = threadIdx.x & 31;
         nt = t - rt * n_tiles;
         for (;; e += 32) {   // the group whose tiles hold rt: ascending from the last one
-            const unsigned past = __ballot_sync(0xffffffffu, cum[min(e + lane + 1, groups)] > rt);
+            const unsigned past = __ballot_sync(0xffffffffu, cum[min(e + lane + 1, groups)].x > rt);
             if (past) {
                 e += __ffs(past) - 1;
                 break;
             }
         }
-        const int lo = min(max(__ldg(p.offsets + e), 0), p.M);
-        const int hi = e < p.E ? min(max(__ldg(p.offsets + e + 1), 0), p.M) : p.M;
-        const int done = (rt - cum[e]) * C::TM;
-        row0 = lo + done;
-        rows = min(C::TM, hi - row0);
+        const int2 at = cum[e];
+        row0 = at.y + (rt - at.x) * C::TM;
+        rows = min(C::TM, (e < p.E ? min(max(cum[e + 1].y, at.y), p.M) : p.M) - row0);
         return true;
     }
 };
@@ -506,7 +516,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
     uint64_t *c_full = t_empty + C::NB, *c_empty = c_full + C::SLOTS, *done = c_empty + C::SLOTS;
     int *info = reinterpret_cast<int *>(done + 1);           // abort, TMEM base
     float *scales = reinterpret_cast<float *>(smem + C::OFF_SC);
-    int *cum = reinterpret_cast<int *>(smem + C::OFF_CUM);
+    int2 *cum = reinterpret_cast<int2 *>(smem + C::OFF_CUM);
     volatile int *abort_flag = info;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = C::PAIR ? (int)cluster_ctarank() : 0;
@@ -535,13 +545,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
         for (int g = threadIdx.x; g <= p.E; g += C::THREADS) {
             const int lo = min(max(__ldg(p.offsets + g), 0), p.M);
             const int hi = g < p.E ? min(max(__ldg(p.offsets + g + 1), 0), p.M) : (C::GU ? lo : p.M);
-            cum[g] = (max(hi - lo, 0) + C::TM - 1) / C::TM;
+            cum[g] = make_int2((max(hi - lo, 0) + C::TM - 1) / C::TM, lo);
         }
         __syncthreads();
         if (warp == 0) {
             const int per = (p.E + 32) / 32, g0 = min(lane * per, p.E + 1), g1 = min(g0 + per, p.E + 1);
             int n = 0;
-            for (int g = g0; g < g1; ++g) n += cum[g];
+            for (int g = g0; g < g1; ++g) n += cum[g].x;
             int inc = n;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -550,11 +560,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
             }
             int at = inc - n;
             for (int g = g0; g < g1; ++g) {
-                const int c = cum[g];
-                cum[g] = at;
+                const int c = cum[g].x;
+                cum[g].x = at;
                 at += c;
             }
-            if (lane == 31) cum[p.E + 1] = inc;
+            if (lane == 31) cum[p.E + 1] = make_int2(inc, p.M);
         }
     }
     __syncthreads();
@@ -676,7 +686,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
         const int nb = (p.N + kF8Block - 1) / kF8Block;
         const uint32_t taddr = tmem + w * 128 + ((uint32_t)(q * 32) << 16);
         const uint32_t empty0 = C::PAIR ? mapa_shared(smem_u32(t_empty), 0) : 0;
-        uint8_t *out = smem + C::OFF_OUT + warp * 2048;
+        uint8_t *out = smem + C::OFF_OUT + warp * C::OUT_BYTES;
         uint32_t it = 0, ck = 0;
         int parity = 0;
         for (; wk.get(p, cum); wk.t += gridDim.x / C::CTAS) {
@@ -726,34 +736,55 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
             const int left = wk.rows - wrow;                 // and how many are the tile's
             const int64_t row = wk.row0 + wrow;
             const int nt = wk.nt;
-            // 64 bytes of every row of the warp, by 16 per thread, through shared
-            // memory: a row's bytes are then written by neighbouring lanes (each lane
-            // storing its own row would touch 32 lines an instruction: 3.4 us a tile
-            // of 256 columns in bf16)
-            auto store = [&](uint8_t *dst, int64_t pitch, int bytes, int elem, bool vec, const uint4 (&v)[4]) {
+            // The rows leave by TMA, 32 rows of a box at a time: nothing waits for the
+            // stores, which go out at 32 bytes a clock (64 KB a tile of bf16: 2000
+            // clocks that overlap with the next tile).  A warp whose rows are not all
+            // the tile's, and rows that are not 16-byte multiples, are written from
+            // shared memory by the warp's lanes, a row's bytes by neighbouring lanes.
+            auto at = [&](int box, int r, int chunk) {
+                return out + box * 32 * C::OUT_BOX + r * C::OUT_BOX +
+                       ((C::GU ? chunk ^ ((r >> 1) & 3) : chunk ^ (r & 7)) << 4);
+            };
+            auto ready = [&] {   // the boxes sent before have been read
+                if (lane == 0) bulk_wait_group_read<0>();
                 __syncwarp();
-#pragma unroll
-                for (int c = 0; c < 4; ++c) *reinterpret_cast<uint4 *>(out + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) = v[c];
-                __syncwarp();
-                if (vec) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int r = i * 8 + (lane >> 2), c = lane & 3;
-                        if (r < left && c * 16 < bytes)
-                            *reinterpret_cast<uint4 *>(dst + r * pitch + c * 16) =
-                                *reinterpret_cast<const uint4 *>(out + r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+            };
+            // `boxes` boxes from column n0 on, elements of `elem` bytes
+            auto send = [&](int boxes, int n0, int elem, bool vec) {
+                const int per = C::OUT_BOX / elem;           // columns of a box
+                if (vec && left >= 32) {
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        for (int x = 0; x < boxes; ++x)
+                            if (n0 + x * per < p.N) tma_store_2d(&maps.y, smem_u32(out) + x * 32 * C::OUT_BOX, n0 + x * per, (int)row);
+                        bulk_commit_group();
                     }
-                } else {
-                    // rows of any alignment: element by element
-                    const int at = lane * elem & 63;
-                    for (int r = lane * elem >> 6; r < left && r < 32; r += elem >> 1) {
-                        const uint8_t *from = out + r * 64 + (((at >> 4) ^ ((r >> 1) & 3)) << 4) + (at & 15);
-                        if (at < bytes) {
-                            if (elem == 2) *reinterpret_cast<uint16_t *>(dst + r * pitch + at) = *reinterpret_cast<const uint16_t *>(from);
-                            else *reinterpret_cast<uint32_t *>(dst + r * pitch + at) = *reinterpret_cast<const uint32_t *>(from);
+                    return;
+                }
+                __syncwarp();
+                uint8_t *y = static_cast<uint8_t *>(p.y) + row * p.N * elem;
+                const int64_t pitch = (int64_t)p.N * elem;
+                constexpr int CH = C::OUT_BOX / 16;          // chunks of a row
+                for (int x = 0; x < boxes; ++x) {
+                    const int col = n0 + x * per, bytes = min(per, p.N - col) * elem;
+                    if (vec) {
+                        for (int i = lane; i < 32 * CH; i += 32)
+                            if (i / CH < left && i % CH * 16 < bytes)
+                                *reinterpret_cast<uint4 *>(y + i / CH * pitch + (int64_t)col * elem + i % CH * 16) =
+                                    *reinterpret_cast<const uint4 *>(at(x, i / CH, i % CH));
+                    } else {
+                        for (int i = lane; i < 32 * per; i += 32) {
+                            const int r = i / per, b = i % per * elem;
+                            if (r >= left || b >= bytes) continue;
+                            uint8_t *dst = y + r * pitch + (int64_t)col * elem + b;
+                            const uint8_t *src = at(x, r, b >> 4) + (b & 15);
+                            if (elem == 2) *reinterpret_cast<uint16_t *>(dst) = *reinterpret_cast<const uint16_t *>(src);
+                            else *reinterpret_cast<uint32_t *>(dst) = *reinterpret_cast<const uint32_t *>(src);
                         }
                     }
                 }
+                __syncwarp();
             };
             if constexpr (C::GU) {
                 // h of features 64 w .. 64 w + 63 of the tile; the block's largest
@@ -773,7 +804,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
                 parity ^= 1;
                 const int sp = f8_scale_exp(top);
                 const float inv = pow2f(-sp);
-                uint4 v[4];
+                ready();
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     uint32_t u[4];
@@ -782,46 +813,43 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
                         const float2 lo = acc[c * 8 + 2 * k], hi = acc[c * 8 + 2 * k + 1];
                         u[k] = f8x4_satfinite(lo.x * inv, lo.y * inv, hi.x * inv, hi.y * inv);
                     }
-                    v[c] = make_uint4(u[0], u[1], u[2], u[3]);
+                    *reinterpret_cast<uint4 *>(at(0, lane, c)) = make_uint4(u[0], u[1], u[2], u[3]);
                 }
                 // (N is a multiple of 16 and h 16-byte aligned)
-                store(static_cast<uint8_t *>(p.y) + row * p.N + n, p.N, p.N - n, 1, true, v);
+                send(1, n, 1, true);
                 if (w == 0 && lane < left) p.y_scale[(row + lane) * nb + nt] = pow2f(sp);
             } else {
                 const int n = nt * 256 + w * 128;
                 if (p.y_bf16) {
-                    uint8_t *dst = static_cast<uint8_t *>(p.y) + (row * p.N + n) * 2;
+                    ready();
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {            // 32 columns
-                        uint4 v[4];
+                    for (int c = 0; c < 16; ++c) {           // 8 columns
+                        uint32_t u[4];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            uint32_t u[4];
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const float2 f = acc[c * 16 + i * 4 + k];
-                                const __nv_bfloat162 two = __floats2bfloat162_rn(f.x, f.y);
-                                u[k] = *reinterpret_cast<const uint32_t *>(&two);
-                            }
-                            v[i] = make_uint4(u[0], u[1], u[2], u[3]);
+                        for (int k = 0; k < 4; ++k) {
+                            const float2 f = acc[c * 4 + k];
+                            const __nv_bfloat162 two = __floats2bfloat162_rn(f.x, f.y);
+                            u[k] = *reinterpret_cast<const uint32_t *>(&two);
                         }
-                        store(dst + c * 64, (int64_t)p.N * 2, (p.N - n) * 2 - c * 64, 2, p.vec, v);
+                        *reinterpret_cast<uint4 *>(at(c >> 3, lane, c & 7)) = make_uint4(u[0], u[1], u[2], u[3]);
                     }
+                    send(2, n, 2, p.vec);
                 } else {
-                    uint8_t *dst = static_cast<uint8_t *>(p.y) + (row * p.N + n) * 4;
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) {            // 16 columns
-                        uint4 v[4];
+                    for (int h = 0; h < 2; ++h) {            // 64 columns
+                        ready();
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float2 lo = acc[c * 8 + i * 2], hi = acc[c * 8 + i * 2 + 1];
-                            v[i] = make_uint4(__float_as_uint(lo.x), __float_as_uint(lo.y), __float_as_uint(hi.x), __float_as_uint(hi.y));
+                        for (int c = 0; c < 16; ++c) {
+                            const float2 lo = acc[h * 32 + c * 2], hi = acc[h * 32 + c * 2 + 1];
+                            *reinterpret_cast<float4 *>(at(c >> 3, lane, c & 7)) = make_float4(lo.x, lo.y, hi.x, hi.y);
                         }
-                        store(dst + c * 64, (int64_t)p.N * 4, (p.N - n) * 4 - c * 64, 4, p.vec, v);
+                        send(2, n + h * 64, 4, p.vec);
                     }
                 }
             }
         }
+        if (lane == 0) bulk_wait_group_all();
+        __syncwarp();
     }
     tc_fence_before();
     __syncthreads();
@@ -884,7 +912,7 @@ static int64_t row_tiles_bound(const Fp8Args &a, int tr) {
 template <class C>
 static cudaError_t launch_small(const Fp8Args &a, cudaStream_t s) {
     const DeviceInfo &di = device_info();
-    Maps maps;
+    Maps maps{};
     if (!encode(&maps.a, a.a, a.M, a.K, C::TN) || !encode(&maps.w0, a.w, (int64_t)a.E * a.N, a.K, 128) ||
         !encode(&maps.w1, C::GU ? a.w1 : a.w, (int64_t)a.E * a.N, a.K, 128))
         return cudaErrorInvalidValue;
@@ -919,7 +947,7 @@ static cudaError_t launch_small(const Fp8Args &a, cudaStream_t s) {
 template <class C>
 static cudaError_t launch_large(const Fp8Args &a, cudaStream_t s) {
     const DeviceInfo &di = device_info();
-    Maps maps;
+    Maps maps{};
     if (!encode(&maps.a, a.a, a.M, a.K, 128) || !encode(&maps.w0, a.w, (int64_t)a.E * a.N, a.K, C::W_BOX) ||
         !encode(&maps.w1, C::GU ? a.w1 : a.w, (int64_t)a.E * a.N, a.K, C::W_BOX))
         return cudaErrorInvalidValue;
@@ -931,7 +959,19 @@ static cudaError_t launch_large(const Fp8Args &a, cudaStream_t s) {
     p.vec = a.N % (p.y_bf16 ? 8 : 4) == 0 && (reinterpret_cast<uintptr_t>(a.y) & 15) == 0;
     int64_t clusters = di.num_sms / C::CTAS;
     if (tiles < clusters) clusters = tiles;
-    const size_t smem = C::SMEM + (a.offsets ? ((size_t)a.E + 2) * 4 : 0);
+    if (C::GU || p.vec) {
+        const int elem = C::GU ? 1 : p.y_bf16 ? 2 : 4;
+        const cuuint64_t dims[2] = {(cuuint64_t)a.N, (cuuint64_t)a.M};
+        const cuuint64_t strides[1] = {(cuuint64_t)a.N * elem};
+        const cuuint32_t box[2] = {(cuuint32_t)(C::OUT_BOX / elem), 32};
+        const cuuint32_t estr[2] = {1, 1};
+        if (encode_fn()(&maps.y, elem == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : elem == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+                        2, a.y, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        C::GU ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return cudaErrorInvalidValue;
+    }
+    const size_t smem = C::SMEM + (a.offsets ? ((size_t)a.E + 2) * 8 : 0);
     // the registers' shift adds up only for the count that the kernel is launched with
     static const int regs = [] {
         cudaFuncAttributes f{};
@@ -963,7 +1003,7 @@ static cudaError_t launch(const Fp8Args &a, cudaStream_t s) {
     // many rows: the large tiles, where they fill the SMs at least twice over (a
     // dense call with fewer splits K instead)
     const int64_t per = (a.N + LargeCfg<false, GU>::TNW - 1) / LargeCfg<false, GU>::TNW;
-    const bool fits = LargeCfg<false, GU>::SMEM + (a.E + 2) * 4 <= device_info().max_smem_optin;   // (E <= 4046)
+    const bool fits = LargeCfg<false, GU>::SMEM + (a.E + 2) * 8 <= device_info().max_smem_optin;   // (E up to about 400)
     if (a.offsets ? fits && a.M / a.E > 64 : a.M > 64 && (a.M + 127) / 128 * per >= 76) {
         if (!a.offsets && a.M >= 256) return launch_large<LargeCfg<true, GU>>(a, s);
         return launch_large<LargeCfg<false, GU>>(a, s);
