@@ -105,9 +105,18 @@ def _check(status: int, what: str):
         raise ZffnError(status, what)
 
 
-def _stream(stream: Optional[torch.cuda.Stream]) -> ctypes.c_void_p:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
+def _stream(stream: Optional[torch.cuda.Stream]) -> int:
+    """The handle of `stream`, or of the current device's current stream (asked without making a
+    Stream object: a small call is bound by what the host does)."""
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is None or not torch.cuda.is_initialized():
+        return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(_device())
 
 
 def _cuda(t: torch.Tensor, name: str, dtype=None):
@@ -306,6 +315,7 @@ def moe_router_topk(logits: torch.Tensor, top_k: int, expert_ids: Optional[torch
 
 DT_F32, DT_BF16 = 0, 1
 _DTYPES = {torch.float32: DT_F32, torch.bfloat16: DT_BF16}
+_F32, _I32, _F8, _U8 = torch.float32, torch.int32, torch.float8_e4m3fn, torch.uint8
 
 
 def _dtype(t: torch.Tensor, name: str) -> int:
@@ -315,56 +325,57 @@ def _dtype(t: torch.Tensor, name: str) -> int:
     return d
 
 
-def _f8(t: torch.Tensor, name: str):
-    return _cuda(t, name, torch.uint8 if t.dtype == torch.uint8 else torch.float8_e4m3fn)
-
-
-def _shaped(t: torch.Tensor, name: str, dtype, shape):
+def _ptr(t: torch.Tensor, name: str, dtype, shape) -> int:
+    """Address of a contiguous CUDA tensor of this type and shape."""
+    if t.dtype is dtype and t.is_cuda and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    return _cuda(t, name, dtype)
+    return _cuda(t, name, dtype).value
 
 
-def _blocks(n: int) -> int:
-    return -(-n // 128)
+def _ptr8(t: torch.Tensor, name: str, shape) -> int:
+    return _ptr(t, name, _U8 if t.dtype is _U8 else _F8, shape)
+
+
+def _fail(status: int, what: str):
+    raise ZffnError(status, what)
 
 
 def fp8_quantize(x: torch.Tensor, block_rows: int = 1, q: Optional[torch.Tensor] = None,
                  scale: Optional[torch.Tensor] = None, stream=None):
     """(q float8_e4m3fn [R, C], scale fp32 [ceil(R / block_rows), ceil(C / 128)]) of x (bf16 or
     fp32 [R, C]): power-of-two scales for blocks of block_rows (1 or 128) x 128."""
-    R, C = x.shape
-    if q is None:
-        q = torch.empty((R, C), dtype=torch.float8_e4m3fn, device=x.device)
-    if block_rows not in (1, 128):
+    shape = R, C = x.shape
+    if block_rows != 1 and block_rows != 128:
         raise ValueError("block_rows must be 1 or 128")
-    shape = (-(-R // block_rows), _blocks(C))
+    blocks = (-(-R // block_rows), -(-C // 128))
+    if q is None:
+        q = torch.empty(shape, dtype=_F8, device=x.device)
     if scale is None:
-        scale = torch.empty(shape, dtype=torch.float32, device=x.device)
-    if q.shape != x.shape:
-        raise ValueError(f"q must have shape {tuple(x.shape)}, got {tuple(q.shape)}")
-    _check(load().zffn_fp8_quantize(_dtype(x, "x"), _cuda(x, "x"), _f8(q, "q"),
-                                    _shaped(scale, "scale", torch.float32, shape), R, C, block_rows,
-                                    _stream(stream)), "zffn_fp8_quantize")
+        scale = torch.empty(blocks, dtype=_F32, device=x.device)
+    st = (_lib or load()).zffn_fp8_quantize(
+        _dtype(x, "x"), _ptr(x, "x", x.dtype, shape), _ptr8(q, "q", shape), _ptr(scale, "scale", _F32, blocks),
+        R, C, block_rows, _stream(stream))
+    if st:
+        _fail(st, "zffn_fp8_quantize")
     return q, scale
 
 
 def fp8_dequant(q: torch.Tensor, scale: torch.Tensor, block_rows: int = 1,
                 out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """fp32 [R, C]: each e4m3 value times its block's scale."""
-    R, C = q.shape
-    if block_rows not in (1, 128):
+    shape = R, C = q.shape
+    if block_rows != 1 and block_rows != 128:
         raise ValueError("block_rows must be 1 or 128")
     if out is None:
-        out = torch.empty((R, C), dtype=torch.float32, device=q.device)
-    _check(load().zffn_fp8_dequant(
-        _f8(q, "q"), _shaped(scale, "scale", torch.float32, (-(-R // block_rows), _blocks(C))),
-        _shaped(out, "out", torch.float32, (R, C)), R, C, block_rows, _stream(stream)), "zffn_fp8_dequant")
+        out = torch.empty(shape, dtype=_F32, device=q.device)
+    st = (_lib or load()).zffn_fp8_dequant(
+        _ptr8(q, "q", shape), _ptr(scale, "scale", _F32, (-(-R // block_rows), -(-C // 128))),
+        _ptr(out, "out", _F32, shape), R, C, block_rows, _stream(stream))
+    if st:
+        _fail(st, "zffn_fp8_dequant")
     return out
-
-
-def _offsets(offsets: Optional[torch.Tensor], E: int):
-    return None if offsets is None else _shaped(offsets, "offsets", torch.int32, (E + 1,))
 
 
 def fp8_matmul(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
@@ -375,17 +386,21 @@ def fp8_matmul(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale:
     MoePlan.offsets) w is [E, N, K] and rows offsets[e]:offsets[e + 1] take expert e; rows of no
     expert become 0.  y: given (fp32 or bf16), or made with `dtype`."""
     M, K = a.shape
-    E = 1 if offsets is None else w.shape[0]
     N = w.shape[-2]
-    lead = () if offsets is None else (E,)
+    bn, bk = -(-N // 128), -(-K // 128)
+    if offsets is None:
+        E, po, ws, ss = 1, None, (N, K), (bn, bk)
+    else:
+        E = w.shape[0]
+        po, ws, ss = _ptr(offsets, "offsets", _I32, (E + 1,)), (E, N, K), (E, bn, bk)
     if y is None:
         y = torch.empty((M, N), dtype=dtype, device=a.device)
-    if tuple(w.shape) != (*lead, N, K):
-        raise ValueError(f"w must have shape {(*lead, 'N', K)}, got {tuple(w.shape)}")
-    _check(load().zffn_fp8_matmul(
-        _f8(a, "a"), _shaped(a_scale, "a_scale", torch.float32, (M, _blocks(K))), _f8(w, "w"),
-        _shaped(w_scale, "w_scale", torch.float32, (*lead, _blocks(N), _blocks(K))), _offsets(offsets, E),
-        _dtype(y, "y"), _shaped(y, "y", y.dtype, (M, N)), M, N, K, E, _stream(stream)), "zffn_fp8_matmul")
+    st = (_lib or load()).zffn_fp8_matmul(
+        _ptr8(a, "a", (M, K)), _ptr(a_scale, "a_scale", _F32, (M, bk)), _ptr8(w, "w", ws),
+        _ptr(w_scale, "w_scale", _F32, ss), po, _dtype(y, "y"), _ptr(y, "y", y.dtype, (M, N)), M, N, K, E,
+        _stream(stream))
+    if st:
+        _fail(st, "zffn_fp8_matmul")
     return y
 
 
@@ -396,20 +411,22 @@ def fp8_experts(a: torch.Tensor, a_scale: torch.Tensor, Wg: torch.Tensor, sg: to
     with scales for blocks of 128; with offsets the weights are stacked [E, ...] and the rows of
     each expert take its own (rows of no expert become 0)."""
     P, H = a.shape
-    E = 1 if offsets is None else Wg.shape[0]
     I = Wg.shape[-2]
-    lead = () if offsets is None else (E,)
+    bi, bh = -(-I // 128), -(-H // 128)
+    if offsets is None:
+        E, po, up, down, s_up, s_down = 1, None, (I, H), (H, I), (bi, bh), (bh, bi)
+    else:
+        E = Wg.shape[0]
+        po = _ptr(offsets, "offsets", _I32, (E + 1,))
+        up, down, s_up, s_down = (E, I, H), (E, H, I), (E, bi, bh), (E, bh, bi)
     if y is None:
         y = torch.empty((P, H), dtype=dtype, device=a.device)
-    for t, name, shape in ((Wg, "Wg", (I, H)), (Wu, "Wu", (I, H)), (Wd, "Wd", (H, I))):
-        if tuple(t.shape) != (*lead, *shape):
-            raise ValueError(f"{name} must have shape {(*lead, *shape)}, got {tuple(t.shape)}")
-    f32, bi, bh = torch.float32, _blocks(I), _blocks(H)
-    _check(load().zffn_fp8_experts(
-        _f8(a, "a"), _shaped(a_scale, "a_scale", f32, (P, bh)), _offsets(offsets, E), _f8(Wg, "Wg"),
-        _shaped(sg, "sg", f32, (*lead, bi, bh)), _f8(Wu, "Wu"), _shaped(su, "su", f32, (*lead, bi, bh)),
-        _f8(Wd, "Wd"), _shaped(sd, "sd", f32, (*lead, bh, bi)), _dtype(y, "y"), _shaped(y, "y", y.dtype, (P, H)),
-        P, H, I, E, _stream(stream)), "zffn_fp8_experts")
+    st = (_lib or load()).zffn_fp8_experts(
+        _ptr8(a, "a", (P, H)), _ptr(a_scale, "a_scale", _F32, (P, bh)), po, _ptr8(Wg, "Wg", up),
+        _ptr(sg, "sg", _F32, s_up), _ptr8(Wu, "Wu", up), _ptr(su, "su", _F32, s_up), _ptr8(Wd, "Wd", down),
+        _ptr(sd, "sd", _F32, s_down), _dtype(y, "y"), _ptr(y, "y", y.dtype, (P, H)), P, H, I, E, _stream(stream))
+    if st:
+        _fail(st, "zffn_fp8_experts")
     return y
 
 
@@ -425,16 +442,15 @@ class MoePlan(NamedTuple):
 def moe_sort(expert_ids: torch.Tensor, E: int, plan: Optional[MoePlan] = None, stream=None) -> MoePlan:
     """The stable sort of expert_ids (int32 [T, top_k], e.g. from moe_router_topk) by expert; ids
     outside [0, E) get no row."""
-    T, k = expert_ids.shape
+    shape = T, k = expert_ids.shape
+    pi = _ptr(expert_ids, "expert_ids", _I32, shape)
     if plan is None:
-        dev = expert_ids.device
-        plan = MoePlan(torch.empty((T * k,), dtype=torch.int32, device=dev),
-                       torch.empty((T, k), dtype=torch.int32, device=dev),
-                       torch.empty((E + 1,), dtype=torch.int32, device=dev))
-    _check(load().zffn_moe_sort(
-        _cuda(expert_ids, "expert_ids", torch.int32), _shaped(plan.row_slot, "row_slot", torch.int32, (T * k,)),
-        _shaped(plan.slot_row, "slot_row", torch.int32, (T, k)),
-        _shaped(plan.offsets, "offsets", torch.int32, (E + 1,)), T, E, k, _stream(stream)), "zffn_moe_sort")
+        plan = MoePlan(expert_ids.new_empty(T * k), expert_ids.new_empty(shape), expert_ids.new_empty(E + 1))
+    st = (_lib or load()).zffn_moe_sort(
+        pi, _ptr(plan[0], "row_slot", _I32, (T * k,)), _ptr(plan[1], "slot_row", _I32, shape),
+        _ptr(plan[2], "offsets", _I32, (E + 1,)), T, E, k, _stream(stream))
+    if st:
+        _fail(st, "zffn_moe_sort")
     return plan
 
 
@@ -443,21 +459,22 @@ def moe_dispatch(x: torch.Tensor, plan: MoePlan, scale: Optional[torch.Tensor] =
     """xs[T * top_k, H]: every token's row of x (any type) at its sorted places, 0 in rows of no
     pair.  With scale (fp32 [T, C], the scales of 8-bit rows) returns (xs, scales moved alike)."""
     T, H = x.shape
-    k = plan.slot_row.shape[1]
+    slot_row = plan[1]
+    k = slot_row.shape[1]
     P = T * k
     if out is None:
         out = torch.empty((P, H), dtype=x.dtype, device=x.device)
-    C = 0
+    C, ps, pso = 0, None, None
     if scale is not None:
         C = scale.shape[1]
         if scale_out is None:
-            scale_out = torch.empty((P, C), dtype=torch.float32, device=x.device)
-    _check(load().zffn_moe_dispatch(
-        _cuda(x, "x"), H * x.element_size(), None if scale is None else _shaped(scale, "scale", torch.float32, (T, C)),
-        C, _shaped(plan.row_slot, "row_slot", torch.int32, (P,)), _shaped(plan.slot_row, "slot_row", torch.int32, (T, k)),
-        _shaped(out, "out", x.dtype, (P, H)),
-        None if scale is None else _shaped(scale_out, "scale_out", torch.float32, (P, C)), T, k,
-        _stream(stream)), "zffn_moe_dispatch")
+            scale_out = torch.empty((P, C), dtype=_F32, device=x.device)
+        ps, pso = _ptr(scale, "scale", _F32, (T, C)), _ptr(scale_out, "scale_out", _F32, (P, C))
+    st = (_lib or load()).zffn_moe_dispatch(
+        _ptr(x, "x", x.dtype, (T, H)), H * x.element_size(), ps, C, _ptr(plan[0], "row_slot", _I32, (P,)),
+        _ptr(slot_row, "slot_row", _I32, (T, k)), _ptr(out, "out", x.dtype, (P, H)), pso, T, k, _stream(stream))
+    if st:
+        _fail(st, "zffn_moe_dispatch")
     return out if scale is None else (out, scale_out)
 
 
@@ -465,17 +482,19 @@ def moe_combine(rows: torch.Tensor, plan: MoePlan, weights: Optional[torch.Tenso
                 y: Optional[torch.Tensor] = None, accumulate: bool = False, stream=None) -> torch.Tensor:
     """y[T, H] fp32 (+)= sum_j weights[t, j] rows[row of (t, j)] (rows bf16 or fp32 [T * top_k, H];
     weights fp32 [T, top_k], or None for ones: the gradient of moe_dispatch)."""
-    T, k = plan.slot_row.shape
+    slot_row = plan[1]
+    T, k = slot_row.shape
     H = rows.shape[1]
     if y is None:
         if accumulate:
             raise ValueError("accumulate=True needs y")
-        y = torch.empty((T, H), dtype=torch.float32, device=rows.device)
-    _check(load().zffn_moe_combine(
-        _dtype(rows, "rows"), _shaped(rows, "rows", rows.dtype, (T * k, H)),
-        _cuda(plan.slot_row, "slot_row", torch.int32),
-        None if weights is None else _shaped(weights, "weights", torch.float32, (T, k)),
-        _shaped(y, "y", torch.float32, (T, H)), T, H, k, int(bool(accumulate)), _stream(stream)), "zffn_moe_combine")
+        y = torch.empty((T, H), dtype=_F32, device=rows.device)
+    st = (_lib or load()).zffn_moe_combine(
+        _dtype(rows, "rows"), _ptr(rows, "rows", rows.dtype, (T * k, H)), _ptr(slot_row, "slot_row", _I32, (T, k)),
+        None if weights is None else _ptr(weights, "weights", _F32, (T, k)), _ptr(y, "y", _F32, (T, H)), T, H, k,
+        1 if accumulate else 0, _stream(stream))
+    if st:
+        _fail(st, "zffn_moe_combine")
     return y
 
 
@@ -483,17 +502,20 @@ def moe_combine_grad(dy: torch.Tensor, rows: torch.Tensor, plan: MoePlan, weight
                      drows: Optional[torch.Tensor] = None, dweights: Optional[torch.Tensor] = None, stream=None):
     """(drows [T * top_k, H] of rows' type, dweights fp32 [T, top_k]): the gradients of
     moe_combine(rows, plan, weights) for dy fp32 [T, H]; drows is 0 in rows of no pair."""
-    T, k = plan.slot_row.shape
+    slot_row = plan[1]
+    T, k = slot_row.shape
     H = rows.shape[1]
     if drows is None:
         drows = torch.empty_like(rows)
     if dweights is None:
-        dweights = torch.empty((T, k), dtype=torch.float32, device=rows.device)
-    _check(load().zffn_moe_combine_grad(
-        _dtype(rows, "rows"), _shaped(dy, "dy", torch.float32, (T, H)), _shaped(rows, "rows", rows.dtype, (T * k, H)),
-        _shaped(plan.row_slot, "row_slot", torch.int32, (T * k,)), _cuda(plan.slot_row, "slot_row", torch.int32),
-        _shaped(weights, "weights", torch.float32, (T, k)), _shaped(drows, "drows", rows.dtype, (T * k, H)),
-        _shaped(dweights, "dweights", torch.float32, (T, k)), T, H, k, _stream(stream)), "zffn_moe_combine_grad")
+        dweights = torch.empty((T, k), dtype=_F32, device=rows.device)
+    st = (_lib or load()).zffn_moe_combine_grad(
+        _dtype(rows, "rows"), _ptr(dy, "dy", _F32, (T, H)), _ptr(rows, "rows", rows.dtype, (T * k, H)),
+        _ptr(plan[0], "row_slot", _I32, (T * k,)), _ptr(slot_row, "slot_row", _I32, (T, k)),
+        _ptr(weights, "weights", _F32, (T, k)), _ptr(drows, "drows", rows.dtype, (T * k, H)),
+        _ptr(dweights, "dweights", _F32, (T, k)), T, H, k, _stream(stream))
+    if st:
+        _fail(st, "zffn_moe_combine_grad")
     return drows, dweights
 
 
@@ -508,16 +530,16 @@ def moe_swiglu_fp8(x: torch.Tensor, expert_ids: torch.Tensor, expert_weights: to
     if y is None:
         if accumulate:
             raise ValueError("accumulate=True needs y")
-        y = torch.empty((T, H), dtype=torch.float32, device=x.device)
-    for t, name, shape in ((Wg, "Wg", (E, I, H)), (Wu, "Wu", (E, I, H)), (Wd, "Wd", (E, H, I))):
-        if tuple(t.shape) != shape:
-            raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    f32, bi, bh = torch.float32, _blocks(I), _blocks(H)
-    _check(load().zffn_moe_swiglu_fp8(
-        _cuda(x, "x", torch.bfloat16), _shaped(expert_ids, "expert_ids", torch.int32, (T, k)),
-        _shaped(expert_weights, "expert_weights", f32, (T, k)), _f8(Wg, "Wg"), _shaped(sg, "sg", f32, (E, bi, bh)),
-        _f8(Wu, "Wu"), _shaped(su, "su", f32, (E, bi, bh)), _f8(Wd, "Wd"), _shaped(sd, "sd", f32, (E, bh, bi)),
-        _shaped(y, "y", f32, (T, H)), T, H, I, E, k, int(bool(accumulate)), _stream(stream)), "zffn_moe_swiglu_fp8")
+        y = torch.empty((T, H), dtype=_F32, device=x.device)
+    bi, bh = -(-I // 128), -(-H // 128)
+    st = (_lib or load()).zffn_moe_swiglu_fp8(
+        _ptr(x, "x", torch.bfloat16, (T, H)), _ptr(expert_ids, "expert_ids", _I32, (T, k)),
+        _ptr(expert_weights, "expert_weights", _F32, (T, k)), _ptr8(Wg, "Wg", (E, I, H)), _ptr(sg, "sg", _F32, (E, bi, bh)),
+        _ptr8(Wu, "Wu", (E, I, H)), _ptr(su, "su", _F32, (E, bi, bh)), _ptr8(Wd, "Wd", (E, H, I)),
+        _ptr(sd, "sd", _F32, (E, bh, bi)), _ptr(y, "y", _F32, (T, H)), T, H, I, E, k, 1 if accumulate else 0,
+        _stream(stream))
+    if st:
+        _fail(st, "zffn_moe_swiglu_fp8")
     return y
 
 
