@@ -39,51 +39,64 @@ __device__ __forceinline__ void load8(const float *p, float (&v)[8]) {
 
 constexpr int kQuantThreads = 256;
 
-// 1 x 128 blocks: 16 lanes per block, 8 columns per lane.  VEC: 16-byte loads
-// and 8-byte stores (rows of 16-byte multiples from 16-byte aligned pointers);
-// otherwise element by element.  Bound by HBM.
-template <typename T, bool VEC>
+// 1 x 128 blocks: 16 lanes per block, 8 columns per lane, UNITS blocks a thread
+// with all of their loads in flight.  VEC: 16-byte loads and 8-byte stores (rows
+// of 16-byte multiples from 16-byte aligned pointers); otherwise element by
+// element.  WHOLE: the columns are a multiple of 128, so that blocks follow each
+// other in memory (no division by the row's blocks).  Bound by HBM.
+template <typename T, bool VEC, bool WHOLE, int UNITS>
 __global__ void __launch_bounds__(kQuantThreads)
     fp8_quantize_rows_kernel(const T *__restrict__ x, uint8_t *__restrict__ q, float *__restrict__ scale,
-                             int64_t rows, int cols, int nb) {
+                             int64_t units, int cols, int nb) {
+    constexpr int kPer = kQuantThreads / 16;
     const int sub = threadIdx.x & 15;
-    const int64_t unit = (int64_t)blockIdx.x * (kQuantThreads / 16) + (threadIdx.x >> 4);
-    const int64_t row = unit / nb;
-    const int b = (int)(unit - row * nb);
-    const bool live = row < rows;
-    const int c0 = b * kF8Block + sub * 8;
-    const T *px = x + (live ? row : 0) * cols;
-    float v[8];
+    const int64_t u0 = (int64_t)blockIdx.x * (kPer * UNITS) + (threadIdx.x >> 4);
+    float v[UNITS][8];
+    int64_t at[UNITS];    // element of the thread's first column
+    int left[UNITS];      // columns of the row from there on
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-    if (live) {
+    for (int k = 0; k < UNITS; ++k) {
+        const int64_t u = u0 + k * kPer;
+        if (WHOLE) {
+            at[k] = u * kF8Block + sub * 8;
+            left[k] = u < units ? 8 : 0;
+        } else {
+            const int64_t row = u < 0x7fffffff ? (int64_t)((uint32_t)u / (uint32_t)nb) : u / nb;
+            const int c0 = (int)(u - row * nb) * kF8Block + sub * 8;
+            at[k] = row * cols + c0;
+            left[k] = u < units ? cols - c0 : 0;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[k][i] = 0.0f;
         if (VEC) {
-            if (c0 < cols) load8(px + c0, v);
+            if (left[k] > 0) load8(x + at[k], v[k]);
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                if (c0 + i < cols) v[i] = to_f32(px[c0 + i]);
+                if (i < left[k]) v[k][i] = to_f32(x[at[k] + i]);
         }
     }
-    float top = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = fmaxf(top, finite_abs(v[i]));
+    for (int k = 0; k < UNITS; ++k) {
+        float top = 0.0f;
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (!live) return;
-    const int p = f8_scale_exp(top);
-    const float inv = pow2f(-p);
-    const uint32_t lo = f8x4_satfinite(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
-    const uint32_t hi = f8x4_satfinite(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv);
-    uint8_t *pq = q + row * cols;
-    if (VEC) {
-        if (c0 < cols) *reinterpret_cast<uint2 *>(pq + c0) = make_uint2(lo, hi);
-    } else {
+        for (int i = 0; i < 8; ++i) top = fmaxf(top, finite_abs(v[k][i]));
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (c0 + i < cols) pq[c0 + i] = (uint8_t)((i < 4 ? lo : hi) >> (8 * (i & 3)));
+        for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const int p = f8_scale_exp(top);
+        const float inv = pow2f(-p);
+        const uint32_t lo = f8x4_satfinite(v[k][0] * inv, v[k][1] * inv, v[k][2] * inv, v[k][3] * inv);
+        const uint32_t hi = f8x4_satfinite(v[k][4] * inv, v[k][5] * inv, v[k][6] * inv, v[k][7] * inv);
+        if (VEC) {
+            if (left[k] > 0) *reinterpret_cast<uint2 *>(q + at[k]) = make_uint2(lo, hi);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < left[k]) q[at[k] + i] = (uint8_t)((i < 4 ? lo : hi) >> (8 * (i & 3)));
+        }
+        const int64_t u = u0 + k * kPer;
+        if (sub == 0 && u < units) scale[u] = pow2f(p);
     }
-    if (sub == 0) scale[row * nb + b] = pow2f(p);
 }
 
 // 128 x 128 blocks: one thread block each; two passes over the block (the
@@ -145,14 +158,16 @@ cudaError_t quantize(const T *x, uint8_t *q, float *scale, int64_t rows, int64_t
         fp8_quantize_tiles_kernel<T><<<(unsigned)tiles, kQuantThreads, 0, s>>>(x, q, scale, rows, (int)cols, (int)nb);
         return cudaGetLastError();
     }
-    const int64_t units = rows * nb, per = kQuantThreads / 16;
-    const int64_t grid = (units + per - 1) / per;
-    if (grid > 0x7fffffff) return cudaErrorInvalidValue;
+    const int64_t units = rows * nb;
     const bool vec = ((reinterpret_cast<uintptr_t>(x) & 15) | (reinterpret_cast<uintptr_t>(q) & 7)) == 0 && cols % 8 == 0;
-    if (vec)
-        fp8_quantize_rows_kernel<T, true><<<(unsigned)grid, kQuantThreads, 0, s>>>(x, q, scale, rows, (int)cols, (int)nb);
-    else
-        fp8_quantize_rows_kernel<T, false><<<(unsigned)grid, kQuantThreads, 0, s>>>(x, q, scale, rows, (int)cols, (int)nb);
+    // few blocks: one a thread, so that more SMs take part
+    const bool few = units < (int64_t)(kQuantThreads / 16) * 4 * 1024;
+    const int64_t per = kQuantThreads / 16 * (few ? 1 : 4), grid = (units + per - 1) / per;
+    if (grid > 0x7fffffff) return cudaErrorInvalidValue;
+    auto run = [&](auto kernel) { kernel<<<(unsigned)grid, kQuantThreads, 0, s>>>(x, q, scale, units, (int)cols, (int)nb); };
+    if (vec && cols % kF8Block == 0) few ? run(fp8_quantize_rows_kernel<T, true, true, 1>) : run(fp8_quantize_rows_kernel<T, true, true, 4>);
+    else if (vec) few ? run(fp8_quantize_rows_kernel<T, true, false, 1>) : run(fp8_quantize_rows_kernel<T, true, false, 4>);
+    else few ? run(fp8_quantize_rows_kernel<T, false, false, 1>) : run(fp8_quantize_rows_kernel<T, false, false, 4>);
     return cudaGetLastError();
 }
 

@@ -2,6 +2,8 @@
 // sorted places and the weighted sum back, and the gradients of both.
 #include "moe_sort.h"
 
+#include <atomic>
+
 #include "zffn_internal.cuh"
 
 namespace zffn {
@@ -17,8 +19,9 @@ namespace {
 // launch: a cluster of CTAs shares the warps' totals through distributed
 // shared memory.  Latency bound (16 bytes a pair move).
 // ---------------------------------------------------------------------------
-constexpr int kSortMaxWarps = 32;
-constexpr int kSortCluster = 8;
+constexpr int kSortMaxWarps = 32;      // of one CTA alone; 16 of a cluster's (a turn of 32 pairs costs a
+constexpr int kSortClusterWarps = 16;  // warp about 0.6 us, so 32768 pairs take 6.8 us on 16 x 16 warps,
+constexpr int kSortCluster = 16;       // 9.8 us on 8 x 32 and 12.7 us there with the count by matches)
 
 __device__ __forceinline__ int ld_cluster_s32(uint32_t addr) {
     int v;
@@ -28,6 +31,8 @@ __device__ __forceinline__ int ld_cluster_s32(uint32_t addr) {
 
 // Shared memory: hist [warps][E], total [E] (this CTA's pairs of each expert),
 // base [E], 33 words of scan scratch.
+constexpr int kSortKeys = 8;   // turns of a warp whose keys stay in registers from the count to the placing
+
 template <int CS>
 __global__ void __launch_bounds__(kSortMaxWarps * 32)
     moe_sort_kernel(const int32_t *__restrict__ ids, int32_t *__restrict__ row_slot, int32_t *__restrict__ slot_row,
@@ -36,59 +41,67 @@ __global__ void __launch_bounds__(kSortMaxWarps * 32)
     const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int *hist = sm, *total = sm + warps * E, *base = total + E, *scratch = base + E;
     const int rank = CS > 1 ? (int)cluster_ctarank() : 0;
-    for (int i = threadIdx.x; i < warps * E; i += blockDim.x) hist[i] = 0;
-    __syncthreads();
     // this warp's run of pairs, a multiple of 32 long
     const int64_t all = (int64_t)CS * warps;
     const int64_t run = ((P + all - 1) / all + 31) / 32 * 32;
     const int64_t lo = ((int64_t)rank * warps + warp) * run;
     const int64_t hi = lo + run < P ? lo + run : P;
+    auto load_key = [&](int64_t i) {
+        const int e = i < hi ? __ldg(ids + i) : -1;
+        return e < 0 || e >= E ? -1 : e;
+    };
+    int key[kSortKeys];
+#pragma unroll
+    for (int k = 0; k < kSortKeys; ++k) key[k] = load_key(lo + 32 * k + lane);
+    for (int i = threadIdx.x; i < warps * E; i += blockDim.x) hist[i] = 0;
+    __syncthreads();
     int *mine = hist + warp * E;
-    for (int64_t i = lo; i < hi; i += 32) {
-        int e = i + lane < hi ? __ldg(ids + i + lane) : -1;
-        if (e < 0 || e >= E) e = -1;
-        const unsigned same = __match_any_sync(0xffffffffu, e);
-        if (e >= 0 && lane == __ffs(same) - 1) mine[e] += __popc(same);
-        __syncwarp();
-    }
+    auto count = [&](int e) {   // (a sum: the order of the additions does not show)
+        if (e >= 0) atomicAdd(&mine[e], 1);
+    };
+#pragma unroll
+    for (int k = 0; k < kSortKeys; ++k)
+        if (lo + 32 * k < hi) count(key[k]);
+    for (int64_t i = lo + 32 * kSortKeys; i < hi; i += 32) count(load_key(i + lane));
     __syncthreads();
     // each expert: exclusive sums over this CTA's warps, and the CTA's total
     for (int e = threadIdx.x; e < E; e += blockDim.x) {
-        int n = 0;
-        for (int w = 0; w < warps; ++w) {
-            const int c = hist[w * E + e];
-            hist[w * E + e] = n;
-            n += c;
+        int c[kSortMaxWarps], n = 0;
+#pragma unroll
+        for (int w = 0; w < kSortMaxWarps; ++w) c[w] = w < warps ? hist[w * E + e] : 0;
+#pragma unroll
+        for (int w = 0; w < kSortMaxWarps; ++w) {
+            if (w < warps) hist[w * E + e] = n;
+            n += c[w];
         }
         total[e] = n;
     }
     if (CS > 1) cluster_sync_all();
     else __syncthreads();
     // over the cluster: the expert's pairs in all CTAs (base, scanned below) and
-    // in the CTAs before this one (kept in total)
+    // in the CTAs before this one
     const uint32_t t_addr = smem_u32(total);
-    for (int e = threadIdx.x; e < E; e += blockDim.x) {
-        int n = 0, before = 0;
-        if (CS > 1) {
-#pragma unroll
-            for (int r = 0; r < CS; ++r) {
-                const int c = ld_cluster_s32(mapa_shared(t_addr + 4 * e, r));
-                if (r < rank) before += c;
-                n += c;
-            }
-        } else {
-            n = total[e];
-        }
-        base[e] = n;
-        // (the other CTAs still read total: what comes before is put into hist)
-        for (int w = 0; CS > 1 && w < warps; ++w) hist[w * E + e] += before;
-    }
-    __syncthreads();
-    // exclusive scan of base over the experts: contiguous shares, warp scans
-    const int per = (E + blockDim.x - 1) / blockDim.x;
+    const int per = (E + blockDim.x - 1) / blockDim.x;   // experts of a thread, consecutive
     const int e0 = threadIdx.x * per, e1 = min(E, e0 + per);
     int sum = 0;
-    for (int e = e0; e < e1; ++e) sum += base[e];
+    for (int e = e0; e < e1; ++e) {
+        int n = total[e];
+        if (CS > 1) {
+            int c[CS], before = 0;
+#pragma unroll
+            for (int r = 0; r < CS; ++r) c[r] = ld_cluster_s32(mapa_shared(t_addr + 4 * e, r));
+            n = 0;
+#pragma unroll
+            for (int r = 0; r < CS; ++r) {
+                if (r < rank) before += c[r];
+                n += c[r];
+            }
+            base[e] = before;
+        }
+        sum += n;
+        // (total is still read by other CTAs: n is summed up again below)
+    }
+    // exclusive scan over the threads' shares
     int inc = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -111,42 +124,52 @@ __global__ void __launch_bounds__(kSortMaxWarps * 32)
     __syncthreads();
     int at = scratch[warp] + inc - sum;
     for (int e = e0; e < e1; ++e) {
-        const int c = base[e];
-        base[e] = at;
+        int n = per == 1 ? sum : total[e];
+        if (CS > 1 && per > 1) {
+            n = 0;
+#pragma unroll
+            for (int r = 0; r < CS; ++r) n += ld_cluster_s32(mapa_shared(t_addr + 4 * e, r));
+        }
+        base[e] = at + (CS > 1 ? base[e] : 0);   // this CTA's first row of the expert
         if (rank == 0) offsets[e] = at;
-        at += c;
+        at += n;
     }
+    // the other CTAs' totals have been read: this is waited for before leaving
+    if (CS > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     const int used = scratch[32];
     if (rank == 0 && threadIdx.x == 0) offsets[E] = used;
     __syncthreads();
-    for (int64_t i = lo; i < hi; i += 32) {
-        const bool in = i + lane < hi;
-        int e = in ? __ldg(ids + i + lane) : -1;
-        if (e < 0 || e >= E) e = -1;
+    auto place = [&](int64_t i, int e) {
         const unsigned same = __match_any_sync(0xffffffffu, e);
         int row = -1;
         if (e >= 0) row = base[e] + mine[e] + __popc(same & ((1u << lane) - 1));
         __syncwarp();
         if (e >= 0 && lane == __ffs(same) - 1) mine[e] += __popc(same);
         __syncwarp();
-        if (in) slot_row[i + lane] = row;
-        if (row >= 0) row_slot[row] = (int)(i + lane);
-        // a row from `used` on is nobody's: its own index is as good a place as any
-        if (in && i + lane >= used) row_slot[i + lane] = -1;
-    }
-    if (CS > 1) cluster_sync_all();   // no CTA leaves while another reads its totals
+        if (i < hi) {
+            slot_row[i] = row;
+            // a row from `used` on is nobody's: its own index is as good a place as any
+            if (i >= used) row_slot[i] = -1;
+        }
+        if (row >= 0) row_slot[row] = (int)i;
+    };
+#pragma unroll
+    for (int k = 0; k < kSortKeys; ++k)
+        if (lo + 32 * k < hi) place(lo + 32 * k + lane, key[k]);
+    for (int64_t i = lo + 32 * kSortKeys; i < hi; i += 32) place(i + lane, load_key(i + lane));
+    if (CS > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // ---------------------------------------------------------------------------
-// Rows to their sorted places.  One thread block per token: its row is read
-// once and written to each of its places.  Bound by HBM writes.
+// Rows to their sorted places.  A thread block per token and share of its row,
+// which is read once and written to each of its places.  Bound by HBM writes.
 // ---------------------------------------------------------------------------
 constexpr int kRowThreads = 128;
 
 template <typename V>
 __device__ __forceinline__ void copy_row(const V *__restrict__ src, V *__restrict__ dst, int64_t n, int64_t P,
                                          const int32_t *rows, const int32_t *row_slot, int64_t t, int k) {
-    for (int64_t c = threadIdx.x; c < n; c += blockDim.x) {
+    for (int64_t c = blockIdx.y * kRowThreads + threadIdx.x; c < n; c += gridDim.y * kRowThreads) {
         const V v = __ldg(src + t * n + c);
         for (int j = 0; j < k; ++j) {
             const int64_t r = rows[j];
@@ -157,7 +180,7 @@ __device__ __forceinline__ void copy_row(const V *__restrict__ src, V *__restric
     for (int j = 0; j < k; ++j) {
         const int64_t r = t * k + j;
         if (row_slot[r] >= 0) continue;
-        for (int64_t c = threadIdx.x; c < n; c += blockDim.x) dst[r * n + c] = V{};
+        for (int64_t c = blockIdx.y * kRowThreads + threadIdx.x; c < n; c += gridDim.y * kRowThreads) dst[r * n + c] = V{};
     }
 }
 
@@ -236,8 +259,8 @@ template <int VEC> __device__ __forceinline__ void store_vec(__nv_bfloat16 *p, c
 }
 
 // ---------------------------------------------------------------------------
-// Sorted rows back to tokens: one thread block per token, fp32 sums over its
-// slots in order.  Bound by HBM reads.
+// Sorted rows back to tokens: a thread block per token and share of its columns,
+// fp32 sums over the slots in order.  Bound by HBM reads.
 // ---------------------------------------------------------------------------
 template <typename T, int VEC>
 __global__ void __launch_bounds__(kRowThreads)
@@ -252,7 +275,7 @@ __global__ void __launch_bounds__(kRowThreads)
         wt[threadIdx.x] = weights ? weights[t * k + threadIdx.x] : 1.0f;
     }
     __syncthreads();
-    for (int c = threadIdx.x * VEC; c < H; c += kRowThreads * VEC) {
+    for (int c = (blockIdx.y * kRowThreads + threadIdx.x) * VEC; c < H; c += gridDim.y * kRowThreads * VEC) {
         Vec<VEC> acc;
 #pragma unroll
         for (int i = 0; i < VEC; ++i) acc.v[i] = 0.0f;
@@ -328,11 +351,17 @@ __global__ void __launch_bounds__(kGradWarps * 32)
 
 inline uintptr_t bits(const void *p) { return reinterpret_cast<uintptr_t>(p); }
 
+// Blocks of a token of n column steps: one step a thread, and at most 16 blocks.
+inline dim3 row_grid(int T, int64_t n) {
+    const int64_t y = (n + kRowThreads - 1) / kRowThreads;
+    return dim3((unsigned)T, (unsigned)(y < 16 ? y : 16));
+}
+
 template <typename V>
 cudaError_t dispatch_as(const void *x, int64_t row_bytes, const void *scale, int64_t scale_bytes,
                         const int32_t *row_slot, const int32_t *slot_row, void *xs, void *xs_scale, int T, int k,
                         cudaStream_t s) {
-    moe_dispatch_kernel<V><<<T, kRowThreads, 0, s>>>(
+    moe_dispatch_kernel<V><<<row_grid(T, row_bytes / (int64_t)sizeof(V)), kRowThreads, 0, s>>>(
         static_cast<const V *>(x), row_bytes / (int64_t)sizeof(V), static_cast<const uint32_t *>(scale), scale_bytes / 4,
         row_slot, slot_row, static_cast<V *>(xs), static_cast<uint32_t *>(xs_scale), T, k);
     return cudaGetLastError();
@@ -342,9 +371,9 @@ template <typename T>
 cudaError_t combine_as(const T *rows, const int32_t *slot_row, const float *weights, float *y, int Tn, int H, int k,
                        bool accumulate, cudaStream_t s) {
     if (((bits(rows) | bits(y)) & 15) == 0 && H % 8 == 0)
-        moe_combine_kernel<T, 8><<<Tn, kRowThreads, 0, s>>>(rows, slot_row, weights, y, Tn, H, k, accumulate);
+        moe_combine_kernel<T, 8><<<row_grid(Tn, H / 8), kRowThreads, 0, s>>>(rows, slot_row, weights, y, Tn, H, k, accumulate);
     else
-        moe_combine_kernel<T, 1><<<Tn, kRowThreads, 0, s>>>(rows, slot_row, weights, y, Tn, H, k, accumulate);
+        moe_combine_kernel<T, 1><<<row_grid(Tn, H), kRowThreads, 0, s>>>(rows, slot_row, weights, y, Tn, H, k, accumulate);
     return cudaGetLastError();
 }
 
@@ -368,7 +397,10 @@ cudaError_t launch_moe_sort(const int32_t *ids, int32_t *row_slot, int32_t *slot
     int warps = (160 * 1024) / (4 * E);
     if (warps > kSortMaxWarps) warps = kSortMaxWarps;
     const bool one = P <= 32 * kSortMaxWarps;
-    if (one && warps > (P + 31) / 32) warps = (int)((P + 31) / 32);
+    // (one CTA: enough warps for the pairs, and for a thread to an expert in the scan)
+    const int64_t need = (P + 31) / 32 > (E + 31) / 32 ? (P + 31) / 32 : (E + 31) / 32;
+    if (one && warps > need) warps = (int)need;
+    if (!one && warps > kSortClusterWarps) warps = kSortClusterWarps;
     const int smem = 4 * ((warps + 2) * E + 33);
     const void *fn = one ? (const void *)moe_sort_kernel<1> : (const void *)moe_sort_kernel<kSortCluster>;
     const cudaError_t e = ensure_dynamic_smem(fn, (size_t)smem);
@@ -376,6 +408,14 @@ cudaError_t launch_moe_sort(const int32_t *ids, int32_t *row_slot, int32_t *slot
     if (one) {
         moe_sort_kernel<1><<<1, warps * 32, smem, s>>>(ids, row_slot, slot_row, offsets, (int)P, E);
         return cudaGetLastError();
+    }
+    // clusters of more than 8 CTAs have to be asked for, once a device
+    static std::atomic<uint64_t> allowed{0};
+    const uint64_t bit = 1ull << (device_info().device & 63);
+    if (!(allowed.load(std::memory_order_relaxed) & bit)) {
+        const cudaError_t a = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (a != cudaSuccess) return a;
+        allowed.fetch_or(bit, std::memory_order_relaxed);
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(kSortCluster);
