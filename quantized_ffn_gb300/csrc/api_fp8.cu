@@ -81,6 +81,7 @@ zffn_status run_experts(const uint8_t *a, const float *a_scale, const int32_t *o
     d.y_dtype = y_dtype;
     d.M = P; d.N = H; d.K = I; d.E = E;
     d.err = err;
+    d.early = true;   // (the product before writes h and its scales)
     return to_status(launch_fp8_matmul(d, s));
 }
 

@@ -61,6 +61,10 @@ struct Fp8Args {
     int y_dtype;             // zffn_dtype (without SwiGLU)
     int M, N, K, E;
     int *err;
+    // the grid launched just before writes a and a_scale and nothing else that this
+    // product reads, and it waited for the grids before it: the weights are asked
+    // for before it ends
+    bool early;
 };
 cudaError_t launch_fp8_matmul(const Fp8Args &a, cudaStream_t s);
 

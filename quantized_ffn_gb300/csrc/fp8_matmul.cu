@@ -59,12 +59,17 @@ __device__ __forceinline__ void named_barrier(int id, int threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 // acc += d * s on a pair of fp32 values (one instruction, each half rounded once).
-__device__ __forceinline__ void fma2(float2 &acc, uint32_t d0, uint32_t d1, float s) {
-    asm("{\n\t.reg .b64 a, d, f;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 d, {%2, %3};\n\tmov.b64 f, {%4, %4};\n\t"
+__device__ __forceinline__ void fma2(float2 &acc, uint32_t d0, uint32_t d1, float s0, float s1) {
+    asm("{\n\t.reg .b64 a, d, f;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 d, {%2, %3};\n\tmov.b64 f, {%4, %5};\n\t"
         "fma.rn.f32x2 a, d, f, a;\n\tmov.b64 {%0, %1}, a;\n\t}"
         : "+f"(acc.x), "+f"(acc.y)
-        : "r"(d0), "r"(d1), "f"(s));
+        : "r"(d0), "r"(d1), "f"(s0), "f"(s1));
 }
+__device__ __forceinline__ void fma2(float2 &acc, uint32_t d0, uint32_t d1, float s) { fma2(acc, d0, d1, s, s); }
+// Programmatic launch: wait until the grids before this one in the stream are
+// complete and their writes visible; let the next grid's blocks be scheduled.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 template <int R> __device__ __forceinline__ void reg_alloc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
 template <int R> __device__ __forceinline__ void reg_dealloc() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
 // mbar_wait of the large tiles' roles: the barrier is asked without suspending the
@@ -91,51 +96,6 @@ __device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, volatil
 }
 __device__ __forceinline__ float swiglu(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
 
-// A tile of rows of one expert (e == E: rows that belong to no expert).
-struct RowTile {
-    int e, row0, rows;
-};
-// Row tile t of a call: every expert's rows in tiles of at most `tr`, experts in
-// order, then the rows past the last expert.  Called by one full warp; false
-// past the last tile.  offsets are kept within [0, M] whatever they hold.
-__device__ __forceinline__ bool row_tile(const int32_t *offsets, int E, int M, int tr, int t, RowTile &out) {
-    const int lane = threadIdx.x & 31;
-    if (!offsets) {
-        out = {0, t * tr, min(tr, M - t * tr)};
-        return out.rows > 0;
-    }
-    const int per = (E + 32) / 32, g0 = min(lane * per, E + 1), g1 = min(g0 + per, E + 1);
-    auto lo = [&](int g) { return min(max(__ldg(offsets + g), 0), M); };
-    auto hi = [&](int g) { return g < E ? min(max(__ldg(offsets + g + 1), 0), M) : M; };
-    int n = 0;
-    for (int g = g0; g < g1; ++g) n += (max(hi(g) - lo(g), 0) + tr - 1) / tr;
-    int inc = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += v;
-    }
-    int left = t - (inc - n);
-    const bool mine = left >= 0 && left < n;
-    if (mine) {
-        for (int g = g0; g < g1; ++g) {
-            const int r = max(hi(g) - lo(g), 0), c = (r + tr - 1) / tr;
-            if (left < c) {
-                out = {g, lo(g) + left * tr, min(tr, r - left * tr)};
-                break;
-            }
-            left -= c;
-        }
-    }
-    const unsigned who = __ballot_sync(0xffffffffu, mine);
-    if (!who) return false;
-    const int src = __ffs(who) - 1;
-    out.e = __shfl_sync(0xffffffffu, out.e, src);
-    out.row0 = __shfl_sync(0xffffffffu, out.row0, src);
-    out.rows = __shfl_sync(0xffffffffu, out.rows, src);
-    return true;
-}
-
 struct Params {
     const float *sa, *sw0, *sw1;
     const int32_t *offsets;
@@ -146,18 +106,96 @@ struct Params {
     int row_tiles;      // bound of the number of row tiles
     int n_tiles;        // large: tiles of W's rows
     int y_bf16;         // plain: y is bf16 (else fp32)
+    int early;          // small: all but a and its scales are complete before the previous grid is
     int vec;            // y's rows take vector stores (small: 4 elements, large: 16 bytes)
 };
 struct Maps {
     CUtensorMap a, w0, w1, y;   // y: the large tiles' stores
 };
 
+// A tile of the result: rows of one expert (e == E: rows of none) times a tile of W's rows.
+struct RowTile {
+    int e, row0, rows, nt;
+};
+
+// Tile i of a cluster's walk: the group of rows, its rows, the W tile.
+template <class C>
+struct Walk {
+    int e, row0, rows, nt;   // rows: of the tile, <= C::TM
+    int t;
+
+    __device__ __forceinline__ void start(int cluster) { t = cluster; e = 0; }
+    // false past the last tile.  One full warp.  cum[g]: row tiles before group
+    // g and its first row; one entry past the last.
+    __device__ __forceinline__ bool get(const Params &p, const int2 *cum) {
+        const int n_tiles = p.n_tiles;
+        if (!p.offsets) {
+            const int rt_all = p.row_tiles;
+            if (t >= rt_all * n_tiles) return false;
+            const int first = t / (C::GROUP * n_tiles) * C::GROUP;
+            const int in = t - first * n_tiles, wide = min(C::GROUP, rt_all - first);
+            nt = in / wide;
+            row0 = (first + in - nt * wide) * C::TM;
+            rows = min(C::TM, p.M - row0);
+            return true;
+        }
+        const int groups = p.E + 1;
+        if (t >= cum[groups].x * n_tiles) return false;
+        const int rt = t / n_tiles, lane = threadIdx.x & 31;
+        nt = t - rt * n_tiles;
+        for (;; e += 32) {   // the group whose tiles hold rt: ascending from the last one
+            const unsigned past = __ballot_sync(0xffffffffu, cum[min(e + lane + 1, groups)].x > rt);
+            if (past) {
+                e += __ffs(past) - 1;
+                break;
+            }
+        }
+        const int2 at = cum[e];
+        row0 = at.y + (rt - at.x) * C::TM;
+        rows = min(C::TM, (e < p.E ? min(max(cum[e + 1].y, at.y), p.M) : p.M) - row0);
+        return true;
+    }
+};
+
+// The groups of rows (the experts, then the rows of none; h needs no zeros there)
+// in shared memory: {row tiles before the group, its first row}, one entry past the
+// last.  Called by the whole block; offsets are kept within [0, M] whatever they hold.
+template <class C>
+__device__ __forceinline__ void build_groups(const Params &p, int2 *cum) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int g = threadIdx.x; g <= p.E; g += C::THREADS) {
+        const int lo = min(max(__ldg(p.offsets + g), 0), p.M);
+        const int hi = g < p.E ? min(max(__ldg(p.offsets + g + 1), 0), p.M) : (C::GU ? lo : p.M);
+        cum[g] = make_int2((max(hi - lo, 0) + C::TM - 1) / C::TM, lo);
+    }
+    __syncthreads();
+    if (warp == 0) {
+        const int per = (p.E + 32) / 32, g0 = min(lane * per, p.E + 1), g1 = min(g0 + per, p.E + 1);
+        int n = 0;
+        for (int g = g0; g < g1; ++g) n += cum[g].x;
+        int inc = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += v;
+        }
+        int at = inc - n;
+        for (int g = g0; g < g1; ++g) {
+            const int c = cum[g].x;
+            cum[g].x = at;
+            at += c;
+        }
+        if (lane == 31) cum[p.E + 1] = make_int2(inc, p.M);
+    }
+}
+
 // ---------------------------------------------------------------------------
-// Few rows an expert: the weights on the MMA's M side.  A block takes 128 rows
-// of W (GU: 128 gate and 128 up rows) times TN rows of a; a cluster of
-// blocks splits K and joins through distributed shared memory in rank order, so
-// that the result is the same every time.  Bound by HBM: every weight byte is
-// read once, by TMA, into a ring.
+// Few rows an expert: the weights on the MMA's M side.  A tile is 128 rows of W
+// (GU: 128 gate and 128 up rows) times TN rows of a; each cluster takes tiles in
+// turn, the ring of TMA loads running on from one to the next.  Where the tiles
+// are fewer than the SMs a cluster's blocks split K and join through distributed
+// shared memory in rank order, so that the result is the same every time.  Bound
+// by HBM: every weight byte is read once.
 //
 // Roles: warps 0 .. 4 NW - 1 take a block's product out of tensor memory, scale
 // and sum it in registers, and write the result; then one warp loads by TMA and
@@ -165,212 +203,80 @@ struct Maps {
 // ---------------------------------------------------------------------------
 template <int TN_, bool GU_>
 struct SmallCfg {
-    static constexpr int TN = TN_;
+    static constexpr int TN = TN_, TM = TN_;
     static constexpr bool GU = GU_;
+    static constexpr int CTAS = 1;
+    static constexpr int TNW = 128;                          // rows of W (of each, GU)
+    static constexpr int GROUP = 8;                          // dense: row tiles that share a W tile in turn
     static constexpr int NW = GU ? 2 : 1;                    // weight tiles
     static constexpr int W_BYTES = 128 * 128;
     static constexpr int STAGE = NW * W_BYTES + TN * 128;
-    // TN = 64 holds 64 sums a thread: one block an SM with a deep ring, else two
-    static constexpr int BLOCKS = TN == 64 ? 1 : 2;
-    static constexpr int RING = BLOCKS == 2 ? 110 * 1024 : 205 * 1024;
-    static constexpr int NS = RING / STAGE;
+    static constexpr int BLOCKS = GU ? 1 : 2;                // blocks an SM
+    static constexpr int NS = GU ? (TN == 64 ? 3 : 5) : TN == 16 ? 5 : TN == 32 ? 4 : 3;
     static constexpr int NB = TN == 16 ? 4 : 2;              // accumulators in tensor memory
     static constexpr int TMEM_COLS = NB * NW * TN;           // 64 .. 256, a power of two
     static constexpr int SEG = 4;                            // K blocks of scales kept at a time
     static constexpr int TAB = NW * SEG * TN;                // floats of one segment's scales
     static constexpr int EPI = 4 * NW;                       // warps that sum
     static constexpr int THREADS = (EPI + 2) * 32;
-    static constexpr int OFF_TAB = NS * STAGE;
+    static constexpr int OFF_PART = NS * STAGE;              // sums [weight tile][row][128]
+    static constexpr int OFF_TAB = OFF_PART + NW * TN * 128 * 4;
     static constexpr int OFF_BAR = OFF_TAB + 2 * TAB * 4;
-    static constexpr int SMEM = OFF_BAR + (2 * NS + 2 * NB + 1) * 8 + 32 + 1024;
-    static_assert(NW * TN * 128 * 4 <= NS * STAGE, "the partial sums reuse the ring");
+    static constexpr int OFF_CUM = OFF_BAR + (2 * NS + 2 * NB + 1) * 8 + 8;
+    static constexpr int SMEM = OFF_CUM + 1024;              // + {row tiles before, first row} of each group of rows
 };
 
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) small_kernel(const __grid_constant__ Maps maps, const Params p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    float *part = reinterpret_cast<float *>(smem + C::OFF_PART);
     float *tab = reinterpret_cast<float *>(smem + C::OFF_TAB);
     uint64_t *s_full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
     uint64_t *s_empty = s_full + C::NS, *t_full = s_empty + C::NS, *t_empty = t_full + C::NB, *done = t_empty + C::NB;
-    int *info = reinterpret_cast<int *>(done + 1);           // abort, TMEM base, row tile (3), found
+    int *info = reinterpret_cast<int *>(done + 1);           // abort, TMEM base
+    int2 *cum = reinterpret_cast<int2 *>(smem + C::OFF_CUM);
     volatile int *abort_flag = info;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    uint32_t split, rank;
+    uint32_t split;
     asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(split));
-    rank = cluster_ctarank();
-    const int tile = blockIdx.x / split;
-    const int nt = tile / p.row_tiles;                        // row tiles of one expert follow each other,
-                                                              // so that its weights are found in L2
-    if (warp == 0) {
-        RowTile rt{0, 0, 0};
-        const bool found = row_tile(p.offsets, p.E, p.M, C::TN, tile - nt * p.row_tiles, rt);
-        if (lane == 0) {
-            info[0] = 0;
-            info[2] = rt.e;
-            info[3] = rt.row0;
-            info[4] = rt.rows;
-            info[5] = found;
-        }
-    } else if (warp == 1 && lane == 0) {
+    const uint32_t rank = cluster_ctarank();
+    if (warp == C::EPI && lane == 0) {
+        info[0] = 0;
         for (int i = 0; i < C::NS; ++i) { mbar_init(&s_full[i], 1); mbar_init(&s_empty[i], 1); }
         for (int i = 0; i < C::NB; ++i) { mbar_init(&t_full[i], 1); mbar_init(&t_empty[i], C::EPI); }
         mbar_init(done, 1);
         fence_mbarrier_init();
-    }
-    __syncthreads();
-    const int e = info[2], row0 = info[3], rows = info[4], n0 = nt * 128;
-    if (!info[5]) return;
-    if (e >= p.E) {
-        // rows of no expert: zeros (no product reads their h)
-        if (!C::GU)
-            for (int j = rank; j < rows; j += split)
-                for (int n = n0 + threadIdx.x; n < min(n0 + 128, p.N); n += C::THREADS) {
-                    const int64_t at = (int64_t)(row0 + j) * p.N + n;
-                    if (p.y_bf16) static_cast<__nv_bfloat16 *>(p.y)[at] = __float2bfloat16_rn(0.0f);
-                    else static_cast<float *>(p.y)[at] = 0.0f;
-                }
-        return;
+        prefetch_tensormap(&maps.a);
+        prefetch_tensormap(&maps.w0);
+        if (C::GU) prefetch_tensormap(&maps.w1);
     }
     if (warp == C::EPI + 1) {
         tmem_alloc(reinterpret_cast<uint32_t *>(info + 1), C::TMEM_COLS);
         tmem_relinquish();
         tc_fence_before();
     }
+    if (!p.early) grid_wait();
+    if (p.offsets) build_groups<C>(p, cum);
     __syncthreads();
+    // (once this block has its tensor memory: a block of the next grid on this SM
+    // could otherwise take it and then wait for this grid; and after the wait, so
+    // that an early reader of the next grid finds the grids before this complete)
+    if (!p.early) grid_launch_dependents();
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(info + 1);
-    const int KB = (p.K + kF8Block - 1) / kF8Block;
+    const int KB = (p.K + kF8Block - 1) / kF8Block, nb = p.n_tiles;
     const int kb0 = (int)((int64_t)KB * rank / split), nkb = (int)((int64_t)KB * (rank + 1) / split) - kb0;
-    float acc[C::TN];
-#pragma unroll
-    for (int j = 0; j < C::TN; ++j) acc[j] = 0.0f;
+    const int step = gridDim.x / split;
+    Walk<C> wk;
+    wk.start(blockIdx.x / split);
+    RowTile tile{0, 0, 0, 0};   // the last tile whose sums are in `part` (split > 1: the only one)
 
-    if (warp == C::EPI) {
-        // ---- TMA producer
-        if (lane == 0) {
-            int i = 0;
-            for (; i < nkb; ++i) {
-                const int s = i % C::NS;
-                if (i >= C::NS && !mbar_wait(&s_empty[s], ((i / C::NS) & 1) ^ 1, abort_flag, p.err)) break;
-                uint8_t *st = smem + s * C::STAGE;
-                mbar_arrive_expect_tx(&s_full[s], C::STAGE);
-                const int kc = (kb0 + i) * kF8Block;
-                tma_load_2d(st, &maps.w0, &s_full[s], kc, e * p.N + n0);
-                if (C::GU) tma_load_2d(st + C::W_BYTES, &maps.w1, &s_full[s], kc, e * p.N + n0);
-                tma_load_2d(st + C::NW * C::W_BYTES, &maps.a, &s_full[s], kc, row0);
-            }
-            if (*abort_flag)   // wait for the copies in flight before the block leaves
-                for (int j = i > C::NS ? i - C::NS : 0; j < i; ++j)
-                    mbar_wait(&s_full[j % C::NS], (j / C::NS) & 1, nullptr, p.err);
-        }
-        __syncwarp();
-    } else if (warp == C::EPI + 1) {
-        // ---- MMA issuer
-        constexpr uint32_t idesc = idesc_f8_f32(128, C::TN);
-        if (lane == 0) {
-            for (int i = 0; i < nkb; ++i) {
-                const int s = i % C::NS, b = i % C::NB;
-                if (!mbar_wait(&s_full[s], (i / C::NS) & 1, abort_flag, p.err)) break;
-                if (i >= C::NB && !mbar_wait(&t_empty[b], ((i / C::NB) & 1) ^ 1, abort_flag, p.err)) break;
-                tc_fence_after();
-                const uint32_t st = smem_u32(smem + s * C::STAGE);
-                const uint64_t bd = smem_desc_k_sw128(st + C::NW * C::W_BYTES);
-#pragma unroll
-                for (int w = 0; w < C::NW; ++w) {
-                    const uint64_t ad = smem_desc_k_sw128(st + w * C::W_BYTES);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)   // 32 bytes of K a step
-                        tc_mma_f8(tmem + (b * C::NW + w) * C::TN, ad + 2 * k, bd + 2 * k, idesc, k != 0);
-                }
-                tc_commit(&s_empty[s]);
-                tc_commit(&t_full[b]);
-            }
-            tc_commit(done);
-            mbar_wait(done, 0, nullptr, p.err);
-        }
-        __syncwarp();
-    } else {
-        // ---- scale and sum: thread = one row of W
-        const int w = warp >> 2, q = warp & 3, tid = threadIdx.x & 127;
-        const int nb = (p.N + kF8Block - 1) / kF8Block;
-        const float *sw = (w ? p.sw1 : p.sw0) + ((int64_t)e * nb + nt) * KB;
-        const uint32_t taddr = tmem + w * C::TN + ((uint32_t)(q * 32) << 16);
-        constexpr int PER = (C::SEG * C::TN + 127) / 128;
-        float next[PER];
-        // the scales' products of segment g: [K block][row of a]
-        auto fetch = [&](int g) {
-#pragma unroll
-            for (int r = 0; r < PER; ++r) {
-                const int v = r * 128 + tid, j = v / C::SEG, i = g * C::SEG + v % C::SEG;
-                next[r] = v < C::SEG * C::TN && j < rows && i < nkb
-                              ? __ldg(p.sa + (int64_t)(row0 + j) * KB + kb0 + i) * __ldg(sw + kb0 + i)
-                              : 0.0f;
-            }
-        };
-        fetch(0);
-        for (int i = 0; i < nkb; ++i) {
-            const int g = i / C::SEG, b = i % C::NB;
-            float *seg = tab + (g & 1) * C::TAB + w * C::SEG * C::TN;
-            if (i % C::SEG == 0) {
-                // (this half of the table was last read two segments ago, before
-                // the barrier of the one between)
-#pragma unroll
-                for (int r = 0; r < PER; ++r) {
-                    const int v = r * 128 + tid;
-                    if (v < C::SEG * C::TN) seg[(v % C::SEG) * C::TN + v / C::SEG] = next[r];
-                }
-                named_barrier(1 + w, 128);
-                fetch(g + 1);
-            }
-            // (a thread that gives up still meets the others at the barriers)
-            mbar_wait(&t_full[b], (i / C::NB) & 1, abort_flag, p.err);
-            tc_fence_after();
-            const float4 *s4 = reinterpret_cast<const float4 *>(seg + (i % C::SEG) * C::TN);
-            const uint32_t from = taddr + b * C::NW * C::TN;
-            constexpr int STEP = C::TN >= 32 ? 32 : 16;
-#pragma unroll
-            for (int c = 0; c < C::TN; c += STEP) {
-                uint32_t d[STEP];
-                if constexpr (STEP == 32) tmem_ld_32x32b_x32(from + c, d);
-                else tmem_ld_32x32b_x16(from + c, d);
-                tmem_ld_wait(d);
-                if (c + STEP == C::TN) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&t_empty[b]);
-                }
-#pragma unroll
-                for (int j = 0; j < STEP; j += 4) {
-                    const float4 s = s4[(c + j) / 4];
-                    acc[c + j] = fmaf(__uint_as_float(d[j]), s.x, acc[c + j]);
-                    acc[c + j + 1] = fmaf(__uint_as_float(d[j + 1]), s.y, acc[c + j + 1]);
-                    acc[c + j + 2] = fmaf(__uint_as_float(d[j + 2]), s.z, acc[c + j + 2]);
-                    acc[c + j + 3] = fmaf(__uint_as_float(d[j + 3]), s.w, acc[c + j + 3]);
-                }
-            }
-        }
-    }
-    // every product has been taken out of tensor memory, so every copy into the
-    // ring has been read: it now holds the partial sums, [weight tile][row][128]
-    __syncthreads();
-    float *part = reinterpret_cast<float *>(smem);
-    if (warp < C::EPI) {
-        float *mine = part + (warp >> 2) * C::TN * 128 + (threadIdx.x & 127);
-#pragma unroll
-        for (int j = 0; j < C::TN; ++j) mine[j * 128] = acc[j];
-    }
-    if (warp == C::EPI + 1) {
-        tc_fence_after();
-        tmem_dealloc(tmem, C::TMEM_COLS);
-    }
-    if (split > 1) cluster_sync_all();
-    else __syncthreads();
-    if (warp < C::EPI) {
-        // a warp per row, 4 columns a lane: the ranks' sums in rank order
+    // the sums in `part` -> y or h: a warp per row, 4 columns a lane, the ranks' sums in rank order
+    auto emit = [&](const RowTile &t) {
         const uint32_t base = smem_u32(part);
-        const int n = n0 + lane * 4;
-        for (int j = rank + split * warp; j < rows; j += split * C::EPI) {
+        const int n = t.nt * 128 + lane * 4;
+        for (int j = rank + split * warp; j < t.rows; j += split * C::EPI) {
             float v[C::NW][4];
 #pragma unroll
             for (int w = 0; w < C::NW; ++w) {
@@ -382,7 +288,7 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) small_kernel(const __gr
                 }
                 v[w][0] = s.x; v[w][1] = s.y; v[w][2] = s.z; v[w][3] = s.w;
             }
-            const int64_t row = row0 + j;
+            const int64_t row = t.row0 + j;
             if constexpr (C::GU) {
                 float h[4], top = 0.0f;
 #pragma unroll
@@ -397,7 +303,7 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) small_kernel(const __gr
                 if (n < p.N)
                     *reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(p.y) + row * p.N + n) =
                         f8x4_satfinite(h[0] * inv, h[1] * inv, h[2] * inv, h[3] * inv);
-                if (lane == 0) p.y_scale[row * ((p.N + kF8Block - 1) / kF8Block) + nt] = pow2f(sp);
+                if (lane == 0) p.y_scale[row * nb + t.nt] = pow2f(sp);
             } else if (p.vec && n + 3 < p.N) {
                 if (p.y_bf16) {
                     const __nv_bfloat162 lo = __floats2bfloat162_rn(v[0][0], v[0][1]), hi = __floats2bfloat162_rn(v[0][2], v[0][3]);
@@ -416,8 +322,178 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) small_kernel(const __gr
                     }
             }
         }
+    };
+
+    if (warp == C::EPI) {
+        // ---- TMA producer
+        uint32_t it = 0;
+        bool ok = true;
+        auto load_w = [&](int s, int i) {
+            uint8_t *st = smem + s * C::STAGE;
+            mbar_arrive_expect_tx(&s_full[s], C::STAGE);
+            tma_load_2d(st, &maps.w0, &s_full[s], (kb0 + i) * kF8Block, wk.e * p.N + wk.nt * 128);
+            if (C::GU) tma_load_2d(st + C::W_BYTES, &maps.w1, &s_full[s], (kb0 + i) * kF8Block, wk.e * p.N + wk.nt * 128);
+        };
+        auto load_a = [&](int s, int i) {
+            tma_load_2d(smem + s * C::STAGE + C::NW * C::W_BYTES, &maps.a, &s_full[s], (kb0 + i) * kF8Block, wk.row0);
+        };
+        bool waited = !p.early;
+        for (; ok && wk.get(p, cum); wk.t += step) {
+            int i = 0;
+            if (!waited && wk.e < p.E) {
+                // the weights of the first stages are asked for before what the
+                // previous kernel writes is waited for
+                const int first = min(nkb, C::NS);
+                if (lane == 0)
+                    for (int j = 0; j < first; ++j) load_w(j, j);
+                grid_wait();
+                if (lane == 0)
+                    for (int j = 0; j < first; ++j) load_a(j, j);
+                waited = true;
+                it = i = first;
+            }
+            for (; i < nkb && lane == 0 && wk.e < p.E; ++i, ++it) {
+                const uint32_t s = it % C::NS;
+                if (it >= C::NS && !bar_wait(&s_empty[s], ((it / C::NS) & 1) ^ 1, abort_flag, p.err)) { ok = false; break; }
+                load_w(s, i);
+                load_a(s, i);
+            }
+            ok = __shfl_sync(0xffffffffu, ok && !*abort_flag, 0);
+        }
+        if (lane == 0 && *abort_flag)   // wait for the copies in flight before the block leaves
+            for (uint32_t j = it > C::NS ? it - C::NS : 0; j < it; ++j)
+                mbar_wait(&s_full[j % C::NS], (j / C::NS) & 1, nullptr, p.err);
+        __syncwarp();
+    } else if (warp == C::EPI + 1) {
+        // ---- MMA issuer
+        constexpr uint32_t idesc = idesc_f8_f32(128, C::TN);
+        uint32_t it = 0;
+        bool ok = true;
+        for (; ok && wk.get(p, cum); wk.t += step) {
+            for (int i = 0; i < nkb && wk.e < p.E; ++i, ++it) {
+                const uint32_t s = it % C::NS, b = it % C::NB;
+                ok = bar_wait(&s_full[s], (it / C::NS) & 1, abort_flag, p.err) &&
+                     (it < C::NB || bar_wait(&t_empty[b], ((it / C::NB) & 1) ^ 1, abort_flag, p.err));
+                if (!__all_sync(0xffffffffu, ok)) break;
+                tc_fence_after();
+                const uint32_t st = smem_u32(smem) + s * C::STAGE;
+                const uint64_t bd = smem_desc_k_sw128(st + C::NW * C::W_BYTES);
+                if (elect_one()) {
+#pragma unroll
+                    for (int w = 0; w < C::NW; ++w) {
+                        const uint64_t ad = smem_desc_k_sw128(st + w * C::W_BYTES);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)   // 32 bytes of K a step
+                            tc_mma_f8(tmem + (b * C::NW + w) * C::TN, ad + 2 * k, bd + 2 * k, idesc, k != 0);
+                    }
+                    tc_commit(&t_full[b]);
+                    tc_commit(&s_empty[s]);
+                }
+                __syncwarp();
+            }
+            ok = __all_sync(0xffffffffu, ok && !*abort_flag);
+        }
+        if (elect_one()) tc_commit(done);
+        __syncwarp();
+        if (lane == 0) mbar_wait(done, 0, nullptr, p.err);
+        __syncwarp();
+    } else {
+        // ---- scale and sum: thread = one row of W
+        if (p.early) grid_wait();
+        const int w = warp >> 2, q = warp & 3, tid = threadIdx.x & 127;
+        const uint32_t taddr = tmem + w * C::TN + ((uint32_t)(q * 32) << 16);
+        float *mine = part + w * C::TN * 128 + tid;
+        constexpr int PER = (C::SEG * C::TN + 127) / 128;
+        float next[PER];
+        // the scales' products of segment g of the tile at hand: [K block][row of a]
+        auto fetch = [&](int g) {
+            const float *sw = (w ? p.sw1 : p.sw0) + ((int64_t)wk.e * nb + wk.nt) * KB + kb0;
+#pragma unroll
+            for (int r = 0; r < PER; ++r) {
+                const int v = r * 128 + tid, j = v / C::SEG, i = g * C::SEG + v % C::SEG;
+                next[r] = v < C::SEG * C::TN && j < wk.rows && i < nkb && wk.e < p.E
+                              ? __ldg(p.sa + (int64_t)(wk.row0 + j) * KB + kb0 + i) * __ldg(sw + i)
+                              : 0.0f;
+            }
+        };
+        uint32_t it = 0, half = 0;
+        bool have = wk.get(p, cum), second = false;
+        if (have) fetch(0);
+        while (have) {
+            float2 acc[C::TN / 2];
+#pragma unroll
+            for (int j = 0; j < C::TN / 2; ++j) acc[j] = make_float2(0.0f, 0.0f);
+            float *seg = tab;
+            for (int i = 0; i < nkb && wk.e < p.E; ++i, ++it) {
+                const int b = it % C::NB;
+                if (i % C::SEG == 0) {
+                    // (this half of the table was last read two segments ago, before
+                    // the barrier of the one between)
+                    seg = tab + half * C::TAB + w * C::SEG * C::TN;
+                    half ^= 1;
+#pragma unroll
+                    for (int r = 0; r < PER; ++r) {
+                        const int v = r * 128 + tid;
+                        if (v < C::SEG * C::TN) seg[(v % C::SEG) * C::TN + v / C::SEG] = next[r];
+                    }
+                    named_barrier(1 + w, 128);
+                    fetch(i / C::SEG + 1);
+                }
+                // (a thread that gives up still meets the others at the barriers)
+                bar_wait(&t_full[b], (it / C::NB) & 1, abort_flag, p.err);
+                __syncwarp();
+                tc_fence_after();
+                const float4 *s4 = reinterpret_cast<const float4 *>(seg + (i % C::SEG) * C::TN);
+                const uint32_t from = taddr + b * C::NW * C::TN;
+                constexpr int STEP = C::TN >= 32 ? 32 : 16;
+#pragma unroll
+                for (int c = 0; c < C::TN; c += STEP) {
+                    uint32_t d[STEP];
+                    if constexpr (STEP == 32) tmem_ld_32x32b_x32(from + c, d);
+                    else tmem_ld_32x32b_x16(from + c, d);
+                    tmem_ld_wait(d);
+                    if (c + STEP == C::TN) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&t_empty[b]);
+                    }
+#pragma unroll
+                    for (int j = 0; j < STEP; j += 4) {
+                        const float4 s = s4[(c + j) / 4];
+                        fma2(acc[(c + j) / 2], d[j], d[j + 1], s.x, s.y);
+                        fma2(acc[(c + j) / 2 + 1], d[j + 2], d[j + 3], s.z, s.w);
+                    }
+                }
+            }
+            tile = {wk.e, wk.row0, wk.rows, wk.nt};
+            wk.t += step;
+            have = wk.get(p, cum);
+            if (have) fetch(0);
+            if (second) named_barrier(3, C::EPI * 32);       // the tile before has been written
+            second = true;
+#pragma unroll
+            for (int j = 0; j < C::TN / 2; ++j) {
+                mine[2 * j * 128] = acc[j].x;
+                mine[(2 * j + 1) * 128] = acc[j].y;
+            }
+            if (split == 1) {
+                named_barrier(3, C::EPI * 32);
+                emit(tile);
+            }
+        }
     }
-    if (split > 1) cluster_sync_all();   // no block leaves while another reads its sums
+    tc_fence_before();
+    __syncthreads();
+    if (split > 1) {
+        // (fewer tiles than clusters: each has one)
+        cluster_sync_all();
+        if (warp < C::EPI) emit(tile);
+        cluster_sync_all();   // no block leaves while another reads its sums
+    }
+    if (warp == C::EPI + 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, C::TMEM_COLS);
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -467,45 +543,6 @@ struct LargeCfg {
     static constexpr int SMEM = OFF_CUM + 1024;              // + {row tiles before, first row} of each group of rows
 };
 
-// Tile i of a cluster's walk: the group of rows, its rows, the W tile.
-template <class C>
-struct Walk {
-    int e, row0, rows, nt;   // rows: of the tile, <= C::TM
-    int t;
-
-    __device__ __forceinline__ void start(int cluster) { t = cluster; e = 0; }
-    // false past the last tile.  One full warp.  cum[g]: row tiles before group
-    // g and its first row; one entry past the last.
-    __device__ __forceinline__ bool get(const Params &p, const int2 *cum) {
-        const int n_tiles = p.n_tiles;
-        if (!p.offsets) {
-            const int rt_all = p.row_tiles;
-            if (t >= rt_all * n_tiles) return false;
-            const int first = t / (C::GROUP * n_tiles) * C::GROUP;
-            const int in = t - first * n_tiles, wide = min(C::GROUP, rt_all - first);
-            nt = in / wide;
-            row0 = (first + in - nt * wide) * C::TM;
-            rows = min(C::TM, p.M - row0);
-            return true;
-        }
-        const int groups = p.E + 1;
-        if (t >= cum[groups].x * n_tiles) return false;
-        const int rt = t / n_tiles, lane = threadIdx.x & 31;
-        nt = t - rt * n_tiles;
-        for (;; e += 32) {   // the group whose tiles hold rt: ascending from the last one
-            const unsigned past = __ballot_sync(0xffffffffu, cum[min(e + lane + 1, groups)].x > rt);
-            if (past) {
-                e += __ffs(past) - 1;
-                break;
-            }
-        }
-        const int2 at = cum[e];
-        row0 = at.y + (rt - at.x) * C::TM;
-        rows = min(C::TM, (e < p.E ? min(max(cum[e + 1].y, at.y), p.M) : p.M) - row0);
-        return true;
-    }
-};
-
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_constant__ Maps maps, const Params p) {
     extern __shared__ uint8_t smem_raw[];
@@ -539,35 +576,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
         else { tmem_alloc(dst, 512); tmem_relinquish(); }
         tc_fence_before();
     }
-    if (p.offsets) {
-        // row tiles of each group (the experts, then the rows of none: h needs no
-        // zeros there), then their exclusive sums
-        for (int g = threadIdx.x; g <= p.E; g += C::THREADS) {
-            const int lo = min(max(__ldg(p.offsets + g), 0), p.M);
-            const int hi = g < p.E ? min(max(__ldg(p.offsets + g + 1), 0), p.M) : (C::GU ? lo : p.M);
-            cum[g] = make_int2((max(hi - lo, 0) + C::TM - 1) / C::TM, lo);
-        }
-        __syncthreads();
-        if (warp == 0) {
-            const int per = (p.E + 32) / 32, g0 = min(lane * per, p.E + 1), g1 = min(g0 + per, p.E + 1);
-            int n = 0;
-            for (int g = g0; g < g1; ++g) n += cum[g].x;
-            int inc = n;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xffffffffu, inc, o);
-                if (lane >= o) inc += v;
-            }
-            int at = inc - n;
-            for (int g = g0; g < g1; ++g) {
-                const int c = cum[g].x;
-                cum[g].x = at;
-                at += c;
-            }
-            if (lane == 31) cum[p.E + 1] = make_int2(inc, p.M);
-        }
-    }
+    grid_wait();
+    if (p.offsets) build_groups<C>(p, cum);
     __syncthreads();
+    grid_launch_dependents();          // (this block has its tensor memory: see the small tiles)
     if (C::PAIR) cluster_sync_all();   // the peer's barriers are set up
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(info + 1);
@@ -909,6 +921,27 @@ static int64_t row_tiles_bound(const Fp8Args &a, int tr) {
     return a.M / tr + (a.E + 1 < a.M ? a.E + 1 : a.M);
 }
 
+// Launch as a programmatic dependent of what is before it in the stream (the
+// kernels wait for it before they read anything of theirs).
+static cudaError_t launch_cluster(void (*kernel)(Maps, Params), unsigned grid, unsigned threads, size_t smem, unsigned cluster,
+                                  cudaStream_t s, const Maps &maps, const Params &p) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, maps, p);
+}
+
 template <class C>
 static cudaError_t launch_small(const Fp8Args &a, cudaStream_t s) {
     const DeviceInfo &di = device_info();
@@ -917,31 +950,23 @@ static cudaError_t launch_small(const Fp8Args &a, cudaStream_t s) {
         !encode(&maps.w1, C::GU ? a.w1 : a.w, (int64_t)a.E * a.N, a.K, 128))
         return cudaErrorInvalidValue;
     Params p = params(a);
-    const int64_t rt = row_tiles_bound(a, C::TN), tiles = rt * f8_blocks(a.N);
+    const int64_t rt = row_tiles_bound(a, C::TN), tiles = rt * f8_blocks(a.N), slots = (int64_t)di.num_sms * C::BLOCKS;
     const int KB = (int)f8_blocks(a.K);
-    // split K so that the blocks fill the SMs, two K blocks each at least
-    int64_t split = (int64_t)di.num_sms * C::BLOCKS / tiles;
+    // fewer tiles than blocks: split K so that the blocks fill the SMs, two K blocks each at least
+    int64_t split = slots / tiles;
     split = split > 8 ? 8 : split;
     split = split > KB / 2 ? KB / 2 : split;
     split = split < 1 ? 1 : split;
-    if (rt > 0x7fffffff || tiles * split > 0x7fffffff) return cudaErrorInvalidValue;
+    const int64_t clusters = split > 1 || tiles < slots ? tiles : slots;
+    if (tiles + slots > 0x7fffffff) return cudaErrorInvalidValue;
     p.row_tiles = (int)rt;
+    p.n_tiles = (int)f8_blocks(a.N);
+    p.early = a.early;
     p.vec = a.N % 4 == 0 && (reinterpret_cast<uintptr_t>(a.y) & (p.y_bf16 ? 7 : 15)) == 0;
-    const cudaError_t e = ensure_dynamic_smem((const void *)small_kernel<C>, C::SMEM);
+    const size_t smem = C::SMEM + (a.offsets ? ((size_t)a.E + 2) * 8 : 0);
+    const cudaError_t e = ensure_dynamic_smem((const void *)small_kernel<C>, smem);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(tiles * split));
-    cfg.blockDim = dim3(C::THREADS);
-    cfg.dynamicSmemBytes = C::SMEM;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)split;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, small_kernel<C>, maps, p);
+    return launch_cluster(small_kernel<C>, (unsigned)(clusters * split), C::THREADS, smem, (unsigned)split, s, maps, p);
 }
 
 template <class C>
@@ -980,19 +1005,7 @@ static cudaError_t launch_large(const Fp8Args &a, cudaStream_t s) {
     if (regs != C::REGS) return cudaErrorInvalidConfiguration;
     const cudaError_t e = ensure_dynamic_smem((const void *)large_kernel<C>, smem);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(clusters * C::CTAS));
-    cfg.blockDim = dim3(C::THREADS);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = C::CTAS;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, large_kernel<C>, maps, p);
+    return launch_cluster(large_kernel<C>, (unsigned)(clusters * C::CTAS), C::THREADS, smem, C::CTAS, s, maps, p);
 }
 
 template <bool GU>
