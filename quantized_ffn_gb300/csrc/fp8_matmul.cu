@@ -8,6 +8,8 @@
 // (the scales' product is rounded once before).
 #include <cudaTypedefs.h>
 
+#include <atomic>
+
 #include "fp8.h"
 #include "zffn_internal.cuh"
 
@@ -40,13 +42,17 @@ __device__ __forceinline__ void tc_mma_f8_pair(uint32_t d_tmem, uint64_t a_desc,
 __host__ __device__ constexpr uint32_t idesc_f8_f32(int M, int N) {
     return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
-__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr)
+__device__ __forceinline__ void st_cluster_f4(uint32_t addr, float4 v) {
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
                  : "memory");
-    return v;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// Bring a tile of a tensor map's matrix into L2.
+__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap *map, int c0, int c1) {
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(map)),
+                 "r"(c0), "r"(c1)
+                 : "memory");
 }
 // 2-D TMA tile store shared -> global, tracked by the issuing thread's bulk-async group.
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, uint32_t smem_src, int c0, int c1) {
@@ -193,9 +199,11 @@ __device__ __forceinline__ void build_groups(const Params &p, int2 *cum) {
 // Few rows an expert: the weights on the MMA's M side.  A tile is 128 rows of W
 // (GU: 128 gate and 128 up rows) times TN rows of a; each cluster takes tiles in
 // turn, the ring of TMA loads running on from one to the next.  Where the tiles
-// are fewer than the SMs a cluster's blocks split K and join through distributed
-// shared memory in rank order, so that the result is the same every time.  Bound
-// by HBM: every weight byte is read once.
+// are fewer than the SMs a cluster's blocks split K: row j's sums go to the shared
+// memory of rank j % split, which adds them in rank order, so that the result is
+// the same every time.  (Each rank writes to the others: one barrier of the
+// cluster, where reading from the others takes a second one before a block may
+// leave, 0.8 us.)  Bound by HBM: every weight byte is read once.
 //
 // Roles: warps 0 .. 4 NW - 1 take a block's product out of tensor memory, scale
 // and sum it in registers, and write the result; then one warp loads by TMA and
@@ -212,15 +220,20 @@ struct SmallCfg {
     static constexpr int W_BYTES = 128 * 128;
     static constexpr int STAGE = NW * W_BYTES + TN * 128;
     static constexpr int BLOCKS = GU ? 1 : 2;                // blocks an SM
-    static constexpr int NS = GU ? (TN == 64 ? 3 : 5) : TN == 16 ? 5 : TN == 32 ? 4 : 3;
+    // (GU, TN = 16: three, so that a block of the down product fits beside it)
+    static constexpr int NS = GU ? (TN == 32 ? 5 : 3) : TN == 64 ? 3 : 4;
     static constexpr int NB = TN == 16 ? 4 : 2;              // accumulators in tensor memory
     static constexpr int TMEM_COLS = NB * NW * TN;           // 64 .. 256, a power of two
     static constexpr int SEG = 4;                            // K blocks of scales kept at a time
     static constexpr int TAB = NW * SEG * TN;                // floats of one segment's scales
     static constexpr int EPI = 4 * NW;                       // warps that sum
     static constexpr int THREADS = (EPI + 2) * 32;
-    static constexpr int OFF_PART = NS * STAGE;              // sums [weight tile][row][128]
-    static constexpr int OFF_TAB = OFF_PART + NW * TN * 128 * 4;
+    static constexpr int MAX_SPLIT = 8;
+    // sums [weight tile][rank][row / split][128]
+    static constexpr int PART_ROWS = TN + MAX_SPLIT - 1;     // split * ceil(TN / split), at most
+    static constexpr int OFF_PART = NS * STAGE;
+    static_assert(NW * TN * 128 * 4 <= NS * STAGE, "a block's own sums fit into its ring");
+    static constexpr int OFF_TAB = OFF_PART + NW * PART_ROWS * 128 * 4;
     static constexpr int OFF_BAR = OFF_TAB + 2 * TAB * 4;
     static constexpr int OFF_CUM = OFF_BAR + (2 * NS + 2 * NB + 1) * 8 + 8;
     static constexpr int SMEM = OFF_CUM + 1024;              // + {row tiles before, first row} of each group of rows
@@ -241,6 +254,8 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) small_kernel(const __gr
     uint32_t split;
     asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(split));
     const uint32_t rank = cluster_ctarank();
+    const uint32_t slice = (C::TN + split - 1) / split;       // rows of a tile that a rank adds up
+    if (split > 1) cluster_arrive();                          // (waited for before another's memory is written)
     if (warp == C::EPI && lane == 0) {
         info[0] = 0;
         for (int i = 0; i < C::NS; ++i) { mbar_init(&s_full[i], 1); mbar_init(&s_empty[i], 1); }
@@ -256,6 +271,19 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) small_kernel(const __gr
         tmem_relinquish();
         tc_fence_before();
     }
+    const int KB = (p.K + kF8Block - 1) / kF8Block, nb = p.n_tiles;
+    const int kb0 = KB * rank / split, nkb = KB * (rank + 1) / split - kb0;
+    const int step = gridDim.x / split;
+    Walk<C> wk;
+    wk.start(blockIdx.x / split);
+    if (!p.offsets && warp == C::EPI && wk.get(p, cum) && elect_one()) {
+        // dense: the first weights are brought into L2 while the previous grid ends
+        // (L2 is where that grid's writes arrive too, so nothing stale can be read)
+        for (int i = 0; i < min(nkb, 2 * C::NS); ++i) {
+            tma_prefetch_2d(&maps.w0, (kb0 + i) * kF8Block, wk.nt * 128);
+            if (C::GU) tma_prefetch_2d(&maps.w1, (kb0 + i) * kF8Block, wk.nt * 128);
+        }
+    }
     if (!p.early) grid_wait();
     if (p.offsets) build_groups<C>(p, cum);
     __syncthreads();
@@ -265,25 +293,20 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) small_kernel(const __gr
     if (!p.early) grid_launch_dependents();
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(info + 1);
-    const int KB = (p.K + kF8Block - 1) / kF8Block, nb = p.n_tiles;
-    const int kb0 = (int)((int64_t)KB * rank / split), nkb = (int)((int64_t)KB * (rank + 1) / split) - kb0;
-    const int step = gridDim.x / split;
-    Walk<C> wk;
-    wk.start(blockIdx.x / split);
     RowTile tile{0, 0, 0, 0};   // the last tile whose sums are in `part` (split > 1: the only one)
+    bool second = false;
 
     // the sums in `part` -> y or h: a warp per row, 4 columns a lane, the ranks' sums in rank order
     auto emit = [&](const RowTile &t) {
-        const uint32_t base = smem_u32(part);
         const int n = t.nt * 128 + lane * 4;
         for (int j = rank + split * warp; j < t.rows; j += split * C::EPI) {
             float v[C::NW][4];
 #pragma unroll
             for (int w = 0; w < C::NW; ++w) {
-                const uint32_t at = base + ((w * C::TN + j) * 128 + lane * 4) * 4;
-                float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                for (uint32_t r = 0; r < split; ++r) {
-                    const float4 f = ld_cluster_f4(mapa_shared(at, r));
+                const float *at = part + ((w * split * slice + j / split) * 128 + lane * 4);
+                float4 s = *reinterpret_cast<const float4 *>(at);
+                for (uint32_t r = 1; r < split; ++r) {
+                    const float4 f = *reinterpret_cast<const float4 *>(at + r * slice * 128);
                     s.x += f.x; s.y += f.y; s.z += f.z; s.w += f.w;
                 }
                 v[w][0] = s.x; v[w][1] = s.y; v[w][2] = s.z; v[w][3] = s.w;
@@ -402,7 +425,7 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) small_kernel(const __gr
         if (p.early) grid_wait();
         const int w = warp >> 2, q = warp & 3, tid = threadIdx.x & 127;
         const uint32_t taddr = tmem + w * C::TN + ((uint32_t)(q * 32) << 16);
-        float *mine = part + w * C::TN * 128 + tid;
+        float *mine = part + w * split * slice * 128 + tid;
         constexpr int PER = (C::SEG * C::TN + 127) / 128;
         float next[PER];
         // the scales' products of segment g of the tile at hand: [K block][row of a]
@@ -417,7 +440,7 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) small_kernel(const __gr
             }
         };
         uint32_t it = 0, half = 0;
-        bool have = wk.get(p, cum), second = false;
+        bool have = wk.get(p, cum);
         if (have) fetch(0);
         while (have) {
             float2 acc[C::TN / 2];
@@ -471,24 +494,38 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) small_kernel(const __gr
             if (have) fetch(0);
             if (second) named_barrier(3, C::EPI * 32);       // the tile before has been written
             second = true;
-#pragma unroll
-            for (int j = 0; j < C::TN / 2; ++j) {
-                mine[2 * j * 128] = acc[j].x;
-                mine[(2 * j + 1) * 128] = acc[j].y;
-            }
             if (split == 1) {
+#pragma unroll
+                for (int j = 0; j < C::TN / 2; ++j) {
+                    mine[2 * j * 128] = acc[j].x;
+                    mine[(2 * j + 1) * 128] = acc[j].y;
+                }
                 named_barrier(3, C::EPI * 32);
                 emit(tile);
+            } else {
+                // (fewer tiles than clusters: each has one)
+                cluster_wait();                              // every block of the cluster runs
+                // this block's sums into its ring, which its products have left; then row j,
+                // a warp per row, to rank j % split
+                float *own = reinterpret_cast<float *>(smem) + w * C::TN * 128;
+#pragma unroll
+                for (int j = 0; j < C::TN / 2; ++j) {
+                    own[2 * j * 128 + tid] = acc[j].x;
+                    own[(2 * j + 1) * 128 + tid] = acc[j].y;
+                }
+                named_barrier(1 + w, 128);
+                const uint32_t to = smem_u32(part + (w * split + rank) * slice * 128) + lane * 16;
+                for (int j = q; j < tile.rows; j += 4)
+                    st_cluster_f4(mapa_shared(to + j / split * 512, j % split), reinterpret_cast<const float4 *>(own + j * 128)[lane]);
             }
         }
     }
     tc_fence_before();
     __syncthreads();
     if (split > 1) {
-        // (fewer tiles than clusters: each has one)
+        if (warp >= C::EPI || !second) cluster_wait();       // (who has not met the first barrier above)
         cluster_sync_all();
         if (warp < C::EPI) emit(tile);
-        cluster_sync_all();   // no block leaves while another reads its sums
     }
     if (warp == C::EPI + 1) {
         tc_fence_after();
@@ -921,16 +958,13 @@ static int64_t row_tiles_bound(const Fp8Args &a, int tr) {
     return a.M / tr + (a.E + 1 < a.M ? a.E + 1 : a.M);
 }
 
-// Launch as a programmatic dependent of what is before it in the stream (the
-// kernels wait for it before they read anything of theirs).
-static cudaError_t launch_cluster(void (*kernel)(Maps, Params), unsigned grid, unsigned threads, size_t smem, unsigned cluster,
-                                  cudaStream_t s, const Maps &maps, const Params &p) {
+static cudaLaunchConfig_t cluster_config(unsigned grid, unsigned threads, size_t smem, unsigned cluster, cudaStream_t s,
+                                         cudaLaunchAttribute (&attr)[2]) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = cluster;
     attr[0].val.clusterDim.y = 1;
@@ -939,7 +973,48 @@ static cudaError_t launch_cluster(void (*kernel)(Maps, Params), unsigned grid, u
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
+    return cfg;
+}
+// Launch as a programmatic dependent of what is before it in the stream (the
+// kernels wait for it before they read anything of theirs).
+static cudaError_t launch_cluster(void (*kernel)(Maps, Params), unsigned grid, unsigned threads, size_t smem, unsigned cluster,
+                                  cudaStream_t s, const Maps &maps, const Params &p) {
+    cudaLaunchAttribute attr[2];
+    const cudaLaunchConfig_t cfg = cluster_config(grid, threads, smem, cluster, s, attr);
     return cudaLaunchKernelEx(&cfg, kernel, maps, p);
+}
+
+// Ask once a device for the largest share of shared memory, so that C::BLOCKS
+// blocks run on an SM.
+template <class C>
+static cudaError_t prefer_shared() {
+    static std::atomic<uint64_t> asked{0};
+    const uint64_t bit = 1ull << (device_info().device & 63);
+    if (asked.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    const cudaError_t e =
+        cudaFuncSetAttribute(small_kernel<C>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    if (e == cudaSuccess) asked.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
+
+// Clusters of `split` small-tile blocks that the current device runs at once with
+// one block an SM (asked once for each device and split; the answer counts one
+// block an SM whatever the shared memory).
+template <class C>
+static int clusters_at_once(int split, size_t smem) {
+    static std::atomic<int> known[64][C::MAX_SPLIT + 1];
+    std::atomic<int> &k = known[device_info().device & 63][split];
+    int n = k.load(std::memory_order_relaxed);
+    if (n == 0) {
+        cudaLaunchAttribute attr[2];
+        const cudaLaunchConfig_t cfg = cluster_config(split, C::THREADS, smem, split, nullptr, attr);
+        if (cudaOccupancyMaxActiveClusters(&n, small_kernel<C>, &cfg) != cudaSuccess || n < 1) {
+            cudaGetLastError();
+            n = 1;
+        }
+        k.store(n, std::memory_order_relaxed);
+    }
+    return n;
 }
 
 template <class C>
@@ -953,19 +1028,23 @@ static cudaError_t launch_small(const Fp8Args &a, cudaStream_t s) {
     const int64_t rt = row_tiles_bound(a, C::TN), tiles = rt * f8_blocks(a.N), slots = (int64_t)di.num_sms * C::BLOCKS;
     const int KB = (int)f8_blocks(a.K);
     // fewer tiles than blocks: split K so that the blocks fill the SMs, two K blocks each at least
-    int64_t split = slots / tiles;
-    split = split > 8 ? 8 : split;
-    split = split > KB / 2 ? KB / 2 : split;
-    split = split < 1 ? 1 : split;
+    const size_t smem = C::SMEM + (a.offsets ? ((size_t)a.E + 2) * 8 : 0);
+    cudaError_t e = ensure_dynamic_smem((const void *)small_kernel<C>, smem);
+    if (e == cudaSuccess) e = prefer_shared<C>();
+    if (e != cudaSuccess) return e;
+    int split = KB / 2 < C::MAX_SPLIT ? KB / 2 : C::MAX_SPLIT;
+    if (split > slots / tiles) split = (int)(slots / tiles);
+    // (all at once: a cluster's blocks lie within one part of the chip, so that fewer
+    // of them run together than the SMs alone would take; a second wave costs more
+    // than the split gains)
+    while (split > 1 && (int64_t)clusters_at_once<C>(split, smem) * C::BLOCKS < tiles) --split;
+    if (split < 1) split = 1;
     const int64_t clusters = split > 1 || tiles < slots ? tiles : slots;
     if (tiles + slots > 0x7fffffff) return cudaErrorInvalidValue;
     p.row_tiles = (int)rt;
     p.n_tiles = (int)f8_blocks(a.N);
     p.early = a.early;
     p.vec = a.N % 4 == 0 && (reinterpret_cast<uintptr_t>(a.y) & (p.y_bf16 ? 7 : 15)) == 0;
-    const size_t smem = C::SMEM + (a.offsets ? ((size_t)a.E + 2) * 8 : 0);
-    const cudaError_t e = ensure_dynamic_smem((const void *)small_kernel<C>, smem);
-    if (e != cudaSuccess) return e;
     return launch_cluster(small_kernel<C>, (unsigned)(clusters * split), C::THREADS, smem, (unsigned)split, s, maps, p);
 }
 
