@@ -100,7 +100,17 @@ __device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, volatil
         }
     }
 }
-__device__ __forceinline__ float swiglu(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
+// silu(g) u = g / (1 + 2^(-g log2 e)) u: two instructions of the special function
+// unit and four others (off by a few 2^-22 of the value; 2^x past the range gives
+// infinity and so 0, as it should).  Written out once for each value that a thread
+// holds, so its length counts: with the divide's and exponential's own handling of
+// denormals a 128 x 128 tile of h took 7500 clocks, fetching instructions.
+__device__ __forceinline__ float swiglu(float g, float u) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+    return g * r * u;
+}
 
 struct Params {
     const float *sa, *sw0, *sw1;
@@ -840,11 +850,20 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
                 // over the two groups through shared memory
                 const int n = nt * 128 + w * 64;
                 float top = 0.0f;
+                bool past = false;
 #pragma unroll
                 for (int j = 0; j < 32; ++j) {
-                    acc[j].x = n + 2 * j < p.N ? swiglu(acc[j].x, acc[32 + j].x) : 0.0f;
-                    acc[j].y = n + 2 * j < p.N ? swiglu(acc[j].y, acc[32 + j].y) : 0.0f;
-                    top = fmaxf(top, fmaxf(finite_abs(acc[j].x), finite_abs(acc[j].y)));
+                    acc[j].x = swiglu(acc[j].x, acc[32 + j].x);
+                    acc[j].y = swiglu(acc[j].y, acc[32 + j].y);
+                    // (features past N: their W rows are zeros or another expert's)
+                    if (j % 8 == 0 && n + 2 * j >= p.N) past = true;
+                    if (past) acc[j] = make_float2(0.0f, 0.0f);
+                    top = fmaxf(top, fmaxf(fabsf(acc[j].x), fabsf(acc[j].y)));   // (NaN is passed over)
+                }
+                if (top > 3.402823466e38f) {                 // an infinity: the largest finite value
+                    top = 0.0f;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) top = fmaxf(top, fmaxf(finite_abs(acc[j].x), finite_abs(acc[j].y)));
                 }
                 float *t2 = tops + parity * 2 * 128 + lrow;
                 t2[w * 128] = top;
