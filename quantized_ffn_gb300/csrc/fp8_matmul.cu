@@ -78,27 +78,30 @@ __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;
 __device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 template <int R> __device__ __forceinline__ void reg_alloc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
 template <int R> __device__ __forceinline__ void reg_dealloc() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
-// mbar_wait of the large tiles' roles: the barrier is asked without suspending the
+// Whether the barrier's phase is complete, without suspending the thread.
+__device__ __forceinline__ bool bar_test(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+// mbar_wait of the products' roles: the barrier is asked without suspending the
 // thread (a suspended thread is woken hundreds of clocks late, once for every
 // K block on the way from the tensor cores to the sums and back), and the bound
 // is a count of tries: the roles have no registers to spare for the clock.
 __device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, volatile int *abort, int *err) {
-    for (int n = 0;; ++n) {
-        uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(smem_u32(bar)), "r"(parity)
-            : "memory");
-        if (ok) return true;
+    for (int n = 0; !bar_test(bar, parity); ++n)
         if (n > (1 << 26) || ((n & 1023) == 1023 && *abort)) {
             record_error(err, ZFFN_ERR_TIMEOUT);
             *abort = 1;
             return false;
         }
-    }
+    return true;
 }
 // silu(g) u = g / (1 + 2^(-g log2 e)) u: two instructions of the special function
 // unit and four others (off by a few 2^-22 of the value; 2^x past the range gives
@@ -572,8 +575,8 @@ struct LargeCfg {
     static constexpr int EPI = 8;
     static constexpr int THREADS = 384;                      // three warpgroups
     // registers a thread: 168 at launch (what 384 threads can have), then shifted
-    // to the two summing warpgroups: 256 * 224 + 128 * 56 = 384 * 168
-    static constexpr int REGS = 168, REGS_SUM = 224, REGS_REST = 56;
+    // to the two summing warpgroups: 256 * 216 + 128 * 72 = 384 * 168
+    static constexpr int REGS = 168, REGS_SUM = 216, REGS_REST = 72;
     static constexpr int GROUP = 8;                          // dense: row tiles that share a W tile in turn
     // scales: slots of SEG K blocks, [K block][128 rows of a, then 2 of W's blocks]
     static constexpr int SEG = 4, SLOTS = 4, SROW = 136;
@@ -711,29 +714,37 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
         // blocks of rows; GU: gate and up), SEG K blocks at a time, 64 rows a warp
         const int half = (warp - C::EPI - 2) * 64;
         const int nb = (p.N + kF8Block - 1) / kF8Block;
+        // of rows; a tile's first slot says which tile it is (the summing warps do not
+        // walk themselves), and after the last tile one says so.
         uint32_t ck = 0;
         bool ok = true;
-        for (; ok && wk.get(p, cum); wk.t += gridDim.x / C::CTAS) {
+        for (bool more = true; ok && more; wk.t += gridDim.x / C::CTAS) {
+            more = wk.get(p, cum);
             const int b0 = C::GU ? wk.nt : wk.nt * 2, b1 = C::GU ? b0 : min(b0 + 1, nb - 1);
-            for (int i = 0; i < KB && wk.e < p.E; i += C::SEG, ++ck) {
+            const int kbs = more && wk.e < p.E ? KB : 1;     // (tiles without a product: one slot, no scales)
+            for (int i = 0; i < kbs; i += C::SEG, ++ck) {
                 const uint32_t c = ck % C::SLOTS;
                 ok = ck < C::SLOTS || bar_wait(&c_empty[c], ((ck / C::SLOTS) & 1) ^ 1, abort_flag, p.err);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 float *dst = scales + c * C::SLOT;
-                const int kb = min(i + (lane & 3), KB - 1);
-                const float *pa = p.sa + (int64_t)wk.row0 * KB + kb;
-                float f[8];
+                if (i == 0 && half == 0 && lane == 0)
+                    *reinterpret_cast<int4 *>(dst + 132) = make_int4(wk.e, wk.row0, more ? wk.rows : -1, wk.nt);
+                if (more && wk.e < p.E) {
+                    const int kb = min(i + (lane & 3), KB - 1);
+                    const float *pa = p.sa + (int64_t)wk.row0 * KB + kb;
+                    float f[8];
 #pragma unroll
-                for (int r = 0; r < 8; ++r)
-                    f[r] = __ldg(pa + (int64_t)min(128 * rank + half + r * 8 + (lane >> 2), wk.rows - 1) * KB);
-                if (half == 0 && lane < 8) {
-                    const float *pw = C::GU && (lane >> 2) ? p.sw1 : p.sw0;
-                    dst[(lane & 3) * C::SROW + 128 + (lane >> 2)] =
-                        __ldg(pw + ((int64_t)wk.e * nb + ((lane >> 2) ? b1 : b0)) * KB + kb);
+                    for (int r = 0; r < 8; ++r)
+                        f[r] = __ldg(pa + (int64_t)min(128 * rank + half + r * 8 + (lane >> 2), wk.rows - 1) * KB);
+                    if (half == 0 && lane < 8) {
+                        const float *pw = C::GU && (lane >> 2) ? p.sw1 : p.sw0;
+                        dst[(lane & 3) * C::SROW + 128 + (lane >> 2)] =
+                            __ldg(pw + ((int64_t)wk.e * nb + ((lane >> 2) ? b1 : b0)) * KB + kb);
+                    }
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) dst[(lane & 3) * C::SROW + half + r * 8 + (lane >> 2)] = f[r];
                 }
-#pragma unroll
-                for (int r = 0; r < 8; ++r) dst[(lane & 3) * C::SROW + half + r * 8 + (lane >> 2)] = f[r];
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&c_full[c]);
             }
@@ -748,7 +759,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
         uint8_t *out = smem + C::OFF_OUT + warp * C::OUT_BYTES;
         uint32_t it = 0, ck = 0;
         int parity = 0;
-        for (; wk.get(p, cum); wk.t += gridDim.x / C::CTAS) {
+        for (;;) {
+            // which tile
+            if (!__all_sync(0xffffffffu, bar_wait(&c_full[ck % C::SLOTS], (ck / C::SLOTS) & 1, abort_flag, p.err))) break;
+            const int4 tile = *reinterpret_cast<const int4 *>(scales + (ck % C::SLOTS) * C::SLOT + 132);   // e, row0, rows, nt
+            __syncwarp();
+            if (tile.z < 0) break;
+            const int blocks = tile.x < p.E ? KB : 0;
             float2 acc[64];
 #pragma unroll
             for (int j = 0; j < 64; ++j) acc[j] = make_float2(0.0f, 0.0f);
@@ -758,7 +775,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
             float last = 0.0f;
 #pragma unroll
             for (int j = 0; j < 32; ++j) d[1][j] = 0;
-            for (int i = 0; i < KB && wk.e < p.E; ++i, ++it) {
+            if (blocks == 0) {
+                if (lane == 0) mbar_arrive(&c_empty[ck % C::SLOTS]);
+                ++ck;
+            }
+            for (int i = 0; i < blocks; ++i, ++it) {
                 const uint32_t b = it % C::NB, c4 = ck % C::SLOTS, from = taddr + b * 256;
                 if (i % C::SEG == 0) bar_wait(&c_full[c4], (ck / C::SLOTS) & 1, abort_flag, p.err);
                 const float *sc = scales + c4 * C::SLOT + (i % C::SEG) * C::SROW;
@@ -767,7 +788,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
                 __syncwarp();
                 tc_fence_after();
                 tmem_ld_32x32b_x32(from, d[0]);
-                if (i % C::SEG == C::SEG - 1 || i == KB - 1) {
+                if (i % C::SEG == C::SEG - 1 || i == blocks - 1) {
                     if (lane == 0) mbar_arrive(&c_empty[c4]);
                     ++ck;
                 }
@@ -792,9 +813,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
 #pragma unroll
             for (int j = 0; j < 16; ++j) fma2(acc[48 + j], d[1][2 * j], d[1][2 * j + 1], last);
             const int wrow = 128 * rank + q * 32;            // this warp's first row of the tile
-            const int left = wk.rows - wrow;                 // and how many are the tile's
-            const int64_t row = wk.row0 + wrow;
-            const int nt = wk.nt;
+            const int left = tile.z - wrow;                  // and how many are the tile's
+            const int64_t row = tile.y + wrow;
+            const int nt = tile.w;
             // The rows leave by TMA, 32 rows of a box at a time: nothing waits for the
             // stores, which go out at 32 bytes a clock (64 KB a tile of bf16: 2000
             // clocks that overlap with the next tile).  A warp whose rows are not all
@@ -804,7 +825,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
                 return out + box * 32 * C::OUT_BOX + r * C::OUT_BOX +
                        ((C::GU ? chunk ^ ((r >> 1) & 3) : chunk ^ (r & 7)) << 4);
             };
-            auto ready = [&] {   // the boxes sent before have been read
+            auto emptied = [&] {   // the boxes sent before have been read
                 if (lane == 0) bulk_wait_group_read<0>();
                 __syncwarp();
             };
@@ -872,7 +893,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
                 parity ^= 1;
                 const int sp = f8_scale_exp(top);
                 const float inv = pow2f(-sp);
-                ready();
+                emptied();
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     uint32_t u[4];
@@ -889,7 +910,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
             } else {
                 const int n = nt * 256 + w * 128;
                 if (p.y_bf16) {
-                    ready();
+                    emptied();
 #pragma unroll
                     for (int c = 0; c < 16; ++c) {           // 8 columns
                         uint32_t u[4];
@@ -905,7 +926,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
                 } else {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {            // 64 columns
-                        ready();
+                        emptied();
 #pragma unroll
                         for (int c = 0; c < 16; ++c) {
                             const float2 lo = acc[h * 32 + c * 2], hi = acc[h * 32 + c * 2 + 1];
