@@ -72,10 +72,6 @@ __device__ __forceinline__ void fma2(float2 &acc, uint32_t d0, uint32_t d1, floa
         : "r"(d0), "r"(d1), "f"(s0), "f"(s1));
 }
 __device__ __forceinline__ void fma2(float2 &acc, uint32_t d0, uint32_t d1, float s) { fma2(acc, d0, d1, s, s); }
-// Programmatic launch: wait until the grids before this one in the stream are
-// complete and their writes visible; let the next grid's blocks be scheduled.
-__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 template <int R> __device__ __forceinline__ void reg_alloc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
 template <int R> __device__ __forceinline__ void reg_dealloc() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
 // Whether the barrier's phase is complete, without suspending the thread.

@@ -48,6 +48,8 @@ template <typename T, bool VEC, bool WHOLE, int UNITS>
 __global__ void __launch_bounds__(kQuantThreads)
     fp8_quantize_rows_kernel(const T *__restrict__ x, uint8_t *__restrict__ q, float *__restrict__ scale,
                              int64_t units, int cols, int nb) {
+    grid_wait();
+    grid_launch_dependents();
     constexpr int kPer = kQuantThreads / 16;
     const int sub = threadIdx.x & 15;
     const int64_t u0 = (int64_t)blockIdx.x * (kPer * UNITS) + (threadIdx.x >> 4);
@@ -106,6 +108,8 @@ template <typename T>
 __global__ void __launch_bounds__(kQuantThreads)
     fp8_quantize_tiles_kernel(const T *__restrict__ x, uint8_t *__restrict__ q, float *__restrict__ scale,
                               int64_t rows, int cols, int nb) {
+    grid_wait();
+    grid_launch_dependents();
     const int64_t br = blockIdx.x / nb;
     const int b = (int)(blockIdx.x - br * nb);
     const int64_t r0 = br * kF8Block;
@@ -135,6 +139,8 @@ __global__ void __launch_bounds__(kQuantThreads)
 __global__ void __launch_bounds__(256)
     fp8_dequant_kernel(const uint8_t *__restrict__ q, const float *__restrict__ scale,
                        float *__restrict__ out, int64_t rows, int cols, int nb, int block_rows) {
+    grid_wait();
+    grid_launch_dependents();
     const int64_t n = rows * cols;
     for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
         const int64_t r = i / cols;
@@ -155,8 +161,7 @@ cudaError_t quantize(const T *x, uint8_t *q, float *scale, int64_t rows, int64_t
     if (block_rows != 1) {
         const int64_t tiles = f8_blocks(rows) * nb;
         if (tiles > 0x7fffffff) return cudaErrorInvalidValue;
-        fp8_quantize_tiles_kernel<T><<<(unsigned)tiles, kQuantThreads, 0, s>>>(x, q, scale, rows, (int)cols, (int)nb);
-        return cudaGetLastError();
+        return launch_dependent(fp8_quantize_tiles_kernel<T>, dim3((unsigned)tiles), kQuantThreads, 0, 1, s, x, q, scale, rows, cols, nb);
     }
     const int64_t units = rows * nb;
     const bool vec = ((reinterpret_cast<uintptr_t>(x) & 15) | (reinterpret_cast<uintptr_t>(q) & 7)) == 0 && cols % 8 == 0;
@@ -164,11 +169,10 @@ cudaError_t quantize(const T *x, uint8_t *q, float *scale, int64_t rows, int64_t
     const bool few = units < (int64_t)(kQuantThreads / 16) * 4 * 1024;
     const int64_t per = kQuantThreads / 16 * (few ? 1 : 4), grid = (units + per - 1) / per;
     if (grid > 0x7fffffff) return cudaErrorInvalidValue;
-    auto run = [&](auto kernel) { kernel<<<(unsigned)grid, kQuantThreads, 0, s>>>(x, q, scale, units, (int)cols, (int)nb); };
-    if (vec && cols % kF8Block == 0) few ? run(fp8_quantize_rows_kernel<T, true, true, 1>) : run(fp8_quantize_rows_kernel<T, true, true, 4>);
-    else if (vec) few ? run(fp8_quantize_rows_kernel<T, true, false, 1>) : run(fp8_quantize_rows_kernel<T, true, false, 4>);
-    else few ? run(fp8_quantize_rows_kernel<T, false, false, 1>) : run(fp8_quantize_rows_kernel<T, false, false, 4>);
-    return cudaGetLastError();
+    auto run = [&](auto kernel) { return launch_dependent(kernel, dim3((unsigned)grid), kQuantThreads, 0, 1, s, x, q, scale, units, cols, nb); };
+    if (vec && cols % kF8Block == 0) return few ? run(fp8_quantize_rows_kernel<T, true, true, 1>) : run(fp8_quantize_rows_kernel<T, true, true, 4>);
+    if (vec) return few ? run(fp8_quantize_rows_kernel<T, true, false, 1>) : run(fp8_quantize_rows_kernel<T, true, false, 4>);
+    return few ? run(fp8_quantize_rows_kernel<T, false, false, 1>) : run(fp8_quantize_rows_kernel<T, false, false, 4>);
 }
 
 }  // namespace
@@ -183,9 +187,8 @@ cudaError_t launch_fp8_quantize(int dtype, const void *x, uint8_t *q, float *sca
 cudaError_t launch_fp8_dequant(const uint8_t *q, const float *scale, float *out, int64_t rows,
                                int64_t cols, int block_rows, cudaStream_t s) {
     const int64_t n = rows * cols, blocks = (n + 255) / 256;
-    fp8_dequant_kernel<<<(unsigned)(blocks < 65536 ? blocks : 65536), 256, 0, s>>>(
-        q, scale, out, rows, (int)cols, (int)f8_blocks(cols), block_rows);
-    return cudaGetLastError();
+    return launch_dependent(fp8_dequant_kernel, dim3((unsigned)(blocks < 65536 ? blocks : 65536)), 256, 0, 1, s, q, scale, out, rows, cols,
+                            f8_blocks(cols), block_rows);
 }
 
 }  // namespace zffn

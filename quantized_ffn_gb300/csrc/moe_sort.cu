@@ -41,6 +41,8 @@ __global__ void __launch_bounds__(kSortMaxWarps * 32)
     const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int *hist = sm, *total = sm + warps * E, *base = total + E, *scratch = base + E;
     const int rank = CS > 1 ? (int)cluster_ctarank() : 0;
+    grid_wait();
+    grid_launch_dependents();
     // this warp's run of pairs, a multiple of 32 long
     const int64_t all = (int64_t)CS * warps;
     const int64_t run = ((P + all - 1) / all + 31) / 32 * 32;
@@ -190,6 +192,8 @@ __global__ void __launch_bounds__(kRowThreads)
                         const int32_t *__restrict__ row_slot, const int32_t *__restrict__ slot_row, V *__restrict__ xs,
                         uint32_t *__restrict__ xs_scale, int T, int k) {
     __shared__ int32_t rows[64];
+    grid_wait();
+    grid_launch_dependents();
     const int64_t t = blockIdx.x, P = (int64_t)T * k;
     if ((int)threadIdx.x < k) rows[threadIdx.x] = slot_row[t * k + threadIdx.x];
     __syncthreads();
@@ -268,6 +272,8 @@ __global__ void __launch_bounds__(kRowThreads)
                        float *__restrict__ y, int Tn, int H, int k, bool accumulate) {
     __shared__ int32_t row[64];
     __shared__ float wt[64];
+    grid_wait();
+    grid_launch_dependents();
     const int64_t t = blockIdx.x, P = (int64_t)Tn * k;
     if ((int)threadIdx.x < k) {
         const int r = slot_row[t * k + threadIdx.x];
@@ -307,6 +313,8 @@ __global__ void __launch_bounds__(kGradWarps * 32)
     moe_combine_grad_kernel(const float *__restrict__ dy, const T *__restrict__ rows, const int32_t *__restrict__ row_slot,
                             const int32_t *__restrict__ slot_row, const float *__restrict__ weights,
                             T *__restrict__ drows, float *__restrict__ dweights, int Tn, int H, int k) {
+    grid_wait();
+    grid_launch_dependents();
     const int64_t t = blockIdx.x, P = (int64_t)Tn * k;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const float *d = dy + t * H;
@@ -361,30 +369,26 @@ template <typename V>
 cudaError_t dispatch_as(const void *x, int64_t row_bytes, const void *scale, int64_t scale_bytes,
                         const int32_t *row_slot, const int32_t *slot_row, void *xs, void *xs_scale, int T, int k,
                         cudaStream_t s) {
-    moe_dispatch_kernel<V><<<row_grid(T, row_bytes / (int64_t)sizeof(V)), kRowThreads, 0, s>>>(
-        static_cast<const V *>(x), row_bytes / (int64_t)sizeof(V), static_cast<const uint32_t *>(scale), scale_bytes / 4,
-        row_slot, slot_row, static_cast<V *>(xs), static_cast<uint32_t *>(xs_scale), T, k);
-    return cudaGetLastError();
+    const int64_t n = row_bytes / (int64_t)sizeof(V);
+    return launch_dependent(moe_dispatch_kernel<V>, row_grid(T, n), kRowThreads, 0, 1, s, static_cast<const V *>(x), n,
+                            static_cast<const uint32_t *>(scale), scale_bytes / 4, row_slot, slot_row, static_cast<V *>(xs),
+                            static_cast<uint32_t *>(xs_scale), T, k);
 }
 
 template <typename T>
 cudaError_t combine_as(const T *rows, const int32_t *slot_row, const float *weights, float *y, int Tn, int H, int k,
                        bool accumulate, cudaStream_t s) {
     if (((bits(rows) | bits(y)) & 15) == 0 && H % 8 == 0)
-        moe_combine_kernel<T, 8><<<row_grid(Tn, H / 8), kRowThreads, 0, s>>>(rows, slot_row, weights, y, Tn, H, k, accumulate);
-    else
-        moe_combine_kernel<T, 1><<<row_grid(Tn, H), kRowThreads, 0, s>>>(rows, slot_row, weights, y, Tn, H, k, accumulate);
-    return cudaGetLastError();
+        return launch_dependent(moe_combine_kernel<T, 8>, row_grid(Tn, H / 8), kRowThreads, 0, 1, s, rows, slot_row, weights, y, Tn, H, k, accumulate);
+    return launch_dependent(moe_combine_kernel<T, 1>, row_grid(Tn, H), kRowThreads, 0, 1, s, rows, slot_row, weights, y, Tn, H, k, accumulate);
 }
 
 template <typename T>
 cudaError_t grad_as(const float *dy, const T *rows, const int32_t *row_slot, const int32_t *slot_row,
                     const float *weights, T *drows, float *dweights, int Tn, int H, int k, cudaStream_t s) {
     if (((bits(dy) | bits(rows) | bits(drows)) & 15) == 0 && H % 8 == 0)
-        moe_combine_grad_kernel<T, 8><<<Tn, kGradWarps * 32, 0, s>>>(dy, rows, row_slot, slot_row, weights, drows, dweights, Tn, H, k);
-    else
-        moe_combine_grad_kernel<T, 1><<<Tn, kGradWarps * 32, 0, s>>>(dy, rows, row_slot, slot_row, weights, drows, dweights, Tn, H, k);
-    return cudaGetLastError();
+        return launch_dependent(moe_combine_grad_kernel<T, 8>, dim3(Tn), kGradWarps * 32, 0, 1, s, dy, rows, row_slot, slot_row, weights, drows, dweights, Tn, H, k);
+    return launch_dependent(moe_combine_grad_kernel<T, 1>, dim3(Tn), kGradWarps * 32, 0, 1, s, dy, rows, row_slot, slot_row, weights, drows, dweights, Tn, H, k);
 }
 
 }  // namespace
@@ -406,8 +410,7 @@ cudaError_t launch_moe_sort(const int32_t *ids, int32_t *row_slot, int32_t *slot
     const cudaError_t e = ensure_dynamic_smem(fn, (size_t)smem);
     if (e != cudaSuccess) return e;
     if (one) {
-        moe_sort_kernel<1><<<1, warps * 32, smem, s>>>(ids, row_slot, slot_row, offsets, (int)P, E);
-        return cudaGetLastError();
+        return launch_dependent(moe_sort_kernel<1>, dim3(1), warps * 32, smem, 1, s, ids, row_slot, slot_row, offsets, P, E);
     }
     // clusters of more than 8 CTAs have to be asked for, once a device
     static std::atomic<uint64_t> allowed{0};
@@ -417,19 +420,8 @@ cudaError_t launch_moe_sort(const int32_t *ids, int32_t *row_slot, int32_t *slot
         if (a != cudaSuccess) return a;
         allowed.fetch_or(bit, std::memory_order_relaxed);
     }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(kSortCluster);
-    cfg.blockDim = dim3(warps * 32);
-    cfg.dynamicSmemBytes = (size_t)smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = kSortCluster;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, moe_sort_kernel<kSortCluster>, ids, row_slot, slot_row, offsets, (int)P, E);
+    return launch_dependent(moe_sort_kernel<kSortCluster>, dim3(kSortCluster), warps * 32, smem, kSortCluster, s, ids, row_slot, slot_row,
+                            offsets, P, E);
 }
 
 cudaError_t launch_moe_dispatch(const void *x, int64_t row_bytes, const void *scale, int64_t scale_bytes,

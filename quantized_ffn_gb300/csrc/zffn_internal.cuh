@@ -457,6 +457,35 @@ __device__ __forceinline__ void q4k_f16_scales4(uint4 hd, int sb0, uint32_t (&a)
 }
 
 // ---------------------------------------------------------------------------
+// Programmatic launches: the kernel may be scheduled while the grid before it in
+// the stream ends, and waits for it (grid_wait) before it touches anything of the
+// caller's; it lets the next grid be scheduled in turn (grid_launch_dependents).
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// (cluster > 1: a cluster launch)
+template <typename... P, typename... A>
+inline cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, unsigned cluster,
+                                    cudaStream_t s, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
+// ---------------------------------------------------------------------------
 // Host-side launchers (defined in the kernel translation units).
 // ---------------------------------------------------------------------------
 struct DeviceInfo {

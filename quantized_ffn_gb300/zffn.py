@@ -445,7 +445,9 @@ def moe_sort(expert_ids: torch.Tensor, E: int, plan: Optional[MoePlan] = None, s
     shape = T, k = expert_ids.shape
     pi = _ptr(expert_ids, "expert_ids", _I32, shape)
     if plan is None:
-        plan = MoePlan(expert_ids.new_empty(T * k), expert_ids.new_empty(shape), expert_ids.new_empty(E + 1))
+        dev = expert_ids.device
+        plan = MoePlan(torch.empty(T * k, dtype=_I32, device=dev), torch.empty_like(expert_ids),
+                       torch.empty(E + 1, dtype=_I32, device=dev))
     st = (_lib or load()).zffn_moe_sort(
         pi, _ptr(plan[0], "row_slot", _I32, (T * k,)), _ptr(plan[1], "slot_row", _I32, shape),
         _ptr(plan[2], "offsets", _I32, (E + 1,)), T, E, k, _stream(stream))
