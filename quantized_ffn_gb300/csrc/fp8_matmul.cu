@@ -72,6 +72,7 @@ __device__ __forceinline__ void fma2(float2 &acc, uint32_t d0, uint32_t d1, floa
         : "r"(d0), "r"(d1), "f"(s0), "f"(s1));
 }
 __device__ __forceinline__ void fma2(float2 &acc, uint32_t d0, uint32_t d1, float s) { fma2(acc, d0, d1, s, s); }
+template <int N> struct Bytes { static constexpr int value = N; };
 template <int R> __device__ __forceinline__ void reg_alloc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
 template <int R> __device__ __forceinline__ void reg_dealloc() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
 // Whether the barrier's phase is complete, without suspending the thread.
@@ -826,8 +827,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
                 __syncwarp();
             };
             // `boxes` boxes from column n0 on, elements of `elem` bytes
-            auto send = [&](int boxes, int n0, int elem, bool vec) {
-                const int per = C::OUT_BOX / elem;           // columns of a box
+            auto send = [&](int boxes, int n0, auto elem_size, bool vec) {
+                constexpr int elem = decltype(elem_size)::value, per = C::OUT_BOX / elem;   // columns of a box
                 if (vec && left >= 32) {
                     fence_proxy_async_smem();
                     __syncwarp();
@@ -849,14 +850,18 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
                             if (i / CH < left && i % CH * 16 < bytes)
                                 *reinterpret_cast<uint4 *>(y + i / CH * pitch + (int64_t)col * elem + i % CH * 16) =
                                     *reinterpret_cast<const uint4 *>(at(x, i / CH, i % CH));
-                    } else {
-                        for (int i = lane; i < 32 * per; i += 32) {
-                            const int r = i / per, b = i % per * elem;
-                            if (r >= left || b >= bytes) continue;
-                            uint8_t *dst = y + r * pitch + (int64_t)col * elem + b;
-                            const uint8_t *src = at(x, r, b >> 4) + (b & 15);
-                            if (elem == 2) *reinterpret_cast<uint16_t *>(dst) = *reinterpret_cast<const uint16_t *>(src);
-                            else *reinterpret_cast<uint32_t *>(dst) = *reinterpret_cast<const uint32_t *>(src);
+                    } else if constexpr (!C::GU) {
+#pragma unroll
+                        for (int l = 0; l < per / 32; ++l) {
+                            const int b = (lane + 32 * l) * elem;
+                            uint8_t *dst = y + (int64_t)col * elem + b;
+#pragma unroll 8
+                            for (int r = 0; r < 32; ++r) {
+                                const uint8_t *src = at(x, r, b >> 4) + (b & 15);
+                                if (r >= left || b >= bytes) continue;
+                                if constexpr (elem == 2) *reinterpret_cast<uint16_t *>(dst + r * pitch) = *reinterpret_cast<const uint16_t *>(src);
+                                else *reinterpret_cast<uint32_t *>(dst + r * pitch) = *reinterpret_cast<const uint32_t *>(src);
+                            }
                         }
                     }
                 }
@@ -901,7 +906,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
                     *reinterpret_cast<uint4 *>(at(0, lane, c)) = make_uint4(u[0], u[1], u[2], u[3]);
                 }
                 // (N is a multiple of 16 and h 16-byte aligned)
-                send(1, n, 1, true);
+                send(1, n, Bytes<1>{}, true);
                 if (w == 0 && lane < left) p.y_scale[(row + lane) * nb + nt] = pow2f(sp);
             } else {
                 const int n = nt * 256 + w * 128;
@@ -918,7 +923,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
                         }
                         *reinterpret_cast<uint4 *>(at(c >> 3, lane, c & 7)) = make_uint4(u[0], u[1], u[2], u[3]);
                     }
-                    send(2, n, 2, p.vec);
+                    send(2, n, Bytes<2>{}, p.vec);
                 } else {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {            // 64 columns
@@ -928,7 +933,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
                             const float2 lo = acc[h * 32 + c * 2], hi = acc[h * 32 + c * 2 + 1];
                             *reinterpret_cast<float4 *>(at(c >> 3, lane, c & 7)) = make_float4(lo.x, lo.y, hi.x, hi.y);
                         }
-                        send(2, n + h * 64, 4, p.vec);
+                        send(2, n + h * 64, Bytes<4>{}, p.vec);
                     }
                 }
             }
@@ -1128,11 +1133,13 @@ static cudaError_t launch(const Fp8Args &a, cudaStream_t s) {
     // rows a tile: the least of 16, 32, 64 that takes an expert's rows (with some
     // spread over their mean) at once, so that its weights are read once
     const int64_t mean = a.offsets ? ((int64_t)a.M * 3 / 2 + a.E - 1) / a.E : a.M;
-    // many rows: the large tiles, where they fill the SMs at least twice over (a
-    // dense call with fewer splits K instead)
+    // many rows: the large tiles, where there are tiles for half of the SMs at least
+    // (the small ones split K where there are fewer: 1856 rows of 2 experts times 136 x
+    // 5136, 16 large tiles, 26 us; 240 blocks of small ones 12 us)
     const int64_t per = (a.N + LargeCfg<false, GU>::TNW - 1) / LargeCfg<false, GU>::TNW;
+    const int64_t tiles = (a.M + 127) / 128 > a.E ? (a.M + 127) / 128 * per : (int64_t)a.E * per;
     const bool fits = LargeCfg<false, GU>::SMEM + (a.E + 2) * 8 <= device_info().max_smem_optin;   // (E up to about 400)
-    if (a.offsets ? fits && a.M / a.E > 64 : a.M > 64 && (a.M + 127) / 128 * per >= 76) {
+    if ((!a.offsets || fits) && a.M / a.E > 64 && tiles >= device_info().num_sms / 2) {
         // (pairs where few of their rows are past an expert's: 8 experts of 1024 rows
         // 211 -> 201 us, 128 of 256 rows 213 -> 242 us)
         if (a.M / a.E >= (a.offsets ? 1024 : 256)) return launch_large<LargeCfg<true, GU>>(a, s);

@@ -168,14 +168,25 @@ __global__ void __launch_bounds__(kSortMaxWarps * 32)
 // ---------------------------------------------------------------------------
 constexpr int kRowThreads = 128;
 
+// Steps that a thread takes at once, kRowThreads apart: one of 16 bytes, four of
+// less (rows that are not 16-byte multiples), to have as much in flight.
+template <int BYTES> constexpr int kRowSteps = BYTES >= 16 ? 1 : 4;
+
 template <typename V>
 __device__ __forceinline__ void copy_row(const V *__restrict__ src, V *__restrict__ dst, int64_t n, int64_t P,
                                          const int32_t *rows, const int32_t *row_slot, int64_t t, int k) {
-    for (int64_t c = blockIdx.y * kRowThreads + threadIdx.x; c < n; c += gridDim.y * kRowThreads) {
-        const V v = __ldg(src + t * n + c);
+    constexpr int U = kRowSteps<sizeof(V)>;
+    for (int64_t c = (int64_t)blockIdx.y * kRowThreads * U + threadIdx.x; c < n; c += (int64_t)gridDim.y * kRowThreads * U) {
+        V v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (c + u * kRowThreads < n) v[u] = __ldg(src + t * n + c + u * kRowThreads);
         for (int j = 0; j < k; ++j) {
             const int64_t r = rows[j];
-            if (r >= 0 && r < P) dst[r * n + c] = v;
+            if (r < 0 || r >= P) continue;
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (c + u * kRowThreads < n) dst[r * n + c + u * kRowThreads] = v[u];
         }
     }
     // rows of no pair: block t looks after rows t k .. t k + k - 1
@@ -214,9 +225,11 @@ template <int VEC> __device__ __forceinline__ Vec<VEC> load_vec(const float *p) 
             const float4 f = __ldg(reinterpret_cast<const float4 *>(p) + i);
             r.v[4 * i] = f.x; r.v[4 * i + 1] = f.y; r.v[4 * i + 2] = f.z; r.v[4 * i + 3] = f.w;
         }
+    } else if (VEC == 2) {
+        const float2 f = __ldg(reinterpret_cast<const float2 *>(p));
+        r.v[0] = f.x; r.v[VEC - 1] = f.y;
     } else {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) r.v[i] = __ldg(p + i);
+        r.v[0] = __ldg(p);
     }
     return r;
 }
@@ -230,9 +243,11 @@ template <int VEC> __device__ __forceinline__ Vec<VEC> load_vec(const __nv_bfloa
             r.v[2 * i] = __uint_as_float(w[i] << 16);
             r.v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
         }
+    } else if (VEC == 2) {
+        const uint32_t w = __ldg(reinterpret_cast<const uint32_t *>(p));
+        r.v[0] = __uint_as_float(w << 16); r.v[VEC - 1] = __uint_as_float(w & 0xFFFF0000u);
     } else {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) r.v[i] = __bfloat162float(p[i]);
+        r.v[0] = __bfloat162float(p[0]);
     }
     return r;
 }
@@ -241,9 +256,10 @@ template <int VEC> __device__ __forceinline__ void store_vec(float *p, const Vec
 #pragma unroll
         for (int i = 0; i < VEC / 4; ++i)
             reinterpret_cast<float4 *>(p)[i] = make_float4(r.v[4 * i], r.v[4 * i + 1], r.v[4 * i + 2], r.v[4 * i + 3]);
+    } else if (VEC == 2) {
+        *reinterpret_cast<float2 *>(p) = make_float2(r.v[0], r.v[VEC - 1]);
     } else {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) p[i] = r.v[i];
+        p[0] = r.v[0];
     }
 }
 // (one rounding to bf16, to nearest even)
@@ -256,9 +272,10 @@ template <int VEC> __device__ __forceinline__ void store_vec(__nv_bfloat16 *p, c
             w[i] = *reinterpret_cast<const uint32_t *>(&b);
         }
         *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else if (VEC == 2) {
+        *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(r.v[0], r.v[VEC - 1]);
     } else {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) p[i] = __float2bfloat16_rn(r.v[i]);
+        p[0] = __float2bfloat16_rn(r.v[0]);
     }
 }
 
@@ -281,24 +298,30 @@ __global__ void __launch_bounds__(kRowThreads)
         wt[threadIdx.x] = weights ? weights[t * k + threadIdx.x] : 1.0f;
     }
     __syncthreads();
-    for (int c = (blockIdx.y * kRowThreads + threadIdx.x) * VEC; c < H; c += gridDim.y * kRowThreads * VEC) {
-        Vec<VEC> acc;
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) acc.v[i] = 0.0f;
+    constexpr int U = kRowSteps<VEC * (int)sizeof(T)>, APART = kRowThreads * VEC;
+    for (int c = blockIdx.y * APART * U + threadIdx.x * VEC; c < H; c += gridDim.y * APART * U) {
+        Vec<VEC> acc[U];
         float *py = y + t * H + c;
-        if (accumulate) {
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) acc.v[i] = py[i];
-        }
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) acc[u].v[i] = accumulate && c + u * APART < H ? py[u * APART + i] : 0.0f;
 #pragma unroll 8
         for (int j = 0; j < k; ++j) {
             const int r = row[j];
             if (r < 0) continue;
-            const Vec<VEC> v = load_vec<VEC>(rows + (int64_t)r * H + c);
+            const T *pr = rows + (int64_t)r * H + c;
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) acc.v[i] = fmaf(wt[j], v.v[i], acc.v[i]);
+            for (int u = 0; u < U; ++u) {
+                if (c + u * APART >= H) continue;
+                const Vec<VEC> v = load_vec<VEC>(pr + u * APART);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) acc[u].v[i] = fmaf(wt[j], v.v[i], acc[u].v[i]);
+            }
         }
-        store_vec<VEC>(py, acc);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (c + u * APART < H) store_vec<VEC>(py + u * APART, acc[u]);
     }
 }
 
@@ -324,7 +347,7 @@ __global__ void __launch_bounds__(kGradWarps * 32)
         if (r >= 0 && r < P) {
             const float w = drows ? weights[f] : 0.0f;
             float dot = 0.0f;
-#pragma unroll 4
+#pragma unroll (VEC == 8 ? 2 : 8)
             for (int c = lane * VEC; c < H; c += 32 * VEC) {
                 const Vec<VEC> g = load_vec<VEC>(d + c);
                 if (dweights) {
@@ -359,9 +382,9 @@ __global__ void __launch_bounds__(kGradWarps * 32)
 
 inline uintptr_t bits(const void *p) { return reinterpret_cast<uintptr_t>(p); }
 
-// Blocks of a token of n column steps: one step a thread, and at most 16 blocks.
-inline dim3 row_grid(int T, int64_t n) {
-    const int64_t y = (n + kRowThreads - 1) / kRowThreads;
+// Blocks of a token of n column steps, `steps` a thread; at most 16.
+inline dim3 row_grid(int T, int64_t n, int steps) {
+    const int64_t y = (n + kRowThreads * steps - 1) / (kRowThreads * steps);
     return dim3((unsigned)T, (unsigned)(y < 16 ? y : 16));
 }
 
@@ -370,7 +393,7 @@ cudaError_t dispatch_as(const void *x, int64_t row_bytes, const void *scale, int
                         const int32_t *row_slot, const int32_t *slot_row, void *xs, void *xs_scale, int T, int k,
                         cudaStream_t s) {
     const int64_t n = row_bytes / (int64_t)sizeof(V);
-    return launch_dependent(moe_dispatch_kernel<V>, row_grid(T, n), kRowThreads, 0, 1, s, static_cast<const V *>(x), n,
+    return launch_dependent(moe_dispatch_kernel<V>, row_grid(T, n, kRowSteps<sizeof(V)>), kRowThreads, 0, 1, s, static_cast<const V *>(x), n,
                             static_cast<const uint32_t *>(scale), scale_bytes / 4, row_slot, slot_row, static_cast<V *>(xs),
                             static_cast<uint32_t *>(xs_scale), T, k);
 }
@@ -378,17 +401,25 @@ cudaError_t dispatch_as(const void *x, int64_t row_bytes, const void *scale, int
 template <typename T>
 cudaError_t combine_as(const T *rows, const int32_t *slot_row, const float *weights, float *y, int Tn, int H, int k,
                        bool accumulate, cudaStream_t s) {
-    if (((bits(rows) | bits(y)) & 15) == 0 && H % 8 == 0)
-        return launch_dependent(moe_combine_kernel<T, 8>, row_grid(Tn, H / 8), kRowThreads, 0, 1, s, rows, slot_row, weights, y, Tn, H, k, accumulate);
-    return launch_dependent(moe_combine_kernel<T, 1>, row_grid(Tn, H), kRowThreads, 0, 1, s, rows, slot_row, weights, y, Tn, H, k, accumulate);
+    auto run = [&](auto kernel, int vec, int steps) {
+        return launch_dependent(kernel, row_grid(Tn, H / vec, steps), kRowThreads, 0, 1, s, rows, slot_row, weights, y, Tn, H, k, accumulate);
+    };
+    constexpr int E = (int)sizeof(T);
+    if (((bits(rows) | bits(y)) & 15) == 0 && H % 8 == 0) return run(moe_combine_kernel<T, 8>, 8, kRowSteps<8 * E>);
+    if ((bits(rows) & (2 * E - 1)) == 0 && (bits(y) & 7) == 0 && H % 2 == 0) return run(moe_combine_kernel<T, 2>, 2, kRowSteps<2 * E>);
+    return run(moe_combine_kernel<T, 1>, 1, kRowSteps<E>);
 }
 
 template <typename T>
 cudaError_t grad_as(const float *dy, const T *rows, const int32_t *row_slot, const int32_t *slot_row,
                     const float *weights, T *drows, float *dweights, int Tn, int H, int k, cudaStream_t s) {
-    if (((bits(dy) | bits(rows) | bits(drows)) & 15) == 0 && H % 8 == 0)
-        return launch_dependent(moe_combine_grad_kernel<T, 8>, dim3(Tn), kGradWarps * 32, 0, 1, s, dy, rows, row_slot, slot_row, weights, drows, dweights, Tn, H, k);
-    return launch_dependent(moe_combine_grad_kernel<T, 1>, dim3(Tn), kGradWarps * 32, 0, 1, s, dy, rows, row_slot, slot_row, weights, drows, dweights, Tn, H, k);
+    auto run = [&](auto kernel) {
+        return launch_dependent(kernel, dim3(Tn), kGradWarps * 32, 0, 1, s, dy, rows, row_slot, slot_row, weights, drows, dweights, Tn, H, k);
+    };
+    constexpr int E = (int)sizeof(T);
+    if (((bits(dy) | bits(rows) | bits(drows)) & 15) == 0 && H % 8 == 0) return run(moe_combine_grad_kernel<T, 8>);
+    if (((bits(rows) | bits(drows)) & (2 * E - 1)) == 0 && (bits(dy) & 7) == 0 && H % 2 == 0) return run(moe_combine_grad_kernel<T, 2>);
+    return run(moe_combine_grad_kernel<T, 1>);
 }
 
 }  // namespace
@@ -429,6 +460,7 @@ cudaError_t launch_moe_dispatch(const void *x, int64_t row_bytes, const void *sc
                                 int T, int k, cudaStream_t s) {
     const uintptr_t a = bits(x) | bits(xs) | (uintptr_t)row_bytes;   // the widest copy that every row allows
     if ((a & 15) == 0) return dispatch_as<uint4>(x, row_bytes, scale, scale_bytes, row_slot, slot_row, xs, xs_scale, T, k, s);
+    if ((a & 7) == 0) return dispatch_as<uint2>(x, row_bytes, scale, scale_bytes, row_slot, slot_row, xs, xs_scale, T, k, s);
     if ((a & 3) == 0) return dispatch_as<uint32_t>(x, row_bytes, scale, scale_bytes, row_slot, slot_row, xs, xs_scale, T, k, s);
     if ((a & 1) == 0) return dispatch_as<uint16_t>(x, row_bytes, scale, scale_bytes, row_slot, slot_row, xs, xs_scale, T, k, s);
     return dispatch_as<uint8_t>(x, row_bytes, scale, scale_bytes, row_slot, slot_row, xs, xs_scale, T, k, s);

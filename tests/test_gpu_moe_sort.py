@@ -83,7 +83,8 @@ def test_dispatch_of_scales_and_unaligned_rows():
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("kind", ["random", "dropped", "none"])
-@pytest.mark.parametrize("T,E,k,H", [(1, 128, 8, 2048), (5, 4, 3, 1), (37, 60, 5, 1041), (50, 8, 2, 4096), (9, 3, 64, 130), (300, 16, 8, 512)])
+@pytest.mark.parametrize("T,E,k,H", [(1, 128, 8, 2048), (5, 4, 3, 1), (37, 60, 5, 1041), (50, 8, 2, 4096), (9, 3, 64, 130), (300, 16, 8, 512),
+                                     (7, 5, 3, 2026), (3, 2, 2, 9001), (2, 2, 1, 65536)])
 def test_combine_and_gradients(T, E, k, H, kind, dtype):
     rng = np.random.default_rng(T + H)
     ids = make_ids(rng, T, E, k, kind)
