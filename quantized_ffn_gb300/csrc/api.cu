@@ -4,7 +4,7 @@
 // kernels; there is no host fallback.
 #include <mutex>
 
-#include "zffn_internal.cuh"
+#include "launch.cuh"
 #include "formats.h"
 #include "rmsnorm.h"
 #include "router.h"

@@ -2,7 +2,7 @@
 // expert: host-side argument checks and the composition of the launches.
 #include "fp8.h"
 #include "moe_sort.h"
-#include "zffn_internal.cuh"
+#include "launch.cuh"
 
 namespace zffn {
 

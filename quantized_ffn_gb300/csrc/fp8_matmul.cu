@@ -11,7 +11,7 @@
 #include <atomic>
 
 #include "fp8.h"
-#include "zffn_internal.cuh"
+#include "launch.cuh"
 
 namespace zffn {
 namespace f8 {
@@ -999,32 +999,6 @@ static int64_t row_tiles_bound(const Fp8Args &a, int tr) {
     return a.M / tr + (a.E + 1 < a.M ? a.E + 1 : a.M);
 }
 
-static cudaLaunchConfig_t cluster_config(unsigned grid, unsigned threads, size_t smem, unsigned cluster, cudaStream_t s,
-                                         cudaLaunchAttribute (&attr)[2]) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = cluster;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cfg;
-}
-// Launch as a programmatic dependent of what is before it in the stream (the
-// kernels wait for it before they read anything of theirs).
-static cudaError_t launch_cluster(void (*kernel)(Maps, Params), unsigned grid, unsigned threads, size_t smem, unsigned cluster,
-                                  cudaStream_t s, const Maps &maps, const Params &p) {
-    cudaLaunchAttribute attr[2];
-    const cudaLaunchConfig_t cfg = cluster_config(grid, threads, smem, cluster, s, attr);
-    return cudaLaunchKernelEx(&cfg, kernel, maps, p);
-}
-
 // Ask once a device for the largest share of shared memory, so that C::BLOCKS
 // blocks run on an SM.
 template <class C>
@@ -1047,8 +1021,17 @@ static int clusters_at_once(int split, size_t smem) {
     std::atomic<int> &k = known[device_info().device & 63][split];
     int n = k.load(std::memory_order_relaxed);
     if (n == 0) {
-        cudaLaunchAttribute attr[2];
-        const cudaLaunchConfig_t cfg = cluster_config(split, C::THREADS, smem, split, nullptr, attr);
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(split);
+        cfg.blockDim = dim3(C::THREADS);
+        cfg.dynamicSmemBytes = smem;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = split;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
         if (cudaOccupancyMaxActiveClusters(&n, small_kernel<C>, &cfg) != cudaSuccess || n < 1) {
             cudaGetLastError();
             n = 1;
@@ -1086,7 +1069,7 @@ static cudaError_t launch_small(const Fp8Args &a, cudaStream_t s) {
     p.n_tiles = (int)f8_blocks(a.N);
     p.early = a.early;
     p.vec = a.N % 4 == 0 && (reinterpret_cast<uintptr_t>(a.y) & (p.y_bf16 ? 7 : 15)) == 0;
-    return launch_cluster(small_kernel<C>, (unsigned)(clusters * split), C::THREADS, smem, (unsigned)split, s, maps, p);
+    return launch_dependent(small_kernel<C>, dim3((unsigned)(clusters * split)), C::THREADS, smem, (unsigned)split, s, maps, p);
 }
 
 template <class C>
@@ -1125,7 +1108,7 @@ static cudaError_t launch_large(const Fp8Args &a, cudaStream_t s) {
     if (regs != C::REGS) return cudaErrorInvalidConfiguration;
     const cudaError_t e = ensure_dynamic_smem((const void *)large_kernel<C>, smem);
     if (e != cudaSuccess) return e;
-    return launch_cluster(large_kernel<C>, (unsigned)(clusters * C::CTAS), C::THREADS, smem, C::CTAS, s, maps, p);
+    return launch_dependent(large_kernel<C>, dim3((unsigned)(clusters * C::CTAS)), C::THREADS, smem, C::CTAS, s, maps, p);
 }
 
 template <bool GU>

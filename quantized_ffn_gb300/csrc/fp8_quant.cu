@@ -9,7 +9,7 @@
 // rounded once and the result does not depend on how the division is done.
 #include "fp8.h"
 
-#include "zffn_internal.cuh"
+#include "launch.cuh"
 
 namespace zffn {
 

@@ -4,7 +4,7 @@
 
 #include <atomic>
 
-#include "zffn_internal.cuh"
+#include "launch.cuh"
 
 namespace zffn {
 
