@@ -2,7 +2,9 @@
 
 Each translation unit under csrc/ is compiled by nvcc in parallel, then linked
 into quantized_ffn_gb300/_lib/libzffn.so (CUDA runtime linked statically; the
-driver entry point used for TMA descriptors is looked up at run time).
+driver entry point used for TMA descriptors is looked up at run time).  The
+Python binding of the 8-bit entry points (csrc/binding.cpp) is compiled by the
+host compiler against the installed torch into _lib/_zffn_native.so.
 """
 from __future__ import annotations
 
@@ -18,6 +20,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(HERE, "_lib")
 LIB = os.path.join(OUT_DIR, "libzffn.so")
+NATIVE = os.path.join(OUT_DIR, "_zffn_native.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC,
          "--expt-relaxed-constexpr"]
@@ -45,6 +48,23 @@ def _stale(target, deps):
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _native_command():
+    """The host compiler's command line for the binding, with the installed torch's paths."""
+    import sysconfig
+
+    import torch
+
+    home = os.path.dirname(torch.__file__)
+    lib = os.path.join(home, "lib")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")
+    inc = [INCLUDE, os.path.join(home, "include"), os.path.join(home, "include", "torch", "csrc", "api", "include"), cuda,
+           sysconfig.get_paths()["include"]]
+    return [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-w",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *["-I" + i for i in inc],
+            os.path.join(CSRC, "binding.cpp"), "-L" + lib, "-Wl,-rpath," + lib,
+            "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+
+
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     os.makedirs(OUT_DIR, exist_ok=True)
     nvcc = _nvcc()
@@ -56,6 +76,10 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
         if force or _stale(obj, [src] + hdrs):
             cmd = [nvcc, *ARCH, *FLAGS, *extra, "-c", src, "-o", obj]
             jobs.append(cmd)
+    native_tmp = NATIVE + f".{os.getpid()}.tmp"
+    native = force or _stale(NATIVE, [os.path.join(CSRC, "binding.cpp"), os.path.join(INCLUDE, "zffn.h")])
+    if native:
+        jobs.append(_native_command() + ["-o", native_tmp])
     if jobs:
         with cf.ThreadPoolExecutor(max_workers=min(len(jobs), os.cpu_count() or 4)) as ex:
             futs = [ex.submit(subprocess.run, cmd, capture_output=True, text=True) for cmd in jobs]
@@ -64,7 +88,9 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
                 if verbose or r.returncode != 0:
                     sys.stderr.write(r.stdout + r.stderr)
                 if r.returncode != 0:
-                    raise RuntimeError("nvcc failed: " + " ".join(cmd))
+                    raise RuntimeError("the compiler failed: " + " ".join(cmd))
+    if native:
+        os.replace(native_tmp, NATIVE)
     if force or jobs or _stale(LIB, objs):
         tmp = LIB + f".{os.getpid()}.tmp"
         subprocess.check_call([nvcc, *ARCH, "-shared", "-o", tmp, *objs])

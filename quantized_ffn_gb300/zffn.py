@@ -1,4 +1,5 @@
-"""Python binding of libzffn (include/zffn.h): argument marshalling only.
+"""Python binding of libzffn (include/zffn.h): argument marshalling only, for the 8-bit and sorting
+entry points in a native module (csrc/binding.cpp).
 
 Every function takes CUDA tensors, checks dtype/shape/contiguity, and passes
 raw device pointers and the current (or given) CUDA stream to the C ABI.  All
@@ -8,6 +9,8 @@ importing the functions raises -- there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import threading
 from typing import NamedTuple, Optional
@@ -105,18 +108,9 @@ def _check(status: int, what: str):
         raise ZffnError(status, what)
 
 
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-_device = getattr(torch._C, "_cuda_getDevice", None)
-
-
-def _stream(stream: Optional[torch.cuda.Stream]) -> int:
-    """The handle of `stream`, or of the current device's current stream (asked without making a
-    Stream object: a small call is bound by what the host does)."""
-    if stream is not None:
-        return stream.cuda_stream
-    if _raw_stream is None or not torch.cuda.is_initialized():
-        return torch.cuda.current_stream().cuda_stream
-    return _raw_stream(_device())
+def _stream(stream: Optional[torch.cuda.Stream]) -> ctypes.c_void_p:
+    s = stream if stream is not None else torch.cuda.current_stream()
+    return ctypes.c_void_p(s.cuda_stream)
 
 
 def _cuda(t: torch.Tensor, name: str, dtype=None):
@@ -314,68 +308,47 @@ def moe_router_topk(logits: torch.Tensor, top_k: int, expert_ids: Optional[torch
 # too) with one fp32 scale for each block of 128 (include/zffn.h).
 
 DT_F32, DT_BF16 = 0, 1
-_DTYPES = {torch.float32: DT_F32, torch.bfloat16: DT_BF16}
-_F32, _I32, _F8, _U8 = torch.float32, torch.int32, torch.float8_e4m3fn, torch.uint8
-
-
-def _dtype(t: torch.Tensor, name: str) -> int:
-    d = _DTYPES.get(t.dtype)
-    if d is None:
-        raise ValueError(f"{name} must be torch.float32 or torch.bfloat16, got {t.dtype}")
-    return d
-
-
-def _ptr(t: torch.Tensor, name: str, dtype, shape) -> int:
-    """Address of a contiguous CUDA tensor of this type and shape."""
-    if t.dtype is dtype and t.is_cuda and t.shape == shape and t.is_contiguous():
-        return t.data_ptr()
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    return _cuda(t, name, dtype).value
-
-
-def _ptr8(t: torch.Tensor, name: str, shape) -> int:
-    return _ptr(t, name, _U8 if t.dtype is _U8 else _F8, shape)
+NATIVE_PATH = os.path.join(_HERE, "_lib", "_zffn_native.so")
+_native_module = None
+_NATIVE_CALLS = ("zffn_fp8_quantize", "zffn_fp8_dequant", "zffn_fp8_matmul", "zffn_fp8_experts", "zffn_moe_sort",
+                 "zffn_moe_dispatch", "zffn_moe_combine", "zffn_moe_combine_grad", "zffn_moe_swiglu_fp8")
 
 
 def _fail(status: int, what: str):
     raise ZffnError(status, what)
 
 
+def _native():
+    """The native binding, loaded once (raises if it has not been built for this torch)."""
+    global _native_module
+    lib = load()
+    with _lock:
+        if _native_module is None:
+            if not os.path.exists(NATIVE_PATH):
+                raise RuntimeError(
+                    f"{NATIVE_PATH} is missing: build it with quantized_ffn_gb300.build.build()")
+            loader = importlib.machinery.ExtensionFileLoader("_zffn_native", NATIVE_PATH)
+            m = importlib.util.module_from_spec(importlib.util.spec_from_loader("_zffn_native", loader))
+            loader.exec_module(m)
+            if m.torch_version.split("+")[0] != torch.__version__.split("+")[0]:
+                raise RuntimeError(f"{NATIVE_PATH} was built for torch {m.torch_version}, this is {torch.__version__}: "
+                                   "build it again")
+            m.bind(_fail, *(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in _NATIVE_CALLS))
+            _native_module = m
+    return _native_module
+
+
 def fp8_quantize(x: torch.Tensor, block_rows: int = 1, q: Optional[torch.Tensor] = None,
                  scale: Optional[torch.Tensor] = None, stream=None):
     """(q float8_e4m3fn [R, C], scale fp32 [ceil(R / block_rows), ceil(C / 128)]) of x (bf16 or
     fp32 [R, C]): power-of-two scales for blocks of block_rows (1 or 128) x 128."""
-    shape = R, C = x.shape
-    if block_rows != 1 and block_rows != 128:
-        raise ValueError("block_rows must be 1 or 128")
-    blocks = (-(-R // block_rows), -(-C // 128))
-    if q is None:
-        q = torch.empty(shape, dtype=_F8, device=x.device)
-    if scale is None:
-        scale = torch.empty(blocks, dtype=_F32, device=x.device)
-    st = (_lib or load()).zffn_fp8_quantize(
-        _dtype(x, "x"), _ptr(x, "x", x.dtype, shape), _ptr8(q, "q", shape), _ptr(scale, "scale", _F32, blocks),
-        R, C, block_rows, _stream(stream))
-    if st:
-        _fail(st, "zffn_fp8_quantize")
-    return q, scale
+    return (_native_module or _native()).fp8_quantize(x, block_rows, q, scale, stream)
 
 
 def fp8_dequant(q: torch.Tensor, scale: torch.Tensor, block_rows: int = 1,
                 out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """fp32 [R, C]: each e4m3 value times its block's scale."""
-    shape = R, C = q.shape
-    if block_rows != 1 and block_rows != 128:
-        raise ValueError("block_rows must be 1 or 128")
-    if out is None:
-        out = torch.empty(shape, dtype=_F32, device=q.device)
-    st = (_lib or load()).zffn_fp8_dequant(
-        _ptr8(q, "q", shape), _ptr(scale, "scale", _F32, (-(-R // block_rows), -(-C // 128))),
-        _ptr(out, "out", _F32, shape), R, C, block_rows, _stream(stream))
-    if st:
-        _fail(st, "zffn_fp8_dequant")
-    return out
+    return (_native_module or _native()).fp8_dequant(q, scale, block_rows, out, stream)
 
 
 def fp8_matmul(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
@@ -385,23 +358,7 @@ def fp8_matmul(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale:
     a [M, K] (scales [M, K/128]), w [N, K] (scales [N/128, K/128]).  With offsets (int32 [E + 1],
     MoePlan.offsets) w is [E, N, K] and rows offsets[e]:offsets[e + 1] take expert e; rows of no
     expert become 0.  y: given (fp32 or bf16), or made with `dtype`."""
-    M, K = a.shape
-    N = w.shape[-2]
-    bn, bk = -(-N // 128), -(-K // 128)
-    if offsets is None:
-        E, po, ws, ss = 1, None, (N, K), (bn, bk)
-    else:
-        E = w.shape[0]
-        po, ws, ss = _ptr(offsets, "offsets", _I32, (E + 1,)), (E, N, K), (E, bn, bk)
-    if y is None:
-        y = torch.empty((M, N), dtype=dtype, device=a.device)
-    st = (_lib or load()).zffn_fp8_matmul(
-        _ptr8(a, "a", (M, K)), _ptr(a_scale, "a_scale", _F32, (M, bk)), _ptr8(w, "w", ws),
-        _ptr(w_scale, "w_scale", _F32, ss), po, _dtype(y, "y"), _ptr(y, "y", y.dtype, (M, N)), M, N, K, E,
-        _stream(stream))
-    if st:
-        _fail(st, "zffn_fp8_matmul")
-    return y
+    return (_native_module or _native()).fp8_matmul(a, a_scale, w, w_scale, offsets, y, dtype, stream)
 
 
 def fp8_experts(a: torch.Tensor, a_scale: torch.Tensor, Wg: torch.Tensor, sg: torch.Tensor, Wu: torch.Tensor,
@@ -410,24 +367,7 @@ def fp8_experts(a: torch.Tensor, a_scale: torch.Tensor, Wg: torch.Tensor, sg: to
     """y[P, H] = quantise(silu(a Wg^T) * (a Wu^T)) Wd^T on e4m3 weights Wg, Wu [I, H], Wd [H, I]
     with scales for blocks of 128; with offsets the weights are stacked [E, ...] and the rows of
     each expert take its own (rows of no expert become 0)."""
-    P, H = a.shape
-    I = Wg.shape[-2]
-    bi, bh = -(-I // 128), -(-H // 128)
-    if offsets is None:
-        E, po, up, down, s_up, s_down = 1, None, (I, H), (H, I), (bi, bh), (bh, bi)
-    else:
-        E = Wg.shape[0]
-        po = _ptr(offsets, "offsets", _I32, (E + 1,))
-        up, down, s_up, s_down = (E, I, H), (E, H, I), (E, bi, bh), (E, bh, bi)
-    if y is None:
-        y = torch.empty((P, H), dtype=dtype, device=a.device)
-    st = (_lib or load()).zffn_fp8_experts(
-        _ptr8(a, "a", (P, H)), _ptr(a_scale, "a_scale", _F32, (P, bh)), po, _ptr8(Wg, "Wg", up),
-        _ptr(sg, "sg", _F32, s_up), _ptr8(Wu, "Wu", up), _ptr(su, "su", _F32, s_up), _ptr8(Wd, "Wd", down),
-        _ptr(sd, "sd", _F32, s_down), _dtype(y, "y"), _ptr(y, "y", y.dtype, (P, H)), P, H, I, E, _stream(stream))
-    if st:
-        _fail(st, "zffn_fp8_experts")
-    return y
+    return (_native_module or _native()).fp8_experts(a, a_scale, Wg, sg, Wu, su, Wd, sd, offsets, y, dtype, stream)
 
 
 class MoePlan(NamedTuple):
@@ -442,83 +382,28 @@ class MoePlan(NamedTuple):
 def moe_sort(expert_ids: torch.Tensor, E: int, plan: Optional[MoePlan] = None, stream=None) -> MoePlan:
     """The stable sort of expert_ids (int32 [T, top_k], e.g. from moe_router_topk) by expert; ids
     outside [0, E) get no row."""
-    shape = T, k = expert_ids.shape
-    pi = _ptr(expert_ids, "expert_ids", _I32, shape)
-    if plan is None:
-        dev = expert_ids.device
-        plan = MoePlan(torch.empty(T * k, dtype=_I32, device=dev), torch.empty_like(expert_ids),
-                       torch.empty(E + 1, dtype=_I32, device=dev))
-    st = (_lib or load()).zffn_moe_sort(
-        pi, _ptr(plan[0], "row_slot", _I32, (T * k,)), _ptr(plan[1], "slot_row", _I32, shape),
-        _ptr(plan[2], "offsets", _I32, (E + 1,)), T, E, k, _stream(stream))
-    if st:
-        _fail(st, "zffn_moe_sort")
-    return plan
+    return tuple.__new__(MoePlan, (_native_module or _native()).moe_sort(expert_ids, E, plan, stream))
 
 
 def moe_dispatch(x: torch.Tensor, plan: MoePlan, scale: Optional[torch.Tensor] = None,
                  out: Optional[torch.Tensor] = None, scale_out: Optional[torch.Tensor] = None, stream=None):
     """xs[T * top_k, H]: every token's row of x (any type) at its sorted places, 0 in rows of no
     pair.  With scale (fp32 [T, C], the scales of 8-bit rows) returns (xs, scales moved alike)."""
-    T, H = x.shape
-    slot_row = plan[1]
-    k = slot_row.shape[1]
-    P = T * k
-    if out is None:
-        out = torch.empty((P, H), dtype=x.dtype, device=x.device)
-    C, ps, pso = 0, None, None
-    if scale is not None:
-        C = scale.shape[1]
-        if scale_out is None:
-            scale_out = torch.empty((P, C), dtype=_F32, device=x.device)
-        ps, pso = _ptr(scale, "scale", _F32, (T, C)), _ptr(scale_out, "scale_out", _F32, (P, C))
-    st = (_lib or load()).zffn_moe_dispatch(
-        _ptr(x, "x", x.dtype, (T, H)), H * x.element_size(), ps, C, _ptr(plan[0], "row_slot", _I32, (P,)),
-        _ptr(slot_row, "slot_row", _I32, (T, k)), _ptr(out, "out", x.dtype, (P, H)), pso, T, k, _stream(stream))
-    if st:
-        _fail(st, "zffn_moe_dispatch")
-    return out if scale is None else (out, scale_out)
+    return (_native_module or _native()).moe_dispatch(x, plan, scale, out, scale_out, stream)
 
 
 def moe_combine(rows: torch.Tensor, plan: MoePlan, weights: Optional[torch.Tensor] = None,
                 y: Optional[torch.Tensor] = None, accumulate: bool = False, stream=None) -> torch.Tensor:
     """y[T, H] fp32 (+)= sum_j weights[t, j] rows[row of (t, j)] (rows bf16 or fp32 [T * top_k, H];
     weights fp32 [T, top_k], or None for ones: the gradient of moe_dispatch)."""
-    slot_row = plan[1]
-    T, k = slot_row.shape
-    H = rows.shape[1]
-    if y is None:
-        if accumulate:
-            raise ValueError("accumulate=True needs y")
-        y = torch.empty((T, H), dtype=_F32, device=rows.device)
-    st = (_lib or load()).zffn_moe_combine(
-        _dtype(rows, "rows"), _ptr(rows, "rows", rows.dtype, (T * k, H)), _ptr(slot_row, "slot_row", _I32, (T, k)),
-        None if weights is None else _ptr(weights, "weights", _F32, (T, k)), _ptr(y, "y", _F32, (T, H)), T, H, k,
-        1 if accumulate else 0, _stream(stream))
-    if st:
-        _fail(st, "zffn_moe_combine")
-    return y
+    return (_native_module or _native()).moe_combine(rows, plan, weights, y, accumulate, stream)
 
 
 def moe_combine_grad(dy: torch.Tensor, rows: torch.Tensor, plan: MoePlan, weights: torch.Tensor,
                      drows: Optional[torch.Tensor] = None, dweights: Optional[torch.Tensor] = None, stream=None):
     """(drows [T * top_k, H] of rows' type, dweights fp32 [T, top_k]): the gradients of
     moe_combine(rows, plan, weights) for dy fp32 [T, H]; drows is 0 in rows of no pair."""
-    slot_row = plan[1]
-    T, k = slot_row.shape
-    H = rows.shape[1]
-    if drows is None:
-        drows = torch.empty_like(rows)
-    if dweights is None:
-        dweights = torch.empty((T, k), dtype=_F32, device=rows.device)
-    st = (_lib or load()).zffn_moe_combine_grad(
-        _dtype(rows, "rows"), _ptr(dy, "dy", _F32, (T, H)), _ptr(rows, "rows", rows.dtype, (T * k, H)),
-        _ptr(plan[0], "row_slot", _I32, (T * k,)), _ptr(slot_row, "slot_row", _I32, (T, k)),
-        _ptr(weights, "weights", _F32, (T, k)), _ptr(drows, "drows", rows.dtype, (T * k, H)),
-        _ptr(dweights, "dweights", _F32, (T, k)), T, H, k, _stream(stream))
-    if st:
-        _fail(st, "zffn_moe_combine_grad")
-    return drows, dweights
+    return (_native_module or _native()).moe_combine_grad(dy, rows, plan, weights, drows, dweights, stream)
 
 
 def moe_swiglu_fp8(x: torch.Tensor, expert_ids: torch.Tensor, expert_weights: torch.Tensor, Wg: torch.Tensor,
@@ -526,23 +411,8 @@ def moe_swiglu_fp8(x: torch.Tensor, expert_ids: torch.Tensor, expert_weights: to
                    y: Optional[torch.Tensor] = None, accumulate: bool = False, stream=None) -> torch.Tensor:
     """Routed experts on e4m3 weights: y[T, H] fp32 (+)= sum_j w[t, j] FFN_{ids[t, j]}(quantise(x[t])),
     x bf16 [T, H], weights stacked [E, ...] as for fp8_experts."""
-    T, H = x.shape
-    E, I, _ = Wg.shape
-    k = expert_ids.shape[1]
-    if y is None:
-        if accumulate:
-            raise ValueError("accumulate=True needs y")
-        y = torch.empty((T, H), dtype=_F32, device=x.device)
-    bi, bh = -(-I // 128), -(-H // 128)
-    st = (_lib or load()).zffn_moe_swiglu_fp8(
-        _ptr(x, "x", torch.bfloat16, (T, H)), _ptr(expert_ids, "expert_ids", _I32, (T, k)),
-        _ptr(expert_weights, "expert_weights", _F32, (T, k)), _ptr8(Wg, "Wg", (E, I, H)), _ptr(sg, "sg", _F32, (E, bi, bh)),
-        _ptr8(Wu, "Wu", (E, I, H)), _ptr(su, "su", _F32, (E, bi, bh)), _ptr8(Wd, "Wd", (E, H, I)),
-        _ptr(sd, "sd", _F32, (E, bh, bi)), _ptr(y, "y", _F32, (T, H)), T, H, I, E, k, 1 if accumulate else 0,
-        _stream(stream))
-    if st:
-        _fail(st, "zffn_moe_swiglu_fp8")
-    return y
+    return (_native_module or _native()).moe_swiglu_fp8(x, expert_ids, expert_weights, Wg, sg, Wu, su, Wd, sd, y,
+                                                        accumulate, stream)
 
 
 def _host(t: torch.Tensor, name: str, dtype, shape):

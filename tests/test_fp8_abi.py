@@ -117,6 +117,23 @@ def test_python_checks_shapes():
         zffn.moe_sort(torch.zeros((2, 2), dtype=torch.int32), 4)                      # not on the GPU
 
 
+def test_binding_checks_its_arguments():
+    plan = zffn.MoePlan(torch.zeros(4).int(), torch.zeros((2, 2)).int(), torch.zeros(3).int())
+    rows = torch.zeros((4, 8))
+    for bad in (lambda: zffn.fp8_quantize([1.0, 2.0]), lambda: zffn.fp8_quantize(torch.zeros(8)),
+                lambda: zffn.moe_combine(rows, (plan[0], plan[1])), lambda: zffn.moe_combine(rows, plan, accumulate=True),
+                lambda: zffn.moe_combine(rows.double(), plan), lambda: zffn.moe_dispatch(torch.zeros((3, 8)), plan),
+                lambda: zffn.moe_combine_grad(torch.zeros((2, 7)), rows, plan, torch.zeros((2, 2))),
+                lambda: zffn.fp8_matmul(torch.zeros((4, 256)).to(torch.float8_e4m3fn), torch.zeros((4, 2)),
+                                        torch.zeros((8, 256)).to(torch.float8_e4m3fn), torch.zeros((1, 2)), dtype="float32"),
+                lambda: zffn.fp8_matmul(torch.zeros((4, 256)), torch.zeros((4, 2)), torch.zeros((8, 256)), torch.zeros((1, 2))),
+                lambda: zffn.moe_sort(torch.zeros((2, 2), dtype=torch.int64), 4)):
+        with pytest.raises(ValueError):
+            bad()
+    with pytest.raises(TypeError):
+        zffn._native().moe_sort(plan[1])
+
+
 # ---- the reference forms ---------------------------------------------------------------------
 
 def test_reference_byte_values_are_torch_float8():
