@@ -481,7 +481,7 @@ zffn_status zffn_swiglu_q4k_token_static(const void *x, const void *Wg, const vo
                                          const void *Wd, float *y, int H, int I, void *stream);
 
 /* Allocate (or grow) the current device's workspace for calls up to the given
- * sizes, so that later calls allocate nothing (call it before capturing calls
+ * sizes (of the Q4_K and of the 8-bit entry points), so that later calls allocate nothing (call it before capturing calls
  * into a CUDA graph).  Calls that share a device share its workspace: issue
  * them on one stream, or order them, since concurrent calls race on it.
  * Errors: INVALID_ARG (a size < 1), NO_WORKSPACE. */

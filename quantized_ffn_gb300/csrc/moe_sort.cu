@@ -164,7 +164,8 @@ __global__ void __launch_bounds__(kSortMaxWarps * 32)
 
 // ---------------------------------------------------------------------------
 // Rows to their sorted places.  A thread block per token and share of its row,
-// which is read once and written to each of its places.  Bound by HBM writes.
+// which is read once and written to each of its places.  Bound by HBM writes: 32768
+// rows of 4 KB (8 of each token) take 25.5 us, 5.9 TB/s.
 // ---------------------------------------------------------------------------
 constexpr int kRowThreads = 128;
 
@@ -303,7 +304,8 @@ template <int VEC> __device__ __forceinline__ void store_vec(__nv_bfloat16 *p, c
 
 // ---------------------------------------------------------------------------
 // Sorted rows back to tokens: a thread block per token and share of its columns,
-// fp32 sums over the slots in order.  Bound by HBM reads.
+// fp32 sums over the slots in order.  Bound by HBM reads: 32768 rows of 2048 bf16
+// to 4096 of fp32 take 26.8 us, 6.3 TB/s.
 // ---------------------------------------------------------------------------
 template <typename T, int VEC>
 __global__ void __launch_bounds__(kRowThreads, VEC == 8 ? 12 : 8)   // (registers for the loads in flight: without it 31 us)
@@ -367,7 +369,8 @@ __global__ void __launch_bounds__(kRowThreads, VEC == 8 ? 12 : 8)   // (register
 
 // ---------------------------------------------------------------------------
 // Gradients of the combine: a warp per (token, slot); the token's dy row is
-// shared by the block's warps through L1.  Bound by HBM.
+// shared by the block's warps through L1.  Bound by HBM: 32768 rows of 2048 bf16
+// take 48 us, 6.3 TB/s.
 // ---------------------------------------------------------------------------
 constexpr int kGradWarps = 8;
 
