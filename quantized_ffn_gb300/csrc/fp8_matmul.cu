@@ -1129,16 +1129,18 @@ static cudaError_t launch(const Fp8Args &a, cudaStream_t s) {
     // 5136, 16 large tiles, 26 us; 240 blocks of small ones 12 us)
     const int64_t per = (a.N + LargeCfg<false, GU>::TNW - 1) / LargeCfg<false, GU>::TNW;
     const int64_t tiles = (a.M + 127) / 128 > a.E ? (a.M + 127) / 128 * per : (int64_t)a.E * per;
-    const bool fits = LargeCfg<false, GU>::SMEM + (a.E + 2) * 8 <= device_info().max_smem_optin;   // (E up to about 400)
-    if ((!a.offsets || fits) && a.M / a.E > 64 && tiles >= device_info().num_sms / 2) {
+    // (whether the table of the experts' rows fits beside the tiles: gate/up up to 930 experts)
+    const int room = device_info().max_smem_optin - (a.offsets ? (a.E + 2) * 8 : 0);
+    if (LargeCfg<false, GU>::SMEM <= room && LargeCfg<true, GU>::SMEM <= room && a.M / a.E > 64 && tiles >= device_info().num_sms / 2) {
         // (pairs where few of their rows are past an expert's: 8 experts of 1024 rows
         // 211 -> 201 us, 128 of 256 rows 213 -> 242 us)
         if (a.M / a.E >= (a.offsets ? 1024 : 256)) return launch_large<LargeCfg<true, GU>>(a, s);
         return launch_large<LargeCfg<false, GU>>(a, s);
     }
-    if (mean <= 16) return launch_small<SmallCfg<16, GU>>(a, s);
-    if (mean <= 32) return launch_small<SmallCfg<32, GU>>(a, s);
-    return launch_small<SmallCfg<64, GU>>(a, s);
+    // (gate/up tiles of 32 rows have room for 622 experts' table, of 64 rows for 3954's)
+    if (mean > 16 && mean <= 32 && SmallCfg<32, GU>::SMEM <= room) return launch_small<SmallCfg<32, GU>>(a, s);
+    if (mean > 16 && SmallCfg<64, GU>::SMEM <= room) return launch_small<SmallCfg<64, GU>>(a, s);
+    return launch_small<SmallCfg<16, GU>>(a, s);
 }
 
 }  // namespace f8

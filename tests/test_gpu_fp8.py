@@ -328,6 +328,19 @@ def test_experts_of_large_tiles(P, H, I, kind):
         assert np.all(np.abs(y.double().cpu().numpy() - want) <= tol + 1e-37)
 
 
+@pytest.mark.parametrize("P,H,I,E", [(12000, 144, 32, 1000), (3000, 32, 16, 4096), (130000, 32, 16, 4096)])
+def test_experts_of_many_experts(P, H, I, E):
+    # the table of the experts' rows takes shared memory beside the tiles
+    rng = np.random.default_rng(P + E)
+    t = expert_inputs(rng, P, H, I, E)
+    cut = split_rows(rng, P, E, "random")
+    a, sa, wg, sg, wu, su, wd, sd = t
+    y = zffn.fp8_experts(f8(a), f32(sa), f8(wg), f32(sg), f8(wu), f32(su), f8(wd), f32(sd), offsets=dev(cut), dtype=torch.float32)
+    want, tol = experts_ref(*t, cut)
+    assert np.all(np.abs(y.double().cpu().numpy() - want) <= tol + 1e-37)
+    assert zffn.get_device_error() == zffn.OK
+
+
 def test_routed_layer_end_to_end():
     # router -> routed block against the oracle's router and the steps in 64 bits; the sum over slots
     # adds the bf16 rows' half step and k fp32 steps
