@@ -403,6 +403,7 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) small_kernel(const __gr
     } else if (warp == C::EPI + 1) {
         // ---- MMA issuer
         constexpr uint32_t idesc = idesc_f8_f32(128, C::TN);
+        if (p.early) grid_wait();   // (the wait for the previous grid is not one of the bounded ones)
         uint32_t it = 0;
         bool ok = true;
         for (; ok && wk.get(p, cum); wk.t += step) {
