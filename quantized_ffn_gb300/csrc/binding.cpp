@@ -10,12 +10,15 @@
 #include <Python.h>
 
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 #include <torch/version.h>
 
+#include <optional>
 #include <sstream>
 #include <stdexcept>
 #include <string>
@@ -94,15 +97,26 @@ void dims(const at::Tensor &t, const char *name, int n) {
     if (t.dim() != n) throw ValueError(std::string(name) + " must have " + std::to_string(n) + " dimensions, got " + shape_text(t.sizes()));
 }
 
-void *stream_of(PyObject *stream) {
-    if (stream == Py_None) return c10::cuda::getCurrentCUDAStream().stream();
-    PyObject *h = PyObject_GetAttrString(stream, "cuda_stream");
-    if (!h) throw Raised{};
-    void *s = PyLong_AsVoidPtr(h);
-    Py_DECREF(h);
-    if (PyErr_Occurred()) throw Raised{};
-    return s;
-}
+// The stream of a call: the given one, else the current one.  While it lives a given
+// stream is the current one, so that the outputs made for the call come from that
+// stream's memory (a block that another stream has let go of may still be written by
+// kernels there).
+struct Stream {
+    std::optional<c10::cuda::CUDAStreamGuard> guard;
+    void *s;
+    explicit Stream(PyObject *stream) {
+        if (stream == Py_None) {
+            s = c10::cuda::getCurrentCUDAStream().stream();
+            return;
+        }
+        PyObject *h = PyObject_GetAttrString(stream, "cuda_stream");
+        if (!h) throw Raised{};
+        s = PyLong_AsVoidPtr(h);
+        Py_DECREF(h);
+        if (PyErr_Occurred()) throw Raised{};
+        guard.emplace(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(s), c10::cuda::current_device()));
+    }
+};
 
 // The given output, or a new one like `like` (kept alive in `made`).
 struct Output {
@@ -167,11 +181,11 @@ PyObject *fp8_quantize(PyObject *const *a) {
     const int dtype = dtype_of(x, "x");
     const void *px = place(x, "x");
     const int64_t sc[2] = {(R + block_rows - 1) / block_rows, blocks(C)};
+    const Stream on(a[4]);
     Output q(a[2], "q", x.sizes(), kF8, x), s(a[3], "scale", sc, kF32, x);
     void *pq = ptr(q.t, "q", q.t.scalar_type() == kU8 ? kU8 : kF8, x.sizes());
     float *ps = static_cast<float *>(ptr(s.t, "scale", kF32, sc));
-    void *st = stream_of(a[4]);
-    call("zffn_fp8_quantize", [&] { return api.quantize(dtype, px, pq, ps, R, C, block_rows, st); });
+    call("zffn_fp8_quantize", [&] { return api.quantize(dtype, px, pq, ps, R, C, block_rows, on.s); });
     return pair(q.object(), s.object());
 }
 
@@ -185,10 +199,10 @@ PyObject *fp8_dequant(PyObject *const *a) {
     const int64_t sc[2] = {(R + block_rows - 1) / block_rows, blocks(C)};
     const void *pq = f8(a[0], "q", q.sizes());
     const float *ps = f32(a[1], "scale", sc);
+    const Stream on(a[4]);
     Output out(a[3], "out", q.sizes(), kF32, q);
     float *po = static_cast<float *>(ptr(out.t, "out", kF32, q.sizes()));
-    void *st = stream_of(a[4]);
-    call("zffn_fp8_dequant", [&] { return api.dequant(pq, ps, po, R, C, block_rows, st); });
+    call("zffn_fp8_dequant", [&] { return api.dequant(pq, ps, po, R, C, block_rows, on.s); });
     return out.object();
 }
 
@@ -206,12 +220,12 @@ PyObject *fp8_matmul(PyObject *const *a) {
     const void *pw = f8(a[2], "w", Sizes(ws + skip, 3 - skip));
     const float *pws = f32(a[3], "w_scale", Sizes(ss + skip, 3 - skip));
     const int32_t *po = grouped ? i32(a[4], "offsets", os) : nullptr;
+    const Stream on(a[7]);
     Output y(a[5], "y", ys, a[5] == Py_None ? type_of(a[6]) : kF32, x);
     const int yd = dtype_of(y.t, "y");
     void *py = ptr(y.t, "y", y.t.scalar_type(), ys);
     const int m = narrow(M, "M"), n = narrow(N, "N"), k = narrow(K, "K"), e = narrow(E, "E");
-    void *st = stream_of(a[7]);
-    call("zffn_fp8_matmul", [&] { return api.matmul(px, pxs, pw, pws, po, yd, py, m, n, k, e, st); });
+    call("zffn_fp8_matmul", [&] { return api.matmul(px, pxs, pw, pws, po, yd, py, m, n, k, e, on.s); });
     return y.object();
 }
 
@@ -248,12 +262,12 @@ PyObject *fp8_experts(PyObject *const *a) {
     const void *px = f8(a[0], "a", x.sizes());
     const float *pxs = f32(a[1], "a_scale", as);
     const int32_t *po = grouped ? i32(a[8], "offsets", os) : nullptr;
+    const Stream on(a[11]);
     Output y(a[9], "y", x.sizes(), a[9] == Py_None ? type_of(a[10]) : kF32, x);
     const int yd = dtype_of(y.t, "y");
     void *py = ptr(y.t, "y", y.t.scalar_type(), x.sizes());
     const int p = narrow(P, "P"), h = narrow(H, "H"), i = narrow(w.I, "I"), e = narrow(w.E, "E");
-    void *st = stream_of(a[11]);
-    call("zffn_fp8_experts", [&] { return api.experts(px, pxs, po, w.wg, w.sg, w.wu, w.su, w.wd, w.sd, yd, py, p, h, i, e, st); });
+    call("zffn_fp8_experts", [&] { return api.experts(px, pxs, po, w.wg, w.sg, w.wu, w.su, w.wd, w.sd, yd, py, p, h, i, e, on.s); });
     return y.object();
 }
 
@@ -266,6 +280,7 @@ PyObject *moe_sort(PyObject *const *a) {
     const int64_t rs[1] = {T * k}, os[1] = {E < 0 ? 0 : (int64_t)E + 1};
     const int32_t *pi = i32(a[0], "expert_ids", ids.sizes());
     const bool given = a[2] != Py_None;
+    const Stream on(a[3]);
     Output row_slot(given ? plan_item(a[2], 0) : Py_None, "row_slot", rs, kI32, ids);
     Output slot_row(given ? plan_item(a[2], 1) : Py_None, "slot_row", ids.sizes(), kI32, ids);
     Output offsets(given ? plan_item(a[2], 2) : Py_None, "offsets", os, kI32, ids);
@@ -273,8 +288,7 @@ PyObject *moe_sort(PyObject *const *a) {
             *ps = static_cast<int32_t *>(ptr(slot_row.t, "slot_row", kI32, ids.sizes())),
             *po = static_cast<int32_t *>(ptr(offsets.t, "offsets", kI32, os));
     const int t = narrow(T, "T"), kk = narrow(k, "top_k");
-    void *st = stream_of(a[3]);
-    call("zffn_moe_sort", [&] { return api.sort(pi, pr, ps, po, t, E, kk, st); });
+    call("zffn_moe_sort", [&] { return api.sort(pi, pr, ps, po, t, E, kk, on.s); });
     PyObject *out = PyTuple_New(3);
     if (!out) throw Raised{};
     const Output *all[3] = {&row_slot, &slot_row, &offsets};
@@ -304,13 +318,13 @@ PyObject *moe_dispatch(PyObject *const *a) {
     const int64_t rs[1] = {P}, ss[2] = {T, k}, xs[2] = {P, H};
     const void *px = place(x, "x");
     const int32_t *pr = i32(plan_item(a[1], 0), "row_slot", rs), *ps = i32(plan_item(a[1], 1), "slot_row", ss);
+    const Stream on(a[5]);
     Output out(a[3], "out", xs, x.scalar_type(), x);
     void *po = ptr(out.t, "out", x.scalar_type(), xs);
     const int t = narrow(T, "T"), kk = narrow(k, "top_k");
     const int64_t bytes = H * (int64_t)x.element_size();
-    void *st = stream_of(a[5]);
     if (a[2] == Py_None) {
-        call("zffn_moe_dispatch", [&] { return api.dispatch(px, bytes, nullptr, 0, pr, ps, po, nullptr, t, kk, st); });
+        call("zffn_moe_dispatch", [&] { return api.dispatch(px, bytes, nullptr, 0, pr, ps, po, nullptr, t, kk, on.s); });
         return out.object();
     }
     const at::Tensor &sc = tensor(a[2], "scale");
@@ -319,7 +333,7 @@ PyObject *moe_dispatch(PyObject *const *a) {
     const float *pc = f32(a[2], "scale", cs);
     Output sout(a[4], "scale_out", cos, kF32, x);
     float *pco = static_cast<float *>(ptr(sout.t, "scale_out", kF32, cos));
-    call("zffn_moe_dispatch", [&] { return api.dispatch(px, bytes, pc, C, pr, ps, po, pco, t, kk, st); });
+    call("zffn_moe_dispatch", [&] { return api.dispatch(px, bytes, pc, C, pr, ps, po, pco, t, kk, on.s); });
     return pair(out.object(), sout.object());
 }
 
@@ -335,11 +349,11 @@ PyObject *moe_combine(PyObject *const *a) {
     const void *pr = ptr(r, "rows", r.scalar_type(), rs);
     const int32_t *ps = i32(plan_item(a[1], 1), "slot_row", s.sizes());
     const float *pw = a[2] == Py_None ? nullptr : f32(a[2], "weights", s.sizes());
+    const Stream on(a[5]);
     Output y(a[3], "y", ys, kF32, r);
     float *py = static_cast<float *>(ptr(y.t, "y", kF32, ys));
     const int t = narrow(T, "T"), h = narrow(H, "H"), kk = narrow(k, "top_k");
-    void *st = stream_of(a[5]);
-    call("zffn_moe_combine", [&] { return api.combine(dtype, pr, ps, pw, py, t, h, kk, accumulate, st); });
+    call("zffn_moe_combine", [&] { return api.combine(dtype, pr, ps, pw, py, t, h, kk, accumulate, on.s); });
     return y.object();
 }
 
@@ -353,12 +367,12 @@ PyObject *moe_combine_grad(PyObject *const *a) {
     const void *pr = ptr(r, "rows", r.scalar_type(), rs);
     const int32_t *pn = i32(plan_item(a[2], 0), "row_slot", ns), *ps = i32(plan_item(a[2], 1), "slot_row", s.sizes());
     const float *pw = f32(a[3], "weights", s.sizes());
+    const Stream on(a[6]);
     Output dr(a[4], "drows", rs, r.scalar_type(), r), dw(a[5], "dweights", s.sizes(), kF32, r);
     void *pdr = ptr(dr.t, "drows", r.scalar_type(), rs);
     float *pdw = static_cast<float *>(ptr(dw.t, "dweights", kF32, s.sizes()));
     const int t = narrow(T, "T"), h = narrow(H, "H"), kk = narrow(k, "top_k");
-    void *st = stream_of(a[6]);
-    call("zffn_moe_combine_grad", [&] { return api.combine_grad(dtype, pd, pr, pn, ps, pw, pdr, pdw, t, h, kk, st); });
+    call("zffn_moe_combine_grad", [&] { return api.combine_grad(dtype, pd, pr, pn, ps, pw, pdr, pdw, t, h, kk, on.s); });
     return pair(dr.object(), dw.object());
 }
 
@@ -375,11 +389,11 @@ PyObject *moe_swiglu_fp8(PyObject *const *a) {
     const void *px = ptr(x, "x", kBF16, x.sizes());
     const int32_t *pi = i32(a[1], "expert_ids", ss);
     const float *pw = f32(a[2], "expert_weights", ss);
+    const Stream on(a[11]);
     Output y(a[9], "y", x.sizes(), kF32, x);
     float *py = static_cast<float *>(ptr(y.t, "y", kF32, x.sizes()));
     const int t = narrow(T, "T"), h = narrow(H, "H"), i = narrow(w.I, "I"), e = narrow(w.E, "E"), kk = narrow(k, "top_k");
-    void *st = stream_of(a[11]);
-    call("zffn_moe_swiglu_fp8", [&] { return api.swiglu(px, pi, pw, w.wg, w.sg, w.wu, w.su, w.wd, w.sd, py, t, h, i, e, kk, accumulate, st); });
+    call("zffn_moe_swiglu_fp8", [&] { return api.swiglu(px, pi, pw, w.wg, w.sg, w.wu, w.su, w.wd, w.sd, py, t, h, i, e, kk, accumulate, on.s); });
     return y.object();
 }
 
