@@ -362,10 +362,10 @@ zffn_status zffn_fp8_dequant(const void *q, const float *scale, float *out, int6
  *     y[m][n] = sum_b a_scale[m][b] w_scale[n / 128][b] sum_{k in block b} a[m][k] w[n][k]
  * Each block's sum and the sum over blocks are fp32; y is rounded once.
  *   a: e4m3 [M][K], a_scale fp32 [M][ceil(K/128)].
- *   offsets: NULL (dense, E = 1), or int32 [E + 1] (device, ascending, as
+ *   offsets: NULL (dense, E = 1), or int32 [E + 1] (device, ascending from 0, as
  *     zffn_moe_sort writes it): rows offsets[e] .. offsets[e+1] - 1 of a are
- *     multiplied with expert e's weights; rows of y outside every expert are
- *     set to 0.
+ *     multiplied with expert e's weights; rows of y from offsets[E] on are set
+ *     to 0.
  *   w: e4m3 [E][N][K], w_scale fp32 [E][ceil(N/128)][ceil(K/128)].
  *   y: y_dtype (zffn_dtype) [M][N], overwritten.
  * Requirements: 1 <= M <= 2^24, 1 <= N <= 2^20, 16 <= K <= 65536, K % 16 == 0,
@@ -387,7 +387,7 @@ zffn_status zffn_fp8_matmul(const void *a, const float *a_scale, const void *w,
  *   (NULL: dense, E = 1).
  *   Wg, Wu: e4m3 [E][I][H], sg, su fp32 [E][ceil(I/128)][ceil(H/128)].
  *   Wd: e4m3 [E][H][I], sd fp32 [E][ceil(H/128)][ceil(I/128)].
- *   y: y_dtype [P][H], overwritten; rows outside every expert are set to 0.
+ *   y: y_dtype [P][H], overwritten; rows from offsets[E] on are set to 0.
  * Requirements: 1 <= P <= 2^24, H and I multiples of 16 in [16, 65536], E as
  * above, alignments as above.  Uses library workspace for h (zffn_reserve with
  * T * top_k >= P covers it).  Errors: INVALID_ARG, CUDA, NO_WORKSPACE. */

@@ -101,8 +101,8 @@ __device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, volatil
     return true;
 }
 // silu(g) u = g / (1 + 2^(-g log2 e)) u: two instructions of the special function
-// unit and four others (off by a few 2^-22 of the value; 2^x past the range gives
-// infinity and so 0, as it should).  Written out once for each value that a thread
+// unit and four others (off by a few 2^-22 of the value; below g = -87, where silu is
+// 1e-36 at most, 0).  Written out once for each value that a thread
 // holds, so its length counts: with the divide's and exponential's own handling of
 // denormals a 128 x 128 tile of h took 7500 clocks, fetching instructions.
 __device__ __forceinline__ float swiglu(float g, float u) {
