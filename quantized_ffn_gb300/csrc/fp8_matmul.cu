@@ -176,32 +176,37 @@ struct Walk {
 // The groups of rows (the experts, then the rows of none; h needs no zeros there)
 // in shared memory: {row tiles before the group, its first row}, one entry past the
 // last.  Called by the whole block; offsets are kept within [0, M] whatever they hold.
+// sums: 2 * THREADS / 32 words of shared memory that nothing else uses yet.
 template <class C>
-__device__ __forceinline__ void build_groups(const Params &p, int2 *cum) {
+__device__ __forceinline__ void build_groups(const Params &p, int2 *cum, int *sums) {
+    // a thread to a group, THREADS groups at a time: sums within the warps by shuffles,
+    // over the warps through shared memory
+    constexpr int WARPS = C::THREADS / 32;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int g = threadIdx.x; g <= p.E; g += C::THREADS) {
-        const int lo = min(max(__ldg(p.offsets + g), 0), p.M);
-        const int hi = g < p.E ? min(max(__ldg(p.offsets + g + 1), 0), p.M) : (C::GU ? lo : p.M);
-        cum[g] = make_int2((max(hi - lo, 0) + C::TM - 1) / C::TM, lo);
-    }
-    __syncthreads();
-    if (warp == 0) {
-        const int per = (p.E + 32) / 32, g0 = min(lane * per, p.E + 1), g1 = min(g0 + per, p.E + 1);
-        int n = 0;
-        for (int g = g0; g < g1; ++g) n += cum[g].x;
+    int before = 0;
+    for (int g0 = 0, half = 0; g0 <= p.E; g0 += C::THREADS, half ^= 1) {
+        const int g = g0 + threadIdx.x;
+        int n = 0, lo = 0;
+        if (g <= p.E) {
+            lo = min(max(__ldg(p.offsets + g), 0), p.M);
+            const int hi = g < p.E ? min(max(__ldg(p.offsets + g + 1), 0), p.M) : (C::GU ? lo : p.M);
+            n = (max(hi - lo, 0) + C::TM - 1) / C::TM;
+        }
         int inc = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int v = __shfl_up_sync(0xffffffffu, inc, o);
             if (lane >= o) inc += v;
         }
-        int at = inc - n;
-        for (int g = g0; g < g1; ++g) {
-            const int c = cum[g].x;
-            cum[g].x = at;
-            at += c;
-        }
-        if (lane == 31) cum[p.E + 1] = make_int2(inc, p.M);
+        if (lane == 31) sums[half * WARPS + warp] = inc;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w)
+            if (w < warp) before += sums[half * WARPS + w];
+        if (g <= p.E) cum[g] = make_int2(before + inc - n, lo);
+        if (g == p.E) cum[p.E + 1] = make_int2(before + inc, p.M);
+        if (g0 + C::THREADS <= p.E)
+            for (int w = warp; w < WARPS; ++w) before += sums[half * WARPS + w];
     }
 }
 
@@ -289,7 +294,8 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) small_kernel(const __gr
     const int step = gridDim.x / split;
     Walk<C> wk;
     wk.start(blockIdx.x / split);
-    if (!p.offsets && warp == C::EPI && wk.get(p, cum) && elect_one()) {
+    bool have = !p.offsets && wk.get(p, cum);
+    if (!p.offsets && warp == C::EPI && have && elect_one()) {
         // dense: the first weights are brought into L2 while the previous grid ends
         // (L2 is where that grid's writes arrive too, so nothing stale can be read)
         for (int i = 0; i < min(nkb, 2 * C::NS); ++i) {
@@ -297,15 +303,19 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) small_kernel(const __gr
             if (C::GU) tma_prefetch_2d(&maps.w1, (kb0 + i) * kF8Block, wk.nt * 128);
         }
     }
-    if (!p.early) grid_wait();
-    if (p.offsets) build_groups<C>(p, cum);
+    if (p.offsets) {
+        if (!p.early) grid_wait();
+        build_groups<C>(p, cum, reinterpret_cast<int *>(tab));
+    }
     __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(info + 1);
+    if (p.offsets) have = wk.get(p, cum);
+    else if (!p.early) grid_wait();   // (the block is set up and its first tile known while the previous grid ends)
     // (once this block has its tensor memory: a block of the next grid on this SM
     // could otherwise take it and then wait for this grid; and after the wait, so
     // that an early reader of the next grid finds the grids before this complete)
     if (!p.early) grid_launch_dependents();
-    tc_fence_after();
-    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(info + 1);
     RowTile tile{0, 0, 0, 0};   // the last tile whose sums are in `part` (split > 1: the only one)
     bool second = false;
 
@@ -374,7 +384,7 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) small_kernel(const __gr
             tma_load_2d(smem + s * C::STAGE + C::NW * C::W_BYTES, &maps.a, &s_full[s], (kb0 + i) * kF8Block, wk.row0);
         };
         bool waited = !p.early;
-        for (; ok && wk.get(p, cum); wk.t += step) {
+        for (; ok && have; wk.t += step, have = wk.get(p, cum)) {
             int i = 0;
             if (!waited && wk.e < p.E) {
                 // the weights of the first stages are asked for before what the
@@ -406,7 +416,7 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) small_kernel(const __gr
         if (p.early) grid_wait();   // (the wait for the previous grid is not one of the bounded ones)
         uint32_t it = 0;
         bool ok = true;
-        for (; ok && wk.get(p, cum); wk.t += step) {
+        for (; ok && have; wk.t += step, have = wk.get(p, cum)) {
             for (int i = 0; i < nkb && wk.e < p.E; ++i, ++it) {
                 const uint32_t s = it % C::NS, b = it % C::NB;
                 ok = bar_wait(&s_full[s], (it / C::NS) & 1, abort_flag, p.err) &&
@@ -454,7 +464,6 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) small_kernel(const __gr
             }
         };
         uint32_t it = 0, half = 0;
-        bool have = wk.get(p, cum);
         if (have) fetch(0);
         while (have) {
             float2 acc[C::TN / 2];
@@ -633,7 +642,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
         tc_fence_before();
     }
     grid_wait();
-    if (p.offsets) build_groups<C>(p, cum);
+    if (p.offsets) build_groups<C>(p, cum, reinterpret_cast<int *>(scales));
     __syncthreads();
     grid_launch_dependents();          // (this block has its tensor memory: see the small tiles)
     if (C::PAIR) cluster_sync_all();   // the peer's barriers are set up
