@@ -273,6 +273,7 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) small_kernel(const __gr
     asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(split));
     const uint32_t rank = cluster_ctarank();
     const uint32_t slice = (C::TN + split - 1) / split;       // rows of a tile that a rank adds up
+    const uint32_t inverse = (65536 + split - 1) / split;     // j * inverse >> 16 = j / split for j < 64
     if (split > 1) cluster_arrive();                          // (waited for before another's memory is written)
     if (warp == C::EPI && lane == 0) {
         info[0] = 0;
@@ -326,7 +327,7 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) small_kernel(const __gr
             float v[C::NW][4];
 #pragma unroll
             for (int w = 0; w < C::NW; ++w) {
-                const float *at = part + ((w * split * slice + j / split) * 128 + lane * 4);
+                const float *at = part + ((w * split * slice + (j * inverse >> 16)) * 128 + lane * 4);
                 float4 s = *reinterpret_cast<const float4 *>(at);
                 for (uint32_t r = 1; r < split; ++r) {
                     const float4 f = *reinterpret_cast<const float4 *>(at + r * slice * 128);
@@ -538,8 +539,10 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) small_kernel(const __gr
                 }
                 named_barrier(1 + w, 128);
                 const uint32_t to = smem_u32(part + (w * split + rank) * slice * 128) + lane * 16;
-                for (int j = q; j < tile.rows; j += 4)
-                    st_cluster_f4(mapa_shared(to + j / split * 512, j % split), reinterpret_cast<const float4 *>(own + j * 128)[lane]);
+                for (int j = q; j < tile.rows; j += 4) {
+                    const uint32_t at = j * inverse >> 16;
+                    st_cluster_f4(mapa_shared(to + at * 512, j - at * split), reinterpret_cast<const float4 *>(own + j * 128)[lane]);
+                }
             }
         }
     }
