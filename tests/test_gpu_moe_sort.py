@@ -184,3 +184,19 @@ def test_sort_in_a_graph_and_on_another_stream():
         other = zffn.moe_sort(ids, E)
     s.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(other, plan))
+
+
+def test_plan_parts_outlive_each_other():
+    # the three parts of a new plan are one allocation, which lives as long as any of them
+    rng = np.random.default_rng(23)
+    T, E, k = 37, 12, 3
+    ids = make_ids(rng, T, E, k, "random")
+    want = ref.sort(ids, E)
+    for keep in range(3):
+        part = zffn.moe_sort(dev(ids), E)[keep]
+        assert part.is_contiguous() and part.dtype == torch.int32 and part.shape == want[keep].shape
+        torch.full((2 * T * k + 64,), -9, dtype=torch.int32, device="cuda")
+        assert np.array_equal(part.cpu().numpy(), want[keep])
+        copy = part.clone()
+        part += 1
+        assert torch.equal(part, copy + 1)
