@@ -188,8 +188,8 @@ __device__ __forceinline__ void build_groups(const Params &p, int2 *cum, int *su
         const int g = g0 + threadIdx.x;
         int n = 0, lo = 0;
         if (g <= p.E) {
-            lo = min(max(__ldg(p.offsets + g), 0), p.M);
-            const int hi = g < p.E ? min(max(__ldg(p.offsets + g + 1), 0), p.M) : (C::GU ? lo : p.M);
+            lo = min(max(__ldcg(p.offsets + g), 0), p.M);   // (from L2: an early grid reads them before its wait)
+            const int hi = g < p.E ? min(max(__ldcg(p.offsets + g + 1), 0), p.M) : (C::GU ? lo : p.M);
             n = (max(hi - lo, 0) + C::TM - 1) / C::TM;
         }
         int inc = n;

@@ -113,3 +113,36 @@ def test_calls_back_to_back_on_one_stream():
         wq.view(torch.uint8).zero_()
         zffn.fp8_quantize(wf, block_rows=128, q=wq, scale=ws)
         assert torch.equal(zffn.fp8_matmul(q, s, wq, ws), want)
+
+
+def test_routes_that_change_from_call_to_call():
+    # the same memory holds another routing in every call of a chain (offsets are read before the
+    # down product's wait); each result as when the call is waited for
+    E, H, I, n = 16, 256, 256, 24
+    g = torch.Generator(device="cuda")
+    g.manual_seed(6)
+    layer = ex.make_layer(E, H, I, g)
+    for P in (8, 200, 4000):
+        a, s = zffn.fp8_quantize(torch.randn((P, H), generator=g, device="cuda"))
+        cuts = torch.sort(torch.randint(0, P + 1, (n, E + 1), generator=g, device="cuda", dtype=torch.int32), dim=1)[0]
+        cuts[:, 0] = 0
+        offsets = torch.empty(E + 1, dtype=torch.int32, device="cuda")
+        chain, waited = (torch.empty((n, P, H), device="cuda") for _ in range(2))
+        for i in range(n):
+            zffn.fp8_experts(a, s, *layer, offsets=cuts[i].contiguous(), y=waited[i])
+            torch.cuda.synchronize()
+        for i in range(n):
+            offsets.copy_(cuts[i])
+            zffn.fp8_experts(a, s, *layer, offsets=offsets, y=chain[i])
+        assert torch.equal(chain, waited)
+    for T in (1, 33):
+        x = torch.randn((T, H), generator=g, device="cuda").to(torch.bfloat16)
+        routes = [zffn.moe_router_topk(torch.randn((T, E), generator=g, device="cuda"), 2) for _ in range(n)]
+        chain, waited = (torch.empty((n, T, H), device="cuda") for _ in range(2))
+        for i in range(n):
+            zffn.moe_swiglu_fp8(x, *routes[i], *layer, y=waited[i])
+            torch.cuda.synchronize()
+        for i in range(n):
+            zffn.moe_swiglu_fp8(x, *routes[i], *layer, y=chain[i])
+        assert torch.equal(chain, waited)
+    assert zffn.get_device_error() == zffn.OK
