@@ -365,7 +365,8 @@ zffn_status zffn_fp8_dequant(const void *q, const float *scale, float *out, int6
  *   offsets: NULL (dense, E = 1), or int32 [E + 1] (device, ascending from 0, as
  *     zffn_moe_sort writes it): rows offsets[e] .. offsets[e+1] - 1 of a are
  *     multiplied with expert e's weights; rows of y from offsets[E] on are set
- *     to 0.
+ *     to 0.  Whatever the array holds, an entry counts as the largest of those up
+ *     to it, kept within [0, M]; rows of y before offsets[0] are left as they are.
  *   w: e4m3 [E][N][K], w_scale fp32 [E][ceil(N/128)][ceil(K/128)].
  *   y: y_dtype (zffn_dtype) [M][N], overwritten.
  * Requirements: 1 <= M <= 2^24, 1 <= N <= 2^20, 16 <= K <= 65536, K % 16 == 0,

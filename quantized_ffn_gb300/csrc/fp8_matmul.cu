@@ -168,14 +168,16 @@ struct Walk {
         }
         const int2 at = cum[e];
         row0 = at.y + (rt - at.x) * C::TM;
-        rows = min(C::TM, (e < p.E ? min(max(cum[e + 1].y, at.y), p.M) : p.M) - row0);
+        rows = min(C::TM, (e < p.E ? cum[e + 1].y : p.M) - row0);
         return true;
     }
 };
 
 // The groups of rows (the experts, then the rows of none; h needs no zeros there)
 // in shared memory: {row tiles before the group, its first row}, one entry past the
-// last.  Called by the whole block; offsets are kept within [0, M] whatever they hold.
+// last.  Called by the whole block.  Whatever the offsets hold, the groups part the
+// rows: an offset counts as the largest of those up to it, kept within [0, M], so that
+// the row tiles are never more than row_tiles_bound, which the grid is sized by.
 // sums: 2 * THREADS / 32 words of shared memory that nothing else uses yet.
 template <class C>
 __device__ __forceinline__ void build_groups(const Params &p, int2 *cum, int *sums) {
@@ -184,22 +186,36 @@ __device__ __forceinline__ void build_groups(const Params &p, int2 *cum, int *su
     constexpr int WARPS = C::THREADS / 32;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int before = 0;
+    bool descend = false;
+    auto offset = [&](int g) { return min(max(__ldcg(p.offsets + g), 0), p.M); };   // (from L2: an early grid reads them before its wait)
     for (int g0 = 0, half = 0; g0 <= p.E; g0 += C::THREADS, half ^= 1) {
         const int g = g0 + threadIdx.x;
-        int n = 0, lo = 0;
+        int lo = 0, hi = 0, n, inc;
         if (g <= p.E) {
-            lo = min(max(__ldcg(p.offsets + g), 0), p.M);   // (from L2: an early grid reads them before its wait)
-            const int hi = g < p.E ? min(max(__ldcg(p.offsets + g + 1), 0), p.M) : (C::GU ? lo : p.M);
-            n = (max(hi - lo, 0) + C::TM - 1) / C::TM;
+            lo = offset(g);
+            hi = g < p.E ? offset(g + 1) : (C::GU ? lo : p.M);
         }
-        int inc = n;
+        auto scan = [&] {
+            n = (hi - lo + C::TM - 1) / C::TM;
+            inc = n;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += v;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += v;
+            }
+            if (lane == 31) sums[half * WARPS + warp] = inc;
+        };
+        scan();
+        if (__syncthreads_or(hi < lo || descend)) {
+            // (never for offsets as the sort writes them, so the running maximum is
+            // found the plain way)
+            descend = true;
+            lo = 0;
+            for (int i = 0; i <= min(g, p.E); ++i) lo = max(lo, offset(i));
+            hi = g < p.E ? max(lo, offset(g + 1)) : (C::GU || g > p.E ? lo : p.M);
+            scan();
+            __syncthreads();
         }
-        if (lane == 31) sums[half * WARPS + warp] = inc;
-        __syncthreads();
 #pragma unroll
         for (int w = 0; w < WARPS; ++w)
             if (w < warp) before += sums[half * WARPS + w];
@@ -385,7 +401,7 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) small_kernel(const __gr
             tma_load_2d(smem + s * C::STAGE + C::NW * C::W_BYTES, &maps.a, &s_full[s], (kb0 + i) * kF8Block, wk.row0);
         };
         bool waited = !p.early;
-        for (; ok && have; wk.t += step, have = wk.get(p, cum)) {
+        for (; ok && have; wk.t += step, have = split == 1 && wk.get(p, cum)) {
             int i = 0;
             if (!waited && wk.e < p.E) {
                 // the weights of the first stages are asked for before what the
@@ -417,7 +433,7 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) small_kernel(const __gr
         if (p.early) grid_wait();   // (the wait for the previous grid is not one of the bounded ones)
         uint32_t it = 0;
         bool ok = true;
-        for (; ok && have; wk.t += step, have = wk.get(p, cum)) {
+        for (; ok && have; wk.t += step, have = split == 1 && wk.get(p, cum)) {
             for (int i = 0; i < nkb && wk.e < p.E; ++i, ++it) {
                 const uint32_t s = it % C::NS, b = it % C::NB;
                 ok = bar_wait(&s_full[s], (it / C::NS) & 1, abort_flag, p.err) &&
@@ -514,7 +530,7 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) small_kernel(const __gr
             }
             tile = {wk.e, wk.row0, wk.rows, wk.nt};
             wk.t += step;
-            have = wk.get(p, cum);
+            have = split == 1 && wk.get(p, cum);
             if (have) fetch(0);
             if (second) named_barrier(3, C::EPI * 32);       // the tile before has been written
             second = true;
@@ -527,7 +543,7 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) small_kernel(const __gr
                 named_barrier(3, C::EPI * 32);
                 emit(tile);
             } else {
-                // (fewer tiles than clusters: each has one)
+                // (no more tiles than clusters: each has one at most, and its walk ends there)
                 cluster_wait();                              // every block of the cluster runs
                 // this block's sums into its ring, which its products have left; then row j,
                 // a warp per row, to rank j % split
