@@ -740,9 +740,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
             }
             __syncwarp();
         }
-        // (both CTAs of a pair: no commit's arrival is left on its way)
-        if (lane == 0) mbar_wait(done, 0, nullptr, p.err);
-        __syncwarp();
     } else if (warp >= C::EPI + 2) {
         // ---- scales: this CTA's rows of a, and the tile's blocks of W (plain: two
         // blocks of rows; GU: gate and up), SEG K blocks at a time, 64 rows a warp
@@ -980,6 +977,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
     }
     tc_fence_before();
     __syncthreads();
+    // (both CTAs of a pair: no commit's arrival is left on its way.  The wait is bounded,
+    // so it begins when the sums have been taken out: the pair's second CTA issues
+    // nothing, and from the kernel's start would wait as long as the product takes)
+    if (warp == C::EPI + 1) {
+        if (lane == 0) mbar_wait(done, 0, nullptr, p.err);
+        __syncwarp();
+    }
     // (of a pair: no CTA leaves while the other's MMAs may read its shared memory
     // or it may still arrive on the other's barriers)
     if (C::PAIR) cluster_sync_all();
