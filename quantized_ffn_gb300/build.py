@@ -4,7 +4,8 @@ Each translation unit under csrc/ is compiled by nvcc in parallel, then linked
 into quantized_ffn_gb300/_lib/libzffn.so (CUDA runtime linked statically; the
 driver entry point used for TMA descriptors is looked up at run time).  The
 Python binding of the 8-bit entry points (csrc/binding.cpp) is compiled by the
-host compiler against the installed torch into _lib/_zffn_native.so.
+host compiler against the installed torch into _lib/_zffn_native.so; where that
+fails, build() warns and the library stands alone.
 """
 from __future__ import annotations
 
@@ -13,6 +14,7 @@ import os
 import shutil
 import subprocess
 import sys
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -76,25 +78,36 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
         if force or _stale(obj, [src] + hdrs):
             cmd = [nvcc, *ARCH, *FLAGS, *extra, "-c", src, "-o", obj]
             jobs.append(cmd)
-    native_tmp = NATIVE + f".{os.getpid()}.tmp"
+    def run(cmd):
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if verbose or r.returncode != 0:
+            sys.stderr.write(r.stdout + r.stderr)
+        if r.returncode != 0:
+            raise RuntimeError("the compiler failed: " + " ".join(cmd))
+
+    def bind():
+        tmp = NATIVE + f".{os.getpid()}.tmp"
+        run(_native_command() + ["-o", tmp])
+        os.replace(tmp, NATIVE)
+
     native = force or _stale(NATIVE, [os.path.join(CSRC, "binding.cpp"), os.path.join(INCLUDE, "zffn.h")])
-    if native:
-        jobs.append(_native_command() + ["-o", native_tmp])
-    if jobs:
-        with cf.ThreadPoolExecutor(max_workers=min(len(jobs), os.cpu_count() or 4)) as ex:
-            futs = [ex.submit(subprocess.run, cmd, capture_output=True, text=True) for cmd in jobs]
-            for cmd, f in zip(jobs, futs):
-                r = f.result()
-                if verbose or r.returncode != 0:
-                    sys.stderr.write(r.stdout + r.stderr)
-                if r.returncode != 0:
-                    raise RuntimeError("the compiler failed: " + " ".join(cmd))
-    if native:
-        os.replace(native_tmp, NATIVE)
+    if jobs or native:
+        with cf.ThreadPoolExecutor(max_workers=min(len(jobs) + native, os.cpu_count() or 4)) as ex:
+            bound = ex.submit(bind) if native else None
+            for f in [ex.submit(run, cmd) for cmd in jobs]:
+                f.result()
     if force or jobs or _stale(LIB, objs):
         tmp = LIB + f".{os.getpid()}.tmp"
         subprocess.check_call([nvcc, *ARCH, "-shared", "-o", tmp, *objs])
         os.replace(tmp, LIB)
+    if native and bound.exception() is not None:
+        # the library needs nvcc alone: a host without torch's headers, Python's or a
+        # CUDA build of torch keeps it (and the calls that do not go through the binding).
+        # A module of other sources is not left to be loaded instead.
+        if os.path.exists(NATIVE):
+            os.remove(NATIVE)
+        warnings.warn(f"{NATIVE} was not built, so the 8-bit and sorting functions are missing from Python: "
+                      f"{bound.exception()}", RuntimeWarning, stacklevel=2)
     return LIB
 
 
