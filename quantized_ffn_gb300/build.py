@@ -22,7 +22,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(HERE, "_lib")
 LIB = os.path.join(OUT_DIR, "libzffn.so")
-NATIVE = os.path.join(OUT_DIR, "_zffn_native.so")
+NATIVE = os.path.join(OUT_DIR, "_zffn_native.so")   # beside it NATIVE + ".for": what it was made for
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC,
          "--expt-relaxed-constexpr"]
@@ -48,6 +48,30 @@ def _stale(target, deps):
         return True
     t = os.path.getmtime(target)
     return any(os.path.getmtime(d) > t for d in deps)
+
+
+def native_is_for(native: str) -> str:
+    """The torch and the Python that this binding was compiled against ("" where nothing says so)."""
+    try:
+        with open(native + ".for") as f:
+            return f.read()
+    except OSError:
+        return ""
+
+
+def native_wanted() -> str:
+    """The same of this process: a binding for another pair is not loaded, and built again."""
+    import torch
+
+    return f"torch {torch.__version__}, Python {sys.version_info[0]}.{sys.version_info[1]}"
+
+
+def _native_stale() -> bool:
+    try:
+        wanted = native_wanted()
+    except ImportError:
+        return True
+    return native_is_for(NATIVE) != wanted or _stale(NATIVE, [os.path.join(CSRC, "binding.cpp"), os.path.join(INCLUDE, "zffn.h")])
 
 
 def _native_command():
@@ -89,8 +113,11 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
         tmp = NATIVE + f".{os.getpid()}.tmp"
         run(_native_command() + ["-o", tmp])
         os.replace(tmp, NATIVE)
+        with open(tmp, "w") as f:
+            f.write(native_wanted())
+        os.replace(tmp, NATIVE + ".for")
 
-    native = force or _stale(NATIVE, [os.path.join(CSRC, "binding.cpp"), os.path.join(INCLUDE, "zffn.h")])
+    native = force or _native_stale()
     if jobs or native:
         with cf.ThreadPoolExecutor(max_workers=min(len(jobs) + native, os.cpu_count() or 4)) as ex:
             bound = ex.submit(bind) if native else None

@@ -16,7 +16,6 @@
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
-#include <torch/version.h>
 
 #include <optional>
 #include <sstream>
@@ -459,10 +458,5 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_zffn_native", nullptr, -1, method
 }  // namespace
 
 PyMODINIT_FUNC PyInit__zffn_native() {
-    PyObject *m = PyModule_Create(&module);
-    if (m && PyModule_AddStringConstant(m, "torch_version", TORCH_VERSION) != 0) {
-        Py_DECREF(m);
-        return nullptr;
-    }
-    return m;
+    return PyModule_Create(&module);
 }

@@ -17,6 +17,8 @@ from typing import NamedTuple, Optional
 
 import torch
 
+from . import build as _build
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_lib", "libzffn.so")
 
@@ -327,12 +329,14 @@ def _native():
             if not os.path.exists(NATIVE_PATH):
                 raise RuntimeError(
                     f"{NATIVE_PATH} is missing: build it with quantized_ffn_gb300.build.build()")
+            # (before it is loaded: a module for another torch may fail on a missing symbol, or not at all)
+            made_for, wanted = _build.native_is_for(NATIVE_PATH), _build.native_wanted()
+            if made_for != wanted:
+                raise RuntimeError(f"{NATIVE_PATH} was built for {made_for or 'an unknown torch'}, this is {wanted}: "
+                                   "build it again with quantized_ffn_gb300.build.build()")
             loader = importlib.machinery.ExtensionFileLoader("_zffn_native", NATIVE_PATH)
             m = importlib.util.module_from_spec(importlib.util.spec_from_loader("_zffn_native", loader))
             loader.exec_module(m)
-            if m.torch_version.split("+")[0] != torch.__version__.split("+")[0]:
-                raise RuntimeError(f"{NATIVE_PATH} was built for torch {m.torch_version}, this is {torch.__version__}: "
-                                   "build it again")
             m.bind(_fail, *(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in _NATIVE_CALLS))
             _native_module = m
     return _native_module

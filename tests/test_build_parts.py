@@ -1,12 +1,14 @@
 """The library and its Python binding are built apart: a host that cannot compile the binding still gets
-libzffn.so."""
+libzffn.so, and a binding for another torch or Python is neither loaded nor kept."""
 import ctypes
 import os
 import shutil
 
 import pytest
+import torch
 
 from quantized_ffn_gb300 import build as zbuild
+from quantized_ffn_gb300 import zffn
 
 
 @pytest.fixture
@@ -44,3 +46,31 @@ def test_library_where_torch_cannot_be_asked(elsewhere, monkeypatch):
     monkeypatch.setattr(zbuild, "_native_command", no_torch)
     with pytest.warns(RuntimeWarning, match="No module named 'torch'"):
         assert os.path.exists(zbuild.build())
+
+
+def test_binding_is_built_again_for_another_torch(elsewhere, monkeypatch):
+    # (the stand-in for the compiler notes its calls and makes the file that it is asked for)
+    calls = elsewhere / "calls"
+    cxx = compiler(elsewhere / "cxx", f'echo called >> {calls}\nfor a; do out="$a"; done\necho module > "$out"\n')
+    monkeypatch.setenv("CXX", cxx)
+    count = lambda: len(calls.read_text().split())   # noqa: E731
+    zbuild.build()
+    assert count() == 1 and (elsewhere / "_zffn_native.so").exists()
+    zbuild.build()
+    assert count() == 1                               # nothing changed
+    monkeypatch.setattr(torch, "__version__", "1.2.3+other")
+    zbuild.build()
+    assert count() == 2
+    zbuild.build()
+    assert count() == 2
+
+
+def test_binding_of_another_torch_is_not_loaded(elsewhere, monkeypatch):
+    monkeypatch.setenv("CXX", compiler(elsewhere / "cxx", 'for a; do out="$a"; done\necho no module > "$out"\n'))
+    monkeypatch.setattr(torch, "__version__", "1.2.3+other")
+    zbuild.build()
+    monkeypatch.undo()
+    monkeypatch.setattr(zffn, "NATIVE_PATH", str(elsewhere / "_zffn_native.so"))
+    monkeypatch.setattr(zffn, "_native_module", None)
+    with pytest.raises(RuntimeError, match="1.2.3.*build it again"):
+        zffn.moe_sort(torch.zeros((1, 1), dtype=torch.int32), 1)
