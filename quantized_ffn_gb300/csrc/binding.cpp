@@ -61,8 +61,22 @@ const at::Tensor &tensor(PyObject *o, const char *name) {
     return THPVariable_Unpack(o);
 }
 
+// The current device (asked for once a call: entry() forgets it): the library's
+// workspace, its error word and the launches are of this one.
+thread_local int t_device = -1;
+int current_device() {
+    if (t_device < 0) t_device = c10::cuda::current_device();
+    return t_device;
+}
+void on_device(int64_t device, const char *name) {
+    if (device != current_device())
+        throw ValueError(std::string(name) + " must be on the current device, cuda:" + std::to_string(current_device()) + ", got cuda:" +
+                         std::to_string(device));
+}
+
 void *place(const at::Tensor &t, const char *name) {
     if (!t.is_cuda()) throw ValueError(std::string(name) + " must be a CUDA tensor");
+    on_device(t.get_device(), name);
     if (!t.is_contiguous()) throw ValueError(std::string(name) + " must be contiguous");
     return const_cast<void *>(t.const_data_ptr());
 }
@@ -113,7 +127,15 @@ struct Stream {
         s = PyLong_AsVoidPtr(h);
         Py_DECREF(h);
         if (PyErr_Occurred()) throw Raised{};
-        guard.emplace(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(s), c10::cuda::current_device()));
+        if (PyObject *d = PyObject_GetAttrString(stream, "device_index")) {
+            const long device = PyLong_AsLong(d);
+            Py_DECREF(d);
+            if (PyErr_Occurred()) throw Raised{};
+            on_device(device, "stream");
+        } else {
+            PyErr_Clear();   // (a bare handle: the current device's)
+        }
+        guard.emplace(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(s), current_device()));
     }
 };
 
@@ -417,6 +439,7 @@ PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
         PyErr_Format(PyExc_TypeError, "%d arguments expected, got %zd", N, n);
         return nullptr;
     }
+    t_device = -1;
     try {
         return F(args);
     } catch (const ValueError &e) {
