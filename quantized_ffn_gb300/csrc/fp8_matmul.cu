@@ -1054,10 +1054,11 @@ static cudaError_t prefer_shared() {
 }
 
 // Clusters of `split` small-tile blocks that the current device runs at once with
-// one block an SM (asked once for each device and split; the answer counts one
-// block an SM whatever the shared memory).
+// one block an SM (asked once for each device and split, without the experts' table,
+// so that the answer is not the first caller's: it counts one block an SM whatever
+// the shared memory).
 template <class C>
-static int clusters_at_once(int split, size_t smem) {
+static int clusters_at_once(int split) {
     static std::atomic<int> known[64][C::MAX_SPLIT + 1];
     std::atomic<int> &k = known[device_info().device & 63][split];
     int n = k.load(std::memory_order_relaxed);
@@ -1065,7 +1066,7 @@ static int clusters_at_once(int split, size_t smem) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(split);
         cfg.blockDim = dim3(C::THREADS);
-        cfg.dynamicSmemBytes = smem;
+        cfg.dynamicSmemBytes = C::SMEM;
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeClusterDimension;
         attr[0].val.clusterDim.x = split;
@@ -1075,7 +1076,7 @@ static int clusters_at_once(int split, size_t smem) {
         cfg.numAttrs = 1;
         if (cudaOccupancyMaxActiveClusters(&n, small_kernel<C>, &cfg) != cudaSuccess || n < 1) {
             cudaGetLastError();
-            n = 1;
+            return 1;   // (no split for this call; the next one asks again)
         }
         k.store(n, std::memory_order_relaxed);
     }
@@ -1102,7 +1103,7 @@ static cudaError_t launch_small(const Fp8Args &a, cudaStream_t s) {
     // (all at once: a cluster's blocks lie within one part of the chip, so that fewer
     // of them run together than the SMs alone would take; a second wave costs more
     // than the split gains)
-    while (split > 1 && (int64_t)clusters_at_once<C>(split, smem) * C::BLOCKS < tiles) --split;
+    while (split > 1 && (int64_t)clusters_at_once<C>(split) * C::BLOCKS < tiles) --split;
     if (split < 1) split = 1;
     const int64_t clusters = split > 1 || tiles < slots ? tiles : slots;
     if (tiles + slots > 0x7fffffff) return cudaErrorInvalidValue;
