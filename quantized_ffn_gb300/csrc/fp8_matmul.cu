@@ -1143,11 +1143,15 @@ static cudaError_t launch_large(const Fp8Args &a, cudaStream_t s) {
     }
     const size_t smem = C::SMEM + (a.offsets ? ((size_t)a.E + 2) * 8 : 0);
     // the registers' shift adds up only for the count that the kernel is launched with
-    static const int regs = [] {
+    // (asked until it is known)
+    static std::atomic<int> regs{0};
+    if (regs.load(std::memory_order_relaxed) == 0) {
         cudaFuncAttributes f{};
-        return cudaFuncGetAttributes(&f, large_kernel<C>) == cudaSuccess ? f.numRegs : 0;
-    }();
-    if (regs != C::REGS) return cudaErrorInvalidConfiguration;
+        const cudaError_t asked = cudaFuncGetAttributes(&f, large_kernel<C>);
+        if (asked != cudaSuccess) return asked;
+        regs.store(f.numRegs, std::memory_order_relaxed);
+    }
+    if (regs.load(std::memory_order_relaxed) != C::REGS) return cudaErrorInvalidConfiguration;
     const cudaError_t e = ensure_dynamic_smem((const void *)large_kernel<C>, smem);
     if (e != cudaSuccess) return e;
     return launch_dependent(large_kernel<C>, dim3((unsigned)(clusters * C::CTAS)), C::THREADS, smem, C::CTAS, s, maps, p);
