@@ -360,7 +360,10 @@ zffn_status zffn_fp8_dequant(const void *q, const float *scale, float *out, int6
 
 /* Product of block-scaled matrices, dense or grouped by expert:
  *     y[m][n] = sum_b a_scale[m][b] w_scale[n / 128][b] sum_{k in block b} a[m][k] w[n][k]
- * Each block's sum and the sum over blocks are fp32; y is rounded once.
+ * Each block's sum and the sum over blocks are fp32; y is rounded once.  The two
+ * scales of a block are multiplied first, in fp32: their product must stay below
+ * 2^128 (an infinite one makes infinities, and NaN of a block's sum of 0), and
+ * where it is below 2^-126 the block's term is off by up to 2^-125.
  *   a: e4m3 [M][K], a_scale fp32 [M][ceil(K/128)].
  *   offsets: NULL (dense, E = 1), or int32 [E + 1] (device, ascending from 0, as
  *     zffn_moe_sort writes it): rows offsets[e] .. offsets[e+1] - 1 of a are

@@ -5,7 +5,8 @@
 // The scales are any fp32 values, so a block's product (K = 128, four MMAs of
 // K = 32) is one accumulation in tensor memory, and the sum over blocks is kept
 // in registers: acc += d * (sa * sw), one fp32 multiply-add per value and block
-// (the scales' product is rounded once before).
+// (the scales' product is rounded once before; below 2^-126 it is held in steps of
+// 2^-149, which moves a block's term by less than 2^-125, since its sum is below 2^25).
 #include <cudaTypedefs.h>
 
 #include <atomic>
