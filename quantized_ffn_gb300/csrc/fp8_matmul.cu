@@ -102,8 +102,12 @@ __device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, volatil
     return true;
 }
 // silu(g) u = g / (1 + 2^(-g log2 e)) u: two instructions of the special function
-// unit and four others (off by a few 2^-22 of the value; below g = -87, where silu is
-// 1e-36 at most, 0).  Written out once for each value that a thread
+// unit and four others.  Off by at most (3 + |g| / 3) 2^-22 of the value for g < 0
+// and 3 x 2^-22 for g > 0: the exponent -g log2 e is rounded to fp32, by up to 2^-24
+// of itself and the constant by 2^-26, and the instructions are off by 2^-22 and 2^-23
+// (with exact ones 1.4 x 2^-22 at g = -5, 8 at -40, 16 at -87), where h keeps 2^-4.
+// Below g = -87.3 the reciprocal is subnormal and h is 0; silu is above -1.1e-36
+// there.  Written out once for each value that a thread
 // holds, so its length counts: with the divide's and exponential's own handling of
 // denormals a 128 x 128 tile of h took 7500 clocks, fetching instructions.
 __device__ __forceinline__ float swiglu(float g, float u) {
