@@ -51,7 +51,7 @@ def test_product(M, N, K, E, kind, dtype):
     assert zffn.get_device_error() == zffn.OK
 
 
-@pytest.mark.parametrize("kind,dtype", zip(KINDS, [torch.float32, torch.bfloat16] * 2))
+@pytest.mark.parametrize("kind,dtype", list(zip(KINDS, [torch.float32, torch.bfloat16] * 2)))
 @pytest.mark.parametrize("P,H,I,E", [(1500, 2576, 2576, 4), (4500, 2576, 1296, 3)])
 def test_experts(P, H, I, E, kind, dtype):
     rng = np.random.default_rng(P + len(kind))
