@@ -2,7 +2,8 @@
 entry points in a native module (csrc/binding.cpp).
 
 Every function takes CUDA tensors, checks dtype/shape/contiguity, and passes
-raw device pointers and the current (or given) CUDA stream to the C ABI.  All
+raw device pointers and the current (or given) CUDA stream to the C ABI.  None is
+known to autograd: results carry no gradient, whatever the inputs require.  All
 computation happens in the library's kernels; if the library is not built,
 importing the functions raises -- there is no fallback.
 """
