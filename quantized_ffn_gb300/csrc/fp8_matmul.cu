@@ -628,7 +628,7 @@ struct LargeCfg {
     static constexpr int OFF_TOP = OFF_OUT + EPI * OUT_BYTES;     // GU: largest h of (tile parity, group, row)
     static constexpr int OFF_SC = OFF_TOP + (GU ? 2 * 2 * 128 * 4 : 0);
     static constexpr int OFF_BAR = OFF_SC + SLOTS * SLOT * 4;
-    static constexpr int OFF_CUM = OFF_BAR + (2 * NS + 2 * NB + 2 * SLOTS + 1) * 8 + 24;   // (a multiple of 8)
+    static constexpr int OFF_CUM = OFF_BAR + (2 * NS + 2 * NB + 2 * SLOTS + 1 + (GU ? 8 : 0)) * 8 + 24;   // (a multiple of 8)
     static constexpr int SMEM = OFF_CUM + 1024;              // + {row tiles before, first row} of each group of rows
 };
 
@@ -640,7 +640,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
     uint64_t *s_full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
     uint64_t *s_empty = s_full + C::NS, *t_full = s_empty + C::NS, *t_empty = t_full + C::NB;
     uint64_t *c_full = t_empty + C::NB, *c_empty = c_full + C::SLOTS, *done = c_empty + C::SLOTS;
-    int *info = reinterpret_cast<int *>(done + 1);           // abort, TMEM base
+    uint64_t *top_full = done + 1;                           // GU: of each tile parity and 32 rows
+    int *info = reinterpret_cast<int *>(done + 1 + (C::GU ? 8 : 0));   // abort, TMEM base
     float *scales = reinterpret_cast<float *>(smem + C::OFF_SC);
     int2 *cum = reinterpret_cast<int2 *>(smem + C::OFF_CUM);
     volatile int *abort_flag = info;
@@ -654,6 +655,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
         for (int i = 0; i < C::NB; ++i) { mbar_init(&t_full[i], 1); mbar_init(&t_empty[i], C::EPI * C::CTAS); }
         for (int i = 0; i < C::SLOTS; ++i) { mbar_init(&c_full[i], 2); mbar_init(&c_empty[i], C::EPI); }
         mbar_init(done, 1);
+        if (C::GU)
+            for (int i = 0; i < 8; ++i) mbar_init(&top_full[i], 2);
         fence_mbarrier_init();
         prefetch_tensormap(&maps.a);
         prefetch_tensormap(&maps.w0);
@@ -794,7 +797,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
         const uint32_t empty0 = C::PAIR ? mapa_shared(smem_u32(t_empty), 0) : 0;
         uint8_t *out = smem + C::OFF_OUT + warp * C::OUT_BYTES;
         uint32_t it = 0, ck = 0;
-        int parity = 0;
+        uint32_t turn = 0;                                   // tiles before this one
         for (;;) {
             // which tile
             if (!__all_sync(0xffffffffu, bar_wait(&c_full[ck % C::SLOTS], (ck / C::SLOTS) & 1, abort_flag, p.err))) break;
@@ -926,11 +929,16 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
 #pragma unroll
                     for (int j = 0; j < 32; ++j) top = fmaxf(top, fmaxf(finite_abs(acc[j].x), finite_abs(acc[j].y)));
                 }
-                float *t2 = tops + parity * 2 * 128 + lrow;
+                float *t2 = tops + (turn & 1) * 2 * 128 + lrow;
                 t2[w * 128] = top;
-                named_barrier(1, C::EPI * 32);
+                // (a barrier in memory of the two warps of these rows, whose wait is
+                // bounded: a warp that has given up does not come to this tile)
+                uint64_t *both = &top_full[(turn & 1) * 4 + q];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(both);
+                bar_wait(both, (turn >> 1) & 1, abort_flag, p.err);
                 top = fmaxf(t2[0], t2[128]);
-                parity ^= 1;
+                ++turn;
                 const int sp = f8_scale_exp(top);
                 const float inv = pow2f(-sp);
                 emptied();
