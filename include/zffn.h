@@ -411,7 +411,9 @@ zffn_status zffn_fp8_experts(const void *a, const float *a_scale, const int32_t 
  *   offsets: output, int32 [E + 1]: expert e's rows are offsets[e] ..
  *     offsets[e + 1] - 1.
  * Requirements: T >= 1, 1 <= E <= 4096, 1 <= top_k <= 64, T * top_k <= 2^24,
- * 4-byte aligned pointers.  No workspace.  Errors: INVALID_ARG, CUDA. */
+ * 4-byte aligned pointers.  No workspace.  More than 1024 pairs are sorted by a
+ * cluster of 16 thread blocks, which a part of a GPU may not run (CUDA then).
+ * Errors: INVALID_ARG, CUDA. */
 zffn_status zffn_moe_sort(const int32_t *expert_ids, int32_t *row_slot, int32_t *slot_row,
                           int32_t *offsets, int T, int E, int top_k, void *stream);
 

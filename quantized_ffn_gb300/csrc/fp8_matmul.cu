@@ -242,7 +242,7 @@ __device__ __forceinline__ void build_groups(const Params &p, int2 *cum, int *su
 // leave, 0.8 us.)  Bound by HBM: every weight byte is read once.  The experts of
 // 256 tokens (128 of 2048 x 768, 8 a token; 617 MB) take 100 us, 6.2 TB/s.  Short
 // calls are bound by the way from the launch to the first bytes and from the last
-// ones through the join: 1 x 11008 x 4096 (45 MB) takes 10.2 us, 4.4 TB/s.
+// ones through the join: 1 x 11008 x 4096 (45 MB) takes 10.1 us, 4.5 TB/s.
 //
 // Roles: warps 0 .. 4 NW - 1 take a block's product out of tensor memory, scale
 // and sum it in registers, and write the result; then one warp loads by TMA and

