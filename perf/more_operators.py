@@ -68,7 +68,7 @@ def draw(rng):
             experts = max(1, experts // 2)
         top_k = rng.randint(1, min(8, experts))
         tokens = _log(rng, 1, 4096)
-        tokens = max(1, min(tokens, int(1e11 / (top_k * n * k))))
+        tokens = max(1, min(tokens, int(1e11 / (top_k * n * k)), int(3e8 / (top_k * (n + k)) / (2 if out == "fp32" else 1))))
         case = {"op": op, "tokens": tokens, "top_k": top_k, "experts": experts, "n": n, "k": k, "out": out, "dropped": rng.choice([0.0, 0.0, 0.1])}
         if op == "product":
             case["back"] = rng.random() < 0.5
