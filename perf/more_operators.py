@@ -64,7 +64,7 @@ def draw(rng):
     n, k = 8 * _log(rng, 8, 1376), 8 * _log(rng, 8, 1376)
     if op in ("product", "weights"):
         experts = _log(rng, 1, 128)
-        while experts * n * k > 128 * 1536 * 2048 // (2 if (op, out) == ("weights", "fp32") else 1):
+        while experts * n * k > 128 * 1536 * 2048 // (2 if out == "fp32" else 1):
             experts = max(1, experts // 2)
         top_k = rng.randint(1, min(8, experts))
         tokens = _log(rng, 1, 4096)
