@@ -470,6 +470,107 @@ zffn_status zffn_moe_swiglu_fp8(const void *x, const int32_t *expert_ids,
                                 float *y, int T, int H, int I, int E, int top_k, int accumulate,
                                 void *stream);
 
+/* ---------------------------------------------------------------------------
+ * Training and adapting layers in bf16: the experts' products with their
+ * gradients, SwiGLU with its gradient, and low-rank adapters beside a
+ * projection of any kind.  Operands are bf16, every sum is fp32 and every result
+ * is rounded once.  The source pages have no counterpart of these entry points.
+ * None takes library workspace, so calls on several streams may overlap as long
+ * as their arguments do not.
+ * ------------------------------------------------------------------------- */
+
+/* Product of bf16 matrices, dense or grouped by expert:
+ *     y[m][n] = sum_k a[m][k] w[n][k]        (transposed = 0: w is [E][N][K])
+ *     y[m][n] = sum_k a[m][k] w[k][n]        (transposed = 1: w is [E][K][N])
+ * The second form is the gradient of the first by a: with w as the first has it,
+ * da = zffn_bf16_matmul(dy, w, transposed = 1) with N and K changed over.
+ *   a: bf16 [M][K].  y: y_dtype (zffn_dtype) [M][N], overwritten.
+ *   offsets: NULL (dense, E = 1), or int32 [E + 1] (device, ascending from 0, as
+ *     zffn_moe_sort writes it): rows offsets[e] .. offsets[e+1] - 1 of a take
+ *     expert e's weights; rows of y from offsets[E] on are set to 0.  Whatever the
+ *     array holds, an entry counts as the largest of those up to it, kept within
+ *     [0, M]; rows of y before offsets[0] are left as they are.
+ * A row of y depends on no other row of a, whatever the others hold (rows of no
+ * expert may hold anything).
+ * Requirements: 1 <= M <= 2^24, 1 <= N <= 65536, 8 <= K <= 65536, K % 8 == 0 (with
+ * transposed also N % 8 == 0), 1 <= E <= 4096; a and w 16-byte aligned, offsets
+ * 4-byte, y to its element (a 16-byte aligned y with rows of 16-byte multiples is
+ * written faster).  y may not overlap a or w.
+ * Errors: INVALID_ARG, CUDA. */
+zffn_status zffn_bf16_matmul(const void *a, const void *w, const int32_t *offsets, int transposed,
+                             int y_dtype, void *y, int M, int N, int K, int E, void *stream);
+
+/* Gradient of zffn_bf16_matmul (transposed = 0) by its weights:
+ *     dw[e][n][k] = sum over expert e's rows m of dy[m][n] a[m][k]
+ * 0 for an expert without rows; rows of no expert are not read.
+ *   dy: bf16 [M][N].  a: bf16 [M][K].  offsets as above (NULL: E = 1, all rows).
+ *   dw: dw_dtype [E][N][K], overwritten.
+ * The sums of an expert's rows are taken in their order (the same result every
+ * time).  Requirements as above, and N % 8 == 0; dy, a and dw 16-byte aligned.
+ * Errors: INVALID_ARG, CUDA. */
+zffn_status zffn_bf16_matmul_grad_w(const void *dy, const void *a, const int32_t *offsets,
+                                    int dw_dtype, void *dw, int M, int N, int K, int E,
+                                    void *stream);
+
+/* h[r][i] = silu(g) u with g = gu[r][i], u = gu[r][I + i] (the rows of one product
+ * with the gate and up weights stacked), silu(g) = g / (1 + e^-g), in fp32.
+ *   gu: dtype (zffn_dtype) [rows][2 I].  h: dtype [rows][I].
+ * Any rows, I >= 1 (rows <= 2^31 - 1, I <= 2^20), pointers aligned to their element
+ * (16-byte aligned ones with rows of 16-byte multiples are faster).
+ * Infinities and NaN as the formula has them in IEEE arithmetic (silu(-inf) is NaN).
+ * Errors: INVALID_ARG, CUDA. */
+zffn_status zffn_swiglu(int dtype, const void *gu, void *h, int64_t rows, int64_t I, void *stream);
+
+/* Gradient of zffn_swiglu: with s = 1 / (1 + e^-g),
+ *     dgu[r][i] = dh u s (1 + g (1 - s)),   dgu[r][I + i] = dh g s
+ *   dh: dtype [rows][I].  gu, dgu: dtype [rows][2 I]; dgu may be gu.
+ * Requirements and errors as zffn_swiglu. */
+zffn_status zffn_swiglu_grad(int dtype, const void *dh, const void *gu, void *dgu, int64_t rows,
+                             int64_t I, void *stream);
+
+/* Low-rank adapters of many requests at once, beside a projection that they share:
+ *     v[row]  = scale[e] x[t] A[e]^T                 (fp32 [r])
+ *     out[t]  = base[t] + v[row] B[e]^T
+ * for every token t with an adapter e; a token of none keeps base.  The tokens are
+ * sorted by adapter with zffn_moe_sort(ids, ..., T, E = L, top_k = 1), whose
+ * outputs this call takes; the sort is made once for all projections of a step.
+ *   x: bf16 [T][K].  A: bf16 [L][r][K].  B: bf16 [L][N][r].
+ *   scale: fp32 [L], or NULL for ones.
+ *   row_slot: int32 [T]; slot_row: int32 [T]; offsets: int32 [L + 1].  A row whose
+ *     row_slot is outside [0, T) adds nothing; offsets count as for
+ *     zffn_bf16_matmul; no two rows may have the same token.
+ *   base: dtype (zffn_dtype) [T][N], or NULL for zeros.  out: dtype [T][N]; it may be
+ *     base (tokens of no adapter are then left alone), and may not overlap it otherwise.
+ *   v: output, fp32 [T][r], the sorted rows' (0 from offsets[L] on): what
+ *     zffn_lora_grad needs again.
+ * Both products have fp32 sums; v is not rounded to fewer bits between them.
+ * Requirements: 1 <= T <= 2^24, K and N multiples of 8 in [8, 65536], r a multiple
+ * of 8 in [8, 128], 1 <= L <= 4096; x, A, B, base and out 16-byte aligned, v 16-byte,
+ * the others 4-byte.  Errors: INVALID_ARG, CUDA. */
+zffn_status zffn_lora_add(const void *x, const void *A, const void *B, const float *scale,
+                          const int32_t *row_slot, const int32_t *slot_row, const int32_t *offsets,
+                          int dtype, const void *base, void *out, float *v, int T, int N, int K,
+                          int r, int L, void *stream);
+
+/* Gradients of zffn_lora_add:
+ *     dv[row] = scale[e] dy[t] B[e]                  (fp32 [r])
+ *     dx[t]   = base[t] + dv[row] A[e]
+ *     dA[e]   = sum over e's rows of dv[row]^T x[t]
+ *     dB[e]   = sum over e's rows of dy[t]^T v[row]
+ * dA and dB are 0 for an adapter without tokens; base is what the shared projection
+ * gives back to x.  The sums over rows are taken in a fixed order.
+ *   dy: bf16 [T][N].  v: fp32 [T][r] as zffn_lora_add wrote it.
+ *   base: dx_dtype [T][K] or NULL.  dx: dx_dtype [T][K], may be base.
+ *   dA: dw_dtype [L][r][K].  dB: dw_dtype [L][N][r].  dv: output, fp32 [T][r] (0 from
+ *     offsets[L] on).
+ * Requirements and the other arguments as zffn_lora_add; dy, v, dx, dA, dB and dv
+ * 16-byte aligned.  Errors: INVALID_ARG, CUDA. */
+zffn_status zffn_lora_grad(const void *dy, const void *x, const float *v, const void *A,
+                           const void *B, const float *scale, const int32_t *row_slot,
+                           const int32_t *slot_row, const int32_t *offsets, int dx_dtype,
+                           const void *base, void *dx, int dw_dtype, void *dA, void *dB, float *dv,
+                           int T, int N, int K, int r, int L, void *stream);
+
 /* Single-token dense block (T = 1) that allocates no device memory.  The
  * source pages have no counterpart of this entry point.  It is for callers
  * that cannot let the library call cudaMalloc/cudaFree during a call -- for

@@ -1,0 +1,54 @@
+// bf16.h -- launchers of the bf16 products and their weights' gradients
+// (bf16_matmul.cu), of SwiGLU (swiglu.cu) and of the low-rank adapters (lora.cu).
+#pragma once
+
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+namespace zffn {
+
+// y = a . w^T (w [E][N][K]) or a . w (transposed: w [E][K][N])
+struct Bf16Args {
+    const void *a;           // bf16 [M][K]
+    const void *w;
+    const int32_t *offsets;  // [E + 1] rows of each expert, or nullptr (dense)
+    bool transposed;
+    int y_dtype;             // zffn_dtype
+    void *y;                 // [M][N]
+    int M, N, K, E;
+    int *err;
+};
+cudaError_t launch_bf16_matmul(const Bf16Args &a, cudaStream_t s);
+
+// dw[e] = sum of dy[m]^T a[m] over expert e's rows
+struct Bf16GradArgs {
+    const void *dy;          // bf16 [M][N]
+    const void *a;           // bf16 [M][K]
+    const int32_t *offsets;
+    int dw_dtype;
+    void *dw;                // [E][N][K]
+    int M, N, K, E;
+    int *err;
+};
+cudaError_t launch_bf16_grad_w(const Bf16GradArgs &a, cudaStream_t s);
+
+cudaError_t launch_swiglu(int dtype, const void *gu, void *h, int64_t rows, int64_t I, cudaStream_t s);
+cudaError_t launch_swiglu_grad(int dtype, const void *dh, const void *gu, void *dgu, int64_t rows, int64_t I, cudaStream_t s);
+
+// The tokens sorted by adapter.
+struct LoraPlan {
+    const int32_t *row_slot, *slot_row, *offsets;
+    const float *scale;      // [L] or nullptr
+    int T, r, L;
+    int *err;
+};
+// v[row] = scale x[t] W^T: W [L][r][C], or (transposed) [L][C][r]
+cudaError_t launch_lora_shrink(const LoraPlan &p, const void *x, const void *w, bool transposed, float *v, int C, cudaStream_t s);
+// out[t] = base[t] + v[row] W^T: W [L][C][r], or (transposed) [L][r][C]
+cudaError_t launch_lora_expand(const LoraPlan &p, const float *v, const void *w, bool transposed, int dtype, const void *base, void *out,
+                               int C, cudaStream_t s);
+// d[e] = sum of v[row]^T x[t] over e's rows: d [L][r][C], or (transposed) [L][C][r]
+cudaError_t launch_lora_outer(const LoraPlan &p, const float *v, const void *x, bool transposed, int dtype, void *d, int C, cudaStream_t s);
+
+}  // namespace zffn

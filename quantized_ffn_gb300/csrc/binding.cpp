@@ -1,5 +1,5 @@
-// binding.cpp -- the Python binding of the 8-bit and sorting entry points as a
-// native module: it checks each tensor's type, shape, place and contiguity, makes
+// binding.cpp -- the Python binding of the 8-bit, sorting, bf16 and adapter entry points as
+// a native module: it checks each tensor's type, shape, place and contiguity, makes
 // the outputs that are not given, and calls the C ABI on the current (or given)
 // stream.  A small call is bound by what the host does: the sort, dispatch and
 // combine of one token take 6.5 us on the GPU, and 8.7 to 9.6 us of host time from
@@ -36,6 +36,12 @@ struct Api {
     decltype(&zffn_moe_combine) combine;
     decltype(&zffn_moe_combine_grad) combine_grad;
     decltype(&zffn_moe_swiglu_fp8) swiglu;
+    decltype(&zffn_bf16_matmul) bf16_matmul;
+    decltype(&zffn_bf16_matmul_grad_w) bf16_matmul_grad_w;
+    decltype(&zffn_swiglu) plain_swiglu;
+    decltype(&zffn_swiglu_grad) plain_swiglu_grad;
+    decltype(&zffn_lora_add) lora_add;
+    decltype(&zffn_lora_grad) lora_grad;
 } api{};
 PyObject *g_fail = nullptr;   // (status, name) -> raises ZffnError
 
@@ -432,6 +438,168 @@ PyObject *moe_swiglu_fp8(PyObject *const *a) {
     return y.object();
 }
 
+// An output that may be given: its type is the given one's, else `type`.
+ScalarType given_type(PyObject *o, const char *name, ScalarType type) {
+    return o == Py_None ? type : tensor(o, name).scalar_type();
+}
+
+// (a, w, offsets, transposed, y, dtype, stream) -> y
+PyObject *bf16_matmul(PyObject *const *a) {
+    const at::Tensor &x = tensor(a[0], "a"), &w = tensor(a[1], "w");
+    const bool grouped = a[2] != Py_None;
+    const int transposed = PyObject_IsTrue(a[3]);
+    if (transposed < 0) throw Raised{};
+    dims(x, "a", 2);
+    dims(w, "w", grouped ? 3 : 2);
+    const int64_t M = x.size(0), K = x.size(1), N = w.size(transposed ? -1 : -2), E = grouped ? w.size(0) : 1;
+    const int64_t ws[3] = {E, transposed ? K : N, transposed ? N : K}, ys[2] = {M, N}, os[1] = {E + 1};
+    const int skip = grouped ? 0 : 1;
+    const void *px = ptr(x, "a", kBF16, x.sizes());
+    const void *pw = ptr(w, "w", kBF16, Sizes(ws + skip, 3 - skip));
+    const int32_t *po = grouped ? i32(a[2], "offsets", os) : nullptr;
+    const Stream on(a[6]);
+    Output y(a[4], "y", ys, given_type(a[4], "y", type_of(a[5])), x);
+    const int yd = dtype_of(y.t, "y");
+    void *py = ptr(y.t, "y", y.t.scalar_type(), ys);
+    const int m = narrow(M, "M"), n = narrow(N, "N"), k = narrow(K, "K"), e = narrow(E, "E");
+    call("zffn_bf16_matmul", [&] { return api.bf16_matmul(px, pw, po, transposed, yd, py, m, n, k, e, on.s); });
+    return y.object();
+}
+
+// (dy, a, offsets, dw, dtype, stream) -> dw
+PyObject *bf16_matmul_grad_w(PyObject *const *a) {
+    const at::Tensor &d = tensor(a[0], "dy"), &x = tensor(a[1], "a");
+    dims(d, "dy", 2);
+    dims(x, "a", 2);
+    const bool grouped = a[2] != Py_None;
+    const int64_t M = x.size(0), K = x.size(1), N = d.size(1), ds[2] = {M, N};
+    int64_t E = 1;
+    if (grouped) {
+        const at::Tensor &o = tensor(a[2], "offsets");
+        dims(o, "offsets", 1);
+        E = o.size(0) - 1;
+        if (E < 1) throw ValueError("offsets must have shape (E + 1,)");
+    }
+    const int64_t ws[3] = {E, N, K}, os[1] = {E + 1};
+    const int skip = grouped ? 0 : 1;
+    const void *pd = ptr(d, "dy", kBF16, ds), *px = ptr(x, "a", kBF16, x.sizes());
+    const int32_t *po = grouped ? i32(a[2], "offsets", os) : nullptr;
+    const Stream on(a[5]);
+    Output dw(a[3], "dw", Sizes(ws + skip, 3 - skip), given_type(a[3], "dw", type_of(a[4])), x);
+    const int wd = dtype_of(dw.t, "dw");
+    void *pw = ptr(dw.t, "dw", dw.t.scalar_type(), Sizes(ws + skip, 3 - skip));
+    const int m = narrow(M, "M"), n = narrow(N, "N"), k = narrow(K, "K"), e = narrow(E, "E");
+    call("zffn_bf16_matmul_grad_w", [&] { return api.bf16_matmul_grad_w(pd, px, po, wd, pw, m, n, k, e, on.s); });
+    return dw.object();
+}
+
+// (gu, h, stream) -> h
+PyObject *swiglu(PyObject *const *a) {
+    const at::Tensor &gu = tensor(a[0], "gu");
+    dims(gu, "gu", 2);
+    if (gu.size(1) % 2) throw ValueError("gu must have an even number of columns");
+    const int64_t R = gu.size(0), I = gu.size(1) / 2, hs[2] = {R, I};
+    const int dtype = dtype_of(gu, "gu");
+    const void *pg = place(gu, "gu");
+    const Stream on(a[2]);
+    Output h(a[1], "h", hs, gu.scalar_type(), gu);
+    void *ph = ptr(h.t, "h", gu.scalar_type(), hs);
+    call("zffn_swiglu", [&] { return api.plain_swiglu(dtype, pg, ph, R, I, on.s); });
+    return h.object();
+}
+
+// (dh, gu, dgu, stream) -> dgu
+PyObject *swiglu_grad(PyObject *const *a) {
+    const at::Tensor &gu = tensor(a[1], "gu");
+    dims(gu, "gu", 2);
+    if (gu.size(1) % 2) throw ValueError("gu must have an even number of columns");
+    const int64_t R = gu.size(0), I = gu.size(1) / 2, hs[2] = {R, I};
+    const int dtype = dtype_of(gu, "gu");
+    const void *pg = place(gu, "gu"), *pd = ptr(a[0], "dh", gu.scalar_type(), hs);
+    const Stream on(a[3]);
+    Output out(a[2], "dgu", gu.sizes(), gu.scalar_type(), gu);
+    void *po = ptr(out.t, "dgu", gu.scalar_type(), gu.sizes());
+    call("zffn_swiglu_grad", [&] { return api.plain_swiglu_grad(dtype, pd, pg, po, R, I, on.s); });
+    return out.object();
+}
+
+// What both adapter calls check: x [T, K], A [L, r, K], B [L, N, r], the plan of top_k = 1, the scales.
+struct Lora {
+    int64_t T, K, L, r, N;
+    const void *x, *A, *B;
+    const int32_t *row_slot, *slot_row, *offsets;
+    const float *scale;
+    Lora(PyObject *x_, PyObject *A_, PyObject *B_, PyObject *plan, PyObject *scale_) {
+        const at::Tensor &tx = tensor(x_, "x"), &ta = tensor(A_, "A"), &tb = tensor(B_, "B");
+        dims(tx, "x", 2);
+        dims(ta, "A", 3);
+        dims(tb, "B", 3);
+        T = tx.size(0), K = tx.size(1), L = ta.size(0), r = ta.size(1), N = tb.size(1);
+        const int64_t as[3] = {L, r, K}, bs[3] = {L, N, r}, rs[1] = {T}, ss[2] = {T, 1}, os[1] = {L + 1}, ls[1] = {L};
+        x = ptr(tx, "x", kBF16, tx.sizes());
+        A = ptr(ta, "A", kBF16, as);
+        B = ptr(tb, "B", kBF16, bs);
+        row_slot = i32(plan_item(plan, 0), "row_slot", rs);
+        slot_row = i32(plan_item(plan, 1), "slot_row", ss);
+        offsets = i32(plan_item(plan, 2), "offsets", os);
+        scale = scale_ == Py_None ? nullptr : f32(scale_, "scale", ls);
+        narrow(T, "T"), narrow(K, "K"), narrow(L, "L"), narrow(r, "r"), narrow(N, "N");
+    }
+};
+
+// (x, A, B, plan, scale, base, out, v, dtype, stream) -> (out, v)
+PyObject *lora_add(PyObject *const *a) {
+    const Lora p(a[0], a[1], a[2], a[3], a[4]);
+    const at::Tensor &x = tensor(a[0], "x");
+    const int64_t os[2] = {p.T, p.N}, vs[2] = {p.T, p.r};
+    const ScalarType type = given_type(a[5], "base", given_type(a[6], "out", type_of(a[8])));
+    const void *pb = a[5] == Py_None ? nullptr : ptr(a[5], "base", type, os);
+    const Stream on(a[9]);
+    Output out(a[6], "out", os, type, x), v(a[7], "v", vs, kF32, x);
+    const int dtype = dtype_of(out.t, "out");
+    void *po = ptr(out.t, "out", type, os);
+    float *pv = static_cast<float *>(ptr(v.t, "v", kF32, vs));
+    call("zffn_lora_add", [&] {
+        return api.lora_add(p.x, p.A, p.B, p.scale, p.row_slot, p.slot_row, p.offsets, dtype, pb, po, pv, (int)p.T, (int)p.N, (int)p.K, (int)p.r,
+                            (int)p.L, on.s);
+    });
+    return pair(out.object(), v.object());
+}
+
+// (dy, x, v, A, B, plan, scale, base, dx, dA, dB, dtype, stream) -> (dx, dA, dB)
+PyObject *lora_grad(PyObject *const *a) {
+    const Lora p(a[1], a[3], a[4], a[5], a[6]);
+    const at::Tensor &x = tensor(a[1], "x"), &tA = tensor(a[3], "A"), &tB = tensor(a[4], "B");
+    const int64_t ds[2] = {p.T, p.N}, vs[2] = {p.T, p.r};
+    const void *pd = ptr(a[0], "dy", kBF16, ds);
+    const float *pv = f32(a[2], "v", vs);
+    const ScalarType type = given_type(a[7], "base", given_type(a[8], "dx", type_of(a[11])));
+    const ScalarType wtype = given_type(a[9], "dA", given_type(a[10], "dB", type_of(a[11])));
+    const void *pb = a[7] == Py_None ? nullptr : ptr(a[7], "base", type, x.sizes());
+    const Stream on(a[12]);
+    Output dx(a[8], "dx", x.sizes(), type, x), dA(a[9], "dA", tA.sizes(), wtype, x), dB(a[10], "dB", tB.sizes(), wtype, x);
+    const Output dv(Py_None, "dv", vs, kF32, x);
+    const int xd = dtype_of(dx.t, "dx"), wd = dtype_of(dA.t, "dA");
+    void *px = ptr(dx.t, "dx", type, x.sizes()), *pA = ptr(dA.t, "dA", wtype, tA.sizes()), *pB = ptr(dB.t, "dB", wtype, tB.sizes());
+    float *pdv = static_cast<float *>(ptr(dv.t, "dv", kF32, vs));
+    call("zffn_lora_grad", [&] {
+        return api.lora_grad(pd, p.x, pv, p.A, p.B, p.scale, p.row_slot, p.slot_row, p.offsets, xd, pb, px, wd, pA, pB, pdv, (int)p.T, (int)p.N,
+                             (int)p.K, (int)p.r, (int)p.L, on.s);
+    });
+    PyObject *out = PyTuple_New(3);
+    if (!out) throw Raised{};
+    const Output *items[3] = {&dx, &dA, &dB};
+    for (int i = 0; i < 3; ++i) {
+        PyObject *o = items[i]->object();
+        if (!o) {
+            Py_DECREF(out);
+            throw Raised{};
+        }
+        PyTuple_SET_ITEM(out, i, o);
+    }
+    return out;
+}
+
 template <PyObject *(*F)(PyObject *const *), int N>
 PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
     HANDLE_TH_ERRORS
@@ -474,6 +642,7 @@ PyObject *bind(PyObject *, PyObject *const *args, Py_ssize_t n) {
 PyMethodDef methods[] = {
     ENTRY(fp8_quantize, 5), ENTRY(fp8_dequant, 5), ENTRY(fp8_matmul, 8), ENTRY(fp8_experts, 12), ENTRY(moe_sort, 4),
     ENTRY(moe_dispatch, 6), ENTRY(moe_combine, 6), ENTRY(moe_combine_grad, 7), ENTRY(moe_swiglu_fp8, 12),
+    ENTRY(bf16_matmul, 7), ENTRY(bf16_matmul_grad_w, 6), ENTRY(swiglu, 3), ENTRY(swiglu_grad, 4), ENTRY(lora_add, 10), ENTRY(lora_grad, 13),
     {"bind", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(bind)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_zffn_native", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -1,5 +1,5 @@
-"""Python binding of libzffn (include/zffn.h): argument marshalling only, for the 8-bit and sorting
-entry points in a native module (csrc/binding.cpp).
+"""Python binding of libzffn (include/zffn.h): argument marshalling only, for the 8-bit, sorting, bf16
+and adapter entry points in a native module (csrc/binding.cpp).
 
 Every function takes CUDA tensors, checks dtype/shape/contiguity, and passes
 raw device pointers and the current (or given) CUDA stream to the C ABI.  None is
@@ -78,6 +78,13 @@ def load() -> ctypes.CDLL:
                 "zffn_moe_combine": ([I32, P, P, P, P, I32, I32, I32, I32, P], I32),
                 "zffn_moe_combine_grad": ([I32, P, P, P, P, P, P, P, I32, I32, I32, P], I32),
                 "zffn_moe_swiglu_fp8": ([P, P, P, P, P, P, P, P, P, P, I32, I32, I32, I32, I32, I32, P], I32),
+                "zffn_bf16_matmul": ([P, P, P, I32, I32, P, I32, I32, I32, I32, P], I32),
+                "zffn_bf16_matmul_grad_w": ([P, P, P, I32, P, I32, I32, I32, I32, P], I32),
+                "zffn_swiglu": ([I32, P, P, I64, I64, P], I32),
+                "zffn_swiglu_grad": ([I32, P, P, P, I64, I64, P], I32),
+                "zffn_lora_add": ([P, P, P, P, P, P, P, I32, P, P, P, I32, I32, I32, I32, I32, P], I32),
+                "zffn_lora_grad": ([P, P, P, P, P, P, P, P, P, I32, P, P, I32, P, P, P, I32, I32, I32, I32, I32, P],
+                                   I32),
                 "zffn_rmsnorm_bf16": ([P, P, ctypes.c_float, P, I32, I32, P], I32),
                 "zffn_swiglu_q4k_prenorm_residual": ([P, P, ctypes.c_float, P, P, P, I32, I32, I32, P],
                                                      I32),
@@ -314,7 +321,9 @@ DT_F32, DT_BF16 = 0, 1
 NATIVE_PATH = os.path.join(_HERE, "_lib", "_zffn_native.so")
 _native_module = None
 _NATIVE_CALLS = ("zffn_fp8_quantize", "zffn_fp8_dequant", "zffn_fp8_matmul", "zffn_fp8_experts", "zffn_moe_sort",
-                 "zffn_moe_dispatch", "zffn_moe_combine", "zffn_moe_combine_grad", "zffn_moe_swiglu_fp8")
+                 "zffn_moe_dispatch", "zffn_moe_combine", "zffn_moe_combine_grad", "zffn_moe_swiglu_fp8",
+                 "zffn_bf16_matmul", "zffn_bf16_matmul_grad_w", "zffn_swiglu", "zffn_swiglu_grad", "zffn_lora_add",
+                 "zffn_lora_grad")
 
 
 def _fail(status: int, what: str):
@@ -418,6 +427,59 @@ def moe_swiglu_fp8(x: torch.Tensor, expert_ids: torch.Tensor, expert_weights: to
     x bf16 [T, H], weights stacked [E, ...] as for fp8_experts."""
     return (_native_module or _native()).moe_swiglu_fp8(x, expert_ids, expert_weights, Wg, sg, Wu, su, Wd, sd, y,
                                                         accumulate, stream)
+
+
+# ---- training and adapting layers in bf16 ---------------------------------------------------
+
+def bf16_matmul(a: torch.Tensor, w: torch.Tensor, offsets: Optional[torch.Tensor] = None, transposed: bool = False,
+                y: Optional[torch.Tensor] = None, dtype=torch.bfloat16, stream=None) -> torch.Tensor:
+    """y[M, N] = a w^T of bf16 matrices a [M, K], w [N, K]; transposed: y = a w with w [K, N], the
+    gradient of the first by a.  With offsets (int32 [E + 1], MoePlan.offsets) w is stacked [E, ...]
+    and rows offsets[e]:offsets[e + 1] take expert e; rows of no expert become 0.  y: given (fp32 or
+    bf16), or made with `dtype`."""
+    return (_native_module or _native()).bf16_matmul(a, w, offsets, transposed, y, dtype, stream)
+
+
+def bf16_matmul_grad_w(dy: torch.Tensor, a: torch.Tensor, offsets: Optional[torch.Tensor] = None,
+                       dw: Optional[torch.Tensor] = None, dtype=torch.bfloat16, stream=None) -> torch.Tensor:
+    """dw[E, N, K] (without offsets [N, K]): the gradient of bf16_matmul(a, w, offsets) by w, the sum of
+    dy[m]^T a[m] over each expert's rows, 0 for an expert without rows.  dw: given (fp32 or bf16), or
+    made with `dtype`."""
+    return (_native_module or _native()).bf16_matmul_grad_w(dy, a, offsets, dw, dtype, stream)
+
+
+def swiglu(gu: torch.Tensor, h: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """h[R, I] = silu(g) * u of gu = [g | u] (bf16 or fp32 [R, 2 I]: one product with the gate and up
+    weights stacked)."""
+    return (_native_module or _native()).swiglu(gu, h, stream)
+
+
+def swiglu_grad(dh: torch.Tensor, gu: torch.Tensor, dgu: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """dgu[R, 2 I]: the gradient of swiglu(gu) for dh [R, I] of gu's type; dgu may be gu."""
+    return (_native_module or _native()).swiglu_grad(dh, gu, dgu, stream)
+
+
+def lora_add(x: torch.Tensor, A: torch.Tensor, B: torch.Tensor, plan: MoePlan, scale: Optional[torch.Tensor] = None,
+             base: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None, v: Optional[torch.Tensor] = None,
+             dtype=torch.bfloat16, stream=None):
+    """(out[T, N], v[T, r]): out[t] = base[t] + v B_e^T with v = scale_e x[t] A_e^T, e the adapter of token t,
+    for tokens of many adapters at once beside a projection that they share (base: its result, fp32 or
+    bf16; None for zeros).  x bf16 [T, K], A bf16 [L, r, K], B bf16 [L, N, r], scale fp32 [L];
+    plan = moe_sort(ids[:, None], L), made once for all projections of a step; a token whose id is outside
+    [0, L) keeps base.  out: given (it may be base), or made like base, or with `dtype`.  v fp32, the
+    sorted rows' (0 in rows of no token): lora_grad needs it again."""
+    return (_native_module or _native()).lora_add(x, A, B, plan, scale, base, out, v, dtype, stream)
+
+
+def lora_grad(dy: torch.Tensor, x: torch.Tensor, v: torch.Tensor, A: torch.Tensor, B: torch.Tensor, plan: MoePlan,
+              scale: Optional[torch.Tensor] = None, base: Optional[torch.Tensor] = None,
+              dx: Optional[torch.Tensor] = None, dA: Optional[torch.Tensor] = None, dB: Optional[torch.Tensor] = None,
+              dtype=torch.bfloat16, stream=None):
+    """(dx[T, K], dA, dB): the gradients of lora_add for dy bf16 [T, N] with the v that it returned:
+    dx[t] = base[t] + dv A_e with dv = scale_e dy[t] B_e (base: what the shared projection gives back to
+    x, or None), dA_e = sum dv^T x[t], dB_e = sum dy[t]^T v, 0 for an adapter without tokens.  dx: given
+    (it may be base), or made like base, or with `dtype`; dA and dB (of one type) given, or with `dtype`."""
+    return (_native_module or _native()).lora_grad(dy, x, v, A, B, plan, scale, base, dx, dA, dB, dtype, stream)
 
 
 def _host(t: torch.Tensor, name: str, dtype, shape):
