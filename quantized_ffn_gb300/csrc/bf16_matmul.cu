@@ -1,116 +1,486 @@
-// bf16_matmul.cu -- products of rows grouped by expert or adapter, and the sums of
-// outer products over a group's rows.  One thread sums one value.
+// bf16_matmul.cu -- products of bf16 matrices on the 5th-generation tensor cores, dense
+// or grouped by expert, and their gradients:
+//     forward    y[m][n]     = sum_k a[m][k] w[e][n][k]
+//     back       y[m][n]     = sum_k a[m][k] w[e][k][n]
+//     weights    dw[e][n][k] = sum_m dy[m][n] a[m][k]      over expert e's rows m
+// Sums stay in tensor memory in fp32 over the whole contraction and are rounded once.
+// An operand whose contracted index runs along its rows' memory is taken K-major, the
+// other ones (w in `back`, both in `weights`) as they lie in memory, MN-major: nothing
+// is transposed on the way.
+#include <atomic>
+
 #include "bf16.h"
+#include "groups.cuh"
 #include "launch.cuh"
+#include "roles.cuh"
 
 namespace zffn {
-namespace {
+namespace b16 {
 
-__device__ __forceinline__ float value(const void *p, int64_t i, bool bf16) {
-    return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]) : static_cast<const float *>(p)[i];
+enum Kind { FORWARD, BACK, WEIGHTS };
+constexpr int KB = 64;            // contracted values of a stage: rows of 128 bytes, or 64 rows
+
+// ---- pieces -----------------------------------------------------------------
+
+// 3-D TMA tile load, completion counted on `bar`.
+__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, uint64_t *bar, int c0, int c1, int c2) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
 }
-__device__ __forceinline__ void put(void *p, int64_t i, bool bf16, float v) {
-    if (bf16) static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(v);
-    else static_cast<float *>(p)[i] = v;
+__device__ __forceinline__ void tma_load_3d_pair(void *dst, const CUtensorMap *map, uint32_t bar, int c0, int c1, int c2) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
 }
-// First row of group g (g == E: of the rows of none): the largest offset up to it.
-__device__ int first_row(const int32_t *offsets, int g, int E, int M) {
-    if (!offsets) return g == 0 ? 0 : M;
-    int lo = 0;
-    for (int i = 0; i <= min(g, E); ++i) lo = max(lo, min(max(offsets[i], 0), M));
-    return g > E ? M : lo;
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, uint32_t src, int c0, int c1, int c2) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(src), "r"(c0), "r"(c1), "r"(c2)
+                 : "memory");
+}
+// Shared-memory matrix descriptor of an MN-major operand, 128-byte swizzle: boxes of 64
+// values of the free index (128 bytes) by 64 of the contracted one, 8192 bytes each;
+// groups of 8 of the contracted index lie 1024 bytes apart.
+__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr) {
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+    d |= (uint64_t)(8192 >> 4) << 16;          // from box to box
+    d |= (uint64_t)(1024 >> 4) << 32;          // from 8 contracted values to the next
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+// Instruction descriptor: A = B = bf16, D = fp32.
+__host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, bool a_mn, bool b_mn) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) |
+           ((uint32_t)(M >> 4) << 24);
+}
+// What 16 contracted values are in units of a descriptor's address.
+__device__ __forceinline__ uint64_t k_step(bool mn) { return mn ? 16 * 128 / 16 : 32 / 16; }
+__device__ __forceinline__ uint32_t bf16x2(uint32_t lo, uint32_t hi) {
+    const __nv_bfloat162 two = __floats2bfloat162_rn(__uint_as_float(lo), __uint_as_float(hi));
+    return *reinterpret_cast<const uint32_t *>(&two);
 }
 
-struct Rows {
-    const void *x, *w, *base;
+struct Params {
+    const int32_t *offsets;
     void *y;
-    const int32_t *offsets, *in_row, *out_row, *slot_row;   // in_row, out_row: row -> row of x, of y (nullptr: itself)
-    const float *scale;
-    bool x_bf16, y_bf16;
+    int *err;
     int M, N, K, E;
-    int64_t wn, wk;   // strides of w by n and k
+    int n_tiles;        // tiles of w's rows; weights: of dw[e]'s columns
+    int m_tiles;        // weights: tiles of dw[e]'s rows
+    int y_bf16;
+    int vec;            // y's rows are 16-byte multiples
 };
-// y[out(m)][n] = base + scale sum_k x[in(m)][k] w[e][n][k]
-__global__ void rows_kernel(const Rows p) {
-    const int g = blockIdx.y, n = blockIdx.x * 32 + threadIdx.x;
-    const int lo = first_row(p.offsets, g, p.E, p.M), hi = first_row(p.offsets, g + 1, p.E, p.M);
-    if (n >= p.N) return;
-    for (int m = lo + blockIdx.z * blockDim.y + threadIdx.y; m < hi; m += gridDim.z * blockDim.y) {
-        const int in = p.in_row ? p.in_row[m] : m, out = p.out_row ? p.out_row[m] : m;
-        const bool some = g < p.E && (unsigned)in < (unsigned)p.M;
-        float sum = 0.0f;
-        if (some)
-            for (int k = 0; k < p.K; ++k)
-                sum += value(p.x, (int64_t)in * p.K + k, p.x_bf16) * value(p.w, (int64_t)g * p.N * p.K + n * p.wn + k * p.wk, true);
-        if (p.scale && some) sum *= p.scale[g];
-        if ((unsigned)out >= (unsigned)p.M || (p.out_row && !some)) continue;
-        const int64_t at = (int64_t)out * p.N + n;
-        put(p.y, at, p.y_bf16, (p.base ? value(p.base, at, p.y_bf16) : 0.0f) + sum);
-    }
-}
-// tokens of no adapter: y = base or 0
-__global__ void rest_kernel(const Rows p) {
-    const int n = blockIdx.x * 32 + threadIdx.x;
-    if (n >= p.N) return;
-    for (int t = blockIdx.z * blockDim.y + threadIdx.y; t < p.M; t += gridDim.z * blockDim.y)
-        if (p.slot_row[t] < 0) put(p.y, (int64_t)t * p.N + n, p.y_bf16, p.base ? value(p.base, (int64_t)t * p.N + n, p.y_bf16) : 0.0f);
-}
-cudaError_t launch_rows(const Rows &p, cudaStream_t s) {
-    const dim3 grid((p.N + 31) / 32, p.E + (p.offsets ? 1 : 0), p.M / p.E / 8 + 1 < 64 ? p.M / p.E / 8 + 1 : 64);
-    rows_kernel<<<grid, dim3(32, 8), 0, s>>>(p);
-    if (p.slot_row && p.y != p.base) rest_kernel<<<dim3((p.N + 31) / 32, 1, 64), dim3(32, 8), 0, s>>>(p);
-    return cudaGetLastError();
-}
+// a: forward, back: [M][K]; weights: dy.  w: w; weights: a.  a16, w16: weights: the same in
+// boxes of 16 rows.  y: what the stores go to.
+struct Maps {
+    CUtensorMap a, w, y, a16, w16;
+};
 
-struct Outer {
-    const void *a, *b;
-    void *d;
-    const int32_t *offsets, *a_row, *b_row;
-    bool a_bf16, b_bf16, d_bf16;
-    int M, NA, NB, E;
+// ---------------------------------------------------------------------------
+// Many rows: tiles of 128 rows (a CTA pair: 256) times 256 columns of the result, a
+// (weights: dy) on the MMA's M side.  Persistent: every cluster takes tiles in turn;
+// two accumulators in tensor memory, so that one is taken out while the next tile's
+// MMAs run.
+//
+// Roles: warps 0 .. 3 take a tile out of tensor memory (32 rows each) and write it,
+// warp 4 loads by TMA, warp 5 issues the MMAs.
+// ---------------------------------------------------------------------------
+template <int KIND_, bool PAIR_>
+struct LargeCfg {
+    static constexpr int KIND = KIND_;
+    static constexpr bool PAIR = PAIR_;
+    static constexpr int CTAS = PAIR ? 2 : 1;
+    static constexpr int TM = 128 * CTAS, TN = 256;
+    static constexpr bool A_MN = KIND == WEIGHTS, W_MN = KIND != FORWARD;
+    static constexpr int W_ROWS = TN / CTAS;                 // of the tile's columns that a CTA holds
+    static constexpr int A_BYTES = 128 * 128;
+    static constexpr int STAGE = A_BYTES + W_ROWS * 128;
+    static constexpr int NS = PAIR ? 6 : 4;
+    static constexpr int EPI = 4;
+    static constexpr int THREADS = (EPI + 2) * 32;
+    static constexpr int OUT_BYTES = 8192;                   // a warp's two boxes of 32 rows x 128 bytes
+    static constexpr int OFF_OUT = NS * STAGE;
+    static constexpr int OFF_BAR = OFF_OUT + EPI * OUT_BYTES;
+    static constexpr int SMEM = OFF_BAR + (2 * NS + 5) * 8 + 8 + 1024;
+    using Walk = GroupWalk<TM, 8, KIND == WEIGHTS>;
 };
-// d[e][i][j] = sum over e's rows of a[.][i] b[.][j]
-__global__ void outer_kernel(const Outer p) {
-    const int g = blockIdx.z;
-    const int lo = first_row(p.offsets, g, p.E, p.M), hi = first_row(p.offsets, g + 1, p.E, p.M);
-    const int j = blockIdx.x * 32 + threadIdx.x;
-    for (int i = blockIdx.y * 8 + threadIdx.y; i < p.NA; i += gridDim.y * 8) {
-        if (j >= p.NB) return;
-        float sum = 0.0f;
-        for (int m = lo; m < hi; ++m) {
-            const int ra = p.a_row ? p.a_row[m] : m, rb = p.b_row ? p.b_row[m] : m;
-            if ((unsigned)ra >= (unsigned)p.M || (unsigned)rb >= (unsigned)p.M) continue;
-            sum += value(p.a, (int64_t)ra * p.NA + i, p.a_bf16) * value(p.b, (int64_t)rb * p.NB + j, p.b_bf16);
+
+template <class C>
+__global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_constant__ Maps maps, const Params p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint64_t *s_full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
+    uint64_t *s_empty = s_full + C::NS, *t_full = s_empty + C::NS, *t_empty = t_full + 2, *done = t_empty + 2;
+    int *info = reinterpret_cast<int *>(done + 1);           // abort, TMEM base
+    volatile int *abort_flag = info;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = C::PAIR ? (int)cluster_ctarank() : 0;
+    constexpr bool GRAD = C::KIND == WEIGHTS;
+
+    if (warp == C::EPI && lane == 0) {
+        info[0] = 0;
+        for (int i = 0; i < C::NS; ++i) { mbar_init(&s_full[i], 1); mbar_init(&s_empty[i], 1); }
+        for (int i = 0; i < 2; ++i) { mbar_init(&t_full[i], 1); mbar_init(&t_empty[i], C::EPI * C::CTAS); }
+        mbar_init(done, 1);
+        fence_mbarrier_init();
+        prefetch_tensormap(&maps.a);
+        prefetch_tensormap(&maps.w);
+    }
+    if (warp == C::EPI + 1) {
+        uint32_t *dst = reinterpret_cast<uint32_t *>(info + 1);
+        if constexpr (C::PAIR) { tmem_alloc_pair(dst, 512); tmem_relinquish_pair(); }
+        else { tmem_alloc(dst, 512); tmem_relinquish(); }
+        tc_fence_before();
+    }
+    __syncthreads();
+    grid_wait();
+    grid_launch_dependents();          // (this block has its tensor memory)
+    if (C::PAIR) cluster_sync_all();   // the peer's barriers are set up
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(info + 1);
+    typename C::Walk wk;
+    wk.start(p.offsets, p.M, p.E, GRAD ? p.m_tiles * p.n_tiles : p.n_tiles, !GRAD, blockIdx.x / C::CTAS);
+    const int step = gridDim.x / C::CTAS;
+    // stages of the tile at hand (none: zeros)
+    auto blocks = [&] { return GRAD ? (wk.rows + KB - 1) / KB : wk.e < p.E ? (p.K + KB - 1) / KB : 0; };
+    // groups of 16 contracted values in stage i
+    auto steps = [&](int i) { return (min(KB, (GRAD ? wk.rows : p.K) - i * KB) + 15) / 16; };
+
+    if (warp == C::EPI) {
+        // ---- TMA producer
+        const uint32_t full0 = C::PAIR ? mapa_shared(smem_u32(s_full), 0) : 0;
+        uint32_t it = 0;
+        bool ok = true;
+        for (; ok && wk.get(); wk.t += step) {
+            const int nb = blocks();
+            const int mt = GRAD ? wk.nt / p.n_tiles : 0, nt = GRAD ? wk.nt - mt * p.n_tiles : wk.nt;
+            for (int i = 0; i < nb && lane == 0; ++i, ++it) {
+                const uint32_t s = it % C::NS;
+                if (it >= C::NS && !bar_wait(&s_empty[s], ((it / C::NS) & 1) ^ 1, abort_flag, p.err)) { ok = false; break; }
+                uint8_t *sa = smem + s * C::STAGE, *sw = sa + C::A_BYTES;
+                if constexpr (GRAD) {
+                    const int row = wk.row0 + i * KB, n = steps(i);
+                    if (n == KB / 16) {
+                        mbar_arrive_expect_tx(&s_full[s], C::STAGE);
+#pragma unroll
+                        for (int b = 0; b < 2; ++b) tma_load_2d(sa + b * 8192, &maps.a, &s_full[s], mt * 128 + b * 64, row);
+#pragma unroll
+                        for (int b = 0; b < 4; ++b) tma_load_2d(sw + b * 8192, &maps.w, &s_full[s], nt * 256 + b * 64, row);
+                    } else {
+                        // (an expert's last rows: no more of the next one's than the MMA takes)
+                        mbar_arrive_expect_tx(&s_full[s], n * 6 * 2048);
+                        for (int j = 0; j < n; ++j) {
+#pragma unroll
+                            for (int b = 0; b < 2; ++b)
+                                tma_load_2d(sa + b * 8192 + j * 2048, &maps.a16, &s_full[s], mt * 128 + b * 64, row + j * 16);
+#pragma unroll
+                            for (int b = 0; b < 4; ++b)
+                                tma_load_2d(sw + b * 8192 + j * 2048, &maps.w16, &s_full[s], nt * 256 + b * 64, row + j * 16);
+                        }
+                    }
+                } else {
+                    if (rank == 0) mbar_arrive_expect_tx(&s_full[s], C::STAGE * C::CTAS);
+                    const int col = wk.nt * C::TN + rank * C::W_ROWS;
+                    if constexpr (C::PAIR) tma_load_2d_pair(sa, &maps.a, full0 + s * 8, i * KB, wk.row0 + 128 * rank);
+                    else tma_load_2d(sa, &maps.a, &s_full[s], i * KB, wk.row0);
+                    if constexpr (C::KIND == FORWARD) {
+                        if constexpr (C::PAIR) tma_load_3d_pair(sw, &maps.w, full0 + s * 8, i * KB, col, wk.e);
+                        else tma_load_3d(sw, &maps.w, &s_full[s], i * KB, col, wk.e);
+                    } else {
+#pragma unroll
+                        for (int b = 0; b < C::W_ROWS / 64; ++b) {
+                            if constexpr (C::PAIR) tma_load_3d_pair(sw + b * 8192, &maps.w, full0 + s * 8, col + b * 64, i * KB, wk.e);
+                            else tma_load_3d(sw + b * 8192, &maps.w, &s_full[s], col + b * 64, i * KB, wk.e);
+                        }
+                    }
+                }
+            }
+            ok = __shfl_sync(0xffffffffu, ok && !*abort_flag, 0);
         }
-        put(p.d, ((int64_t)g * p.NA + i) * p.NB + j, p.d_bf16, sum);
+        // (a launch that gave up: wait for the copies in flight before leaving)
+        if (lane == 0 && *abort_flag && rank == 0)
+            for (uint32_t j = it > C::NS ? it - C::NS : 0; j < it; ++j)
+                mbar_wait(&s_full[j % C::NS], (j / C::NS) & 1, nullptr, p.err);
+        __syncwarp();
+    } else if (warp == C::EPI + 1) {
+        // ---- MMA issuer (of a pair: its first CTA)
+        constexpr uint32_t idesc = idesc_bf16_f32(C::TM, C::TN, C::A_MN, C::W_MN);
+        if (rank == 0) {
+            uint32_t it = 0, acc = 0;
+            bool ok = true;
+            for (; ok && wk.get(); wk.t += step) {
+                const int nb = blocks();
+                if (nb == 0) continue;
+                const uint32_t b = acc & 1, dst = tmem + b * 256;
+                ok = acc < 2 || bar_wait(&t_empty[b], ((acc >> 1) & 1) ^ 1, abort_flag, p.err);
+                for (int i = 0; i < nb; ++i, ++it) {
+                    const uint32_t s = it % C::NS;
+                    ok = ok && bar_wait(&s_full[s], (it / C::NS) & 1, abort_flag, p.err);
+                    if (!__all_sync(0xffffffffu, ok)) break;
+                    const uint32_t sa = smem_u32(smem) + s * C::STAGE, sw = sa + C::A_BYTES;
+                    const int n = steps(i);
+                    if constexpr (GRAD) {
+                        // rows of the next expert in the last 16: zeros, in both operands
+                        // (whatever they hold may be infinite)
+                        const int valid = wk.rows - i * KB;
+                        if (valid < n * 16) {
+                            const int each = (n * 16 - valid) * 8;   // chunks of 16 bytes in a box
+                            for (int c = lane; c < 6 * each; c += 32) {
+                                const int box = c / each;
+                                st_shared_v4(sa + box * 8192 + valid * 128 + (c - box * each) * 16, 0, 0, 0, 0);
+                            }
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                        }
+                    }
+                    tc_fence_after();
+                    const uint64_t ad = C::A_MN ? smem_desc_mn_sw128(sa) : smem_desc_k_sw128(sa);
+                    const uint64_t wd = C::W_MN ? smem_desc_mn_sw128(sw) : smem_desc_k_sw128(sw);
+                    if (elect_one()) {
+#pragma unroll
+                        for (int k = 0; k < KB / 16; ++k) {
+                            if (k >= n) break;
+                            if constexpr (C::PAIR) tc_mma_bf16_pair(dst, ad + k * k_step(C::A_MN), wd + k * k_step(C::W_MN), idesc, (i | k) != 0);
+                            else tc_mma_bf16(dst, ad + k * k_step(C::A_MN), wd + k * k_step(C::W_MN), idesc, (i | k) != 0);
+                        }
+                        if constexpr (C::PAIR) {
+                            tc_commit_pair(&s_empty[s]);
+                            if (i == nb - 1) tc_commit_pair(&t_full[b]);
+                        } else {
+                            tc_commit(&s_empty[s]);
+                            if (i == nb - 1) tc_commit(&t_full[b]);
+                        }
+                    }
+                    __syncwarp();
+                }
+                ++acc;
+                ok = __all_sync(0xffffffffu, ok && !*abort_flag);
+            }
+            if (elect_one()) {
+                if constexpr (C::PAIR) tc_commit_pair(done);
+                else tc_commit(done);
+            }
+            __syncwarp();
+        }
+    } else {
+        // ---- take out and write: thread = one row of the tile
+        const uint32_t taddr = tmem + ((uint32_t)(warp * 32) << 16);
+        const uint32_t empty0 = C::PAIR ? mapa_shared(smem_u32(t_empty), 0) : 0;
+        uint8_t *out = smem + C::OFF_OUT + warp * C::OUT_BYTES;
+        uint32_t acc = 0;
+        for (bool ok = true; ok && wk.get(); wk.t += step) {
+            const bool some = blocks() != 0;
+            const uint32_t b = acc & 1, from = taddr + b * 256;
+            if (some) {
+                ok = __all_sync(0xffffffffu, bar_wait(&t_full[b], (acc >> 1) & 1, abort_flag, p.err));
+                if (!ok) break;
+                tc_fence_after();
+                ++acc;
+            }
+            const int mt = GRAD ? wk.nt / p.n_tiles : 0, nt = GRAD ? wk.nt - mt * p.n_tiles : wk.nt;
+            const int wrow = GRAD ? mt * 128 + warp * 32 : 128 * rank + warp * 32;   // this warp's first row (of dw[e], of the tile)
+            const int left = GRAD ? p.N - wrow : wk.rows - wrow;
+            const int64_t row = GRAD ? wrow : wk.row0 + wrow;
+            const int cols = GRAD ? p.K : p.N;
+            auto at = [&](int box, int r, int chunk) { return out + box * 4096 + r * 128 + ((chunk ^ (r & 7)) << 4); };
+            // both boxes, from column n0 on, in elements of `elem` bytes
+            auto send = [&](int n0, auto elem_size) {
+                constexpr int elem = decltype(elem_size)::value, per = 128 / elem;
+                if (GRAD || (p.vec && left >= 32)) {
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        for (int x = 0; x < 2; ++x)
+                            if (n0 + x * per < cols && left > 0) {
+                                if constexpr (GRAD) tma_store_3d(&maps.y, smem_u32(out) + x * 4096, n0 + x * per, (int)row, wk.e);
+                                else tma_store_2d(&maps.y, smem_u32(out) + x * 4096, n0 + x * per, (int)row);
+                            }
+                        bulk_commit_group();
+                    }
+                    return;
+                }
+                // rows that are not all the tile's, or not 16-byte multiples: a row's bytes by
+                // neighbouring lanes
+                __syncwarp();
+                uint8_t *y = static_cast<uint8_t *>(p.y) + row * p.N * elem;
+                const int64_t pitch = (int64_t)p.N * elem;
+                for (int x = 0; x < 2; ++x) {
+                    const int col = n0 + x * per, bytes = min(per, p.N - col) * elem;
+                    if (p.vec) {
+                        for (int i = lane; i < 32 * 8; i += 32)
+                            if (i / 8 < left && i % 8 * 16 < bytes)
+                                *reinterpret_cast<uint4 *>(y + i / 8 * pitch + (int64_t)col * elem + i % 8 * 16) =
+                                    *reinterpret_cast<const uint4 *>(at(x, i / 8, i % 8));
+                    } else {
+#pragma unroll
+                        for (int l = 0; l < per / 32; ++l) {
+                            const int c = (lane + 32 * l) * elem;
+                            uint8_t *dst = y + (int64_t)col * elem + c;
+#pragma unroll 8
+                            for (int r = 0; r < 32; ++r) {
+                                const uint8_t *src = at(x, r, c >> 4) + (c & 15);
+                                if (r >= left || c >= bytes) continue;
+                                if constexpr (elem == 2) *reinterpret_cast<uint16_t *>(dst + r * pitch) = *reinterpret_cast<const uint16_t *>(src);
+                                else *reinterpret_cast<uint32_t *>(dst + r * pitch) = *reinterpret_cast<const uint32_t *>(src);
+                            }
+                        }
+                    }
+                }
+                __syncwarp();
+            };
+            // 32 columns of the tile (zeros where nothing was summed)
+            auto fetch = [&](int c, uint32_t (&d)[32]) {
+                if (some) tmem_ld_32x32b_x32(from + c, d);
+                else
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) d[j] = 0;
+            };
+            auto emptied = [&] {   // the boxes sent before have been read
+                if (lane == 0) bulk_wait_group_read<0>();
+                __syncwarp();
+            };
+            auto taken = [&] {     // the accumulator has been read
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if constexpr (C::PAIR) mbar_arrive_cluster(empty0 + b * 8);
+                    else mbar_arrive(&t_empty[b]);
+                }
+            };
+            if (p.y_bf16) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {                // 128 columns
+                    uint32_t d[4][32];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) fetch(h * 128 + c * 32, d[c]);
+                    emptied();
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        if (some) tmem_ld_wait(d[c]);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            *reinterpret_cast<uint4 *>(at(c >> 1, lane, (c & 1) * 4 + j)) =
+                                make_uint4(bf16x2(d[c][8 * j], d[c][8 * j + 1]), bf16x2(d[c][8 * j + 2], d[c][8 * j + 3]),
+                                           bf16x2(d[c][8 * j + 4], d[c][8 * j + 5]), bf16x2(d[c][8 * j + 6], d[c][8 * j + 7]));
+                    }
+                    if (h == 1 && some) taken();
+                    send(nt * 256 + h * 128, std::integral_constant<int, 2>{});
+                }
+            } else {
+#pragma unroll 1
+                for (int h = 0; h < 4; ++h) {                // 64 columns
+                    uint32_t d[2][32];
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) fetch(h * 64 + c * 32, d[c]);
+                    emptied();
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        if (some) tmem_ld_wait(d[c]);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            *reinterpret_cast<uint4 *>(at(c, lane, j)) = make_uint4(d[c][4 * j], d[c][4 * j + 1], d[c][4 * j + 2], d[c][4 * j + 3]);
+                    }
+                    if (h == 3 && some) taken();
+                    send(nt * 256 + h * 64, std::integral_constant<int, 4>{});
+                }
+            }
+        }
+        if (lane == 0) bulk_wait_group_all();
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+    // (no commit's arrival is left on its way; the wait is bounded, so it begins when the
+    // sums have been taken out)
+    if (warp == C::EPI + 1) {
+        if (lane == 0) mbar_wait(done, 0, nullptr, p.err);
+        __syncwarp();
+    }
+    // (of a pair: no CTA leaves while the other's MMAs may read its shared memory
+    // or it may still arrive on the other's barriers)
+    if (C::PAIR) cluster_sync_all();
+    if (warp == C::EPI + 1) {
+        tc_fence_after();
+        if constexpr (C::PAIR) tmem_dealloc_pair(tmem, 512);
+        else tmem_dealloc(tmem, 512);
     }
 }
-cudaError_t launch_outer(const Outer &p, cudaStream_t s) {
-    outer_kernel<<<dim3((p.NB + 31) / 32, (p.NA + 7) / 8, p.E), dim3(32, 8), 0, s>>>(p);
-    return cudaGetLastError();
+
+// ---- host -------------------------------------------------------------------
+
+// bf16 or fp32 tensor [d2][d1][d0] in boxes of 128 bytes x box1, 128-byte swizzle; loads
+// give zeros past each edge, stores write nothing there.
+static bool encode(CUtensorMap *m, const void *base, int elem, int64_t d0, int64_t d1, int64_t d2, int box1, bool three) {
+    const cuuint64_t dims[3] = {(cuuint64_t)d0, (cuuint64_t)d1, (cuuint64_t)d2};
+    const cuuint64_t strides[2] = {(cuuint64_t)(d0 * elem), (cuuint64_t)(d0 * d1 * elem)};
+    const cuuint32_t box[3] = {(cuuint32_t)(128 / elem), (cuuint32_t)box1, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return encode_fn()(m, elem == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, three ? 3 : 2,
+                       const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-}  // namespace
+// Row tiles of at most tr rows, at most: every expert may have one cut tile, and so may
+// the rows of none.
+static int64_t row_tiles_bound(int M, int E, const int32_t *offsets, int tr) {
+    if (!offsets) return ((int64_t)M + tr - 1) / tr;
+    return M / tr + (E + 1 < M ? E + 1 : M);
+}
+
+template <class C>
+static cudaError_t run_large(const Maps &maps, const Params &p, int64_t tiles, cudaStream_t s) {
+    const DeviceInfo &di = device_info();
+    if (tiles + di.num_sms > 0x7fffffff) return cudaErrorInvalidValue;
+    int64_t clusters = di.num_sms / C::CTAS;
+    if (tiles < clusters) clusters = tiles;
+    const cudaError_t e = ensure_dynamic_smem((const void *)large_kernel<C>, C::SMEM);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(large_kernel<C>, dim3((unsigned)(clusters * C::CTAS)), C::THREADS, C::SMEM, C::CTAS, s, maps, p);
+}
+
+template <class C>
+static cudaError_t launch_large(const Bf16Args &a, cudaStream_t s) {
+    Maps maps{};
+    Params p{a.offsets, a.y, a.err, a.M, a.N, a.K, a.E, (a.N + C::TN - 1) / C::TN, 0, a.y_dtype == ZFFN_DT_BF16, 0};
+    const int elem = p.y_bf16 ? 2 : 4;
+    p.vec = a.N * elem % 16 == 0 && (reinterpret_cast<uintptr_t>(a.y) & 15) == 0;
+    if (!encode(&maps.a, a.a, 2, a.K, a.M, 1, 128, false)) return cudaErrorInvalidValue;
+    if (!(C::KIND == FORWARD ? encode(&maps.w, a.w, 2, a.K, a.N, a.E, C::W_ROWS, true) : encode(&maps.w, a.w, 2, a.N, a.K, a.E, KB, true)))
+        return cudaErrorInvalidValue;
+    if (p.vec && !encode(&maps.y, a.y, elem, a.N, a.M, 1, 32, false)) return cudaErrorInvalidValue;
+    return run_large<C>(maps, p, row_tiles_bound(a.M, a.E, a.offsets, C::TM) * p.n_tiles, s);
+}
+
+template <int KIND>
+static cudaError_t launch(const Bf16Args &a, cudaStream_t s) {
+    return launch_large<LargeCfg<KIND, false>>(a, s);
+}
+
+}  // namespace b16
 
 cudaError_t launch_bf16_matmul(const Bf16Args &a, cudaStream_t s) {
-    return launch_rows({a.a, a.w, nullptr, a.y, a.offsets, nullptr, nullptr, nullptr, nullptr, true, a.y_dtype == ZFFN_DT_BF16, a.M, a.N, a.K, a.E,
-                        a.transposed ? 1 : a.K, a.transposed ? a.N : 1}, s);
+    if (!encode_fn()) return cudaErrorNotSupported;
+    return a.transposed ? b16::launch<b16::BACK>(a, s) : b16::launch<b16::FORWARD>(a, s);
 }
+
 cudaError_t launch_bf16_grad_w(const Bf16GradArgs &a, cudaStream_t s) {
-    return launch_outer({a.dy, a.a, a.dw, a.offsets, nullptr, nullptr, true, true, a.dw_dtype == ZFFN_DT_BF16, a.M, a.N, a.K, a.E}, s);
-}
-cudaError_t launch_lora_shrink(const LoraPlan &p, const void *x, const void *w, bool transposed, float *v, int C, cudaStream_t s) {
-    return launch_rows({x, w, nullptr, v, p.offsets, p.row_slot, nullptr, nullptr, p.scale, true, false, p.T, p.r, C, p.L,
-                        transposed ? 1 : C, transposed ? p.r : 1}, s);
-}
-cudaError_t launch_lora_expand(const LoraPlan &p, const float *v, const void *w, bool transposed, int dtype, const void *base, void *out,
-                               int C, cudaStream_t s) {
-    return launch_rows({v, w, base, out, p.offsets, nullptr, p.row_slot, p.slot_row, nullptr, false, dtype == ZFFN_DT_BF16, p.T, C, p.r, p.L,
-                        transposed ? 1 : p.r, transposed ? C : 1}, s);
-}
-cudaError_t launch_lora_outer(const LoraPlan &p, const float *v, const void *x, bool transposed, int dtype, void *d, int C, cudaStream_t s) {
-    if (transposed) return launch_outer({x, v, d, p.offsets, p.row_slot, nullptr, true, false, dtype == ZFFN_DT_BF16, p.T, C, p.r, p.L}, s);
-    return launch_outer({v, x, d, p.offsets, nullptr, p.row_slot, false, true, dtype == ZFFN_DT_BF16, p.T, p.r, C, p.L}, s);
+    using namespace b16;
+    using C = LargeCfg<WEIGHTS, false>;
+    if (!encode_fn()) return cudaErrorNotSupported;
+    Maps maps{};
+    const Params p{a.offsets, a.dw, a.err, a.M, a.N, a.K, a.E, (a.K + C::TN - 1) / C::TN, (a.N + C::TM - 1) / C::TM, a.dw_dtype == ZFFN_DT_BF16, 1};
+    if (!encode(&maps.a, a.dy, 2, a.N, a.M, 1, KB, false) || !encode(&maps.a16, a.dy, 2, a.N, a.M, 1, 16, false) ||
+        !encode(&maps.w, a.a, 2, a.K, a.M, 1, KB, false) || !encode(&maps.w16, a.a, 2, a.K, a.M, 1, 16, false) ||
+        !encode(&maps.y, a.dw, p.y_bf16 ? 2 : 4, a.K, a.N, a.E, 32, true))
+        return cudaErrorInvalidValue;
+    return run_large<C>(maps, p, (int64_t)a.E * p.m_tiles * p.n_tiles, s);
 }
 
 }  // namespace zffn

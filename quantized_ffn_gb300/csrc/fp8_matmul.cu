@@ -7,12 +7,11 @@
 // in registers: acc += d * (sa * sw), one fp32 multiply-add per value and block
 // (the scales' product is rounded once before; below 2^-126 it is held in steps of
 // 2^-149, which moves a block's term by less than 2^-125, since its sum is below 2^25).
-#include <cudaTypedefs.h>
-
 #include <atomic>
 
 #include "fp8.h"
 #include "launch.cuh"
+#include "roles.cuh"
 
 namespace zffn {
 namespace f8 {
@@ -43,28 +42,6 @@ __device__ __forceinline__ void tc_mma_f8_pair(uint32_t d_tmem, uint64_t a_desc,
 __host__ __device__ constexpr uint32_t idesc_f8_f32(int M, int N) {
     return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
-__device__ __forceinline__ void st_cluster_f4(uint32_t addr, float4 v) {
-    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
-                 : "memory");
-}
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-// Bring a tile of a tensor map's matrix into L2.
-__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap *map, int c0, int c1) {
-    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(map)),
-                 "r"(c0), "r"(c1)
-                 : "memory");
-}
-// 2-D TMA tile store shared -> global, tracked by the issuing thread's bulk-async group.
-__device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, uint32_t smem_src, int c0, int c1) {
-    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
-                     reinterpret_cast<uint64_t>(map)),
-                 "r"(smem_src), "r"(c0), "r"(c1)
-                 : "memory");
-}
-__device__ __forceinline__ void named_barrier(int id, int threads) {
-    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
 // acc += d * s on a pair of fp32 values (one instruction, each half rounded once).
 __device__ __forceinline__ void fma2(float2 &acc, uint32_t d0, uint32_t d1, float s0, float s1) {
     asm("{\n\t.reg .b64 a, d, f;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 d, {%2, %3};\n\tmov.b64 f, {%4, %5};\n\t"
@@ -76,31 +53,6 @@ __device__ __forceinline__ void fma2(float2 &acc, uint32_t d0, uint32_t d1, floa
 template <int N> struct Bytes { static constexpr int value = N; };
 template <int R> __device__ __forceinline__ void reg_alloc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
 template <int R> __device__ __forceinline__ void reg_dealloc() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
-// Whether the barrier's phase is complete, without suspending the thread.
-__device__ __forceinline__ bool bar_test(uint64_t *bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-// mbar_wait of the products' roles: the barrier is asked without suspending the
-// thread (a suspended thread is woken hundreds of clocks late, once for every
-// K block on the way from the tensor cores to the sums and back), and the bound
-// is a count of tries: the roles have no registers to spare for the clock.
-__device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, volatile int *abort, int *err) {
-    for (int n = 0; !bar_test(bar, parity); ++n)
-        if (n > (1 << 26) || ((n & 1023) == 1023 && *abort)) {
-            record_error(err, ZFFN_ERR_TIMEOUT);
-            *abort = 1;
-            return false;
-        }
-    return true;
-}
 // silu(g) u = g / (1 + 2^(-g log2 e)) u: two instructions of the special function
 // unit and four others.  Off by at most (3 + |g| / 3) 2^-22 of the value for g < 0
 // and 3 x 2^-22 for g > 0: the exponent -g log2 e is rounded to fp32, by up to 2^-24
@@ -1009,18 +961,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
 
 // ---- host -------------------------------------------------------------------
 
-static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-        void *ptr = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            ptr = nullptr;
-        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-    }();
-    return fn;
-}
-
 // Byte matrix [rows][K] in boxes of 128 columns, 128-byte swizzle, zeros past the edges.
 static bool encode(CUtensorMap *m, const void *base, int64_t rows, int K, int box_rows) {
     const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
@@ -1197,7 +1137,7 @@ static cudaError_t launch(const Fp8Args &a, cudaStream_t s) {
 }  // namespace f8
 
 cudaError_t launch_fp8_matmul(const Fp8Args &a, cudaStream_t s) {
-    if (!f8::encode_fn()) return cudaErrorNotSupported;
+    if (!encode_fn()) return cudaErrorNotSupported;
     return a.w1 ? f8::launch<true>(a, s) : f8::launch<false>(a, s);
 }
 
