@@ -37,6 +37,20 @@ __device__ __forceinline__ void tma_load_3d_pair(void *dst, const CUtensorMap *m
         "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
         : "memory");
 }
+__device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, uint64_t *bar, int c0, int c1, int c2, int c3) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_4d_pair(void *dst, const CUtensorMap *map, uint32_t bar, int c0, int c1, int c2, int c3) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+        : "memory");
+}
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, uint32_t src, int c0, int c1, int c2) {
     asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
                      reinterpret_cast<uint64_t>(map)),
@@ -44,12 +58,12 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, uint32_t sr
                  : "memory");
 }
 // Shared-memory matrix descriptor of an MN-major operand, 128-byte swizzle: boxes of 64
-// values of the free index (128 bytes) by 64 of the contracted one, 8192 bytes each;
-// groups of 8 of the contracted index lie 1024 bytes apart.
-__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr) {
+// values of the free index (128 bytes) by 64 (or 16, or 32) of the contracted one, box_bytes
+// each; groups of 8 of the contracted index lie 1024 bytes apart.
+__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr, uint32_t box_bytes) {
     uint64_t d = 0;
     d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
-    d |= (uint64_t)(8192 >> 4) << 16;          // from box to box
+    d |= (uint64_t)(box_bytes >> 4) << 16;     // from box to box
     d |= (uint64_t)(1024 >> 4) << 32;          // from 8 contracted values to the next
     d |= (uint64_t)1 << 46;
     d |= (uint64_t)2 << 61;
@@ -76,11 +90,16 @@ struct Params {
     int m_tiles;        // weights: tiles of dw[e]'s rows
     int y_bf16;
     int vec;            // y's rows are 16-byte multiples
+    // an MN-major operand whose rows are whole boxes wide (the columns a multiple of 64):
+    // one copy takes all boxes of a tile, its map counting boxes by an index of their own.
+    // (With a copy a box the one issuing thread held the weights' gradients back: 32768 rows
+    // of 128 experts, 1536 x 2048, WIDE_US us against NARROW_US us.)
+    int wide_a, wide_w;
 };
-// a: forward, back: [M][K]; weights: dy.  w: w; weights: a.  a16, w16: weights: the same in
-// boxes of 16 rows.  y: what the stores go to.
+// a: forward, back: [M][K]; weights: dy, in boxes of 16, 32 and 64 rows.  w: w; weights: a,
+// in the same.  y: what the stores go to.
 struct Maps {
-    CUtensorMap a, w, y, a16, w16;
+    CUtensorMap a[3], w[3], y;
 };
 
 // ---------------------------------------------------------------------------
@@ -130,8 +149,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
         for (int i = 0; i < 2; ++i) { mbar_init(&t_full[i], 1); mbar_init(&t_empty[i], C::EPI * C::CTAS); }
         mbar_init(done, 1);
         fence_mbarrier_init();
-        prefetch_tensormap(&maps.a);
-        prefetch_tensormap(&maps.w);
+        for (int i = 0; i < (GRAD ? 3 : 1); ++i) {
+            prefetch_tensormap(&maps.a[i]);
+            prefetch_tensormap(&maps.w[i]);
+        }
     }
     if (warp == C::EPI + 1) {
         uint32_t *dst = reinterpret_cast<uint32_t *>(info + 1);
@@ -153,6 +174,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
     // groups of 16 contracted values in stage i
     auto steps = [&](int i) { return (min(KB, (GRAD ? wk.rows : p.K) - i * KB) + 15) / 16; };
 
+    // weights: which boxes (16, 32 or 64 rows) hold that many groups of 16
+    auto box_of = [](int n) { return n > 2 ? 2 : n - 1; };
+
     if (warp == C::EPI) {
         // ---- TMA producer
         const uint32_t full0 = C::PAIR ? mapa_shared(smem_u32(s_full), 0) : 0;
@@ -166,38 +190,30 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
                 if (it >= C::NS && !bar_wait(&s_empty[s], ((it / C::NS) & 1) ^ 1, abort_flag, p.err)) { ok = false; break; }
                 uint8_t *sa = smem + s * C::STAGE, *sw = sa + C::A_BYTES;
                 if constexpr (GRAD) {
-                    const int row = wk.row0 + i * KB, n = steps(i);
-                    if (n == KB / 16) {
-                        mbar_arrive_expect_tx(&s_full[s], C::STAGE);
-#pragma unroll
-                        for (int b = 0; b < 2; ++b) tma_load_2d(sa + b * 8192, &maps.a, &s_full[s], mt * 128 + b * 64, row);
-#pragma unroll
-                        for (int b = 0; b < 4; ++b) tma_load_2d(sw + b * 8192, &maps.w, &s_full[s], nt * 256 + b * 64, row);
-                    } else {
-                        // (an expert's last rows: no more of the next one's than the MMA takes)
-                        mbar_arrive_expect_tx(&s_full[s], n * 6 * 2048);
-                        for (int j = 0; j < n; ++j) {
-#pragma unroll
-                            for (int b = 0; b < 2; ++b)
-                                tma_load_2d(sa + b * 8192 + j * 2048, &maps.a16, &s_full[s], mt * 128 + b * 64, row + j * 16);
-#pragma unroll
-                            for (int b = 0; b < 4; ++b)
-                                tma_load_2d(sw + b * 8192 + j * 2048, &maps.w16, &s_full[s], nt * 256 + b * 64, row + j * 16);
-                        }
-                    }
+                    // (of an expert's last rows no more than the MMA takes, or half as many again)
+                    const int row = wk.row0 + i * KB, x = box_of(steps(i)), bytes = 2048 << x;
+                    mbar_arrive_expect_tx(&s_full[s], 6 * bytes);
+                    if (p.wide_a) tma_load_3d(sa, &maps.a[x], &s_full[s], 0, row, mt * 2);
+                    else
+                        for (int b = 0; b < 2; ++b) tma_load_2d(sa + b * bytes, &maps.a[x], &s_full[s], mt * 128 + b * 64, row);
+                    if (p.wide_w) tma_load_3d(sw, &maps.w[x], &s_full[s], 0, row, nt * 4);
+                    else
+                        for (int b = 0; b < 4; ++b) tma_load_2d(sw + b * bytes, &maps.w[x], &s_full[s], nt * 256 + b * 64, row);
                 } else {
                     if (rank == 0) mbar_arrive_expect_tx(&s_full[s], C::STAGE * C::CTAS);
                     const int col = wk.nt * C::TN + rank * C::W_ROWS;
-                    if constexpr (C::PAIR) tma_load_2d_pair(sa, &maps.a, full0 + s * 8, i * KB, wk.row0 + 128 * rank);
-                    else tma_load_2d(sa, &maps.a, &s_full[s], i * KB, wk.row0);
+                    if constexpr (C::PAIR) tma_load_2d_pair(sa, maps.a, full0 + s * 8, i * KB, wk.row0 + 128 * rank);
+                    else tma_load_2d(sa, maps.a, &s_full[s], i * KB, wk.row0);
                     if constexpr (C::KIND == FORWARD) {
-                        if constexpr (C::PAIR) tma_load_3d_pair(sw, &maps.w, full0 + s * 8, i * KB, col, wk.e);
-                        else tma_load_3d(sw, &maps.w, &s_full[s], i * KB, col, wk.e);
+                        if constexpr (C::PAIR) tma_load_3d_pair(sw, maps.w, full0 + s * 8, i * KB, col, wk.e);
+                        else tma_load_3d(sw, maps.w, &s_full[s], i * KB, col, wk.e);
+                    } else if (p.wide_w) {
+                        if constexpr (C::PAIR) tma_load_4d_pair(sw, maps.w, full0 + s * 8, 0, i * KB, col / 64, wk.e);
+                        else tma_load_4d(sw, maps.w, &s_full[s], 0, i * KB, col / 64, wk.e);
                     } else {
-#pragma unroll
                         for (int b = 0; b < C::W_ROWS / 64; ++b) {
-                            if constexpr (C::PAIR) tma_load_3d_pair(sw + b * 8192, &maps.w, full0 + s * 8, col + b * 64, i * KB, wk.e);
-                            else tma_load_3d(sw + b * 8192, &maps.w, &s_full[s], col + b * 64, i * KB, wk.e);
+                            if constexpr (C::PAIR) tma_load_3d_pair(sw + b * 8192, maps.w, full0 + s * 8, col + b * 64, i * KB, wk.e);
+                            else tma_load_3d(sw + b * 8192, maps.w, &s_full[s], col + b * 64, i * KB, wk.e);
                         }
                     }
                 }
@@ -226,6 +242,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
                     if (!__all_sync(0xffffffffu, ok)) break;
                     const uint32_t sa = smem_u32(smem) + s * C::STAGE, sw = sa + C::A_BYTES;
                     const int n = steps(i);
+                    const uint32_t box = GRAD ? 2048u << box_of(n) : 8192u;
                     if constexpr (GRAD) {
                         // rows of the next expert in the last 16: zeros, in both operands
                         // (whatever they hold may be infinite)
@@ -233,16 +250,16 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
                         if (valid < n * 16) {
                             const int each = (n * 16 - valid) * 8;   // chunks of 16 bytes in a box
                             for (int c = lane; c < 6 * each; c += 32) {
-                                const int box = c / each;
-                                st_shared_v4(sa + box * 8192 + valid * 128 + (c - box * each) * 16, 0, 0, 0, 0);
+                                const int b = c / each;
+                                st_shared_v4((b < 2 ? sa + b * box : sw + (b - 2) * box) + valid * 128 + (c - b * each) * 16, 0, 0, 0, 0);
                             }
                             fence_proxy_async_smem();
                             __syncwarp();
                         }
                     }
                     tc_fence_after();
-                    const uint64_t ad = C::A_MN ? smem_desc_mn_sw128(sa) : smem_desc_k_sw128(sa);
-                    const uint64_t wd = C::W_MN ? smem_desc_mn_sw128(sw) : smem_desc_k_sw128(sw);
+                    const uint64_t ad = C::A_MN ? smem_desc_mn_sw128(sa, box) : smem_desc_k_sw128(sa);
+                    const uint64_t wd = C::W_MN ? smem_desc_mn_sw128(sw, box) : smem_desc_k_sw128(sw);
                     if (elect_one()) {
 #pragma unroll
                         for (int k = 0; k < KB / 16; ++k) {
@@ -416,13 +433,22 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
 // ---- host -------------------------------------------------------------------
 
 // bf16 or fp32 tensor [d2][d1][d0] in boxes of 128 bytes x box1, 128-byte swizzle; loads
-// give zeros past each edge, stores write nothing there.
-static bool encode(CUtensorMap *m, const void *base, int elem, int64_t d0, int64_t d1, int64_t d2, int box1, bool three) {
-    const cuuint64_t dims[3] = {(cuuint64_t)d0, (cuuint64_t)d1, (cuuint64_t)d2};
-    const cuuint64_t strides[2] = {(cuuint64_t)(d0 * elem), (cuuint64_t)(d0 * d1 * elem)};
-    const cuuint32_t box[3] = {(cuuint32_t)(128 / elem), (cuuint32_t)box1, 1};
-    const cuuint32_t estr[3] = {1, 1, 1};
-    return encode_fn()(m, elem == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, three ? 3 : 2,
+// give zeros past each edge, stores write nothing there.  boxes > 0: rows of a multiple of
+// 64 bf16 values, of which a copy takes `boxes` boxes side by side, one after another:
+// [d2][d0 / 64][d1][64].
+static bool encode(CUtensorMap *m, const void *base, int elem, int64_t d0, int64_t d1, int64_t d2, int box1, bool three, int boxes = 0) {
+    cuuint64_t dims[4] = {(cuuint64_t)d0, (cuuint64_t)d1, (cuuint64_t)d2, 1};
+    cuuint64_t strides[3] = {(cuuint64_t)(d0 * elem), (cuuint64_t)(d0 * d1 * elem), 0};
+    cuuint32_t box[4] = {(cuuint32_t)(128 / elem), (cuuint32_t)box1, 1, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    cuuint32_t rank = three ? 3 : 2;
+    if (boxes) {
+        dims[0] = 64; dims[2] = (cuuint64_t)(d0 / 64); dims[3] = (cuuint64_t)d2;
+        strides[2] = strides[1]; strides[1] = 128;
+        box[2] = (cuuint32_t)boxes;
+        ++rank;
+    }
+    return encode_fn()(m, elem == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, rank,
                        const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -448,11 +474,11 @@ static cudaError_t run_large(const Maps &maps, const Params &p, int64_t tiles, c
 template <class C>
 static cudaError_t launch_large(const Bf16Args &a, cudaStream_t s) {
     Maps maps{};
-    Params p{a.offsets, a.y, a.err, a.M, a.N, a.K, a.E, (a.N + C::TN - 1) / C::TN, 0, a.y_dtype == ZFFN_DT_BF16, 0};
+    Params p{a.offsets, a.y, a.err, a.M, a.N, a.K, a.E, (a.N + C::TN - 1) / C::TN, 0, a.y_dtype == ZFFN_DT_BF16, 0, 0, C::KIND == BACK && a.N % 64 == 0};
     const int elem = p.y_bf16 ? 2 : 4;
     p.vec = a.N * elem % 16 == 0 && (reinterpret_cast<uintptr_t>(a.y) & 15) == 0;
-    if (!encode(&maps.a, a.a, 2, a.K, a.M, 1, 128, false)) return cudaErrorInvalidValue;
-    if (!(C::KIND == FORWARD ? encode(&maps.w, a.w, 2, a.K, a.N, a.E, C::W_ROWS, true) : encode(&maps.w, a.w, 2, a.N, a.K, a.E, KB, true)))
+    if (!encode(maps.a, a.a, 2, a.K, a.M, 1, 128, false)) return cudaErrorInvalidValue;
+    if (!(C::KIND == FORWARD ? encode(maps.w, a.w, 2, a.K, a.N, a.E, C::W_ROWS, true) : encode(maps.w, a.w, 2, a.N, a.K, a.E, KB, true, p.wide_w ? C::W_ROWS / 64 : 0)))
         return cudaErrorInvalidValue;
     if (p.vec && !encode(&maps.y, a.y, elem, a.N, a.M, 1, 32, false)) return cudaErrorInvalidValue;
     return run_large<C>(maps, p, row_tiles_bound(a.M, a.E, a.offsets, C::TM) * p.n_tiles, s);
@@ -475,11 +501,12 @@ cudaError_t launch_bf16_grad_w(const Bf16GradArgs &a, cudaStream_t s) {
     using C = LargeCfg<WEIGHTS, false>;
     if (!encode_fn()) return cudaErrorNotSupported;
     Maps maps{};
-    const Params p{a.offsets, a.dw, a.err, a.M, a.N, a.K, a.E, (a.K + C::TN - 1) / C::TN, (a.N + C::TM - 1) / C::TM, a.dw_dtype == ZFFN_DT_BF16, 1};
-    if (!encode(&maps.a, a.dy, 2, a.N, a.M, 1, KB, false) || !encode(&maps.a16, a.dy, 2, a.N, a.M, 1, 16, false) ||
-        !encode(&maps.w, a.a, 2, a.K, a.M, 1, KB, false) || !encode(&maps.w16, a.a, 2, a.K, a.M, 1, 16, false) ||
-        !encode(&maps.y, a.dw, p.y_bf16 ? 2 : 4, a.K, a.N, a.E, 32, true))
-        return cudaErrorInvalidValue;
+    const Params p{a.offsets, a.dw, a.err, a.M, a.N, a.K, a.E, (a.K + C::TN - 1) / C::TN, (a.N + C::TM - 1) / C::TM, a.dw_dtype == ZFFN_DT_BF16, 1, a.N % 64 == 0, a.K % 64 == 0};
+    for (int x = 0; x < 3; ++x)
+        if (!encode(&maps.a[x], a.dy, 2, a.N, a.M, 1, 16 << x, false, p.wide_a ? 2 : 0) ||
+            !encode(&maps.w[x], a.a, 2, a.K, a.M, 1, 16 << x, false, p.wide_w ? 4 : 0))
+            return cudaErrorInvalidValue;
+    if (!encode(&maps.y, a.dw, p.y_bf16 ? 2 : 4, a.K, a.N, a.E, 32, true)) return cudaErrorInvalidValue;
     return run_large<C>(maps, p, (int64_t)a.E * p.m_tiles * p.n_tiles, s);
 }
 
