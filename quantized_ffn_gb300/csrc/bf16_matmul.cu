@@ -17,6 +17,9 @@
 namespace zffn {
 namespace b16 {
 
+#ifndef PAIR_RULE
+#define PAIR_RULE 1
+#endif
 enum Kind { FORWARD, BACK, WEIGHTS };
 constexpr int KB = 64;            // contracted values of a stage: rows of 128 bytes, or 64 rows
 
@@ -109,7 +112,9 @@ struct Maps {
 // MMAs run.
 //
 // Roles: warps 0 .. 3 take a tile out of tensor memory (32 rows each) and write it,
-// warp 4 loads by TMA, warp 5 issues the MMAs.
+// warp 4 loads by TMA, warp 5 issues the MMAs; weights: warp 6 zeroes the rows past an
+// expert's last in its last stage (in the MMA's own warp that held the MMAs back: 32768
+// rows of 128 experts, 1536 x 2048, 217 us).
 // ---------------------------------------------------------------------------
 template <int KIND_, bool PAIR_>
 struct LargeCfg {
@@ -123,11 +128,11 @@ struct LargeCfg {
     static constexpr int STAGE = A_BYTES + W_ROWS * 128;
     static constexpr int NS = PAIR ? 6 : 4;
     static constexpr int EPI = 4;
-    static constexpr int THREADS = (EPI + 2) * 32;
+    static constexpr int THREADS = (EPI + 2 + (KIND == WEIGHTS)) * 32;
     static constexpr int OUT_BYTES = 8192;                   // a warp's two boxes of 32 rows x 128 bytes
     static constexpr int OFF_OUT = NS * STAGE;
     static constexpr int OFF_BAR = OFF_OUT + EPI * OUT_BYTES;
-    static constexpr int SMEM = OFF_BAR + (2 * NS + 5) * 8 + 8 + 1024;
+    static constexpr int SMEM = OFF_BAR + (3 * NS + 5) * 8 + 8 + 1024;
     using Walk = GroupWalk<TM, 8, KIND == WEIGHTS>;
 };
 
@@ -137,7 +142,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint64_t *s_full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
     uint64_t *s_empty = s_full + C::NS, *t_full = s_empty + C::NS, *t_empty = t_full + 2, *done = t_empty + 2;
-    int *info = reinterpret_cast<int *>(done + 1);           // abort, TMEM base
+    uint64_t *cut_full = done + 1;                           // weights: an expert's last rows
+    int *info = reinterpret_cast<int *>(cut_full + C::NS);   // abort, TMEM base
     volatile int *abort_flag = info;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = C::PAIR ? (int)cluster_ctarank() : 0;
@@ -145,7 +151,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
 
     if (warp == C::EPI && lane == 0) {
         info[0] = 0;
-        for (int i = 0; i < C::NS; ++i) { mbar_init(&s_full[i], 1); mbar_init(&s_empty[i], 1); }
+        for (int i = 0; i < C::NS; ++i) {
+            mbar_init(&s_full[i], GRAD && C::PAIR ? 2 : 1);
+            mbar_init(&s_empty[i], 1);
+            mbar_init(&cut_full[i], 1);
+        }
         for (int i = 0; i < 2; ++i) { mbar_init(&t_full[i], 1); mbar_init(&t_empty[i], C::EPI * C::CTAS); }
         mbar_init(done, 1);
         fence_mbarrier_init();
@@ -177,10 +187,24 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
     // weights: which boxes (16, 32 or 64 rows) hold that many groups of 16
     auto box_of = [](int n) { return n > 2 ? 2 : n - 1; };
 
+    // Weights: rows of the next expert among a stage's last 16 become zeros, in both operands
+    // (whatever they hold may be infinite).  A warp, after the copies and before the MMAs.
+    auto zero_past = [&](uint32_t sa, uint32_t sw, int valid, int n) {
+        if (valid >= n * 16) return;
+        const uint32_t box = 2048u << box_of(n);
+        const int each = (n * 16 - valid) * 8;               // chunks of 16 bytes in a box
+        for (int c = lane; c < each; c += 32)
+#pragma unroll
+            for (int b = 0; b < 2 + C::W_ROWS / 64; ++b)
+                st_shared_v4((b < 2 ? sa + b * box : sw + (b - 2) * box) + valid * 128 + c * 16, 0, 0, 0, 0);
+        fence_proxy_async_smem();
+        __syncwarp();
+    };
+
     if (warp == C::EPI) {
         // ---- TMA producer
         const uint32_t full0 = C::PAIR ? mapa_shared(smem_u32(s_full), 0) : 0;
-        uint32_t it = 0;
+        uint32_t it = 0, cut_used = 0, cut_phase = 0;         // cut_full: stages that used it, each one's last phase
         bool ok = true;
         for (; ok && wk.get(); wk.t += step) {
             const int nb = blocks();
@@ -192,13 +216,37 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
                 if constexpr (GRAD) {
                     // (of an expert's last rows no more than the MMA takes, or half as many again)
                     const int row = wk.row0 + i * KB, x = box_of(steps(i)), bytes = 2048 << x;
-                    mbar_arrive_expect_tx(&s_full[s], 6 * bytes);
-                    if (p.wide_a) tma_load_3d(sa, &maps.a[x], &s_full[s], 0, row, mt * 2);
-                    else
-                        for (int b = 0; b < 2; ++b) tma_load_2d(sa + b * bytes, &maps.a[x], &s_full[s], mt * 128 + b * 64, row);
-                    if (p.wide_w) tma_load_3d(sw, &maps.w[x], &s_full[s], 0, row, nt * 4);
-                    else
-                        for (int b = 0; b < 4; ++b) tma_load_2d(sw + b * bytes, &maps.w[x], &s_full[s], nt * 256 + b * 64, row);
+                    constexpr int WB = C::W_ROWS / 64;
+                    const int c0 = mt * C::TM + rank * 128, c1 = nt * C::TN + rank * C::W_ROWS;
+                    // s_full counts an arrival of each CTA.  Where rows have to be zeroed, the
+                    // copies complete on a barrier of their own, and the arrival follows the
+                    // zeroing.
+                    const bool cut = wk.rows - i * KB < steps(i) * 16;
+                    if (cut) {
+                        mbar_arrive_expect_tx(&cut_full[s], (2 + WB) * bytes);
+                        cut_phase ^= cut_used & (1u << s);
+                        cut_used |= 1u << s;
+                    }
+                    if constexpr (C::PAIR) {
+                        const uint32_t bar = cut ? smem_u32(&cut_full[s]) : full0 + s * 8;
+                        if (!cut && rank == 0) mbar_arrive_expect_tx(&s_full[s], 2 * (2 + WB) * bytes);
+                        else if (!cut) mbar_arrive_cluster(full0 + s * 8);
+                        if (p.wide_a) tma_load_3d_pair(sa, &maps.a[x], bar, 0, row, c0 / 64);
+                        else
+                            for (int b = 0; b < 2; ++b) tma_load_2d_pair(sa + b * bytes, &maps.a[x], bar, c0 + b * 64, row);
+                        if (p.wide_w) tma_load_3d_pair(sw, &maps.w[x], bar, 0, row, c1 / 64);
+                        else
+                            for (int b = 0; b < WB; ++b) tma_load_2d_pair(sw + b * bytes, &maps.w[x], bar, c1 + b * 64, row);
+                    } else {
+                        uint64_t *bar = cut ? &cut_full[s] : &s_full[s];
+                        if (!cut) mbar_arrive_expect_tx(bar, (2 + WB) * bytes);
+                        if (p.wide_a) tma_load_3d(sa, &maps.a[x], bar, 0, row, c0 / 64);
+                        else
+                            for (int b = 0; b < 2; ++b) tma_load_2d(sa + b * bytes, &maps.a[x], bar, c0 + b * 64, row);
+                        if (p.wide_w) tma_load_3d(sw, &maps.w[x], bar, 0, row, c1 / 64);
+                        else
+                            for (int b = 0; b < WB; ++b) tma_load_2d(sw + b * bytes, &maps.w[x], bar, c1 + b * 64, row);
+                    }
                 } else {
                     if (rank == 0) mbar_arrive_expect_tx(&s_full[s], C::STAGE * C::CTAS);
                     const int col = wk.nt * C::TN + rank * C::W_ROWS;
@@ -221,6 +269,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
             ok = __shfl_sync(0xffffffffu, ok && !*abort_flag, 0);
         }
         // (a launch that gave up: wait for the copies in flight before leaving)
+        if (lane == 0 && *abort_flag)
+            for (uint32_t s = 0; s < C::NS; ++s)
+                if ((cut_used >> s) & 1) mbar_wait(&cut_full[s], (cut_phase >> s) & 1, nullptr, p.err);
         if (lane == 0 && *abort_flag && rank == 0)
             for (uint32_t j = it > C::NS ? it - C::NS : 0; j < it; ++j)
                 mbar_wait(&s_full[j % C::NS], (j / C::NS) & 1, nullptr, p.err);
@@ -243,20 +294,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
                     const uint32_t sa = smem_u32(smem) + s * C::STAGE, sw = sa + C::A_BYTES;
                     const int n = steps(i);
                     const uint32_t box = GRAD ? 2048u << box_of(n) : 8192u;
-                    if constexpr (GRAD) {
-                        // rows of the next expert in the last 16: zeros, in both operands
-                        // (whatever they hold may be infinite)
-                        const int valid = wk.rows - i * KB;
-                        if (valid < n * 16) {
-                            const int each = (n * 16 - valid) * 8;   // chunks of 16 bytes in a box
-                            for (int c = lane; c < 6 * each; c += 32) {
-                                const int b = c / each;
-                                st_shared_v4((b < 2 ? sa + b * box : sw + (b - 2) * box) + valid * 128 + (c - b * each) * 16, 0, 0, 0, 0);
-                            }
-                            fence_proxy_async_smem();
-                            __syncwarp();
-                        }
-                    }
                     tc_fence_after();
                     const uint64_t ad = C::A_MN ? smem_desc_mn_sw128(sa, box) : smem_desc_k_sw128(sa);
                     const uint64_t wd = C::W_MN ? smem_desc_mn_sw128(sw, box) : smem_desc_k_sw128(sw);
@@ -286,6 +323,27 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
             }
             __syncwarp();
         }
+    } else if (warp == C::EPI + 2) {
+        // ---- weights: zeroes the rows past an expert's last
+        const uint32_t full0 = C::PAIR ? mapa_shared(smem_u32(s_full), 0) : 0;
+        uint32_t it = 0, phases = 0;
+        for (bool ok = true; ok && wk.get(); wk.t += step) {
+            const int nb = blocks();
+            it += nb;
+            const int n = nb ? steps(nb - 1) : 0, valid = wk.rows - (nb - 1) * KB;
+            if (valid >= n * 16) continue;
+            const uint32_t s = (it - 1) % C::NS;
+            ok = __all_sync(0xffffffffu, bar_wait(&cut_full[s], (phases >> s) & 1, abort_flag, p.err));
+            if (!ok) break;
+            phases ^= 1u << s;
+            const uint32_t sa = smem_u32(smem) + s * C::STAGE;
+            zero_past(sa, sa + C::A_BYTES, valid, n);
+            if (lane == 0) {
+                if constexpr (C::PAIR) mbar_arrive_cluster(full0 + s * 8);
+                else mbar_arrive(&s_full[s]);
+            }
+            __syncwarp();
+        }
     } else {
         // ---- take out and write: thread = one row of the tile
         const uint32_t taddr = tmem + ((uint32_t)(warp * 32) << 16);
@@ -302,7 +360,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
                 ++acc;
             }
             const int mt = GRAD ? wk.nt / p.n_tiles : 0, nt = GRAD ? wk.nt - mt * p.n_tiles : wk.nt;
-            const int wrow = GRAD ? mt * 128 + warp * 32 : 128 * rank + warp * 32;   // this warp's first row (of dw[e], of the tile)
+            const int wrow = (GRAD ? mt * C::TM : 0) + 128 * rank + warp * 32;   // this warp's first row (of dw[e], of the tile)
             const int left = GRAD ? p.N - wrow : wk.rows - wrow;
             const int64_t row = GRAD ? wrow : wk.row0 + wrow;
             const int cols = GRAD ? p.K : p.N;
@@ -486,7 +544,21 @@ static cudaError_t launch_large(const Bf16Args &a, cudaStream_t s) {
 
 template <int KIND>
 static cudaError_t launch(const Bf16Args &a, cudaStream_t s) {
+    if (PAIR_RULE) return launch_large<LargeCfg<KIND, true>>(a, s);
     return launch_large<LargeCfg<KIND, false>>(a, s);
+}
+
+template <class C>
+static cudaError_t launch_weights(const Bf16GradArgs &a, cudaStream_t s) {
+    Maps maps{};
+    const Params p{a.offsets, a.dw, a.err, a.M, a.N, a.K, a.E, (a.K + C::TN - 1) / C::TN, (a.N + C::TM - 1) / C::TM, a.dw_dtype == ZFFN_DT_BF16, 1,
+                   a.N % 64 == 0, a.K % 64 == 0};
+    for (int x = 0; x < 3; ++x)
+        if (!encode(&maps.a[x], a.dy, 2, a.N, a.M, 1, 16 << x, false, p.wide_a ? 2 : 0) ||
+            !encode(&maps.w[x], a.a, 2, a.K, a.M, 1, 16 << x, false, p.wide_w ? C::W_ROWS / 64 : 0))
+            return cudaErrorInvalidValue;
+    if (!encode(&maps.y, a.dw, p.y_bf16 ? 2 : 4, a.K, a.N, a.E, 32, true)) return cudaErrorInvalidValue;
+    return run_large<C>(maps, p, (int64_t)a.E * p.m_tiles * p.n_tiles, s);
 }
 
 }  // namespace b16
@@ -498,16 +570,9 @@ cudaError_t launch_bf16_matmul(const Bf16Args &a, cudaStream_t s) {
 
 cudaError_t launch_bf16_grad_w(const Bf16GradArgs &a, cudaStream_t s) {
     using namespace b16;
-    using C = LargeCfg<WEIGHTS, false>;
     if (!encode_fn()) return cudaErrorNotSupported;
-    Maps maps{};
-    const Params p{a.offsets, a.dw, a.err, a.M, a.N, a.K, a.E, (a.K + C::TN - 1) / C::TN, (a.N + C::TM - 1) / C::TM, a.dw_dtype == ZFFN_DT_BF16, 1, a.N % 64 == 0, a.K % 64 == 0};
-    for (int x = 0; x < 3; ++x)
-        if (!encode(&maps.a[x], a.dy, 2, a.N, a.M, 1, 16 << x, false, p.wide_a ? 2 : 0) ||
-            !encode(&maps.w[x], a.a, 2, a.K, a.M, 1, 16 << x, false, p.wide_w ? 4 : 0))
-            return cudaErrorInvalidValue;
-    if (!encode(&maps.y, a.dw, p.y_bf16 ? 2 : 4, a.K, a.N, a.E, 32, true)) return cudaErrorInvalidValue;
-    return run_large<C>(maps, p, (int64_t)a.E * p.m_tiles * p.n_tiles, s);
+    if (PAIR_RULE) return launch_weights<LargeCfg<WEIGHTS, true>>(a, s);
+    return launch_weights<LargeCfg<WEIGHTS, false>>(a, s);
 }
 
 }  // namespace zffn
