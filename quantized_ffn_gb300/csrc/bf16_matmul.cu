@@ -98,6 +98,7 @@ struct Params {
     // (With a copy a box the one issuing thread held the weights' gradients back: 32768 rows
     // of 128 experts, 1536 x 2048, WIDE_US us against NARROW_US us.)
     int wide_a, wide_w;
+    FastDiv each, across;   // of the walk; weights: by n_tiles
 };
 // a: forward, back: [M][K]; weights: dy, in boxes of 16, 32 and 64 rows.  w: w; weights: a,
 // in the same.  y: what the stores go to.
@@ -111,8 +112,8 @@ struct Maps {
 // two accumulators in tensor memory, so that one is taken out while the next tile's
 // MMAs run.
 //
-// Roles: warps 0 .. 3 take a tile out of tensor memory (32 rows each) and write it,
-// warp 4 loads by TMA, warp 5 issues the MMAs; weights: warp 6 zeroes the rows past an
+// Roles: warps 0 .. 7 take a tile out of tensor memory (32 rows by 128 columns each) and
+// write it, warp 8 loads by TMA, warp 9 issues the MMAs; weights: warp 10 zeroes the rows past an
 // expert's last in its last stage (in the MMA's own warp that held the MMAs back: 32768
 // rows of 128 experts, 1536 x 2048, 217 us).
 // ---------------------------------------------------------------------------
@@ -127,9 +128,9 @@ struct LargeCfg {
     static constexpr int A_BYTES = 128 * 128;
     static constexpr int STAGE = A_BYTES + W_ROWS * 128;
     static constexpr int NS = PAIR ? 6 : 4;
-    static constexpr int EPI = 4;
+    static constexpr int EPI = 8;
     static constexpr int THREADS = (EPI + 2 + (KIND == WEIGHTS)) * 32;
-    static constexpr int OUT_BYTES = 8192;                   // a warp's two boxes of 32 rows x 128 bytes
+    static constexpr int OUT_BYTES = 4096;                   // a warp's box of 32 rows x 128 bytes
     static constexpr int OFF_OUT = NS * STAGE;
     static constexpr int OFF_BAR = OFF_OUT + EPI * OUT_BYTES;
     static constexpr int SMEM = OFF_BAR + (3 * NS + 5) * 8 + 8 + 1024;
@@ -177,7 +178,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(info + 1);
     typename C::Walk wk;
-    wk.start(p.offsets, p.M, p.E, GRAD ? p.m_tiles * p.n_tiles : p.n_tiles, !GRAD, blockIdx.x / C::CTAS);
+    wk.start(p.offsets, p.M, p.E, GRAD ? p.m_tiles * p.n_tiles : p.n_tiles, p.each, !GRAD, blockIdx.x / C::CTAS);
     const int step = gridDim.x / C::CTAS;
     // stages of the tile at hand (none: zeros)
     auto blocks = [&] { return GRAD ? (wk.rows + KB - 1) / KB : wk.e < p.E ? (p.K + KB - 1) / KB : 0; };
@@ -208,7 +209,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
         bool ok = true;
         for (; ok && wk.get(); wk.t += step) {
             const int nb = blocks();
-            const int mt = GRAD ? wk.nt / p.n_tiles : 0, nt = GRAD ? wk.nt - mt * p.n_tiles : wk.nt;
+            const int mt = GRAD ? p.across.div(wk.nt) : 0, nt = GRAD ? wk.nt - mt * p.n_tiles : wk.nt;
             for (int i = 0; i < nb && lane == 0; ++i, ++it) {
                 const uint32_t s = it % C::NS;
                 if (it >= C::NS && !bar_wait(&s_empty[s], ((it / C::NS) & 1) ^ 1, abort_flag, p.err)) { ok = false; break; }
@@ -346,7 +347,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
         }
     } else {
         // ---- take out and write: thread = one row of the tile
-        const uint32_t taddr = tmem + ((uint32_t)(warp * 32) << 16);
+        const int q = warp & 3, half = warp >> 2;
+        const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + half * 128;
         const uint32_t empty0 = C::PAIR ? mapa_shared(smem_u32(t_empty), 0) : 0;
         uint8_t *out = smem + C::OFF_OUT + warp * C::OUT_BYTES;
         uint32_t acc = 0;
@@ -359,69 +361,17 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
                 tc_fence_after();
                 ++acc;
             }
-            const int mt = GRAD ? wk.nt / p.n_tiles : 0, nt = GRAD ? wk.nt - mt * p.n_tiles : wk.nt;
-            const int wrow = (GRAD ? mt * C::TM : 0) + 128 * rank + warp * 32;   // this warp's first row (of dw[e], of the tile)
+            const int mt = GRAD ? p.across.div(wk.nt) : 0, nt = GRAD ? wk.nt - mt * p.n_tiles : wk.nt;
+            const int wrow = (GRAD ? mt * C::TM : 0) + 128 * rank + q * 32;   // this warp's first row (of dw[e], of the tile)
             const int left = GRAD ? p.N - wrow : wk.rows - wrow;
             const int64_t row = GRAD ? wrow : wk.row0 + wrow;
             const int cols = GRAD ? p.K : p.N;
-            auto at = [&](int box, int r, int chunk) { return out + box * 4096 + r * 128 + ((chunk ^ (r & 7)) << 4); };
-            // both boxes, from column n0 on, in elements of `elem` bytes
-            auto send = [&](int n0, auto elem_size) {
-                constexpr int elem = decltype(elem_size)::value, per = 128 / elem;
-                if (GRAD || (p.vec && left >= 32)) {
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        for (int x = 0; x < 2; ++x)
-                            if (n0 + x * per < cols && left > 0) {
-                                if constexpr (GRAD) tma_store_3d(&maps.y, smem_u32(out) + x * 4096, n0 + x * per, (int)row, wk.e);
-                                else tma_store_2d(&maps.y, smem_u32(out) + x * 4096, n0 + x * per, (int)row);
-                            }
-                        bulk_commit_group();
-                    }
-                    return;
-                }
-                // rows that are not all the tile's, or not 16-byte multiples: a row's bytes by
-                // neighbouring lanes
-                __syncwarp();
-                uint8_t *y = static_cast<uint8_t *>(p.y) + row * p.N * elem;
-                const int64_t pitch = (int64_t)p.N * elem;
-                for (int x = 0; x < 2; ++x) {
-                    const int col = n0 + x * per, bytes = min(per, p.N - col) * elem;
-                    if (p.vec) {
-                        for (int i = lane; i < 32 * 8; i += 32)
-                            if (i / 8 < left && i % 8 * 16 < bytes)
-                                *reinterpret_cast<uint4 *>(y + i / 8 * pitch + (int64_t)col * elem + i % 8 * 16) =
-                                    *reinterpret_cast<const uint4 *>(at(x, i / 8, i % 8));
-                    } else {
-#pragma unroll
-                        for (int l = 0; l < per / 32; ++l) {
-                            const int c = (lane + 32 * l) * elem;
-                            uint8_t *dst = y + (int64_t)col * elem + c;
-#pragma unroll 8
-                            for (int r = 0; r < 32; ++r) {
-                                const uint8_t *src = at(x, r, c >> 4) + (c & 15);
-                                if (r >= left || c >= bytes) continue;
-                                if constexpr (elem == 2) *reinterpret_cast<uint16_t *>(dst + r * pitch) = *reinterpret_cast<const uint16_t *>(src);
-                                else *reinterpret_cast<uint32_t *>(dst + r * pitch) = *reinterpret_cast<const uint32_t *>(src);
-                            }
-                        }
-                    }
-                }
-                __syncwarp();
-            };
-            // 32 columns of the tile (zeros where nothing was summed)
-            auto fetch = [&](int c, uint32_t (&d)[32]) {
-                if (some) tmem_ld_32x32b_x32(from + c, d);
-                else
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) d[j] = 0;
-            };
-            auto emptied = [&] {   // the boxes sent before have been read
-                if (lane == 0) bulk_wait_group_read<0>();
-                __syncwarp();
-            };
-            auto taken = [&] {     // the accumulator has been read
+            // The tile leaves in boxes of 128 bytes a row: by TMA where all 32 rows are the tile's
+            // and 16-byte multiples, else by the lanes, a row's bytes by neighbouring ones.
+            const int col0 = nt * C::TN + half * 128;
+            const int need = min(4, (cols - col0 + 31) / 32);   // groups of 32 columns that are the result's
+            auto taken = [&] {                               // the accumulator has been read
+                if (!some) return;
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
@@ -429,43 +379,84 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
                     else mbar_arrive(&t_empty[b]);
                 }
             };
-            if (p.y_bf16) {
+            auto at = [&](int r, int chunk) { return out + r * 128 + ((chunk ^ (r & 7)) << 4); };
+            auto fetch = [&](int l, uint32_t (&to)[32]) {
+                if (some) tmem_ld_32x32b_x32(from + l * 32, to);
+                else
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {                // 128 columns
-                    uint32_t d[4][32];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) fetch(h * 128 + c * 32, d[c]);
-                    emptied();
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        if (some) tmem_ld_wait(d[c]);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            *reinterpret_cast<uint4 *>(at(c >> 1, lane, (c & 1) * 4 + j)) =
-                                make_uint4(bf16x2(d[c][8 * j], d[c][8 * j + 1]), bf16x2(d[c][8 * j + 2], d[c][8 * j + 3]),
-                                           bf16x2(d[c][8 * j + 4], d[c][8 * j + 5]), bf16x2(d[c][8 * j + 6], d[c][8 * j + 7]));
-                    }
-                    if (h == 1 && some) taken();
-                    send(nt * 256 + h * 128, std::integral_constant<int, 2>{});
+                    for (int j = 0; j < 32; ++j) to[j] = 0;
+            };
+            auto write = [&](auto elem_size) {
+                constexpr int elem = decltype(elem_size)::value, per = 128 / elem, LOADS = per / 32;
+                if (need <= 0) {
+                    taken();
+                    return;
                 }
-            } else {
-#pragma unroll 1
-                for (int h = 0; h < 4; ++h) {                // 64 columns
-                    uint32_t d[2][32];
+                uint32_t d[2][32];
+                fetch(0, d[0]);
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) fetch(h * 64 + c * 32, d[c]);
-                    emptied();
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        if (some) tmem_ld_wait(d[c]);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            *reinterpret_cast<uint4 *>(at(c, lane, j)) = make_uint4(d[c][4 * j], d[c][4 * j + 1], d[c][4 * j + 2], d[c][4 * j + 3]);
+                for (int l = 0; l < 4; ++l) {
+                    if (l >= need) break;
+                    uint32_t (&v)[32] = d[l & 1];
+                    if (some) tmem_ld_wait(v);
+                    if (l + 1 < need) fetch(l + 1, d[(l + 1) & 1]);
+                    else taken();
+                    if (l % LOADS == 0) {                    // (the store before has read the box)
+                        if (lane == 0) bulk_wait_group_read<0>();
+                        __syncwarp();
                     }
-                    if (h == 3 && some) taken();
-                    send(nt * 256 + h * 64, std::integral_constant<int, 4>{});
+#pragma unroll
+                    for (int j = 0; j < 8 / LOADS; ++j) {
+                        uint4 u;
+                        if constexpr (elem == 2) {
+                            const uint32_t *f = v + j * 8;
+                            u = make_uint4(bf16x2(f[0], f[1]), bf16x2(f[2], f[3]), bf16x2(f[4], f[5]), bf16x2(f[6], f[7]));
+                        } else {
+                            const uint32_t *f = v + j * 4;
+                            u = make_uint4(f[0], f[1], f[2], f[3]);
+                        }
+                        *reinterpret_cast<uint4 *>(at(lane, l % LOADS * (8 / LOADS) + j)) = u;
+                    }
+                    if (l % LOADS != LOADS - 1 && l + 1 < need) continue;
+                    const int col = col0 + l / LOADS * per;
+                    if (GRAD || (p.vec && left >= 32)) {
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            if (left > 0) {
+                                if constexpr (GRAD) tma_store_3d(&maps.y, smem_u32(out), col, (int)row, wk.e);
+                                else tma_store_2d(&maps.y, smem_u32(out), col, (int)row);
+                            }
+                            bulk_commit_group();
+                        }
+                        continue;
+                    }
+                    __syncwarp();
+                    uint8_t *y = static_cast<uint8_t *>(p.y) + row * p.N * elem + (int64_t)col * elem;
+                    const int64_t pitch = (int64_t)p.N * elem;
+                    const int bytes = min(per, p.N - col) * elem;
+                    if (p.vec) {
+                        for (int i = lane; i < 32 * 8; i += 32)
+                            if (i / 8 < left && i % 8 * 16 < bytes)
+                                *reinterpret_cast<uint4 *>(y + i / 8 * pitch + i % 8 * 16) = *reinterpret_cast<const uint4 *>(at(i / 8, i % 8));
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < LOADS; ++k) {
+                            const int c = (lane + 32 * k) * elem;
+#pragma unroll 8
+                            for (int r = 0; r < 32; ++r) {
+                                const uint8_t *src = at(r, c >> 4) + (c & 15);
+                                if (r >= left || c >= bytes) continue;
+                                if constexpr (elem == 2) *reinterpret_cast<uint16_t *>(y + c + r * pitch) = *reinterpret_cast<const uint16_t *>(src);
+                                else *reinterpret_cast<uint32_t *>(y + c + r * pitch) = *reinterpret_cast<const uint32_t *>(src);
+                            }
+                        }
+                    }
+                    __syncwarp();
                 }
-            }
+            };
+            if (p.y_bf16) write(std::integral_constant<int, 2>{});
+            else write(std::integral_constant<int, 4>{});
         }
         if (lane == 0) bulk_wait_group_all();
         __syncwarp();
@@ -532,7 +523,8 @@ static cudaError_t run_large(const Maps &maps, const Params &p, int64_t tiles, c
 template <class C>
 static cudaError_t launch_large(const Bf16Args &a, cudaStream_t s) {
     Maps maps{};
-    Params p{a.offsets, a.y, a.err, a.M, a.N, a.K, a.E, (a.N + C::TN - 1) / C::TN, 0, a.y_dtype == ZFFN_DT_BF16, 0, 0, C::KIND == BACK && a.N % 64 == 0};
+    Params p{a.offsets, a.y, a.err, a.M, a.N, a.K, a.E, (a.N + C::TN - 1) / C::TN, 0, a.y_dtype == ZFFN_DT_BF16, 0, 0, C::KIND == BACK && a.N % 64 == 0, {}, {}};
+    p.each = C::Walk::divisor(p.n_tiles);
     const int elem = p.y_bf16 ? 2 : 4;
     p.vec = a.N * elem % 16 == 0 && (reinterpret_cast<uintptr_t>(a.y) & 15) == 0;
     if (!encode(maps.a, a.a, 2, a.K, a.M, 1, 128, false)) return cudaErrorInvalidValue;
@@ -551,8 +543,9 @@ static cudaError_t launch(const Bf16Args &a, cudaStream_t s) {
 template <class C>
 static cudaError_t launch_weights(const Bf16GradArgs &a, cudaStream_t s) {
     Maps maps{};
-    const Params p{a.offsets, a.dw, a.err, a.M, a.N, a.K, a.E, (a.K + C::TN - 1) / C::TN, (a.N + C::TM - 1) / C::TM, a.dw_dtype == ZFFN_DT_BF16, 1,
-                   a.N % 64 == 0, a.K % 64 == 0};
+    Params p{a.offsets, a.dw, a.err, a.M, a.N, a.K, a.E, (a.K + C::TN - 1) / C::TN, (a.N + C::TM - 1) / C::TM, a.dw_dtype == ZFFN_DT_BF16, 1,
+                   a.N % 64 == 0, a.K % 64 == 0, {}, FastDiv((a.K + C::TN - 1) / C::TN)};
+    p.each = C::Walk::divisor(p.m_tiles * p.n_tiles);
     for (int x = 0; x < 3; ++x)
         if (!encode(&maps.a[x], a.dy, 2, a.N, a.M, 1, 16 << x, false, p.wide_a ? 2 : 0) ||
             !encode(&maps.w[x], a.a, 2, a.K, a.M, 1, 16 << x, false, p.wide_w ? C::W_ROWS / 64 : 0))
