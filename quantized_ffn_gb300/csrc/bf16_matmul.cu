@@ -20,6 +20,9 @@ namespace b16 {
 #ifndef PAIR_RULE
 #define PAIR_RULE 1
 #endif
+#ifndef SMALL_RULE
+#define SMALL_RULE 64
+#endif
 enum Kind { FORWARD, BACK, WEIGHTS };
 constexpr int KB = 64;            // contracted values of a stage: rows of 128 bytes, or 64 rows
 
@@ -59,6 +62,9 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, uint32_t sr
                      reinterpret_cast<uint64_t>(map)),
                  "r"(src), "r"(c0), "r"(c1), "r"(c2)
                  : "memory");
+}
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 // Shared-memory matrix descriptor of an MN-major operand, 128-byte swizzle: boxes of 64
 // values of the free index (128 bytes) by 64 (or 16, or 32) of the contracted one, box_bytes
@@ -479,6 +485,227 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
     }
 }
 
+// ---------------------------------------------------------------------------
+// Few rows an expert: the weights on the MMA's M side.  A tile is 128 columns of the
+// result times TN rows of a; each cluster takes tiles in turn.  Where the tiles are
+// fewer than the SMs a cluster's blocks split K: row j's sums go to the shared memory
+// of rank j % split, which adds them in rank order, so that the result is the same
+// every time.  Bound by HBM: every weight is read once.
+//
+// Roles: warps 0 .. 3 take a tile out of tensor memory (32 columns of the result each)
+// and write it, warp 4 loads by TMA, warp 5 issues the MMAs.
+// ---------------------------------------------------------------------------
+template <int KIND_, int TN_>
+struct SmallCfg {
+    static constexpr int KIND = KIND_, TN = TN_;
+    static constexpr bool W_MN = KIND == BACK;
+    static constexpr int W_BYTES = 128 * 128;
+    static constexpr int STAGE = W_BYTES + TN * 128;
+    static constexpr int BLOCKS = 2;                         // blocks an SM
+    static constexpr int NS = TN == 64 ? 3 : TN == 32 ? 4 : 5;
+    static constexpr int EPI = 4;
+    static constexpr int THREADS = (EPI + 2) * 32;
+    static constexpr int MAX_SPLIT = 8;
+    static constexpr int TMEM_COLS = 2 * TN;                 // two accumulators
+    static constexpr int PART_ROWS = TN + MAX_SPLIT - 1;     // split * ceil(TN / split), at most
+    static constexpr int OFF_PART = NS * STAGE;              // sums [rank][row / split][128]
+    static constexpr int OFF_BAR = OFF_PART + PART_ROWS * 512;
+    static constexpr int SMEM = OFF_BAR + (2 * NS + 5) * 8 + 8 + 1024;
+    using Walk = GroupWalk<TN, 8>;
+};
+
+template <class C>
+__global__ void __launch_bounds__(C::THREADS, C::BLOCKS) small_kernel(const __grid_constant__ Maps maps, const Params p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    float *part = reinterpret_cast<float *>(smem + C::OFF_PART);
+    uint64_t *s_full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
+    uint64_t *s_empty = s_full + C::NS, *t_full = s_empty + C::NS, *t_empty = t_full + 2, *done = t_empty + 2;
+    int *info = reinterpret_cast<int *>(done + 1);           // abort, TMEM base
+    volatile int *abort_flag = info;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint32_t split;
+    asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(split));
+    const uint32_t rank = cluster_ctarank();
+    if (split > 1) cluster_arrive();                         // (waited for before another's memory is written)
+    if (warp == C::EPI && lane == 0) {
+        info[0] = 0;
+        for (int i = 0; i < C::NS; ++i) { mbar_init(&s_full[i], 1); mbar_init(&s_empty[i], 1); }
+        for (int i = 0; i < 2; ++i) { mbar_init(&t_full[i], 1); mbar_init(&t_empty[i], C::EPI); }
+        mbar_init(done, 1);
+        fence_mbarrier_init();
+        prefetch_tensormap(maps.a);
+        prefetch_tensormap(maps.w);
+    }
+    if (warp == C::EPI + 1) {
+        tmem_alloc(reinterpret_cast<uint32_t *>(info + 1), C::TMEM_COLS);
+        tmem_relinquish();
+        tc_fence_before();
+    }
+    __syncthreads();
+    grid_wait();
+    grid_launch_dependents();          // (this block has its tensor memory)
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(info + 1);
+    const int blocks = (p.K + KB - 1) / KB;
+    const int kb0 = blocks * rank / split, nkb = blocks * (rank + 1) / split - kb0;   // this rank's share of K
+    const int step = gridDim.x / split;
+    typename C::Walk wk;
+    wk.start(p.offsets, p.M, p.E, p.n_tiles, p.each, true, blockIdx.x / split);
+    const uint32_t slice = (C::TN + split - 1) / split;      // rows of a tile that a rank adds up
+    const uint32_t inverse = (65536 + split - 1) / split;    // j * inverse >> 16 = j / split for j < 64
+    // (split > 1: no more tiles than clusters, so each has one at most, and its walk ends there)
+    auto next = [&] {
+        wk.t += step;
+        return split == 1 && wk.get();
+    };
+    bool some_tile = false;            // warps 0 .. 3, split > 1: sums were sent
+    int last_row0 = 0, last_rows = 0, last_nt = 0;
+
+    if (warp == C::EPI) {
+        // ---- TMA producer
+        uint32_t it = 0;
+        bool ok = true;
+        for (bool have = wk.get(); ok && have; have = next()) {
+            for (int i = kb0; i < kb0 + nkb && lane == 0 && wk.e < p.E; ++i, ++it) {
+                const uint32_t s = it % C::NS;
+                if (it >= C::NS && !bar_wait(&s_empty[s], ((it / C::NS) & 1) ^ 1, abort_flag, p.err)) { ok = false; break; }
+                uint8_t *sw = smem + s * C::STAGE;
+                mbar_arrive_expect_tx(&s_full[s], C::STAGE);
+                if constexpr (!C::W_MN) {
+                    tma_load_3d(sw, maps.w, &s_full[s], i * KB, wk.nt * 128, wk.e);
+                } else if (p.wide_w) {
+                    tma_load_4d(sw, maps.w, &s_full[s], 0, i * KB, wk.nt * 2, wk.e);
+                } else {
+                    for (int b = 0; b < 2; ++b) tma_load_3d(sw + b * 8192, maps.w, &s_full[s], wk.nt * 128 + b * 64, i * KB, wk.e);
+                }
+                tma_load_2d(sw + C::W_BYTES, maps.a, &s_full[s], i * KB, wk.row0);
+            }
+            ok = __shfl_sync(0xffffffffu, ok && !*abort_flag, 0);
+        }
+        if (lane == 0 && *abort_flag)   // wait for the copies in flight before the block leaves
+            for (uint32_t j = it > C::NS ? it - C::NS : 0; j < it; ++j)
+                mbar_wait(&s_full[j % C::NS], (j / C::NS) & 1, nullptr, p.err);
+        __syncwarp();
+    } else if (warp == C::EPI + 1) {
+        // ---- MMA issuer
+        constexpr uint32_t idesc = idesc_bf16_f32(128, C::TN, C::W_MN, false);
+        uint32_t it = 0, acc = 0;
+        bool ok = true;
+        for (bool have = wk.get(); ok && have; have = next()) {
+            if (wk.e >= p.E || nkb == 0) continue;
+            const uint32_t b = acc & 1, dst = tmem + b * C::TN;
+            ok = acc < 2 || bar_wait(&t_empty[b], ((acc >> 1) & 1) ^ 1, abort_flag, p.err);
+            for (int i = 0; i < nkb; ++i, ++it) {
+                const uint32_t s = it % C::NS;
+                ok = ok && bar_wait(&s_full[s], (it / C::NS) & 1, abort_flag, p.err);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                tc_fence_after();
+                const uint32_t sw = smem_u32(smem) + s * C::STAGE;
+                const int n = (min(KB, p.K - (kb0 + i) * KB) + 15) / 16;
+                const uint64_t wd = C::W_MN ? smem_desc_mn_sw128(sw, 8192) : smem_desc_k_sw128(sw);
+                const uint64_t ad = smem_desc_k_sw128(sw + C::W_BYTES);
+                if (elect_one()) {
+#pragma unroll
+                    for (int k = 0; k < KB / 16; ++k) {
+                        if (k >= n) break;
+                        tc_mma_bf16(dst, wd + k * k_step(C::W_MN), ad + k * k_step(false), idesc, (i | k) != 0);
+                    }
+                    tc_commit(&s_empty[s]);
+                    if (i == nkb - 1) tc_commit(&t_full[b]);
+                }
+                __syncwarp();
+            }
+            ++acc;
+            ok = __all_sync(0xffffffffu, ok && !*abort_flag);
+        }
+        if (elect_one()) tc_commit(done);
+        __syncwarp();
+    } else {
+        // ---- take out and write: thread = one column of the result
+        const uint32_t taddr = tmem + ((uint32_t)(warp * 32) << 16);
+        const int tid = threadIdx.x;
+        uint32_t acc = 0;
+        bool ok = true;
+        for (bool have = wk.get(); ok && have; have = next()) {
+            const bool some = wk.e < p.E && nkb != 0;
+            const uint32_t b = acc & 1;
+            if (some) {
+                ok = __all_sync(0xffffffffu, bar_wait(&t_full[b], (acc >> 1) & 1, abort_flag, p.err));
+                if (!ok) break;
+                tc_fence_after();
+                ++acc;
+            }
+            const int n = wk.nt * 128 + tid;
+            constexpr int CH = 16;
+            if (split > 1) {
+                cluster_wait();                              // every block of the cluster runs
+                some_tile = true;
+                last_row0 = wk.row0; last_rows = wk.rows; last_nt = wk.nt;
+            }
+            const uint32_t to = smem_u32(part + rank * slice * 128) + tid * 4;
+#pragma unroll
+            for (int c = 0; c < C::TN; c += CH) {
+                if (c >= wk.rows) break;
+                uint32_t d[CH];
+                if (some) {
+                    tmem_ld_32x32b_x16(taddr + b * C::TN + c, d);
+                    tmem_ld_wait(d);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < CH; ++j) d[j] = 0;
+                }
+                if (split > 1) {
+#pragma unroll
+                    for (int j = 0; j < CH; ++j)
+                        if (c + j < wk.rows) {
+                            const uint32_t at = (c + j) * inverse >> 16;
+                            st_cluster_f32(mapa_shared(to + at * 512, c + j - at * split), __uint_as_float(d[j]));
+                        }
+                } else if (n < p.N) {
+                    const int64_t at = (int64_t)(wk.row0 + c) * p.N + n;
+#pragma unroll
+                    for (int j = 0; j < CH; ++j)
+                        if (c + j < wk.rows) {
+                            if (p.y_bf16) static_cast<__nv_bfloat16 *>(p.y)[at + (int64_t)j * p.N] = __float2bfloat16_rn(__uint_as_float(d[j]));
+                            else static_cast<float *>(p.y)[at + (int64_t)j * p.N] = __uint_as_float(d[j]);
+                        }
+                }
+            }
+            if (some) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&t_empty[b]);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (split > 1) {
+        if (!some_tile) cluster_wait();                      // (who has not met the first barrier above)
+        cluster_sync_all();
+        if (some_tile) {
+            // the ranks' sums in rank order
+            const int n = last_nt * 128 + threadIdx.x;
+            for (int j = rank, i = 0; j < last_rows; j += split, ++i) {
+                float v = part[i * 128 + threadIdx.x];
+                for (uint32_t r = 1; r < split; ++r) v += part[(r * slice + i) * 128 + threadIdx.x];
+                const int64_t at = (int64_t)(last_row0 + j) * p.N + n;
+                if (n < p.N) {
+                    if (p.y_bf16) static_cast<__nv_bfloat16 *>(p.y)[at] = __float2bfloat16_rn(v);
+                    else static_cast<float *>(p.y)[at] = v;
+                }
+            }
+        }
+    }
+    if (warp == C::EPI + 1) {
+        if (lane == 0) mbar_wait(done, 0, nullptr, p.err);
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, C::TMEM_COLS);
+    }
+}
+
 // ---- host -------------------------------------------------------------------
 
 // bf16 or fp32 tensor [d2][d1][d0] in boxes of 128 bytes x box1, 128-byte swizzle; loads
@@ -534,8 +761,79 @@ static cudaError_t launch_large(const Bf16Args &a, cudaStream_t s) {
     return run_large<C>(maps, p, row_tiles_bound(a.M, a.E, a.offsets, C::TM) * p.n_tiles, s);
 }
 
+// Ask once a device for the largest share of shared memory, so that C::BLOCKS blocks run
+// on an SM.
+template <class C>
+static cudaError_t prefer_shared() {
+    static std::atomic<uint64_t> asked{0};
+    const uint64_t bit = 1ull << (device_info().device & 63);
+    if (asked.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    const cudaError_t e =
+        cudaFuncSetAttribute(small_kernel<C>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    if (e == cudaSuccess) asked.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
+
+// Clusters of `split` small-tile blocks that the current device runs at once with one block
+// an SM (the query counts one whatever the shared memory; asked once for each device and
+// split, and again where it failed).
+template <class C>
+static int clusters_at_once(int split) {
+    static std::atomic<int> known[64][C::MAX_SPLIT + 1];
+    std::atomic<int> &k = known[device_info().device & 63][split];
+    int n = k.load(std::memory_order_relaxed);
+    if (n == 0) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(split);
+        cfg.blockDim = dim3(C::THREADS);
+        cfg.dynamicSmemBytes = C::SMEM;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = split;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&n, small_kernel<C>, &cfg) != cudaSuccess || n < 1) {
+            cudaGetLastError();
+            return 1;
+        }
+        k.store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
+
+template <class C>
+static cudaError_t launch_small(const Bf16Args &a, cudaStream_t s) {
+    const DeviceInfo &di = device_info();
+    Maps maps{};
+    Params p{a.offsets, a.y, a.err, a.M, a.N, a.K, a.E, (a.N + 127) / 128, 0, a.y_dtype == ZFFN_DT_BF16, 0, 0, C::KIND == BACK && a.N % 64 == 0, {}, {}};
+    p.each = C::Walk::divisor(p.n_tiles);
+    if (!encode(maps.a, a.a, 2, a.K, a.M, 1, C::TN, false)) return cudaErrorInvalidValue;
+    if (!(C::KIND == FORWARD ? encode(maps.w, a.w, 2, a.K, a.N, a.E, 128, true) : encode(maps.w, a.w, 2, a.N, a.K, a.E, KB, true, p.wide_w ? 2 : 0)))
+        return cudaErrorInvalidValue;
+    cudaError_t e = ensure_dynamic_smem((const void *)small_kernel<C>, C::SMEM);
+    if (e == cudaSuccess) e = prefer_shared<C>();
+    if (e != cudaSuccess) return e;
+    // fewer tiles than blocks: split K so that the blocks fill the SMs, two stages each at
+    // least, and all clusters run at once (a second wave costs more than the split gains)
+    const int64_t tiles = row_tiles_bound(a.M, a.E, a.offsets, C::TN) * p.n_tiles, slots = (int64_t)di.num_sms * C::BLOCKS;
+    if (tiles + slots > 0x7fffffff) return cudaErrorInvalidValue;
+    const int most = (a.K + KB - 1) / KB / 2;
+    int split = most < C::MAX_SPLIT ? most : C::MAX_SPLIT;
+    if (split > slots / tiles) split = (int)(slots / tiles);
+    while (split > 1 && (int64_t)clusters_at_once<C>(split) * C::BLOCKS < tiles) --split;
+    if (split < 1) split = 1;
+    const int64_t clusters = split > 1 || tiles < slots ? tiles : slots;
+    return launch_dependent(small_kernel<C>, dim3((unsigned)(clusters * split)), C::THREADS, C::SMEM, (unsigned)split, s, maps, p);
+}
+
 template <int KIND>
 static cudaError_t launch(const Bf16Args &a, cudaStream_t s) {
+    const int64_t mean = a.offsets ? ((int64_t)a.M * 3 / 2 + a.E - 1) / a.E : a.M;
+    if (mean <= 16) return launch_small<SmallCfg<KIND, 16>>(a, s);
+    if (mean <= 32) return launch_small<SmallCfg<KIND, 32>>(a, s);
+    if (mean <= SMALL_RULE) return launch_small<SmallCfg<KIND, 64>>(a, s);
     if (PAIR_RULE) return launch_large<LargeCfg<KIND, true>>(a, s);
     return launch_large<LargeCfg<KIND, false>>(a, s);
 }
