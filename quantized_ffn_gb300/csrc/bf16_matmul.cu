@@ -17,12 +17,6 @@
 namespace zffn {
 namespace b16 {
 
-#ifndef PAIR_RULE
-#define PAIR_RULE 1
-#endif
-#ifndef SMALL_RULE
-#define SMALL_RULE 64
-#endif
 enum Kind { FORWARD, BACK, WEIGHTS };
 constexpr int KB = 64;            // contracted values of a stage: rows of 128 bytes, or 64 rows
 
@@ -101,8 +95,8 @@ struct Params {
     int vec;            // y's rows are 16-byte multiples
     // an MN-major operand whose rows are whole boxes wide (the columns a multiple of 64):
     // one copy takes all boxes of a tile, its map counting boxes by an index of their own.
-    // (With a copy a box the one issuing thread held the weights' gradients back: 32768 rows
-    // of 128 experts, 1536 x 2048, WIDE_US us against NARROW_US us.)
+    // (With a copy a box the one issuing thread held the weights' gradients back: an even
+    // 256 rows of 128 experts, 1536 x 2048, 185 us against 202.)
     int wide_a, wide_w;
     FastDiv each, across;   // of the walk; weights: by n_tiles
 };
@@ -830,11 +824,20 @@ static cudaError_t launch_small(const Bf16Args &a, cudaStream_t s) {
 
 template <int KIND>
 static cudaError_t launch(const Bf16Args &a, cudaStream_t s) {
-    const int64_t mean = a.offsets ? ((int64_t)a.M * 3 / 2 + a.E - 1) / a.E : a.M;
+    // Rows an expert, and 128 x 256 tiles at least.  Small tiles: the least of 16, 32 rows
+    // that takes an expert's rows (with some spread over their mean) at once, so that its
+    // weights are read once; of 64 where the large ones are so few that splitting K gains more
+    // (times of 1536 x 2048 in us, small and large: 128 experts of 24 rows 138 / 140, of 48
+    // rows 135 / 144, of 64 rows 148 / 144; one of 64 rows 9.5 / 15.4, of 256 rows 11.7 / 15.7,
+    // of 512 rows 15.9 / 16.0).
+    const int64_t rows = a.M / a.E, mean = a.offsets ? ((int64_t)a.M * 3 / 2 + a.E - 1) / a.E : a.M;
     if (mean <= 16) return launch_small<SmallCfg<KIND, 16>>(a, s);
     if (mean <= 32) return launch_small<SmallCfg<KIND, 32>>(a, s);
-    if (mean <= SMALL_RULE) return launch_small<SmallCfg<KIND, 64>>(a, s);
-    if (PAIR_RULE) return launch_large<LargeCfg<KIND, true>>(a, s);
+    const int64_t most = (int64_t)a.M / 128 + (a.E < a.M ? a.E : a.M), tiles = most * ((a.N + 255) / 256);
+    if (tiles <= device_info().num_sms / 6) return launch_small<SmallCfg<KIND, 64>>(a, s);
+    // CTA pairs where few of their 256 rows are past an expert's (single and pair: 128 experts
+    // of 96 rows 142 / 154, of 192 rows 184 / 176, of 256 rows 207 / 195, 8 of 4096 rows 139 / 124)
+    if (rows >= 192) return launch_large<LargeCfg<KIND, true>>(a, s);
     return launch_large<LargeCfg<KIND, false>>(a, s);
 }
 
@@ -862,7 +865,10 @@ cudaError_t launch_bf16_matmul(const Bf16Args &a, cudaStream_t s) {
 cudaError_t launch_bf16_grad_w(const Bf16GradArgs &a, cudaStream_t s) {
     using namespace b16;
     if (!encode_fn()) return cudaErrorNotSupported;
-    if (PAIR_RULE) return launch_weights<LargeCfg<WEIGHTS, true>>(a, s);
+    // CTA pairs where their tiles are four rounds at least (dw of 2056 x 1032, single and pair:
+    // 128 experts of 24 rows 122 / 115 us, of 256 rows 260 / 228, one of 64 rows 6.5 / 7.5)
+    const int64_t tiles = (int64_t)a.E * ((a.N + 255) / 256) * ((a.K + 255) / 256);
+    if (tiles >= 2 * (int64_t)device_info().num_sms) return launch_weights<LargeCfg<WEIGHTS, true>>(a, s);
     return launch_weights<LargeCfg<WEIGHTS, false>>(a, s);
 }
 
