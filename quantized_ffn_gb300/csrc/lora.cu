@@ -1,109 +1,904 @@
-// lora.cu -- low-rank adapters: products of rows grouped by adapter, and the sums of
-// outer products over an adapter's rows.  One thread sums one value.
+// lora.cu -- low-rank adapters of many requests at once.  With the tokens sorted by
+// adapter (rows), e the adapter of a row and t its token:
+//     shrink   v[row]  = scale[e] x[t] W_e^T      fp32 [T][r]
+//     expand   out[t]  = base[t] + v[row] W_e^T
+//     outer    d_e     = sum over e's rows of v[row]^T x[t]
+// The forward pass is shrink by A and expand by B; the way back shrink of dy by B,
+// expand by A, and two outer products.  r is small (8 to 128), so each is bound by the
+// tokens' rows, which are gathered (and written back) by their tokens where they lie.
+//
+// Tensor cores take bf16, and v is fp32: it goes as the sum of three bf16 pieces of 8
+// bits each, which is exact, so that v is not rounded between the products.
+#include <atomic>
+
 #include "bf16.h"
+#include "groups.cuh"
 #include "launch.cuh"
+#include "roles.cuh"
+#include "tiles.cuh"
 
 namespace zffn {
-namespace {
+namespace lora {
 
-__device__ __forceinline__ float value(const void *p, int64_t i, bool bf16) {
-    return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]) : static_cast<const float *>(p)[i];
-}
-__device__ __forceinline__ void put(void *p, int64_t i, bool bf16, float v) {
-    if (bf16) static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(v);
-    else static_cast<float *>(p)[i] = v;
-}
-// First row of group g (g == E: of the rows of none): the largest offset up to it.
-__device__ int first_row(const int32_t *offsets, int g, int E, int M) {
-    if (!offsets) return g == 0 ? 0 : M;
-    int lo = 0;
-    for (int i = 0; i <= min(g, E); ++i) lo = max(lo, min(max(offsets[i], 0), M));
-    return g > E ? M : lo;
-}
+// ---- pieces -----------------------------------------------------------------
 
-struct Rows {
-    const void *x, *w, *base;
-    void *y;
-    const int32_t *offsets, *in_row, *out_row, *slot_row;   // in_row, out_row: row -> row of x, of y (nullptr: itself)
+// 16 bytes global -> shared, or 16 zero bytes (the address is then not read).
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool some) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(some ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+// A row's bytes (a multiple of 16) by the copy engine, and back.
+__device__ __forceinline__ void row_load(uint32_t dst, const void *src, uint32_t bytes, uint64_t *bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src), "r"(bytes),
+                 "r"(smem_u32(bar))
+                 : "memory");
+}
+__device__ __forceinline__ void row_store(void *dst, uint32_t src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ float lo_f32(uint32_t two) { return __uint_as_float(two << 16); }
+__device__ __forceinline__ float hi_f32(uint32_t two) { return __uint_as_float(two & 0xFFFF0000u); }
+// v = p[0] + p[1] + p[2], bf16 values in the high halves: v's bits cut after 8 and 16
+// (differences of values that agree so far are exact).  Infinities and NaN stay in p[0].
+__device__ __forceinline__ void pieces(float v, uint32_t (&p)[3]) {
+    p[0] = __float_as_uint(v) & 0xFFFF0000u;
+    const float rest = v - __uint_as_float(p[0]);
+    p[1] = __float_as_uint(rest) & 0xFFFF0000u;
+    p[2] = __float_as_uint(rest - __uint_as_float(p[1]));
+    if (!(fabsf(v) <= 3.402823466e38f)) {
+        p[0] = v != v ? 0x7FFF0000u : p[0];
+        p[1] = p[2] = 0;
+    }
+}
+__device__ __forceinline__ uint32_t high_halves(uint32_t lo, uint32_t hi) { return __byte_perm(lo, hi, 0x7632); }
+__host__ __device__ constexpr int up16(int r) { return (r + 15) / 16 * 16; }
+
+struct Params {
+    const int32_t *row_slot, *slot_row, *offsets;
     const float *scale;
-    bool x_bf16, y_bf16;
-    int M, N, K, E;
-    int64_t wn, wk;   // strides of w by n and k
+    int *err;
+    int T, r, L, C;
+    FastDiv each;
 };
-// y[out(m)][n] = base + scale sum_k x[in(m)][k] w[e][n][k]
-__global__ void rows_kernel(const Rows p) {
-    const int g = blockIdx.y, n = blockIdx.x * 32 + threadIdx.x;
-    const int lo = first_row(p.offsets, g, p.E, p.M), hi = first_row(p.offsets, g + 1, p.E, p.M);
-    if (n >= p.N) return;
-    for (int m = lo + blockIdx.z * blockDim.y + threadIdx.y; m < hi; m += gridDim.z * blockDim.y) {
-        const int in = p.in_row ? p.in_row[m] : m, out = p.out_row ? p.out_row[m] : m;
-        const bool some = g < p.E && (unsigned)in < (unsigned)p.M;
-        float sum = 0.0f;
-        if (some)
-            for (int k = 0; k < p.K; ++k)
-                sum += value(p.x, (int64_t)in * p.K + k, p.x_bf16) * value(p.w, (int64_t)g * p.N * p.K + n * p.wn + k * p.wk, true);
-        if (p.scale && some) sum *= p.scale[g];
-        if ((unsigned)out >= (unsigned)p.M || (p.out_row && !some)) continue;
-        const int64_t at = (int64_t)out * p.N + n;
-        put(p.y, at, p.y_bf16, (p.base ? value(p.base, at, p.y_bf16) : 0.0f) + sum);
-    }
-}
-// tokens of no adapter: y = base or 0
-__global__ void rest_kernel(const Rows p) {
-    const int n = blockIdx.x * 32 + threadIdx.x;
-    if (n >= p.N) return;
-    for (int t = blockIdx.z * blockDim.y + threadIdx.y; t < p.M; t += gridDim.z * blockDim.y)
-        if (p.slot_row[t] < 0) put(p.y, (int64_t)t * p.N + n, p.y_bf16, p.base ? value(p.base, (int64_t)t * p.N + n, p.y_bf16) : 0.0f);
-}
-cudaError_t launch_rows(const Rows &p, cudaStream_t s) {
-    const dim3 grid((p.N + 31) / 32, p.E + (p.offsets ? 1 : 0), p.M / p.E / 8 + 1 < 64 ? p.M / p.E / 8 + 1 : 64);
-    rows_kernel<<<grid, dim3(32, 8), 0, s>>>(p);
-    if (p.slot_row && p.y != p.base) rest_kernel<<<dim3((p.N + 31) / 32, 1, 64), dim3(32, 8), 0, s>>>(p);
-    return cudaGetLastError();
+
+// ---------------------------------------------------------------------------
+// Shrink on the tensor cores: 128 rows (gathered, on the MMA's M side) times all r rows
+// of W.  The blocks of a cluster share the contraction; rows 128 / split * i and on are
+// added up by rank i, in rank order.
+//
+// Roles: warps 0 .. 3 gather x's rows, then take the sums out; warp 4 loads W by TMA,
+// warp 5 issues the MMAs.
+// ---------------------------------------------------------------------------
+constexpr int S_NS = 4, S_LAG = 2, S_THREADS = 192, S_MAX_SPLIT = 8;
+
+// W's bytes of a stage: K-major [r][64], or MN-major boxes [64][64]
+__host__ __device__ constexpr int s_w_bytes(int r, bool mn) { return mn ? (r + 63) / 64 * 8192 : up16(r) * 128; }
+static size_t s_smem(int r, bool mn, int split) {
+    return 1024 + (size_t)S_NS * (16384 + s_w_bytes(r, mn)) + (split > 1 ? 128 * r * 4 : 0) + (2 * S_NS + 1) * 8 + 8;
 }
 
-struct Outer {
-    const void *a, *b;
-    void *d;
-    const int32_t *offsets, *a_row, *b_row;
-    bool a_bf16, b_bf16, d_bf16;
-    int M, NA, NB, E;
-};
-// d[e][i][j] = sum over e's rows of a[.][i] b[.][j]
-__global__ void outer_kernel(const Outer p) {
-    const int g = blockIdx.z;
-    const int lo = first_row(p.offsets, g, p.E, p.M), hi = first_row(p.offsets, g + 1, p.E, p.M);
-    const int j = blockIdx.x * 32 + threadIdx.x;
-    for (int i = blockIdx.y * 8 + threadIdx.y; i < p.NA; i += gridDim.y * 8) {
-        if (j >= p.NB) return;
-        float sum = 0.0f;
-        for (int m = lo; m < hi; ++m) {
-            const int ra = p.a_row ? p.a_row[m] : m, rb = p.b_row ? p.b_row[m] : m;
-            if ((unsigned)ra >= (unsigned)p.M || (unsigned)rb >= (unsigned)p.M) continue;
-            sum += value(p.a, (int64_t)ra * p.NA + i, p.a_bf16) * value(p.b, (int64_t)rb * p.NB + j, p.b_bf16);
+template <bool MN>
+__global__ void __launch_bounds__(S_THREADS) shrink_kernel(const __grid_constant__ CUtensorMap w, const Params p, const __nv_bfloat16 *x, float *v) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint32_t split;
+    asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(split));
+    const uint32_t rank = cluster_ctarank();
+    const int wb = s_w_bytes(p.r, MN), stage = 16384 + wb;
+    float *part = reinterpret_cast<float *>(smem + S_NS * stage);
+    uint64_t *s_full = reinterpret_cast<uint64_t *>(smem + S_NS * stage + (split > 1 ? 128 * p.r * 4 : 0));
+    uint64_t *s_empty = s_full + S_NS, *t_full = s_empty + S_NS;
+    int *info = reinterpret_cast<int *>(t_full + 1);         // abort, TMEM base
+    volatile int *abort_flag = info;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
+    const int r16 = up16(p.r), cols = r16 <= 32 ? 32 : r16 <= 64 ? 64 : 128;
+    if (split > 1) cluster_arrive();                         // (waited for before another's memory is written)
+    if (tid == 0) {
+        info[0] = 0;
+        for (int i = 0; i < S_NS; ++i) { mbar_init(&s_full[i], 5); mbar_init(&s_empty[i], 1); }
+        mbar_init(t_full, 1);
+        fence_mbarrier_init();
+    }
+    if (warp == 4 && lane == 0) prefetch_tensormap(&w);
+    if (warp == 5) {
+        tmem_alloc(reinterpret_cast<uint32_t *>(info + 1), cols);
+        tmem_relinquish();
+        tc_fence_before();
+    }
+    __syncthreads();
+    grid_wait();
+    grid_launch_dependents();          // (this block has its tensor memory)
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(info + 1);
+    GroupWalk<128, 1> wk;
+    wk.start(p.offsets, p.T, p.L, 1, p.each, true, blockIdx.x / split);
+    const bool have = wk.get(), some = have && wk.e < p.L;
+    const int blocks = (p.C + KB - 1) / KB;
+    const int kb0 = blocks * rank / split, nkb = blocks * (rank + 1) / split - kb0;
+    const float scale = some && p.scale ? __ldcg(p.scale + wk.e) : 1.0f;
+
+    if (some && warp < 4) {
+        // ---- gather: thread = one 16-byte column of rows tid / 8 + 16 i
+        const int chunk = tid & 7, first = tid >> 3;
+        const uint32_t dst = smem_u32(smem) + first * 128 + ((chunk ^ (first & 7)) << 4);
+        const __nv_bfloat16 *src[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int row = first + 16 * i, t = row < wk.rows ? __ldcg(p.row_slot + wk.row0 + row) : -1;
+            src[i] = (unsigned)t < (unsigned)p.T ? x + (int64_t)t * p.C + chunk * 8 : nullptr;
         }
-        put(p.d, ((int64_t)g * p.NA + i) * p.NB + j, p.d_bf16, sum);
+        bool ok = true;
+        auto filled = [&](int i) {     // this thread's copies of stage i have arrived
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s_full[i % S_NS]);
+        };
+        for (int i = 0; i < nkb; ++i) {
+            const int s = i % S_NS, c = (kb0 + i) * KB;
+            if (i >= S_NS) ok = __all_sync(0xffffffffu, bar_wait(&s_empty[s], ((i / S_NS) & 1) ^ 1, abort_flag, p.err));
+            if (!ok) break;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const bool there = src[j] && c + chunk * 8 < p.C;
+                copy16(dst + s * stage + j * 2048, there ? src[j] + c : x, there);
+            }
+            copy_commit();
+            if (i >= S_LAG) {
+                copy_wait<S_LAG>();
+                filled(i - S_LAG);
+            }
+        }
+        copy_wait<0>();
+        if (ok)
+            for (int i = nkb > S_LAG ? nkb - S_LAG : 0; i < nkb; ++i) filled(i);
+    } else if (some && warp == 4) {
+        // ---- W by TMA
+        if (lane == 0) {
+            int i = 0;
+            for (; i < nkb; ++i) {
+                const int s = i % S_NS;
+                if (i >= S_NS && !bar_wait(&s_empty[s], ((i / S_NS) & 1) ^ 1, abort_flag, p.err)) break;
+                uint8_t *to = smem + s * stage + 16384;
+                if constexpr (MN) {
+                    mbar_arrive_expect_tx(&s_full[s], wb);
+                    for (int b = 0; b * 64 < p.r; ++b) tma_load_3d(to + b * 8192, &w, &s_full[s], b * 64, (kb0 + i) * KB, wk.e);
+                } else {
+                    mbar_arrive_expect_tx(&s_full[s], p.r * 128);
+                    tma_load_3d(to, &w, &s_full[s], (kb0 + i) * KB, 0, wk.e);
+                }
+            }
+            if (*abort_flag)           // wait for the copies in flight before the block leaves
+                for (int j = i > S_NS ? i - S_NS : 0; j < i; ++j) mbar_wait(&s_full[j % S_NS], (j / S_NS) & 1, nullptr, p.err);
+        }
+        __syncwarp();
+    } else if (some && warp == 5) {
+        // ---- MMA issuer
+        const uint32_t idesc = idesc_bf16_f32(128, r16, false, MN);
+        bool ok = true;
+        for (int i = 0; i < nkb; ++i) {
+            const int s = i % S_NS;
+            ok = __all_sync(0xffffffffu, bar_wait(&s_full[s], (i / S_NS) & 1, abort_flag, p.err));
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t sx = smem_u32(smem) + s * stage;
+            const int n = (min(KB, p.C - (kb0 + i) * KB) + 15) / 16;
+            const uint64_t xd = smem_desc_k_sw128(sx), wd = MN ? smem_desc_mn_sw128(sx + 16384, 8192) : smem_desc_k_sw128(sx + 16384);
+            if (elect_one()) {
+#pragma unroll
+                for (int k = 0; k < KB / 16; ++k) {
+                    if (k >= n) break;
+                    tc_mma_bf16(tmem, xd + k * k_step(false), wd + k * k_step(MN), idesc, (i | k) != 0);
+                }
+                tc_commit(&s_empty[s]);
+                if (i == nkb - 1) tc_commit(t_full);
+            }
+            __syncwarp();
+        }
+        if (!ok) {                     // (nothing issued is left on its way)
+            if (elect_one()) tc_commit(t_full);
+            __syncwarp();
+        }
+    }
+    if (have && warp < 4) {
+        // ---- take out: thread = one row
+        if (some) {
+            bar_wait(t_full, 0, abort_flag, p.err);
+            __syncwarp();
+            tc_fence_after();
+        }
+        if (split > 1) cluster_wait();                       // every block of the cluster runs
+        const uint32_t from = tmem + ((uint32_t)(warp * 32) << 16);
+        const int per = 128 / split, row = tid;
+        float *to = v + (int64_t)(wk.row0 + row) * p.r;
+        const uint32_t send = split > 1 ? mapa_shared(smem_u32(part + (rank * per + row % per) * p.r), row / per) : 0;
+        for (int c = 0; c < p.r; c += 16) {
+            uint32_t d[16];
+            if (some) {
+                tmem_ld_32x32b_x16(from + c, d);
+                tmem_ld_wait(d);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) d[j] = 0;
+            }
+#pragma unroll
+            for (int j = 0; j < 16; j += 4) {
+                if (c + j >= p.r || row >= wk.rows) continue;
+                float4 f = make_float4(__uint_as_float(d[j]), __uint_as_float(d[j + 1]), __uint_as_float(d[j + 2]), __uint_as_float(d[j + 3]));
+                if (split > 1) {
+                    st_cluster_f4(send + (c + j) * 4, f);
+                } else {
+                    f.x *= scale; f.y *= scale; f.z *= scale; f.w *= scale;
+                    *reinterpret_cast<float4 *>(to + c + j) = f;
+                }
+            }
+        }
+        tc_fence_before();
+    } else if (split > 1) {
+        cluster_wait();
+    }
+    __syncthreads();
+    if (split > 1) {
+        cluster_sync_all();
+        if (have) {
+            const int per = 128 / split, quads = p.r / 4;
+            for (int i = tid; i < per * quads; i += S_THREADS) {
+                const int lrow = i / quads, row = rank * per + lrow;
+                if (row >= wk.rows) break;
+                float4 f = reinterpret_cast<const float4 *>(part)[i];
+                for (uint32_t k = 1; k < split; ++k) {
+                    const float4 g = reinterpret_cast<const float4 *>(part)[k * per * quads + i];
+                    f.x += g.x; f.y += g.y; f.z += g.z; f.w += g.w;
+                }
+                f.x *= scale; f.y *= scale; f.z *= scale; f.w *= scale;
+                *reinterpret_cast<float4 *>(v + (int64_t)(wk.row0 + row) * p.r + (i - lrow * quads) * 4) = f;
+            }
+        }
+    }
+    if (warp == 5) {
+        tc_fence_after();
+        tmem_dealloc(tmem, cols);
     }
 }
-cudaError_t launch_outer(const Outer &p, cudaStream_t s) {
-    outer_kernel<<<dim3((p.NB + 31) / 32, (p.NA + 7) / 8, p.E), dim3(32, 8), 0, s>>>(p);
-    return cudaGetLastError();
+
+// ---------------------------------------------------------------------------
+// Expand on the tensor cores: 128 sorted rows times TN columns of out, RB bytes of each
+// row.  A block keeps one row tile's v (its three pieces) and takes every G-th tile of the
+// columns.  base's rows come by row copies into shared memory, the sums are added there
+// and the rows leave the same way: thread = row, so that nothing but the sums is waited
+// for.  base and W are asked for before the grid that writes v has ended.
+//
+// Roles: warps 0 .. 3 the rows, warp 4 loads W by TMA, warp 5 issues the MMAs, warps 6
+// and 7 copy base to out for tokens of no adapter.
+// ---------------------------------------------------------------------------
+constexpr int E_THREADS = 256;
+
+template <int ELEM_, int RB_, bool MN_>
+struct ExpandCfg {
+    static constexpr int ELEM = ELEM_, RB = RB_;
+    static constexpr bool MN = MN_;
+    static constexpr int TN = RB / ELEM;
+    static constexpr int BOXES = RB == 512 ? 1 : 2;          // 64-wide boxes of r
+    static constexpr int V_BYTES = BOXES * 16384;            // a piece
+    static constexpr int W_BYTES = BOXES * TN * 128;
+    static constexpr int PITCH = RB + 16;                    // (spreads the rows over the banks)
+    static constexpr int OFF_W = 3 * V_BYTES;
+    static constexpr int OFF_ROWS = OFF_W + W_BYTES;
+    static constexpr int OFF_BAR = OFF_ROWS + 2 * 128 * PITCH;
+    static constexpr int SMEM = 1024 + OFF_BAR + 8 * 8 + 8;
+    static constexpr int TMEM_COLS = 2 * TN;
+};
+
+template <class C>
+__global__ void __launch_bounds__(E_THREADS, 1) expand_kernel(const __grid_constant__ CUtensorMap w, const Params p, const float *v, const void *base,
+                                                              void *out, int G) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint64_t *w_full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
+    uint64_t *w_empty = w_full + 1, *t_full = w_full + 2, *t_empty = w_full + 4, *b_full = w_full + 6;
+    int *info = reinterpret_cast<int *>(w_full + 8);         // abort, TMEM base
+    volatile int *abort_flag = info;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
+    const int r16 = up16(p.r);
+    if (tid == 0) {
+        info[0] = 0;
+        mbar_init(w_full, 1);
+        mbar_init(w_empty, 1);
+        for (int i = 0; i < 2; ++i) { mbar_init(&t_full[i], 1); mbar_init(&t_empty[i], 4); mbar_init(&b_full[i], 128); }
+        fence_mbarrier_init();
+    }
+    if (warp == 4 && lane == 0) prefetch_tensormap(&w);
+    if (warp == 5) {
+        tmem_alloc(reinterpret_cast<uint32_t *>(info + 1), C::TMEM_COLS);
+        tmem_relinquish();
+        tc_fence_before();
+    }
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(info + 1);
+    // (what the grid before this one does not write may be read before its end: it let this
+    // one start after the grids before it had ended)
+    GroupWalk<128, 1> wk;
+    wk.start(p.offsets, p.T, p.L, 1, p.each, false, blockIdx.x / G);
+    const bool have = wk.get();
+    const int n_tiles = (p.C + C::TN - 1) / C::TN, g = blockIdx.x % G;
+    const int64_t pitch = (int64_t)p.C * C::ELEM;
+
+    // warps 0 .. 3: this thread's row
+    int t = -1;
+    if (have && warp < 4 && tid < wk.rows) t = __ldcg(p.row_slot + wk.row0 + tid);
+    if ((unsigned)t >= (unsigned)p.T) t = -1;
+    const uint8_t *from = static_cast<const uint8_t *>(base) + t * pitch;
+    uint8_t *to = static_cast<uint8_t *>(out) + t * pitch;
+    uint8_t *rows = smem + C::OFF_ROWS + tid * C::PITCH;
+    auto bytes_of = [&](int nt) { return (uint32_t)min((int64_t)C::RB, pitch - (int64_t)nt * C::RB); };
+    auto ask = [&](int nt, int b) {    // base's part of tile nt into buffer b
+        if (!base) return;
+        if (t >= 0) {
+            mbar_arrive_expect_tx(&b_full[b], bytes_of(nt));
+            row_load(smem_u32(rows) + b * 128 * C::PITCH, from + (int64_t)nt * C::RB, bytes_of(nt), &b_full[b]);
+        } else {
+            mbar_arrive(&b_full[b]);
+        }
+    };
+    auto load_w = [&](int nt) {
+        if constexpr (C::MN) {
+            mbar_arrive_expect_tx(w_full, C::TN / 64 * r16 * 128);
+            for (int b = 0; b < C::TN / 64; ++b) tma_load_3d(smem + C::OFF_W + b * r16 * 128, &w, w_full, nt * C::TN + b * 64, 0, wk.e);
+        } else {
+            const int boxes = (p.r + 63) / 64;
+            mbar_arrive_expect_tx(w_full, boxes * C::TN * 128);
+            for (int b = 0; b < boxes; ++b) tma_load_3d(smem + C::OFF_W + b * C::TN * 128, &w, w_full, b * 64, nt * C::TN, wk.e);
+        }
+    };
+    const bool any = have && g < n_tiles;
+    if (any && warp < 4) {
+        ask(g, 0);
+        if (g + G < n_tiles) ask(g + G, 1);
+    } else if (any && warp == 4 && lane == 0) {
+        load_w(g);
+    }
+    grid_wait();
+    grid_launch_dependents();
+    if (any) {
+        // v's pieces, K-major; zeros past r and past the tile's rows
+        const int quads = r16 / 4;
+        for (int i = tid; i < 128 * quads; i += E_THREADS) {
+            const int row = i / quads, c = (i - row * quads) * 4;
+            float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (row < wk.rows && c < p.r) f = __ldcg(reinterpret_cast<const float4 *>(v + (int64_t)(wk.row0 + row) * p.r + c));
+            uint32_t a[4][3];
+            pieces(f.x, a[0]); pieces(f.y, a[1]); pieces(f.z, a[2]); pieces(f.w, a[3]);
+            const uint32_t at = (c >> 6) * 16384 + row * 128 + ((((c & 63) >> 3) ^ (row & 7)) << 4) + (c & 4) * 2;
+#pragma unroll
+            for (int k = 0; k < 3; ++k)
+                *reinterpret_cast<uint2 *>(smem + k * C::V_BYTES + at) = make_uint2(high_halves(a[0][k], a[1][k]), high_halves(a[2][k], a[3][k]));
+        }
+        fence_proxy_async_smem();
+    }
+    __syncthreads();
+
+    if (any && warp < 4) {
+        int i = 0;
+        bool ok = true;
+        for (int nt = g; nt < n_tiles; nt += G, ++i) {
+            const int b = i & 1;
+            if (i > 0) {
+                // the tile before has left its buffer: the next but one's base goes there
+                bulk_wait_group_read<0>();
+                if (nt + G < n_tiles) ask(nt + G, b ^ 1);
+            }
+            ok = __all_sync(0xffffffffu, bar_wait(&t_full[b], (i >> 1) & 1, abort_flag, p.err) &&
+                                             (!base || bar_wait(&b_full[b], (i >> 1) & 1, abort_flag, p.err)));
+            if (!ok) break;
+            tc_fence_after();
+            uint8_t *mine = rows + b * 128 * C::PITCH;
+            const uint32_t acc = tmem + b * C::TN + ((uint32_t)(warp * 32) << 16);
+            const int cols = bytes_of(nt) / C::ELEM;
+#pragma unroll
+            for (int c = 0; c < C::TN; c += 32) {
+                if (c >= cols) break;
+                uint32_t d[32];
+                tmem_ld_32x32b_x32(acc + c, d);
+                tmem_ld_wait(d);
+                if (t < 0) continue;
+#pragma unroll
+                for (int j = 0; j < 32; j += 16 / C::ELEM) {
+                    if (c + j >= cols) break;
+                    uint4 *at = reinterpret_cast<uint4 *>(mine + (c + j) * C::ELEM);
+                    uint4 f = base ? *at : make_uint4(0, 0, 0, 0);
+                    if constexpr (C::ELEM == 2) {
+                        auto add = [&](uint32_t two, int k) {
+                            const __nv_bfloat162 s = __floats2bfloat162_rn(lo_f32(two) + __uint_as_float(d[j + k]), hi_f32(two) + __uint_as_float(d[j + k + 1]));
+                            return *reinterpret_cast<const uint32_t *>(&s);
+                        };
+                        *at = make_uint4(add(f.x, 0), add(f.y, 2), add(f.z, 4), add(f.w, 6));
+                    } else {
+                        auto add = [&](uint32_t one, int k) { return __float_as_uint(__uint_as_float(one) + __uint_as_float(d[j + k])); };
+                        *at = make_uint4(add(f.x, 0), add(f.y, 1), add(f.z, 2), add(f.w, 3));
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&t_empty[b]);
+            if (t >= 0) {
+                fence_proxy_async_smem();
+                row_store(to + (int64_t)nt * C::RB, smem_u32(mine), bytes_of(nt));
+            }
+            bulk_commit_group();
+        }
+        if (!ok && base)               // (a launch that gave up: no copy is left on its way)
+            for (int k = i; k < i + 2; ++k)
+                if (g + k * G < n_tiles) mbar_wait(&b_full[k & 1], (k >> 1) & 1, nullptr, p.err);
+        bulk_wait_group_all();
+    } else if (any && warp == 4) {
+        if (lane == 0) {
+            int i = 1;
+            for (int nt = g + G; nt < n_tiles; nt += G, ++i) {
+                if (!bar_wait(w_empty, (i - 1) & 1, abort_flag, p.err)) break;
+                load_w(nt);
+            }
+            if (*abort_flag) mbar_wait(w_full, (i - 1) & 1, nullptr, p.err);
+        }
+        __syncwarp();
+    } else if (any && warp == 5) {
+        const uint32_t idesc = idesc_bf16_f32(128, C::TN, false, C::MN), sv = smem_u32(smem), sw = sv + C::OFF_W;
+        int i = 0;
+        bool ok = true;
+        for (int nt = g; ok && nt < n_tiles; nt += G, ++i) {
+            const int b = i & 1;
+            ok = __all_sync(0xffffffffu, bar_wait(w_full, i & 1, abort_flag, p.err) &&
+                                             (i < 2 || bar_wait(&t_empty[b], ((i >> 1) & 1) ^ 1, abort_flag, p.err)));
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+                for (int k = 0; k < r16 / 16; ++k) {
+                    const uint64_t wd = C::MN ? smem_desc_mn_sw128(sw, r16 * 128) + k * k_step(true)
+                                              : smem_desc_k_sw128(sw + (k >> 2) * C::TN * 128) + (k & 3) * k_step(false);
+#pragma unroll
+                    for (int q = 0; q < 3; ++q)
+                        tc_mma_bf16(tmem + b * C::TN, smem_desc_k_sw128(sv + q * C::V_BYTES + (k >> 2) * 16384) + (k & 3) * k_step(false), wd, idesc,
+                                    (k | q) != 0);
+                }
+                tc_commit(w_empty);
+                tc_commit(&t_full[b]);
+            }
+            __syncwarp();
+        }
+        // (nothing issued is left on its way: the rows' warps have waited for it, or gave up)
+        if (*abort_flag) {
+            if (i > 0) mbar_wait(w_empty, (i - 1) & 1, nullptr, p.err);
+            __syncwarp();
+        }
+    } else if (warp >= 6 && out != base) {
+        // tokens of no adapter keep base
+        for (int q = blockIdx.x; q < p.T; q += gridDim.x) {
+            if ((unsigned)__ldcg(p.slot_row + q) < (unsigned)p.T) continue;
+            const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(base) + q * pitch);
+            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(out) + q * pitch);
+            for (int64_t c = tid - 192; c < pitch / 16; c += 64) dst[c] = base ? __ldcg(src + c) : make_uint4(0, 0, 0, 0);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 5) {
+        tc_fence_after();
+        tmem_dealloc(tmem, C::TMEM_COLS);
+    }
 }
 
-}  // namespace
+// ---------------------------------------------------------------------------
+// Outer products on the tensor cores: a tile is 128 columns of x (on the MMA's M side, as
+// they lie in memory) times r, summed over an adapter's rows, 64 a stage.  Persistent;
+// two accumulators, so that one is taken out while the next tile's MMAs run.
+//
+// Roles: warps 0 .. 7 gather x's rows and split v into its pieces, warp 8 issues the MMAs,
+// warps 12 .. 15 take a tile out (32 columns of x each).
+// ---------------------------------------------------------------------------
+constexpr int O_THREADS = 512, O_LAG = 2;
 
-cudaError_t launch_lora_shrink(const LoraPlan &p, const void *x, const void *w, bool transposed, float *v, int C, cudaStream_t s) {
-    return launch_rows({x, w, nullptr, v, p.offsets, p.row_slot, nullptr, nullptr, p.scale, true, false, p.T, p.r, C, p.L,
-                        transposed ? 1 : C, transposed ? p.r : 1}, s);
+template <int BOXES_>
+struct OuterCfg {
+    static constexpr int BOXES = BOXES_;                     // 64-wide boxes of r
+    static constexpr int V_BYTES = BOXES * 8192;             // a piece
+    static constexpr int STAGE = 16384 + 3 * V_BYTES;
+    static constexpr int NS = BOXES == 1 ? 5 : 3;
+    static constexpr int TMEM_COLS = BOXES * 128;            // two accumulators
+    static constexpr int PER = BOXES * 4;                    // float4 of v a thread and stage, at most
+    static constexpr int OFF_BAR = NS * STAGE;
+    static constexpr int SMEM = 1024 + OFF_BAR + (2 * NS + 4) * 8 + 8;
+};
+
+template <class C>
+__global__ void __launch_bounds__(O_THREADS, 1) outer_kernel(const Params p, const float *v, const __nv_bfloat16 *x, void *d, int n_tiles,
+                                                             int transposed, int d_bf16) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint64_t *s_full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
+    uint64_t *s_empty = s_full + C::NS, *t_full = s_empty + C::NS, *t_empty = t_full + 2;
+    int *info = reinterpret_cast<int *>(t_empty + 2);        // abort, TMEM base
+    volatile int *abort_flag = info;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
+    const int r16 = up16(p.r);
+    if (tid == 0) {
+        info[0] = 0;
+        for (int i = 0; i < C::NS; ++i) { mbar_init(&s_full[i], 8); mbar_init(&s_empty[i], 1); }
+        for (int i = 0; i < 2; ++i) { mbar_init(&t_full[i], 1); mbar_init(&t_empty[i], 4); }
+        fence_mbarrier_init();
+    }
+    if (warp == 8) {
+        tmem_alloc(reinterpret_cast<uint32_t *>(info + 1), C::TMEM_COLS);
+        tmem_relinquish();
+        tc_fence_before();
+    }
+    __syncthreads();
+    grid_wait();
+    grid_launch_dependents();          // (this block has its tensor memory)
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(info + 1);
+    GroupWalk<128, 1, true> wk;
+    if (warp < 9 || warp >= 12) wk.start(p.offsets, p.T, p.L, n_tiles, p.each, false, blockIdx.x);
+    auto stages = [&] { return (wk.rows + KB - 1) / KB; };
+
+    if (warp < 8) {
+        // ---- gather x: thread = one 16-byte column of rows tid / 16 + 16 j; split v: float4s
+        const int chunk = tid & 15, first = tid >> 4;
+        const uint32_t dst = smem_u32(smem) + (chunk >> 3) * 8192 + first * 128 + (((chunk & 7) ^ (first & 7)) << 4);
+        const int quads = r16 / 4;
+        uint32_t it = 0, sent = 0;
+        bool ok = true;
+        auto filled = [&] {            // this thread's copies of the oldest stage have arrived
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s_full[sent % C::NS]);
+            ++sent;
+        };
+        for (; ok && wk.get(); wk.t += gridDim.x) {
+            const int ns = stages(), col = wk.nt * 128 + chunk * 8;
+            for (int i = 0; i < ns; ++i, ++it) {
+                const int s = it % C::NS, valid = min(KB, wk.rows - i * KB);
+                const int row0 = wk.row0 + i * KB;
+                int tok[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) tok[j] = first + 16 * j < valid ? __ldcg(p.row_slot + row0 + first + 16 * j) : -1;
+                float4 f[C::PER];
+                bool named[C::PER];
+#pragma unroll
+                for (int j = 0; j < C::PER; ++j) {
+                    const int q = tid + 256 * j, row = q / quads, c = (q - row * quads) * 4;
+                    f[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    named[j] = false;
+                    if (row < valid && c < p.r) {
+                        f[j] = __ldcg(reinterpret_cast<const float4 *>(v + (int64_t)(row0 + row) * p.r + c));
+                        named[j] = (unsigned)__ldcg(p.row_slot + row0 + row) < (unsigned)p.T;
+                    }
+                }
+                if (it >= (uint32_t)C::NS) ok = __all_sync(0xffffffffu, bar_wait(&s_empty[s], ((it / C::NS) & 1) ^ 1, abort_flag, p.err));
+                if (!ok) break;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const bool there = (unsigned)tok[j] < (unsigned)p.T && col < p.C;
+                    copy16(dst + s * C::STAGE + j * 2048, there ? x + (int64_t)tok[j] * p.C + col : x, there);
+                }
+                copy_commit();
+                uint8_t *sv = smem + s * C::STAGE + 16384;
+#pragma unroll
+                for (int j = 0; j < C::PER; ++j) {
+                    const int q = tid + 256 * j, row = q / quads, c = (q - row * quads) * 4;
+                    if (row >= KB) continue;
+                    if (!named[j]) f[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    uint32_t a[4][3];
+                    pieces(f[j].x, a[0]); pieces(f[j].y, a[1]); pieces(f[j].z, a[2]); pieces(f[j].w, a[3]);
+                    const uint32_t at = (c >> 6) * 8192 + row * 128 + ((((c & 63) >> 3) ^ (row & 7)) << 4) + (c & 4) * 2;
+#pragma unroll
+                    for (int k = 0; k < 3; ++k)
+                        *reinterpret_cast<uint2 *>(sv + k * C::V_BYTES + at) = make_uint2(high_halves(a[0][k], a[1][k]), high_halves(a[2][k], a[3][k]));
+                }
+                if (it - sent >= (uint32_t)O_LAG) {
+                    copy_wait<O_LAG>();
+                    filled();
+                }
+            }
+        }
+        copy_wait<0>();
+        if (ok)
+            while (sent != it) filled();
+    } else if (warp == 8) {
+        // ---- MMA issuer
+        const uint32_t idesc = idesc_bf16_f32(128, r16, true, true);
+        uint32_t it = 0, acc = 0;
+        bool ok = true;
+        for (; ok && wk.get(); wk.t += gridDim.x) {
+            const int ns = stages();
+            if (ns == 0) continue;
+            const uint32_t b = acc & 1, dst = tmem + b * (C::TMEM_COLS / 2);
+            ok = acc < 2 || bar_wait(&t_empty[b], ((acc >> 1) & 1) ^ 1, abort_flag, p.err);
+            for (int i = 0; i < ns; ++i, ++it) {
+                const uint32_t s = it % C::NS;
+                ok = ok && bar_wait(&s_full[s], (it / C::NS) & 1, abort_flag, p.err);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                tc_fence_after();
+                const uint32_t sx = smem_u32(smem) + s * C::STAGE, sv = sx + 16384;
+                const int n = (min(KB, wk.rows - i * KB) + 15) / 16;
+                if (elect_one()) {
+                    for (int k = 0; k < n; ++k) {
+                        const uint64_t xd = smem_desc_mn_sw128(sx, 8192) + k * k_step(true);
+#pragma unroll
+                        for (int q = 0; q < 3; ++q)
+                            tc_mma_bf16(dst, xd, smem_desc_mn_sw128(sv + q * C::V_BYTES, 8192) + k * k_step(true), idesc, (i | k | q) != 0);
+                    }
+                    tc_commit(&s_empty[s]);
+                    if (i == ns - 1) tc_commit(&t_full[b]);
+                }
+                __syncwarp();
+            }
+            ++acc;
+            ok = __all_sync(0xffffffffu, ok && !*abort_flag);
+        }
+        // (what was issued is waited for by the warps that take it out; a launch that gave up
+        // waits here, on a barrier that nothing else arrives on any more)
+        if (!ok && it > 0) {
+            if (lane == 0) mbar_wait(&s_empty[(it - 1) % C::NS], ((it - 1) / C::NS) & 1, nullptr, p.err);
+            __syncwarp();
+        }
+    } else if (warp >= 12) {
+        // ---- take out and write: thread = one column of x
+        const uint32_t from = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        uint32_t acc = 0;
+        for (bool ok = true; ok && wk.get(); wk.t += gridDim.x) {
+            const bool some = wk.rows > 0;
+            const uint32_t b = acc & 1;
+            if (some) {
+                ok = __all_sync(0xffffffffu, bar_wait(&t_full[b], (acc >> 1) & 1, abort_flag, p.err));
+                if (!ok) break;
+                tc_fence_after();
+                ++acc;
+            }
+            const int c = wk.nt * 128 + (warp & 3) * 32 + lane;
+            for (int j0 = 0; j0 < p.r; j0 += 16) {
+                uint32_t w[16];
+                if (some) {
+                    tmem_ld_32x32b_x16(from + b * (C::TMEM_COLS / 2) + j0, w);
+                    tmem_ld_wait(w);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) w[j] = 0;
+                }
+                if (c >= p.C) continue;
+                if (transposed) {      // d [L][C][r]
+                    const int64_t at = ((int64_t)wk.e * p.C + c) * p.r + j0;
+#pragma unroll
+                    for (int j = 0; j < 16; j += 8) {
+                        if (j0 + j >= p.r) break;
+                        if (d_bf16) {
+                            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(d) + at + j) =
+                                make_uint4(bf16x2(w[j], w[j + 1]), bf16x2(w[j + 2], w[j + 3]), bf16x2(w[j + 4], w[j + 5]), bf16x2(w[j + 6], w[j + 7]));
+                        } else {
+                            *reinterpret_cast<uint4 *>(static_cast<float *>(d) + at + j) = make_uint4(w[j], w[j + 1], w[j + 2], w[j + 3]);
+                            *reinterpret_cast<uint4 *>(static_cast<float *>(d) + at + j + 4) = make_uint4(w[j + 4], w[j + 5], w[j + 6], w[j + 7]);
+                        }
+                    }
+                } else {               // d [L][r][C]
+                    const int64_t at = ((int64_t)wk.e * p.r + j0) * p.C + c;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        if (j0 + j >= p.r) break;
+                        if (d_bf16) static_cast<__nv_bfloat16 *>(d)[at + (int64_t)j * p.C] = __float2bfloat16_rn(__uint_as_float(w[j]));
+                        else static_cast<float *>(d)[at + (int64_t)j * p.C] = __uint_as_float(w[j]);
+                    }
+                }
+            }
+            if (some) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&t_empty[b]);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 8) {
+        tc_fence_after();
+        tmem_dealloc(tmem, C::TMEM_COLS);
+    }
 }
-cudaError_t launch_lora_expand(const LoraPlan &p, const float *v, const void *w, bool transposed, int dtype, const void *base, void *out,
-                               int C, cudaStream_t s) {
-    return launch_rows({v, w, base, out, p.offsets, nullptr, p.row_slot, p.slot_row, nullptr, false, dtype == ZFFN_DT_BF16, p.T, C, p.r, p.L,
-                        transposed ? 1 : p.r, transposed ? C : 1}, s);
+
+// ---------------------------------------------------------------------------
+// Few tokens (decoding requests): one block for a token's row and some rows of W, sums in
+// fp32 by the ordinary units.
+// ---------------------------------------------------------------------------
+
+// The group of `row`: the last offset up to the first one above it; L: none, -1: before
+// the first.  The whole block; `sh`: a word of shared memory.
+__device__ __forceinline__ int group_of(const int32_t *offsets, int L, int T, int row, int *sh) {
+    if (threadIdx.x == 0) *sh = L + 1;
+    __syncthreads();
+    int first = L + 1;
+    for (int g = threadIdx.x; g <= L; g += blockDim.x)
+        if (__ldcg(offsets + g) > row) {
+            first = g;
+            break;
+        }
+    first = __reduce_min_sync(0xffffffffu, first);
+    if ((threadIdx.x & 31) == 0 && first <= L) atomicMin(sh, first);
+    __syncthreads();
+    return *sh - 1;
 }
-cudaError_t launch_lora_outer(const LoraPlan &p, const float *v, const void *x, bool transposed, int dtype, void *d, int C, cudaStream_t s) {
-    if (transposed) return launch_outer({x, v, d, p.offsets, p.row_slot, nullptr, true, false, dtype == ZFFN_DT_BF16, p.T, C, p.r, p.L}, s);
-    return launch_outer({v, x, d, p.offsets, nullptr, p.row_slot, false, true, dtype == ZFFN_DT_BF16, p.T, p.r, C, p.L}, s);
+
+__device__ __forceinline__ float dot8(uint4 a, uint4 b, float s) {
+    s = fmaf(lo_f32(a.x), lo_f32(b.x), s); s = fmaf(hi_f32(a.x), hi_f32(b.x), s);
+    s = fmaf(lo_f32(a.y), lo_f32(b.y), s); s = fmaf(hi_f32(a.y), hi_f32(b.y), s);
+    s = fmaf(lo_f32(a.z), lo_f32(b.z), s); s = fmaf(hi_f32(a.z), hi_f32(b.z), s);
+    s = fmaf(lo_f32(a.w), lo_f32(b.w), s); s = fmaf(hi_f32(a.w), hi_f32(b.w), s);
+    return s;
+}
+
+// A warp for one value of v: blocks (row, 8 of r).
+__global__ void __launch_bounds__(256) shrink_row_kernel(const Params p, const __nv_bfloat16 *x, const __nv_bfloat16 *w, float *v) {
+    __shared__ int sh;
+    grid_wait();
+    grid_launch_dependents();
+    const int row = blockIdx.x, j = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const int t = __ldcg(p.row_slot + row);
+    const int e = group_of(p.offsets, p.L, p.T, row, &sh);
+    if (e < 0) return;
+    float sum = 0.0f;
+    if (e < p.L && (unsigned)t < (unsigned)p.T) {
+        const uint4 *a = reinterpret_cast<const uint4 *>(x + (int64_t)t * p.C);
+        const uint4 *b = reinterpret_cast<const uint4 *>(w + ((int64_t)e * p.r + j) * p.C);
+        const int n = p.C / 8;
+        float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        int c = lane;
+        for (; c + 7 * 32 < n; c += 8 * 32) {
+            uint4 fa[8], fb[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) { fb[i] = __ldcg(b + c + i * 32); fa[i] = __ldcg(a + c + i * 32); }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s[i & 3] = dot8(fa[i], fb[i], s[i & 3]);
+        }
+        for (; c < n; c += 32) s[0] = dot8(__ldcg(a + c), __ldcg(b + c), s[0]);
+        sum = (s[0] + s[1]) + (s[2] + s[3]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (p.scale) sum *= __ldcg(p.scale + e);
+    }
+    if (lane == 0) v[(int64_t)row * p.r + j] = sum;
+}
+
+// Two columns of out a thread: blocks (token, 256 columns).  W's rows are asked for before
+// the grid that writes v has ended.
+template <typename O>
+__global__ void __launch_bounds__(128) expand_row_kernel(const Params p, const float *v, const __nv_bfloat16 *w, const O *base, O *out) {
+    __shared__ int sh;
+    __shared__ float vs[128];
+    const int t = blockIdx.x, n = blockIdx.y * 256 + threadIdx.x * 2, row = __ldcg(p.slot_row + t);
+    const bool some = (unsigned)row < (unsigned)p.T;
+    const int e = some ? group_of(p.offsets, p.L, p.T, row, &sh) : p.L;
+    const bool there = n < p.C;        // (C is a multiple of 8)
+    const int64_t at = (int64_t)t * p.C + n;
+    float a = 0.0f, b = 0.0f;
+    if (there && base) { a = static_cast<float>(base[at]); b = static_cast<float>(base[at + 1]); }
+    constexpr int AHEAD = 4;
+    const uint4 *w0 = reinterpret_cast<const uint4 *>(w + ((int64_t)e * p.C + n) * p.r), *w1 = w0 + p.r / 8;
+    const bool mine = there && e >= 0 && e < p.L;
+    uint4 f[2][AHEAD];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i)
+        if (mine && i * 8 < p.r) { f[0][i] = __ldcg(w0 + i); f[1][i] = __ldcg(w1 + i); }
+    grid_wait();
+    grid_launch_dependents();
+    if (e >= 0 && e < p.L) {
+        for (int i = threadIdx.x; i < p.r; i += 128) vs[i] = __ldcg(v + (int64_t)row * p.r + i);
+        __syncthreads();
+    }
+    if (mine) {
+        auto dot = [&](uint4 q, int c, float s) {
+            const float4 lo = *reinterpret_cast<const float4 *>(vs + c), hi = *reinterpret_cast<const float4 *>(vs + c + 4);
+            s = fmaf(lo_f32(q.x), lo.x, s); s = fmaf(hi_f32(q.x), lo.y, s); s = fmaf(lo_f32(q.y), lo.z, s); s = fmaf(hi_f32(q.y), lo.w, s);
+            s = fmaf(lo_f32(q.z), hi.x, s); s = fmaf(hi_f32(q.z), hi.y, s); s = fmaf(lo_f32(q.w), hi.z, s); s = fmaf(hi_f32(q.w), hi.w, s);
+            return s;
+        };
+        float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i)
+            if (i * 8 < p.r) { s0 = dot(f[0][i], i * 8, s0); s1 = dot(f[1][i], i * 8, s1); }
+        for (int i = AHEAD; i * 8 < p.r; ++i) { s0 = dot(__ldcg(w0 + i), i * 8, s0); s1 = dot(__ldcg(w1 + i), i * 8, s1); }
+        a += s0;
+        b += s1;
+    }
+    if (there && (mine || out != base)) {
+        if constexpr (sizeof(O) == 2) *reinterpret_cast<__nv_bfloat162 *>(out + at) = __floats2bfloat162_rn(a, b);
+        else *reinterpret_cast<float2 *>(out + at) = make_float2(a, b);
+    }
+}
+
+// ---- host -------------------------------------------------------------------
+
+static Params params(const LoraPlan &q, int C) { return Params{q.row_slot, q.slot_row, q.offsets, q.scale, q.err, q.T, q.r, q.L, C, FastDiv(1)}; }
+// Row tiles of 128 rows, at most, with those of the rows of none.
+static int64_t row_tiles(const LoraPlan &q) { return q.T / 128 + (q.L + 1 < q.T ? q.L + 1 : q.T); }
+// Few tokens: by the row kernels.
+static bool few(const LoraPlan &q) { return (int64_t)q.T * q.r <= 2048; }
+
+template <bool MN>
+static cudaError_t shrink(const LoraPlan &q, const void *x, const void *w, float *v, int C, cudaStream_t s) {
+    CUtensorMap map;
+    if (!(MN ? encode(&map, w, 2, q.r, C, q.L, KB, true) : encode(&map, w, 2, C, q.r, q.L, q.r, true))) return cudaErrorInvalidValue;
+    const DeviceInfo &di = device_info();
+    // few tiles: the contraction over as many blocks as run at once, two stages each at least
+    const int64_t tiles = row_tiles(q);
+    const int blocks = (C + KB - 1) / KB;
+    int split = S_MAX_SPLIT;
+    while (split > 1 && (tiles * split > di.num_sms * (s_smem(q.r, MN, split) <= 113 * 1024 ? 2 : 1) || blocks < 2 * split)) split /= 2;
+    const size_t smem = s_smem(q.r, MN, split);
+    const cudaError_t e = ensure_dynamic_smem((const void *)shrink_kernel<MN>, smem);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(shrink_kernel<MN>, dim3((unsigned)(tiles * split)), S_THREADS, smem, (unsigned)split, s, map, params(q, C),
+                            static_cast<const __nv_bfloat16 *>(x), v);
+}
+
+template <int ELEM, int RB, bool MN>
+static cudaError_t expand(const LoraPlan &q, const float *v, const void *w, const void *base, void *out, int C, cudaStream_t s) {
+    using Cfg = ExpandCfg<ELEM, RB, MN>;
+    CUtensorMap map;
+    if (!(MN ? encode(&map, w, 2, C, q.r, q.L, up16(q.r), true) : encode(&map, w, 2, q.r, C, q.L, Cfg::TN, true))) return cudaErrorInvalidValue;
+    const int64_t tiles = row_tiles(q), sms = device_info().num_sms, n_tiles = (C + Cfg::TN - 1) / Cfg::TN;
+    int64_t G = (sms + tiles - 1) / tiles;
+    if (G > n_tiles) G = n_tiles;
+    const cudaError_t e = ensure_dynamic_smem((const void *)expand_kernel<Cfg>, Cfg::SMEM);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(expand_kernel<Cfg>, dim3((unsigned)(tiles * G)), E_THREADS, Cfg::SMEM, 1, s, map, params(q, C), v, base, out, (int)G);
+}
+template <int ELEM>
+static cudaError_t expand(const LoraPlan &q, const float *v, const void *w, bool mn, const void *base, void *out, int C, cudaStream_t s) {
+    if (q.r <= 64) return mn ? expand<ELEM, 512, true>(q, v, w, base, out, C, s) : expand<ELEM, 512, false>(q, v, w, base, out, C, s);
+    return mn ? expand<ELEM, 256, true>(q, v, w, base, out, C, s) : expand<ELEM, 256, false>(q, v, w, base, out, C, s);
+}
+
+template <int BOXES>
+static cudaError_t outer(const LoraPlan &q, const float *v, const void *x, bool transposed, int dtype, void *d, int C, cudaStream_t s) {
+    using Cfg = OuterCfg<BOXES>;
+    const int n_tiles = (C + 127) / 128;
+    const int64_t tiles = (int64_t)q.L * n_tiles, sms = device_info().num_sms;
+    Params p = params(q, C);
+    p.each = GroupWalk<128, 1, true>::divisor(n_tiles);
+    const cudaError_t e = ensure_dynamic_smem((const void *)outer_kernel<Cfg>, Cfg::SMEM);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(outer_kernel<Cfg>, dim3((unsigned)(tiles < sms ? tiles : sms)), O_THREADS, Cfg::SMEM, 1, s, p, v,
+                            static_cast<const __nv_bfloat16 *>(x), d, n_tiles, (int)transposed, (int)(dtype == ZFFN_DT_BF16));
+}
+
+}  // namespace lora
+
+cudaError_t launch_lora_shrink(const LoraPlan &q, const void *x, const void *w, bool transposed, float *v, int C, cudaStream_t s) {
+    using namespace lora;
+    if (!encode_fn()) return cudaErrorNotSupported;
+    if (transposed) return shrink<true>(q, x, w, v, C, s);
+    if (few(q))
+        return launch_dependent(shrink_row_kernel, dim3((unsigned)q.T, (unsigned)(q.r / 8)), 256, 0, 1, s, params(q, C),
+                                static_cast<const __nv_bfloat16 *>(x), static_cast<const __nv_bfloat16 *>(w), v);
+    return shrink<false>(q, x, w, v, C, s);
+}
+
+cudaError_t launch_lora_expand(const LoraPlan &q, const float *v, const void *w, bool transposed, int dtype, const void *base, void *out, int C,
+                               cudaStream_t s) {
+    using namespace lora;
+    if (!encode_fn()) return cudaErrorNotSupported;
+    if (few(q) && !transposed) {
+        const dim3 grid((unsigned)q.T, (unsigned)((C + 255) / 256));
+        const __nv_bfloat16 *w16 = static_cast<const __nv_bfloat16 *>(w);
+        if (dtype == ZFFN_DT_BF16)
+            return launch_dependent(expand_row_kernel<__nv_bfloat16>, grid, 128, 0, 1, s, params(q, C), v, w16, static_cast<const __nv_bfloat16 *>(base),
+                                    static_cast<__nv_bfloat16 *>(out));
+        return launch_dependent(expand_row_kernel<float>, grid, 128, 0, 1, s, params(q, C), v, w16, static_cast<const float *>(base), static_cast<float *>(out));
+    }
+    return dtype == ZFFN_DT_BF16 ? expand<2>(q, v, w, transposed, base, out, C, s) : expand<4>(q, v, w, transposed, base, out, C, s);
+}
+
+cudaError_t launch_lora_outer(const LoraPlan &q, const float *v, const void *x, bool transposed, int dtype, void *d, int C, cudaStream_t s) {
+    using namespace lora;
+    return q.r <= 64 ? outer<1>(q, v, x, transposed, dtype, d, C, s) : outer<2>(q, v, x, transposed, dtype, d, C, s);
 }
 
 }  // namespace zffn

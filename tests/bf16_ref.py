@@ -60,7 +60,9 @@ def cuts(M, E, kind, seed=0):
 
 
 def groups(offsets, M):
-    return [(0, M)] if offsets is None else list(zip(offsets[:-1].tolist(), offsets[1:].tolist()))
+    """(group, first row, past its last) of the groups that have rows."""
+    at = [(0, M)] if offsets is None else zip(offsets[:-1].tolist(), offsets[1:].tolist())
+    return [(e, lo, hi) for e, (lo, hi) in enumerate(at) if lo < hi]
 
 
 def product(a, w, offsets, transposed):
@@ -69,7 +71,7 @@ def product(a, w, offsets, transposed):
     N = w.shape[2] if transposed else w.shape[1]
     y = torch.zeros((a.shape[0], N), dtype=torch.float64, device=a.device)
     mag = torch.zeros_like(y)
-    for e, (lo, hi) in enumerate(groups(offsets, a.shape[0])):
+    for e, lo, hi in groups(offsets, a.shape[0]):
         x, v = a[lo:hi].double(), (w[e] if transposed else w[e].T).double()
         y[lo:hi], mag[lo:hi] = x @ v, x.abs() @ v.abs()
     return y, mag
@@ -77,10 +79,10 @@ def product(a, w, offsets, transposed):
 
 def grad_w(dy, a, offsets):
     """(dw, tolerance of fp32 sums), [E, N, K]."""
-    at = groups(offsets, a.shape[0])
-    dw = torch.zeros((len(at), dy.shape[1], a.shape[1]), dtype=torch.float64, device=a.device)
+    E = 1 if offsets is None else offsets.numel() - 1
+    dw = torch.zeros((E, dy.shape[1], a.shape[1]), dtype=torch.float64, device=a.device)
     tol = torch.zeros_like(dw)
-    for e, (lo, hi) in enumerate(at):
+    for e, lo, hi in groups(offsets, a.shape[0]):
         d, x = dy[lo:hi].double().T, a[lo:hi].double()
         dw[e], tol[e] = d @ x, sum_bound(hi - lo) * (d.abs() @ x.abs())
     return dw, tol
@@ -93,7 +95,7 @@ def lora(x, A, B, plan, scale, base):
     tol = sum_bound(0) * out.abs()
     v = torch.zeros((T, r), dtype=torch.float64, device=x.device)
     vtol = torch.zeros_like(v)
-    for e, (lo, hi) in enumerate(groups(plan.offsets, T)):
+    for e, lo, hi in groups(plan.offsets, T):
         t = plan.row_slot[lo:hi].long()
         s = 1.0 if scale is None else float(scale[e])
         a, b = A[e].double().T, B[e].double().T
@@ -109,7 +111,7 @@ def lora_grad(dy, x, v, A, B, plan, scale, base):
     dx, dx_tol, dv, dv_tol = lora(dy, B.transpose(1, 2), A.transpose(1, 2), plan, scale, base)
     dA, dB = torch.zeros(A.shape, dtype=torch.float64, device=x.device), torch.zeros(B.shape, dtype=torch.float64, device=x.device)
     A_tol, B_tol = torch.zeros_like(dA), torch.zeros_like(dB)
-    for e, (lo, hi) in enumerate(groups(plan.offsets, x.shape[0])):
+    for e, lo, hi in groups(plan.offsets, x.shape[0]):
         t = plan.row_slot[lo:hi].long()
         xe, de, d, d_tol, ve = x[t].double(), dy[t].double(), dv[lo:hi], dv_tol[lo:hi], v[lo:hi].double()
         c = sum_bound(3 * (hi - lo))

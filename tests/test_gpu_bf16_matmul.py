@@ -9,6 +9,7 @@ from tests import bf16_ref as ref
 pytestmark = pytest.mark.gpu
 
 DTYPES = [torch.bfloat16, torch.float32]
+KINDS = ["random", "one", "none", "unused", "borders"]
 
 
 def run_product(M, N, K, E, kind, transposed, dtype, seed=0):
@@ -50,7 +51,7 @@ GROUPED = [(1, 64, 64, 1), (8, 768, 256, 128), (37, 136, 1032, 5), (256, 264, 72
 
 
 @pytest.mark.parametrize("transposed", [False, True])
-@pytest.mark.parametrize("kind", ["random", "one", "none", "unused", "borders"])
+@pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("M,N,K,E", GROUPED)
 def test_grouped(M, N, K, E, kind, transposed):
     for dtype in DTYPES:
@@ -62,11 +63,8 @@ GRADS = [(1, 8, 8, 0), (1, 264, 136, 0), (37, 136, 264, 0), (700, 392, 1032, 0),
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("kind", ["random", "one", "none", "unused", "borders"])
-@pytest.mark.parametrize("M,N,K,E", GRADS)
+@pytest.mark.parametrize("M,N,K,E,kind", [(*g, k) for g in GRADS for k in (KINDS if g[3] else [None])])
 def test_weights_gradient(M, N, K, E, kind, dtype):
-    if not E and kind != "random":
-        pytest.skip("dense: no offsets")
     gen = ref.generator(M + N + K + E)
     dy, a = ref.randn(gen, M, N, scale=0.1), ref.randn(gen, M, K)
     offsets = ref.cuts(M, E, kind) if E else None
