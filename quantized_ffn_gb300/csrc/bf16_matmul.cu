@@ -379,7 +379,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
 #pragma unroll
                         for (int k = 0; k < LOADS; ++k) {
                             const int c = (lane + 32 * k) * elem;
-#pragma unroll 8
+#pragma unroll 4
                             for (int r = 0; r < 32; ++r) {
                                 const uint8_t *src = at(r, c >> 4) + (c & 15);
                                 if (r >= left || c >= bytes) continue;
@@ -574,7 +574,7 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) small_kernel(const __gr
                 last_row0 = wk.row0; last_rows = wk.rows; last_nt = wk.nt;
             }
             const uint32_t to = smem_u32(part + rank * slice * 128) + tid * 4;
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < C::TN; c += CH) {
                 if (c >= wk.rows) break;
                 uint32_t d[CH];

@@ -28,15 +28,6 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool some)
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-// A row's bytes (a multiple of 16) by the copy engine, and back.
-__device__ __forceinline__ void row_load(uint32_t dst, const void *src, uint32_t bytes, uint64_t *bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src), "r"(bytes),
-                 "r"(smem_u32(bar))
-                 : "memory");
-}
-__device__ __forceinline__ void row_store(void *dst, uint32_t src, uint32_t bytes) {
-    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
-}
 __device__ __forceinline__ float lo_f32(uint32_t two) { return __uint_as_float(two << 16); }
 __device__ __forceinline__ float hi_f32(uint32_t two) { return __uint_as_float(two & 0xFFFF0000u); }
 // v = p[0] + p[1] + p[2], bf16 values in the high halves: v's bits cut after 8 and 16
@@ -59,48 +50,51 @@ struct Params {
     const float *scale;
     int *err;
     int T, r, L, C;
-    FastDiv each;
+    FastDiv each, by_quads;   // of the walk; by the float4s of a row of v, up to 16 values
 };
 
 // ---------------------------------------------------------------------------
-// Shrink on the tensor cores: 128 rows (gathered, on the MMA's M side) times all r rows
-// of W.  The blocks of a cluster share the contraction; rows 128 / split * i and on are
-// added up by rank i, in rank order.
+// Shrink on the tensor cores: 128 rows (on the MMA's M side) times all r rows of W.  The
+// blocks of a cluster share the contraction; rows 128 / split * i and on are added up by
+// rank i, in rank order.  A tile whose tokens follow one another (a packed sequence) is
+// loaded by TMA, another gathered by 16-byte copies.  (The copy engine's own gather takes
+// four rows of 128 bytes at a time, and about 100 clocks for it.)
 //
-// Roles: warps 0 .. 3 gather x's rows, then take the sums out; warp 4 loads W by TMA,
-// warp 5 issues the MMAs.
+// Roles: warps 0 .. 3 gather x's rows, then take the sums out; warp 4 loads W, and x's
+// rows where they follow one another, warp 5 issues the MMAs.
 // ---------------------------------------------------------------------------
-constexpr int S_NS = 4, S_LAG = 2, S_THREADS = 192, S_MAX_SPLIT = 8;
+constexpr int S_NS = 4, S_LAG = 3, S_THREADS = 192, S_MAX_SPLIT = 8;
 
 // W's bytes of a stage: K-major [r][64], or MN-major boxes [64][64]
 __host__ __device__ constexpr int s_w_bytes(int r, bool mn) { return mn ? (r + 63) / 64 * 8192 : up16(r) * 128; }
-static size_t s_smem(int r, bool mn, int split) {
-    return 1024 + (size_t)S_NS * (16384 + s_w_bytes(r, mn)) + (split > 1 ? 128 * r * 4 : 0) + (2 * S_NS + 1) * 8 + 8;
-}
+static size_t s_smem(int r, bool mn) { return 1024 + (size_t)S_NS * (16384 + s_w_bytes(r, mn)) + (2 * S_NS + 1) * 8 + 8; }
 
 template <bool MN>
-__global__ void __launch_bounds__(S_THREADS) shrink_kernel(const __grid_constant__ CUtensorMap w, const Params p, const __nv_bfloat16 *x, float *v) {
+__global__ void __launch_bounds__(S_THREADS) shrink_kernel(const __grid_constant__ CUtensorMap xm, const __grid_constant__ CUtensorMap w, const Params p,
+                                                           const __nv_bfloat16 *x, float *v) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint32_t split;
     asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(split));
     const uint32_t rank = cluster_ctarank();
     const int wb = s_w_bytes(p.r, MN), stage = 16384 + wb;
-    float *part = reinterpret_cast<float *>(smem + S_NS * stage);
-    uint64_t *s_full = reinterpret_cast<uint64_t *>(smem + S_NS * stage + (split > 1 ? 128 * p.r * 4 : 0));
+    float *part = reinterpret_cast<float *>(smem);           // sums [rank][row / split][r], once the stages are idle
+    uint64_t *s_full = reinterpret_cast<uint64_t *>(smem + S_NS * stage);
     uint64_t *s_empty = s_full + S_NS, *t_full = s_empty + S_NS;
     int *info = reinterpret_cast<int *>(t_full + 1);         // abort, TMEM base
     volatile int *abort_flag = info;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
     const int r16 = up16(p.r), cols = r16 <= 32 ? 32 : r16 <= 64 ? 64 : 128;
-    if (split > 1) cluster_arrive();                         // (waited for before another's memory is written)
     if (tid == 0) {
         info[0] = 0;
         for (int i = 0; i < S_NS; ++i) { mbar_init(&s_full[i], 5); mbar_init(&s_empty[i], 1); }
         mbar_init(t_full, 1);
         fence_mbarrier_init();
     }
-    if (warp == 4 && lane == 0) prefetch_tensormap(&w);
+    if (warp == 4 && lane == 0) {
+        prefetch_tensormap(&xm);
+        prefetch_tensormap(&w);
+    }
     if (warp == 5) {
         tmem_alloc(reinterpret_cast<uint32_t *>(info + 1), cols);
         tmem_relinquish();
@@ -118,59 +112,77 @@ __global__ void __launch_bounds__(S_THREADS) shrink_kernel(const __grid_constant
     const int kb0 = blocks * rank / split, nkb = blocks * (rank + 1) / split - kb0;
     const float scale = some && p.scale ? __ldcg(p.scale + wk.e) : 1.0f;
 
+    // the tile's tokens, 4 lane + j, and whether they follow one another
+    int tok[4];
+    bool packed = true;
+    if (some && warp < 5) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) tok[j] = lane * 4 + j < wk.rows ? __ldcg(p.row_slot + wk.row0 + lane * 4 + j) : -1;
+        const int t0 = __shfl_sync(0xffffffffu, tok[0], 0);
+        for (int j = 0; j < 4; ++j) packed = packed && (lane * 4 + j >= wk.rows || tok[j] == t0 + lane * 4 + j);
+        packed = __all_sync(0xffffffffu, packed) && t0 >= 0 && t0 + wk.rows <= p.T;
+    }
+
     if (some && warp < 4) {
         // ---- gather: thread = one 16-byte column of rows tid / 8 + 16 i
-        const int chunk = tid & 7, first = tid >> 3;
-        const uint32_t dst = smem_u32(smem) + first * 128 + ((chunk ^ (first & 7)) << 4);
-        const __nv_bfloat16 *src[8];
+        if (!packed) {
+            const int chunk = tid & 7, first = tid >> 3;
+            const uint32_t dst = smem_u32(smem) + first * 128 + ((chunk ^ (first & 7)) << 4);
+            const __nv_bfloat16 *src[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int row = first + 16 * i, t = row < wk.rows ? __ldcg(p.row_slot + wk.row0 + row) : -1;
-            src[i] = (unsigned)t < (unsigned)p.T ? x + (int64_t)t * p.C + chunk * 8 : nullptr;
-        }
-        bool ok = true;
-        auto filled = [&](int i) {     // this thread's copies of stage i have arrived
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&s_full[i % S_NS]);
-        };
-        for (int i = 0; i < nkb; ++i) {
-            const int s = i % S_NS, c = (kb0 + i) * KB;
-            if (i >= S_NS) ok = __all_sync(0xffffffffu, bar_wait(&s_empty[s], ((i / S_NS) & 1) ^ 1, abort_flag, p.err));
-            if (!ok) break;
+            for (int i = 0; i < 8; ++i) {
+                const int row = first + 16 * i, t = row < wk.rows ? __ldcg(p.row_slot + wk.row0 + row) : -1;
+                src[i] = (unsigned)t < (unsigned)p.T ? x + (int64_t)t * p.C + chunk * 8 : nullptr;
+            }
+            bool ok = true;
+            auto filled = [&](int i) {     // this thread's copies of stage i have arrived
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s_full[i % S_NS]);
+            };
+            for (int i = 0; i < nkb; ++i) {
+                const int s = i % S_NS, c = (kb0 + i) * KB;
+                if (i >= S_NS) ok = __all_sync(0xffffffffu, bar_wait(&s_empty[s], ((i / S_NS) & 1) ^ 1, abort_flag, p.err));
+                if (!ok) break;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const bool there = src[j] && c + chunk * 8 < p.C;
-                copy16(dst + s * stage + j * 2048, there ? src[j] + c : x, there);
-            }
-            copy_commit();
-            if (i >= S_LAG) {
-                copy_wait<S_LAG>();
-                filled(i - S_LAG);
-            }
-        }
-        copy_wait<0>();
-        if (ok)
-            for (int i = nkb > S_LAG ? nkb - S_LAG : 0; i < nkb; ++i) filled(i);
-    } else if (some && warp == 4) {
-        // ---- W by TMA
-        if (lane == 0) {
-            int i = 0;
-            for (; i < nkb; ++i) {
-                const int s = i % S_NS;
-                if (i >= S_NS && !bar_wait(&s_empty[s], ((i / S_NS) & 1) ^ 1, abort_flag, p.err)) break;
-                uint8_t *to = smem + s * stage + 16384;
-                if constexpr (MN) {
-                    mbar_arrive_expect_tx(&s_full[s], wb);
-                    for (int b = 0; b * 64 < p.r; ++b) tma_load_3d(to + b * 8192, &w, &s_full[s], b * 64, (kb0 + i) * KB, wk.e);
-                } else {
-                    mbar_arrive_expect_tx(&s_full[s], p.r * 128);
-                    tma_load_3d(to, &w, &s_full[s], (kb0 + i) * KB, 0, wk.e);
+                for (int j = 0; j < 8; ++j) {
+                    const bool there = src[j] && c + chunk * 8 < p.C;
+                    copy16(dst + s * stage + j * 2048, there ? src[j] + c : x, there);
+                }
+                copy_commit();
+                if (i >= S_LAG) {
+                    copy_wait<S_LAG>();
+                    filled(i - S_LAG);
                 }
             }
-            if (*abort_flag)           // wait for the copies in flight before the block leaves
-                for (int j = i > S_NS ? i - S_NS : 0; j < i; ++j) mbar_wait(&s_full[j % S_NS], (j / S_NS) & 1, nullptr, p.err);
+            copy_wait<0>();
+            if (ok)
+                for (int i = nkb > S_LAG ? nkb - S_LAG : 0; i < nkb; ++i) filled(i);
         }
+    } else if (some && warp == 4) {
+        // ---- by TMA: W, and a packed tile's rows (past the adapter's last: rows that nothing takes)
+        const int t0 = __shfl_sync(0xffffffffu, tok[0], 0);
+        int i = 0;
+        for (bool ok = true; i < nkb; ++i) {
+            const int s = i % S_NS;
+            if (i >= S_NS) ok = __all_sync(0xffffffffu, bar_wait(&s_empty[s], ((i / S_NS) & 1) ^ 1, abort_flag, p.err));
+            if (!ok) break;
+            uint8_t *to = smem + s * stage;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&s_full[s], (packed ? 16384 : 0) + (MN ? wb : p.r * 128));
+                if (packed) tma_load_2d(to, &xm, &s_full[s], (kb0 + i) * KB, t0);
+                if constexpr (MN) {
+                    for (int b = 0; b * 64 < p.r; ++b) tma_load_3d(to + 16384 + b * 8192, &w, &s_full[s], b * 64, (kb0 + i) * KB, wk.e);
+                } else {
+                    tma_load_3d(to + 16384, &w, &s_full[s], (kb0 + i) * KB, 0, wk.e);
+                }
+            } else if (packed && lane < 5) {
+                mbar_arrive(&s_full[s]);   // (for the gathering warps)
+            }
+            __syncwarp();
+        }
+        if (lane == 0 && *abort_flag)  // wait for the copies in flight before the block leaves
+            for (int j = i > S_NS ? i - S_NS : 0; j < i; ++j) mbar_wait(&s_full[j % S_NS], (j / S_NS) & 1, nullptr, p.err);
         __syncwarp();
     } else if (some && warp == 5) {
         // ---- MMA issuer
@@ -207,7 +219,7 @@ __global__ void __launch_bounds__(S_THREADS) shrink_kernel(const __grid_constant
             __syncwarp();
             tc_fence_after();
         }
-        if (split > 1) cluster_wait();                       // every block of the cluster runs
+        if (split > 1) cluster_sync_all();                   // every block's stages are idle
         const uint32_t from = tmem + ((uint32_t)(warp * 32) << 16);
         const int per = 128 / split, row = tid;
         float *to = v + (int64_t)(wk.row0 + row) * p.r;
@@ -235,7 +247,7 @@ __global__ void __launch_bounds__(S_THREADS) shrink_kernel(const __grid_constant
         }
         tc_fence_before();
     } else if (split > 1) {
-        cluster_wait();
+        cluster_sync_all();
     }
     __syncthreads();
     if (split > 1) {
@@ -262,41 +274,42 @@ __global__ void __launch_bounds__(S_THREADS) shrink_kernel(const __grid_constant
 }
 
 // ---------------------------------------------------------------------------
-// Expand on the tensor cores: 128 sorted rows times TN columns of out, RB bytes of each
-// row.  A block keeps one row tile's v (its three pieces) and takes every G-th tile of the
-// columns.  base's rows come by row copies into shared memory, the sums are added there
-// and the rows leave the same way: thread = row, so that nothing but the sums is waited
-// for.  base and W are asked for before the grid that writes v has ended.
+// Expand on the tensor cores: 128 sorted rows times TN columns of out.  A block keeps one
+// row tile's v (its three pieces) and takes every G-th tile of the columns.  The sums go
+// through shared memory, so that a warp adds a row's base and writes it with its lanes
+// side by side; base is asked for a tile ahead, and it and W before the grid that writes v
+// has ended.
 //
-// Roles: warps 0 .. 3 the rows, warp 4 loads W by TMA, warp 5 issues the MMAs, warps 6
-// and 7 copy base to out for tokens of no adapter.
+// Roles: warps 0 .. 7 the rows (16 each), warp 8 loads W by TMA and issues the MMAs, warps 9
+// .. 11 copy base to out for tokens of no adapter.  (With 16 warps of 8 rows a thread has 96
+// registers: what it spilled went through L2, beside 213 KB of shared memory, and 2048 x 11008
+// took 39 us instead of EXPAND_US.)
 // ---------------------------------------------------------------------------
-constexpr int E_THREADS = 256;
+constexpr int E_WARPS = 8, E_THREADS = (E_WARPS + 4) * 32;
 
-template <int ELEM_, int RB_, bool MN_>
+template <int ELEM_, int TN_, int BOXES_, bool MN_>
 struct ExpandCfg {
-    static constexpr int ELEM = ELEM_, RB = RB_;
+    static constexpr int ELEM = ELEM_, TN = TN_, BOXES = BOXES_;   // BOXES: 64-wide boxes of r
     static constexpr bool MN = MN_;
-    static constexpr int TN = RB / ELEM;
-    static constexpr int BOXES = RB == 512 ? 1 : 2;          // 64-wide boxes of r
     static constexpr int V_BYTES = BOXES * 16384;            // a piece
     static constexpr int W_BYTES = BOXES * TN * 128;
-    static constexpr int PITCH = RB + 16;                    // (spreads the rows over the banks)
+    static constexpr int PITCH = TN + 4;                     // floats (spreads the rows over the banks)
     static constexpr int OFF_W = 3 * V_BYTES;
-    static constexpr int OFF_ROWS = OFF_W + W_BYTES;
-    static constexpr int OFF_BAR = OFF_ROWS + 2 * 128 * PITCH;
-    static constexpr int SMEM = 1024 + OFF_BAR + 8 * 8 + 8;
+    static constexpr int OFF_SUMS = OFF_W + W_BYTES;
+    static constexpr int OFF_BAR = OFF_SUMS + 128 * PITCH * 4;
+    static constexpr int SMEM = 1024 + OFF_BAR + 6 * 8 + 8;
     static constexpr int TMEM_COLS = 2 * TN;
 };
 
 template <class C>
 __global__ void __launch_bounds__(E_THREADS, 1) expand_kernel(const __grid_constant__ CUtensorMap w, const Params p, const float *v, const void *base,
-                                                              void *out, int G) {
+                                                              void *out, int sms, int G) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    float *sums = reinterpret_cast<float *>(smem + C::OFF_SUMS);
     uint64_t *w_full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
-    uint64_t *w_empty = w_full + 1, *t_full = w_full + 2, *t_empty = w_full + 4, *b_full = w_full + 6;
-    int *info = reinterpret_cast<int *>(w_full + 8);         // abort, TMEM base
+    uint64_t *w_empty = w_full + 1, *t_full = w_full + 2, *t_empty = w_full + 4;
+    int *info = reinterpret_cast<int *>(w_full + 6);         // abort, TMEM base
     volatile int *abort_flag = info;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
     const int r16 = up16(p.r);
@@ -304,11 +317,11 @@ __global__ void __launch_bounds__(E_THREADS, 1) expand_kernel(const __grid_const
         info[0] = 0;
         mbar_init(w_full, 1);
         mbar_init(w_empty, 1);
-        for (int i = 0; i < 2; ++i) { mbar_init(&t_full[i], 1); mbar_init(&t_empty[i], 4); mbar_init(&b_full[i], 128); }
+        for (int i = 0; i < 2; ++i) { mbar_init(&t_full[i], 1); mbar_init(&t_empty[i], E_WARPS); }
         fence_mbarrier_init();
     }
-    if (warp == 4 && lane == 0) prefetch_tensormap(&w);
-    if (warp == 5) {
+    if (warp == E_WARPS && lane == 0) prefetch_tensormap(&w);
+    if (warp == E_WARPS) {
         tmem_alloc(reinterpret_cast<uint32_t *>(info + 1), C::TMEM_COLS);
         tmem_relinquish();
         tc_fence_before();
@@ -319,27 +332,30 @@ __global__ void __launch_bounds__(E_THREADS, 1) expand_kernel(const __grid_const
     // (what the grid before this one does not write may be read before its end: it let this
     // one start after the grids before it had ended)
     GroupWalk<128, 1> wk;
-    wk.start(p.offsets, p.T, p.L, 1, p.each, false, blockIdx.x / G);
+    wk.start(p.offsets, p.T, p.L, 1, p.each, false, 0);
+    // (G blocks to a row tile, as many as run at once: of the tiles that there are, where 32
+    // groups hold them all, else of those that there may be)
+    if (p.L <= 32) G = max(1, sms / max(1, __shfl_sync(0xffffffffu, wk.inc, 31)));
+    wk.t = blockIdx.x / G;
     const bool have = wk.get();
     const int n_tiles = (p.C + C::TN - 1) / C::TN, g = blockIdx.x % G;
-    const int64_t pitch = (int64_t)p.C * C::ELEM;
+    const bool any = have && g < n_tiles;
 
-    // warps 0 .. 3: this thread's row
-    int t = -1;
-    if (have && warp < 4 && tid < wk.rows) t = __ldcg(p.row_slot + wk.row0 + tid);
-    if ((unsigned)t >= (unsigned)p.T) t = -1;
-    const uint8_t *from = static_cast<const uint8_t *>(base) + t * pitch;
-    uint8_t *to = static_cast<uint8_t *>(out) + t * pitch;
-    uint8_t *rows = smem + C::OFF_ROWS + tid * C::PITCH;
-    auto bytes_of = [&](int nt) { return (uint32_t)min((int64_t)C::RB, pitch - (int64_t)nt * C::RB); };
-    auto ask = [&](int nt, int b) {    // base's part of tile nt into buffer b
-        if (!base) return;
-        if (t >= 0) {
-            mbar_arrive_expect_tx(&b_full[b], bytes_of(nt));
-            row_load(smem_u32(rows) + b * 128 * C::PITCH, from + (int64_t)nt * C::RB, bytes_of(nt), &b_full[b]);
-        } else {
-            mbar_arrive(&b_full[b]);
-        }
+    // warps 0 .. 7: lane i holds the token of row 16 warp + i; a lane has OWN columns of each
+    // row from OWN lane on
+    constexpr int ROWS = 128 / E_WARPS, OWN = C::TN / 32;
+    using Part = std::conditional_t<OWN * C::ELEM == 8, uint2, uint4>;
+    int token = -1;
+    if (any && warp < E_WARPS && lane < ROWS && warp * ROWS + lane < wk.rows) token = __ldcg(p.row_slot + wk.row0 + warp * ROWS + lane);
+    if ((unsigned)token >= (unsigned)p.T) token = -1;
+    Part old[ROWS];
+    const int64_t pitch = (int64_t)p.C * C::ELEM;
+    const uint8_t *from = static_cast<const uint8_t *>(base) + lane * OWN * C::ELEM;
+    uint8_t *to = static_cast<uint8_t *>(out) + lane * OWN * C::ELEM;
+    auto ask = [&](int i, int nt) {    // base's part of row i in tile nt
+        const int t = __shfl_sync(0xffffffffu, token, i);
+        old[i] = Part{};
+        if (base && t >= 0 && nt * C::TN + lane * OWN < p.C) old[i] = __ldcg(reinterpret_cast<const Part *>(from + t * pitch + nt * (C::TN * C::ELEM)));
     };
     auto load_w = [&](int nt) {
         if constexpr (C::MN) {
@@ -351,11 +367,10 @@ __global__ void __launch_bounds__(E_THREADS, 1) expand_kernel(const __grid_const
             for (int b = 0; b < boxes; ++b) tma_load_3d(smem + C::OFF_W + b * C::TN * 128, &w, w_full, b * 64, nt * C::TN, wk.e);
         }
     };
-    const bool any = have && g < n_tiles;
-    if (any && warp < 4) {
-        ask(g, 0);
-        if (g + G < n_tiles) ask(g + G, 1);
-    } else if (any && warp == 4 && lane == 0) {
+    if (any && warp < E_WARPS) {
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) ask(i, g);
+    } else if (any && warp == E_WARPS && lane == 0) {
         load_w(g);
     }
     grid_wait();
@@ -364,7 +379,7 @@ __global__ void __launch_bounds__(E_THREADS, 1) expand_kernel(const __grid_const
         // v's pieces, K-major; zeros past r and past the tile's rows
         const int quads = r16 / 4;
         for (int i = tid; i < 128 * quads; i += E_THREADS) {
-            const int row = i / quads, c = (i - row * quads) * 4;
+            const int row = p.by_quads.div(i), c = (i - row * quads) * 4;
             float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             if (row < wk.rows && c < p.r) f = __ldcg(reinterpret_cast<const float4 *>(v + (int64_t)(wk.row0 + row) * p.r + c));
             uint32_t a[4][3];
@@ -378,79 +393,101 @@ __global__ void __launch_bounds__(E_THREADS, 1) expand_kernel(const __grid_const
     }
     __syncthreads();
 
-    if (any && warp < 4) {
+    if (any && warp < E_WARPS) {
+        // (a quarter of the warps to 32 rows in tensor memory, SHARE columns each)
+        constexpr int SHARE = C::TN / (E_WARPS / 4);
+        const int quarter = warp & 3, c0 = (warp >> 2) * SHARE;
+        // A lane's 4 or 8 columns are read as one or two float4s: with 8 the first of all lanes
+        // lie before the second ones.
+        auto slot = [](int c) { return OWN == 8 ? (c >> 2 & 1) * (C::TN / 2) + (c >> 3) * 4 : c; };
+        float *mine = sums + (quarter * 32 + lane) * C::PITCH;
         int i = 0;
-        bool ok = true;
         for (int nt = g; nt < n_tiles; nt += G, ++i) {
             const int b = i & 1;
-            if (i > 0) {
-                // the tile before has left its buffer: the next but one's base goes there
-                bulk_wait_group_read<0>();
-                if (nt + G < n_tiles) ask(nt + G, b ^ 1);
-            }
-            ok = __all_sync(0xffffffffu, bar_wait(&t_full[b], (i >> 1) & 1, abort_flag, p.err) &&
-                                             (!base || bar_wait(&b_full[b], (i >> 1) & 1, abort_flag, p.err)));
-            if (!ok) break;
+            // (a warp that gives up still meets the others at the barriers)
+            const bool ok = __all_sync(0xffffffffu, bar_wait(&t_full[b], (i >> 1) & 1, abort_flag, p.err));
             tc_fence_after();
-            uint8_t *mine = rows + b * 128 * C::PITCH;
-            const uint32_t acc = tmem + b * C::TN + ((uint32_t)(warp * 32) << 16);
-            const int cols = bytes_of(nt) / C::ELEM;
+            if (ok) {
+                const uint32_t acc = tmem + b * C::TN + c0 + ((uint32_t)(quarter * 32) << 16);
+#pragma unroll 1
+                for (int c = 0; c < SHARE; c += 32) {
+                    uint32_t d[32];
+                    tmem_ld_32x32b_x32(acc + c, d);
+                    tmem_ld_wait(d);
 #pragma unroll
-            for (int c = 0; c < C::TN; c += 32) {
-                if (c >= cols) break;
-                uint32_t d[32];
-                tmem_ld_32x32b_x32(acc + c, d);
-                tmem_ld_wait(d);
-                if (t < 0) continue;
-#pragma unroll
-                for (int j = 0; j < 32; j += 16 / C::ELEM) {
-                    if (c + j >= cols) break;
-                    uint4 *at = reinterpret_cast<uint4 *>(mine + (c + j) * C::ELEM);
-                    uint4 f = base ? *at : make_uint4(0, 0, 0, 0);
-                    if constexpr (C::ELEM == 2) {
-                        auto add = [&](uint32_t two, int k) {
-                            const __nv_bfloat162 s = __floats2bfloat162_rn(lo_f32(two) + __uint_as_float(d[j + k]), hi_f32(two) + __uint_as_float(d[j + k + 1]));
-                            return *reinterpret_cast<const uint32_t *>(&s);
-                        };
-                        *at = make_uint4(add(f.x, 0), add(f.y, 2), add(f.z, 4), add(f.w, 6));
-                    } else {
-                        auto add = [&](uint32_t one, int k) { return __float_as_uint(__uint_as_float(one) + __uint_as_float(d[j + k])); };
-                        *at = make_uint4(add(f.x, 0), add(f.y, 1), add(f.z, 2), add(f.w, 3));
-                    }
+                    for (int j = 0; j < 32; j += 4) *reinterpret_cast<uint4 *>(mine + slot(c0 + c + j)) = make_uint4(d[j], d[j + 1], d[j + 2], d[j + 3]);
                 }
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&t_empty[b]);
-            if (t >= 0) {
-                fence_proxy_async_smem();
-                row_store(to + (int64_t)nt * C::RB, smem_u32(mine), bytes_of(nt));
+            named_barrier(1, E_WARPS * 32);
+            const bool there = ok && nt * C::TN + lane * OWN < p.C;
+            const bool more = base && (nt + G) * C::TN + lane * OWN < p.C;   // (a lane's part of the next tile)
+            constexpr int TOGETHER = 4;                      // rows whose latencies overlap
+#pragma unroll
+            for (int k0 = 0; k0 < ROWS; k0 += TOGETHER) {
+                float4 f[TOGETHER][OWN / 4];
+                Part n[TOGETHER];
+                int64_t at[TOGETHER];
+#pragma unroll
+                for (int k = 0; k < TOGETHER; ++k) {
+#pragma unroll
+                    for (int h = 0; h < OWN / 4; ++h)
+                        f[k][h] = *reinterpret_cast<const float4 *>(sums + (warp * ROWS + k0 + k) * C::PITCH + h * (C::TN / 2) + lane * 4);
+                    const int t = __shfl_sync(0xffffffffu, token, k0 + k);
+                    at[k] = t < 0 ? -1 : t * pitch + nt * (C::TN * C::ELEM);
+                }
+#pragma unroll
+                for (int k = 0; k < TOGETHER; ++k) {
+                    const Part o = old[k0 + k];
+                    if constexpr (C::ELEM == 2) {
+                        auto add = [](uint32_t two, float a, float b) {
+                            const __nv_bfloat162 s = __floats2bfloat162_rn(lo_f32(two) + a, hi_f32(two) + b);
+                            return *reinterpret_cast<const uint32_t *>(&s);
+                        };
+                        n[k].x = add(o.x, f[k][0].x, f[k][0].y);
+                        n[k].y = add(o.y, f[k][0].z, f[k][0].w);
+                        if constexpr (OWN == 8) {
+                            n[k].z = add(o.z, f[k][1].x, f[k][1].y);
+                            n[k].w = add(o.w, f[k][1].z, f[k][1].w);
+                        }
+                    } else {
+                        n[k] = make_uint4(__float_as_uint(__uint_as_float(o.x) + f[k][0].x), __float_as_uint(__uint_as_float(o.y) + f[k][0].y),
+                                          __float_as_uint(__uint_as_float(o.z) + f[k][0].z), __float_as_uint(__uint_as_float(o.w) + f[k][0].w));
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < TOGETHER; ++k)
+                    if (there && at[k] >= 0) *reinterpret_cast<Part *>(to + at[k]) = n[k];
+                if (more) {
+#pragma unroll
+                    for (int k = 0; k < TOGETHER; ++k) {
+                        old[k0 + k] = Part{};
+                        if (at[k] >= 0) old[k0 + k] = __ldcg(reinterpret_cast<const Part *>(from + at[k] + G * (C::TN * C::ELEM)));
+                    }
+                }
             }
-            bulk_commit_group();
+            named_barrier(1, E_WARPS * 32);
         }
-        if (!ok && base)               // (a launch that gave up: no copy is left on its way)
-            for (int k = i; k < i + 2; ++k)
-                if (g + k * G < n_tiles) mbar_wait(&b_full[k & 1], (k >> 1) & 1, nullptr, p.err);
-        bulk_wait_group_all();
-    } else if (any && warp == 4) {
-        if (lane == 0) {
-            int i = 1;
-            for (int nt = g + G; nt < n_tiles; nt += G, ++i) {
-                if (!bar_wait(w_empty, (i - 1) & 1, abort_flag, p.err)) break;
-                load_w(nt);
-            }
-            if (*abort_flag) mbar_wait(w_full, (i - 1) & 1, nullptr, p.err);
-        }
-        __syncwarp();
-    } else if (any && warp == 5) {
+    } else if (any && warp == E_WARPS) {
         const uint32_t idesc = idesc_bf16_f32(128, C::TN, false, C::MN), sv = smem_u32(smem), sw = sv + C::OFF_W;
         int i = 0;
         bool ok = true;
-        for (int nt = g; ok && nt < n_tiles; nt += G, ++i) {
+        for (int nt = g; nt < n_tiles; nt += G, ++i) {
             const int b = i & 1;
+            if (i > 0) {               // (W's tile before has been read)
+                ok = __all_sync(0xffffffffu, bar_wait(w_empty, (i - 1) & 1, abort_flag, p.err));
+                if (!ok) break;
+                if (lane == 0) load_w(nt);
+                __syncwarp();
+            }
             ok = __all_sync(0xffffffffu, bar_wait(w_full, i & 1, abort_flag, p.err) &&
                                              (i < 2 || bar_wait(&t_empty[b], ((i >> 1) & 1) ^ 1, abort_flag, p.err)));
-            if (!ok) break;
+            if (!ok) {                 // (no copy is left on its way)
+                mbar_wait(w_full, i & 1, nullptr, p.err);
+                break;
+            }
             tc_fence_after();
             if (elect_one()) {
                 for (int k = 0; k < r16 / 16; ++k) {
@@ -466,23 +503,22 @@ __global__ void __launch_bounds__(E_THREADS, 1) expand_kernel(const __grid_const
             }
             __syncwarp();
         }
-        // (nothing issued is left on its way: the rows' warps have waited for it, or gave up)
-        if (*abort_flag) {
-            if (i > 0) mbar_wait(w_empty, (i - 1) & 1, nullptr, p.err);
-            __syncwarp();
-        }
-    } else if (warp >= 6 && out != base) {
+        // (nor is anything issued: the rows' warps have waited for it, or gave up)
+        if (!ok && i > 0) mbar_wait(w_empty, (i - 1) & 1, nullptr, p.err);
+        __syncwarp();
+    } else if (warp > E_WARPS && out != base) {
         // tokens of no adapter keep base
         for (int q = blockIdx.x; q < p.T; q += gridDim.x) {
             if ((unsigned)__ldcg(p.slot_row + q) < (unsigned)p.T) continue;
             const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(base) + q * pitch);
             uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(out) + q * pitch);
-            for (int64_t c = tid - 192; c < pitch / 16; c += 64) dst[c] = base ? __ldcg(src + c) : make_uint4(0, 0, 0, 0);
+#pragma unroll 4
+            for (int64_t c = tid - (E_WARPS + 1) * 32; c < pitch / 16; c += 96) dst[c] = base ? __ldcg(src + c) : make_uint4(0, 0, 0, 0);
         }
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 5) {
+    if (warp == E_WARPS) {
         tc_fence_after();
         tmem_dealloc(tmem, C::TMEM_COLS);
     }
@@ -490,29 +526,32 @@ __global__ void __launch_bounds__(E_THREADS, 1) expand_kernel(const __grid_const
 
 // ---------------------------------------------------------------------------
 // Outer products on the tensor cores: a tile is 128 columns of x (on the MMA's M side, as
-// they lie in memory) times r, summed over an adapter's rows, 64 a stage.  Persistent;
-// two accumulators, so that one is taken out while the next tile's MMAs run.
+// they lie in memory) times v's three pieces side by side (one MMA reads x once for all
+// three: with one for each piece their reads of x were the bound), summed over an adapter's
+// rows, 64 a stage.  Persistent; where tensor memory has room for two accumulators (r up to
+// 80) one is taken out while the next tile's MMAs run.  Rows as in shrink: by TMA where
+// their tokens follow one another.
 //
-// Roles: warps 0 .. 7 gather x's rows and split v into its pieces, warp 8 issues the MMAs,
-// warps 12 .. 15 take a tile out (32 columns of x each).
+// Roles: warps 0 and 1 bring x's rows, warp 2 issues the MMAs, warps 4 .. 11 split v into its
+// pieces, warps 12 .. 15 take a tile out (32 columns of x each).
 // ---------------------------------------------------------------------------
-constexpr int O_THREADS = 512, O_LAG = 2;
+constexpr int O_THREADS = 512;
 
-template <int BOXES_>
+template <bool WIDE_>
 struct OuterCfg {
-    static constexpr int BOXES = BOXES_;                     // 64-wide boxes of r
-    static constexpr int V_BYTES = BOXES * 8192;             // a piece
-    static constexpr int STAGE = 16384 + 3 * V_BYTES;
-    static constexpr int NS = BOXES == 1 ? 5 : 3;
-    static constexpr int TMEM_COLS = BOXES * 128;            // two accumulators
-    static constexpr int PER = BOXES * 4;                    // float4 of v a thread and stage, at most
+    static constexpr bool WIDE = WIDE_;                      // r > 80
+    static constexpr int V_BYTES = (WIDE ? 6 : 4) * 8192;    // 64-wide boxes of the pieces
+    static constexpr int STAGE = 16384 + V_BYTES;
+    static constexpr int NS = WIDE ? 3 : 4, LAG = NS - 1;
+    static constexpr int ACC = WIDE ? 1 : 2, ACC_COLS = 512 / ACC;
+    static constexpr int PER = WIDE ? 8 : 5;                 // float4 of v a thread and stage, at most
     static constexpr int OFF_BAR = NS * STAGE;
     static constexpr int SMEM = 1024 + OFF_BAR + (2 * NS + 4) * 8 + 8;
 };
 
 template <class C>
-__global__ void __launch_bounds__(O_THREADS, 1) outer_kernel(const Params p, const float *v, const __nv_bfloat16 *x, void *d, int n_tiles,
-                                                             int transposed, int d_bf16) {
+__global__ void __launch_bounds__(O_THREADS, 1) outer_kernel(const __grid_constant__ CUtensorMap xm, const Params p, const float *v,
+                                                             const __nv_bfloat16 *x, void *d, int n_tiles, int wide_x, int transposed, int d_bf16) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint64_t *s_full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
@@ -523,12 +562,13 @@ __global__ void __launch_bounds__(O_THREADS, 1) outer_kernel(const Params p, con
     const int r16 = up16(p.r);
     if (tid == 0) {
         info[0] = 0;
-        for (int i = 0; i < C::NS; ++i) { mbar_init(&s_full[i], 8); mbar_init(&s_empty[i], 1); }
+        for (int i = 0; i < C::NS; ++i) { mbar_init(&s_full[i], 10); mbar_init(&s_empty[i], 1); }
         for (int i = 0; i < 2; ++i) { mbar_init(&t_full[i], 1); mbar_init(&t_empty[i], 4); }
         fence_mbarrier_init();
+        prefetch_tensormap(&xm);
     }
-    if (warp == 8) {
-        tmem_alloc(reinterpret_cast<uint32_t *>(info + 1), C::TMEM_COLS);
+    if (warp == 2) {
+        tmem_alloc(reinterpret_cast<uint32_t *>(info + 1), 512);
         tmem_relinquish();
         tc_fence_before();
     }
@@ -538,65 +578,77 @@ __global__ void __launch_bounds__(O_THREADS, 1) outer_kernel(const Params p, con
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(info + 1);
     GroupWalk<128, 1, true> wk;
-    if (warp < 9 || warp >= 12) wk.start(p.offsets, p.T, p.L, n_tiles, p.each, false, blockIdx.x);
+    if (warp != 3) wk.start(p.offsets, p.T, p.L, n_tiles, p.each, false, blockIdx.x);
     auto stages = [&] { return (wk.rows + KB - 1) / KB; };
 
-    if (warp < 8) {
-        // ---- gather x: thread = one 16-byte column of rows tid / 16 + 16 j; split v: float4s
+    if (warp < 2) {
+        // ---- x's rows: by TMA, or thread = one 16-byte column of rows tid / 16 + 4 j
         const int chunk = tid & 15, first = tid >> 4;
-        const uint32_t dst = smem_u32(smem) + (chunk >> 3) * 8192 + first * 128 + (((chunk & 7) ^ (first & 7)) << 4);
-        const int quads = r16 / 4;
-        uint32_t it = 0, sent = 0;
+        const uint32_t dst = smem_u32(smem) + (chunk >> 3) * 8192 + first * 128;
+        const uint32_t even = ((chunk & 7) ^ first) << 4, odd = ((chunk & 7) ^ (first + 4)) << 4;
+        uint32_t it = 0, sent = 0, gathered = 0;             // gathered: a bit for each stage
         bool ok = true;
         auto filled = [&] {            // this thread's copies of the oldest stage have arrived
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&s_full[sent % C::NS]);
+            const uint32_t s = sent % C::NS;
+            if ((gathered >> s) & 1) {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s_full[s]);
+            }
             ++sent;
         };
         for (; ok && wk.get(); wk.t += gridDim.x) {
-            const int ns = stages(), col = wk.nt * 128 + chunk * 8;
-            for (int i = 0; i < ns; ++i, ++it) {
-                const int s = it % C::NS, valid = min(KB, wk.rows - i * KB);
-                const int row0 = wk.row0 + i * KB;
-                int tok[4];
+            const int ns = stages();
+            // tokens of rows lane and 32 + lane of four stages, and of the next four on their way
+            int now[4][2], next[4][2];
+            auto tokens = [&](int i, int (&t)[4][2]) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) tok[j] = first + 16 * j < valid ? __ldcg(p.row_slot + row0 + first + 16 * j) : -1;
-                float4 f[C::PER];
-                bool named[C::PER];
-#pragma unroll
-                for (int j = 0; j < C::PER; ++j) {
-                    const int q = tid + 256 * j, row = q / quads, c = (q - row * quads) * 4;
-                    f[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    named[j] = false;
-                    if (row < valid && c < p.r) {
-                        f[j] = __ldcg(reinterpret_cast<const float4 *>(v + (int64_t)(row0 + row) * p.r + c));
-                        named[j] = (unsigned)__ldcg(p.row_slot + row0 + row) < (unsigned)p.T;
-                    }
+                for (int j = 0; j < 8; ++j) {
+                    const int at = i * KB + j * 32 + lane;
+                    t[j >> 1][j & 1] = at < wk.rows ? __ldcg(p.row_slot + wk.row0 + at) : -1;
                 }
+            };
+            tokens(0, next);
+            for (int i = 0; i < ns; ++i, ++it) {
+                if (i % 4 == 0) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) { now[j][0] = next[j][0]; now[j][1] = next[j][1]; }
+                    if (i + 4 < ns) tokens(i + 4, next);
+                }
+                const int t[2] = {i % 4 < 2 ? i % 4 ? now[1][0] : now[0][0] : i % 4 == 2 ? now[2][0] : now[3][0],
+                                  i % 4 < 2 ? i % 4 ? now[1][1] : now[0][1] : i % 4 == 2 ? now[2][1] : now[3][1]};
+                const uint32_t s = it % C::NS;
                 if (it >= (uint32_t)C::NS) ok = __all_sync(0xffffffffu, bar_wait(&s_empty[s], ((it / C::NS) & 1) ^ 1, abort_flag, p.err));
                 if (!ok) break;
+                const int t0 = __shfl_sync(0xffffffffu, t[0], 0);
+                const bool packed = __all_sync(0xffffffffu, t[0] == t0 + lane && t[1] == t0 + 32 + lane) && t0 >= 0 && t0 + KB <= p.T;
+                if (packed) {
+                    gathered &= ~(1u << s);
+                    if (tid == 0) {
+                        uint8_t *to = smem + s * C::STAGE;
+                        mbar_arrive_expect_tx(&s_full[s], 16384);
+                        if (wide_x) {
+                            tma_load_3d(to, &xm, &s_full[s], 0, t0, wk.nt * 2);
+                        } else {
+                            tma_load_2d(to, &xm, &s_full[s], wk.nt * 128, t0);
+                            tma_load_2d(to + 8192, &xm, &s_full[s], wk.nt * 128 + 64, t0);
+                        }
+                    } else if (tid == 32) {
+                        mbar_arrive(&s_full[s]);
+                    }
+                } else {
+                    gathered |= 1u << s;
+                    const int col = wk.nt * 128 + chunk * 8;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const bool there = (unsigned)tok[j] < (unsigned)p.T && col < p.C;
-                    copy16(dst + s * C::STAGE + j * 2048, there ? x + (int64_t)tok[j] * p.C + col : x, there);
+                    for (int j = 0; j < 16; ++j) {
+                        const int tok = __shfl_sync(0xffffffffu, t[j >> 3], (first + 4 * j) & 31);
+                        const bool there = (unsigned)tok < (unsigned)p.T && col < p.C;
+                        copy16(dst + s * C::STAGE + j * 512 + (j & 1 ? odd : even), there ? x + (int64_t)tok * p.C + col : x, there);
+                    }
                 }
                 copy_commit();
-                uint8_t *sv = smem + s * C::STAGE + 16384;
-#pragma unroll
-                for (int j = 0; j < C::PER; ++j) {
-                    const int q = tid + 256 * j, row = q / quads, c = (q - row * quads) * 4;
-                    if (row >= KB) continue;
-                    if (!named[j]) f[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    uint32_t a[4][3];
-                    pieces(f[j].x, a[0]); pieces(f[j].y, a[1]); pieces(f[j].z, a[2]); pieces(f[j].w, a[3]);
-                    const uint32_t at = (c >> 6) * 8192 + row * 128 + ((((c & 63) >> 3) ^ (row & 7)) << 4) + (c & 4) * 2;
-#pragma unroll
-                    for (int k = 0; k < 3; ++k)
-                        *reinterpret_cast<uint2 *>(sv + k * C::V_BYTES + at) = make_uint2(high_halves(a[0][k], a[1][k]), high_halves(a[2][k], a[3][k]));
-                }
-                if (it - sent >= (uint32_t)O_LAG) {
-                    copy_wait<O_LAG>();
+                if (it - sent >= (uint32_t)C::LAG) {
+                    copy_wait<C::LAG>();
                     filled();
                 }
             }
@@ -604,16 +656,90 @@ __global__ void __launch_bounds__(O_THREADS, 1) outer_kernel(const Params p, con
         copy_wait<0>();
         if (ok)
             while (sent != it) filled();
-    } else if (warp == 8) {
-        // ---- MMA issuer
-        const uint32_t idesc = idesc_bf16_f32(128, r16, true, true);
+        // (a launch that gave up: the copies in flight are waited for, as long as the bound lasts)
+        if (tid == 0 && *abort_flag)
+            for (uint32_t j = it > (uint32_t)C::NS ? it - C::NS : 0; j < it; ++j)
+                mbar_wait(&s_full[j % C::NS], (j / C::NS) & 1, nullptr, p.err);
+        __syncwarp();
+    } else if (warp >= 4 && warp < 12) {
+        // ---- v's pieces side by side, MN-major; zeros past r, past the group's rows and for rows of no token
+        // (a thread has the same r16 / 16 places of every stage)
+        const int per = r16 / 16;
+        int row[C::PER], from[C::PER];                       // row of the stage; place in v from the stage's first row, -1: past r
+        uint32_t at[C::PER][3];                              // where each piece goes
+#pragma unroll
+        for (int j = 0; j < C::PER; ++j) {
+            const int q = tid - 128 + 256 * j;
+            row[j] = p.by_quads.div(q);
+            const int c = (q - row[j] * (r16 / 4)) * 4;
+            from[j] = c < p.r ? row[j] * p.r + c : -1;
+#pragma unroll
+            for (int k = 0; k < 3; ++k) {
+                const int n = k * r16 + c;
+                at[j][k] = smem_u32(smem) + 16384 + (n >> 6) * 8192 + row[j] * 128 + ((((n & 63) >> 3) ^ (row[j] & 7)) << 4) + (n & 4) * 2;
+            }
+        }
+        uint32_t it = 0;
+        bool ok = true;
+        for (; ok && wk.get(); wk.t += gridDim.x) {
+            const int ns = stages();
+            // (two stages' values on their way)
+            float4 f[2][C::PER];
+            int tok[2][C::PER];
+            auto ask = [&](int i, float4 (&f)[C::PER], int (&tok)[C::PER]) {
+                const float *src = v + (int64_t)(wk.row0 + i * KB) * p.r;
+                const int32_t *slot = p.row_slot + wk.row0 + i * KB;
+#pragma unroll
+                for (int j = 0; j < C::PER; ++j) {
+                    f[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    tok[j] = -1;
+                    if (j >= per) break;
+                    if (row[j] < wk.rows - i * KB && from[j] >= 0) {
+                        tok[j] = __ldcg(slot + row[j]);
+                        f[j] = __ldcg(reinterpret_cast<const float4 *>(src + from[j]));
+                    }
+                }
+            };
+            auto stage = [&](int i, float4 (&f)[C::PER], int (&tok)[C::PER]) {
+                const int s = it % C::NS;
+                if (it >= (uint32_t)C::NS) ok = __all_sync(0xffffffffu, bar_wait(&s_empty[s], ((it / C::NS) & 1) ^ 1, abort_flag, p.err));
+                if (!ok) return;
+#pragma unroll
+                for (int j = 0; j < C::PER; ++j) {
+                    if (j >= per) break;
+                    if ((unsigned)tok[j] >= (unsigned)p.T) f[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    uint32_t a[4][3];
+                    pieces(f[j].x, a[0]); pieces(f[j].y, a[1]); pieces(f[j].z, a[2]); pieces(f[j].w, a[3]);
+#pragma unroll
+                    for (int k = 0; k < 3; ++k)
+                        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at[j][k] + s * C::STAGE), "r"(high_halves(a[0][k], a[1][k])),
+                                     "r"(high_halves(a[2][k], a[3][k]))
+                                     : "memory");
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s_full[s]);
+                if (i + 2 < ns) ask(i + 2, f, tok);          // (after the fence, which waits for loads before it)
+                ++it;
+            };
+            if (ns > 0) ask(0, f[0], tok[0]);
+            if (ns > 1) ask(1, f[1], tok[1]);
+            for (int i = 0; ok && i < ns; i += 2) {
+                stage(i, f[0], tok[0]);
+                if (ok && i + 1 < ns) stage(i + 1, f[1], tok[1]);
+            }
+        }
+    } else if (warp == 2) {
+        // ---- MMA issuer: columns 0 .. 255 of the pieces, and those past them
+        const int cols = 3 * r16, low = cols < 256 ? cols : 256;
+        const uint32_t idesc = idesc_bf16_f32(128, low, true, true), idesc_high = idesc_bf16_f32(128, C::WIDE ? cols - 256 : 16, true, true);
         uint32_t it = 0, acc = 0;
         bool ok = true;
         for (; ok && wk.get(); wk.t += gridDim.x) {
             const int ns = stages();
             if (ns == 0) continue;
-            const uint32_t b = acc & 1, dst = tmem + b * (C::TMEM_COLS / 2);
-            ok = acc < 2 || bar_wait(&t_empty[b], ((acc >> 1) & 1) ^ 1, abort_flag, p.err);
+            const uint32_t b = acc % C::ACC, dst = tmem + b * C::ACC_COLS;
+            ok = acc < (uint32_t)C::ACC || bar_wait(&t_empty[b], ((acc / C::ACC) & 1) ^ 1, abort_flag, p.err);
             for (int i = 0; i < ns; ++i, ++it) {
                 const uint32_t s = it % C::NS;
                 ok = ok && bar_wait(&s_full[s], (it / C::NS) & 1, abort_flag, p.err);
@@ -621,12 +747,11 @@ __global__ void __launch_bounds__(O_THREADS, 1) outer_kernel(const Params p, con
                 tc_fence_after();
                 const uint32_t sx = smem_u32(smem) + s * C::STAGE, sv = sx + 16384;
                 const int n = (min(KB, wk.rows - i * KB) + 15) / 16;
+                const uint64_t xd = smem_desc_mn_sw128(sx, 8192), vd = smem_desc_mn_sw128(sv, 8192), vh = smem_desc_mn_sw128(sv + 4 * 8192, 8192);
                 if (elect_one()) {
                     for (int k = 0; k < n; ++k) {
-                        const uint64_t xd = smem_desc_mn_sw128(sx, 8192) + k * k_step(true);
-#pragma unroll
-                        for (int q = 0; q < 3; ++q)
-                            tc_mma_bf16(dst, xd, smem_desc_mn_sw128(sv + q * C::V_BYTES, 8192) + k * k_step(true), idesc, (i | k | q) != 0);
+                        tc_mma_bf16(dst, xd + k * k_step(true), vd + k * k_step(true), idesc, (i | k) != 0);
+                        if constexpr (C::WIDE) tc_mma_bf16(dst + 256, xd + k * k_step(true), vh + k * k_step(true), idesc_high, (i | k) != 0);
                     }
                     tc_commit(&s_empty[s]);
                     if (i == ns - 1) tc_commit(&t_full[b]);
@@ -643,14 +768,14 @@ __global__ void __launch_bounds__(O_THREADS, 1) outer_kernel(const Params p, con
             __syncwarp();
         }
     } else if (warp >= 12) {
-        // ---- take out and write: thread = one column of x
+        // ---- take out, add the three pieces' sums, write: thread = one column of x
         const uint32_t from = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         uint32_t acc = 0;
         for (bool ok = true; ok && wk.get(); wk.t += gridDim.x) {
             const bool some = wk.rows > 0;
-            const uint32_t b = acc & 1;
+            const uint32_t b = acc % C::ACC;
             if (some) {
-                ok = __all_sync(0xffffffffu, bar_wait(&t_full[b], (acc >> 1) & 1, abort_flag, p.err));
+                ok = __all_sync(0xffffffffu, bar_wait(&t_full[b], (acc / C::ACC) & 1, abort_flag, p.err));
                 if (!ok) break;
                 tc_fence_after();
                 ++acc;
@@ -659,8 +784,15 @@ __global__ void __launch_bounds__(O_THREADS, 1) outer_kernel(const Params p, con
             for (int j0 = 0; j0 < p.r; j0 += 16) {
                 uint32_t w[16];
                 if (some) {
-                    tmem_ld_32x32b_x16(from + b * (C::TMEM_COLS / 2) + j0, w);
+                    uint32_t w1[16], w2[16];
+                    tmem_ld_32x32b_x16(from + b * C::ACC_COLS + j0, w);
+                    tmem_ld_32x32b_x16(from + b * C::ACC_COLS + r16 + j0, w1);
+                    tmem_ld_32x32b_x16(from + b * C::ACC_COLS + 2 * r16 + j0, w2);
                     tmem_ld_wait(w);
+                    tmem_ld_wait(w1);
+                    tmem_ld_wait(w2);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) w[j] = __float_as_uint(__uint_as_float(w[j]) + (__uint_as_float(w1[j]) + __uint_as_float(w2[j])));
                 } else {
 #pragma unroll
                     for (int j = 0; j < 16; ++j) w[j] = 0;
@@ -698,9 +830,9 @@ __global__ void __launch_bounds__(O_THREADS, 1) outer_kernel(const Params p, con
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 8) {
+    if (warp == 2) {
         tc_fence_after();
-        tmem_dealloc(tmem, C::TMEM_COLS);
+        tmem_dealloc(tmem, 512);
     }
 }
 
@@ -815,7 +947,7 @@ __global__ void __launch_bounds__(128) expand_row_kernel(const Params p, const f
 
 // ---- host -------------------------------------------------------------------
 
-static Params params(const LoraPlan &q, int C) { return Params{q.row_slot, q.slot_row, q.offsets, q.scale, q.err, q.T, q.r, q.L, C, FastDiv(1)}; }
+static Params params(const LoraPlan &q, int C) { return Params{q.row_slot, q.slot_row, q.offsets, q.scale, q.err, q.T, q.r, q.L, C, FastDiv(1), FastDiv(up16(q.r) / 4)}; }
 // Row tiles of 128 rows, at most, with those of the rows of none.
 static int64_t row_tiles(const LoraPlan &q) { return q.T / 128 + (q.L + 1 < q.T ? q.L + 1 : q.T); }
 // Few tokens: by the row kernels.
@@ -823,50 +955,54 @@ static bool few(const LoraPlan &q) { return (int64_t)q.T * q.r <= 2048; }
 
 template <bool MN>
 static cudaError_t shrink(const LoraPlan &q, const void *x, const void *w, float *v, int C, cudaStream_t s) {
-    CUtensorMap map;
+    CUtensorMap rows, map;
+    if (!encode(&rows, x, 2, C, q.T, 1, 128, false)) return cudaErrorInvalidValue;
     if (!(MN ? encode(&map, w, 2, q.r, C, q.L, KB, true) : encode(&map, w, 2, C, q.r, q.L, q.r, true))) return cudaErrorInvalidValue;
     const DeviceInfo &di = device_info();
     // few tiles: the contraction over as many blocks as run at once, two stages each at least
     const int64_t tiles = row_tiles(q);
     const int blocks = (C + KB - 1) / KB;
     int split = S_MAX_SPLIT;
-    while (split > 1 && (tiles * split > di.num_sms * (s_smem(q.r, MN, split) <= 113 * 1024 ? 2 : 1) || blocks < 2 * split)) split /= 2;
-    const size_t smem = s_smem(q.r, MN, split);
+    while (split > 1 && (tiles * split > di.num_sms * (s_smem(q.r, MN) <= 113 * 1024 ? 2 : 1) || blocks < 2 * split)) split /= 2;
+    const size_t smem = s_smem(q.r, MN);
     const cudaError_t e = ensure_dynamic_smem((const void *)shrink_kernel<MN>, smem);
     if (e != cudaSuccess) return e;
-    return launch_dependent(shrink_kernel<MN>, dim3((unsigned)(tiles * split)), S_THREADS, smem, (unsigned)split, s, map, params(q, C),
+    return launch_dependent(shrink_kernel<MN>, dim3((unsigned)(tiles * split)), S_THREADS, smem, (unsigned)split, s, rows, map, params(q, C),
                             static_cast<const __nv_bfloat16 *>(x), v);
 }
 
-template <int ELEM, int RB, bool MN>
+template <int ELEM, int TN, int BOXES, bool MN>
 static cudaError_t expand(const LoraPlan &q, const float *v, const void *w, const void *base, void *out, int C, cudaStream_t s) {
-    using Cfg = ExpandCfg<ELEM, RB, MN>;
+    using Cfg = ExpandCfg<ELEM, TN, BOXES, MN>;
     CUtensorMap map;
     if (!(MN ? encode(&map, w, 2, C, q.r, q.L, up16(q.r), true) : encode(&map, w, 2, q.r, C, q.L, Cfg::TN, true))) return cudaErrorInvalidValue;
-    const int64_t tiles = row_tiles(q), sms = device_info().num_sms, n_tiles = (C + Cfg::TN - 1) / Cfg::TN;
-    int64_t G = (sms + tiles - 1) / tiles;
-    if (G > n_tiles) G = n_tiles;
+    const int64_t tiles = row_tiles(q), sms = device_info().num_sms;
+    const int64_t G = sms / tiles < 1 ? 1 : sms / tiles;
     const cudaError_t e = ensure_dynamic_smem((const void *)expand_kernel<Cfg>, Cfg::SMEM);
     if (e != cudaSuccess) return e;
-    return launch_dependent(expand_kernel<Cfg>, dim3((unsigned)(tiles * G)), E_THREADS, Cfg::SMEM, 1, s, map, params(q, C), v, base, out, (int)G);
+    return launch_dependent(expand_kernel<Cfg>, dim3((unsigned)(tiles > sms ? tiles : sms)), E_THREADS, Cfg::SMEM, 1, s, map, params(q, C), v, base, out, (int)sms,
+                            (int)G);
 }
-template <int ELEM>
-static cudaError_t expand(const LoraPlan &q, const float *v, const void *w, bool mn, const void *base, void *out, int C, cudaStream_t s) {
-    if (q.r <= 64) return mn ? expand<ELEM, 512, true>(q, v, w, base, out, C, s) : expand<ELEM, 512, false>(q, v, w, base, out, C, s);
-    return mn ? expand<ELEM, 256, true>(q, v, w, base, out, C, s) : expand<ELEM, 256, false>(q, v, w, base, out, C, s);
+template <bool MN>
+static cudaError_t expand(const LoraPlan &q, const float *v, const void *w, int dtype, const void *base, void *out, int C, cudaStream_t s) {
+    if (dtype == ZFFN_DT_BF16) return q.r <= 64 ? expand<2, 256, 1, MN>(q, v, w, base, out, C, s) : expand<2, 128, 2, MN>(q, v, w, base, out, C, s);
+    return q.r <= 64 ? expand<4, 128, 1, MN>(q, v, w, base, out, C, s) : expand<4, 128, 2, MN>(q, v, w, base, out, C, s);
 }
 
-template <int BOXES>
+template <bool WIDE>
 static cudaError_t outer(const LoraPlan &q, const float *v, const void *x, bool transposed, int dtype, void *d, int C, cudaStream_t s) {
-    using Cfg = OuterCfg<BOXES>;
+    using Cfg = OuterCfg<WIDE>;
+    CUtensorMap rows;
+    const bool wide_x = C % 64 == 0;
+    if (!encode(&rows, x, 2, C, q.T, 1, KB, false, wide_x ? 2 : 0)) return cudaErrorInvalidValue;
     const int n_tiles = (C + 127) / 128;
     const int64_t tiles = (int64_t)q.L * n_tiles, sms = device_info().num_sms;
     Params p = params(q, C);
     p.each = GroupWalk<128, 1, true>::divisor(n_tiles);
     const cudaError_t e = ensure_dynamic_smem((const void *)outer_kernel<Cfg>, Cfg::SMEM);
     if (e != cudaSuccess) return e;
-    return launch_dependent(outer_kernel<Cfg>, dim3((unsigned)(tiles < sms ? tiles : sms)), O_THREADS, Cfg::SMEM, 1, s, p, v,
-                            static_cast<const __nv_bfloat16 *>(x), d, n_tiles, (int)transposed, (int)(dtype == ZFFN_DT_BF16));
+    return launch_dependent(outer_kernel<Cfg>, dim3((unsigned)(tiles < sms ? tiles : sms)), O_THREADS, Cfg::SMEM, 1, s, rows, p, v,
+                            static_cast<const __nv_bfloat16 *>(x), d, n_tiles, (int)wide_x, (int)transposed, (int)(dtype == ZFFN_DT_BF16));
 }
 
 }  // namespace lora
@@ -893,12 +1029,13 @@ cudaError_t launch_lora_expand(const LoraPlan &q, const float *v, const void *w,
                                     static_cast<__nv_bfloat16 *>(out));
         return launch_dependent(expand_row_kernel<float>, grid, 128, 0, 1, s, params(q, C), v, w16, static_cast<const float *>(base), static_cast<float *>(out));
     }
-    return dtype == ZFFN_DT_BF16 ? expand<2>(q, v, w, transposed, base, out, C, s) : expand<4>(q, v, w, transposed, base, out, C, s);
+    return transposed ? expand<true>(q, v, w, dtype, base, out, C, s) : expand<false>(q, v, w, dtype, base, out, C, s);
 }
 
 cudaError_t launch_lora_outer(const LoraPlan &q, const float *v, const void *x, bool transposed, int dtype, void *d, int C, cudaStream_t s) {
     using namespace lora;
-    return q.r <= 64 ? outer<1>(q, v, x, transposed, dtype, d, C, s) : outer<2>(q, v, x, transposed, dtype, d, C, s);
+    if (!encode_fn()) return cudaErrorNotSupported;
+    return q.r <= 80 ? outer<false>(q, v, x, transposed, dtype, d, C, s) : outer<true>(q, v, x, transposed, dtype, d, C, s);
 }
 
 }  // namespace zffn
