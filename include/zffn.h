@@ -475,7 +475,7 @@ zffn_status zffn_moe_swiglu_fp8(const void *x, const int32_t *expert_ids,
  * gradients, SwiGLU with its gradient, and low-rank adapters beside a
  * projection of any kind.  Operands are bf16, every sum is fp32 and every result
  * is rounded once.  The source pages have no counterpart of these entry points.
- * None takes library workspace, so calls on several streams may overlap as long
+ * None takes library workspace (the adapters take the caller's), so calls on several streams may overlap as long
  * as their arguments do not.
  * ------------------------------------------------------------------------- */
 
@@ -536,21 +536,26 @@ zffn_status zffn_swiglu_grad(int dtype, const void *dh, const void *gu, void *dg
  * outputs this call takes; the sort is made once for all projections of a step.
  *   x: bf16 [T][K].  A: bf16 [L][r][K].  B: bf16 [L][N][r].
  *   scale: fp32 [L], or NULL for ones.
- *   row_slot: int32 [T]; slot_row: int32 [T]; offsets: int32 [L + 1].  A row whose
- *     row_slot is outside [0, T) adds nothing; offsets count as for
- *     zffn_bf16_matmul; no two rows may have the same token.
+ *   row_slot: int32 [T]; slot_row: int32 [T]; offsets: int32 [L + 1], from 0 on.  A row
+ *     whose row_slot is outside [0, T) and a token whose slot_row is are of no adapter;
+ *     the two must name each other otherwise.
  *   base: dtype (zffn_dtype) [T][N], or NULL for zeros.  out: dtype [T][N]; it may be
  *     base (tokens of no adapter are then left alone), and may not overlap it otherwise.
  *   v: output, fp32 [T][r], the sorted rows' (0 from offsets[L] on): what
  *     zffn_lora_grad needs again.
+ *   work: zffn_lora_work_bytes(T, r, 0) bytes of the caller's, for the call (NULL
+ *     where that is 0).
  * Both products have fp32 sums; v is not rounded to fewer bits between them.
  * Requirements: 1 <= T <= 2^24, K and N multiples of 8 in [8, 65536], r a multiple
- * of 8 in [8, 128], 1 <= L <= 4096; x, A, B, base and out 16-byte aligned, v 16-byte,
+ * of 8 in [8, 128], 1 <= L <= 4096; x, A, B, base, out, v and work 16-byte aligned,
  * the others 4-byte.  Errors: INVALID_ARG, CUDA. */
 zffn_status zffn_lora_add(const void *x, const void *A, const void *B, const float *scale,
                           const int32_t *row_slot, const int32_t *slot_row, const int32_t *offsets,
-                          int dtype, const void *base, void *out, float *v, int T, int N, int K,
-                          int r, int L, void *stream);
+                          int dtype, const void *base, void *out, float *v, void *work, int T, int N,
+                          int K, int r, int L, void *stream);
+/* Bytes of `work` for zffn_lora_add (backward = 0) or zffn_lora_grad (backward = 1);
+ * 0 also for T or r that they refuse.  Host-side query. */
+size_t zffn_lora_work_bytes(int T, int r, int backward);
 
 /* Gradients of zffn_lora_add:
  *     dv[row] = scale[e] dy[t] B[e]                  (fp32 [r])
@@ -563,13 +568,14 @@ zffn_status zffn_lora_add(const void *x, const void *A, const void *B, const flo
  *   base: dx_dtype [T][K] or NULL.  dx: dx_dtype [T][K], may be base.
  *   dA: dw_dtype [L][r][K].  dB: dw_dtype [L][N][r].  dv: output, fp32 [T][r] (0 from
  *     offsets[L] on).
- * Requirements and the other arguments as zffn_lora_add; dy, v, dx, dA, dB and dv
- * 16-byte aligned.  Errors: INVALID_ARG, CUDA. */
+ *   work: zffn_lora_work_bytes(T, r, 1) bytes.
+ * Requirements and the other arguments as zffn_lora_add; dy, v, dx, dA, dB, dv and
+ * work 16-byte aligned.  Errors: INVALID_ARG, CUDA. */
 zffn_status zffn_lora_grad(const void *dy, const void *x, const float *v, const void *A,
                            const void *B, const float *scale, const int32_t *row_slot,
                            const int32_t *slot_row, const int32_t *offsets, int dx_dtype,
                            const void *base, void *dx, int dw_dtype, void *dA, void *dB, float *dv,
-                           int T, int N, int K, int r, int L, void *stream);
+                           void *work, int T, int N, int K, int r, int L, void *stream);
 
 /* Single-token dense block (T = 1) that allocates no device memory.  The
  * source pages have no counterpart of this entry point.  It is for callers

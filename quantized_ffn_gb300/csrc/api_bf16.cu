@@ -80,42 +80,51 @@ zffn_status zffn_swiglu_grad(int dtype, const void *dh, const void *gu, void *dg
     return to_status(launch_swiglu_grad(dtype, dh, gu, dgu, rows, I, (cudaStream_t)stream));
 }
 
+size_t zffn_lora_work_bytes(int T, int r, int backward) {
+    if (T < 1 || T > (1 << 24) || r < 8 || r > 128 || r % 8) return 0;
+    return backward ? 2 * lora_pieces_bytes(T, r) : lora_by_rows(T, r) ? 0 : lora_pieces_bytes(T, r);
+}
+
 zffn_status zffn_lora_add(const void *x, const void *A, const void *B, const float *scale, const int32_t *row_slot,
                           const int32_t *slot_row, const int32_t *offsets, int dtype, const void *base, void *out, float *v,
-                          int T, int N, int K, int r, int L, void *stream) {
+                          void *work, int T, int N, int K, int r, int L, void *stream) {
     LoraPlan p{row_slot, slot_row, offsets, scale, T, r, L, nullptr};
     if (!x || !A || !B || !out || !v) return invalid("a pointer argument is NULL");
     if (!dtype_valid(dtype)) return invalid("unknown dtype");
     if (check_lora(p, N, K) != ZFFN_OK) return ZFFN_ERR_INVALID_ARG;
-    if ((bits(x) | bits(A) | bits(B) | bits(base) | bits(out) | bits(v)) & 15)
-        return invalid("x, A, B, base, out and v must be 16-byte aligned");
+    const bool by_rows = lora_by_rows(T, r);
+    if (!work && !by_rows) return invalid("work is NULL");
+    if ((bits(x) | bits(A) | bits(B) | bits(base) | bits(out) | bits(v) | bits(work)) & 15)
+        return invalid("x, A, B, base, out, v and work must be 16-byte aligned");
     const DeviceInfo &di = device_info();
     if (di.device < 0) return ZFFN_ERR_CUDA;
     p.err = di.err_word;
     cudaStream_t s = (cudaStream_t)stream;
-    const cudaError_t e = launch_lora_shrink(p, x, A, false, v, K, s);
+    if (by_rows) return to_status(launch_lora_rows(p, x, A, B, dtype, base, out, v, N, K, s));
+    const cudaError_t e = launch_lora_shrink(p, x, A, false, v, work, nullptr, nullptr, K, s);
     if (e != cudaSuccess) return to_status(e);
-    return to_status(launch_lora_expand(p, v, B, false, dtype, base, out, N, s));
+    return to_status(launch_lora_expand(p, work, B, false, dtype, base, out, N, s));
 }
 
 zffn_status zffn_lora_grad(const void *dy, const void *x, const float *v, const void *A, const void *B, const float *scale,
                            const int32_t *row_slot, const int32_t *slot_row, const int32_t *offsets, int dx_dtype,
-                           const void *base, void *dx, int dw_dtype, void *dA, void *dB, float *dv, int T, int N, int K,
-                           int r, int L, void *stream) {
+                           const void *base, void *dx, int dw_dtype, void *dA, void *dB, float *dv, void *work, int T,
+                           int N, int K, int r, int L, void *stream) {
     LoraPlan p{row_slot, slot_row, offsets, scale, T, r, L, nullptr};
-    if (!dy || !x || !v || !A || !B || !dx || !dA || !dB || !dv) return invalid("a pointer argument is NULL");
+    if (!dy || !x || !v || !A || !B || !dx || !dA || !dB || !dv || !work) return invalid("a pointer argument is NULL");
     if (!dtype_valid(dx_dtype) || !dtype_valid(dw_dtype)) return invalid("unknown dtype");
     if (check_lora(p, N, K) != ZFFN_OK) return ZFFN_ERR_INVALID_ARG;
-    if ((bits(dy) | bits(x) | bits(v) | bits(A) | bits(B) | bits(base) | bits(dx) | bits(dA) | bits(dB) | bits(dv)) & 15)
-        return invalid("dy, x, v, A, B, base, dx, dA, dB and dv must be 16-byte aligned");
+    if ((bits(dy) | bits(x) | bits(v) | bits(A) | bits(B) | bits(base) | bits(dx) | bits(dA) | bits(dB) | bits(dv) | bits(work)) & 15)
+        return invalid("dy, x, v, A, B, base, dx, dA, dB, dv and work must be 16-byte aligned");
     const DeviceInfo &di = device_info();
     if (di.device < 0) return ZFFN_ERR_CUDA;
     p.err = di.err_word;
     cudaStream_t s = (cudaStream_t)stream;
-    cudaError_t e = launch_lora_shrink(p, dy, B, true, dv, N, s);
-    if (e == cudaSuccess) e = launch_lora_expand(p, dv, A, true, dx_dtype, base, dx, K, s);
-    if (e == cudaSuccess) e = launch_lora_outer(p, dv, x, false, dw_dtype, dA, K, s);
-    if (e == cudaSuccess) e = launch_lora_outer(p, v, dy, true, dw_dtype, dB, N, s);
+    uint8_t *dv16 = static_cast<uint8_t *>(work), *v16 = dv16 + lora_pieces_bytes(T, r);
+    cudaError_t e = launch_lora_shrink(p, dy, B, true, dv, dv16, v, v16, N, s);
+    if (e == cudaSuccess) e = launch_lora_expand(p, dv16, A, true, dx_dtype, base, dx, K, s);
+    if (e == cudaSuccess) e = launch_lora_outer(p, dv16, x, false, dw_dtype, dA, K, s);
+    if (e == cudaSuccess) e = launch_lora_outer(p, v16, dy, true, dw_dtype, dB, N, s);
     return to_status(e);
 }
 

@@ -43,12 +43,21 @@ struct LoraPlan {
     int T, r, L;
     int *err;
 };
-// v[row] = scale x[t] W^T: W [L][r][C], or (transposed) [L][C][r]
-cudaError_t launch_lora_shrink(const LoraPlan &p, const void *x, const void *w, bool transposed, float *v, int C, cudaStream_t s);
-// out[t] = base[t] + v[row] W^T: W [L][C][r], or (transposed) [L][r][C]
-cudaError_t launch_lora_expand(const LoraPlan &p, const float *v, const void *w, bool transposed, int dtype, const void *base, void *out,
+// Bytes of v's bf16 pieces, and whether a forward call goes row by row, without them.
+size_t lora_pieces_bytes(int T, int r);
+bool lora_by_rows(int T, int r);
+// v[row] = scale x[t] W^T, and its pieces v16: W [L][r][C], or (transposed) [L][C][r].  other:
+// nullptr, or fp32 [T][r] whose pieces are written to other16 on the way.
+cudaError_t launch_lora_shrink(const LoraPlan &p, const void *x, const void *w, bool transposed, float *v, void *v16, const float *other, void *other16,
                                int C, cudaStream_t s);
+// out[t] = base[t] + v[row] W^T: W [L][C][r], or (transposed) [L][r][C].  Launched right after
+// the shrink that writes v16.
+cudaError_t launch_lora_expand(const LoraPlan &p, const void *v16, const void *w, bool transposed, int dtype, const void *base, void *out, int C,
+                               cudaStream_t s);
+// Both steps of the forward pass row by row.
+cudaError_t launch_lora_rows(const LoraPlan &p, const void *x, const void *A, const void *B, int dtype, const void *base, void *out, float *v, int N, int K,
+                             cudaStream_t s);
 // d[e] = sum of v[row]^T x[t] over e's rows: d [L][r][C], or (transposed) [L][C][r]
-cudaError_t launch_lora_outer(const LoraPlan &p, const float *v, const void *x, bool transposed, int dtype, void *d, int C, cudaStream_t s);
+cudaError_t launch_lora_outer(const LoraPlan &p, const void *v16, const void *x, bool transposed, int dtype, void *d, int C, cudaStream_t s);
 
 }  // namespace zffn

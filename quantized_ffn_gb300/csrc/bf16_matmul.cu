@@ -223,11 +223,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
                 const int nb = blocks();
                 if (nb == 0) continue;
                 const uint32_t b = acc & 1, dst = tmem + b * 256;
-                ok = acc < 2 || bar_wait(&t_empty[b], ((acc >> 1) & 1) ^ 1, abort_flag, p.err);
+                ok = acc < 2 || bar_wait_warp(&t_empty[b], ((acc >> 1) & 1) ^ 1, abort_flag, p.err);
                 for (int i = 0; i < nb; ++i, ++it) {
                     const uint32_t s = it % C::NS;
-                    ok = ok && bar_wait(&s_full[s], (it / C::NS) & 1, abort_flag, p.err);
-                    if (!__all_sync(0xffffffffu, ok)) break;
+                    ok = ok && bar_wait_warp(&s_full[s], (it / C::NS) & 1, abort_flag, p.err);
+                    if (!ok) break;
                     const uint32_t sa = smem_u32(smem) + s * C::STAGE, sw = sa + C::A_BYTES;
                     const int n = steps(i);
                     const uint32_t box = GRAD ? 2048u << box_of(n) : 8192u;
@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
             const int n = nb ? steps(nb - 1) : 0, valid = wk.rows - (nb - 1) * KB;
             if (valid >= n * 16) continue;
             const uint32_t s = (it - 1) % C::NS;
-            ok = __all_sync(0xffffffffu, bar_wait(&cut_full[s], (phases >> s) & 1, abort_flag, p.err));
+            ok = bar_wait_warp(&cut_full[s], (phases >> s) & 1, abort_flag, p.err);
             if (!ok) break;
             phases ^= 1u << s;
             const uint32_t sa = smem_u32(smem) + s * C::STAGE;
@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
             const bool some = blocks() != 0;
             const uint32_t b = acc & 1, from = taddr + b * 256;
             if (some) {
-                ok = __all_sync(0xffffffffu, bar_wait(&t_full[b], (acc >> 1) & 1, abort_flag, p.err));
+                ok = bar_wait_warp(&t_full[b], (acc >> 1) & 1, abort_flag, p.err);
                 if (!ok) break;
                 tc_fence_after();
                 ++acc;
@@ -525,11 +525,11 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) small_kernel(const __gr
         for (bool have = wk.get(); ok && have; have = next()) {
             if (wk.e >= p.E || nkb == 0) continue;
             const uint32_t b = acc & 1, dst = tmem + b * C::TN;
-            ok = acc < 2 || bar_wait(&t_empty[b], ((acc >> 1) & 1) ^ 1, abort_flag, p.err);
+            ok = acc < 2 || bar_wait_warp(&t_empty[b], ((acc >> 1) & 1) ^ 1, abort_flag, p.err);
             for (int i = 0; i < nkb; ++i, ++it) {
                 const uint32_t s = it % C::NS;
-                ok = ok && bar_wait(&s_full[s], (it / C::NS) & 1, abort_flag, p.err);
-                if (!__all_sync(0xffffffffu, ok)) break;
+                ok = ok && bar_wait_warp(&s_full[s], (it / C::NS) & 1, abort_flag, p.err);
+                if (!ok) break;
                 tc_fence_after();
                 const uint32_t sw = smem_u32(smem) + s * C::STAGE;
                 const int n = (min(KB, p.K - (kb0 + i) * KB) + 15) / 16;
@@ -561,7 +561,7 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) small_kernel(const __gr
             const bool some = wk.e < p.E && nkb != 0;
             const uint32_t b = acc & 1;
             if (some) {
-                ok = __all_sync(0xffffffffu, bar_wait(&t_full[b], (acc >> 1) & 1, abort_flag, p.err));
+                ok = bar_wait_warp(&t_full[b], (acc >> 1) & 1, abort_flag, p.err);
                 if (!ok) break;
                 tc_fence_after();
                 ++acc;

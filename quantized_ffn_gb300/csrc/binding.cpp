@@ -42,6 +42,7 @@ struct Api {
     decltype(&zffn_swiglu_grad) plain_swiglu_grad;
     decltype(&zffn_lora_add) lora_add;
     decltype(&zffn_lora_grad) lora_grad;
+    decltype(&zffn_lora_work_bytes) lora_work_bytes;
 } api{};
 PyObject *g_fail = nullptr;   // (status, name) -> raises ZffnError
 
@@ -547,6 +548,18 @@ struct Lora {
     }
 };
 
+// What a call works in, from the current stream's memory.
+struct Work {
+    at::Tensor t;
+    void *at = nullptr;
+    Work(const Lora &p, int backward, const at::Tensor &like) {
+        if (const size_t bytes = api.lora_work_bytes((int)p.T, (int)p.r, backward)) {
+            t = at::empty({(int64_t)bytes}, like.options().dtype(kU8));
+            at = t.data_ptr();
+        }
+    }
+};
+
 // (x, A, B, plan, scale, base, out, v, dtype, stream) -> (out, v)
 PyObject *lora_add(PyObject *const *a) {
     const Lora p(a[0], a[1], a[2], a[3], a[4]);
@@ -559,8 +572,9 @@ PyObject *lora_add(PyObject *const *a) {
     const int dtype = dtype_of(out.t, "out");
     void *po = ptr(out.t, "out", type, os);
     float *pv = static_cast<float *>(ptr(v.t, "v", kF32, vs));
+    const Work work(p, 0, x);
     call("zffn_lora_add", [&] {
-        return api.lora_add(p.x, p.A, p.B, p.scale, p.row_slot, p.slot_row, p.offsets, dtype, pb, po, pv, (int)p.T, (int)p.N, (int)p.K, (int)p.r,
+        return api.lora_add(p.x, p.A, p.B, p.scale, p.row_slot, p.slot_row, p.offsets, dtype, pb, po, pv, work.at, (int)p.T, (int)p.N, (int)p.K, (int)p.r,
                             (int)p.L, on.s);
     });
     return pair(out.object(), v.object());
@@ -582,8 +596,9 @@ PyObject *lora_grad(PyObject *const *a) {
     const int xd = dtype_of(dx.t, "dx"), wd = dtype_of(dA.t, "dA");
     void *px = ptr(dx.t, "dx", type, x.sizes()), *pA = ptr(dA.t, "dA", wtype, tA.sizes()), *pB = ptr(dB.t, "dB", wtype, tB.sizes());
     float *pdv = static_cast<float *>(ptr(dv.t, "dv", kF32, vs));
+    const Work work(p, 1, x);
     call("zffn_lora_grad", [&] {
-        return api.lora_grad(pd, p.x, pv, p.A, p.B, p.scale, p.row_slot, p.slot_row, p.offsets, xd, pb, px, wd, pA, pB, pdv, (int)p.T, (int)p.N,
+        return api.lora_grad(pd, p.x, pv, p.A, p.B, p.scale, p.row_slot, p.slot_row, p.offsets, xd, pb, px, wd, pA, pB, pdv, work.at, (int)p.T, (int)p.N,
                              (int)p.K, (int)p.r, (int)p.L, on.s);
     });
     PyObject *out = PyTuple_New(3);

@@ -8,7 +8,10 @@
 // tokens' rows, which are gathered (and written back) by their tokens where they lie.
 //
 // Tensor cores take bf16, and v is fp32: it goes as the sum of three bf16 pieces of 8
-// bits each, which is exact, so that v is not rounded between the products.
+// bits each, which is exact, so that v is not rounded between the products.  Shrink writes
+// them beside v, [T][3][up16(r)], so that expand and outer load them by TMA: split in the
+// blocks that multiply them, once for each tile of columns, they were outer's bound (4096
+// rows of r = 32: 62 us for both outer products).
 #include <atomic>
 
 #include "bf16.h"
@@ -43,6 +46,14 @@ __device__ __forceinline__ void pieces(float v, uint32_t (&p)[3]) {
     }
 }
 __device__ __forceinline__ uint32_t high_halves(uint32_t lo, uint32_t hi) { return __byte_perm(lo, hi, 0x7632); }
+// A quad of v's row to its three places.
+__device__ __forceinline__ void put_pieces(__nv_bfloat16 *row, int r16, int c, float4 f) {
+    uint32_t a[4][3];
+    pieces(f.x, a[0]); pieces(f.y, a[1]); pieces(f.z, a[2]); pieces(f.w, a[3]);
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+        *reinterpret_cast<uint2 *>(row + k * r16 + c) = make_uint2(high_halves(a[0][k], a[1][k]), high_halves(a[2][k], a[3][k]));
+}
 __host__ __device__ constexpr int up16(int r) { return (r + 15) / 16 * 16; }
 
 struct Params {
@@ -50,7 +61,7 @@ struct Params {
     const float *scale;
     int *err;
     int T, r, L, C;
-    FastDiv each, by_quads;   // of the walk; by the float4s of a row of v, up to 16 values
+    FastDiv each, by_quads, by_wide;   // of the walk; by the float4s of a row of v, up to 16 values; by its pieces' 16 bytes
 };
 
 // ---------------------------------------------------------------------------
@@ -71,7 +82,8 @@ static size_t s_smem(int r, bool mn) { return 1024 + (size_t)S_NS * (16384 + s_w
 
 template <bool MN>
 __global__ void __launch_bounds__(S_THREADS) shrink_kernel(const __grid_constant__ CUtensorMap xm, const __grid_constant__ CUtensorMap w, const Params p,
-                                                           const __nv_bfloat16 *x, float *v) {
+                                                           const __nv_bfloat16 *x, float *v, __nv_bfloat16 *v16,
+                                                           const float *other, __nv_bfloat16 *other16) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint32_t split;
@@ -142,7 +154,7 @@ __global__ void __launch_bounds__(S_THREADS) shrink_kernel(const __grid_constant
             };
             for (int i = 0; i < nkb; ++i) {
                 const int s = i % S_NS, c = (kb0 + i) * KB;
-                if (i >= S_NS) ok = __all_sync(0xffffffffu, bar_wait(&s_empty[s], ((i / S_NS) & 1) ^ 1, abort_flag, p.err));
+                if (i >= S_NS) ok = bar_wait_warp(&s_empty[s], ((i / S_NS) & 1) ^ 1, abort_flag, p.err);
                 if (!ok) break;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
@@ -165,7 +177,7 @@ __global__ void __launch_bounds__(S_THREADS) shrink_kernel(const __grid_constant
         int i = 0;
         for (bool ok = true; i < nkb; ++i) {
             const int s = i % S_NS;
-            if (i >= S_NS) ok = __all_sync(0xffffffffu, bar_wait(&s_empty[s], ((i / S_NS) & 1) ^ 1, abort_flag, p.err));
+            if (i >= S_NS) ok = bar_wait_warp(&s_empty[s], ((i / S_NS) & 1) ^ 1, abort_flag, p.err);
             if (!ok) break;
             uint8_t *to = smem + s * stage;
             if (lane == 0) {
@@ -190,7 +202,7 @@ __global__ void __launch_bounds__(S_THREADS) shrink_kernel(const __grid_constant
         bool ok = true;
         for (int i = 0; i < nkb; ++i) {
             const int s = i % S_NS;
-            ok = __all_sync(0xffffffffu, bar_wait(&s_full[s], (i / S_NS) & 1, abort_flag, p.err));
+            ok = bar_wait_warp(&s_full[s], (i / S_NS) & 1, abort_flag, p.err);
             if (!ok) break;
             tc_fence_after();
             const uint32_t sx = smem_u32(smem) + s * stage;
@@ -215,14 +227,14 @@ __global__ void __launch_bounds__(S_THREADS) shrink_kernel(const __grid_constant
     if (have && warp < 4) {
         // ---- take out: thread = one row
         if (some) {
-            bar_wait(t_full, 0, abort_flag, p.err);
-            __syncwarp();
+            bar_wait_warp(t_full, 0, abort_flag, p.err);
             tc_fence_after();
         }
         if (split > 1) cluster_sync_all();                   // every block's stages are idle
         const uint32_t from = tmem + ((uint32_t)(warp * 32) << 16);
         const int per = 128 / split, row = tid;
         float *to = v + (int64_t)(wk.row0 + row) * p.r;
+        __nv_bfloat16 *to16 = v16 + (int64_t)(wk.row0 + row) * 3 * r16;
         const uint32_t send = split > 1 ? mapa_shared(smem_u32(part + (rank * per + row % per) * p.r), row / per) : 0;
         for (int c = 0; c < p.r; c += 16) {
             uint32_t d[16];
@@ -235,14 +247,16 @@ __global__ void __launch_bounds__(S_THREADS) shrink_kernel(const __grid_constant
             }
 #pragma unroll
             for (int j = 0; j < 16; j += 4) {
-                if (c + j >= p.r || row >= wk.rows) continue;
+                if (row >= wk.rows) continue;
                 float4 f = make_float4(__uint_as_float(d[j]), __uint_as_float(d[j + 1]), __uint_as_float(d[j + 2]), __uint_as_float(d[j + 3]));
                 if (split > 1) {
-                    st_cluster_f4(send + (c + j) * 4, f);
-                } else {
-                    f.x *= scale; f.y *= scale; f.z *= scale; f.w *= scale;
-                    *reinterpret_cast<float4 *>(to + c + j) = f;
+                    if (c + j < p.r) st_cluster_f4(send + (c + j) * 4, f);
+                    continue;
                 }
+                f.x *= scale; f.y *= scale; f.z *= scale; f.w *= scale;
+                if (c + j < p.r) *reinterpret_cast<float4 *>(to + c + j) = f;
+                else f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (some) put_pieces(to16, r16, c + j, f);
             }
         }
         tc_fence_before();
@@ -253,18 +267,32 @@ __global__ void __launch_bounds__(S_THREADS) shrink_kernel(const __grid_constant
     if (split > 1) {
         cluster_sync_all();
         if (have) {
-            const int per = 128 / split, quads = p.r / 4;
+            const int per = 128 / split, quads = r16 / 4;
             for (int i = tid; i < per * quads; i += S_THREADS) {
-                const int lrow = i / quads, row = rank * per + lrow;
+                const int lrow = p.by_quads.div(i), row = rank * per + lrow, c = (i - lrow * quads) * 4;
                 if (row >= wk.rows) break;
-                float4 f = reinterpret_cast<const float4 *>(part)[i];
-                for (uint32_t k = 1; k < split; ++k) {
-                    const float4 g = reinterpret_cast<const float4 *>(part)[k * per * quads + i];
-                    f.x += g.x; f.y += g.y; f.z += g.z; f.w += g.w;
+                float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (c < p.r) {
+                    f = *reinterpret_cast<const float4 *>(part + lrow * p.r + c);
+                    for (uint32_t k = 1; k < split; ++k) {
+                        const float4 g = *reinterpret_cast<const float4 *>(part + (k * per + lrow) * p.r + c);
+                        f.x += g.x; f.y += g.y; f.z += g.z; f.w += g.w;
+                    }
+                    f.x *= scale; f.y *= scale; f.z *= scale; f.w *= scale;
+                    *reinterpret_cast<float4 *>(v + (int64_t)(wk.row0 + row) * p.r + c) = f;
                 }
-                f.x *= scale; f.y *= scale; f.z *= scale; f.w *= scale;
-                *reinterpret_cast<float4 *>(v + (int64_t)(wk.row0 + row) * p.r + (i - lrow * quads) * 4) = f;
+                if (some) put_pieces(v16 + (int64_t)(wk.row0 + row) * 3 * r16, r16, c, f);
             }
+        }
+    }
+    if (some && other) {
+        // the other outer product's rows of this tile
+        const int per = 128 / split, quads = r16 / 4;
+        for (int i = tid; i < per * quads; i += S_THREADS) {
+            const int lrow = p.by_quads.div(i), row = rank * per + lrow, c = (i - lrow * quads) * 4;
+            if (row >= wk.rows) break;
+            const float4 f = c < p.r ? __ldcg(reinterpret_cast<const float4 *>(other + (int64_t)(wk.row0 + row) * p.r + c)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            put_pieces(other16 + (int64_t)(wk.row0 + row) * 3 * r16, r16, c, f);
         }
     }
     if (warp == 5) {
@@ -291,25 +319,25 @@ template <int ELEM_, int TN_, int BOXES_, bool MN_>
 struct ExpandCfg {
     static constexpr int ELEM = ELEM_, TN = TN_, BOXES = BOXES_;   // BOXES: 64-wide boxes of r
     static constexpr bool MN = MN_;
-    static constexpr int V_BYTES = BOXES * 16384;            // a piece
+    static constexpr int V_BYTES = 3 * BOXES * 16384;        // the pieces
     static constexpr int W_BYTES = BOXES * TN * 128;
     static constexpr int PITCH = TN + 4;                     // floats (spreads the rows over the banks)
-    static constexpr int OFF_W = 3 * V_BYTES;
+    static constexpr int OFF_W = V_BYTES;
     static constexpr int OFF_SUMS = OFF_W + W_BYTES;
     static constexpr int OFF_BAR = OFF_SUMS + 128 * PITCH * 4;
-    static constexpr int SMEM = 1024 + OFF_BAR + 6 * 8 + 8;
+    static constexpr int SMEM = 1024 + OFF_BAR + 8 * 8 + 8;
     static constexpr int TMEM_COLS = 2 * TN;
 };
 
 template <class C>
-__global__ void __launch_bounds__(E_THREADS, 1) expand_kernel(const __grid_constant__ CUtensorMap w, const Params p, const float *v, const void *base,
-                                                              void *out, int sms, int G) {
+__global__ void __launch_bounds__(E_THREADS, 1) expand_kernel(const __grid_constant__ CUtensorMap vm, const __grid_constant__ CUtensorMap w, const Params p,
+                                                              const void *base, void *out, int sms, int G) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     float *sums = reinterpret_cast<float *>(smem + C::OFF_SUMS);
     uint64_t *w_full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
-    uint64_t *w_empty = w_full + 1, *t_full = w_full + 2, *t_empty = w_full + 4;
-    int *info = reinterpret_cast<int *>(w_full + 6);         // abort, TMEM base
+    uint64_t *w_empty = w_full + 1, *t_full = w_full + 2, *t_empty = w_full + 4, *v_full = w_full + 6;
+    int *info = reinterpret_cast<int *>(w_full + 8);         // abort, TMEM base
     volatile int *abort_flag = info;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
     const int r16 = up16(p.r);
@@ -317,10 +345,14 @@ __global__ void __launch_bounds__(E_THREADS, 1) expand_kernel(const __grid_const
         info[0] = 0;
         mbar_init(w_full, 1);
         mbar_init(w_empty, 1);
+        mbar_init(v_full, 1);
         for (int i = 0; i < 2; ++i) { mbar_init(&t_full[i], 1); mbar_init(&t_empty[i], E_WARPS); }
         fence_mbarrier_init();
     }
-    if (warp == E_WARPS && lane == 0) prefetch_tensormap(&w);
+    if (warp == E_WARPS && lane == 0) {
+        prefetch_tensormap(&vm);
+        prefetch_tensormap(&w);
+    }
     if (warp == E_WARPS) {
         tmem_alloc(reinterpret_cast<uint32_t *>(info + 1), C::TMEM_COLS);
         tmem_relinquish();
@@ -375,24 +407,6 @@ __global__ void __launch_bounds__(E_THREADS, 1) expand_kernel(const __grid_const
     }
     grid_wait();
     grid_launch_dependents();
-    if (any) {
-        // v's pieces, K-major; zeros past r and past the tile's rows
-        const int quads = r16 / 4;
-        for (int i = tid; i < 128 * quads; i += E_THREADS) {
-            const int row = p.by_quads.div(i), c = (i - row * quads) * 4;
-            float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (row < wk.rows && c < p.r) f = __ldcg(reinterpret_cast<const float4 *>(v + (int64_t)(wk.row0 + row) * p.r + c));
-            uint32_t a[4][3];
-            pieces(f.x, a[0]); pieces(f.y, a[1]); pieces(f.z, a[2]); pieces(f.w, a[3]);
-            const uint32_t at = (c >> 6) * 16384 + row * 128 + ((((c & 63) >> 3) ^ (row & 7)) << 4) + (c & 4) * 2;
-#pragma unroll
-            for (int k = 0; k < 3; ++k)
-                *reinterpret_cast<uint2 *>(smem + k * C::V_BYTES + at) = make_uint2(high_halves(a[0][k], a[1][k]), high_halves(a[2][k], a[3][k]));
-        }
-        fence_proxy_async_smem();
-    }
-    __syncthreads();
-
     if (any && warp < E_WARPS) {
         // (a quarter of the warps to 32 rows in tensor memory, SHARE columns each)
         constexpr int SHARE = C::TN / (E_WARPS / 4);
@@ -405,7 +419,7 @@ __global__ void __launch_bounds__(E_THREADS, 1) expand_kernel(const __grid_const
         for (int nt = g; nt < n_tiles; nt += G, ++i) {
             const int b = i & 1;
             // (a warp that gives up still meets the others at the barriers)
-            const bool ok = __all_sync(0xffffffffu, bar_wait(&t_full[b], (i >> 1) & 1, abort_flag, p.err));
+            const bool ok = bar_wait_warp(&t_full[b], (i >> 1) & 1, abort_flag, p.err);
             tc_fence_after();
             if (ok) {
                 const uint32_t acc = tmem + b * C::TN + c0 + ((uint32_t)(quarter * 32) << 16);
@@ -471,32 +485,45 @@ __global__ void __launch_bounds__(E_THREADS, 1) expand_kernel(const __grid_const
             named_barrier(1, E_WARPS * 32);
         }
     } else if (any && warp == E_WARPS) {
+        // v's pieces, K-major, the three one after another
         const uint32_t idesc = idesc_bf16_f32(128, C::TN, false, C::MN), sv = smem_u32(smem), sw = sv + C::OFF_W;
+        const int steps = r16 / 16;
+        if (lane == 0) {
+            const int boxes = (3 * r16 + 63) / 64;
+            mbar_arrive_expect_tx(v_full, boxes * 16384);
+            for (int b = 0; b < boxes; ++b) tma_load_2d(smem + b * 16384, &vm, v_full, b * 64, wk.row0);
+        }
+        __syncwarp();
         int i = 0;
-        bool ok = true;
-        for (int nt = g; nt < n_tiles; nt += G, ++i) {
+        bool ok = bar_wait_warp(v_full, 0, abort_flag, p.err);
+        if (!ok) {                     // (no copy is left on its way)
+            mbar_wait(v_full, 0, nullptr, p.err);
+            mbar_wait(w_full, 0, nullptr, p.err);
+        }
+        for (int nt = g; ok && nt < n_tiles; nt += G, ++i) {
             const int b = i & 1;
             if (i > 0) {               // (W's tile before has been read)
-                ok = __all_sync(0xffffffffu, bar_wait(w_empty, (i - 1) & 1, abort_flag, p.err));
+                ok = bar_wait_warp(w_empty, (i - 1) & 1, abort_flag, p.err);
                 if (!ok) break;
                 if (lane == 0) load_w(nt);
                 __syncwarp();
             }
-            ok = __all_sync(0xffffffffu, bar_wait(w_full, i & 1, abort_flag, p.err) &&
-                                             (i < 2 || bar_wait(&t_empty[b], ((i >> 1) & 1) ^ 1, abort_flag, p.err)));
+            ok = bar_wait_warp(w_full, i & 1, abort_flag, p.err) &&
+                 (i < 2 || bar_wait_warp(&t_empty[b], ((i >> 1) & 1) ^ 1, abort_flag, p.err));
             if (!ok) {                 // (no copy is left on its way)
                 mbar_wait(w_full, i & 1, nullptr, p.err);
                 break;
             }
             tc_fence_after();
             if (elect_one()) {
-                for (int k = 0; k < r16 / 16; ++k) {
+                for (int k = 0; k < steps; ++k) {
                     const uint64_t wd = C::MN ? smem_desc_mn_sw128(sw, r16 * 128) + k * k_step(true)
                                               : smem_desc_k_sw128(sw + (k >> 2) * C::TN * 128) + (k & 3) * k_step(false);
 #pragma unroll
-                    for (int q = 0; q < 3; ++q)
-                        tc_mma_bf16(tmem + b * C::TN, smem_desc_k_sw128(sv + q * C::V_BYTES + (k >> 2) * 16384) + (k & 3) * k_step(false), wd, idesc,
-                                    (k | q) != 0);
+                    for (int q = 0; q < 3; ++q) {
+                        const int a = q * steps + k;
+                        tc_mma_bf16(tmem + b * C::TN, smem_desc_k_sw128(sv + (a >> 2) * 16384) + (a & 3) * k_step(false), wd, idesc, (k | q) != 0);
+                    }
                 }
                 tc_commit(w_empty);
                 tc_commit(&t_full[b]);
@@ -530,10 +557,10 @@ __global__ void __launch_bounds__(E_THREADS, 1) expand_kernel(const __grid_const
 // three: with one for each piece their reads of x were the bound), summed over an adapter's
 // rows, 64 a stage.  Persistent; where tensor memory has room for two accumulators (r up to
 // 80) one is taken out while the next tile's MMAs run.  Rows as in shrink: by TMA where
-// their tokens follow one another.
+// their tokens follow one another, but for an adapter's last ones.
 //
-// Roles: warps 0 and 1 bring x's rows, warp 2 issues the MMAs, warps 4 .. 11 split v into its
-// pieces, warps 12 .. 15 take a tile out (32 columns of x each).
+// Roles: warp 0 loads by TMA, warp 2 issues the MMAs, warps 4 .. 11 gather what TMA does not,
+// warps 12 .. 15 take a tile out (32 columns of x each).
 // ---------------------------------------------------------------------------
 constexpr int O_THREADS = 512;
 
@@ -544,14 +571,14 @@ struct OuterCfg {
     static constexpr int STAGE = 16384 + V_BYTES;
     static constexpr int NS = WIDE ? 3 : 4, LAG = NS - 1;
     static constexpr int ACC = WIDE ? 1 : 2, ACC_COLS = 512 / ACC;
-    static constexpr int PER = WIDE ? 8 : 5;                 // float4 of v a thread and stage, at most
     static constexpr int OFF_BAR = NS * STAGE;
     static constexpr int SMEM = 1024 + OFF_BAR + (2 * NS + 4) * 8 + 8;
 };
 
 template <class C>
-__global__ void __launch_bounds__(O_THREADS, 1) outer_kernel(const __grid_constant__ CUtensorMap xm, const Params p, const float *v,
-                                                             const __nv_bfloat16 *x, void *d, int n_tiles, int wide_x, int transposed, int d_bf16) {
+__global__ void __launch_bounds__(O_THREADS, 1) outer_kernel(const __grid_constant__ CUtensorMap xm, const __grid_constant__ CUtensorMap vm, const Params p,
+                                                             const __nv_bfloat16 *v16, const __nv_bfloat16 *x, void *d, int n_tiles, int wide_x,
+                                                             int transposed, int d_bf16) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint64_t *s_full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
@@ -562,10 +589,11 @@ __global__ void __launch_bounds__(O_THREADS, 1) outer_kernel(const __grid_consta
     const int r16 = up16(p.r);
     if (tid == 0) {
         info[0] = 0;
-        for (int i = 0; i < C::NS; ++i) { mbar_init(&s_full[i], 10); mbar_init(&s_empty[i], 1); }
+        for (int i = 0; i < C::NS; ++i) { mbar_init(&s_full[i], 9); mbar_init(&s_empty[i], 1); }
         for (int i = 0; i < 2; ++i) { mbar_init(&t_full[i], 1); mbar_init(&t_empty[i], 4); }
         fence_mbarrier_init();
         prefetch_tensormap(&xm);
+        prefetch_tensormap(&vm);
     }
     if (warp == 2) {
         tmem_alloc(reinterpret_cast<uint32_t *>(info + 1), 512);
@@ -578,19 +606,81 @@ __global__ void __launch_bounds__(O_THREADS, 1) outer_kernel(const __grid_consta
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(info + 1);
     GroupWalk<128, 1, true> wk;
-    if (warp != 3) wk.start(p.offsets, p.T, p.L, n_tiles, p.each, false, blockIdx.x);
+    if (warp != 1 && warp != 3) wk.start(p.offsets, p.T, p.L, n_tiles, p.each, false, blockIdx.x);
     auto stages = [&] { return (wk.rows + KB - 1) / KB; };
+    // The tile's stages that TMA loads, the first ones: all whole ones where the group's tokens
+    // follow one another, else none (looked at again only where the group has changed).
+    int whole_of = -1, whole = 0;
+    auto whole_stages = [&] {
+        if (wk.e == whole_of) return whole;
+        bool packed = wk.rows > 0;
+        const int32_t *slot = p.row_slot + wk.row0;
+        const int t0 = packed ? __ldcg(slot) : -1;
+        packed = packed && t0 >= 0 && t0 <= p.T - wk.rows;
+        // (eight loads on their way: one after another, ending at the first stranger, they took
+        // three quarters of the kernel's time)
+        for (int i = lane; i < wk.rows; i += 32 * 8) {
+            int t[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) t[j] = i + 32 * j < wk.rows ? __ldcg(slot + i + 32 * j) : t0 + i + 32 * j;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) packed = packed && t[j] == t0 + i + 32 * j;
+        }
+        whole_of = wk.e;
+        whole = __all_sync(0xffffffffu, packed) ? wk.rows / KB : 0;
+        return whole;
+    };
 
-    if (warp < 2) {
-        // ---- x's rows: by TMA, or thread = one 16-byte column of rows tid / 16 + 4 j
-        const int chunk = tid & 15, first = tid >> 4;
-        const uint32_t dst = smem_u32(smem) + (chunk >> 3) * 8192 + first * 128;
-        const uint32_t even = ((chunk & 7) ^ first) << 4, odd = ((chunk & 7) ^ (first + 4)) << 4;
-        uint32_t it = 0, sent = 0, gathered = 0;             // gathered: a bit for each stage
+    if (warp == 0) {
+        // ---- by TMA
+        const int boxes = (3 * r16 + 63) / 64;
+        uint32_t it = 0, asked = 0;                          // asked: the stages whose last fill was this warp's
+        bool ok = true;
+        for (; ok && wk.get(); wk.t += gridDim.x) {
+            const int ns = stages(), n = whole_stages(), t0 = n ? __ldcg(p.row_slot + wk.row0) : 0;
+            // (This warp and the gathering ones each arrive for every stage, whoever fills it: who
+            // only waited for s_empty could be left more than a phase behind, and a barrier
+            // tells a phase from the next one alone.)
+            for (int i = 0; i < ns; ++i, ++it) {
+                const uint32_t s = it % C::NS;
+                if (it >= (uint32_t)C::NS) ok = bar_wait_warp(&s_empty[s], ((it / C::NS) & 1) ^ 1, abort_flag, p.err);
+                if (!ok) break;
+                if (i >= n) {
+                    asked &= ~(1u << s);
+                    if (lane == 0) mbar_arrive(&s_full[s]);
+                    __syncwarp();
+                    continue;
+                }
+                asked |= 1u << s;
+                uint8_t *to = smem + s * C::STAGE;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&s_full[s], 16384 + boxes * 8192);
+                    if (wide_x) {
+                        tma_load_3d(to, &xm, &s_full[s], 0, t0 + i * KB, wk.nt * 2);
+                    } else {
+                        tma_load_2d(to, &xm, &s_full[s], wk.nt * 128, t0 + i * KB);
+                        tma_load_2d(to + 8192, &xm, &s_full[s], wk.nt * 128 + 64, t0 + i * KB);
+                    }
+                    for (int b = 0; b < boxes; ++b) tma_load_2d(to + 16384 + b * 8192, &vm, &s_full[s], b * 64, wk.row0 + i * KB);
+                }
+                __syncwarp();
+            }
+        }
+        if (lane == 0 && *abort_flag)                        // no copy is left on its way
+            for (uint32_t j = it > (uint32_t)C::NS ? it - C::NS : 0; j < it; ++j)
+                if ((asked >> (j % C::NS)) & 1) mbar_wait(&s_full[j % C::NS], (j / C::NS) & 1, nullptr, p.err);
+        __syncwarp();
+    } else if (warp >= 4 && warp < 12) {
+        // ---- gather: x's rows (thread = one 16-byte column of rows me / 16 + 16 j) and the
+        // pieces' (16-byte columns in turn); zeros past the group's rows and for rows of no token
+        const int me = tid - 128, chunk = me & 15, first = me >> 4, wide = 3 * r16 / 8;
+        const uint32_t dst = smem_u32(smem) + (chunk >> 3) * 8192 + first * 128 + (((chunk & 7) ^ (first & 7)) << 4);
+        const FastDiv by_wide = p.by_wide;
+        uint32_t it = 0, sent = 0, mine = 0;                 // mine: a bit for each stage
         bool ok = true;
         auto filled = [&] {            // this thread's copies of the oldest stage have arrived
             const uint32_t s = sent % C::NS;
-            if ((gathered >> s) & 1) {
+            if ((mine >> s) & 1) {
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s_full[s]);
@@ -598,52 +688,34 @@ __global__ void __launch_bounds__(O_THREADS, 1) outer_kernel(const __grid_consta
             ++sent;
         };
         for (; ok && wk.get(); wk.t += gridDim.x) {
-            const int ns = stages();
-            // tokens of rows lane and 32 + lane of four stages, and of the next four on their way
-            int now[4][2], next[4][2];
-            auto tokens = [&](int i, int (&t)[4][2]) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int at = i * KB + j * 32 + lane;
-                    t[j >> 1][j & 1] = at < wk.rows ? __ldcg(p.row_slot + wk.row0 + at) : -1;
-                }
-            };
-            tokens(0, next);
+            const int ns = stages(), n = whole_stages(), col = wk.nt * 128 + chunk * 8;
             for (int i = 0; i < ns; ++i, ++it) {
-                if (i % 4 == 0) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) { now[j][0] = next[j][0]; now[j][1] = next[j][1]; }
-                    if (i + 4 < ns) tokens(i + 4, next);
-                }
-                const int t[2] = {i % 4 < 2 ? i % 4 ? now[1][0] : now[0][0] : i % 4 == 2 ? now[2][0] : now[3][0],
-                                  i % 4 < 2 ? i % 4 ? now[1][1] : now[0][1] : i % 4 == 2 ? now[2][1] : now[3][1]};
                 const uint32_t s = it % C::NS;
-                if (it >= (uint32_t)C::NS) ok = __all_sync(0xffffffffu, bar_wait(&s_empty[s], ((it / C::NS) & 1) ^ 1, abort_flag, p.err));
-                if (!ok) break;
-                const int t0 = __shfl_sync(0xffffffffu, t[0], 0);
-                const bool packed = __all_sync(0xffffffffu, t[0] == t0 + lane && t[1] == t0 + 32 + lane) && t0 >= 0 && t0 + KB <= p.T;
-                if (packed) {
-                    gathered &= ~(1u << s);
-                    if (tid == 0) {
-                        uint8_t *to = smem + s * C::STAGE;
-                        mbar_arrive_expect_tx(&s_full[s], 16384);
-                        if (wide_x) {
-                            tma_load_3d(to, &xm, &s_full[s], 0, t0, wk.nt * 2);
-                        } else {
-                            tma_load_2d(to, &xm, &s_full[s], wk.nt * 128, t0);
-                            tma_load_2d(to + 8192, &xm, &s_full[s], wk.nt * 128 + 64, t0);
-                        }
-                    } else if (tid == 32) {
-                        mbar_arrive(&s_full[s]);
-                    }
+                mine &= ~(1u << s);
+                if (i < n) {
+                    if (it >= (uint32_t)C::NS) ok = bar_wait_warp(&s_empty[s], ((it / C::NS) & 1) ^ 1, abort_flag, p.err);
+                    if (!ok) break;
+                    if (lane == 0) mbar_arrive(&s_full[s]);
                 } else {
-                    gathered |= 1u << s;
-                    const int col = wk.nt * 128 + chunk * 8;
+                    mine |= 1u << s;
+                    const int32_t *slot = p.row_slot + wk.row0 + i * KB;
+                    const int rows = wk.rows - i * KB;
+                    int tok[4];
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const int tok = __shfl_sync(0xffffffffu, t[j >> 3], (first + 4 * j) & 31);
-                        const bool there = (unsigned)tok < (unsigned)p.T && col < p.C;
-                        copy16(dst + s * C::STAGE + j * 512 + (j & 1 ? odd : even), there ? x + (int64_t)tok * p.C + col : x, there);
+                    for (int j = 0; j < 4; ++j) tok[j] = first + 16 * j < rows ? __ldcg(slot + first + 16 * j) : -1;
+                    if (it >= (uint32_t)C::NS) ok = bar_wait_warp(&s_empty[s], ((it / C::NS) & 1) ^ 1, abort_flag, p.err);
+                    if (!ok) break;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const bool there = (unsigned)tok[j] < (unsigned)p.T && col < p.C;
+                        copy16(dst + s * C::STAGE + j * 2048, there ? x + (int64_t)tok[j] * p.C + col : x, there);
+                    }
+                    const uint32_t to = smem_u32(smem) + s * C::STAGE + 16384;
+                    for (int q = me; q < KB * wide; q += 256) {
+                        const int row = by_wide.div(q), c = q - row * wide;
+                        const bool there = row < rows && (unsigned)__ldcg(slot + row) < (unsigned)p.T;
+                        copy16(to + (c >> 3) * 8192 + row * 128 + (((c & 7) ^ (row & 7)) << 4),
+                               there ? v16 + (int64_t)(wk.row0 + i * KB + row) * 3 * r16 + c * 8 : v16, there);
                     }
                 }
                 copy_commit();
@@ -656,79 +728,6 @@ __global__ void __launch_bounds__(O_THREADS, 1) outer_kernel(const __grid_consta
         copy_wait<0>();
         if (ok)
             while (sent != it) filled();
-        // (a launch that gave up: the copies in flight are waited for, as long as the bound lasts)
-        if (tid == 0 && *abort_flag)
-            for (uint32_t j = it > (uint32_t)C::NS ? it - C::NS : 0; j < it; ++j)
-                mbar_wait(&s_full[j % C::NS], (j / C::NS) & 1, nullptr, p.err);
-        __syncwarp();
-    } else if (warp >= 4 && warp < 12) {
-        // ---- v's pieces side by side, MN-major; zeros past r, past the group's rows and for rows of no token
-        // (a thread has the same r16 / 16 places of every stage)
-        const int per = r16 / 16;
-        int row[C::PER], from[C::PER];                       // row of the stage; place in v from the stage's first row, -1: past r
-        uint32_t at[C::PER][3];                              // where each piece goes
-#pragma unroll
-        for (int j = 0; j < C::PER; ++j) {
-            const int q = tid - 128 + 256 * j;
-            row[j] = p.by_quads.div(q);
-            const int c = (q - row[j] * (r16 / 4)) * 4;
-            from[j] = c < p.r ? row[j] * p.r + c : -1;
-#pragma unroll
-            for (int k = 0; k < 3; ++k) {
-                const int n = k * r16 + c;
-                at[j][k] = smem_u32(smem) + 16384 + (n >> 6) * 8192 + row[j] * 128 + ((((n & 63) >> 3) ^ (row[j] & 7)) << 4) + (n & 4) * 2;
-            }
-        }
-        uint32_t it = 0;
-        bool ok = true;
-        for (; ok && wk.get(); wk.t += gridDim.x) {
-            const int ns = stages();
-            // (two stages' values on their way)
-            float4 f[2][C::PER];
-            int tok[2][C::PER];
-            auto ask = [&](int i, float4 (&f)[C::PER], int (&tok)[C::PER]) {
-                const float *src = v + (int64_t)(wk.row0 + i * KB) * p.r;
-                const int32_t *slot = p.row_slot + wk.row0 + i * KB;
-#pragma unroll
-                for (int j = 0; j < C::PER; ++j) {
-                    f[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    tok[j] = -1;
-                    if (j >= per) break;
-                    if (row[j] < wk.rows - i * KB && from[j] >= 0) {
-                        tok[j] = __ldcg(slot + row[j]);
-                        f[j] = __ldcg(reinterpret_cast<const float4 *>(src + from[j]));
-                    }
-                }
-            };
-            auto stage = [&](int i, float4 (&f)[C::PER], int (&tok)[C::PER]) {
-                const int s = it % C::NS;
-                if (it >= (uint32_t)C::NS) ok = __all_sync(0xffffffffu, bar_wait(&s_empty[s], ((it / C::NS) & 1) ^ 1, abort_flag, p.err));
-                if (!ok) return;
-#pragma unroll
-                for (int j = 0; j < C::PER; ++j) {
-                    if (j >= per) break;
-                    if ((unsigned)tok[j] >= (unsigned)p.T) f[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    uint32_t a[4][3];
-                    pieces(f[j].x, a[0]); pieces(f[j].y, a[1]); pieces(f[j].z, a[2]); pieces(f[j].w, a[3]);
-#pragma unroll
-                    for (int k = 0; k < 3; ++k)
-                        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at[j][k] + s * C::STAGE), "r"(high_halves(a[0][k], a[1][k])),
-                                     "r"(high_halves(a[2][k], a[3][k]))
-                                     : "memory");
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&s_full[s]);
-                if (i + 2 < ns) ask(i + 2, f, tok);          // (after the fence, which waits for loads before it)
-                ++it;
-            };
-            if (ns > 0) ask(0, f[0], tok[0]);
-            if (ns > 1) ask(1, f[1], tok[1]);
-            for (int i = 0; ok && i < ns; i += 2) {
-                stage(i, f[0], tok[0]);
-                if (ok && i + 1 < ns) stage(i + 1, f[1], tok[1]);
-            }
-        }
     } else if (warp == 2) {
         // ---- MMA issuer: columns 0 .. 255 of the pieces, and those past them
         const int cols = 3 * r16, low = cols < 256 ? cols : 256;
@@ -739,11 +738,11 @@ __global__ void __launch_bounds__(O_THREADS, 1) outer_kernel(const __grid_consta
             const int ns = stages();
             if (ns == 0) continue;
             const uint32_t b = acc % C::ACC, dst = tmem + b * C::ACC_COLS;
-            ok = acc < (uint32_t)C::ACC || bar_wait(&t_empty[b], ((acc / C::ACC) & 1) ^ 1, abort_flag, p.err);
+            ok = acc < (uint32_t)C::ACC || bar_wait_warp(&t_empty[b], ((acc / C::ACC) & 1) ^ 1, abort_flag, p.err);
             for (int i = 0; i < ns; ++i, ++it) {
                 const uint32_t s = it % C::NS;
-                ok = ok && bar_wait(&s_full[s], (it / C::NS) & 1, abort_flag, p.err);
-                if (!__all_sync(0xffffffffu, ok)) break;
+                ok = ok && bar_wait_warp(&s_full[s], (it / C::NS) & 1, abort_flag, p.err);
+                if (!ok) break;
                 tc_fence_after();
                 const uint32_t sx = smem_u32(smem) + s * C::STAGE, sv = sx + 16384;
                 const int n = (min(KB, wk.rows - i * KB) + 15) / 16;
@@ -775,7 +774,7 @@ __global__ void __launch_bounds__(O_THREADS, 1) outer_kernel(const __grid_consta
             const bool some = wk.rows > 0;
             const uint32_t b = acc % C::ACC;
             if (some) {
-                ok = __all_sync(0xffffffffu, bar_wait(&t_full[b], (acc / C::ACC) & 1, abort_flag, p.err));
+                ok = bar_wait_warp(&t_full[b], (acc / C::ACC) & 1, abort_flag, p.err);
                 if (!ok) break;
                 tc_fence_after();
                 ++acc;
@@ -947,14 +946,14 @@ __global__ void __launch_bounds__(128) expand_row_kernel(const Params p, const f
 
 // ---- host -------------------------------------------------------------------
 
-static Params params(const LoraPlan &q, int C) { return Params{q.row_slot, q.slot_row, q.offsets, q.scale, q.err, q.T, q.r, q.L, C, FastDiv(1), FastDiv(up16(q.r) / 4)}; }
+static Params params(const LoraPlan &q, int C) { return Params{q.row_slot, q.slot_row, q.offsets, q.scale, q.err, q.T, q.r, q.L, C, FastDiv(1), FastDiv(up16(q.r) / 4), FastDiv(3 * up16(q.r) / 8)}; }
 // Row tiles of 128 rows, at most, with those of the rows of none.
 static int64_t row_tiles(const LoraPlan &q) { return q.T / 128 + (q.L + 1 < q.T ? q.L + 1 : q.T); }
 // Few tokens: by the row kernels.
-static bool few(const LoraPlan &q) { return (int64_t)q.T * q.r <= 2048; }
+static bool few(int T, int r) { return (int64_t)T * r <= 2048; }
 
 template <bool MN>
-static cudaError_t shrink(const LoraPlan &q, const void *x, const void *w, float *v, int C, cudaStream_t s) {
+static cudaError_t shrink(const LoraPlan &q, const void *x, const void *w, float *v, void *v16, const float *other, void *other16, int C, cudaStream_t s) {
     CUtensorMap rows, map;
     if (!encode(&rows, x, 2, C, q.T, 1, 128, false)) return cudaErrorInvalidValue;
     if (!(MN ? encode(&map, w, 2, q.r, C, q.L, KB, true) : encode(&map, w, 2, C, q.r, q.L, q.r, true))) return cudaErrorInvalidValue;
@@ -968,74 +967,81 @@ static cudaError_t shrink(const LoraPlan &q, const void *x, const void *w, float
     const cudaError_t e = ensure_dynamic_smem((const void *)shrink_kernel<MN>, smem);
     if (e != cudaSuccess) return e;
     return launch_dependent(shrink_kernel<MN>, dim3((unsigned)(tiles * split)), S_THREADS, smem, (unsigned)split, s, rows, map, params(q, C),
-                            static_cast<const __nv_bfloat16 *>(x), v);
+                            static_cast<const __nv_bfloat16 *>(x), v, static_cast<__nv_bfloat16 *>(v16), other, static_cast<__nv_bfloat16 *>(other16));
 }
 
 template <int ELEM, int TN, int BOXES, bool MN>
-static cudaError_t expand(const LoraPlan &q, const float *v, const void *w, const void *base, void *out, int C, cudaStream_t s) {
+static cudaError_t expand(const LoraPlan &q, const void *v16, const void *w, const void *base, void *out, int C, cudaStream_t s) {
     using Cfg = ExpandCfg<ELEM, TN, BOXES, MN>;
-    CUtensorMap map;
+    CUtensorMap rows, map;
+    if (!encode(&rows, v16, 2, 3 * up16(q.r), q.T, 1, 128, false)) return cudaErrorInvalidValue;
     if (!(MN ? encode(&map, w, 2, C, q.r, q.L, up16(q.r), true) : encode(&map, w, 2, q.r, C, q.L, Cfg::TN, true))) return cudaErrorInvalidValue;
     const int64_t tiles = row_tiles(q), sms = device_info().num_sms;
     const int64_t G = sms / tiles < 1 ? 1 : sms / tiles;
     const cudaError_t e = ensure_dynamic_smem((const void *)expand_kernel<Cfg>, Cfg::SMEM);
     if (e != cudaSuccess) return e;
-    return launch_dependent(expand_kernel<Cfg>, dim3((unsigned)(tiles > sms ? tiles : sms)), E_THREADS, Cfg::SMEM, 1, s, map, params(q, C), v, base, out, (int)sms,
+    return launch_dependent(expand_kernel<Cfg>, dim3((unsigned)(tiles > sms ? tiles : sms)), E_THREADS, Cfg::SMEM, 1, s, rows, map, params(q, C), base, out, (int)sms,
                             (int)G);
 }
 template <bool MN>
-static cudaError_t expand(const LoraPlan &q, const float *v, const void *w, int dtype, const void *base, void *out, int C, cudaStream_t s) {
+static cudaError_t expand(const LoraPlan &q, const void *v, const void *w, int dtype, const void *base, void *out, int C, cudaStream_t s) {
     if (dtype == ZFFN_DT_BF16) return q.r <= 64 ? expand<2, 256, 1, MN>(q, v, w, base, out, C, s) : expand<2, 128, 2, MN>(q, v, w, base, out, C, s);
     return q.r <= 64 ? expand<4, 128, 1, MN>(q, v, w, base, out, C, s) : expand<4, 128, 2, MN>(q, v, w, base, out, C, s);
 }
 
 template <bool WIDE>
-static cudaError_t outer(const LoraPlan &q, const float *v, const void *x, bool transposed, int dtype, void *d, int C, cudaStream_t s) {
+static cudaError_t outer(const LoraPlan &q, const void *v16, const void *x, bool transposed, int dtype, void *d, int C, cudaStream_t s) {
     using Cfg = OuterCfg<WIDE>;
-    CUtensorMap rows;
+    CUtensorMap rows, map;
     const bool wide_x = C % 64 == 0;
-    if (!encode(&rows, x, 2, C, q.T, 1, KB, false, wide_x ? 2 : 0)) return cudaErrorInvalidValue;
+    if (!encode(&rows, x, 2, C, q.T, 1, KB, false, wide_x ? 2 : 0) || !encode(&map, v16, 2, 3 * up16(q.r), q.T, 1, KB, false)) return cudaErrorInvalidValue;
     const int n_tiles = (C + 127) / 128;
     const int64_t tiles = (int64_t)q.L * n_tiles, sms = device_info().num_sms;
     Params p = params(q, C);
     p.each = GroupWalk<128, 1, true>::divisor(n_tiles);
     const cudaError_t e = ensure_dynamic_smem((const void *)outer_kernel<Cfg>, Cfg::SMEM);
     if (e != cudaSuccess) return e;
-    return launch_dependent(outer_kernel<Cfg>, dim3((unsigned)(tiles < sms ? tiles : sms)), O_THREADS, Cfg::SMEM, 1, s, rows, p, v,
-                            static_cast<const __nv_bfloat16 *>(x), d, n_tiles, (int)wide_x, (int)transposed, (int)(dtype == ZFFN_DT_BF16));
+    return launch_dependent(outer_kernel<Cfg>, dim3((unsigned)(tiles < sms ? tiles : sms)), O_THREADS, Cfg::SMEM, 1, s, rows, map, p,
+                            static_cast<const __nv_bfloat16 *>(v16), static_cast<const __nv_bfloat16 *>(x), d, n_tiles, (int)wide_x, (int)transposed, (int)(dtype == ZFFN_DT_BF16));
 }
 
 }  // namespace lora
 
-cudaError_t launch_lora_shrink(const LoraPlan &q, const void *x, const void *w, bool transposed, float *v, int C, cudaStream_t s) {
+size_t lora_pieces_bytes(int T, int r) { return (size_t)T * 6 * lora::up16(r); }
+bool lora_by_rows(int T, int r) { return lora::few(T, r); }
+
+cudaError_t launch_lora_shrink(const LoraPlan &q, const void *x, const void *w, bool transposed, float *v, void *v16, const float *other, void *other16,
+                               int C, cudaStream_t s) {
     using namespace lora;
     if (!encode_fn()) return cudaErrorNotSupported;
-    if (transposed) return shrink<true>(q, x, w, v, C, s);
-    if (few(q))
-        return launch_dependent(shrink_row_kernel, dim3((unsigned)q.T, (unsigned)(q.r / 8)), 256, 0, 1, s, params(q, C),
-                                static_cast<const __nv_bfloat16 *>(x), static_cast<const __nv_bfloat16 *>(w), v);
-    return shrink<false>(q, x, w, v, C, s);
+    return transposed ? shrink<true>(q, x, w, v, v16, other, other16, C, s) : shrink<false>(q, x, w, v, v16, other, other16, C, s);
 }
 
-cudaError_t launch_lora_expand(const LoraPlan &q, const float *v, const void *w, bool transposed, int dtype, const void *base, void *out, int C,
+cudaError_t launch_lora_expand(const LoraPlan &q, const void *v16, const void *w, bool transposed, int dtype, const void *base, void *out, int C,
                                cudaStream_t s) {
     using namespace lora;
     if (!encode_fn()) return cudaErrorNotSupported;
-    if (few(q) && !transposed) {
-        const dim3 grid((unsigned)q.T, (unsigned)((C + 255) / 256));
-        const __nv_bfloat16 *w16 = static_cast<const __nv_bfloat16 *>(w);
-        if (dtype == ZFFN_DT_BF16)
-            return launch_dependent(expand_row_kernel<__nv_bfloat16>, grid, 128, 0, 1, s, params(q, C), v, w16, static_cast<const __nv_bfloat16 *>(base),
-                                    static_cast<__nv_bfloat16 *>(out));
-        return launch_dependent(expand_row_kernel<float>, grid, 128, 0, 1, s, params(q, C), v, w16, static_cast<const float *>(base), static_cast<float *>(out));
-    }
-    return transposed ? expand<true>(q, v, w, dtype, base, out, C, s) : expand<false>(q, v, w, dtype, base, out, C, s);
+    return transposed ? expand<true>(q, v16, w, dtype, base, out, C, s) : expand<false>(q, v16, w, dtype, base, out, C, s);
 }
 
-cudaError_t launch_lora_outer(const LoraPlan &q, const float *v, const void *x, bool transposed, int dtype, void *d, int C, cudaStream_t s) {
+cudaError_t launch_lora_rows(const LoraPlan &q, const void *x, const void *A, const void *B, int dtype, const void *base, void *out, float *v, int N, int K,
+                             cudaStream_t s) {
+    using namespace lora;
+    const __nv_bfloat16 *b16 = static_cast<const __nv_bfloat16 *>(B);
+    const cudaError_t e = launch_dependent(shrink_row_kernel, dim3((unsigned)q.T, (unsigned)(q.r / 8)), 256, 0, 1, s, params(q, K),
+                                           static_cast<const __nv_bfloat16 *>(x), static_cast<const __nv_bfloat16 *>(A), v);
+    if (e != cudaSuccess) return e;
+    const dim3 grid((unsigned)q.T, (unsigned)((N + 255) / 256));
+    if (dtype == ZFFN_DT_BF16)
+        return launch_dependent(expand_row_kernel<__nv_bfloat16>, grid, 128, 0, 1, s, params(q, N), v, b16, static_cast<const __nv_bfloat16 *>(base),
+                                static_cast<__nv_bfloat16 *>(out));
+    return launch_dependent(expand_row_kernel<float>, grid, 128, 0, 1, s, params(q, N), v, b16, static_cast<const float *>(base), static_cast<float *>(out));
+}
+
+cudaError_t launch_lora_outer(const LoraPlan &q, const void *v16, const void *x, bool transposed, int dtype, void *d, int C, cudaStream_t s) {
     using namespace lora;
     if (!encode_fn()) return cudaErrorNotSupported;
-    return q.r <= 80 ? outer<false>(q, v, x, transposed, dtype, d, C, s) : outer<true>(q, v, x, transposed, dtype, d, C, s);
+    return q.r <= 80 ? outer<false>(q, v16, x, transposed, dtype, d, C, s) : outer<true>(q, v16, x, transposed, dtype, d, C, s);
 }
 
 }  // namespace zffn

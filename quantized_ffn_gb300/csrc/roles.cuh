@@ -57,6 +57,12 @@ __device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, volatil
     return true;
 }
 
+// The same for a full warp, whose lanes all ask (one lane's answer would have to be passed on,
+// which the stages wait for).
+__device__ __forceinline__ bool bar_wait_warp(uint64_t *bar, uint32_t parity, volatile int *abort, int *err) {
+    return __all_sync(0xffffffffu, bar_wait(bar, parity, abort, err));
+}
+
 // The driver's encoder of tensor maps, looked up once (nullptr without one).
 inline PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {

@@ -82,8 +82,9 @@ def load() -> ctypes.CDLL:
                 "zffn_bf16_matmul_grad_w": ([P, P, P, I32, P, I32, I32, I32, I32, P], I32),
                 "zffn_swiglu": ([I32, P, P, I64, I64, P], I32),
                 "zffn_swiglu_grad": ([I32, P, P, P, I64, I64, P], I32),
-                "zffn_lora_add": ([P, P, P, P, P, P, P, I32, P, P, P, I32, I32, I32, I32, I32, P], I32),
-                "zffn_lora_grad": ([P, P, P, P, P, P, P, P, P, I32, P, P, I32, P, P, P, I32, I32, I32, I32, I32, P],
+                "zffn_lora_work_bytes": ([I32, I32, I32], ctypes.c_size_t),
+                "zffn_lora_add": ([P, P, P, P, P, P, P, I32, P, P, P, P, I32, I32, I32, I32, I32, P], I32),
+                "zffn_lora_grad": ([P, P, P, P, P, P, P, P, P, I32, P, P, I32, P, P, P, P, I32, I32, I32, I32, I32, P],
                                    I32),
                 "zffn_rmsnorm_bf16": ([P, P, ctypes.c_float, P, I32, I32, P], I32),
                 "zffn_swiglu_q4k_prenorm_residual": ([P, P, ctypes.c_float, P, P, P, I32, I32, I32, P],
@@ -323,7 +324,7 @@ _native_module = None
 _NATIVE_CALLS = ("zffn_fp8_quantize", "zffn_fp8_dequant", "zffn_fp8_matmul", "zffn_fp8_experts", "zffn_moe_sort",
                  "zffn_moe_dispatch", "zffn_moe_combine", "zffn_moe_combine_grad", "zffn_moe_swiglu_fp8",
                  "zffn_bf16_matmul", "zffn_bf16_matmul_grad_w", "zffn_swiglu", "zffn_swiglu_grad", "zffn_lora_add",
-                 "zffn_lora_grad")
+                 "zffn_lora_grad", "zffn_lora_work_bytes")
 
 
 def _fail(status: int, what: str):

@@ -45,30 +45,36 @@ def test_swiglu_refuses(lib, args):
         assert lib.zffn_swiglu_grad(dt, gu, F, F, rows, i, None) == BAD
 
 
-LORA = dict(dy=F, x=F, v=F, A=F, B=F, s=F, rs=F, sr=F, off=F, dt=0, base=F, out=F, wdt=0, dA=F, dB=F, dv=F, T=4, N=64, K=256, r=16, L=3)
-SHARED = ([{k: None} for k in ("x", "A", "B", "rs", "sr", "off", "out", "v")] +
+LORA = dict(dy=F, x=F, v=F, A=F, B=F, s=F, rs=F, sr=F, off=F, dt=0, base=F, out=F, wdt=0, dA=F, dB=F, dv=F, work=F, T=400, N=64, K=256, r=16, L=3)
+SHARED = ([{k: None} for k in ("x", "A", "B", "rs", "sr", "off", "out", "v", "work")] +
           [dict(dt=2), dict(T=0), dict(T=(1 << 24) + 1), dict(N=60), dict(N=0), dict(N=65544), dict(K=4), dict(K=65544), dict(r=0), dict(r=12),
-           dict(r=136), dict(L=0), dict(L=4097), dict(x=A8), dict(A=A8), dict(B=A8), dict(base=A8), dict(out=A8), dict(v=A8), dict(s=A2), dict(rs=A2),
+           dict(r=136), dict(L=0), dict(L=4097), dict(x=A8), dict(A=A8), dict(B=A8), dict(base=A8), dict(out=A8), dict(v=A8), dict(work=A8), dict(s=A2), dict(rs=A2),
            dict(sr=A2), dict(off=A2)])
 
 
 @pytest.mark.parametrize("bad", SHARED)
 def test_adapters_refuse(lib, bad):
     v = {**LORA, **bad}
-    assert lib.zffn_lora_add(*(v[k] for k in ("x", "A", "B", "s", "rs", "sr", "off", "dt", "base", "out", "v", "T", "N", "K", "r", "L")), None) == BAD
+    assert lib.zffn_lora_add(*(v[k] for k in ("x", "A", "B", "s", "rs", "sr", "off", "dt", "base", "out", "v", "work", "T", "N", "K", "r", "L")), None) == BAD
 
 
 @pytest.mark.parametrize("bad", SHARED + [{k: None} for k in ("dy", "dA", "dB", "dv")] + [dict(wdt=3), dict(dy=A8), dict(dA=A8), dict(dB=A8), dict(dv=A8)])
 def test_adapters_gradients_refuse(lib, bad):
     v = {**LORA, **bad}
-    keys = ("dy", "x", "v", "A", "B", "s", "rs", "sr", "off", "dt", "base", "out", "wdt", "dA", "dB", "dv", "T", "N", "K", "r", "L")
+    keys = ("dy", "x", "v", "A", "B", "s", "rs", "sr", "off", "dt", "base", "out", "wdt", "dA", "dB", "dv", "work", "T", "N", "K", "r", "L")
     assert lib.zffn_lora_grad(*(v[k] for k in keys), None) == BAD
+
+
+def test_work_bytes(lib):
+    assert lib.zffn_lora_work_bytes(400, 24, 0) == 400 * 6 * 32 and lib.zffn_lora_work_bytes(400, 24, 1) == 2 * 400 * 6 * 32
+    assert lib.zffn_lora_work_bytes(1, 16, 0) == 0 and lib.zffn_lora_work_bytes(1, 16, 1) == 2 * 6 * 16      # (row by row)
+    assert all(lib.zffn_lora_work_bytes(*bad, 1) == 0 for bad in ((0, 16), (4, 12), (4, 136), (1 << 25, 16)))
 
 
 def test_reason_is_given(lib):
     assert lib.zffn_bf16_matmul(F, F, None, 1, 0, F, 4, 100, 256, 1, None) == BAD
     assert b"N must be a multiple of 8" in lib.zffn_last_error()
-    assert lib.zffn_lora_add(F, F, F, None, F, F, F, 0, None, F, F, 4, 64, 256, 20, 1, None) == BAD
+    assert lib.zffn_lora_add(F, F, F, None, F, F, F, 0, None, F, F, F, 4, 64, 256, 20, 1, None) == BAD
     assert b"r must be a multiple of 8" in lib.zffn_last_error()
 
 
