@@ -9,7 +9,7 @@
 //
 // Tensor cores take bf16, and v is fp32: it goes as the sum of three bf16 pieces of 8
 // bits each, which is exact, so that v is not rounded between the products.  Shrink writes
-// them beside v, [T][3][up16(r)], so that expand and outer load them by TMA: split in the
+// them beside v, [T][3 up16(r), to the next 64], so that expand and outer load them by TMA: split in the
 // blocks that multiply them, once for each tile of columns, they were outer's bound (4096
 // rows of r = 32: 62 us for both outer products).
 #include <atomic>
@@ -55,6 +55,9 @@ __device__ __forceinline__ void put_pieces(__nv_bfloat16 *row, int r16, int c, f
         *reinterpret_cast<uint2 *>(row + k * r16 + c) = make_uint2(high_halves(a[0][k], a[1][k]), high_halves(a[2][k], a[3][k]));
 }
 __host__ __device__ constexpr int up16(int r) { return (r + 15) / 16 * 16; }
+// Values of a row of pieces: whole boxes of 64, so that one copy takes them all (what is past
+// the third piece is neither written nor used).
+__host__ __device__ constexpr int pieces_pitch(int r) { return (3 * up16(r) + 63) / 64 * 64; }
 
 struct Params {
     const int32_t *row_slot, *slot_row, *offsets;
@@ -90,7 +93,8 @@ __global__ void __launch_bounds__(S_THREADS) shrink_kernel(const __grid_constant
     asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(split));
     const uint32_t rank = cluster_ctarank();
     const int wb = s_w_bytes(p.r, MN), stage = 16384 + wb;
-    float *part = reinterpret_cast<float *>(smem);           // sums [rank][row / split][r], once the stages are idle
+    float *part = reinterpret_cast<float *>(smem);           // sums [rank][row / split][r + 4], once the stages are idle
+    const int pr = p.r + 4;                                  // (rows spread over the banks)
     uint64_t *s_full = reinterpret_cast<uint64_t *>(smem + S_NS * stage);
     uint64_t *s_empty = s_full + S_NS, *t_full = s_empty + S_NS;
     int *info = reinterpret_cast<int *>(t_full + 1);         // abort, TMEM base
@@ -234,8 +238,8 @@ __global__ void __launch_bounds__(S_THREADS) shrink_kernel(const __grid_constant
         const uint32_t from = tmem + ((uint32_t)(warp * 32) << 16);
         const int per = 128 / split, row = tid;
         float *to = v + (int64_t)(wk.row0 + row) * p.r;
-        __nv_bfloat16 *to16 = v16 + (int64_t)(wk.row0 + row) * 3 * r16;
-        const uint32_t send = split > 1 ? mapa_shared(smem_u32(part + (rank * per + row % per) * p.r), row / per) : 0;
+        __nv_bfloat16 *to16 = v16 + (int64_t)(wk.row0 + row) * pieces_pitch(p.r);
+        const uint32_t send = split > 1 ? mapa_shared(smem_u32(part + (rank * per + row % per) * pr), row / per) : 0;
         for (int c = 0; c < p.r; c += 16) {
             uint32_t d[16];
             if (some) {
@@ -273,15 +277,15 @@ __global__ void __launch_bounds__(S_THREADS) shrink_kernel(const __grid_constant
                 if (row >= wk.rows) break;
                 float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                 if (c < p.r) {
-                    f = *reinterpret_cast<const float4 *>(part + lrow * p.r + c);
+                    f = *reinterpret_cast<const float4 *>(part + lrow * pr + c);
                     for (uint32_t k = 1; k < split; ++k) {
-                        const float4 g = *reinterpret_cast<const float4 *>(part + (k * per + lrow) * p.r + c);
+                        const float4 g = *reinterpret_cast<const float4 *>(part + (k * per + lrow) * pr + c);
                         f.x += g.x; f.y += g.y; f.z += g.z; f.w += g.w;
                     }
                     f.x *= scale; f.y *= scale; f.z *= scale; f.w *= scale;
                     *reinterpret_cast<float4 *>(v + (int64_t)(wk.row0 + row) * p.r + c) = f;
                 }
-                if (some) put_pieces(v16 + (int64_t)(wk.row0 + row) * 3 * r16, r16, c, f);
+                if (some) put_pieces(v16 + (int64_t)(wk.row0 + row) * pieces_pitch(p.r), r16, c, f);
             }
         }
     }
@@ -292,7 +296,7 @@ __global__ void __launch_bounds__(S_THREADS) shrink_kernel(const __grid_constant
             const int lrow = p.by_quads.div(i), row = rank * per + lrow, c = (i - lrow * quads) * 4;
             if (row >= wk.rows) break;
             const float4 f = c < p.r ? __ldcg(reinterpret_cast<const float4 *>(other + (int64_t)(wk.row0 + row) * p.r + c)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            put_pieces(other16 + (int64_t)(wk.row0 + row) * 3 * r16, r16, c, f);
+            put_pieces(other16 + (int64_t)(wk.row0 + row) * pieces_pitch(p.r), r16, c, f);
         }
     }
     if (warp == 5) {
@@ -303,15 +307,16 @@ __global__ void __launch_bounds__(S_THREADS) shrink_kernel(const __grid_constant
 
 // ---------------------------------------------------------------------------
 // Expand on the tensor cores: 128 sorted rows times TN columns of out.  A block keeps one
-// row tile's v (its three pieces) and takes every G-th tile of the columns.  The sums go
-// through shared memory, so that a warp adds a row's base and writes it with its lanes
-// side by side; base is asked for a tile ahead, and it and W before the grid that writes v
-// has ended.
+// row tile's pieces of v and takes every G-th tile of the columns.  base's rows come to
+// shared memory as boxes of 32 rows x 128 bytes, NB tiles of them in turn, the sums are added
+// there and the boxes leave: by TMA where the tile's tokens follow one another, else by
+// 16-byte copies and stores.  (Loads to registers pass through L1, which is 28 KB beside this
+// kernel's shared memory: no more than that was on its way, and 2048 x 11008 took 38 us.)
+// base and W are asked for before the grid that writes v has ended.
 //
-// Roles: warps 0 .. 7 the rows (16 each), warp 8 loads W by TMA and issues the MMAs, warps 9
-// .. 11 copy base to out for tokens of no adapter.  (With 16 warps of 8 rows a thread has 96
-// registers: what it spilled went through L2, beside 213 KB of shared memory, and 2048 x 11008
-// took 39 us instead of EXPAND_US.)
+// Roles: warps 0 .. 7 take 32 rows and half of the columns each, with boxes of their own;
+// warp 8 loads v and W and issues the MMAs, warps 9 .. 11 copy base to out for tokens of no
+// adapter.
 // ---------------------------------------------------------------------------
 constexpr int E_WARPS = 8, E_THREADS = (E_WARPS + 4) * 32;
 
@@ -321,23 +326,28 @@ struct ExpandCfg {
     static constexpr bool MN = MN_;
     static constexpr int V_BYTES = 3 * BOXES * 16384;        // the pieces
     static constexpr int W_BYTES = BOXES * TN * 128;
-    static constexpr int PITCH = TN + 4;                     // floats (spreads the rows over the banks)
+    static constexpr int PER = 128 / ELEM;                   // columns of a box
+    static constexpr int OWN = TN / 2 / PER;                 // boxes of a warp and tile
+    static constexpr int TILE = 128 * TN * ELEM;
+    static constexpr int NB = (224 * 1024 - V_BYTES - W_BYTES) / TILE > 4 ? 4 : (224 * 1024 - V_BYTES - W_BYTES) / TILE;
+    static_assert(NB >= 2, "one tile comes while another leaves");
+    static constexpr int AHEAD = NB > 2 ? NB - 2 : 1;        // tiles that base is asked for ahead; the others' leave
     static constexpr int OFF_W = V_BYTES;
-    static constexpr int OFF_SUMS = OFF_W + W_BYTES;
-    static constexpr int OFF_BAR = OFF_SUMS + 128 * PITCH * 4;
-    static constexpr int SMEM = 1024 + OFF_BAR + 8 * 8 + 8;
+    static constexpr int OFF_BOX = OFF_W + W_BYTES;
+    static constexpr int OFF_BAR = OFF_BOX + NB * TILE;
+    static constexpr int SMEM = 1024 + OFF_BAR + (7 + E_WARPS * NB) * 8 + 8;
     static constexpr int TMEM_COLS = 2 * TN;
 };
 
 template <class C>
-__global__ void __launch_bounds__(E_THREADS, 1) expand_kernel(const __grid_constant__ CUtensorMap vm, const __grid_constant__ CUtensorMap w, const Params p,
-                                                              const void *base, void *out, int sms, int G) {
+__global__ void __launch_bounds__(E_THREADS, 1) expand_kernel(const __grid_constant__ CUtensorMap vm, const __grid_constant__ CUtensorMap w,
+                                                              const __grid_constant__ CUtensorMap bm, const __grid_constant__ CUtensorMap om,
+                                                              const Params p, const void *base, void *out, int sms, int G) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    float *sums = reinterpret_cast<float *>(smem + C::OFF_SUMS);
     uint64_t *w_full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
-    uint64_t *w_empty = w_full + 1, *t_full = w_full + 2, *t_empty = w_full + 4, *v_full = w_full + 6;
-    int *info = reinterpret_cast<int *>(w_full + 8);         // abort, TMEM base
+    uint64_t *w_empty = w_full + 1, *t_full = w_full + 2, *t_empty = w_full + 4, *v_full = w_full + 6, *b_full = w_full + 7;
+    int *info = reinterpret_cast<int *>(b_full + E_WARPS * C::NB);   // abort, TMEM base
     volatile int *abort_flag = info;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
     const int r16 = up16(p.r);
@@ -347,11 +357,14 @@ __global__ void __launch_bounds__(E_THREADS, 1) expand_kernel(const __grid_const
         mbar_init(w_empty, 1);
         mbar_init(v_full, 1);
         for (int i = 0; i < 2; ++i) { mbar_init(&t_full[i], 1); mbar_init(&t_empty[i], E_WARPS); }
+        for (int i = 0; i < E_WARPS * C::NB; ++i) mbar_init(&b_full[i], 1);
         fence_mbarrier_init();
     }
     if (warp == E_WARPS && lane == 0) {
         prefetch_tensormap(&vm);
         prefetch_tensormap(&w);
+        prefetch_tensormap(&om);
+        if (base) prefetch_tensormap(&bm);
     }
     if (warp == E_WARPS) {
         tmem_alloc(reinterpret_cast<uint32_t *>(info + 1), C::TMEM_COLS);
@@ -372,22 +385,45 @@ __global__ void __launch_bounds__(E_THREADS, 1) expand_kernel(const __grid_const
     const bool have = wk.get();
     const int n_tiles = (p.C + C::TN - 1) / C::TN, g = blockIdx.x % G;
     const bool any = have && g < n_tiles;
-
-    // warps 0 .. 7: lane i holds the token of row 16 warp + i; a lane has OWN columns of each
-    // row from OWN lane on
-    constexpr int ROWS = 128 / E_WARPS, OWN = C::TN / 32;
-    using Part = std::conditional_t<OWN * C::ELEM == 8, uint2, uint4>;
-    int token = -1;
-    if (any && warp < E_WARPS && lane < ROWS && warp * ROWS + lane < wk.rows) token = __ldcg(p.row_slot + wk.row0 + warp * ROWS + lane);
-    if ((unsigned)token >= (unsigned)p.T) token = -1;
-    Part old[ROWS];
     const int64_t pitch = (int64_t)p.C * C::ELEM;
-    const uint8_t *from = static_cast<const uint8_t *>(base) + lane * OWN * C::ELEM;
-    uint8_t *to = static_cast<uint8_t *>(out) + lane * OWN * C::ELEM;
-    auto ask = [&](int i, int nt) {    // base's part of row i in tile nt
-        const int t = __shfl_sync(0xffffffffu, token, i);
-        old[i] = Part{};
-        if (base && t >= 0 && nt * C::TN + lane * OWN < p.C) old[i] = __ldcg(reinterpret_cast<const Part *>(from + t * pitch + nt * (C::TN * C::ELEM)));
+
+    // warps 0 .. 7: lane i holds the token of its i-th row, -1 for none
+    const int quarter = warp & 3, half = warp >> 2, left = wk.rows - quarter * 32;
+    const bool mine = any && warp < E_WARPS && left > 0;
+    int token = -1;
+    bool packed = false;
+    if (mine) {
+        if (lane < left) token = __ldcg(p.row_slot + wk.row0 + quarter * 32 + lane);
+        if ((unsigned)token >= (unsigned)p.T) token = -1;
+        const int t0 = __shfl_sync(0xffffffffu, token, 0);
+        packed = __all_sync(0xffffffffu, lane >= left || token == t0 + lane) && t0 >= 0;
+    }
+    auto box = [&](int b, int x) { return smem + C::OFF_BOX + b * C::TILE + (warp * C::OWN + x) * 4096; };
+    auto column = [&](int nt, int x) { return nt * C::TN + half * (C::TN / 2) + x * C::PER; };
+    auto place = [&](const void *of, int t, int col, int chunk) {
+        return reinterpret_cast<uint4 *>(static_cast<uint8_t *>(const_cast<void *>(of)) + t * pitch + (int64_t)col * C::ELEM + chunk * 16);
+    };
+    auto chunks = [&](int col) { return min(8, (p.C - col) * C::ELEM / 16); };   // 16-byte columns of a box that are out's
+    auto ask = [&](int nt, int b) {    // base's part of tile nt into buffers b
+        if (!base) return;
+        if (packed) {
+            if (lane == 0) {
+                uint64_t *bar = &b_full[warp * C::NB + b];
+                mbar_arrive_expect_tx(bar, C::OWN * 4096);
+                for (int x = 0; x < C::OWN; ++x) tma_load_2d(box(b, x), &bm, bar, column(nt, x), token);
+            }
+            __syncwarp();
+            return;
+        }
+        for (int x = 0; x < C::OWN; ++x) {
+            const int col = column(nt, x), n = chunks(col);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int r = i * 4 + (lane >> 3), t = __shfl_sync(0xffffffffu, token, r);
+                if (t >= 0 && (lane & 7) < n)
+                    copy16(smem_u32(box(b, x)) + r * 128 + (((lane & 7) ^ (r & 7)) << 4), place(base, t, col, lane & 7), true);
+            }
+        }
     };
     auto load_w = [&](int nt) {
         if constexpr (C::MN) {
@@ -399,99 +435,110 @@ __global__ void __launch_bounds__(E_THREADS, 1) expand_kernel(const __grid_const
             for (int b = 0; b < boxes; ++b) tma_load_3d(smem + C::OFF_W + b * C::TN * 128, &w, w_full, b * 64, nt * C::TN, wk.e);
         }
     };
-    if (any && warp < E_WARPS) {
-#pragma unroll
-        for (int i = 0; i < ROWS; ++i) ask(i, g);
+    if (mine) {
+        for (int i = 0; i < C::AHEAD; ++i) {
+            if (g + i * G < n_tiles) ask(g + i * G, i);
+            copy_commit();
+        }
     } else if (any && warp == E_WARPS && lane == 0) {
         load_w(g);
     }
     grid_wait();
     grid_launch_dependents();
+
     if (any && warp < E_WARPS) {
-        // (a quarter of the warps to 32 rows in tensor memory, SHARE columns each)
-        constexpr int SHARE = C::TN / (E_WARPS / 4);
-        const int quarter = warp & 3, c0 = (warp >> 2) * SHARE;
-        // A lane's 4 or 8 columns are read as one or two float4s: with 8 the first of all lanes
-        // lie before the second ones.
-        auto slot = [](int c) { return OWN == 8 ? (c >> 2 & 1) * (C::TN / 2) + (c >> 3) * 4 : c; };
-        float *mine = sums + (quarter * 32 + lane) * C::PITCH;
-        int i = 0;
+        int i = 0, b = 0;
+        uint32_t phases = 0;
+        bool ok = true;
         for (int nt = g; nt < n_tiles; nt += G, ++i) {
-            const int b = i & 1;
-            // (a warp that gives up still meets the others at the barriers)
-            const bool ok = bar_wait_warp(&t_full[b], (i >> 1) & 1, abort_flag, p.err);
+            const int acc = i & 1;
+            if (mine) {
+                // the tile before (NB > 2: the one before that) has left its buffers: the base
+                // AHEAD tiles on goes there
+                const int next = nt + C::AHEAD * G;
+                if (lane == 0) bulk_wait_group_read<(C::NB > 2 ? 1 : 0)>();
+                __syncwarp();
+                if (next < n_tiles) ask(next, (b + C::AHEAD) % C::NB);
+                copy_commit();
+            }
+            ok = bar_wait_warp(&t_full[acc], (i >> 1) & 1, abort_flag, p.err);
+            if (mine && base) {
+                if (packed) ok = ok && bar_wait_warp(&b_full[warp * C::NB + b], (phases >> b) & 1, abort_flag, p.err);
+                else copy_wait<C::AHEAD>();
+                phases ^= 1u << b;
+                __syncwarp();
+            }
+            if (!ok) break;
             tc_fence_after();
-            if (ok) {
-                const uint32_t acc = tmem + b * C::TN + c0 + ((uint32_t)(quarter * 32) << 16);
-#pragma unroll 1
-                for (int c = 0; c < SHARE; c += 32) {
+            if (mine) {
+                const uint32_t from = tmem + acc * C::TN + half * (C::TN / 2) + ((uint32_t)(quarter * 32) << 16);
+#pragma unroll
+                for (int c = 0; c < C::TN / 2; c += 32) {
                     uint32_t d[32];
-                    tmem_ld_32x32b_x32(acc + c, d);
+                    tmem_ld_32x32b_x32(from + c, d);
+                    uint8_t *row = box(b, c / C::PER) + lane * 128;
+                    const int first = c % C::PER * C::ELEM / 16;
+                    auto at = [&](int j) { return reinterpret_cast<uint4 *>(row + (((first + j) ^ (lane & 7)) << 4)); };
+                    uint4 old[2 * C::ELEM];
+#pragma unroll
+                    for (int j = 0; j < 2 * C::ELEM; ++j) old[j] = base ? *at(j) : make_uint4(0, 0, 0, 0);
                     tmem_ld_wait(d);
 #pragma unroll
-                    for (int j = 0; j < 32; j += 4) *reinterpret_cast<uint4 *>(mine + slot(c0 + c + j)) = make_uint4(d[j], d[j + 1], d[j + 2], d[j + 3]);
+                    for (int j = 0; j < 2 * C::ELEM; ++j) {
+                        const uint4 o = old[j];
+                        if constexpr (C::ELEM == 2) {
+                            auto add = [&](uint32_t two, int k) {
+                                const __nv_bfloat162 v = __floats2bfloat162_rn(lo_f32(two) + __uint_as_float(d[k]), hi_f32(two) + __uint_as_float(d[k + 1]));
+                                return *reinterpret_cast<const uint32_t *>(&v);
+                            };
+                            *at(j) = make_uint4(add(o.x, 8 * j), add(o.y, 8 * j + 2), add(o.z, 8 * j + 4), add(o.w, 8 * j + 6));
+                        } else {
+                            auto add = [&](uint32_t one, int k) { return __float_as_uint(__uint_as_float(one) + __uint_as_float(d[k])); };
+                            *at(j) = make_uint4(add(o.x, 4 * j), add(o.y, 4 * j + 1), add(o.z, 4 * j + 2), add(o.w, 4 * j + 3));
+                        }
+                    }
                 }
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&t_empty[b]);
-            named_barrier(1, E_WARPS * 32);
-            const bool there = ok && nt * C::TN + lane * OWN < p.C;
-            const bool more = base && (nt + G) * C::TN + lane * OWN < p.C;   // (a lane's part of the next tile)
-            constexpr int TOGETHER = 4;                      // rows whose latencies overlap
-#pragma unroll
-            for (int k0 = 0; k0 < ROWS; k0 += TOGETHER) {
-                float4 f[TOGETHER][OWN / 4];
-                Part n[TOGETHER];
-                int64_t at[TOGETHER];
-#pragma unroll
-                for (int k = 0; k < TOGETHER; ++k) {
-#pragma unroll
-                    for (int h = 0; h < OWN / 4; ++h)
-                        f[k][h] = *reinterpret_cast<const float4 *>(sums + (warp * ROWS + k0 + k) * C::PITCH + h * (C::TN / 2) + lane * 4);
-                    const int t = __shfl_sync(0xffffffffu, token, k0 + k);
-                    at[k] = t < 0 ? -1 : t * pitch + nt * (C::TN * C::ELEM);
+            if (lane == 0) mbar_arrive(&t_empty[acc]);
+            if (mine && packed && left >= 32) {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    for (int x = 0; x < C::OWN; ++x)
+                        if (column(nt, x) < p.C) tma_store_2d(&om, smem_u32(box(b, x)), column(nt, x), token);
+                    bulk_commit_group();
                 }
+            } else if (mine) {
+                for (int x = 0; x < C::OWN; ++x) {
+                    const int col = column(nt, x), n = chunks(col);
 #pragma unroll
-                for (int k = 0; k < TOGETHER; ++k) {
-                    const Part o = old[k0 + k];
-                    if constexpr (C::ELEM == 2) {
-                        auto add = [](uint32_t two, float a, float b) {
-                            const __nv_bfloat162 s = __floats2bfloat162_rn(lo_f32(two) + a, hi_f32(two) + b);
-                            return *reinterpret_cast<const uint32_t *>(&s);
-                        };
-                        n[k].x = add(o.x, f[k][0].x, f[k][0].y);
-                        n[k].y = add(o.y, f[k][0].z, f[k][0].w);
-                        if constexpr (OWN == 8) {
-                            n[k].z = add(o.z, f[k][1].x, f[k][1].y);
-                            n[k].w = add(o.w, f[k][1].z, f[k][1].w);
-                        }
-                    } else {
-                        n[k] = make_uint4(__float_as_uint(__uint_as_float(o.x) + f[k][0].x), __float_as_uint(__uint_as_float(o.y) + f[k][0].y),
-                                          __float_as_uint(__uint_as_float(o.z) + f[k][0].z), __float_as_uint(__uint_as_float(o.w) + f[k][0].w));
+                    for (int k = 0; k < 8; ++k) {
+                        const int r = k * 4 + (lane >> 3), t = __shfl_sync(0xffffffffu, token, r);
+                        if (t >= 0 && (lane & 7) < n)
+                            *place(out, t, col, lane & 7) = *reinterpret_cast<const uint4 *>(box(b, x) + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
                     }
                 }
-#pragma unroll
-                for (int k = 0; k < TOGETHER; ++k)
-                    if (there && at[k] >= 0) *reinterpret_cast<Part *>(to + at[k]) = n[k];
-                if (more) {
-#pragma unroll
-                    for (int k = 0; k < TOGETHER; ++k) {
-                        old[k0 + k] = Part{};
-                        if (at[k] >= 0) old[k0 + k] = __ldcg(reinterpret_cast<const Part *>(from + at[k] + G * (C::TN * C::ELEM)));
-                    }
-                }
+                if (packed) fence_proxy_async_smem();        // (the next base comes by TMA)
+                __syncwarp();
             }
-            named_barrier(1, E_WARPS * 32);
+            b = b + 1 == C::NB ? 0 : b + 1;
         }
+        if (!ok && mine && base && packed && lane == 0)      // (a launch that gave up: no copy is left on its way)
+            for (int k = i; k <= i + C::AHEAD; ++k)
+                if (g + k * G < n_tiles) mbar_wait(&b_full[warp * C::NB + k % C::NB], (k / C::NB) & 1, nullptr, p.err);
+        copy_wait<0>();
+        if (lane == 0) bulk_wait_group_all();
+        __syncwarp();
     } else if (any && warp == E_WARPS) {
         // v's pieces, K-major, the three one after another
         const uint32_t idesc = idesc_bf16_f32(128, C::TN, false, C::MN), sv = smem_u32(smem), sw = sv + C::OFF_W;
         const int steps = r16 / 16;
         if (lane == 0) {
-            const int boxes = (3 * r16 + 63) / 64;
+            const int boxes = pieces_pitch(p.r) / 64;
             mbar_arrive_expect_tx(v_full, boxes * 16384);
-            for (int b = 0; b < boxes; ++b) tma_load_2d(smem + b * 16384, &vm, v_full, b * 64, wk.row0);
+            for (int x = 0; x < boxes; ++x) tma_load_2d(smem + x * 16384, &vm, v_full, x * 64, wk.row0);
         }
         __syncwarp();
         int i = 0;
@@ -633,7 +680,7 @@ __global__ void __launch_bounds__(O_THREADS, 1) outer_kernel(const __grid_consta
 
     if (warp == 0) {
         // ---- by TMA
-        const int boxes = (3 * r16 + 63) / 64;
+        const int boxes = pieces_pitch(p.r) / 64;
         uint32_t it = 0, asked = 0;                          // asked: the stages whose last fill was this warp's
         bool ok = true;
         for (; ok && wk.get(); wk.t += gridDim.x) {
@@ -661,7 +708,7 @@ __global__ void __launch_bounds__(O_THREADS, 1) outer_kernel(const __grid_consta
                         tma_load_2d(to, &xm, &s_full[s], wk.nt * 128, t0 + i * KB);
                         tma_load_2d(to + 8192, &xm, &s_full[s], wk.nt * 128 + 64, t0 + i * KB);
                     }
-                    for (int b = 0; b < boxes; ++b) tma_load_2d(to + 16384 + b * 8192, &vm, &s_full[s], b * 64, wk.row0 + i * KB);
+                    tma_load_3d(to + 16384, &vm, &s_full[s], 0, wk.row0 + i * KB, 0);
                 }
                 __syncwarp();
             }
@@ -715,7 +762,7 @@ __global__ void __launch_bounds__(O_THREADS, 1) outer_kernel(const __grid_consta
                         const int row = by_wide.div(q), c = q - row * wide;
                         const bool there = row < rows && (unsigned)__ldcg(slot + row) < (unsigned)p.T;
                         copy16(to + (c >> 3) * 8192 + row * 128 + (((c & 7) ^ (row & 7)) << 4),
-                               there ? v16 + (int64_t)(wk.row0 + i * KB + row) * 3 * r16 + c * 8 : v16, there);
+                               there ? v16 + (int64_t)(wk.row0 + i * KB + row) * pieces_pitch(p.r) + c * 8 : v16, there);
                     }
                 }
                 copy_commit();
@@ -973,20 +1020,21 @@ static cudaError_t shrink(const LoraPlan &q, const void *x, const void *w, float
 template <int ELEM, int TN, int BOXES, bool MN>
 static cudaError_t expand(const LoraPlan &q, const void *v16, const void *w, const void *base, void *out, int C, cudaStream_t s) {
     using Cfg = ExpandCfg<ELEM, TN, BOXES, MN>;
-    CUtensorMap rows, map;
-    if (!encode(&rows, v16, 2, 3 * up16(q.r), q.T, 1, 128, false)) return cudaErrorInvalidValue;
+    CUtensorMap rows, map, from{}, to;
+    if (!encode(&rows, v16, 2, pieces_pitch(q.r), q.T, 1, 128, false) || !encode(&to, out, ELEM, C, q.T, 1, 32, false)) return cudaErrorInvalidValue;
+    if (base && !encode(&from, base, ELEM, C, q.T, 1, 32, false)) return cudaErrorInvalidValue;
     if (!(MN ? encode(&map, w, 2, C, q.r, q.L, up16(q.r), true) : encode(&map, w, 2, q.r, C, q.L, Cfg::TN, true))) return cudaErrorInvalidValue;
     const int64_t tiles = row_tiles(q), sms = device_info().num_sms;
     const int64_t G = sms / tiles < 1 ? 1 : sms / tiles;
     const cudaError_t e = ensure_dynamic_smem((const void *)expand_kernel<Cfg>, Cfg::SMEM);
     if (e != cudaSuccess) return e;
-    return launch_dependent(expand_kernel<Cfg>, dim3((unsigned)(tiles > sms ? tiles : sms)), E_THREADS, Cfg::SMEM, 1, s, rows, map, params(q, C), base, out, (int)sms,
+    return launch_dependent(expand_kernel<Cfg>, dim3((unsigned)(tiles > sms ? tiles : sms)), E_THREADS, Cfg::SMEM, 1, s, rows, map, from, to, params(q, C), base, out, (int)sms,
                             (int)G);
 }
 template <bool MN>
 static cudaError_t expand(const LoraPlan &q, const void *v, const void *w, int dtype, const void *base, void *out, int C, cudaStream_t s) {
-    if (dtype == ZFFN_DT_BF16) return q.r <= 64 ? expand<2, 256, 1, MN>(q, v, w, base, out, C, s) : expand<2, 128, 2, MN>(q, v, w, base, out, C, s);
-    return q.r <= 64 ? expand<4, 128, 1, MN>(q, v, w, base, out, C, s) : expand<4, 128, 2, MN>(q, v, w, base, out, C, s);
+    if (dtype == ZFFN_DT_BF16) return q.r <= 64 ? expand<2, 128, 1, MN>(q, v, w, base, out, C, s) : expand<2, 128, 2, MN>(q, v, w, base, out, C, s);
+    return q.r <= 64 ? expand<4, 128, 1, MN>(q, v, w, base, out, C, s) : expand<4, 64, 2, MN>(q, v, w, base, out, C, s);
 }
 
 template <bool WIDE>
@@ -994,7 +1042,7 @@ static cudaError_t outer(const LoraPlan &q, const void *v16, const void *x, bool
     using Cfg = OuterCfg<WIDE>;
     CUtensorMap rows, map;
     const bool wide_x = C % 64 == 0;
-    if (!encode(&rows, x, 2, C, q.T, 1, KB, false, wide_x ? 2 : 0) || !encode(&map, v16, 2, 3 * up16(q.r), q.T, 1, KB, false)) return cudaErrorInvalidValue;
+    if (!encode(&rows, x, 2, C, q.T, 1, KB, false, wide_x ? 2 : 0) || !encode(&map, v16, 2, pieces_pitch(q.r), q.T, 1, KB, false, pieces_pitch(q.r) / 64)) return cudaErrorInvalidValue;
     const int n_tiles = (C + 127) / 128;
     const int64_t tiles = (int64_t)q.L * n_tiles, sms = device_info().num_sms;
     Params p = params(q, C);
@@ -1007,7 +1055,7 @@ static cudaError_t outer(const LoraPlan &q, const void *v16, const void *x, bool
 
 }  // namespace lora
 
-size_t lora_pieces_bytes(int T, int r) { return (size_t)T * 6 * lora::up16(r); }
+size_t lora_pieces_bytes(int T, int r) { return (size_t)T * 2 * lora::pieces_pitch(r); }
 bool lora_by_rows(int T, int r) { return lora::few(T, r); }
 
 cudaError_t launch_lora_shrink(const LoraPlan &q, const void *x, const void *w, bool transposed, float *v, void *v16, const float *other, void *other16,

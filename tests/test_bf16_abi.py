@@ -66,8 +66,8 @@ def test_adapters_gradients_refuse(lib, bad):
 
 
 def test_work_bytes(lib):
-    assert lib.zffn_lora_work_bytes(400, 24, 0) == 400 * 6 * 32 and lib.zffn_lora_work_bytes(400, 24, 1) == 2 * 400 * 6 * 32
-    assert lib.zffn_lora_work_bytes(1, 16, 0) == 0 and lib.zffn_lora_work_bytes(1, 16, 1) == 2 * 6 * 16      # (row by row)
+    assert lib.zffn_lora_work_bytes(400, 24, 0) == 400 * 2 * 128 and lib.zffn_lora_work_bytes(400, 24, 1) == 2 * 400 * 2 * 128
+    assert lib.zffn_lora_work_bytes(1, 16, 0) == 0 and lib.zffn_lora_work_bytes(1, 16, 1) == 2 * 2 * 64      # (row by row)
     assert all(lib.zffn_lora_work_bytes(*bad, 1) == 0 for bad in ((0, 16), (4, 12), (4, 136), (1 << 25, 16)))
 
 
