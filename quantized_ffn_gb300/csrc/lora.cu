@@ -31,6 +31,11 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool some)
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+// Shared memory to another rank's, completion counted on a barrier there.
+__device__ __forceinline__ void copy_to_rank(uint32_t dst, uint32_t src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "r"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
 __device__ __forceinline__ float lo_f32(uint32_t two) { return __uint_as_float(two << 16); }
 __device__ __forceinline__ float hi_f32(uint32_t two) { return __uint_as_float(two & 0xFFFF0000u); }
 // v = p[0] + p[1] + p[2], bf16 values in the high halves: v's bits cut after 8 and 16
@@ -81,7 +86,7 @@ constexpr int S_NS = 4, S_LAG = 3, S_THREADS = 192, S_MAX_SPLIT = 8;
 
 // W's bytes of a stage: K-major [r][64], or MN-major boxes [64][64]
 __host__ __device__ constexpr int s_w_bytes(int r, bool mn) { return mn ? (r + 63) / 64 * 8192 : up16(r) * 128; }
-static size_t s_smem(int r, bool mn) { return 1024 + (size_t)S_NS * (16384 + s_w_bytes(r, mn)) + (2 * S_NS + 1) * 8 + 8; }
+static size_t s_smem(int r, bool mn) { return 1024 + (size_t)S_NS * (16384 + s_w_bytes(r, mn)) + (2 * S_NS + 2) * 8 + 8; }
 
 template <bool MN>
 __global__ void __launch_bounds__(S_THREADS) shrink_kernel(const __grid_constant__ CUtensorMap xm, const __grid_constant__ CUtensorMap w, const Params p,
@@ -93,11 +98,11 @@ __global__ void __launch_bounds__(S_THREADS) shrink_kernel(const __grid_constant
     asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(split));
     const uint32_t rank = cluster_ctarank();
     const int wb = s_w_bytes(p.r, MN), stage = 16384 + wb;
-    float *part = reinterpret_cast<float *>(smem);           // sums [rank][row / split][r + 4], once the stages are idle
-    const int pr = p.r + 4;                                  // (rows spread over the banks)
+    // once the stages are idle: sums [rank][row / split][r] from every rank, and this one's own
+    float *part = reinterpret_cast<float *>(smem), *own = part + 128 * p.r;
     uint64_t *s_full = reinterpret_cast<uint64_t *>(smem + S_NS * stage);
-    uint64_t *s_empty = s_full + S_NS, *t_full = s_empty + S_NS;
-    int *info = reinterpret_cast<int *>(t_full + 1);         // abort, TMEM base
+    uint64_t *s_empty = s_full + S_NS, *t_full = s_empty + S_NS, *j_full = t_full + 1;
+    int *info = reinterpret_cast<int *>(j_full + 1);         // abort, TMEM base
     volatile int *abort_flag = info;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
     const int r16 = up16(p.r), cols = r16 <= 32 ? 32 : r16 <= 64 ? 64 : 128;
@@ -105,6 +110,8 @@ __global__ void __launch_bounds__(S_THREADS) shrink_kernel(const __grid_constant
         info[0] = 0;
         for (int i = 0; i < S_NS; ++i) { mbar_init(&s_full[i], 5); mbar_init(&s_empty[i], 1); }
         mbar_init(t_full, 1);
+        mbar_init(j_full, 1);
+        mbar_arrive_expect_tx(j_full, 128 * p.r * 4);
         fence_mbarrier_init();
     }
     if (warp == 4 && lane == 0) {
@@ -125,7 +132,9 @@ __global__ void __launch_bounds__(S_THREADS) shrink_kernel(const __grid_constant
     wk.start(p.offsets, p.T, p.L, 1, p.each, true, blockIdx.x / split);
     const bool have = wk.get(), some = have && wk.e < p.L;
     const int blocks = (p.C + KB - 1) / KB;
-    const int kb0 = blocks * rank / split, nkb = blocks * (rank + 1) / split - kb0;
+    // this rank's stages: every split-th, so that the ranks read neighbouring columns at a time
+    const int nkb = (blocks - (int)rank + (int)split - 1) / (int)split;
+    auto block_of = [&](int i) { return i * (int)split + (int)rank; };
     const float scale = some && p.scale ? __ldcg(p.scale + wk.e) : 1.0f;
 
     // the tile's tokens, 4 lane + j, and whether they follow one another
@@ -157,7 +166,7 @@ __global__ void __launch_bounds__(S_THREADS) shrink_kernel(const __grid_constant
                 if (lane == 0) mbar_arrive(&s_full[i % S_NS]);
             };
             for (int i = 0; i < nkb; ++i) {
-                const int s = i % S_NS, c = (kb0 + i) * KB;
+                const int s = i % S_NS, c = block_of(i) * KB;
                 if (i >= S_NS) ok = bar_wait_warp(&s_empty[s], ((i / S_NS) & 1) ^ 1, abort_flag, p.err);
                 if (!ok) break;
 #pragma unroll
@@ -186,11 +195,11 @@ __global__ void __launch_bounds__(S_THREADS) shrink_kernel(const __grid_constant
             uint8_t *to = smem + s * stage;
             if (lane == 0) {
                 mbar_arrive_expect_tx(&s_full[s], (packed ? 16384 : 0) + (MN ? wb : p.r * 128));
-                if (packed) tma_load_2d(to, &xm, &s_full[s], (kb0 + i) * KB, t0);
+                if (packed) tma_load_2d(to, &xm, &s_full[s], block_of(i) * KB, t0);
                 if constexpr (MN) {
-                    for (int b = 0; b * 64 < p.r; ++b) tma_load_3d(to + 16384 + b * 8192, &w, &s_full[s], b * 64, (kb0 + i) * KB, wk.e);
+                    for (int b = 0; b * 64 < p.r; ++b) tma_load_3d(to + 16384 + b * 8192, &w, &s_full[s], b * 64, block_of(i) * KB, wk.e);
                 } else {
-                    tma_load_3d(to + 16384, &w, &s_full[s], (kb0 + i) * KB, 0, wk.e);
+                    tma_load_3d(to + 16384, &w, &s_full[s], block_of(i) * KB, 0, wk.e);
                 }
             } else if (packed && lane < 5) {
                 mbar_arrive(&s_full[s]);   // (for the gathering warps)
@@ -210,7 +219,7 @@ __global__ void __launch_bounds__(S_THREADS) shrink_kernel(const __grid_constant
             if (!ok) break;
             tc_fence_after();
             const uint32_t sx = smem_u32(smem) + s * stage;
-            const int n = (min(KB, p.C - (kb0 + i) * KB) + 15) / 16;
+            const int n = (min(KB, p.C - block_of(i) * KB) + 15) / 16;
             const uint64_t xd = smem_desc_k_sw128(sx), wd = MN ? smem_desc_mn_sw128(sx + 16384, 8192) : smem_desc_k_sw128(sx + 16384);
             if (elect_one()) {
 #pragma unroll
@@ -234,12 +243,12 @@ __global__ void __launch_bounds__(S_THREADS) shrink_kernel(const __grid_constant
             bar_wait_warp(t_full, 0, abort_flag, p.err);
             tc_fence_after();
         }
-        if (split > 1) cluster_sync_all();                   // every block's stages are idle
         const uint32_t from = tmem + ((uint32_t)(warp * 32) << 16);
-        const int per = 128 / split, row = tid;
+        const int row = tid;
         float *to = v + (int64_t)(wk.row0 + row) * p.r;
         __nv_bfloat16 *to16 = v16 + (int64_t)(wk.row0 + row) * pieces_pitch(p.r);
-        const uint32_t send = split > 1 ? mapa_shared(smem_u32(part + (rank * per + row % per) * pr), row / per) : 0;
+        const bool join = some && split > 1;
+        if (join) cluster_sync_all();                        // every block's stages are idle
         for (int c = 0; c < p.r; c += 16) {
             uint32_t d[16];
             if (some) {
@@ -251,42 +260,51 @@ __global__ void __launch_bounds__(S_THREADS) shrink_kernel(const __grid_constant
             }
 #pragma unroll
             for (int j = 0; j < 16; j += 4) {
-                if (row >= wk.rows) continue;
                 float4 f = make_float4(__uint_as_float(d[j]), __uint_as_float(d[j + 1]), __uint_as_float(d[j + 2]), __uint_as_float(d[j + 3]));
-                if (split > 1) {
-                    if (c + j < p.r) st_cluster_f4(send + (c + j) * 4, f);
+                if (join) {
+                    if (c + j < p.r) *reinterpret_cast<float4 *>(own + row * p.r + c + j) = f;
                     continue;
                 }
+                if (row >= wk.rows) continue;
                 f.x *= scale; f.y *= scale; f.z *= scale; f.w *= scale;
                 if (c + j < p.r) *reinterpret_cast<float4 *>(to + c + j) = f;
                 else f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                 if (some) put_pieces(to16, r16, c + j, f);
             }
         }
+        if (join) {
+            // rows 128 / split * i and on to rank i (written by the lanes, 16 bytes each, they
+            // took 8000 clocks for r = 64)
+            fence_proxy_async_smem();
+            named_barrier(1, 128);
+            if (tid < (int)split) {
+                const uint32_t bytes = 128 / split * p.r * 4;
+                copy_to_rank(mapa_shared(smem_u32(part) + rank * bytes, tid), smem_u32(own) + tid * bytes, bytes, mapa_shared(smem_u32(j_full), tid));
+            }
+        }
         tc_fence_before();
-    } else if (split > 1) {
+    } else if (some && split > 1) {
         cluster_sync_all();
     }
     __syncthreads();
-    if (split > 1) {
-        cluster_sync_all();
-        if (have) {
-            const int per = 128 / split, quads = r16 / 4;
-            for (int i = tid; i < per * quads; i += S_THREADS) {
-                const int lrow = p.by_quads.div(i), row = rank * per + lrow, c = (i - lrow * quads) * 4;
-                if (row >= wk.rows) break;
-                float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                if (c < p.r) {
-                    f = *reinterpret_cast<const float4 *>(part + lrow * pr + c);
-                    for (uint32_t k = 1; k < split; ++k) {
-                        const float4 g = *reinterpret_cast<const float4 *>(part + (k * per + lrow) * pr + c);
-                        f.x += g.x; f.y += g.y; f.z += g.z; f.w += g.w;
-                    }
-                    f.x *= scale; f.y *= scale; f.z *= scale; f.w *= scale;
-                    *reinterpret_cast<float4 *>(v + (int64_t)(wk.row0 + row) * p.r + c) = f;
+    if (some && split > 1) {
+        volatile int never = 0;        // (the rows come also from a rank that gave up)
+        bar_wait_warp(j_full, 0, &never, p.err);
+        const int per = 128 / split, quads = r16 / 4;
+        for (int i = tid; i < per * quads; i += S_THREADS) {
+            const int lrow = p.by_quads.div(i), row = rank * per + lrow, c = (i - lrow * quads) * 4;
+            if (row >= wk.rows) break;
+            float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (c < p.r) {
+                f = *reinterpret_cast<const float4 *>(part + lrow * p.r + c);
+                for (uint32_t k = 1; k < split; ++k) {
+                    const float4 g = *reinterpret_cast<const float4 *>(part + (k * per + lrow) * p.r + c);
+                    f.x += g.x; f.y += g.y; f.z += g.z; f.w += g.w;
                 }
-                if (some) put_pieces(v16 + (int64_t)(wk.row0 + row) * pieces_pitch(p.r), r16, c, f);
+                f.x *= scale; f.y *= scale; f.z *= scale; f.w *= scale;
+                *reinterpret_cast<float4 *>(v + (int64_t)(wk.row0 + row) * p.r + c) = f;
             }
+            put_pieces(v16 + (int64_t)(wk.row0 + row) * pieces_pitch(p.r), r16, c, f);
         }
     }
     if (some && other) {
@@ -299,6 +317,7 @@ __global__ void __launch_bounds__(S_THREADS) shrink_kernel(const __grid_constant
             put_pieces(other16 + (int64_t)(wk.row0 + row) * pieces_pitch(p.r), r16, c, f);
         }
     }
+    if (some && split > 1) cluster_sync_all();               // (no block leaves while its rows are on their way)
     if (warp == 5) {
         tc_fence_after();
         tmem_dealloc(tmem, cols);
@@ -325,17 +344,17 @@ struct ExpandCfg {
     static constexpr int ELEM = ELEM_, TN = TN_, BOXES = BOXES_;   // BOXES: 64-wide boxes of r
     static constexpr bool MN = MN_;
     static constexpr int V_BYTES = 3 * BOXES * 16384;        // the pieces
-    static constexpr int W_BYTES = BOXES * TN * 128;
+    static constexpr int W_BYTES = BOXES * TN * 128;         // of a tile; two in turn
     static constexpr int PER = 128 / ELEM;                   // columns of a box
     static constexpr int OWN = TN / 2 / PER;                 // boxes of a warp and tile
     static constexpr int TILE = 128 * TN * ELEM;
-    static constexpr int NB = (224 * 1024 - V_BYTES - W_BYTES) / TILE > 4 ? 4 : (224 * 1024 - V_BYTES - W_BYTES) / TILE;
+    static constexpr int ROOM = (224 * 1024 - V_BYTES - 2 * W_BYTES) / TILE, NB = ROOM > 4 ? 4 : ROOM;
     static_assert(NB >= 2, "one tile comes while another leaves");
     static constexpr int AHEAD = NB > 2 ? NB - 2 : 1;        // tiles that base is asked for ahead; the others' leave
     static constexpr int OFF_W = V_BYTES;
-    static constexpr int OFF_BOX = OFF_W + W_BYTES;
+    static constexpr int OFF_BOX = OFF_W + 2 * W_BYTES;
     static constexpr int OFF_BAR = OFF_BOX + NB * TILE;
-    static constexpr int SMEM = 1024 + OFF_BAR + (7 + E_WARPS * NB) * 8 + 8;
+    static constexpr int SMEM = 1024 + OFF_BAR + (9 + E_WARPS * NB) * 8 + 8;
     static constexpr int TMEM_COLS = 2 * TN;
 };
 
@@ -346,17 +365,20 @@ __global__ void __launch_bounds__(E_THREADS, 1) expand_kernel(const __grid_const
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint64_t *w_full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
-    uint64_t *w_empty = w_full + 1, *t_full = w_full + 2, *t_empty = w_full + 4, *v_full = w_full + 6, *b_full = w_full + 7;
+    uint64_t *w_empty = w_full + 2, *t_full = w_full + 4, *t_empty = w_full + 6, *v_full = w_full + 8, *b_full = w_full + 9;
     int *info = reinterpret_cast<int *>(b_full + E_WARPS * C::NB);   // abort, TMEM base
     volatile int *abort_flag = info;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
     const int r16 = up16(p.r);
     if (tid == 0) {
         info[0] = 0;
-        mbar_init(w_full, 1);
-        mbar_init(w_empty, 1);
         mbar_init(v_full, 1);
-        for (int i = 0; i < 2; ++i) { mbar_init(&t_full[i], 1); mbar_init(&t_empty[i], E_WARPS); }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&w_full[i], 1);
+            mbar_init(&w_empty[i], 1);
+            mbar_init(&t_full[i], 1);
+            mbar_init(&t_empty[i], E_WARPS);
+        }
         for (int i = 0; i < E_WARPS * C::NB; ++i) mbar_init(&b_full[i], 1);
         fence_mbarrier_init();
     }
@@ -425,14 +447,15 @@ __global__ void __launch_bounds__(E_THREADS, 1) expand_kernel(const __grid_const
             }
         }
     };
-    auto load_w = [&](int nt) {
+    auto load_w = [&](int nt, int b) {
+        uint8_t *to = smem + C::OFF_W + b * C::W_BYTES;
         if constexpr (C::MN) {
-            mbar_arrive_expect_tx(w_full, C::TN / 64 * r16 * 128);
-            for (int b = 0; b < C::TN / 64; ++b) tma_load_3d(smem + C::OFF_W + b * r16 * 128, &w, w_full, nt * C::TN + b * 64, 0, wk.e);
+            mbar_arrive_expect_tx(&w_full[b], C::TN / 64 * r16 * 128);
+            for (int x = 0; x < C::TN / 64; ++x) tma_load_3d(to + x * r16 * 128, &w, &w_full[b], nt * C::TN + x * 64, 0, wk.e);
         } else {
             const int boxes = (p.r + 63) / 64;
-            mbar_arrive_expect_tx(w_full, boxes * C::TN * 128);
-            for (int b = 0; b < boxes; ++b) tma_load_3d(smem + C::OFF_W + b * C::TN * 128, &w, w_full, b * 64, nt * C::TN, wk.e);
+            mbar_arrive_expect_tx(&w_full[b], boxes * C::TN * 128);
+            for (int x = 0; x < boxes; ++x) tma_load_3d(to + x * C::TN * 128, &w, &w_full[b], x * 64, nt * C::TN, wk.e);
         }
     };
     if (mine) {
@@ -441,7 +464,8 @@ __global__ void __launch_bounds__(E_THREADS, 1) expand_kernel(const __grid_const
             copy_commit();
         }
     } else if (any && warp == E_WARPS && lane == 0) {
-        load_w(g);
+        load_w(g, 0);
+        if (g + G < n_tiles) load_w(g + G, 1);
     }
     grid_wait();
     grid_launch_dependents();
@@ -543,42 +567,43 @@ __global__ void __launch_bounds__(E_THREADS, 1) expand_kernel(const __grid_const
         __syncwarp();
         int i = 0;
         bool ok = bar_wait_warp(v_full, 0, abort_flag, p.err);
-        if (!ok) {                     // (no copy is left on its way)
-            mbar_wait(v_full, 0, nullptr, p.err);
-            mbar_wait(w_full, 0, nullptr, p.err);
-        }
         for (int nt = g; ok && nt < n_tiles; nt += G, ++i) {
             const int b = i & 1;
-            if (i > 0) {               // (W's tile before has been read)
-                ok = bar_wait_warp(w_empty, (i - 1) & 1, abort_flag, p.err);
-                if (!ok) break;
-                if (lane == 0) load_w(nt);
-                __syncwarp();
-            }
-            ok = bar_wait_warp(w_full, i & 1, abort_flag, p.err) &&
+            ok = bar_wait_warp(&w_full[b], (i >> 1) & 1, abort_flag, p.err) &&
                  (i < 2 || bar_wait_warp(&t_empty[b], ((i >> 1) & 1) ^ 1, abort_flag, p.err));
-            if (!ok) {                 // (no copy is left on its way)
-                mbar_wait(w_full, i & 1, nullptr, p.err);
-                break;
-            }
+            if (!ok) break;
             tc_fence_after();
             if (elect_one()) {
                 for (int k = 0; k < steps; ++k) {
-                    const uint64_t wd = C::MN ? smem_desc_mn_sw128(sw, r16 * 128) + k * k_step(true)
-                                              : smem_desc_k_sw128(sw + (k >> 2) * C::TN * 128) + (k & 3) * k_step(false);
+                    const uint32_t wb = sw + b * C::W_BYTES;
+                    const uint64_t wd = C::MN ? smem_desc_mn_sw128(wb, r16 * 128) + k * k_step(true)
+                                              : smem_desc_k_sw128(wb + (k >> 2) * C::TN * 128) + (k & 3) * k_step(false);
 #pragma unroll
                     for (int q = 0; q < 3; ++q) {
                         const int a = q * steps + k;
                         tc_mma_bf16(tmem + b * C::TN, smem_desc_k_sw128(sv + (a >> 2) * 16384) + (a & 3) * k_step(false), wd, idesc, (k | q) != 0);
                     }
                 }
-                tc_commit(w_empty);
+                tc_commit(&w_empty[b]);
                 tc_commit(&t_full[b]);
             }
             __syncwarp();
+            if (nt + 2 * G < n_tiles) {                      // (once W's tile has been read)
+                ok = bar_wait_warp(&w_empty[b], (i >> 1) & 1, abort_flag, p.err);
+                if (!ok) break;
+                if (lane == 0) load_w(nt + 2 * G, b);
+                __syncwarp();
+            }
         }
-        // (nor is anything issued: the rows' warps have waited for it, or gave up)
-        if (!ok && i > 0) mbar_wait(w_empty, (i - 1) & 1, nullptr, p.err);
+        if (!ok) {
+            // (a launch that gave up: no copy and nothing issued is left on its way; waits for
+            // what was not begun end at their bound)
+            mbar_wait(v_full, 0, nullptr, p.err);
+            for (int k = 0; k < 2; ++k) {
+                mbar_wait(&w_full[k], ((i + (k != (i & 1))) >> 1) & 1, nullptr, p.err);
+                if (i > 1) mbar_wait(&w_empty[k], ((i - 1 - (k != ((i - 1) & 1))) >> 1) & 1, nullptr, p.err);
+            }
+        }
         __syncwarp();
     } else if (warp > E_WARPS && out != base) {
         // tokens of no adapter keep base
