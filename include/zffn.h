@@ -543,7 +543,7 @@ zffn_status zffn_swiglu_grad(int dtype, const void *dh, const void *gu, void *dg
  *     base (tokens of no adapter are then left alone), and may not overlap it otherwise.
  *   v: output, fp32 [T][r], the sorted rows' (0 from offsets[L] on): what
  *     zffn_lora_grad needs again.
- *   work: zffn_lora_work_bytes(T, r, 0) bytes of the caller's, for the call (NULL
+ *   work: zffn_lora_work_bytes(T, r, L, 0) bytes of the caller's, for the call (NULL
  *     where that is 0).
  * Both products have fp32 sums; v is not rounded to fewer bits between them.
  * Requirements: 1 <= T <= 2^24, K and N multiples of 8 in [8, 65536], r a multiple
@@ -554,8 +554,8 @@ zffn_status zffn_lora_add(const void *x, const void *A, const void *B, const flo
                           int dtype, const void *base, void *out, float *v, void *work, int T, int N,
                           int K, int r, int L, void *stream);
 /* Bytes of `work` for zffn_lora_add (backward = 0) or zffn_lora_grad (backward = 1);
- * 0 also for T or r that they refuse.  Host-side query. */
-size_t zffn_lora_work_bytes(int T, int r, int backward);
+ * 0 also for T, r or L that they refuse.  Host-side query. */
+size_t zffn_lora_work_bytes(int T, int r, int L, int backward);
 
 /* Gradients of zffn_lora_add:
  *     dv[row] = scale[e] dy[t] B[e]                  (fp32 [r])
@@ -568,7 +568,7 @@ size_t zffn_lora_work_bytes(int T, int r, int backward);
  *   base: dx_dtype [T][K] or NULL.  dx: dx_dtype [T][K], may be base.
  *   dA: dw_dtype [L][r][K].  dB: dw_dtype [L][N][r].  dv: output, fp32 [T][r] (0 from
  *     offsets[L] on).
- *   work: zffn_lora_work_bytes(T, r, 1) bytes.
+ *   work: zffn_lora_work_bytes(T, r, L, 1) bytes.
  * Requirements and the other arguments as zffn_lora_add; dy, v, dx, dA, dB, dv and
  * work 16-byte aligned.  Errors: INVALID_ARG, CUDA. */
 zffn_status zffn_lora_grad(const void *dy, const void *x, const float *v, const void *A,

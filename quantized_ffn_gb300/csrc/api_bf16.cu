@@ -80,9 +80,9 @@ zffn_status zffn_swiglu_grad(int dtype, const void *dh, const void *gu, void *dg
     return to_status(launch_swiglu_grad(dtype, dh, gu, dgu, rows, I, (cudaStream_t)stream));
 }
 
-size_t zffn_lora_work_bytes(int T, int r, int backward) {
-    if (T < 1 || T > (1 << 24) || r < 8 || r > 128 || r % 8) return 0;
-    return backward ? 2 * lora_pieces_bytes(T, r) : lora_by_rows(T, r) ? 0 : lora_pieces_bytes(T, r);
+size_t zffn_lora_work_bytes(int T, int r, int L, int backward) {
+    if (T < 1 || T > (1 << 24) || r < 8 || r > 128 || r % 8 || L < 1 || L > 4096) return 0;
+    return backward ? 2 * lora_pieces_bytes(T, r) : lora_by_rows(T, r, L) ? 0 : lora_pieces_bytes(T, r);
 }
 
 zffn_status zffn_lora_add(const void *x, const void *A, const void *B, const float *scale, const int32_t *row_slot,
@@ -92,7 +92,7 @@ zffn_status zffn_lora_add(const void *x, const void *A, const void *B, const flo
     if (!x || !A || !B || !out || !v) return invalid("a pointer argument is NULL");
     if (!dtype_valid(dtype)) return invalid("unknown dtype");
     if (check_lora(p, N, K) != ZFFN_OK) return ZFFN_ERR_INVALID_ARG;
-    const bool by_rows = lora_by_rows(T, r);
+    const bool by_rows = lora_by_rows(T, r, L);
     if (!work && !by_rows) return invalid("work is NULL");
     if ((bits(x) | bits(A) | bits(B) | bits(base) | bits(out) | bits(v) | bits(work)) & 15)
         return invalid("x, A, B, base, out, v and work must be 16-byte aligned");
@@ -123,8 +123,7 @@ zffn_status zffn_lora_grad(const void *dy, const void *x, const float *v, const 
     uint8_t *dv16 = static_cast<uint8_t *>(work), *v16 = dv16 + lora_pieces_bytes(T, r);
     cudaError_t e = launch_lora_shrink(p, dy, B, true, dv, dv16, v, v16, N, s);
     if (e == cudaSuccess) e = launch_lora_expand(p, dv16, A, true, dx_dtype, base, dx, K, s);
-    if (e == cudaSuccess) e = launch_lora_outer(p, dv16, x, false, dw_dtype, dA, K, s);
-    if (e == cudaSuccess) e = launch_lora_outer(p, v16, dy, true, dw_dtype, dB, N, s);
+    if (e == cudaSuccess) e = launch_lora_outer(p, dv16, x, dA, K, v16, dy, dB, N, dw_dtype, s);
     return to_status(e);
 }
 

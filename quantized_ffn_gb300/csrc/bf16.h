@@ -45,7 +45,7 @@ struct LoraPlan {
 };
 // Bytes of v's bf16 pieces, and whether a forward call goes row by row, without them.
 size_t lora_pieces_bytes(int T, int r);
-bool lora_by_rows(int T, int r);
+bool lora_by_rows(int T, int r, int L);
 // v[row] = scale x[t] W^T, and its pieces v16: W [L][r][C], or (transposed) [L][C][r].  other:
 // nullptr, or fp32 [T][r] whose pieces are written to other16 on the way.
 cudaError_t launch_lora_shrink(const LoraPlan &p, const void *x, const void *w, bool transposed, float *v, void *v16, const float *other, void *other16,
@@ -57,7 +57,8 @@ cudaError_t launch_lora_expand(const LoraPlan &p, const void *v16, const void *w
 // Both steps of the forward pass row by row.
 cudaError_t launch_lora_rows(const LoraPlan &p, const void *x, const void *A, const void *B, int dtype, const void *base, void *out, float *v, int N, int K,
                              cudaStream_t s);
-// d[e] = sum of v[row]^T x[t] over e's rows: d [L][r][C], or (transposed) [L][C][r]
-cudaError_t launch_lora_outer(const LoraPlan &p, const void *v16, const void *x, bool transposed, int dtype, void *d, int C, cudaStream_t s);
+// dA[e] = sum of dv[row]^T x[t] over e's rows, [L][r][K], and dB[e] = sum of dy[t]^T v[row], [L][N][r]
+cudaError_t launch_lora_outer(const LoraPlan &p, const void *dv16, const void *x, void *dA, int K, const void *v16, const void *dy, void *dB, int N, int dtype,
+                              cudaStream_t s);
 
 }  // namespace zffn

@@ -553,7 +553,7 @@ struct Work {
     at::Tensor t;
     void *at = nullptr;
     Work(const Lora &p, int backward, const at::Tensor &like) {
-        if (const size_t bytes = api.lora_work_bytes((int)p.T, (int)p.r, backward)) {
+        if (const size_t bytes = api.lora_work_bytes((int)p.T, (int)p.r, (int)p.L, backward)) {
             t = at::empty({(int64_t)bytes}, like.options().dtype(kU8));
             at = t.data_ptr();
         }

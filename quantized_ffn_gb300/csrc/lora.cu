@@ -647,10 +647,18 @@ struct OuterCfg {
     static constexpr int SMEM = 1024 + OFF_BAR + (2 * NS + 4) * 8 + 8;
 };
 
+// d [L][r][C], or (transposed) [L][C][r].  A launch has two: an adapter's tiles are the first
+// one's and then the second one's.
+struct OuterJob {
+    CUtensorMap xm, vm;
+    const __nv_bfloat16 *x, *v16;
+    void *d;
+    int C, n_tiles, wide_x, transposed;
+};
+
 template <class C>
-__global__ void __launch_bounds__(O_THREADS, 1) outer_kernel(const __grid_constant__ CUtensorMap xm, const __grid_constant__ CUtensorMap vm, const Params p,
-                                                             const __nv_bfloat16 *v16, const __nv_bfloat16 *x, void *d, int n_tiles, int wide_x,
-                                                             int transposed, int d_bf16) {
+__global__ void __launch_bounds__(O_THREADS, 1) outer_kernel(const __grid_constant__ OuterJob ja, const __grid_constant__ OuterJob jb, const Params p,
+                                                             int d_bf16) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint64_t *s_full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
@@ -664,8 +672,10 @@ __global__ void __launch_bounds__(O_THREADS, 1) outer_kernel(const __grid_consta
         for (int i = 0; i < C::NS; ++i) { mbar_init(&s_full[i], 9); mbar_init(&s_empty[i], 1); }
         for (int i = 0; i < 2; ++i) { mbar_init(&t_full[i], 1); mbar_init(&t_empty[i], 4); }
         fence_mbarrier_init();
-        prefetch_tensormap(&xm);
-        prefetch_tensormap(&vm);
+        prefetch_tensormap(&ja.xm);
+        prefetch_tensormap(&ja.vm);
+        prefetch_tensormap(&jb.xm);
+        prefetch_tensormap(&jb.vm);
     }
     if (warp == 2) {
         tmem_alloc(reinterpret_cast<uint32_t *>(info + 1), 512);
@@ -678,20 +688,20 @@ __global__ void __launch_bounds__(O_THREADS, 1) outer_kernel(const __grid_consta
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(info + 1);
     GroupWalk<128, 1, true> wk;
-    if (warp != 1 && warp != 3) wk.start(p.offsets, p.T, p.L, n_tiles, p.each, false, blockIdx.x);
+    if (warp != 1 && warp != 3) wk.start(p.offsets, p.T, p.L, ja.n_tiles + jb.n_tiles, p.each, false, blockIdx.x);
     auto stages = [&] { return (wk.rows + KB - 1) / KB; };
     // The tile's stages that TMA loads, the first ones: all whole ones where the group's tokens
     // follow one another, else none (looked at again only where the group has changed).
     int whole_of = -1, whole = 0;
     auto whole_stages = [&] {
         if (wk.e == whole_of) return whole;
-        bool packed = wk.rows > 0;
+        bool packed = wk.rows >= KB;
         const int32_t *slot = p.row_slot + wk.row0;
         const int t0 = packed ? __ldcg(slot) : -1;
         packed = packed && t0 >= 0 && t0 <= p.T - wk.rows;
         // (eight loads on their way: one after another, ending at the first stranger, they took
         // three quarters of the kernel's time)
-        for (int i = lane; i < wk.rows; i += 32 * 8) {
+        for (int i = lane; packed && i < wk.rows; i += 32 * 8) {
             int t[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) t[j] = i + 32 * j < wk.rows ? __ldcg(slot + i + 32 * j) : t0 + i + 32 * j;
@@ -710,6 +720,8 @@ __global__ void __launch_bounds__(O_THREADS, 1) outer_kernel(const __grid_consta
         bool ok = true;
         for (; ok && wk.get(); wk.t += gridDim.x) {
             const int ns = stages(), n = whole_stages(), t0 = n ? __ldcg(p.row_slot + wk.row0) : 0;
+            const OuterJob &job = wk.nt < ja.n_tiles ? ja : jb;
+            const int nt = wk.nt < ja.n_tiles ? wk.nt : wk.nt - ja.n_tiles;
             // (This warp and the gathering ones each arrive for every stage, whoever fills it: who
             // only waited for s_empty could be left more than a phase behind, and a barrier
             // tells a phase from the next one alone.)
@@ -727,13 +739,13 @@ __global__ void __launch_bounds__(O_THREADS, 1) outer_kernel(const __grid_consta
                 uint8_t *to = smem + s * C::STAGE;
                 if (lane == 0) {
                     mbar_arrive_expect_tx(&s_full[s], 16384 + boxes * 8192);
-                    if (wide_x) {
-                        tma_load_3d(to, &xm, &s_full[s], 0, t0 + i * KB, wk.nt * 2);
+                    if (job.wide_x) {
+                        tma_load_3d(to, &job.xm, &s_full[s], 0, t0 + i * KB, nt * 2);
                     } else {
-                        tma_load_2d(to, &xm, &s_full[s], wk.nt * 128, t0 + i * KB);
-                        tma_load_2d(to + 8192, &xm, &s_full[s], wk.nt * 128 + 64, t0 + i * KB);
+                        tma_load_2d(to, &job.xm, &s_full[s], nt * 128, t0 + i * KB);
+                        tma_load_2d(to + 8192, &job.xm, &s_full[s], nt * 128 + 64, t0 + i * KB);
                     }
-                    tma_load_3d(to + 16384, &vm, &s_full[s], 0, wk.row0 + i * KB, 0);
+                    tma_load_3d(to + 16384, &job.vm, &s_full[s], 0, wk.row0 + i * KB, 0);
                 }
                 __syncwarp();
             }
@@ -760,7 +772,16 @@ __global__ void __launch_bounds__(O_THREADS, 1) outer_kernel(const __grid_consta
             ++sent;
         };
         for (; ok && wk.get(); wk.t += gridDim.x) {
-            const int ns = stages(), n = whole_stages(), col = wk.nt * 128 + chunk * 8;
+            const int ns = stages(), n = whole_stages();
+            const OuterJob &job = wk.nt < ja.n_tiles ? ja : jb;
+            const int col = (wk.nt < ja.n_tiles ? wk.nt : wk.nt - ja.n_tiles) * 128 + chunk * 8;
+            // tokens of rows lane and 32 + lane of a stage, asked for a stage ahead
+            int t[2];
+            auto tokens = [&](int i) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) t[j] = i * KB + j * 32 + lane < wk.rows ? __ldcg(p.row_slot + wk.row0 + i * KB + j * 32 + lane) : -1;
+            };
+            if (n < ns) tokens(n);
             for (int i = 0; i < ns; ++i, ++it) {
                 const uint32_t s = it % C::NS;
                 mine &= ~(1u << s);
@@ -770,25 +791,24 @@ __global__ void __launch_bounds__(O_THREADS, 1) outer_kernel(const __grid_consta
                     if (lane == 0) mbar_arrive(&s_full[s]);
                 } else {
                     mine |= 1u << s;
-                    const int32_t *slot = p.row_slot + wk.row0 + i * KB;
-                    const int rows = wk.rows - i * KB;
-                    int tok[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) tok[j] = first + 16 * j < rows ? __ldcg(slot + first + 16 * j) : -1;
                     if (it >= (uint32_t)C::NS) ok = bar_wait_warp(&s_empty[s], ((it / C::NS) & 1) ^ 1, abort_flag, p.err);
                     if (!ok) break;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const bool there = (unsigned)tok[j] < (unsigned)p.T && col < p.C;
-                        copy16(dst + s * C::STAGE + j * 2048, there ? x + (int64_t)tok[j] * p.C + col : x, there);
+                        const int tok = __shfl_sync(0xffffffffu, t[j >> 1], (first + 16 * j) & 31);
+                        const bool there = (unsigned)tok < (unsigned)p.T && col < job.C;
+                        copy16(dst + s * C::STAGE + j * 2048, there ? job.x + (int64_t)tok * job.C + col : job.x, there);
                     }
                     const uint32_t to = smem_u32(smem) + s * C::STAGE + 16384;
-                    for (int q = me; q < KB * wide; q += 256) {
-                        const int row = by_wide.div(q), c = q - row * wide;
-                        const bool there = row < rows && (unsigned)__ldcg(slot + row) < (unsigned)p.T;
-                        copy16(to + (c >> 3) * 8192 + row * 128 + (((c & 7) ^ (row & 7)) << 4),
-                               there ? v16 + (int64_t)(wk.row0 + i * KB + row) * pieces_pitch(p.r) + c * 8 : v16, there);
+                    for (int q0 = 0; q0 < KB * wide; q0 += 256) {
+                        const int q = q0 + me, row = min(by_wide.div(q), KB - 1), c = q - row * wide;
+                        const int t0 = __shfl_sync(0xffffffffu, t[0], row & 31), t1 = __shfl_sync(0xffffffffu, t[1], row & 31);
+                        const bool there = (unsigned)(row < 32 ? t0 : t1) < (unsigned)p.T;
+                        if (q < KB * wide)
+                            copy16(to + (c >> 3) * 8192 + row * 128 + (((c & 7) ^ (row & 7)) << 4),
+                                   there ? job.v16 + (int64_t)(wk.row0 + i * KB + row) * pieces_pitch(p.r) + c * 8 : job.v16, there);
                     }
+                    if (i + 1 < ns) tokens(i + 1);
                 }
                 copy_commit();
                 if (it - sent >= (uint32_t)C::LAG) {
@@ -851,7 +871,9 @@ __global__ void __launch_bounds__(O_THREADS, 1) outer_kernel(const __grid_consta
                 tc_fence_after();
                 ++acc;
             }
-            const int c = wk.nt * 128 + (warp & 3) * 32 + lane;
+            const OuterJob &job = wk.nt < ja.n_tiles ? ja : jb;
+            const int c = (wk.nt < ja.n_tiles ? wk.nt : wk.nt - ja.n_tiles) * 128 + (warp & 3) * 32 + lane;
+            void *d = job.d;
             for (int j0 = 0; j0 < p.r; j0 += 16) {
                 uint32_t w[16];
                 if (some) {
@@ -868,9 +890,9 @@ __global__ void __launch_bounds__(O_THREADS, 1) outer_kernel(const __grid_consta
 #pragma unroll
                     for (int j = 0; j < 16; ++j) w[j] = 0;
                 }
-                if (c >= p.C) continue;
-                if (transposed) {      // d [L][C][r]
-                    const int64_t at = ((int64_t)wk.e * p.C + c) * p.r + j0;
+                if (c >= job.C) continue;
+                if (job.transposed) {  // d [L][C][r]
+                    const int64_t at = ((int64_t)wk.e * job.C + c) * p.r + j0;
 #pragma unroll
                     for (int j = 0; j < 16; j += 8) {
                         if (j0 + j >= p.r) break;
@@ -883,12 +905,12 @@ __global__ void __launch_bounds__(O_THREADS, 1) outer_kernel(const __grid_consta
                         }
                     }
                 } else {               // d [L][r][C]
-                    const int64_t at = ((int64_t)wk.e * p.r + j0) * p.C + c;
+                    const int64_t at = ((int64_t)wk.e * p.r + j0) * job.C + c;
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
                         if (j0 + j >= p.r) break;
-                        if (d_bf16) static_cast<__nv_bfloat16 *>(d)[at + (int64_t)j * p.C] = __float2bfloat16_rn(__uint_as_float(w[j]));
-                        else static_cast<float *>(d)[at + (int64_t)j * p.C] = __uint_as_float(w[j]);
+                        if (d_bf16) static_cast<__nv_bfloat16 *>(d)[at + (int64_t)j * job.C] = __float2bfloat16_rn(__uint_as_float(w[j]));
+                        else static_cast<float *>(d)[at + (int64_t)j * job.C] = __uint_as_float(w[j]);
                     }
                 }
             }
@@ -969,13 +991,15 @@ __global__ void __launch_bounds__(256) shrink_row_kernel(const Params p, const _
     if (lane == 0) v[(int64_t)row * p.r + j] = sum;
 }
 
-// Two columns of out a thread: blocks (token, 256 columns).  W's rows are asked for before
-// the grid that writes v has ended.
+constexpr int R_THREADS = 128;
+
+// Two columns of out a thread: blocks (token, 256 columns).  W's rows (through L1: a load takes
+// half of a row's 32 bytes) are asked for before the grid that writes v has ended.
 template <typename O>
-__global__ void __launch_bounds__(128) expand_row_kernel(const Params p, const float *v, const __nv_bfloat16 *w, const O *base, O *out) {
+__global__ void __launch_bounds__(R_THREADS) expand_row_kernel(const Params p, const float *v, const __nv_bfloat16 *w, const O *base, O *out) {
     __shared__ int sh;
     __shared__ float vs[128];
-    const int t = blockIdx.x, n = blockIdx.y * 256 + threadIdx.x * 2, row = __ldcg(p.slot_row + t);
+    const int t = blockIdx.x, n = blockIdx.y * (2 * R_THREADS) + threadIdx.x * 2, row = __ldcg(p.slot_row + t);
     const bool some = (unsigned)row < (unsigned)p.T;
     const int e = some ? group_of(p.offsets, p.L, p.T, row, &sh) : p.L;
     const bool there = n < p.C;        // (C is a multiple of 8)
@@ -988,11 +1012,11 @@ __global__ void __launch_bounds__(128) expand_row_kernel(const Params p, const f
     uint4 f[2][AHEAD];
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i)
-        if (mine && i * 8 < p.r) { f[0][i] = __ldcg(w0 + i); f[1][i] = __ldcg(w1 + i); }
+        if (mine && i * 8 < p.r) { f[0][i] = w0[i]; f[1][i] = w1[i]; }
     grid_wait();
     grid_launch_dependents();
     if (e >= 0 && e < p.L) {
-        for (int i = threadIdx.x; i < p.r; i += 128) vs[i] = __ldcg(v + (int64_t)row * p.r + i);
+        for (int i = threadIdx.x; i < p.r; i += R_THREADS) vs[i] = __ldcg(v + (int64_t)row * p.r + i);
         __syncthreads();
     }
     if (mine) {
@@ -1006,7 +1030,7 @@ __global__ void __launch_bounds__(128) expand_row_kernel(const Params p, const f
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i)
             if (i * 8 < p.r) { s0 = dot(f[0][i], i * 8, s0); s1 = dot(f[1][i], i * 8, s1); }
-        for (int i = AHEAD; i * 8 < p.r; ++i) { s0 = dot(__ldcg(w0 + i), i * 8, s0); s1 = dot(__ldcg(w1 + i), i * 8, s1); }
+        for (int i = AHEAD; i * 8 < p.r; ++i) { s0 = dot(w0[i], i * 8, s0); s1 = dot(w1[i], i * 8, s1); }
         a += s0;
         b += s1;
     }
@@ -1021,8 +1045,11 @@ __global__ void __launch_bounds__(128) expand_row_kernel(const Params p, const f
 static Params params(const LoraPlan &q, int C) { return Params{q.row_slot, q.slot_row, q.offsets, q.scale, q.err, q.T, q.r, q.L, C, FastDiv(1), FastDiv(up16(q.r) / 4), FastDiv(3 * up16(q.r) / 8)}; }
 // Row tiles of 128 rows, at most, with those of the rows of none.
 static int64_t row_tiles(const LoraPlan &q) { return q.T / 128 + (q.L + 1 < q.T ? q.L + 1 : q.T); }
-// Few tokens: by the row kernels.
-static bool few(int T, int r) { return (int64_t)T * r <= 2048; }
+// Whether a forward pass goes row by row: each row reads its adapter through L2 again, where
+// the tensor cores' kernels take a tile for each adapter, however few its rows (4096 -> 11008,
+// us by rows and by tiles: 61 tokens of 48 adapters, r = 16: 10 / 52, 256 of 64: 23 / 73,
+// 64 of 4: 10 / 15, 512 of 4: 46 / 19, 64 of 4 with r = 64: 28 / 18).
+static bool few(int T, int r, int L) { return (int64_t)T * r <= 1024 + 160 * (int64_t)(L < T ? L : T); }
 
 template <bool MN>
 static cudaError_t shrink(const LoraPlan &q, const void *x, const void *w, float *v, void *v16, const float *other, void *other16, int C, cudaStream_t s) {
@@ -1062,26 +1089,36 @@ static cudaError_t expand(const LoraPlan &q, const void *v, const void *w, int d
     return q.r <= 64 ? expand<4, 128, 1, MN>(q, v, w, base, out, C, s) : expand<4, 64, 2, MN>(q, v, w, base, out, C, s);
 }
 
+static bool outer_job(OuterJob *job, const LoraPlan &q, const void *v16, const void *x, void *d, int C, bool transposed) {
+    *job = OuterJob{};
+    job->x = static_cast<const __nv_bfloat16 *>(x);
+    job->v16 = static_cast<const __nv_bfloat16 *>(v16);
+    job->d = d;
+    job->C = C;
+    job->n_tiles = (C + 127) / 128;
+    job->wide_x = C % 64 == 0;
+    job->transposed = transposed;
+    return encode(&job->xm, x, 2, C, q.T, 1, KB, false, job->wide_x ? 2 : 0) &&
+           encode(&job->vm, v16, 2, pieces_pitch(q.r), q.T, 1, KB, false, pieces_pitch(q.r) / 64);
+}
 template <bool WIDE>
-static cudaError_t outer(const LoraPlan &q, const void *v16, const void *x, bool transposed, int dtype, void *d, int C, cudaStream_t s) {
+static cudaError_t outer(const LoraPlan &q, const OuterJob &a, const OuterJob &b, int dtype, cudaStream_t s) {
     using Cfg = OuterCfg<WIDE>;
-    CUtensorMap rows, map;
-    const bool wide_x = C % 64 == 0;
-    if (!encode(&rows, x, 2, C, q.T, 1, KB, false, wide_x ? 2 : 0) || !encode(&map, v16, 2, pieces_pitch(q.r), q.T, 1, KB, false, pieces_pitch(q.r) / 64)) return cudaErrorInvalidValue;
-    const int n_tiles = (C + 127) / 128;
+    const int n_tiles = a.n_tiles + b.n_tiles;
     const int64_t tiles = (int64_t)q.L * n_tiles, sms = device_info().num_sms;
-    Params p = params(q, C);
+    if (tiles + sms > 0x7fffffff) return cudaErrorInvalidValue;
+    Params p = params(q, 0);
     p.each = GroupWalk<128, 1, true>::divisor(n_tiles);
     const cudaError_t e = ensure_dynamic_smem((const void *)outer_kernel<Cfg>, Cfg::SMEM);
     if (e != cudaSuccess) return e;
-    return launch_dependent(outer_kernel<Cfg>, dim3((unsigned)(tiles < sms ? tiles : sms)), O_THREADS, Cfg::SMEM, 1, s, rows, map, p,
-                            static_cast<const __nv_bfloat16 *>(v16), static_cast<const __nv_bfloat16 *>(x), d, n_tiles, (int)wide_x, (int)transposed, (int)(dtype == ZFFN_DT_BF16));
+    return launch_dependent(outer_kernel<Cfg>, dim3((unsigned)(tiles < sms ? tiles : sms)), O_THREADS, Cfg::SMEM, 1, s, a, b, p,
+                            (int)(dtype == ZFFN_DT_BF16));
 }
 
 }  // namespace lora
 
 size_t lora_pieces_bytes(int T, int r) { return (size_t)T * 2 * lora::pieces_pitch(r); }
-bool lora_by_rows(int T, int r) { return lora::few(T, r); }
+bool lora_by_rows(int T, int r, int L) { return lora::few(T, r, L); }
 
 cudaError_t launch_lora_shrink(const LoraPlan &q, const void *x, const void *w, bool transposed, float *v, void *v16, const float *other, void *other16,
                                int C, cudaStream_t s) {
@@ -1104,17 +1141,20 @@ cudaError_t launch_lora_rows(const LoraPlan &q, const void *x, const void *A, co
     const cudaError_t e = launch_dependent(shrink_row_kernel, dim3((unsigned)q.T, (unsigned)(q.r / 8)), 256, 0, 1, s, params(q, K),
                                            static_cast<const __nv_bfloat16 *>(x), static_cast<const __nv_bfloat16 *>(A), v);
     if (e != cudaSuccess) return e;
-    const dim3 grid((unsigned)q.T, (unsigned)((N + 255) / 256));
+    const dim3 grid((unsigned)q.T, (unsigned)((N + 2 * R_THREADS - 1) / (2 * R_THREADS)));
     if (dtype == ZFFN_DT_BF16)
-        return launch_dependent(expand_row_kernel<__nv_bfloat16>, grid, 128, 0, 1, s, params(q, N), v, b16, static_cast<const __nv_bfloat16 *>(base),
+        return launch_dependent(expand_row_kernel<__nv_bfloat16>, grid, R_THREADS, 0, 1, s, params(q, N), v, b16, static_cast<const __nv_bfloat16 *>(base),
                                 static_cast<__nv_bfloat16 *>(out));
-    return launch_dependent(expand_row_kernel<float>, grid, 128, 0, 1, s, params(q, N), v, b16, static_cast<const float *>(base), static_cast<float *>(out));
+    return launch_dependent(expand_row_kernel<float>, grid, R_THREADS, 0, 1, s, params(q, N), v, b16, static_cast<const float *>(base), static_cast<float *>(out));
 }
 
-cudaError_t launch_lora_outer(const LoraPlan &q, const void *v16, const void *x, bool transposed, int dtype, void *d, int C, cudaStream_t s) {
+cudaError_t launch_lora_outer(const LoraPlan &q, const void *dv16, const void *x, void *dA, int K, const void *v16, const void *dy, void *dB, int N, int dtype,
+                              cudaStream_t s) {
     using namespace lora;
     if (!encode_fn()) return cudaErrorNotSupported;
-    return q.r <= 80 ? outer<false>(q, v16, x, transposed, dtype, d, C, s) : outer<true>(q, v16, x, transposed, dtype, d, C, s);
+    OuterJob a, b;
+    if (!outer_job(&a, q, dv16, x, dA, K, false) || !outer_job(&b, q, v16, dy, dB, N, true)) return cudaErrorInvalidValue;
+    return q.r <= 80 ? outer<false>(q, a, b, dtype, s) : outer<true>(q, a, b, dtype, s);
 }
 
 }  // namespace zffn

@@ -82,7 +82,7 @@ def load() -> ctypes.CDLL:
                 "zffn_bf16_matmul_grad_w": ([P, P, P, I32, P, I32, I32, I32, I32, P], I32),
                 "zffn_swiglu": ([I32, P, P, I64, I64, P], I32),
                 "zffn_swiglu_grad": ([I32, P, P, P, I64, I64, P], I32),
-                "zffn_lora_work_bytes": ([I32, I32, I32], ctypes.c_size_t),
+                "zffn_lora_work_bytes": ([I32, I32, I32, I32], ctypes.c_size_t),
                 "zffn_lora_add": ([P, P, P, P, P, P, P, I32, P, P, P, P, I32, I32, I32, I32, I32, P], I32),
                 "zffn_lora_grad": ([P, P, P, P, P, P, P, P, P, I32, P, P, I32, P, P, P, P, I32, I32, I32, I32, I32, P],
                                    I32),

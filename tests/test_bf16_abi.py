@@ -45,7 +45,7 @@ def test_swiglu_refuses(lib, args):
         assert lib.zffn_swiglu_grad(dt, gu, F, F, rows, i, None) == BAD
 
 
-LORA = dict(dy=F, x=F, v=F, A=F, B=F, s=F, rs=F, sr=F, off=F, dt=0, base=F, out=F, wdt=0, dA=F, dB=F, dv=F, work=F, T=400, N=64, K=256, r=16, L=3)
+LORA = dict(dy=F, x=F, v=F, A=F, B=F, s=F, rs=F, sr=F, off=F, dt=0, base=F, out=F, wdt=0, dA=F, dB=F, dv=F, work=F, T=4000, N=64, K=256, r=16, L=3)
 SHARED = ([{k: None} for k in ("x", "A", "B", "rs", "sr", "off", "out", "v", "work")] +
           [dict(dt=2), dict(T=0), dict(T=(1 << 24) + 1), dict(N=60), dict(N=0), dict(N=65544), dict(K=4), dict(K=65544), dict(r=0), dict(r=12),
            dict(r=136), dict(L=0), dict(L=4097), dict(x=A8), dict(A=A8), dict(B=A8), dict(base=A8), dict(out=A8), dict(v=A8), dict(work=A8), dict(s=A2), dict(rs=A2),
@@ -66,9 +66,9 @@ def test_adapters_gradients_refuse(lib, bad):
 
 
 def test_work_bytes(lib):
-    assert lib.zffn_lora_work_bytes(400, 24, 0) == 400 * 2 * 128 and lib.zffn_lora_work_bytes(400, 24, 1) == 2 * 400 * 2 * 128
-    assert lib.zffn_lora_work_bytes(1, 16, 0) == 0 and lib.zffn_lora_work_bytes(1, 16, 1) == 2 * 2 * 64      # (row by row)
-    assert all(lib.zffn_lora_work_bytes(*bad, 1) == 0 for bad in ((0, 16), (4, 12), (4, 136), (1 << 25, 16)))
+    assert lib.zffn_lora_work_bytes(4000, 24, 3, 0) == 4000 * 2 * 128 and lib.zffn_lora_work_bytes(400, 24, 3, 1) == 2 * 400 * 2 * 128
+    assert lib.zffn_lora_work_bytes(1, 16, 8, 0) == 0 and lib.zffn_lora_work_bytes(1, 16, 8, 1) == 2 * 2 * 64      # (row by row)
+    assert all(lib.zffn_lora_work_bytes(*bad, 1) == 0 for bad in ((0, 16, 1), (4, 12, 1), (4, 136, 1), (1 << 25, 16, 1), (4, 16, 0), (4, 16, 4097)))
 
 
 def test_reason_is_given(lib):
