@@ -636,12 +636,12 @@ __global__ void __launch_bounds__(E_THREADS, 1) expand_kernel(const __grid_const
 // ---------------------------------------------------------------------------
 constexpr int O_THREADS = 512;
 
-template <bool WIDE_>
+template <int BOXES_>
 struct OuterCfg {
-    static constexpr bool WIDE = WIDE_;                      // r > 80
-    static constexpr int V_BYTES = (WIDE ? 6 : 4) * 8192;    // 64-wide boxes of the pieces
-    static constexpr int STAGE = 16384 + V_BYTES;
-    static constexpr int NS = WIDE ? 3 : 4, LAG = NS - 1;
+    static constexpr int BOXES = BOXES_;                     // 64-wide boxes of the pieces, at most: 2 (r up to 32), 4 (80), 6
+    static constexpr bool WIDE = BOXES > 4;
+    static constexpr int STAGE = 16384 + BOXES * 8192;
+    static constexpr int NS = BOXES == 2 ? 6 : BOXES == 4 ? 4 : 3, LAG = NS - 1;
     static constexpr int ACC = WIDE ? 1 : 2, ACC_COLS = 512 / ACC;
     static constexpr int OFF_BAR = NS * STAGE;
     static constexpr int SMEM = 1024 + OFF_BAR + (2 * NS + 4) * 8 + 8;
@@ -699,14 +699,14 @@ __global__ void __launch_bounds__(O_THREADS, 1) outer_kernel(const __grid_consta
         const int32_t *slot = p.row_slot + wk.row0;
         const int t0 = packed ? __ldcg(slot) : -1;
         packed = packed && t0 >= 0 && t0 <= p.T - wk.rows;
-        // (eight loads on their way: one after another, ending at the first stranger, they took
-        // three quarters of the kernel's time)
-        for (int i = lane; packed && i < wk.rows; i += 32 * 8) {
-            int t[8];
+        // (all loads of 1024 rows on their way: one after another, ending at the first stranger,
+        // they took three quarters of the kernel's time, in eights a sixth)
+        for (int i = lane; packed && i < wk.rows; i += 32 * 32) {
+            int t[32];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) t[j] = i + 32 * j < wk.rows ? __ldcg(slot + i + 32 * j) : t0 + i + 32 * j;
+            for (int j = 0; j < 32; ++j) t[j] = i + 32 * j < wk.rows ? __ldcg(slot + i + 32 * j) : t0 + i + 32 * j;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) packed = packed && t[j] == t0 + i + 32 * j;
+            for (int j = 0; j < 32; ++j) packed = packed && t[j] == t0 + i + 32 * j;
         }
         whole_of = wk.e;
         whole = __all_sync(0xffffffffu, packed) ? wk.rows / KB : 0;
@@ -1101,9 +1101,9 @@ static bool outer_job(OuterJob *job, const LoraPlan &q, const void *v16, const v
     return encode(&job->xm, x, 2, C, q.T, 1, KB, false, job->wide_x ? 2 : 0) &&
            encode(&job->vm, v16, 2, pieces_pitch(q.r), q.T, 1, KB, false, pieces_pitch(q.r) / 64);
 }
-template <bool WIDE>
+template <int BOXES>
 static cudaError_t outer(const LoraPlan &q, const OuterJob &a, const OuterJob &b, int dtype, cudaStream_t s) {
-    using Cfg = OuterCfg<WIDE>;
+    using Cfg = OuterCfg<BOXES>;
     const int n_tiles = a.n_tiles + b.n_tiles;
     const int64_t tiles = (int64_t)q.L * n_tiles, sms = device_info().num_sms;
     if (tiles + sms > 0x7fffffff) return cudaErrorInvalidValue;
@@ -1154,7 +1154,8 @@ cudaError_t launch_lora_outer(const LoraPlan &q, const void *dv16, const void *x
     if (!encode_fn()) return cudaErrorNotSupported;
     OuterJob a, b;
     if (!outer_job(&a, q, dv16, x, dA, K, false) || !outer_job(&b, q, v16, dy, dB, N, true)) return cudaErrorInvalidValue;
-    return q.r <= 80 ? outer<false>(q, a, b, dtype, s) : outer<true>(q, a, b, dtype, s);
+    const int boxes = pieces_pitch(q.r) / 64;
+    return boxes <= 2 ? outer<2>(q, a, b, dtype, s) : boxes <= 4 ? outer<4>(q, a, b, dtype, s) : outer<6>(q, a, b, dtype, s);
 }
 
 }  // namespace zffn
