@@ -35,6 +35,7 @@ struct Params {
     // 256 rows of 128 experts, 1536 x 2048, 185 us against 202.)
     int wide_a, wide_w;
     FastDiv each, across;   // of the walk; weights: by n_tiles
+    int part_log;           // log2 of a part's stages
 };
 // a: forward, back: [M][K]; weights: dy, in boxes of 16, 32 and 64 rows.  w: w; weights: a,
 // in the same.  y: what the stores go to.
@@ -46,17 +47,18 @@ struct Maps {
 // Many rows: tiles of 128 rows (a CTA pair: 256) times 256 columns of the result, a
 // (weights: dy) on the MMA's M side.  Persistent: every cluster takes tiles in turn;
 // two accumulators in tensor memory, so that one is taken out while the next tile's
-// MMAs run.
+// MMAs run.  PARTS: a long sum in parts (see part_log), joined in the registers of the
+// threads that take them out.
 //
 // Roles: warps 0 .. 7 take a tile out of tensor memory (32 rows by 128 columns each) and
 // write it, warp 8 loads by TMA, warp 9 issues the MMAs; weights: warp 10 zeroes the rows past an
 // expert's last in its last stage (in the MMA's own warp that held the MMAs back: 32768
 // rows of 128 experts, 1536 x 2048, 217 us).
 // ---------------------------------------------------------------------------
-template <int KIND_, bool PAIR_>
+template <int KIND_, bool PAIR_, bool PARTS_>
 struct LargeCfg {
     static constexpr int KIND = KIND_;
-    static constexpr bool PAIR = PAIR_;
+    static constexpr bool PAIR = PAIR_, PARTS = PARTS_;
     static constexpr int CTAS = PAIR ? 2 : 1;
     static constexpr int TM = 128 * CTAS, TN = 256;
     static constexpr bool A_MN = KIND == WEIGHTS, W_MN = KIND != FORWARD;
@@ -115,7 +117,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(info + 1);
     typename C::Walk wk;
     wk.start(p.offsets, p.M, p.E, GRAD ? p.m_tiles * p.n_tiles : p.n_tiles, p.each, !GRAD, blockIdx.x / C::CTAS);
-    const int step = gridDim.x / C::CTAS;
+    const int step = gridDim.x / C::CTAS, part_log = C::PARTS ? p.part_log : 30, part_mask = (1 << part_log) - 1;
     // stages of the tile at hand (none: zeros)
     auto blocks = [&] { return GRAD ? (wk.rows + KB - 1) / KB : wk.e < p.E ? (p.K + KB - 1) / KB : 0; };
     // groups of 16 contracted values in stage i
@@ -222,10 +224,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
             for (; ok && wk.get(); wk.t += step) {
                 const int nb = blocks();
                 if (nb == 0) continue;
-                const uint32_t b = acc & 1, dst = tmem + b * 256;
-                ok = acc < 2 || bar_wait_warp(&t_empty[b], ((acc >> 1) & 1) ^ 1, abort_flag, p.err);
                 for (int i = 0; i < nb; ++i, ++it) {
-                    const uint32_t s = it % C::NS;
+                    const uint32_t s = it % C::NS, b = acc & 1, dst = tmem + b * 256;
+                    const int at = i & part_mask;            // a part's first stage: 0
+                    const bool last = at == part_mask || i == nb - 1;
+                    if (at == 0) ok = acc < 2 || bar_wait_warp(&t_empty[b], ((acc >> 1) & 1) ^ 1, abort_flag, p.err);
                     ok = ok && bar_wait_warp(&s_full[s], (it / C::NS) & 1, abort_flag, p.err);
                     if (!ok) break;
                     const uint32_t sa = smem_u32(smem) + s * C::STAGE, sw = sa + C::A_BYTES;
@@ -238,20 +241,20 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
 #pragma unroll
                         for (int k = 0; k < KB / 16; ++k) {
                             if (k >= n) break;
-                            if constexpr (C::PAIR) tc_mma_bf16_pair(dst, ad + k * k_step(C::A_MN), wd + k * k_step(C::W_MN), idesc, (i | k) != 0);
-                            else tc_mma_bf16(dst, ad + k * k_step(C::A_MN), wd + k * k_step(C::W_MN), idesc, (i | k) != 0);
+                            if constexpr (C::PAIR) tc_mma_bf16_pair(dst, ad + k * k_step(C::A_MN), wd + k * k_step(C::W_MN), idesc, (at | k) != 0);
+                            else tc_mma_bf16(dst, ad + k * k_step(C::A_MN), wd + k * k_step(C::W_MN), idesc, (at | k) != 0);
                         }
                         if constexpr (C::PAIR) {
                             tc_commit_pair(&s_empty[s]);
-                            if (i == nb - 1) tc_commit_pair(&t_full[b]);
+                            if (last) tc_commit_pair(&t_full[b]);
                         } else {
                             tc_commit(&s_empty[s]);
-                            if (i == nb - 1) tc_commit(&t_full[b]);
+                            if (last) tc_commit(&t_full[b]);
                         }
                     }
                     __syncwarp();
+                    acc += last;
                 }
-                ++acc;
                 ok = __all_sync(0xffffffffu, ok && !*abort_flag);
             }
             if (elect_one()) {
@@ -289,14 +292,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
         uint8_t *out = smem + C::OFF_OUT + warp * C::OUT_BYTES;
         uint32_t acc = 0;
         for (bool ok = true; ok && wk.get(); wk.t += step) {
-            const bool some = blocks() != 0;
-            const uint32_t b = acc & 1, from = taddr + b * 256;
-            if (some) {
-                ok = bar_wait_warp(&t_full[b], (acc >> 1) & 1, abort_flag, p.err);
-                if (!ok) break;
-                tc_fence_after();
-                ++acc;
-            }
+            const int parts = (blocks() + part_mask) >> part_log;
+            const bool some = parts != 0;
             const int mt = GRAD ? p.across.div(wk.nt) : 0, nt = GRAD ? wk.nt - mt * p.n_tiles : wk.nt;
             const int wrow = (GRAD ? mt * C::TM : 0) + 128 * rank + q * 32;   // this warp's first row (of dw[e], of the tile)
             const int left = GRAD ? p.N - wrow : wk.rows - wrow;
@@ -306,6 +303,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
             // and 16-byte multiples, else by the lanes, a row's bytes by neighbouring ones.
             const int col0 = nt * C::TN + half * 128;
             const int need = min(4, (cols - col0 + 31) / 32);   // groups of 32 columns that are the result's
+            uint32_t b = 0, from = 0;
+            auto full = [&] {                                // the next part's sums are there
+                b = acc & 1, from = taddr + b * 256;
+                ok = bar_wait_warp(&t_full[b], (acc >> 1) & 1, abort_flag, p.err);
+                tc_fence_after();
+                ++acc;
+            };
             auto taken = [&] {                               // the accumulator has been read
                 if (!some) return;
                 tc_fence_before();
@@ -324,19 +328,51 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
             };
             auto write = [&](auto elem_size) {
                 constexpr int elem = decltype(elem_size)::value, per = 128 / elem, LOADS = per / 32;
-                if (need <= 0) {
-                    taken();
-                    return;
+                constexpr bool PARTS = C::PARTS;
+                uint32_t d[PARTS ? 4 : 2][32];
+                if constexpr (PARTS) {                       // all parts' sums, as they come
+                    float sum[4][32];
+#pragma unroll
+                    for (int l = 0; l < 4; ++l)
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) sum[l][j] = 0.f;
+                    for (int i = 0; i < parts; ++i) {
+                        full();
+                        if (!ok) return;
+#pragma unroll
+                        for (int l = 0; l < 8; ++l) {
+                            if (l >= 2 * need) break;
+                            uint32_t v[16];
+                            tmem_ld_32x32b_x16(from + l * 16, v);
+                            tmem_ld_wait(v);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) sum[l / 2][l % 2 * 16 + j] += __uint_as_float(v[j]);
+                        }
+                        taken();
+                    }
+#pragma unroll
+                    for (int l = 0; l < 4; ++l)
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) d[l][j] = __float_as_uint(sum[l][j]);
+                    if (need <= 0) return;
+                } else {
+                    if (some) full();
+                    if (!ok) return;
+                    if (need <= 0) {
+                        taken();
+                        return;
+                    }
+                    fetch(0, d[0]);
                 }
-                uint32_t d[2][32];
-                fetch(0, d[0]);
 #pragma unroll
                 for (int l = 0; l < 4; ++l) {
                     if (l >= need) break;
-                    uint32_t (&v)[32] = d[l & 1];
-                    if (some) tmem_ld_wait(v);
-                    if (l + 1 < need) fetch(l + 1, d[(l + 1) & 1]);
-                    else taken();
+                    uint32_t (&v)[32] = d[PARTS ? l : l & 1];
+                    if constexpr (!PARTS) {
+                        if (some) tmem_ld_wait(v);
+                        if (l + 1 < need) fetch(l + 1, d[(l + 1) & 1]);
+                        else taken();
+                    }
                     if (l % LOADS == 0) {                    // (the store before has read the box)
                         if (lane == 0) bulk_wait_group_read<0>();
                         __syncwarp();
@@ -436,7 +472,7 @@ struct SmallCfg {
     static constexpr int EPI = 4;
     static constexpr int THREADS = (EPI + 2) * 32;
     static constexpr int MAX_SPLIT = 8;
-    static constexpr int TMEM_COLS = 2 * TN;                 // two accumulators
+    static constexpr int TMEM_COLS = 4 * TN;                 // two accumulators, the parts' sums before the last
     static constexpr int PART_ROWS = TN + MAX_SPLIT - 1;     // split * ceil(TN / split), at most
     static constexpr int OFF_PART = NS * STAGE;              // sums [rank][row / split][128]
     static constexpr int OFF_BAR = OFF_PART + PART_ROWS * 512;
@@ -479,7 +515,7 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) small_kernel(const __gr
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(info + 1);
     const int blocks = (p.K + KB - 1) / KB;
     const int kb0 = blocks * rank / split, nkb = blocks * (rank + 1) / split - kb0;   // this rank's share of K
-    const int step = gridDim.x / split;
+    const int step = gridDim.x / split, part_mask = (1 << p.part_log) - 1;
     typename C::Walk wk;
     wk.start(p.offsets, p.M, p.E, p.n_tiles, p.each, true, blockIdx.x / split);
     const uint32_t slice = (C::TN + split - 1) / split;      // rows of a tile that a rank adds up
@@ -524,10 +560,11 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) small_kernel(const __gr
         bool ok = true;
         for (bool have = wk.get(); ok && have; have = next()) {
             if (wk.e >= p.E || nkb == 0) continue;
-            const uint32_t b = acc & 1, dst = tmem + b * C::TN;
-            ok = acc < 2 || bar_wait_warp(&t_empty[b], ((acc >> 1) & 1) ^ 1, abort_flag, p.err);
             for (int i = 0; i < nkb; ++i, ++it) {
-                const uint32_t s = it % C::NS;
+                const uint32_t s = it % C::NS, b = acc & 1, dst = tmem + b * C::TN;
+                const int at = i & part_mask;                // a part's first stage: 0
+                const bool last = at == part_mask || i == nkb - 1;
+                if (at == 0) ok = acc < 2 || bar_wait_warp(&t_empty[b], ((acc >> 1) & 1) ^ 1, abort_flag, p.err);
                 ok = ok && bar_wait_warp(&s_full[s], (it / C::NS) & 1, abort_flag, p.err);
                 if (!ok) break;
                 tc_fence_after();
@@ -539,14 +576,14 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) small_kernel(const __gr
 #pragma unroll
                     for (int k = 0; k < KB / 16; ++k) {
                         if (k >= n) break;
-                        tc_mma_bf16(dst, wd + k * k_step(C::W_MN), ad + k * k_step(false), idesc, (i | k) != 0);
+                        tc_mma_bf16(dst, wd + k * k_step(C::W_MN), ad + k * k_step(false), idesc, (at | k) != 0);
                     }
                     tc_commit(&s_empty[s]);
-                    if (i == nkb - 1) tc_commit(&t_full[b]);
+                    if (last) tc_commit(&t_full[b]);
                 }
                 __syncwarp();
+                acc += last;
             }
-            ++acc;
             ok = __all_sync(0xffffffffu, ok && !*abort_flag);
         }
         if (elect_one()) tc_commit(done);
@@ -558,14 +595,7 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) small_kernel(const __gr
         uint32_t acc = 0;
         bool ok = true;
         for (bool have = wk.get(); ok && have; have = next()) {
-            const bool some = wk.e < p.E && nkb != 0;
-            const uint32_t b = acc & 1;
-            if (some) {
-                ok = bar_wait_warp(&t_full[b], (acc >> 1) & 1, abort_flag, p.err);
-                if (!ok) break;
-                tc_fence_after();
-                ++acc;
-            }
+            const int parts = wk.e < p.E ? (nkb + part_mask) >> p.part_log : 0;
             const int n = wk.nt * 128 + tid;
             constexpr int CH = 16;
             if (split > 1) {
@@ -574,17 +604,55 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) small_kernel(const __gr
                 last_row0 = wk.row0; last_rows = wk.rows; last_nt = wk.nt;
             }
             const uint32_t to = smem_u32(part + rank * slice * 128) + tid * 4;
+            uint32_t b = 0;
+            auto full = [&] {                                // the next part's sums are there
+                b = acc & 1;
+                ok = bar_wait_warp(&t_full[b], (acc >> 1) & 1, abort_flag, p.err);
+                tc_fence_after();
+                ++acc;
+            };
+            auto taken = [&] {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&t_empty[b]);
+            };
+            // sums of this part, and (add) of those before
+            auto fetch = [&](int c, bool add, uint32_t (&d)[CH]) {
+                tmem_ld_32x32b_x16(taddr + b * C::TN + c, d);
+                tmem_ld_wait(d);
+                if (!add) return;
+                uint32_t sum[CH];
+                tmem_ld_32x32b_x16(taddr + 2 * C::TN + c, sum);
+                tmem_ld_wait(sum);
+#pragma unroll
+                for (int j = 0; j < CH; ++j) d[j] = __float_as_uint(__uint_as_float(sum[j]) + __uint_as_float(d[j]));
+            };
+            // (the parts' sums in tensor memory: in registers they made the code long, one expert of 24
+            // rows 7.5 / 9.3 us)
+#pragma unroll 1
+            for (int i = 1; i < parts; ++i) {
+                full();
+                if (!ok) break;
+#pragma unroll 1
+                for (int c = 0; c < C::TN; c += CH) {
+                    if (c >= wk.rows) break;
+                    uint32_t d[CH];
+                    fetch(c, i > 1, d);
+                    tmem_st_32x32b_x16(taddr + 2 * C::TN + c, d);
+                }
+                tmem_st_wait();
+                taken();
+            }
+            if (ok && parts) full();
+            if (!ok) break;
 #pragma unroll 1
             for (int c = 0; c < C::TN; c += CH) {
                 if (c >= wk.rows) break;
                 uint32_t d[CH];
-                if (some) {
-                    tmem_ld_32x32b_x16(taddr + b * C::TN + c, d);
-                    tmem_ld_wait(d);
-                } else {
+                if (parts) fetch(c, parts > 1, d);
+                else
 #pragma unroll
                     for (int j = 0; j < CH; ++j) d[j] = 0;
-                }
                 if (split > 1) {
 #pragma unroll
                     for (int j = 0; j < CH; ++j)
@@ -602,11 +670,7 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) small_kernel(const __gr
                         }
                 }
             }
-            if (some) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&t_empty[b]);
-            }
+            if (parts) taken();
         }
     }
     tc_fence_before();
@@ -638,6 +702,14 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) small_kernel(const __gr
 
 // ---- host -------------------------------------------------------------------
 
+// Stages of a part, as a logarithm.  The tensor core's adds drop what is below the accumulator's
+// last bit, so that a long sum comes out short (fp32 results of positive values: of 2048 3.8e-7, of 8192
+// 2.2e-6, of 65536 3.5e-5; of signed ones 2.3e-7, 1e-6, 1e-5).  Parts of 512, joined in fp32 registers
+// that round to nearest, hold it at 9e-7 (signed: 5e-7).  Of a bf16 result, whose rounding is 4e-3, a
+// part is 4096.
+constexpr int FP32_PART_LOG = 3, BF16_PART_LOG = 6;
+static int part_log(int dtype) { return dtype == ZFFN_DT_BF16 ? BF16_PART_LOG : FP32_PART_LOG; }
+
 // Row tiles of at most tr rows, at most: every expert may have one cut tile, and so may
 // the rows of none.
 static int64_t row_tiles_bound(int M, int E, const int32_t *offsets, int tr) {
@@ -659,7 +731,7 @@ static cudaError_t run_large(const Maps &maps, const Params &p, int64_t tiles, c
 template <class C>
 static cudaError_t launch_large(const Bf16Args &a, cudaStream_t s) {
     Maps maps{};
-    Params p{a.offsets, a.y, a.err, a.M, a.N, a.K, a.E, (a.N + C::TN - 1) / C::TN, 0, a.y_dtype == ZFFN_DT_BF16, 0, 0, C::KIND == BACK && a.N % 64 == 0, {}, {}};
+    Params p{a.offsets, a.y, a.err, a.M, a.N, a.K, a.E, (a.N + C::TN - 1) / C::TN, 0, a.y_dtype == ZFFN_DT_BF16, 0, 0, C::KIND == BACK && a.N % 64 == 0, {}, {}, part_log(a.y_dtype)};
     p.each = C::Walk::divisor(p.n_tiles);
     const int elem = p.y_bf16 ? 2 : 4;
     p.vec = a.N * elem % 16 == 0 && (reinterpret_cast<uintptr_t>(a.y) & 15) == 0;
@@ -716,7 +788,7 @@ template <class C>
 static cudaError_t launch_small(const Bf16Args &a, cudaStream_t s) {
     const DeviceInfo &di = device_info();
     Maps maps{};
-    Params p{a.offsets, a.y, a.err, a.M, a.N, a.K, a.E, (a.N + 127) / 128, 0, a.y_dtype == ZFFN_DT_BF16, 0, 0, C::KIND == BACK && a.N % 64 == 0, {}, {}};
+    Params p{a.offsets, a.y, a.err, a.M, a.N, a.K, a.E, (a.N + 127) / 128, 0, a.y_dtype == ZFFN_DT_BF16, 0, 0, C::KIND == BACK && a.N % 64 == 0, {}, {}, part_log(a.y_dtype)};
     p.each = C::Walk::divisor(p.n_tiles);
     if (!encode(maps.a, a.a, 2, a.K, a.M, 1, C::TN, false)) return cudaErrorInvalidValue;
     if (!(C::KIND == FORWARD ? encode(maps.w, a.w, 2, a.K, a.N, a.E, 128, true) : encode(maps.w, a.w, 2, a.N, a.K, a.E, KB, true, p.wide_w ? 2 : 0)))
@@ -737,6 +809,14 @@ static cudaError_t launch_small(const Bf16Args &a, cudaStream_t s) {
     return launch_dependent(small_kernel<C>, dim3((unsigned)(clusters * split)), C::THREADS, C::SMEM, (unsigned)split, s, maps, p);
 }
 
+template <int KIND, bool PARTS>
+static cudaError_t launch_tiles(const Bf16Args &a, cudaStream_t s) {
+    // CTA pairs where few of their 256 rows are past an expert's (single and pair: 128 experts
+    // of 96 rows 142 / 154, of 192 rows 184 / 176, of 256 rows 207 / 195, 8 of 4096 rows 139 / 124)
+    if (a.M / a.E >= 192) return launch_large<LargeCfg<KIND, true, PARTS>>(a, s);
+    return launch_large<LargeCfg<KIND, false, PARTS>>(a, s);
+}
+
 template <int KIND>
 static cudaError_t launch(const Bf16Args &a, cudaStream_t s) {
     // Rows an expert, and 128 x 256 tiles at least.  Small tiles: the least of 16, 32 rows
@@ -745,22 +825,21 @@ static cudaError_t launch(const Bf16Args &a, cudaStream_t s) {
     // (times of 1536 x 2048 in us, small and large: 128 experts of 24 rows 138 / 140, of 48
     // rows 135 / 144, of 64 rows 148 / 144; one of 64 rows 9.5 / 15.4, of 256 rows 11.7 / 15.7,
     // of 512 rows 15.9 / 16.0).
-    const int64_t rows = a.M / a.E, mean = a.offsets ? ((int64_t)a.M * 3 / 2 + a.E - 1) / a.E : a.M;
+    const int64_t mean = a.offsets ? ((int64_t)a.M * 3 / 2 + a.E - 1) / a.E : a.M;
     if (mean <= 16) return launch_small<SmallCfg<KIND, 16>>(a, s);
     if (mean <= 32) return launch_small<SmallCfg<KIND, 32>>(a, s);
     const int64_t most = (int64_t)a.M / 128 + (a.E < a.M ? a.E : a.M), tiles = most * ((a.N + 255) / 256);
     if (tiles <= device_info().num_sms / 6) return launch_small<SmallCfg<KIND, 64>>(a, s);
-    // CTA pairs where few of their 256 rows are past an expert's (single and pair: 128 experts
-    // of 96 rows 142 / 154, of 192 rows 184 / 176, of 256 rows 207 / 195, 8 of 4096 rows 139 / 124)
-    if (rows >= 192) return launch_large<LargeCfg<KIND, true>>(a, s);
-    return launch_large<LargeCfg<KIND, false>>(a, s);
+    // Several parts: fp32 results alone (K is 65536 at most)
+    if (a.y_dtype == ZFFN_DT_F32 && a.K > KB << FP32_PART_LOG) return launch_tiles<KIND, true>(a, s);
+    return launch_tiles<KIND, false>(a, s);
 }
 
 template <class C>
 static cudaError_t launch_weights(const Bf16GradArgs &a, cudaStream_t s) {
     Maps maps{};
     Params p{a.offsets, a.dw, a.err, a.M, a.N, a.K, a.E, (a.K + C::TN - 1) / C::TN, (a.N + C::TM - 1) / C::TM, a.dw_dtype == ZFFN_DT_BF16, 1,
-                   a.N % 64 == 0, a.K % 64 == 0, {}, FastDiv((a.K + C::TN - 1) / C::TN)};
+                   a.N % 64 == 0, a.K % 64 == 0, {}, FastDiv((a.K + C::TN - 1) / C::TN), part_log(a.dw_dtype)};
     p.each = C::Walk::divisor(p.m_tiles * p.n_tiles);
     for (int x = 0; x < 3; ++x)
         if (!encode(&maps.a[x], a.dy, 2, a.N, a.M, 1, 16 << x, false, p.wide_a ? 2 : 0) ||
@@ -783,8 +862,13 @@ cudaError_t launch_bf16_grad_w(const Bf16GradArgs &a, cudaStream_t s) {
     // CTA pairs where their tiles are four rounds at least (dw of 2056 x 1032, single and pair:
     // 128 experts of 24 rows 122 / 115 us, of 256 rows 260 / 228, one of 64 rows 6.5 / 7.5)
     const int64_t tiles = (int64_t)a.E * ((a.N + 255) / 256) * ((a.K + 255) / 256);
-    if (tiles >= 2 * (int64_t)device_info().num_sms) return launch_weights<LargeCfg<WEIGHTS, true>>(a, s);
-    return launch_weights<LargeCfg<WEIGHTS, false>>(a, s);
+    const bool pair = tiles >= 2 * (int64_t)device_info().num_sms;
+    // Several parts where an expert may have as many rows (how many it has the host does not know). A
+    // part's registers cost 1 to 3% (fp32 dw of 2048 x 1536, 128 experts of 128 rows 312 / 316 us; bf16,
+    // of 256 rows 197 / 202): of bf16 where cut sums could be seen in it.
+    const bool parts = a.dw_dtype == ZFFN_DT_F32 ? a.M > KB << FP32_PART_LOG : a.M > 1 << 18;
+    if (parts) return pair ? launch_weights<LargeCfg<WEIGHTS, true, true>>(a, s) : launch_weights<LargeCfg<WEIGHTS, false, true>>(a, s);
+    return pair ? launch_weights<LargeCfg<WEIGHTS, true, false>>(a, s) : launch_weights<LargeCfg<WEIGHTS, false, false>>(a, s);
 }
 
 }  // namespace zffn

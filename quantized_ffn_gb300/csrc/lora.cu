@@ -75,7 +75,10 @@ struct Params {
 // ---------------------------------------------------------------------------
 // Shrink on the tensor cores: 128 rows (on the MMA's M side) times all r rows of W.  The
 // blocks of a cluster share the contraction; rows 128 / split * i and on are added up by
-// rank i, in rank order.  A tile whose tokens follow one another (a packed sequence) is
+// rank i, in rank order.  The tensor core's adds drop what is below the accumulator's last
+// bit (65536 positive values: 3.5e-5 short, fp32 sums rounded to nearest 1e-7): stages past
+// the first 8 go to up to four accumulators, a share each, whose sums meet in registers.
+// A tile whose tokens follow one another (a packed sequence) is
 // loaded by TMA, another gathered by 16-byte copies.  (The copy engine's own gather takes
 // four rows of 128 bytes at a time, and about 100 clocks for it.)
 //
@@ -105,7 +108,7 @@ __global__ void __launch_bounds__(S_THREADS) shrink_kernel(const __grid_constant
     int *info = reinterpret_cast<int *>(j_full + 1);         // abort, TMEM base
     volatile int *abort_flag = info;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
-    const int r16 = up16(p.r), cols = r16 <= 32 ? 32 : r16 <= 64 ? 64 : 128;
+    const int r16 = up16(p.r), cols = r16 <= 32 ? 32 : r16 <= 64 ? 64 : 128, accs = cols <= 64 ? 4 : 2;
     if (tid == 0) {
         info[0] = 0;
         for (int i = 0; i < S_NS; ++i) { mbar_init(&s_full[i], 5); mbar_init(&s_empty[i], 1); }
@@ -119,7 +122,7 @@ __global__ void __launch_bounds__(S_THREADS) shrink_kernel(const __grid_constant
         prefetch_tensormap(&w);
     }
     if (warp == 5) {
-        tmem_alloc(reinterpret_cast<uint32_t *>(info + 1), cols);
+        tmem_alloc(reinterpret_cast<uint32_t *>(info + 1), cols * accs);
         tmem_relinquish();
         tc_fence_before();
     }
@@ -135,6 +138,7 @@ __global__ void __launch_bounds__(S_THREADS) shrink_kernel(const __grid_constant
     // this rank's stages: every split-th, so that the ranks read neighbouring columns at a time
     const int nkb = (blocks - (int)rank + (int)split - 1) / (int)split;
     auto block_of = [&](int i) { return i * (int)split + (int)rank; };
+    const int share = max(8, (nkb + accs - 1) / accs);       // stages of an accumulator
     const float scale = some && p.scale ? __ldcg(p.scale + wk.e) : 1.0f;
 
     // the tile's tokens, 4 lane + j, and whether they follow one another
@@ -213,8 +217,10 @@ __global__ void __launch_bounds__(S_THREADS) shrink_kernel(const __grid_constant
         // ---- MMA issuer
         const uint32_t idesc = idesc_bf16_f32(128, r16, false, MN);
         bool ok = true;
-        for (int i = 0; i < nkb; ++i) {
+        uint32_t dst = tmem;
+        for (int i = 0, at = 0; i < nkb; ++i, ++at) {
             const int s = i % S_NS;
+            if (at == share) at = 0, dst += cols;
             ok = bar_wait_warp(&s_full[s], (i / S_NS) & 1, abort_flag, p.err);
             if (!ok) break;
             tc_fence_after();
@@ -225,7 +231,7 @@ __global__ void __launch_bounds__(S_THREADS) shrink_kernel(const __grid_constant
 #pragma unroll
                 for (int k = 0; k < KB / 16; ++k) {
                     if (k >= n) break;
-                    tc_mma_bf16(tmem, xd + k * k_step(false), wd + k * k_step(MN), idesc, (i | k) != 0);
+                    tc_mma_bf16(dst, xd + k * k_step(false), wd + k * k_step(MN), idesc, (at | k) != 0);
                 }
                 tc_commit(&s_empty[s]);
                 if (i == nkb - 1) tc_commit(t_full);
@@ -254,6 +260,13 @@ __global__ void __launch_bounds__(S_THREADS) shrink_kernel(const __grid_constant
             if (some) {
                 tmem_ld_32x32b_x16(from + c, d);
                 tmem_ld_wait(d);
+                for (int i = share, a = cols; i < nkb; i += share, a += cols) {
+                    uint32_t more[16];
+                    tmem_ld_32x32b_x16(from + a + c, more);
+                    tmem_ld_wait(more);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) d[j] = __float_as_uint(__uint_as_float(d[j]) + __uint_as_float(more[j]));
+                }
             } else {
 #pragma unroll
                 for (int j = 0; j < 16; ++j) d[j] = 0;
@@ -320,7 +333,7 @@ __global__ void __launch_bounds__(S_THREADS) shrink_kernel(const __grid_constant
     if (some && split > 1) cluster_sync_all();               // (no block leaves while its rows are on their way)
     if (warp == 5) {
         tc_fence_after();
-        tmem_dealloc(tmem, cols);
+        tmem_dealloc(tmem, cols * accs);
     }
 }
 
@@ -635,6 +648,10 @@ __global__ void __launch_bounds__(E_THREADS, 1) expand_kernel(const __grid_const
 // warps 12 .. 15 take a tile out (32 columns of x each).
 // ---------------------------------------------------------------------------
 constexpr int O_THREADS = 512;
+// Stages of a part: the tensor core's adds drop what is below the accumulator's last bit (8192
+// positive values: 2.2e-6 short, 65536 3.5e-5), so that 4096 tokens at most are summed there; the sum of
+// the parts before is in tensor memory behind the first accumulator's columns.
+constexpr int PART = 64;
 
 template <int BOXES_>
 struct OuterCfg {
@@ -823,16 +840,18 @@ __global__ void __launch_bounds__(O_THREADS, 1) outer_kernel(const __grid_consta
     } else if (warp == 2) {
         // ---- MMA issuer: columns 0 .. 255 of the pieces, and those past them
         const int cols = 3 * r16, low = cols < 256 ? cols : 256;
-        const uint32_t idesc = idesc_bf16_f32(128, low, true, true), idesc_high = idesc_bf16_f32(128, C::WIDE ? cols - 256 : 16, true, true);
+        const uint32_t idesc = idesc_bf16_f32(128, low, true, true), idesc_high = idesc_bf16_f32(128, cols > 256 ? cols - 256 : 16, true, true);
+        const bool high = C::WIDE && cols > 256;
         uint32_t it = 0, acc = 0;
         bool ok = true;
         for (; ok && wk.get(); wk.t += gridDim.x) {
             const int ns = stages();
             if (ns == 0) continue;
-            const uint32_t b = acc % C::ACC, dst = tmem + b * C::ACC_COLS;
-            ok = acc < (uint32_t)C::ACC || bar_wait_warp(&t_empty[b], ((acc / C::ACC) & 1) ^ 1, abort_flag, p.err);
             for (int i = 0; i < ns; ++i, ++it) {
-                const uint32_t s = it % C::NS;
+                const uint32_t s = it % C::NS, b = acc % C::ACC, dst = tmem + b * C::ACC_COLS;
+                const int at = i % PART;                     // a part's first stage: 0
+                const bool last = at == PART - 1 || i == ns - 1;
+                if (at == 0) ok = acc < (uint32_t)C::ACC || bar_wait_warp(&t_empty[b], ((acc / C::ACC) & 1) ^ 1, abort_flag, p.err);
                 ok = ok && bar_wait_warp(&s_full[s], (it / C::NS) & 1, abort_flag, p.err);
                 if (!ok) break;
                 tc_fence_after();
@@ -841,15 +860,15 @@ __global__ void __launch_bounds__(O_THREADS, 1) outer_kernel(const __grid_consta
                 const uint64_t xd = smem_desc_mn_sw128(sx, 8192), vd = smem_desc_mn_sw128(sv, 8192), vh = smem_desc_mn_sw128(sv + 4 * 8192, 8192);
                 if (elect_one()) {
                     for (int k = 0; k < n; ++k) {
-                        tc_mma_bf16(dst, xd + k * k_step(true), vd + k * k_step(true), idesc, (i | k) != 0);
-                        if constexpr (C::WIDE) tc_mma_bf16(dst + 256, xd + k * k_step(true), vh + k * k_step(true), idesc_high, (i | k) != 0);
+                        tc_mma_bf16(dst, xd + k * k_step(true), vd + k * k_step(true), idesc, (at | k) != 0);
+                        if (high) tc_mma_bf16(dst + 256, xd + k * k_step(true), vh + k * k_step(true), idesc_high, (at | k) != 0);
                     }
                     tc_commit(&s_empty[s]);
-                    if (i == ns - 1) tc_commit(&t_full[b]);
+                    if (last) tc_commit(&t_full[b]);
                 }
                 __syncwarp();
+                acc += last;
             }
-            ++acc;
             ok = __all_sync(0xffffffffu, ok && !*abort_flag);
         }
         // (what was issued is waited for by the warps that take it out; a launch that gave up
@@ -860,64 +879,78 @@ __global__ void __launch_bounds__(O_THREADS, 1) outer_kernel(const __grid_consta
         }
     } else if (warp >= 12) {
         // ---- take out, add the three pieces' sums, write: thread = one column of x
-        const uint32_t from = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t from = tmem + ((uint32_t)((warp & 3) * 32) << 16), sums = from + 3 * r16;   // of the parts before
         uint32_t acc = 0;
         for (bool ok = true; ok && wk.get(); wk.t += gridDim.x) {
-            const bool some = wk.rows > 0;
-            const uint32_t b = acc % C::ACC;
-            if (some) {
-                ok = bar_wait_warp(&t_full[b], (acc / C::ACC) & 1, abort_flag, p.err);
-                if (!ok) break;
-                tc_fence_after();
-                ++acc;
-            }
+            const int parts = (stages() + PART - 1) / PART;
+            const bool some = parts > 0;
             const OuterJob &job = wk.nt < ja.n_tiles ? ja : jb;
             const int c = (wk.nt < ja.n_tiles ? wk.nt : wk.nt - ja.n_tiles) * 128 + (warp & 3) * 32 + lane;
             void *d = job.d;
-            for (int j0 = 0; j0 < p.r; j0 += 16) {
-                uint32_t w[16];
+            for (int i = 0; i == 0 || i < parts; ++i) {
+                const uint32_t b = acc % C::ACC;
                 if (some) {
-                    uint32_t w1[16], w2[16];
-                    tmem_ld_32x32b_x16(from + b * C::ACC_COLS + j0, w);
-                    tmem_ld_32x32b_x16(from + b * C::ACC_COLS + r16 + j0, w1);
-                    tmem_ld_32x32b_x16(from + b * C::ACC_COLS + 2 * r16 + j0, w2);
-                    tmem_ld_wait(w);
-                    tmem_ld_wait(w1);
-                    tmem_ld_wait(w2);
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) w[j] = __float_as_uint(__uint_as_float(w[j]) + (__uint_as_float(w1[j]) + __uint_as_float(w2[j])));
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) w[j] = 0;
+                    ok = bar_wait_warp(&t_full[b], (acc / C::ACC) & 1, abort_flag, p.err);
+                    if (!ok) break;
+                    tc_fence_after();
+                    ++acc;
                 }
-                if (c >= job.C) continue;
-                if (job.transposed) {  // d [L][C][r]
-                    const int64_t at = ((int64_t)wk.e * job.C + c) * p.r + j0;
+                for (int j0 = 0; j0 < p.r; j0 += 16) {
+                    uint32_t w[16];
+                    if (some) {
+                        uint32_t w1[16], w2[16];
+                        tmem_ld_32x32b_x16(from + b * C::ACC_COLS + j0, w);
+                        tmem_ld_32x32b_x16(from + b * C::ACC_COLS + r16 + j0, w1);
+                        tmem_ld_32x32b_x16(from + b * C::ACC_COLS + 2 * r16 + j0, w2);
+                        tmem_ld_wait(w);
+                        tmem_ld_wait(w1);
+                        tmem_ld_wait(w2);
 #pragma unroll
-                    for (int j = 0; j < 16; j += 8) {
-                        if (j0 + j >= p.r) break;
-                        if (d_bf16) {
-                            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(d) + at + j) =
-                                make_uint4(bf16x2(w[j], w[j + 1]), bf16x2(w[j + 2], w[j + 3]), bf16x2(w[j + 4], w[j + 5]), bf16x2(w[j + 6], w[j + 7]));
-                        } else {
-                            *reinterpret_cast<uint4 *>(static_cast<float *>(d) + at + j) = make_uint4(w[j], w[j + 1], w[j + 2], w[j + 3]);
-                            *reinterpret_cast<uint4 *>(static_cast<float *>(d) + at + j + 4) = make_uint4(w[j + 4], w[j + 5], w[j + 6], w[j + 7]);
+                        for (int j = 0; j < 16; ++j) w[j] = __float_as_uint(__uint_as_float(w[j]) + (__uint_as_float(w1[j]) + __uint_as_float(w2[j])));
+                        if (i > 0) {
+                            tmem_ld_32x32b_x16(sums + j0, w1);
+                            tmem_ld_wait(w1);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) w[j] = __float_as_uint(__uint_as_float(w1[j]) + __uint_as_float(w[j]));
+                        }
+                        if (i < parts - 1) {
+                            tmem_st_32x32b_x16(sums + j0, w);
+                            continue;
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) w[j] = 0;
+                    }
+                    if (c >= job.C) continue;
+                    if (job.transposed) {  // d [L][C][r]
+                        const int64_t at = ((int64_t)wk.e * job.C + c) * p.r + j0;
+#pragma unroll
+                        for (int j = 0; j < 16; j += 8) {
+                            if (j0 + j >= p.r) break;
+                            if (d_bf16) {
+                                *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(d) + at + j) =
+                                    make_uint4(bf16x2(w[j], w[j + 1]), bf16x2(w[j + 2], w[j + 3]), bf16x2(w[j + 4], w[j + 5]), bf16x2(w[j + 6], w[j + 7]));
+                            } else {
+                                *reinterpret_cast<uint4 *>(static_cast<float *>(d) + at + j) = make_uint4(w[j], w[j + 1], w[j + 2], w[j + 3]);
+                                *reinterpret_cast<uint4 *>(static_cast<float *>(d) + at + j + 4) = make_uint4(w[j + 4], w[j + 5], w[j + 6], w[j + 7]);
+                            }
+                        }
+                    } else {               // d [L][r][C]
+                        const int64_t at = ((int64_t)wk.e * p.r + j0) * job.C + c;
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            if (j0 + j >= p.r) break;
+                            if (d_bf16) static_cast<__nv_bfloat16 *>(d)[at + (int64_t)j * job.C] = __float2bfloat16_rn(__uint_as_float(w[j]));
+                            else static_cast<float *>(d)[at + (int64_t)j * job.C] = __uint_as_float(w[j]);
                         }
                     }
-                } else {               // d [L][r][C]
-                    const int64_t at = ((int64_t)wk.e * p.r + j0) * job.C + c;
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        if (j0 + j >= p.r) break;
-                        if (d_bf16) static_cast<__nv_bfloat16 *>(d)[at + (int64_t)j * job.C] = __float2bfloat16_rn(__uint_as_float(w[j]));
-                        else static_cast<float *>(d)[at + (int64_t)j * job.C] = __uint_as_float(w[j]);
-                    }
                 }
-            }
-            if (some) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&t_empty[b]);
+                if (some) {
+                    if (i < parts - 1) tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&t_empty[b]);
+                }
             }
         }
     }
@@ -1154,7 +1187,8 @@ cudaError_t launch_lora_outer(const LoraPlan &q, const void *dv16, const void *x
     if (!encode_fn()) return cudaErrorNotSupported;
     OuterJob a, b;
     if (!outer_job(&a, q, dv16, x, dA, K, false) || !outer_job(&b, q, v16, dy, dB, N, true)) return cudaErrorInvalidValue;
-    const int boxes = pieces_pitch(q.r) / 64;
+    // (several parts: columns for their sum as well, so that one accumulator alone has room from r = 72)
+    const int boxes = q.T > PART * KB && 4 * up16(q.r) > 256 ? 6 : pieces_pitch(q.r) / 64;
     return boxes <= 2 ? outer<2>(q, a, b, dtype, s) : boxes <= 4 ? outer<4>(q, a, b, dtype, s) : outer<6>(q, a, b, dtype, s);
 }
 
