@@ -475,8 +475,9 @@ zffn_status zffn_moe_swiglu_fp8(const void *x, const int32_t *expert_ids,
  * gradients, SwiGLU with its gradient, and low-rank adapters beside a
  * projection of any kind.  Operands are bf16, every sum is fp32 and every result
  * is rounded once.  The source pages have no counterpart of these entry points.
- * None takes library workspace (the adapters take the caller's), so calls on several streams may overlap as long
- * as their arguments do not.
+ * None takes library workspace (the adapters take the caller's), so calls on several
+ * streams may overlap as long as their arguments do not.  An output overlaps no other
+ * argument but where it says so.
  * ------------------------------------------------------------------------- */
 
 /* Product of bf16 matrices, dense or grouped by expert:
@@ -495,7 +496,7 @@ zffn_status zffn_moe_swiglu_fp8(const void *x, const int32_t *expert_ids,
  * Requirements: 1 <= M <= 2^24, 1 <= N <= 65536, 8 <= K <= 65536, K % 8 == 0 (with
  * transposed also N % 8 == 0), 1 <= E <= 4096; a and w 16-byte aligned, offsets
  * 4-byte, y to its element (a 16-byte aligned y with rows of 16-byte multiples is
- * written faster).  y may not overlap a or w.
+ * written faster).
  * Errors: INVALID_ARG, CUDA. */
 zffn_status zffn_bf16_matmul(const void *a, const void *w, const int32_t *offsets, int transposed,
                              int y_dtype, void *y, int M, int N, int K, int E, void *stream);
@@ -540,7 +541,7 @@ zffn_status zffn_swiglu_grad(int dtype, const void *dh, const void *gu, void *dg
  *     whose row_slot is outside [0, T) and a token whose slot_row is are of no adapter;
  *     the two must name each other otherwise.
  *   base: dtype (zffn_dtype) [T][N], or NULL for zeros.  out: dtype [T][N]; it may be
- *     base (tokens of no adapter are then left alone), and may not overlap it otherwise.
+ *     base (tokens of no adapter are then left alone).
  *   v: output, fp32 [T][r], the sorted rows' (0 from offsets[L] on): what
  *     zffn_lora_grad needs again.
  *   work: zffn_lora_work_bytes(T, r, L, 0) bytes of the caller's, for the call (NULL
