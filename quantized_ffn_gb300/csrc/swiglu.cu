@@ -91,8 +91,9 @@ __global__ void __launch_bounds__(THREADS) swiglu_grad_kernel(const Pack<T, V> *
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const float x = value(g[k].v[j]), s = logistic<T>(x), y = value(d[k].v[j]);
-            put(dg.v[j], y * value(u[k].v[j]) * s * (1.0f + x * (1.0f - s)));
-            put(du.v[j], y * x * s);
+            // (the slope first, at most 1.1: a product of dh and u or g could overflow where the result does not)
+            put(dg.v[j], y * (value(u[k].v[j]) * (s * (1.0f + x * (1.0f - s)))));
+            put(du.v[j], y * (x * s));
         }
         dgu[at[k]] = dg;
         dgu[at[k] + cols.d] = du;
