@@ -14,6 +14,9 @@
 // rows of r = 32: 62 us for both outer products).
 #include <atomic>
 
+#include <algorithm>
+#include <type_traits>
+
 #include "bf16.h"
 #include "groups.cuh"
 #include "launch.cuh"
@@ -987,11 +990,14 @@ __device__ __forceinline__ int group_of(const int32_t *offsets, int L, int T, in
     if (threadIdx.x == 0) *sh = L + 1;
     __syncthreads();
     int first = L + 1;
-    for (int g = threadIdx.x; g <= L; g += blockDim.x)
-        if (__ldcg(offsets + g) > row) {
-            first = g;
-            break;
-        }
+    for (int g = threadIdx.x; g <= L && first > L; g += 4 * blockDim.x) {
+        int o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = __ldcg(offsets + min(L, g + i * (int)blockDim.x));
+#pragma unroll
+        for (int i = 3; i >= 0; --i)
+            if (o[i] > row) first = min(L, g + i * (int)blockDim.x);
+    }
     first = __reduce_min_sync(0xffffffffu, first);
     if ((threadIdx.x & 31) == 0 && first <= L) atomicMin(sh, first);
     __syncthreads();
@@ -1006,12 +1012,15 @@ __device__ __forceinline__ float dot8(uint4 a, uint4 b, float s) {
     return s;
 }
 
-// A warp for one value of v: blocks (row, 8 of r).
-__global__ void __launch_bounds__(256) shrink_row_kernel(const Params p, const __nv_bfloat16 *x, const __nv_bfloat16 *w, float *v) {
+// PARTS warps for one value of v: blocks (row, 8 of r).  Two where the blocks are few (61 tokens
+// of 48 adapters, K = 4096, r = 16, with expand: 10.5 us, one 12.0; 128 of 64, r = 64: 59.9 / 56.7).
+template <int PARTS>
+__global__ void __launch_bounds__(256 * PARTS) shrink_row_kernel(const Params p, const __nv_bfloat16 *x, const __nv_bfloat16 *w, float *v) {
     __shared__ int sh;
+    __shared__ float sums[8 * PARTS];
     grid_wait();
     grid_launch_dependents();
-    const int row = blockIdx.x, j = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const int row = blockIdx.x, warp = threadIdx.x >> 5, part = warp >> 3, j = blockIdx.y * 8 + (warp & 7), lane = threadIdx.x & 31;
     const int t = __ldcg(p.row_slot + row);
     const int e = group_of(p.offsets, p.L, p.T, row, &sh);
     if (e < 0) return;
@@ -1019,9 +1028,9 @@ __global__ void __launch_bounds__(256) shrink_row_kernel(const Params p, const _
     if (e < p.L && (unsigned)t < (unsigned)p.T) {
         const uint4 *a = reinterpret_cast<const uint4 *>(x + (int64_t)t * p.C);
         const uint4 *b = reinterpret_cast<const uint4 *>(w + ((int64_t)e * p.r + j) * p.C);
-        const int n = p.C / 8;
+        const int each = (p.C / 8 + PARTS - 1) / PARTS, n = min(p.C / 8, each * (part + 1));
         float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        int c = lane;
+        int c = each * part + lane;
         for (; c + 7 * 32 < n; c += 8 * 32) {
             uint4 fa[8], fb[8];
 #pragma unroll
@@ -1033,9 +1042,14 @@ __global__ void __launch_bounds__(256) shrink_row_kernel(const Params p, const _
         sum = (s[0] + s[1]) + (s[2] + s[3]);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (p.scale) sum *= __ldcg(p.scale + e);
     }
-    if (lane == 0) v[(int64_t)row * p.r + j] = sum;
+    if constexpr (PARTS > 1) {
+        if (lane == 0) sums[warp] = sum;
+        __syncthreads();
+        if (part) return;
+        for (int k = 1; k < PARTS; ++k) sum += sums[warp + 8 * k];
+    }
+    if (lane == 0) v[(int64_t)row * p.r + j] = p.scale && e < p.L ? sum * __ldcg(p.scale + e) : sum;
 }
 
 constexpr int R_THREADS = 128;
@@ -1097,6 +1111,68 @@ __global__ void __launch_bounds__(R_THREADS) expand_row_kernel(const Params p, c
     }
 }
 
+// The same where r / 8 is a power of two, q: lane l of a load of 512 bytes of W's rows takes 16
+// of them, ranks 8 (l % q) and on of column l / q, whose sums the q lanes join.  A block takes
+// several runs of columns where the blocks are many more than run at once (N = 11008: 61
+// tokens of 48 adapters, r = 16, 8.6 us with shrink, by two columns a thread 9.2; 512 of 64 37.9 /
+// 48.4; 128 of 64, r = 64, 46.5 / 56.2).
+template <typename O>
+__global__ void __launch_bounds__(R_THREADS) expand_lane_kernel(const Params p, const float *v, const __nv_bfloat16 *w, const O *base, O *out, int q_log) {
+    __shared__ int sh;
+    constexpr int LOADS = 8;
+    const int t = blockIdx.x, lane = threadIdx.x & 31, q = 1 << q_log, k = lane & (q - 1), row = __ldcg(p.slot_row + t);
+    const int e = (unsigned)row < (unsigned)p.T ? group_of(p.offsets, p.L, p.T, row, &sh) : p.L;
+    const bool mine = e >= 0 && e < p.L;
+    const int all = p.C << q_log, step = gridDim.y * (R_THREADS * LOADS);     // 16-byte pieces of W[e]
+    const uint4 *from = reinterpret_cast<const uint4 *>(w) + (int64_t)e * all;
+    const O *old = base + (int64_t)t * p.C;
+    O *to = out + (int64_t)t * p.C;
+    float vs[8];
+    bool waited = false;
+    for (int c0 = (blockIdx.y * (R_THREADS / 32) + (threadIdx.x >> 5)) * (32 * LOADS); !waited || c0 < all; c0 += step) {
+        uint4 f[LOADS];
+        float b[LOADS];
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) {
+            const int c = c0 + i * 32 + lane;
+            f[i] = mine && c < all ? __ldcg(from + c) : make_uint4(0, 0, 0, 0);
+            b[i] = 0.0f;
+            if (base && (i & (q - 1)) == k && c < all) {
+                if constexpr (sizeof(O) == 2) b[i] = __uint_as_float((uint32_t)__ldcg(reinterpret_cast<const uint16_t *>(old) + (c >> q_log)) << 16);
+                else b[i] = __ldcg(old + (c >> q_log));
+            }
+        }
+        if (!waited) {
+            grid_wait();
+            grid_launch_dependents();
+            if (mine) {
+                const float4 lo = __ldcg(reinterpret_cast<const float4 *>(v + (int64_t)row * p.r + k * 8)), hi = __ldcg(reinterpret_cast<const float4 *>(v + (int64_t)row * p.r + k * 8 + 4));
+                vs[0] = lo.x; vs[1] = lo.y; vs[2] = lo.z; vs[3] = lo.w;
+                vs[4] = hi.x; vs[5] = hi.y; vs[6] = hi.z; vs[7] = hi.w;
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) vs[i] = 0.0f;
+            }
+            waited = true;
+        }
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) {
+            float s = lo_f32(f[i].x) * vs[0];
+            s = fmaf(hi_f32(f[i].x), vs[1], s); s = fmaf(lo_f32(f[i].y), vs[2], s); s = fmaf(hi_f32(f[i].y), vs[3], s);
+            s = fmaf(lo_f32(f[i].z), vs[4], s); s = fmaf(hi_f32(f[i].z), vs[5], s); s = fmaf(lo_f32(f[i].w), vs[6], s); s = fmaf(hi_f32(f[i].w), vs[7], s);
+#pragma unroll
+            for (int o = 1; o < 16; o <<= 1)
+                if (o < q) s += __shfl_xor_sync(0xffffffffu, s, o);
+            const int c = c0 + i * 32 + lane;
+            if ((i & (q - 1)) == k && c < all && (mine || out != base)) {   // (of the q lanes that have the sum one)
+                const float y = mine ? b[i] + s : b[i];
+                if constexpr (sizeof(O) == 2) to[c >> q_log] = __float2bfloat16_rn(y);
+                else to[c >> q_log] = y;
+            }
+        }
+    }
+}
+
 // ---- host -------------------------------------------------------------------
 
 static Params params(const LoraPlan &q, int C) { return Params{q.row_slot, q.slot_row, q.offsets, q.scale, q.err, q.T, q.r, q.L, C, FastDiv(1), FastDiv(up16(q.r) / 4), FastDiv(3 * up16(q.r) / 8)}; }
@@ -1104,9 +1180,11 @@ static Params params(const LoraPlan &q, int C) { return Params{q.row_slot, q.slo
 static int64_t row_tiles(const LoraPlan &q) { return q.T / 128 + (q.L + 1 < q.T ? q.L + 1 : q.T); }
 // Whether a forward pass goes row by row: each row reads its adapter through L2 again, where
 // the tensor cores' kernels take a tile for each adapter, however few its rows (4096 -> 11008,
-// us by rows and by tiles: 61 tokens of 48 adapters, r = 16: 10 / 52, 256 of 64: 23 / 73,
-// 64 of 4: 10 / 15, 512 of 4: 46 / 19, 64 of 4 with r = 64: 28 / 18).
-static bool few(int T, int r, int L) { return (int64_t)T * r <= 1024 + 160 * (int64_t)(L < T ? L : T); }
+// us by rows and by tiles: 61 tokens of 48 adapters, r = 16: 9 / 52, 512 of 64: 37 / 76, 256 of 16:
+// 20 / 27, 512 of 16: 37 / 28, 64 of 1 with r = 32: 14 / 11; r = 24 and the like, two columns a
+// thread, take a third longer by rows).
+static bool lane_wide(int r) { return (r & (r - 1)) == 0; }   // r is a multiple of 8
+static bool few(int T, int r, int L) { return (int64_t)T * r <= 1024 + (lane_wide(r) ? 256 : 160) * (int64_t)(L < T ? L : T); }
 
 template <bool MN>
 static cudaError_t shrink(const LoraPlan &q, const void *x, const void *w, float *v, void *v16, const float *other, void *other16, int C, cudaStream_t s) {
@@ -1194,15 +1272,24 @@ cudaError_t launch_lora_expand(const LoraPlan &q, const void *v16, const void *w
 cudaError_t launch_lora_rows(const LoraPlan &q, const void *x, const void *A, const void *B, int dtype, const void *base, void *out, float *v, int N, int K,
                              cudaStream_t s) {
     using namespace lora;
-    const __nv_bfloat16 *b16 = static_cast<const __nv_bfloat16 *>(B);
-    const cudaError_t e = launch_dependent(shrink_row_kernel, dim3((unsigned)q.T, (unsigned)(q.r / 8)), 256, 0, 1, s, params(q, K),
-                                           static_cast<const __nv_bfloat16 *>(x), static_cast<const __nv_bfloat16 *>(A), v);
+    const __nv_bfloat16 *x16 = static_cast<const __nv_bfloat16 *>(x), *a16 = static_cast<const __nv_bfloat16 *>(A), *b16 = static_cast<const __nv_bfloat16 *>(B);
+    const int64_t sms = device_info().num_sms;
+    const dim3 rows((unsigned)q.T, (unsigned)(q.r / 8));
+    const cudaError_t e = (int64_t)rows.x * rows.y <= 2 * sms ? launch_dependent(shrink_row_kernel<2>, rows, 512, 0, 1, s, params(q, K), x16, a16, v)
+                                                         : launch_dependent(shrink_row_kernel<1>, rows, 256, 0, 1, s, params(q, K), x16, a16, v);
     if (e != cudaSuccess) return e;
-    const dim3 grid((unsigned)q.T, (unsigned)((N + 2 * R_THREADS - 1) / (2 * R_THREADS)));
-    if (dtype == ZFFN_DT_BF16)
-        return launch_dependent(expand_row_kernel<__nv_bfloat16>, grid, R_THREADS, 0, 1, s, params(q, N), v, b16, static_cast<const __nv_bfloat16 *>(base),
-                                static_cast<__nv_bfloat16 *>(out));
-    return launch_dependent(expand_row_kernel<float>, grid, R_THREADS, 0, 1, s, params(q, N), v, b16, static_cast<const float *>(base), static_cast<float *>(out));
+    auto expand = [&](auto *to) {
+        using O = std::remove_pointer_t<decltype(to)>;
+        const O *from = static_cast<const O *>(base);
+        if (lane_wide(q.r)) {
+            const int g = q.r / 8;
+            const int64_t chunks = ((int64_t)N * g + 8 * R_THREADS - 1) / (8 * R_THREADS), at_once = std::max<int64_t>(1, 12 * sms / q.T);
+            const int64_t turns = (chunks + at_once - 1) / at_once;
+            return launch_dependent(expand_lane_kernel<O>, dim3((unsigned)q.T, (unsigned)((chunks + turns - 1) / turns)), R_THREADS, 0, 1, s, params(q, N), v, b16, from, to, __builtin_ctz(g));
+        }
+        return launch_dependent(expand_row_kernel<O>, dim3((unsigned)q.T, (unsigned)((N + 2 * R_THREADS - 1) / (2 * R_THREADS))), R_THREADS, 0, 1, s, params(q, N), v, b16, from, to);
+    };
+    return dtype == ZFFN_DT_BF16 ? expand(static_cast<__nv_bfloat16 *>(out)) : expand(static_cast<float *>(out));
 }
 
 cudaError_t launch_lora_outer(const LoraPlan &q, const void *dv16, const void *x, void *dA, int K, const void *v16, const void *dy, void *dB, int N, int dtype,
