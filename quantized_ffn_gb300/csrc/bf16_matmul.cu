@@ -71,7 +71,7 @@ struct LargeCfg {
     static constexpr int OUT_BYTES = 4096;                   // a warp's box of 32 rows x 128 bytes
     static constexpr int OFF_OUT = NS * STAGE;
     static constexpr int OFF_BAR = OFF_OUT + EPI * OUT_BYTES;
-    static constexpr int SMEM = OFF_BAR + (3 * NS + 5) * 8 + 8 + 1024;
+    static constexpr int SMEM = OFF_BAR + (3 * NS + 5) * 8 + 16 + 1024;
     using Walk = GroupWalk<TM, 8, KIND == WEIGHTS>;
 };
 
@@ -82,14 +82,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
     uint64_t *s_full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
     uint64_t *s_empty = s_full + C::NS, *t_full = s_empty + C::NS, *t_empty = t_full + 2, *done = t_empty + 2;
     uint64_t *cut_full = done + 1;                           // weights: an expert's last rows
-    int *info = reinterpret_cast<int *>(cut_full + C::NS);   // abort, TMEM base
-    volatile int *abort_flag = info;
+    int *info = reinterpret_cast<int *>(cut_full + C::NS);   // abort, TMEM base, stages that the loads have begun
+    volatile int *abort_flag = info, *begun = info + 2;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = C::PAIR ? (int)cluster_ctarank() : 0;
     constexpr bool GRAD = C::KIND == WEIGHTS;
 
     if (warp == C::EPI && lane == 0) {
-        info[0] = 0;
+        info[0] = info[2] = 0;
         for (int i = 0; i < C::NS; ++i) {
             mbar_init(&s_full[i], GRAD && C::PAIR ? 2 : 1);
             mbar_init(&s_empty[i], 1);
@@ -153,6 +153,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
                 if (it >= C::NS && !bar_wait(&s_empty[s], ((it / C::NS) & 1) ^ 1, abort_flag, p.err)) { ok = false; break; }
                 uint8_t *sa = smem + s * C::STAGE, *sw = sa + C::A_BYTES;
                 if constexpr (GRAD) {
+                    *begun = (int)it;
                     // (of an expert's last rows no more than the MMA takes, or half as many again)
                     const int row = wk.row0 + i * KB, x = box_of(steps(i)), bytes = 2048 << x;
                     constexpr int WB = C::W_ROWS / 64;
@@ -273,7 +274,16 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
             const int n = nb ? steps(nb - 1) : 0, valid = wk.rows - (nb - 1) * KB;
             if (valid >= n * 16) continue;
             const uint32_t s = (it - 1) % C::NS;
-            ok = bar_wait_warp(&cut_full[s], (phases >> s) & 1, abort_flag, p.err);
+            // (the next such stage may be seconds away: the bound counts from the last stage begun)
+            for (int tries = 0, at = *begun; !bar_test(&cut_full[s], (phases >> s) & 1); ++tries) {
+                if (tries > (1 << 26)) {
+                    const int now = *begun;
+                    if (now == at) record_error(p.err, ZFFN_ERR_TIMEOUT), *abort_flag = 1;
+                    tries = 0, at = now;
+                }
+                if ((tries & 1023) == 1023 && *abort_flag) { ok = false; break; }
+            }
+            ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             phases ^= 1u << s;
             const uint32_t sa = smem_u32(smem) + s * C::STAGE;
