@@ -3,7 +3,7 @@
 Each translation unit under csrc/ is compiled by nvcc in parallel, then linked
 into quantized_ffn_gb300/_lib/libzffn.so (CUDA runtime linked statically; the
 driver entry point used for TMA descriptors is looked up at run time).  The
-Python binding of the 8-bit entry points (csrc/binding.cpp) is compiled by the
+Python binding of the 8-bit, bf16 and adapter entry points (csrc/binding.cpp) is compiled by the
 host compiler against the installed torch into _lib/_zffn_native.so; where that
 fails, build() warns and the library stands alone.
 """
