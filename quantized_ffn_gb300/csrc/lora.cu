@@ -834,11 +834,12 @@ __global__ void __launch_bounds__(O_THREADS, 1) outer_kernel(const __grid_consta
                         copy16(dst + s * C::STAGE + j * 2048, there ? job.x + (int64_t)tok * job.C + col : job.x, there);
                     }
                     const uint32_t to = smem_u32(smem) + s * C::STAGE + 16384;
-                    for (int q0 = 0; q0 < KB * wide; q0 += 256) {
+                    const int pieces = min(KB, (wk.rows - i * KB + 15) / 16 * 16) * wide;   // (rows past those: no MMA takes)
+                    for (int q0 = 0; q0 < pieces; q0 += 256) {
                         const int q = q0 + me, row = min(by_wide.div(q), KB - 1), c = q - row * wide;
                         const int t0 = __shfl_sync(0xffffffffu, t[0], row & 31), t1 = __shfl_sync(0xffffffffu, t[1], row & 31);
                         const bool there = (unsigned)(row < 32 ? t0 : t1) < (unsigned)p.T;
-                        if (q < KB * wide)
+                        if (q < pieces)
                             copy16(to + (c >> 3) * 8192 + row * 128 + (((c & 7) ^ (row & 7)) << 4),
                                    there ? job.v16 + (int64_t)(wk.row0 + i * KB + row) * pieces_pitch(p.r) + c * 8 : job.v16, there);
                     }
