@@ -546,7 +546,8 @@ zffn_status zffn_swiglu_grad(int dtype, const void *dh, const void *gu, void *dg
  *     zffn_lora_grad needs again.
  *   work: zffn_lora_work_bytes(T, r, L, 0) bytes of the caller's, for the call (NULL
  *     where that is 0).
- * Both products have fp32 sums; v is not rounded to fewer bits between them.
+ * Both products have fp32 sums; v is not rounded to fewer bits between them.  Where v is
+ * infinite or NaN, its token's out is infinite or NaN (which of them is not said).
  * Requirements: 1 <= T <= 2^24, K and N multiples of 8 in [8, 65536], r a multiple
  * of 8 in [8, 128], 1 <= L <= 4096; x, A, B, base, out, v and work 16-byte aligned,
  * the others 4-byte.  Errors: INVALID_ARG, CUDA. */
