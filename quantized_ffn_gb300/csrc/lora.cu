@@ -419,9 +419,18 @@ __global__ void __launch_bounds__(E_THREADS, 1) expand_kernel(const __grid_const
     // one start after the grids before it had ended)
     GroupWalk<128, 1> wk;
     wk.start(p.offsets, p.T, p.L, 1, p.each, false, 0);
-    // (G blocks to a row tile, as many as run at once: of the tiles that there are, where 32
-    // groups hold them all, else of those that there may be)
-    if (p.L <= 32) G = max(1, sms / max(1, __shfl_sync(0xffffffffu, wk.inc, 31)));
+    // (G blocks to a row tile, as many as run at once: of the tiles that there are, else, past 128
+    // groups, whose counting would take microseconds, of those that there may be; 2048 tokens of
+    // 64 adapters, r = 16: 151 us by those that there may be)
+    if (p.L <= 128) {
+        int tiles = __shfl_sync(0xffffffffu, wk.inc, 31);
+        while (wk.e0 + 32 <= p.L) {
+            wk.hold(wk.e0 + 32);
+            tiles += __shfl_sync(0xffffffffu, wk.inc, 31);
+        }
+        if (wk.e0) wk.start(p.offsets, p.T, p.L, 1, p.each, false, 0);
+        G = max(1, sms / max(1, tiles));
+    }
     wk.t = blockIdx.x / G;
     const bool have = wk.get();
     const int n_tiles = (p.C + C::TN - 1) / C::TN, g = blockIdx.x % G;
