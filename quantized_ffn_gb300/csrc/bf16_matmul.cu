@@ -721,7 +721,7 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) small_kernel(const __gr
 // last bit, so that a long sum comes out short (fp32 results of positive values: of 2048 3.8e-7, of 8192
 // 2.2e-6, of 65536 3.5e-5; of signed ones 2.3e-7, 1e-6, 1e-5).  Parts of 512, joined in fp32 registers
 // that round to nearest, hold it at 9e-7 (signed: 5e-7).  Of a bf16 result, whose rounding is 4e-3, a
-// part is 4096.
+// part is 4096 (y's on large tiles are one part: K is 65536 at most).
 constexpr int FP32_PART_LOG = 3, BF16_PART_LOG = 6;
 static int part_log(int dtype) { return dtype == ZFFN_DT_BF16 ? BF16_PART_LOG : FP32_PART_LOG; }
 
