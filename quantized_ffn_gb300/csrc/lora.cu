@@ -1075,7 +1075,7 @@ constexpr int R_THREADS = 128;
 template <typename O>
 __global__ void __launch_bounds__(R_THREADS) expand_row_kernel(const Params p, const float *v, const __nv_bfloat16 *w, const O *base, O *out) {
     __shared__ int sh;
-    __shared__ float vs[128];
+    __shared__ __align__(16) float vs[128];   // (read 16 bytes at a time)
     const int t = blockIdx.x, n = blockIdx.y * (2 * R_THREADS) + threadIdx.x * 2, row = __ldcg(p.slot_row + t);
     const bool some = (unsigned)row < (unsigned)p.T;
     const int e = some ? group_of(p.offsets, p.L, p.T, row, &sh) : p.L;
