@@ -518,7 +518,9 @@ zffn_status zffn_bf16_matmul_grad_w(const void *dy, const void *a, const int32_t
  *   gu: dtype (zffn_dtype) [rows][2 I].  h: dtype [rows][I].
  * Any rows, I >= 1 (rows <= 2^31 - 1, I <= 2^20), pointers aligned to their element
  * (16-byte aligned ones with rows of 16-byte multiples are faster).
- * Infinities and NaN as the formula has them in IEEE arithmetic (silu(-inf) is NaN).
+ * Infinities and NaN as the formula has them in IEEE arithmetic (silu(-inf) is NaN).  For g
+ * far below zero the factors are multiplied in 64 bits, here and in the gradient: h is right
+ * wherever it is within fp32's range, although silu(g) alone may be below it.
  * Errors: INVALID_ARG, CUDA. */
 zffn_status zffn_swiglu(int dtype, const void *gu, void *h, int64_t rows, int64_t I, void *stream);
 

@@ -15,10 +15,10 @@ constexpr int THREADS = 256;
 // 4.6 us, two 5.0, one 8.6).
 constexpr int together(int bytes) { return bytes == 16 ? 2 : 4; }
 
-// 1 / (1 + e^-g).  fp32: by the exponential and the division of the language.  bf16: by the
-// special function unit's two instructions (off by (3 + |g| / 3) 2^-22 of the value at most,
-// and 0 below g = -87.3, where silu is above -1.1e-36), since a result keeps 2^-8: the other
-// form's 40 instructions a value would take longer than its bytes (27 us for 32768 x 768).
+// 1 / (1 + e^-g) for g >= FAR.  fp32: by the exponential and the division of the language.  bf16:
+// by the special function unit's two instructions (off by (3 + |g| / 3) 2^-22 of the value at
+// most), since a result keeps 2^-8: the other form's 40 instructions a value would take longer
+// than its bytes (27 us for 32768 x 768).
 template <typename T> __device__ __forceinline__ float logistic(float g);
 template <> __device__ __forceinline__ float logistic<float>(float g) { return 1.0f / (1.0f + expf(-g)); }
 template <> __device__ __forceinline__ float logistic<__nv_bfloat16>(float g) {
@@ -34,6 +34,54 @@ __device__ __forceinline__ float value(float x) { return x; }
 __device__ __forceinline__ float value(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ void put(float &to, float x) { to = x; }
 __device__ __forceinline__ void put(__nv_bfloat16 &to, float x) { to = __float2bfloat16_rn(x); }
+
+// Below FAR (which a gate seldom reaches) 1 / (1 + e^-g) is e^g to 2^-46 of it, and may be far below
+// fp32's range where its product with a large u or dh is within it: a pack that holds such a g
+// goes value by value, with products in 64 bits for those.  (A quarter's exponential is a
+// normal number down to g = -349, where no product of two fp32 values brings it back.)  The
+// values are read again: kept in registers they took 8 to 12 of the others' room.  Asking costs
+// rows of whole packs nothing (32768 x 768 bf16: 22.1 / 22.4 us), odd ones some 5 % (1859 x 1021 fp32:
+// 4.6 / 4.8 us, the gradient 5.8 / 6.0; 32768 x 767 bf16 31.8 / 34.3); with a far gate in a thousand
+// 32768 x 768 bf16 take 28 us.
+constexpr float FAR = -32.0f;
+__device__ __forceinline__ double far_logistic(float g) {
+    const double q = expf(0.25f * g);
+    return (q * q) * (q * q);
+}
+template <typename T, int V> __device__ __forceinline__ bool any_far(const Pack<T, V> &g) {
+    float least = value(g.v[0]);
+#pragma unroll
+    for (int j = 1; j < V; ++j) least = fminf(least, value(g.v[j]));
+    return least < FAR;
+}
+template <typename T> __device__ __forceinline__ float forward(float x, float u) { return x * logistic<T>(x) * u; }
+// The slope first, at most 1.1: a product of dh and u or g could overflow where the result does not.
+template <typename T> __device__ __forceinline__ float2 backward(float x, float u, float y) {
+    const float s = logistic<T>(x);
+    return make_float2(y * (u * (s * (1.0f + x * (1.0f - s)))), y * (x * s));
+}
+template <typename T, int V> __device__ __forceinline__ void far_forward(const T *g, const T *u, T *h) {
+#pragma unroll 1
+    for (int j = 0; j < V; ++j) {
+        const float x = value(g[j]), v = value(u[j]);
+        put(h[j], x < FAR ? (float)(x * far_logistic(x) * v) : forward<T>(x, v));
+    }
+}
+template <typename T, int V> __device__ __forceinline__ void far_backward(const T *dh, const T *g, const T *u, T *dg, T *du) {
+#pragma unroll 1
+    for (int j = 0; j < V; ++j) {
+        const float x = value(g[j]), v = value(u[j]), y = value(dh[j]);
+        float2 d;
+        if (x < FAR) {
+            const double ys = y * far_logistic(x);
+            d = make_float2((float)(ys * v * (1.0 + x)), (float)(ys * x));
+        } else {
+            d = backward<T>(x, v, y);
+        }
+        put(dg[j], d.x);
+        put(du[j], d.y);
+    }
+}
 
 // `cols`: packs of a row of I values; n: packs of all rows
 template <typename T, int V>
@@ -55,12 +103,14 @@ __global__ void __launch_bounds__(THREADS) swiglu_kernel(const Pack<T, V> *gu, P
     for (int k = 0; k < TOGETHER; ++k) {
         const int i = first + k * THREADS;
         if (i >= n) break;
+        if (any_far(g[k])) {
+            const Pack<T, V> *from = gu + i + (int64_t)cols.div(i) * cols.d;
+            far_forward<T, V>(from->v, from[cols.d].v, h[i].v);
+            continue;
+        }
         Pack<T, V> out;
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const float x = value(g[k].v[j]);
-            put(out.v[j], x * logistic<T>(x) * value(u[k].v[j]));
-        }
+        for (int j = 0; j < V; ++j) put(out.v[j], forward<T>(value(g[k].v[j]), value(u[k].v[j])));
         h[i] = out;
     }
 }
@@ -87,13 +137,16 @@ __global__ void __launch_bounds__(THREADS) swiglu_grad_kernel(const Pack<T, V> *
     for (int k = 0; k < TOGETHER; ++k) {
         const int i = first + k * THREADS;
         if (i >= n) break;
+        if (any_far(g[k])) {
+            far_backward<T, V>(dh[i].v, gu[at[k]].v, gu[at[k] + cols.d].v, dgu[at[k]].v, dgu[at[k] + cols.d].v);
+            continue;
+        }
         Pack<T, V> dg, du;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const float x = value(g[k].v[j]), s = logistic<T>(x), y = value(d[k].v[j]);
-            // (the slope first, at most 1.1: a product of dh and u or g could overflow where the result does not)
-            put(dg.v[j], y * (value(u[k].v[j]) * (s * (1.0f + x * (1.0f - s)))));
-            put(du.v[j], y * (x * s));
+            const float2 both = backward<T>(value(g[k].v[j]), value(u[k].v[j]), value(d[k].v[j]));
+            put(dg.v[j], both.x);
+            put(du.v[j], both.y);
         }
         dgu[at[k]] = dg;
         dgu[at[k] + cols.d] = du;
