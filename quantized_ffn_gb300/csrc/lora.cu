@@ -79,8 +79,10 @@ struct Params {
 // Shrink on the tensor cores: 128 rows (on the MMA's M side) times all r rows of W.  The
 // blocks of a cluster share the contraction; rows 128 / split * i and on are added up by
 // rank i, in rank order.  The tensor core's adds drop what is below the accumulator's last
-// bit (65536 positive values: 3.5e-5 short, fp32 sums rounded to nearest 1e-7): stages past
-// the first 8 go to up to four accumulators, a share each, whose sums meet in registers.
+// bit (positive values: of 512 2.3e-7 short, of 2048 2.3e-6, of 32768 1.5e-4): S_PART stages, 512 values,
+// go to an accumulator, then the next, of two or four, whose sums meet in registers.  A block
+// with more stages than that takes turns: when all accumulators are full their sum goes to the
+// first one, and the others begin again (2.4e-7 short whatever the length).
 // A tile whose tokens follow one another (a packed sequence) is loaded by TMA, another
 // gathered by 16-byte copies.  (The copy engine's own gather takes four rows of 128 bytes at a
 // time, and about 100 clocks for it.)  A stage takes 0.3 to 0.5 us whatever the number of
@@ -90,11 +92,11 @@ struct Params {
 // Roles: warps 0 .. 3 gather x's rows, then take the sums out; warp 4 loads W, and x's
 // rows where they follow one another, warp 5 issues the MMAs.
 // ---------------------------------------------------------------------------
-constexpr int S_NS = 4, S_LAG = 3, S_THREADS = 192, S_MAX_SPLIT = 8;
+constexpr int S_NS = 4, S_LAG = 3, S_THREADS = 192, S_MAX_SPLIT = 8, S_PART = 8;
 
 // W's bytes of a stage: K-major [r][64], or MN-major boxes [64][64]
 __host__ __device__ constexpr int s_w_bytes(int r, bool mn) { return mn ? (r + 63) / 64 * 8192 : up16(r) * 128; }
-static size_t s_smem(int r, bool mn) { return 1024 + (size_t)S_NS * (16384 + s_w_bytes(r, mn)) + (2 * S_NS + 2) * 8 + 8; }
+static size_t s_smem(int r, bool mn) { return 1024 + (size_t)S_NS * (16384 + s_w_bytes(r, mn)) + (2 * S_NS + 3) * 8 + 8; }
 
 template <bool MN>
 __global__ void __launch_bounds__(S_THREADS) shrink_kernel(const __grid_constant__ CUtensorMap xm, const __grid_constant__ CUtensorMap w, const Params p,
@@ -109,7 +111,7 @@ __global__ void __launch_bounds__(S_THREADS) shrink_kernel(const __grid_constant
     // once the stages are idle: sums [rank][row / split][r] from every rank, and this one's own
     float *part = reinterpret_cast<float *>(smem), *own = part + 128 * p.r;
     uint64_t *s_full = reinterpret_cast<uint64_t *>(smem + S_NS * stage);
-    uint64_t *s_empty = s_full + S_NS, *t_full = s_empty + S_NS, *j_full = t_full + 1;
+    uint64_t *s_empty = s_full + S_NS, *t_full = s_empty + S_NS, *t_empty = t_full + 1, *j_full = t_full + 2;
     int *info = reinterpret_cast<int *>(j_full + 1);         // abort, TMEM base
     volatile int *abort_flag = info;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
@@ -118,6 +120,7 @@ __global__ void __launch_bounds__(S_THREADS) shrink_kernel(const __grid_constant
         info[0] = 0;
         for (int i = 0; i < S_NS; ++i) { mbar_init(&s_full[i], 5); mbar_init(&s_empty[i], 1); }
         mbar_init(t_full, 1);
+        mbar_init(t_empty, 4);
         mbar_init(j_full, 1);
         mbar_arrive_expect_tx(j_full, 128 * p.r * 4);
         fence_mbarrier_init();
@@ -143,7 +146,11 @@ __global__ void __launch_bounds__(S_THREADS) shrink_kernel(const __grid_constant
     // this rank's stages: every split-th, so that the ranks read neighbouring columns at a time
     const int nkb = (blocks - (int)rank + (int)split - 1) / (int)split;
     auto block_of = [&](int i) { return i * (int)split + (int)rank; };
-    const int share = max(8, (nkb + accs - 1) / accs);       // stages of an accumulator
+    // stages of the first turn, of each after it (the first accumulator holds the sum so far); turns
+    // before the last, and the last one's parts besides the first accumulator
+    const int first_turn = accs * S_PART, turn = first_turn - S_PART;
+    const int turns = nkb > first_turn ? (nkb - first_turn + turn - 1) / turn : 0;
+    const int more = turns ? (nkb - first_turn - (turns - 1) * turn + S_PART - 1) / S_PART : (nkb + S_PART - 1) / S_PART - 1;
     const float scale = some && p.scale ? __ldcg(p.scale + wk.e) : 1.0f;
 
     // the tile's tokens, 4 lane + j, and whether they follow one another
@@ -157,8 +164,39 @@ __global__ void __launch_bounds__(S_THREADS) shrink_kernel(const __grid_constant
         packed = __all_sync(0xffffffffu, packed) && t0 >= 0 && t0 + wk.rows <= p.T;
     }
 
+    // 16 columns of this warp's rows, summed over the first accumulator and n others
+    auto sum_of = [&](int c, int n, uint32_t (&d)[16]) {
+        const uint32_t at = tmem + ((uint32_t)(warp * 32) << 16) + c;
+        tmem_ld_32x32b_x16(at, d);
+        tmem_ld_wait(d);
+        for (int k = 1; k <= n; ++k) {
+            uint32_t other_d[16];
+            tmem_ld_32x32b_x16(at + k * cols, other_d);
+            tmem_ld_wait(other_d);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) d[j] = __float_as_uint(__uint_as_float(d[j]) + __uint_as_float(other_d[j]));
+        }
+    };
     if (some && warp < 4) {
         // ---- gather: thread = one 16-byte column of rows tid / 8 + 16 i
+        int joined = 0;                // turns whose sums have gone to the first accumulator
+        auto join = [&] {
+            const bool ok = bar_wait_warp(t_full, joined & 1, abort_flag, p.err);
+            if (!ok) return false;
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < p.r; c += 16) {
+                uint32_t d[16];
+                sum_of(c, accs - 1, d);
+                tmem_st_32x32b_x16(tmem + ((uint32_t)(warp * 32) << 16) + c, d);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(t_empty);
+            ++joined;
+            return true;
+        };
         if (!packed) {
             const int chunk = tid & 7, first = tid >> 3;
             const uint32_t dst = smem_u32(smem) + first * 128 + ((chunk ^ (first & 7)) << 4);
@@ -187,12 +225,16 @@ __global__ void __launch_bounds__(S_THREADS) shrink_kernel(const __grid_constant
                 if (i >= S_LAG) {
                     copy_wait<S_LAG>();
                     filled(i - S_LAG);
+                    // (a turn's last stage: the stages begun since wait for no later one)
+                    if (joined < turns && i - S_LAG == first_turn + joined * turn - 1) ok = join();
+                    if (!ok) break;
                 }
             }
             copy_wait<0>();
             if (ok)
                 for (int i = nkb > S_LAG ? nkb - S_LAG : 0; i < nkb; ++i) filled(i);
         }
+        while (joined < turns && join()) {}
     } else if (some && warp == 4) {
         // ---- by TMA: W, and a packed tile's rows (past the adapter's last: rows that nothing takes)
         const int t0 = __shfl_sync(0xffffffffu, tok[0], 0);
@@ -223,9 +265,17 @@ __global__ void __launch_bounds__(S_THREADS) shrink_kernel(const __grid_constant
         const uint32_t idesc = idesc_bf16_f32(128, r16, false, MN);
         bool ok = true;
         uint32_t dst = tmem;
+        int turned = 0, full = 0;      // turns joined; commits on t_full
         for (int i = 0, at = 0; i < nkb; ++i, ++at) {
             const int s = i % S_NS;
-            if (at == share) at = 0, dst += cols;
+            if (at == S_PART) at = 0, dst += cols;
+            if (at == 0 && dst == tmem + accs * cols) {      // (the last turn's sums have been joined)
+                ok = bar_wait_warp(t_empty, turned & 1, abort_flag, p.err);
+                if (!ok) break;
+                ++turned;
+                dst = tmem + cols;
+            }
+            const bool last = i == nkb - 1 || (at == S_PART - 1 && dst == tmem + (accs - 1) * cols);
             ok = bar_wait_warp(&s_full[s], (i / S_NS) & 1, abort_flag, p.err);
             if (!ok) break;
             tc_fence_after();
@@ -239,22 +289,24 @@ __global__ void __launch_bounds__(S_THREADS) shrink_kernel(const __grid_constant
                     tc_mma_bf16(dst, xd + k * k_step(false), wd + k * k_step(MN), idesc, (at | k) != 0);
                 }
                 tc_commit(&s_empty[s]);
-                if (i == nkb - 1) tc_commit(t_full);
+                if (last) tc_commit(t_full);
             }
             __syncwarp();
+            full += last;
         }
         if (!ok) {                     // (nothing issued is left on its way)
             if (elect_one()) tc_commit(t_full);
+            __syncwarp();
+            if (lane == 0) mbar_wait(t_full, full & 1, nullptr, p.err);
             __syncwarp();
         }
     }
     if (have && warp < 4) {
         // ---- take out: thread = one row
         if (some) {
-            bar_wait_warp(t_full, 0, abort_flag, p.err);
+            bar_wait_warp(t_full, turns & 1, abort_flag, p.err);
             tc_fence_after();
         }
-        const uint32_t from = tmem + ((uint32_t)(warp * 32) << 16);
         const int row = tid;
         float *to = v + (int64_t)(wk.row0 + row) * p.r;
         __nv_bfloat16 *to16 = v16 + (int64_t)(wk.row0 + row) * pieces_pitch(p.r);
@@ -263,15 +315,7 @@ __global__ void __launch_bounds__(S_THREADS) shrink_kernel(const __grid_constant
         for (int c = 0; c < p.r; c += 16) {
             uint32_t d[16];
             if (some) {
-                tmem_ld_32x32b_x16(from + c, d);
-                tmem_ld_wait(d);
-                for (int i = share, a = cols; i < nkb; i += share, a += cols) {
-                    uint32_t more[16];
-                    tmem_ld_32x32b_x16(from + a + c, more);
-                    tmem_ld_wait(more);
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) d[j] = __float_as_uint(__uint_as_float(d[j]) + __uint_as_float(more[j]));
-                }
+                sum_of(c, more, d);
             } else {
 #pragma unroll
                 for (int j = 0; j < 16; ++j) d[j] = 0;
