@@ -722,10 +722,12 @@ __global__ void __launch_bounds__(E_THREADS, 1) expand_kernel(const __grid_const
 // warps 12 .. 15 take a tile out (32 columns of x each).
 // ---------------------------------------------------------------------------
 constexpr int O_THREADS = 512;
-// Stages of a part: the tensor core's adds drop what is below the accumulator's last bit (8192
-// positive values: 2.2e-6 short, 65536 3.5e-5), so that 4096 tokens at most are summed there; the sum of
-// the parts before is in tensor memory behind the first accumulator's columns.
-constexpr int PART = 64;
+// Stages of a part, as a logarithm: the tensor core's adds drop what is below the accumulator's last
+// bit (positive values: of 512 2.3e-7 short, of 4096 7.9e-6), so that 512 tokens at most are summed there
+// for fp32 results, 4096 for bf16 ones, whose rounding is 4e-3.  (In parts of 512 too, 16384 tokens, r =
+// 128, 359 / 395 us a gradient.)  The sum of the parts before is in tensor memory behind the first
+// accumulator's columns.
+constexpr int FP32_PART_LOG = 3, BF16_PART_LOG = 6;
 
 template <int BOXES_>
 struct OuterCfg {
@@ -749,7 +751,7 @@ struct OuterJob {
 
 template <class C>
 __global__ void __launch_bounds__(O_THREADS, 1) outer_kernel(const __grid_constant__ OuterJob ja, const __grid_constant__ OuterJob jb, const Params p,
-                                                             int d_bf16) {
+                                                             int d_bf16, int part_log) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint64_t *s_full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
@@ -757,7 +759,7 @@ __global__ void __launch_bounds__(O_THREADS, 1) outer_kernel(const __grid_consta
     int *info = reinterpret_cast<int *>(t_empty + 2);        // abort, TMEM base
     volatile int *abort_flag = info;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
-    const int r16 = up16(p.r);
+    const int r16 = up16(p.r), part_mask = (1 << part_log) - 1;
     if (tid == 0) {
         info[0] = 0;
         for (int i = 0; i < C::NS; ++i) { mbar_init(&s_full[i], 9); mbar_init(&s_empty[i], 1); }
@@ -924,8 +926,8 @@ __global__ void __launch_bounds__(O_THREADS, 1) outer_kernel(const __grid_consta
             if (ns == 0) continue;
             for (int i = 0; i < ns; ++i, ++it) {
                 const uint32_t s = it % C::NS, b = acc % C::ACC, dst = tmem + b * C::ACC_COLS;
-                const int at = i % PART;                     // a part's first stage: 0
-                const bool last = at == PART - 1 || i == ns - 1;
+                const int at = i & part_mask;                // a part's first stage: 0
+                const bool last = at == part_mask || i == ns - 1;
                 if (at == 0) ok = acc < (uint32_t)C::ACC || bar_wait_warp(&t_empty[b], ((acc / C::ACC) & 1) ^ 1, abort_flag, p.err);
                 ok = ok && bar_wait_warp(&s_full[s], (it / C::NS) & 1, abort_flag, p.err);
                 if (!ok) break;
@@ -957,7 +959,7 @@ __global__ void __launch_bounds__(O_THREADS, 1) outer_kernel(const __grid_consta
         const uint32_t from = tmem + ((uint32_t)((warp & 3) * 32) << 16), sums = from + 3 * r16;   // of the parts before
         uint32_t acc = 0;
         for (bool ok = true; ok && wk.get(); wk.t += gridDim.x) {
-            const int parts = (stages() + PART - 1) / PART;
+            const int parts = (stages() + part_mask) >> part_log;
             const bool some = parts > 0;
             const OuterJob &job = wk.nt < ja.n_tiles ? ja : jb;
             const int c = (wk.nt < ja.n_tiles ? wk.nt : wk.nt - ja.n_tiles) * 128 + (warp & 3) * 32 + lane;
@@ -1295,7 +1297,7 @@ static bool outer_job(OuterJob *job, const LoraPlan &q, const void *v16, const v
            encode(&job->vm, v16, 2, pieces_pitch(q.r), q.T, 1, KB, false, pieces_pitch(q.r) / 64);
 }
 template <int BOXES>
-static cudaError_t outer(const LoraPlan &q, const OuterJob &a, const OuterJob &b, int dtype, cudaStream_t s) {
+static cudaError_t outer(const LoraPlan &q, const OuterJob &a, const OuterJob &b, int dtype, int part_log, cudaStream_t s) {
     using Cfg = OuterCfg<BOXES>;
     const int n_tiles = a.n_tiles + b.n_tiles;
     const int64_t tiles = (int64_t)q.L * n_tiles, sms = device_info().num_sms;
@@ -1305,7 +1307,7 @@ static cudaError_t outer(const LoraPlan &q, const OuterJob &a, const OuterJob &b
     const cudaError_t e = ensure_dynamic_smem((const void *)outer_kernel<Cfg>, Cfg::SMEM);
     if (e != cudaSuccess) return e;
     return launch_dependent(outer_kernel<Cfg>, dim3((unsigned)(tiles < sms ? tiles : sms)), O_THREADS, Cfg::SMEM, 1, s, a, b, p,
-                            (int)(dtype == ZFFN_DT_BF16));
+                            (int)(dtype == ZFFN_DT_BF16), part_log);
 }
 
 }  // namespace lora
@@ -1357,8 +1359,9 @@ cudaError_t launch_lora_outer(const LoraPlan &q, const void *dv16, const void *x
     OuterJob a, b;
     if (!outer_job(&a, q, dv16, x, dA, K, false) || !outer_job(&b, q, v16, dy, dB, N, true)) return cudaErrorInvalidValue;
     // (several parts: columns for their sum as well, so that one accumulator alone has room from r = 72)
-    const int boxes = q.T > PART * KB && 4 * up16(q.r) > 256 ? 6 : pieces_pitch(q.r) / 64;
-    return boxes <= 2 ? outer<2>(q, a, b, dtype, s) : boxes <= 4 ? outer<4>(q, a, b, dtype, s) : outer<6>(q, a, b, dtype, s);
+    const int part_log = dtype == ZFFN_DT_BF16 ? BF16_PART_LOG : FP32_PART_LOG;
+    const int boxes = q.T > KB << part_log && 4 * up16(q.r) > 256 ? 6 : pieces_pitch(q.r) / 64;
+    return boxes <= 2 ? outer<2>(q, a, b, dtype, part_log, s) : boxes <= 4 ? outer<4>(q, a, b, dtype, part_log, s) : outer<6>(q, a, b, dtype, part_log, s);
 }
 
 }  // namespace zffn

@@ -75,3 +75,23 @@ def test_signed_rows_repeat_and_stay_apart(T, C, r):
     other, w = zffn.lora_add(x, A, B, plan, dtype=torch.float32)
     assert torch.equal(w[:5], v[:5]) and torch.equal(w[6:], v[6:]) and torch.isnan(w[5]).all()
     assert zffn.get_device_error() == zffn.OK
+
+
+@pytest.mark.parametrize("packed", [True, False])
+@pytest.mark.parametrize("T,r,L", [(4096, 32, 1), (4100, 16, 2), (5000, 72, 1), (3000, 80, 1), (2500, 128, 1), (30000, 64, 3), (30000, 104, 1)])
+def test_weights_gradients_of_many_tokens(T, r, L, packed):
+    # dB's sums are over tokens alone, in parts of 512 of them (each in three pieces of v, whose sums meet in two
+    # more roundings); dA's have dv's own error before them
+    N, K = 136, 72
+    gen = ref.generator(T + r)
+    plan = plan_of(gen, T, L, packed)
+    x, dy, A, B = positive(gen, T, K), positive(gen, T, N), positive(gen, L, r, K), positive(gen, L, N, r)
+    v = torch.rand((T, r), generator=gen, device="cuda") + 0.5
+    dx, dA, dB = zffn.lora_grad(dy, x, v, A, B, plan, dtype=torch.float32)
+    rows = int(plan.offsets.diff().max())
+    (_, _), (wA, _), (wB, _) = ref.lora_grad(dy, x, v, A, B, plan, None, None)
+    ref.check(dB, wB, (bound(rows) + 2 * ref.U32) * wB)
+    ref.check(dA, wA, (bound(rows) + bound(N) + 2 * ref.U32) * wA)
+    again = zffn.lora_grad(dy, x, v, A, B, plan, dtype=torch.float32)
+    assert all(torch.equal(a, b) for a, b in zip(again, (dx, dA, dB)))
+    assert zffn.get_device_error() == zffn.OK
