@@ -718,10 +718,10 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) small_kernel(const __gr
 // ---- host -------------------------------------------------------------------
 
 // Stages of a part, as a logarithm.  The tensor core's adds drop what is below the accumulator's
-// last bit, so that a long sum comes out short (fp32 results of positive values: of 2048 3.8e-7, of 8192
-// 2.2e-6, of 65536 3.5e-5; of signed ones 2.3e-7, 1e-6, 1e-5).  Parts of 512, joined in fp32 registers
-// that round to nearest, hold it at 9e-7 (signed: 5e-7).  Of a bf16 result, whose rounding is 4e-3, a
-// part is 4096 (y's on large tiles are one part: K is 65536 at most).
+// last bit, so that a long sum comes out short (of positive values, even in [0.5, 1.5]: of 512 2.3e-7, of 2048
+// 2.3e-6, of 4096 7.9e-6, of 32768 1.5e-4, of 65536 some 3e-4).  Parts of 512, joined in fp32 registers that
+// round to nearest, hold it at 2.3e-7 whatever the length (up to 65536 values no more than 9e-7 of any
+// sum).  Of a bf16 result, whose rounding is 4e-3, a part is 4096.
 constexpr int FP32_PART_LOG = 3, BF16_PART_LOG = 6;
 static int part_log(int dtype) { return dtype == ZFFN_DT_BF16 ? BF16_PART_LOG : FP32_PART_LOG; }
 
@@ -845,8 +845,8 @@ static cudaError_t launch(const Bf16Args &a, cudaStream_t s) {
     if (mean <= 32) return launch_small<SmallCfg<KIND, 32>>(a, s);
     const int64_t most = (int64_t)a.M / 128 + (a.E < a.M ? a.E : a.M), tiles = most * ((a.N + 255) / 256);
     if (tiles <= device_info().num_sms / 6) return launch_small<SmallCfg<KIND, 64>>(a, s);
-    // Several parts: fp32 results alone (K is 65536 at most)
-    if (a.y_dtype == ZFFN_DT_F32 && a.K > KB << FP32_PART_LOG) return launch_tiles<KIND, true>(a, s);
+    // Several parts (bf16, 8192 x 8192 of 8192 values one part / two: 509 / 512 us, 4096 x 4096 of 11008 197.1 / 197.9)
+    if (a.K > KB << part_log(a.y_dtype)) return launch_tiles<KIND, true>(a, s);
     return launch_tiles<KIND, false>(a, s);
 }
 
@@ -880,8 +880,9 @@ cudaError_t launch_bf16_grad_w(const Bf16GradArgs &a, cudaStream_t s) {
     const bool pair = tiles >= 2 * (int64_t)device_info().num_sms;
     // Several parts where an expert may have as many rows (how many it has the host does not know). A
     // part's registers cost 1 to 3% (fp32 dw of 2048 x 1536, 128 experts of 128 rows 312 / 316 us; bf16,
-    // of 256 rows 197 / 202): of bf16 where cut sums could be seen in it.
-    const bool parts = a.dw_dtype == ZFFN_DT_F32 ? a.M > KB << FP32_PART_LOG : a.M > 1 << 18;
+    // of 256 rows 197 / 202): of bf16 from where a sum may come out more than 1.5e-4 short, a
+    // twenty-fifth of its rounding.
+    const bool parts = a.M > (a.dw_dtype == ZFFN_DT_F32 ? KB << FP32_PART_LOG : 1 << 15);
     if (parts) return pair ? launch_weights<LargeCfg<WEIGHTS, true, true>>(a, s) : launch_weights<LargeCfg<WEIGHTS, false, true>>(a, s);
     return pair ? launch_weights<LargeCfg<WEIGHTS, true, false>>(a, s) : launch_weights<LargeCfg<WEIGHTS, false, false>>(a, s);
 }
