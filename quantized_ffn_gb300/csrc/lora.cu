@@ -1239,12 +1239,17 @@ static Params params(const LoraPlan &q, int C) { return Params{q.row_slot, q.slo
 // Row tiles of 128 rows, at most, with those of the rows of none.
 static int64_t row_tiles(const LoraPlan &q) { return q.T / 128 + (q.L + 1 < q.T ? q.L + 1 : q.T); }
 // Whether a forward pass goes row by row: each row reads its adapter through L2 again, where
-// the tensor cores' kernels take a tile for each adapter, however few its rows (4096 -> 11008,
-// us by rows and by tiles: 61 tokens of 48 adapters, r = 16: 9 / 52, 512 of 64: 37 / 76, 256 of 16:
-// 20 / 27, 512 of 16: 37 / 28, 64 of 1 with r = 32: 14 / 11; r = 24 and the like, two columns a
-// thread, take a third longer by rows).
+// the tensor cores' kernels take a tile for each adapter, however few its rows.  L is the table's
+// size; how many adapters have tokens the host does not know, and by tiles that decides: the bound
+// lies where neither form is much more than twice the other, whether one adapter has all tokens or
+// each has some (4096 -> 11008, us by rows and by tiles with one in use / all: 512 tokens of 64, r =
+// 16: 41 and 18 / 79; 1024 of 128, r = 16: 75 to 85 and 27 / 150; 512 of 128, r = 32: 78 to 95 and 25 / 144;
+// 1024 of 256, r = 32: 157 to 171 and 108 / 276; 2048 of 256, r = 32: 282 to 303 and 111 / 285; 2048 of 1024,
+// r = 64: 550 to 647 and 243 / 893; 16384 of 4096, r = 16: 1050 to 1310 and 2916 / 4826, whose walk over the
+// table each block takes; 61 of 48, r = 16: 9 and 15 / 52).  r = 24 and the like, two columns a thread,
+// take a third longer and more by rows (512 of 128, r = 24: 91 to 121 and 25 / 144).
 static bool lane_wide(int r) { return (r & (r - 1)) == 0; }   // r is a multiple of 8
-static bool few(int T, int r, int L) { return (int64_t)T * r <= 1024 + (lane_wide(r) ? 256 : 160) * (int64_t)(L < T ? L : T); }
+static bool few(int T, int r, int L) { return (int64_t)T * r <= 1024 + (lane_wide(r) ? 112 : 70) * (int64_t)(L < T ? L : T); }
 
 template <bool MN>
 static cudaError_t shrink(const LoraPlan &q, const void *x, const void *w, float *v, void *v16, const float *other, void *other16, int C, cudaStream_t s) {
