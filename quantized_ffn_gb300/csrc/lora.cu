@@ -160,8 +160,9 @@ __global__ void __launch_bounds__(S_THREADS) shrink_kernel(const __grid_constant
 #pragma unroll
         for (int j = 0; j < 4; ++j) tok[j] = lane * 4 + j < wk.rows ? __ldcg(p.row_slot + wk.row0 + lane * 4 + j) : -1;
         const int t0 = __shfl_sync(0xffffffffu, tok[0], 0);
+        packed = t0 >= 0 && t0 <= p.T - wk.rows;             // (any word may be there: no sum of it before that)
         for (int j = 0; j < 4; ++j) packed = packed && (lane * 4 + j >= wk.rows || tok[j] == t0 + lane * 4 + j);
-        packed = __all_sync(0xffffffffu, packed) && t0 >= 0 && t0 + wk.rows <= p.T;
+        packed = __all_sync(0xffffffffu, packed);
     }
 
     // 16 columns of this warp's rows, summed over the first accumulator and n others
