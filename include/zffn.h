@@ -473,7 +473,8 @@ zffn_status zffn_moe_swiglu_fp8(const void *x, const int32_t *expert_ids,
 /* ---------------------------------------------------------------------------
  * Training and adapting layers in bf16: the experts' products with their
  * gradients, SwiGLU with its gradient, and low-rank adapters beside a
- * projection of any kind.  Operands are bf16, every sum is fp32 and every result
+ * projection of the caller's (zffn_fp8_matmul, zffn_bf16_matmul or another whose result is a
+ * matrix; the Q4_K entry points have whole blocks alone).  Operands are bf16, every sum is fp32 and every result
  * is rounded once.  The source pages have no counterpart of these entry points.
  * None takes library workspace (the adapters take the caller's), so calls on several
  * streams may overlap as long as their arguments do not.  An output overlaps no other
@@ -548,8 +549,9 @@ zffn_status zffn_swiglu_grad(int dtype, const void *dh, const void *gu, void *dg
  *     zffn_lora_grad needs again.
  *   work: zffn_lora_work_bytes(T, r, L, 0) bytes of the caller's, for the call (NULL
  *     where that is 0).
- * Both products have fp32 sums; v is not rounded to fewer bits between them.  Where v is
- * infinite or NaN, its token's out is infinite or NaN (which of them is not said).
+ * Both products have fp32 sums; v is not rounded to fewer bits between them (it goes as a sum
+ * of bf16 pieces, some of them 0).  Where v is infinite or NaN, or is multiplied with an
+ * infinite weight, that value of out is infinite or NaN (which of them is not said).
  * Requirements: 1 <= T <= 2^24, K and N multiples of 8 in [8, 65536], r a multiple
  * of 8 in [8, 128], 1 <= L <= 4096; x, A, B, base, out, v and work 16-byte aligned,
  * the others 4-byte.  Errors: INVALID_ARG, CUDA. */
@@ -567,7 +569,8 @@ size_t zffn_lora_work_bytes(int T, int r, int L, int backward);
  *     dA[e]   = sum over e's rows of dv[row]^T x[t]
  *     dB[e]   = sum over e's rows of dy[t]^T v[row]
  * dA and dB are 0 for an adapter without tokens; base is what the shared projection
- * gives back to x.  The sums over rows are taken in a fixed order.
+ * gives back to x.  The sums over rows are taken in a fixed order.  A result that an infinite
+ * or NaN value enters is infinite or NaN, as above.
  *   dy: bf16 [T][N].  v: fp32 [T][r] as zffn_lora_add wrote it.
  *   base: dx_dtype [T][K] or NULL.  dx: dx_dtype [T][K], may be base.
  *   dA: dw_dtype [L][r][K].  dB: dw_dtype [L][N][r].  dv: output, fp32 [T][r] (0 from
