@@ -21,6 +21,15 @@ namespace b16 {
 
 enum Kind { FORWARD, BACK, WEIGHTS };
 
+// Stages of a part, as a logarithm.  The tensor core's adds drop what is below the accumulator's
+// last bit, so that a long sum comes out short (of positive values, even in [0.5, 1.5]: of 512 2.3e-7, of 2048
+// 2.3e-6, of 4096 7.9e-6, of 32768 1.5e-4, of 65536 some 3e-4).  Parts of 512, joined in fp32 registers that
+// round to nearest, hold it at 2.3e-7 whatever the length (up to 65536 values no more than 9e-7 of any
+// sum).  Also of a bf16 result: of sums of 2048 products 1 in 800 was not the nearest bf16 value in
+// one part, 1 in 2600 is in four, as of fp32 sums by the ordinary units (32768 rows of 128 experts,
+// 1536 x 2048: 198 / 204 us, 2048 rows of 128 and one token's experts the same).
+constexpr int PART_LOG = 3;
+
 struct Params {
     const int32_t *offsets;
     void *y;
@@ -36,7 +45,6 @@ struct Params {
     // 256 rows of 128 experts, 1536 x 2048, 185 us against 202.)
     int wide_a, wide_w;
     FastDiv each, across;   // of the walk; weights: by n_tiles
-    int part_log;           // log2 of a part's stages
 };
 // a: forward, back: [M][K]; weights: dy, in boxes of 16, 32 and 64 rows.  w: w; weights: a,
 // in the same.  y: what the stores go to.
@@ -48,7 +56,7 @@ struct Maps {
 // Many rows: tiles of 128 rows (a CTA pair: 256) times 256 columns of the result, a
 // (weights: dy) on the MMA's M side.  Persistent: every cluster takes tiles in turn;
 // two accumulators in tensor memory, so that one is taken out while the next tile's
-// MMAs run.  PARTS: a long sum in parts (see part_log), joined in the registers of the
+// MMAs run.  PARTS: a long sum in parts (see PART_LOG), joined in the registers of the
 // threads that take them out.
 //
 // Roles: warps 0 .. 7 take a tile out of tensor memory (32 rows by 128 columns each) and
@@ -120,7 +128,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(info + 1);
     typename C::Walk wk;
     wk.start(p.offsets, p.M, p.E, GRAD ? p.m_tiles * p.n_tiles : p.n_tiles, p.each, !GRAD, blockIdx.x / C::CTAS);
-    const int step = gridDim.x / C::CTAS, part_log = C::PARTS ? p.part_log : 30, part_mask = (1 << part_log) - 1;
+    const int step = gridDim.x / C::CTAS;
+    constexpr int part_log = C::PARTS ? PART_LOG : 30, part_mask = (1 << part_log) - 1;
     // stages of the tile at hand (none: zeros)
     auto blocks = [&] { return GRAD ? (wk.rows + KB - 1) / KB : wk.e < p.E ? (p.K + KB - 1) / KB : 0; };
     // groups of 16 contracted values in stage i
@@ -530,7 +539,8 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) small_kernel(const __gr
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(info + 1);
     const int blocks = (p.K + KB - 1) / KB;
     const int kb0 = blocks * rank / split, nkb = blocks * (rank + 1) / split - kb0;   // this rank's share of K
-    const int step = gridDim.x / split, part_mask = (1 << p.part_log) - 1;
+    const int step = gridDim.x / split;
+    constexpr int part_mask = (1 << PART_LOG) - 1;
     typename C::Walk wk;
     wk.start(p.offsets, p.M, p.E, p.n_tiles, p.each, true, blockIdx.x / split);
     const uint32_t slice = (C::TN + split - 1) / split;      // rows of a tile that a rank adds up
@@ -610,7 +620,7 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) small_kernel(const __gr
         uint32_t acc = 0;
         bool ok = true;
         for (bool have = wk.get(); ok && have; have = next()) {
-            const int parts = wk.e < p.E ? (nkb + part_mask) >> p.part_log : 0;
+            const int parts = wk.e < p.E ? (nkb + part_mask) >> PART_LOG : 0;
             const int n = wk.nt * 128 + tid;
             constexpr int CH = 16;
             if (split > 1) {
@@ -717,14 +727,6 @@ __global__ void __launch_bounds__(C::THREADS, C::BLOCKS) small_kernel(const __gr
 
 // ---- host -------------------------------------------------------------------
 
-// Stages of a part, as a logarithm.  The tensor core's adds drop what is below the accumulator's
-// last bit, so that a long sum comes out short (of positive values, even in [0.5, 1.5]: of 512 2.3e-7, of 2048
-// 2.3e-6, of 4096 7.9e-6, of 32768 1.5e-4, of 65536 some 3e-4).  Parts of 512, joined in fp32 registers that
-// round to nearest, hold it at 2.3e-7 whatever the length (up to 65536 values no more than 9e-7 of any
-// sum).  Of a bf16 result, whose rounding is 4e-3, a part is 4096.
-constexpr int FP32_PART_LOG = 3, BF16_PART_LOG = 6;
-static int part_log(int dtype) { return dtype == ZFFN_DT_BF16 ? BF16_PART_LOG : FP32_PART_LOG; }
-
 // Row tiles of at most tr rows, at most: every expert may have one cut tile, and so may
 // the rows of none.
 static int64_t row_tiles_bound(int M, int E, const int32_t *offsets, int tr) {
@@ -746,7 +748,7 @@ static cudaError_t run_large(const Maps &maps, const Params &p, int64_t tiles, c
 template <class C>
 static cudaError_t launch_large(const Bf16Args &a, cudaStream_t s) {
     Maps maps{};
-    Params p{a.offsets, a.y, a.err, a.M, a.N, a.K, a.E, (a.N + C::TN - 1) / C::TN, 0, a.y_dtype == ZFFN_DT_BF16, 0, 0, C::KIND == BACK && a.N % 64 == 0, {}, {}, part_log(a.y_dtype)};
+    Params p{a.offsets, a.y, a.err, a.M, a.N, a.K, a.E, (a.N + C::TN - 1) / C::TN, 0, a.y_dtype == ZFFN_DT_BF16, 0, 0, C::KIND == BACK && a.N % 64 == 0, {}, {}};
     p.each = C::Walk::divisor(p.n_tiles);
     const int elem = p.y_bf16 ? 2 : 4;
     p.vec = a.N * elem % 16 == 0 && (reinterpret_cast<uintptr_t>(a.y) & 15) == 0;
@@ -803,7 +805,7 @@ template <class C>
 static cudaError_t launch_small(const Bf16Args &a, cudaStream_t s) {
     const DeviceInfo &di = device_info();
     Maps maps{};
-    Params p{a.offsets, a.y, a.err, a.M, a.N, a.K, a.E, (a.N + 127) / 128, 0, a.y_dtype == ZFFN_DT_BF16, 0, 0, C::KIND == BACK && a.N % 64 == 0, {}, {}, part_log(a.y_dtype)};
+    Params p{a.offsets, a.y, a.err, a.M, a.N, a.K, a.E, (a.N + 127) / 128, 0, a.y_dtype == ZFFN_DT_BF16, 0, 0, C::KIND == BACK && a.N % 64 == 0, {}, {}};
     p.each = C::Walk::divisor(p.n_tiles);
     if (!encode(maps.a, a.a, 2, a.K, a.M, 1, C::TN, false)) return cudaErrorInvalidValue;
     if (!(C::KIND == FORWARD ? encode(maps.w, a.w, 2, a.K, a.N, a.E, 128, true) : encode(maps.w, a.w, 2, a.N, a.K, a.E, KB, true, p.wide_w ? 2 : 0)))
@@ -845,8 +847,7 @@ static cudaError_t launch(const Bf16Args &a, cudaStream_t s) {
     if (mean <= 32) return launch_small<SmallCfg<KIND, 32>>(a, s);
     const int64_t most = (int64_t)a.M / 128 + (a.E < a.M ? a.E : a.M), tiles = most * ((a.N + 255) / 256);
     if (tiles <= device_info().num_sms / 6) return launch_small<SmallCfg<KIND, 64>>(a, s);
-    // Several parts (bf16, 8192 x 8192 of 8192 values one part / two: 509 / 512 us, 4096 x 4096 of 11008 197.1 / 197.9)
-    if (a.K > KB << part_log(a.y_dtype)) return launch_tiles<KIND, true>(a, s);
+    if (a.K > KB << PART_LOG) return launch_tiles<KIND, true>(a, s);
     return launch_tiles<KIND, false>(a, s);
 }
 
@@ -854,7 +855,7 @@ template <class C>
 static cudaError_t launch_weights(const Bf16GradArgs &a, cudaStream_t s) {
     Maps maps{};
     Params p{a.offsets, a.dw, a.err, a.M, a.N, a.K, a.E, (a.K + C::TN - 1) / C::TN, (a.N + C::TM - 1) / C::TM, a.dw_dtype == ZFFN_DT_BF16, 1,
-                   a.N % 64 == 0, a.K % 64 == 0, {}, FastDiv((a.K + C::TN - 1) / C::TN), part_log(a.dw_dtype)};
+                   a.N % 64 == 0, a.K % 64 == 0, {}, FastDiv((a.K + C::TN - 1) / C::TN)};
     p.each = C::Walk::divisor(p.m_tiles * p.n_tiles);
     for (int x = 0; x < 3; ++x)
         if (!encode(&maps.a[x], a.dy, 2, a.N, a.M, 1, 16 << x, false, p.wide_a ? 2 : 0) ||
@@ -880,9 +881,9 @@ cudaError_t launch_bf16_grad_w(const Bf16GradArgs &a, cudaStream_t s) {
     const bool pair = tiles >= 2 * (int64_t)device_info().num_sms;
     // Several parts where an expert may have as many rows (how many it has the host does not know). A
     // part's registers cost 1 to 3% (fp32 dw of 2048 x 1536, 128 experts of 128 rows 312 / 316 us; bf16,
-    // of 256 rows 197 / 202): of bf16 from where a sum may come out more than 1.5e-4 short, a
-    // twenty-fifth of its rounding.
-    const bool parts = a.M > (a.dw_dtype == ZFFN_DT_F32 ? KB << FP32_PART_LOG : 1 << 15);
+    // of 256 rows 197 / 202): of bf16 where the experts have as many in the mean, or where a sum in
+    // one part might come out more than 1.5e-4 short, a twenty-fifth of its rounding.
+    const bool parts = a.M > KB << PART_LOG && (a.dw_dtype == ZFFN_DT_F32 || a.M / a.E > KB << PART_LOG || a.M > 1 << 15);
     if (parts) return pair ? launch_weights<LargeCfg<WEIGHTS, true, true>>(a, s) : launch_weights<LargeCfg<WEIGHTS, false, true>>(a, s);
     return pair ? launch_weights<LargeCfg<WEIGHTS, true, false>>(a, s) : launch_weights<LargeCfg<WEIGHTS, false, false>>(a, s);
 }
