@@ -724,11 +724,11 @@ __global__ void __launch_bounds__(E_THREADS, 1) expand_kernel(const __grid_const
 // ---------------------------------------------------------------------------
 constexpr int O_THREADS = 512;
 // Stages of a part, as a logarithm: the tensor core's adds drop what is below the accumulator's last
-// bit (positive values: of 512 2.3e-7 short, of 4096 7.9e-6), so that 512 tokens at most are summed there
-// for fp32 results, 4096 for bf16 ones, whose rounding is 4e-3.  (In parts of 512 too, 16384 tokens, r =
-// 128, 359 / 395 us a gradient.)  The sum of the parts before is in tensor memory behind the first
-// accumulator's columns.
-constexpr int FP32_PART_LOG = 3, BF16_PART_LOG = 6;
+// bit (positive values: of 512 2.3e-7 short, of 4096 7.9e-6), so that 512 tokens at most are summed
+// there.  The sum of the parts before is in tensor memory behind the first accumulator's columns.
+// Of bf16 results, whose rounding is 4e-3, 4096 where only one accumulator has room beside that
+// sum (16384 tokens, r = 128: 359 us a gradient, in parts of 512 395; r = 64 250 / 251).
+constexpr int PART_LOG = 3, LONG_PART_LOG = 6;
 
 template <int BOXES_>
 struct OuterCfg {
@@ -1365,8 +1365,9 @@ cudaError_t launch_lora_outer(const LoraPlan &q, const void *dv16, const void *x
     OuterJob a, b;
     if (!outer_job(&a, q, dv16, x, dA, K, false) || !outer_job(&b, q, v16, dy, dB, N, true)) return cudaErrorInvalidValue;
     // (several parts: columns for their sum as well, so that one accumulator alone has room from r = 72)
-    const int part_log = dtype == ZFFN_DT_BF16 ? BF16_PART_LOG : FP32_PART_LOG;
-    const int boxes = q.T > KB << part_log && 4 * up16(q.r) > 256 ? 6 : pieces_pitch(q.r) / 64;
+    const bool one = 4 * up16(q.r) > 256;
+    const int part_log = one && dtype == ZFFN_DT_BF16 ? LONG_PART_LOG : PART_LOG;
+    const int boxes = one && q.T > KB << part_log ? 6 : pieces_pitch(q.r) / 64;
     return boxes <= 2 ? outer<2>(q, a, b, dtype, part_log, s) : boxes <= 4 ? outer<4>(q, a, b, dtype, part_log, s) : outer<6>(q, a, b, dtype, part_log, s);
 }
 

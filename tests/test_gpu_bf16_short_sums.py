@@ -45,3 +45,18 @@ def test_weights_gradients(M, N, K, E):
     nearest(dw[some], want[some], bound(M if E != 20 else M // E) * want[some])
     assert torch.all(dw[~some] == 0)
     assert zffn.get_device_error() == zffn.OK
+
+
+@pytest.mark.parametrize("T,r", [(4096, 16), (5000, 64), (30000, 40)])
+def test_adapters_weights_gradients(T, r):
+    N, K = 1032, 264
+    gen = ref.generator(T + r)
+    plan = zffn.moe_sort(torch.zeros((T, 1), dtype=torch.int32, device="cuda"), 1)
+    x, dy, A, B = positive(gen, T, K), positive(gen, T, N), positive(gen, 1, r, K), positive(gen, 1, N, r)
+    v = torch.rand((T, r), generator=gen, device="cuda") + 0.5
+    _, dA, dB = zffn.lora_grad(dy, x, v, A, B, plan)
+    (_, _), (wA, _), (wB, _) = ref.lora_grad(dy, x, v, A, B, plan, None, None)
+    # (two roundings more for the sums of v's three pieces; dA: dv's own error first)
+    nearest(dB, wB, (bound(T) + 2 * ref.U32) * wB)
+    nearest(dA, wA, (bound(T) + bound(N) + 2 * ref.U32) * wA)
+    assert zffn.get_device_error() == zffn.OK
