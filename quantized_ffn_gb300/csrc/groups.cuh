@@ -86,26 +86,27 @@ struct GroupWalk {
             row0 = __shfl_sync(0xffffffffu, lo, e - e0);
             rows = __shfl_sync(0xffffffffu, hi, e - e0) - row0;
             return true;
-        }
-        for (;;) {
-            const unsigned past = __ballot_sync(0xffffffffu, t < (before + inc) * n_tiles);
-            if (past) {
-                const int l = __ffs(past) - 1;
-                const int first = __shfl_sync(0xffffffffu, inc - n, l), tiles = __shfl_sync(0xffffffffu, n, l);
-                const int at = __shfl_sync(0xffffffffu, lo, l), end = __shfl_sync(0xffffffffu, hi, l);
-                e = e0 + l;
-                int in = t - (before + first) * n_tiles;
-                const int block = each.div(in) * GROUP, wide = min(GROUP, tiles - block);
-                in -= block * n_tiles;
-                // in / wide: below 2^16, so that the product is off by less than the half that is added
-                nt = (int)(((float)in + 0.5f) * __frcp_rn((float)wide));
-                row0 = at + (block + in - nt * wide) * TM;
-                rows = min(TM, end - row0);
-                return true;
+        } else {
+            for (;;) {
+                const unsigned past = __ballot_sync(0xffffffffu, t < (before + inc) * n_tiles);
+                if (past) {
+                    const int l = __ffs(past) - 1;
+                    const int first = __shfl_sync(0xffffffffu, inc - n, l), tiles = __shfl_sync(0xffffffffu, n, l);
+                    const int at = __shfl_sync(0xffffffffu, lo, l), end = __shfl_sync(0xffffffffu, hi, l);
+                    e = e0 + l;
+                    int in = t - (before + first) * n_tiles;
+                    const int block = each.div(in) * GROUP, wide = min(GROUP, tiles - block);
+                    in -= block * n_tiles;
+                    // in / wide: below 2^16, so that the product is off by less than the half that is added
+                    nt = (int)(((float)in + 0.5f) * __frcp_rn((float)wide));
+                    row0 = at + (block + in - nt * wide) * TM;
+                    rows = min(TM, end - row0);
+                    return true;
+                }
+                before += __shfl_sync(0xffffffffu, inc, 31);
+                if (e0 + 32 > E) return false;
+                hold(e0 + 32);
             }
-            before += __shfl_sync(0xffffffffu, inc, 31);
-            if (e0 + 32 > E) return false;
-            hold(e0 + 32);
         }
     }
 };
