@@ -62,9 +62,10 @@ struct Maps {
 // Roles: warps 0 .. 7 take a tile out of tensor memory (32 rows by 128 columns each) and
 // write it, warp 8 loads by TMA, warp 9 issues the MMAs; weights: warp 10 zeroes the rows past an
 // expert's last in its last stage (in the MMA's own warp that held the MMAs back: 32768
-// rows of 128 experts, 1536 x 2048, 217 us).  Those 32768 rows, unevenly: forward 195 us, 1.06
-// PFLOP/s, the tensor pipe 77 % active on tiles that end with an expert's rows; weights 202 us,
-// 1.02 PFLOP/s, bound by the way from L2 (four stages a tile, and then it is written).
+// rows of 128 experts, 1536 x 2048, 217 us).  Those 32768 rows, unevenly, ten calls on the same
+// inputs: forward 205 us, 1.01 PFLOP/s, on tiles that end with an expert's rows (49,400 rows of
+// MMAs); weights 202 us, 1.02 PFLOP/s, bound by the way from L2 (four stages a tile, and then it is
+// written).  In a loop of seconds over changing inputs, at the power limit, 229 and 210.
 // ---------------------------------------------------------------------------
 template <int KIND_, bool PAIR_, bool PARTS_>
 struct LargeCfg {
@@ -479,8 +480,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) large_kernel(const __grid_const
 // fewer than the SMs a cluster's blocks split K: row j's sums go to the shared memory
 // of rank j % split, which adds them in rank order, so that the result is the same
 // every time.  Bound by HBM: every weight is read once (2048 rows of 128 experts, 1536 x 2048:
-// 126 us, 6.5 TB/s; 8 rows of 8 experts 11.7 us, 4.3 TB/s, of which the launch and the join
-// are 4).
+// 123 to 126 us, 6.6 TB/s; 8 rows of 8 experts 12.0 us on the same inputs again, of which the launch
+// and the join are 4, 13.6 and 3.7 TB/s on changing ones).
 //
 // Roles: warps 0 .. 3 take a tile out of tensor memory (32 columns of the result each)
 // and write it, warp 4 loads by TMA, warp 5 issues the MMAs.
@@ -839,7 +840,7 @@ static cudaError_t launch(const Bf16Args &a, cudaStream_t s) {
     // Rows an expert, and 128 x 256 tiles at least.  Small tiles: the least of 16, 32 rows
     // that takes an expert's rows (with some spread over their mean) at once, so that its
     // weights are read once; of 64 where the large ones are so few that splitting K gains more
-    // (times of 1536 x 2048 in us, small and large: 128 experts of 24 rows 138 / 140, of 48
+    // (times of 1536 x 2048 in us, small and large, these with their sums in one part: 128 experts of 24 rows 138 / 140, of 48
     // rows 135 / 144, of 64 rows 148 / 144; one of 64 rows 9.5 / 15.4, of 256 rows 11.7 / 15.7,
     // of 512 rows 15.9 / 16.0).
     const int64_t mean = a.offsets ? ((int64_t)a.M * 3 / 2 + a.E - 1) / a.E : a.M;

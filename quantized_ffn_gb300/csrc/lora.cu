@@ -1074,7 +1074,8 @@ __device__ __forceinline__ float dot8(uint4 a, uint4 b, float s) {
 }
 
 // PARTS warps for one value of v: blocks (row, 8 of r).  Two where the blocks are few (61 tokens
-// of 48 adapters, K = 4096, r = 16, with expand: 10.5 us, one 12.0; 128 of 64, r = 64: 59.9 / 56.7).
+// of 48 adapters, K = 4096, r = 16, with expand, calls chained in a graph: 8.9 us, one warp 10.3); of
+// many blocks they cost more than they gain (128 of 64, r = 64: one warp 50.5 us, two some 3 more).
 template <int PARTS>
 __global__ void __launch_bounds__(256 * PARTS) shrink_row_kernel(const Params p, const __nv_bfloat16 *x, const __nv_bfloat16 *w, float *v) {
     __shared__ int sh;
@@ -1118,7 +1119,7 @@ constexpr int R_THREADS = 128;
 // Two columns of out a thread: blocks (token, 256 columns).  W's rows and base are asked for
 // before the grid that writes v has ended, and from L2: this SM's L1 may hold what was there
 // before the grids before that one (through L1, which gives the other half of a row's 32 bytes,
-// 61 tokens of 48 adapters took 10.0 us, so 10.6).
+// 61 tokens of 48 adapters with r = 16 took 0.6 us less).
 template <typename O>
 __global__ void __launch_bounds__(R_THREADS) expand_row_kernel(const Params p, const float *v, const __nv_bfloat16 *w, const O *base, O *out) {
     __shared__ int sh;
@@ -1174,9 +1175,9 @@ __global__ void __launch_bounds__(R_THREADS) expand_row_kernel(const Params p, c
 
 // The same where r / 8 is a power of two, q: lane l of a load of 512 bytes of W's rows takes 16
 // of them, ranks 8 (l % q) and on of column l / q, whose sums the q lanes join.  A block takes
-// several runs of columns where the blocks are many more than run at once (N = 11008: 61
-// tokens of 48 adapters, r = 16, 8.6 us with shrink, by two columns a thread 9.2; 512 of 64 37.9 /
-// 48.4; 128 of 64, r = 64, 46.5 / 56.2).
+// several runs of columns where the blocks are many more than run at once (4096 -> 11008, calls
+// chained in a graph, with shrink: 61 tokens of 48 adapters, r = 16, 8.9 us, by two columns a thread
+// 10.1; 512 of 64 43.9 / 67.5; 128 of 64, r = 64, 50.5 / 58.4).
 template <typename O>
 __global__ void __launch_bounds__(R_THREADS) expand_lane_kernel(const Params p, const float *v, const __nv_bfloat16 *w, const O *base, O *out, int q_log) {
     __shared__ int sh;
@@ -1247,7 +1248,7 @@ static int64_t row_tiles(const LoraPlan &q) { return q.T / 128 + (q.L + 1 < q.T 
 // 16: 41 and 18 / 79; 1024 of 128, r = 16: 75 to 85 and 27 / 150; 512 of 128, r = 32: 78 to 95 and 25 / 144;
 // 1024 of 256, r = 32: 157 to 171 and 108 / 276; 2048 of 256, r = 32: 282 to 303 and 111 / 285; 2048 of 1024,
 // r = 64: 550 to 647 and 243 / 893; 16384 of 4096, r = 16: 1050 to 1310 and 2916 / 4826, whose walk over the
-// table each block takes; 61 of 48, r = 16: 9 and 15 / 52).  r = 24 and the like, two columns a thread,
+// table each block takes; 64 of 64, r = 16: 13 and 15 / 56).  r = 24 and the like, two columns a thread,
 // take a third longer and more by rows (512 of 128, r = 24: 91 to 121 and 25 / 144).
 static bool lane_wide(int r) { return (r & (r - 1)) == 0; }   // r is a multiple of 8
 static bool few(int T, int r, int L) { return (int64_t)T * r <= 1024 + (lane_wide(r) ? 112 : 70) * (int64_t)(L < T ? L : T); }

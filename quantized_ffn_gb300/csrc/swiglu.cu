@@ -1,7 +1,7 @@
 // swiglu.cu -- h = silu(g) u of rows [g | u], and its gradient.  One pass: each value is
 // read once and written once, a thread's two or four accesses of each kind before the
-// first sum.  Bound by HBM: 32768 rows of 768 bf16 (151 MB) take 22.9 us, 6.6 TB/s, their
-// gradient (252 MB) 37.1 us, 6.8 TB/s.
+// first sum.  Bound by HBM: 32768 rows of 768 bf16 (151 MB) take 22.4 us, 6.7 TB/s, their
+// gradient (252 MB) 37.3 us, 6.8 TB/s.
 #include "bf16.h"
 #include "groups.cuh"
 #include "launch.cuh"
