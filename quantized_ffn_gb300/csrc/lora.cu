@@ -1244,14 +1244,19 @@ static int64_t row_tiles(const LoraPlan &q) { return q.T / 128 + (q.L + 1 < q.T 
 // the tensor cores' kernels take a tile for each adapter, however few its rows.  L is the table's
 // size; how many adapters have tokens the host does not know, and by tiles that decides: the bound
 // lies where neither form is much more than twice the other, whether one adapter has all tokens or
-// each has some (4096 -> 11008, us by rows and by tiles with one in use / all: 512 tokens of 64, r =
-// 16: 41 and 18 / 79; 1024 of 128, r = 16: 75 to 85 and 27 / 150; 512 of 128, r = 32: 78 to 95 and 25 / 144;
-// 1024 of 256, r = 32: 157 to 171 and 108 / 276; 2048 of 256, r = 32: 282 to 303 and 111 / 285; 2048 of 1024,
-// r = 64: 550 to 647 and 243 / 893; 16384 of 4096, r = 16: 1050 to 1310 and 2916 / 4826, whose walk over the
-// table each block takes; 64 of 64, r = 16: 13 and 15 / 56).  r = 24 and the like, two columns a thread,
-// take a third longer and more by rows (512 of 128, r = 24: 91 to 121 and 25 / 144).
+// each has some (4096 -> 11008, us by rows and by tiles with one in use / all: 128 tokens of 8 adapters, r =
+// 16: 13 and 10 / 20; 24 of 8, r = 128: 21 and 16 / 26; 256 of 16, r = 16: 21 and 12 / 27; 40 of 32, r = 128: 28 to
+// 30 and 19 / 43; 512 of 32, r = 16: 39 and 15 / 45; 512 of 64, r = 16: 41 and 18 / 79; 1024 of 128, r = 16: 75 to
+// 85 and 27 / 150; 512 of 128, r = 32: 78 to 95 and 25 / 144; 1024 of 256, r = 32: 157 to 171 and 108 / 276; 2048
+// of 256, r = 32: 282 to 303 and 111 / 285; 2048 of 1024, r = 64: 550 to 647 and 243 / 893; 16384 of 4096, r =
+// 16: 1050 to 1310 and 2916 / 4826, whose walk over the table each block takes).  r = 24 and the like, two
+// columns a thread, take a third longer and more by rows (100 of 32, r = 40: 29 to 32 and 12 / 44; 512 of
+// 128, r = 24: 91 to 121 and 25 / 144).
 static bool lane_wide(int r) { return (r & (r - 1)) == 0; }   // r is a multiple of 8
-static bool few(int T, int r, int L) { return (int64_t)T * r <= 1024 + (lane_wide(r) ? 112 : 70) * (int64_t)(L < T ? L : T); }
+static bool few(int T, int r, int L) {
+    const int64_t in_use = L < T ? L : T;                     // adapters, at most
+    return (int64_t)T * r <= (lane_wide(r) ? 1700 + 104 * in_use : 1400 + 62 * in_use);
+}
 
 template <bool MN>
 static cudaError_t shrink(const LoraPlan &q, const void *x, const void *w, float *v, void *v16, const float *other, void *other16, int C, cudaStream_t s) {
